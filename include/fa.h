@@ -243,6 +243,153 @@ FA_API int fa_backward_noalloc(const void* q, const void* k, const void* v, cons
 /* Size in bytes of the scratch array fa_backward_noalloc uses. */
 FA_API size_t fa_backward_noalloc_max_bytes(void);
 
+/* ---------------------------------------------------------------- serving
+ * Attention of whole prompts and of drafted tokens over a cache in pages, and
+ * the cache's own work. The pages state attention for equal heads over whole
+ * rows only; these entry points compute the same softmax(s Q K^T) V, with
+ * grouped heads, packed token-major rows and masks as stated at each.
+ *
+ * Conventions of these entry points, besides those above:
+ *  - Types: FA_BF16 or FA_FP16, the same for every tensor of a call.
+ *  - Grouped heads: Hq query heads share Hkv key/value heads, Hq a multiple of
+ *    Hkv and Hq / Hkv <= 128; query head h reads key/value head h / (Hq / Hkv).
+ *  - Tokens of all sequences are packed back to back: sequence b has the tokens
+ *    [cu[b], cu[b + 1]), cu a device int32 [B + 1], non-decreasing from 0. cu[B]
+ *    may be less than T: the rows behind it are neither read for a result nor
+ *    written. cu is read on the device only, so that a captured call can be
+ *    replayed with other lengths.
+ *  - A value that only the kernels can check (an offset that decreases or passes
+ *    T, a length that passes the page table, a page id outside the cache) records
+ *    FA_ERR_DEVICE_CHECK in the device status word. Nothing outside the given
+ *    tensors is read or written; what the call says below happens instead. */
+typedef enum { FA_BF16 = 0, FA_FP16 = 1 } fa_dtype;
+
+/* Rows of [T, H, d] tokens: d contiguous, strides in elements, both positive
+ * multiples of 8 (the rows of a wider projection, say); data 16-byte aligned. */
+typedef struct {
+  void* data;
+  int64_t token_stride, head_stride;
+} fa_rows;
+
+/* A cache in pages: K and V of shape [n_pages, Hkv, page_size, d], d contiguous,
+ * with the same strides (elements, positive multiples of 8; any order of the
+ * other dimensions), 16-byte aligned. page_size is 16, 32, 64, 128 or 256.
+ * table: device int32, row b (table_stride entries apart, table_width of them
+ * used) lists the pages of sequence b: token i lies in page
+ * table[b][i / page_size] at place i % page_size. */
+typedef struct {
+  void *k, *v;
+  int64_t page_stride, head_stride, token_stride;
+  int32_t n_pages, page_size;
+  const int32_t* table;
+  int64_t table_stride;
+  int32_t table_width;
+} fa_pages;
+
+/* Causal attention of whole prompts: token i of a sequence attends to the tokens
+ * j <= i of the same sequence. q and o are [T, Hq, d], k and v [T, Hkv, d], lse
+ * [Hq, T] fp32 (NULL: not written). Sequences may have any length, 0 and 1 too.
+ * What lies in rows of k and v behind a sequence's end (other sequences, padding)
+ * does not reach its results, whatever it holds; a NaN or infinity in a token of
+ * the sequence itself may reach its earlier tokens within 128 keys of it.
+ * Decreasing offsets or ones past T record FA_ERR_DEVICE_CHECK; the sequence is
+ * then cut to the tokens that exist. workspace as for fa_forward_tree. */
+FA_API int fa_forward_prompt(const fa_rows* q, const fa_rows* k, const fa_rows* v, const fa_rows* o, float* lse,
+                             const int32_t* cu_seqlens, int B, int T, int Hq, int Hkv, int d, int dtype, float scale,
+                             void* workspace, size_t workspace_bytes, fa_stream_t stream);
+
+/* Attention of drafted tokens ("nodes") over a cache in pages and over each
+ * other. Sequence b has lens[b] tokens in the cache (device int32 [B]) and the
+ * nodes [cu[b], cu[b + 1]), whose queries, keys and values are the packed rows
+ * q [T, Hq, d], k and v [T, Hkv, d]; the nodes are not in the cache. Every node
+ * attends to all lens[b] cached tokens, and
+ *  - mask = NULL: to the nodes j <= i of its sequence (a chain; one node is plain
+ *    decoding, many are a further part of a prompt);
+ *  - mask given: to the nodes whose bits are set: mask is a device uint32
+ *    [T, mask_words], bit j % 32 of word j / 32 of a node's row is node j of its
+ *    sequence (fa_tree_mask makes it from parents). Any bits may be set; those at
+ *    or past the sequence's number of nodes, and nodes past 32 mask_words, count
+ *    as not set.
+ * A node that sees nothing gets O = 0 and LSE = -inf. o is [T, Hq, d], lse
+ * [Hq, T] fp32 (NULL: not written). A sequence without nodes writes nothing, and
+ * its length and pages are not looked at. What lies in the cache past lens[b]
+ * does not reach the results, whatever it holds.
+ * A length outside [0, table_width * page_size] is taken as the nearest one
+ * inside, a page id outside [0, n_pages) as a page of zeros, and either records
+ * FA_ERR_DEVICE_CHECK.
+ * workspace: fa_forward_tree_workspace_size bytes, 256-byte aligned, contents on
+ * entry irrelevant; calls that may overlap need one each. */
+FA_API int fa_forward_tree(const fa_rows* q, const fa_rows* k, const fa_rows* v, const fa_rows* o, float* lse,
+                           const fa_pages* cache, const int32_t* lens, const int32_t* cu_nodes, const uint32_t* mask,
+                           int mask_words, int B, int T, int Hq, int Hkv, int d, int dtype, float scale,
+                           void* workspace, size_t workspace_bytes, fa_stream_t stream);
+
+/* Workspace bytes of fa_forward_tree and fa_forward_prompt on the current
+ * device: two partial results of 256 rows for each SM. 0 for an unsupported d. */
+FA_API size_t fa_forward_tree_workspace_size(int d);
+
+/* Which nodes a node of a tree sees: itself and its ancestors. parents: device
+ * int32 [T], for each node its parent's index within its sequence, less than its
+ * own, or negative for a root. mask: device uint32 [T, mask_words] as
+ * fa_forward_tree reads it. A parent at or past the node's own index counts as a
+ * root and records FA_ERR_DEVICE_CHECK; so does a sequence of more than
+ * 32 mask_words nodes, whose bits past them are left out. */
+FA_API int fa_tree_mask(const int32_t* parents, const int32_t* cu_nodes, uint32_t* mask, int mask_words, int B, int T,
+                        fa_stream_t stream);
+
+/* Writes tokens into their pages: token i of sequence b goes to position
+ * start[b] + i of the cache (start: device int32 [B]). k and v are [Tkv, Hkv, d];
+ * the token's row is cu[b] + i, or rows[cu[b] + i] where rows (device int32, T
+ * entries) is given: the accepted nodes of a draft, say. T: the rows of k and v
+ * without rows, the entries of rows with it. A token whose position, page id or
+ * row lies outside is left out and records FA_ERR_DEVICE_CHECK. Tokens that name
+ * the same place race. */
+FA_API int fa_cache_append(const fa_rows* k, const fa_rows* v, const fa_pages* cache, const int32_t* start,
+                           const int32_t* cu, const int32_t* rows, int B, int T, int Tkv, int Hkv, int d,
+                           fa_stream_t stream);
+
+/* The page tables of a cache with `planes` planes (K and V of every layer) that
+ * share them: plane x lies plane_stride elements after plane 0, each of shape
+ * [n_pages, Hkv, page_size, d], contiguous, 16-bit elements, 16-byte aligned. */
+typedef struct {
+  void* data;
+  int64_t plane_stride;
+  int32_t planes, n_pages, Hkv, page_size, d;
+  int32_t* table;  /* [slots, table_width] pages of each slot */
+  int32_t* lens;   /* [slots] tokens of each slot */
+  int32_t slots, table_width;
+} fa_pool;
+
+/* Every slot s becomes the first min(new_lens[s], lens[src[s]]) tokens of slot
+ * src[s] as it was before the call, with pages for new_lens[s] tokens: src[s] = s
+ * keeps, trims (a shorter new_lens), frees (0) or grows a slot; another src forks
+ * it, and a permutation reorders beams. Pages that only hold kept tokens are
+ * shared. The page in which the next token would be written, where some of its
+ * tokens are kept, is the slot's own afterwards: it stays if src[s] = s and no
+ * other slot keeps it, else its kept tokens are copied (in every plane) to a new
+ * page. New pages come from those free before the call, lowest id first, in the
+ * order of the slots. A page is in use while some slot's table lists it among the
+ * first ceil(lens / page_size) entries; nothing else records that.
+ * table and lens are updated in place, table entries behind a slot's pages become
+ * -1. info: device int32 [2], the pages needed and the pages free; where more are
+ * needed than free, nothing else is changed. A src outside [0, slots), a length
+ * (old or new) outside [0, table_width * page_size] or a listed page id outside
+ * [0, n_pages) records FA_ERR_DEVICE_CHECK, info becomes {-1, -1}, and nothing
+ * else is changed. workspace: fa_cache_workspace_size bytes, 256-byte aligned. */
+FA_API int fa_cache_update(const fa_pool* pool, const int32_t* src, const int32_t* new_lens, int32_t* info,
+                           void* workspace, size_t workspace_bytes, fa_stream_t stream);
+
+/* Moves the pages in use to the lowest ids: with n of them in use, the r-th page
+ * in use at or past n (by id) moves, in every plane, to the r-th page below n that
+ * is free, and the tables follow; entries behind a slot's pages are left as they
+ * are. info: device int32 [2], the pages in use and the pages moved. Lengths and
+ * page ids outside their ranges as for fa_cache_update. */
+FA_API int fa_cache_compact(const fa_pool* pool, int32_t* info, void* workspace, size_t workspace_bytes,
+                            fa_stream_t stream);
+
+/* Workspace bytes of fa_cache_update and fa_cache_compact. 0 for invalid sizes. */
+FA_API size_t fa_cache_workspace_size(int n_pages, int slots, int table_width);
+
 /* Static text for an fa_status value. */
 FA_API const char* fa_status_string(int status);
 

@@ -22,8 +22,42 @@ _i = ctypes.c_int
 _f = ctypes.c_float
 _sz = ctypes.c_size_t
 
+
+class Rows(ctypes.Structure):
+    """fa_rows: [T, H, d] tokens with strides in elements."""
+    _fields_ = [("data", _vp), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class Pages(ctypes.Structure):
+    """fa_pages: a cache in pages and its page table."""
+    _fields_ = [("k", _vp), ("v", _vp), ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("table", _vp), ("table_stride", ctypes.c_int64), ("table_width", ctypes.c_int32)]
+
+
+class Pool(ctypes.Structure):
+    """fa_pool: all planes of a cache with the slots' page tables and lengths."""
+    _fields_ = [("data", _vp), ("plane_stride", ctypes.c_int64), ("planes", ctypes.c_int32),
+                ("n_pages", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("d", ctypes.c_int32), ("table", _vp), ("lens", _vp), ("slots", ctypes.c_int32),
+                ("table_width", ctypes.c_int32)]
+
+
+_rows = ctypes.POINTER(Rows)
+_pages = ctypes.POINTER(Pages)
+_pool = ctypes.POINTER(Pool)
+
 SIGNATURES = {
     "libfa.so": {
+        "fa_forward_prompt": (_i, [_rows, _rows, _rows, _rows, _vp, _vp, _i, _i, _i, _i, _i, _i, _f, _vp, _sz, _vp]),
+        "fa_forward_tree": (_i, [_rows, _rows, _rows, _rows, _vp, _pages, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i,
+                                 _f, _vp, _sz, _vp]),
+        "fa_forward_tree_workspace_size": (_sz, [_i]),
+        "fa_tree_mask": (_i, [_vp, _vp, _vp, _i, _i, _i, _vp]),
+        "fa_cache_append": (_i, [_rows, _rows, _pages, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp]),
+        "fa_cache_update": (_i, [_pool, _vp, _vp, _vp, _vp, _sz, _vp]),
+        "fa_cache_compact": (_i, [_pool, _vp, _vp, _sz, _vp]),
+        "fa_cache_workspace_size": (_sz, [_i, _i, _i]),
         "fa_forward": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _f, _i, _vp]),
         "fa_forward_ex": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _f, _i, _vp, _vp]),
         "fa_forward_qk": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _f, _i, _vp, _vp]),

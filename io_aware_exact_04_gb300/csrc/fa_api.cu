@@ -71,6 +71,8 @@ thread_local char g_last_error[256] = "";
 }  // namespace
 
 namespace fa {
+int* status_word(int* err) { return device_status(err); }
+
 int check_common(int B, int H, int Nq, int Nk, int d, float scale, int causal) {
   if (B < 0 || H < 0 || Nq < 0 || Nk < 0) return FA_ERR_INVALID_ARG;
   if (causal != 0 && causal != 1) return FA_ERR_INVALID_ARG;

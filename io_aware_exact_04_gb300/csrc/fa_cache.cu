@@ -1,0 +1,472 @@
+// The cache in pages: tokens written into their pages, slots updated (forked, trimmed, freed,
+// grown), pages compacted; and the visibility bits of a drafted tree.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "fa_internal.h"
+#include "serve.cuh"
+
+namespace fa {
+
+// ---------------------------------------------------------------------------------------------
+// Bits of a tree: node i sees itself and what its parent sees. A thread walks the chain of one
+// node; every step goes to a smaller index, so that the walk ends whatever the parents are.
+__global__ void __launch_bounds__(128) tree_mask_kernel(const int* parents, const int* cu, uint32_t* mask, int words, int B,
+                                                        int T, int* status) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int b = blockIdx.x;
+  const SeqRange r = seq_range(cu, b, T, status);
+  const int n = r.hi - r.lo;
+  if (n > 32 * words && threadIdx.x == 0) record_check(status, SITE_S_WORDS);
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+    uint32_t* row = mask + (long long)(r.lo + i) * words;
+    for (int w = 0; w < words; ++w) row[w] = 0;
+    for (int j = i;;) {
+      if (j < 32 * words) row[j >> 5] |= 1u << (j & 31);
+      const int p = parents[r.lo + j];
+      if (p < 0) break;
+      if (p >= j) {
+        record_check(status, SITE_S_PARENT);
+        break;
+      }
+      j = p;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------------------------
+struct AppendArgs {
+  const uint16_t *k, *v;
+  long long k_st, k_sh, v_st, v_sh;
+  uint16_t *kc, *vc;
+  long long c_sp, c_sh, c_st;
+  int n_pages, page_shift;
+  const int* table;
+  long long table_stride;
+  int table_width;
+  const int *start, *cu, *rows;
+  int B, T, Tkv, Hkv;
+  int* status;
+};
+
+// A warp for each token.
+template <int D>
+__global__ void __launch_bounds__(128) cache_append_kernel(AppendArgs a) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int t = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (blockIdx.x == 0) check_offsets(a.cu, a.B, a.T, a.status);
+  if (t >= a.T) return;
+  const int b = find_sequence(a.cu, a.B, t);
+  if (b < 0) return;
+  const SeqRange r = seq_range(a.cu, b, a.T, a.status);
+  if (t < r.lo || t >= r.hi) return;
+  const long long pos = (long long)a.start[b] + (t - r.lo);
+  if (pos < 0 || pos >= (long long)a.table_width << a.page_shift) return record_check(a.status, SITE_S_LENGTH);
+  const int id = a.table[b * a.table_stride + (pos >> a.page_shift)];
+  if (id < 0 || id >= a.n_pages) return record_check(a.status, SITE_S_PAGE);
+  const int row = a.rows ? a.rows[t] : t;
+  if (row < 0 || row >= a.Tkv) return record_check(a.status, SITE_S_ROW);
+  const long long to = id * a.c_sp + (pos & ((1 << a.page_shift) - 1)) * a.c_st;
+  for (int i = lane; i < a.Hkv * (D / 8); i += 32) {
+    const int h = i / (D / 8), c = i % (D / 8) * 8;
+    const uint4 x = *reinterpret_cast<const uint4*>(a.k + row * a.k_st + h * a.k_sh + c);
+    const uint4 y = *reinterpret_cast<const uint4*>(a.v + row * a.v_st + h * a.v_sh + c);
+    *reinterpret_cast<uint4*>(a.kc + to + h * a.c_sh + c) = x;
+    *reinterpret_cast<uint4*>(a.vc + to + h * a.c_sh + c) = y;
+  }
+}
+
+// ---------------------------------------------------------------------------------------------
+// Slots and pages. Workspace, in ints: head [8], uses [n_pages], pages [n_pages] (new pages, or
+// where a page goes), slots [slots] x 4, copies [slots] x 3, moves [n_pages] x 2, the old table.
+struct PoolArgs {
+  uint8_t* data;
+  long long plane_bytes;
+  int planes, n_pages, Hkv, page_shift, row_bytes;
+  int *table, *lens;
+  int slots, width;
+  const int *src, *fresh;  // update only
+  int* info;
+  int* status;
+  int *head, *uses, *pages, *slot, *copies, *moves, *old;
+};
+enum { H_ERR = 0, H_NEED, H_FREE, H_COPIES, H_MOVES };
+constexpr int kWasUsed = 1 << 30;
+
+__device__ __forceinline__ int pages_of(int tokens, int shift) { return (tokens + (1 << shift) - 1) >> shift; }
+
+__global__ void __launch_bounds__(256) pool_clear_kernel(PoolArgs a) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int i = blockIdx.x * 256 + threadIdx.x;
+  if (i < a.n_pages) a.uses[i] = 0;
+  if (i < 8) a.head[i] = 0;
+}
+
+__device__ __forceinline__ void pool_error(const PoolArgs& a, int site) {
+  a.head[H_ERR] = 1;
+  record_check(a.status, site);
+}
+
+// A block for each slot: which pages were in use, and how often each is kept.
+template <bool UPDATE>
+__global__ void __launch_bounds__(256) pool_mark_kernel(PoolArgs a) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int s = blockIdx.x, cap = a.width << a.page_shift;
+  const int len = a.lens[s];
+  if (len < 0 || len > cap) return pool_error(a, SITE_S_LENGTH);
+  const int n = pages_of(len, a.page_shift);
+  for (int j = threadIdx.x; j < n; j += 256) {
+    const int id = a.table[(long long)s * a.width + j];
+    a.old[(long long)s * a.width + j] = id;
+    if (id < 0 || id >= a.n_pages) {
+      pool_error(a, SITE_S_PAGE);
+      continue;
+    }
+    atomicOr(&a.uses[id], kWasUsed);
+  }
+  if (!UPDATE) return;
+  const int t = a.src[s], want = a.fresh[s];
+  if (t < 0 || t >= a.slots) return pool_error(a, SITE_S_SLOT);
+  if (want < 0 || want > cap) return pool_error(a, SITE_S_LENGTH);
+  const int keep = min(want, min(max(a.lens[t], 0), cap));
+  const int shared = (keep >> a.page_shift) + (t == s && (keep & ((1 << a.page_shift) - 1)) != 0);
+  for (int j = threadIdx.x; j < shared; j += 256) {
+    const int id = a.table[(long long)t * a.width + j];
+    if (id >= 0 && id < a.n_pages) atomicAdd(&a.uses[id], 1);
+  }
+}
+
+// The sum over the block's threads below this one, and the block's total.
+__device__ __forceinline__ int block_scan(int x, int* total, int* sh) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  int y = x;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int z = __shfl_up_sync(0xffffffffu, y, o);
+    if (lane >= o) y += z;
+  }
+  if (lane == 31) sh[w] = y;
+  __syncthreads();
+  if (w == 0) {
+    int v = sh[lane];
+    for (int o = 1; o < 32; o <<= 1) {
+      const int z = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += z;
+    }
+    sh[lane] = v;
+  }
+  __syncthreads();
+  *total = sh[31];
+  const int before = y - x + (w ? sh[w - 1] : 0);
+  __syncthreads();
+  return before;
+}
+
+__global__ void __launch_bounds__(1024) update_plan_kernel(PoolArgs a) {
+  griddep_wait();
+  griddep_launch_dependents();
+  __shared__ int sh[32];
+  const int tid = threadIdx.x;
+  if (a.head[H_ERR]) {
+    if (tid < 2) a.info[tid] = -1;
+    return;
+  }
+  int need = 0, copies = 0, total;
+  for (int s0 = 0; s0 < a.slots; s0 += 1024) {
+    const int s = s0 + tid;
+    int mine = 0, copy = 0, kept = 0, keep = 0, part = 0, page = 0;
+    if (s < a.slots) {
+      const int t = a.src[s];
+      keep = min(a.fresh[s], a.lens[t]);
+      part = keep & ((1 << a.page_shift) - 1);
+      kept = keep >> a.page_shift;
+      if (part) {
+        page = a.old[(long long)t * a.width + kept];
+        copy = !(t == s && (a.uses[page] & (kWasUsed - 1)) == 1);
+        kept += !copy;
+      }
+      mine = pages_of(a.fresh[s], a.page_shift) - kept;
+    }
+    const int before = block_scan(mine, &total, sh);
+    if (s < a.slots) {
+      a.slot[4 * s] = kept;
+      a.slot[4 * s + 1] = need + before;
+    }
+    need += total;  // at most slots x width
+    const int at = block_scan(copy, &total, sh);
+    if (copy) {
+      a.copies[3 * (copies + at)] = s;
+      a.copies[3 * (copies + at) + 1] = page;
+      a.copies[3 * (copies + at) + 2] = part;
+    }
+    copies += total;
+  }
+  int free = 0;
+  for (int p0 = 0; p0 < a.n_pages; p0 += 1024) {
+    const int p = p0 + tid;
+    const int is_free = p < a.n_pages && a.uses[p] == 0;
+    const int before = block_scan(is_free, &total, sh);
+    if (is_free) a.pages[free + before] = p;
+    free += total;
+  }
+  if (tid == 0) {
+    a.info[0] = need;
+    a.info[1] = free;
+    a.head[H_NEED] = need;
+    a.head[H_FREE] = free;
+    a.head[H_COPIES] = copies;
+  }
+}
+
+// Table rows (a block each), then the copies of partly kept pages.
+__global__ void __launch_bounds__(256) update_apply_kernel(PoolArgs a) {
+  griddep_wait();
+  griddep_launch_dependents();
+  if (a.head[H_ERR] || a.head[H_NEED] > a.head[H_FREE]) return;
+  const int s = blockIdx.x;
+  const int kept = a.slot[4 * s], off = a.slot[4 * s + 1], want = a.fresh[s], n = pages_of(want, a.page_shift);
+  for (int j = threadIdx.x; j < a.width; j += 256)
+    a.table[(long long)s * a.width + j] =
+        j < kept ? a.old[(long long)a.src[s] * a.width + j] : j < n ? a.pages[off + j - kept] : -1;
+  if (threadIdx.x == 0) a.lens[s] = want;
+}
+
+__global__ void __launch_bounds__(256) update_copy_kernel(PoolArgs a) {
+  griddep_wait();
+  griddep_launch_dependents();
+  if (a.head[H_ERR] || a.head[H_NEED] > a.head[H_FREE]) return;
+  const long long units = (long long)a.head[H_COPIES] * a.planes * a.Hkv;
+  const long long head_bytes = (long long)a.row_bytes << a.page_shift;
+  for (long long u = blockIdx.x; u < units; u += gridDim.x) {
+    const int h = (int)(u % a.Hkv), x = (int)(u / a.Hkv % a.planes), c = (int)(u / a.Hkv / a.planes);
+    const int s = a.copies[3 * c], of = a.copies[3 * c + 1], rows = a.copies[3 * c + 2];
+    const int to = a.pages[a.slot[4 * s + 1]];  // the slot's first new page
+    uint8_t* plane = a.data + x * a.plane_bytes;
+    const uint4* from = reinterpret_cast<const uint4*>(plane + ((long long)of * a.Hkv + h) * head_bytes);
+    uint4* dest = reinterpret_cast<uint4*>(plane + ((long long)to * a.Hkv + h) * head_bytes);
+    for (int i = threadIdx.x; i < rows * (a.row_bytes / 16); i += 256) dest[i] = from[i];
+  }
+}
+
+__global__ void __launch_bounds__(1024) compact_plan_kernel(PoolArgs a) {
+  griddep_wait();
+  griddep_launch_dependents();
+  __shared__ int sh[32];
+  const int tid = threadIdx.x;
+  if (a.head[H_ERR]) {
+    if (tid < 2) a.info[tid] = -1;
+    return;
+  }
+  int n = 0, total;
+  for (int p0 = 0; p0 < a.n_pages; p0 += 1024) {
+    const int p = p0 + tid;
+    block_scan(p < a.n_pages && a.uses[p] != 0, &total, sh);
+    n += total;
+  }
+  int holes = 0, high = 0;
+  for (int p0 = 0; p0 < a.n_pages; p0 += 1024) {
+    const int p = p0 + tid;
+    const bool used = p < a.n_pages && a.uses[p] != 0;
+    const int hole = p < n && !used, moves = p >= n && used;
+    int at = block_scan(hole, &total, sh);
+    if (hole) a.moves[2 * (holes + at) + 1] = p;
+    holes += total;
+    at = block_scan(moves, &total, sh);
+    if (moves) a.moves[2 * (high + at)] = p;
+    high += total;
+    if (p < a.n_pages) a.pages[p] = moves ? -1 - (high - total + at) : p;
+  }
+  if (tid == 0) {
+    a.info[0] = n;
+    a.info[1] = high;
+    a.head[H_MOVES] = high;
+  }
+}
+
+__global__ void __launch_bounds__(256) compact_table_kernel(PoolArgs a) {
+  griddep_wait();
+  griddep_launch_dependents();
+  if (a.head[H_ERR]) return;
+  const int s = blockIdx.x, n = pages_of(a.lens[s], a.page_shift);
+  for (int j = threadIdx.x; j < n; j += 256) {
+    int* e = &a.table[(long long)s * a.width + j];
+    const int g = a.pages[*e];
+    if (g < 0) *e = a.moves[2 * (-1 - g) + 1];
+  }
+}
+
+__global__ void __launch_bounds__(256) compact_copy_kernel(PoolArgs a) {
+  griddep_wait();
+  griddep_launch_dependents();
+  if (a.head[H_ERR]) return;
+  const long long units = (long long)a.head[H_MOVES] * a.planes;
+  const long long page_bytes = ((long long)a.row_bytes << a.page_shift) * a.Hkv;
+  for (long long u = blockIdx.x; u < units; u += gridDim.x) {
+    const int x = (int)(u % a.planes), m = (int)(u / a.planes);
+    uint8_t* plane = a.data + x * a.plane_bytes;
+    const uint4* from = reinterpret_cast<const uint4*>(plane + a.moves[2 * m] * page_bytes);
+    uint4* dest = reinterpret_cast<uint4*>(plane + a.moves[2 * m + 1] * page_bytes);
+    for (long long i = threadIdx.x; i < page_bytes / 16; i += 256) dest[i] = from[i];
+  }
+}
+
+}  // namespace fa
+
+namespace {
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+struct PoolLayout {
+  long long uses, pages, slot, copies, moves, old, total;  // in ints
+};
+PoolLayout pool_layout(long long n_pages, long long slots, long long width) {
+  PoolLayout l;
+  l.uses = 64;
+  l.pages = l.uses + (n_pages + 63) / 64 * 64;
+  l.slot = l.pages + (n_pages + 63) / 64 * 64;
+  l.copies = l.slot + 4 * slots;
+  l.moves = l.copies + 3 * slots;
+  l.old = l.moves + 2 * n_pages;
+  l.total = l.old + slots * width;
+  return l;
+}
+
+bool pool_sizes_ok(long long n_pages, long long slots, long long width) {
+  return n_pages >= 1 && slots >= 1 && width >= 1 && n_pages <= (1 << 28) && slots <= (1 << 20) && width <= (1 << 26) &&
+         slots * width <= (1 << 28);
+}
+
+int check_pool(const fa_pool* p, const int32_t* info, const void* workspace, size_t bytes, fa::PoolArgs* a) {
+  if (!p || !p->data || !p->table || !p->lens || !info || !workspace) return FA_ERR_INVALID_ARG;
+  if (!aligned16(p->data)) return FA_ERR_MISALIGNED;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return FA_ERR_MISALIGNED;
+  if (p->planes < 1 || p->Hkv < 1 || p->plane_stride < 0) return FA_ERR_INVALID_ARG;
+  if (p->n_pages < 1 || p->slots < 1 || p->table_width < 1) return FA_ERR_INVALID_ARG;
+  switch (p->page_size) {
+    case 16: case 32: case 64: case 128: case 256: break;
+    default: return FA_ERR_UNSUPPORTED;
+  }
+  if ((p->d != 64 && p->d != 128) || p->planes > (1 << 20) || p->Hkv > 65535) return FA_ERR_UNSUPPORTED;
+  if (!pool_sizes_ok(p->n_pages, p->slots, p->table_width) || (long long)p->table_width * p->page_size > (1 << 30))
+    return FA_ERR_UNSUPPORTED;
+  const long long plane = (long long)p->n_pages * p->Hkv * p->page_size * p->d;
+  if (p->plane_stride % 8 != 0 || (p->planes > 1 && p->plane_stride < plane)) return FA_ERR_INVALID_ARG;
+  if (bytes < fa_cache_workspace_size(p->n_pages, p->slots, p->table_width)) return FA_ERR_INVALID_ARG;
+  int err = FA_OK;
+  a->status = fa::status_word(&err);
+  if (!a->status) return err;
+  a->data = static_cast<uint8_t*>(p->data);
+  a->plane_bytes = p->plane_stride * 2;
+  a->planes = p->planes, a->n_pages = p->n_pages, a->Hkv = p->Hkv, a->row_bytes = 2 * p->d;
+  a->page_shift = 0;
+  while ((1 << a->page_shift) < p->page_size) ++a->page_shift;
+  a->table = p->table, a->lens = p->lens, a->slots = p->slots, a->width = p->table_width;
+  a->info = const_cast<int32_t*>(info);
+  const PoolLayout l = pool_layout(p->n_pages, p->slots, p->table_width);
+  int* w = static_cast<int*>(const_cast<void*>(workspace));
+  a->head = w, a->uses = w + l.uses, a->pages = w + l.pages, a->slot = w + l.slot, a->copies = w + l.copies;
+  a->moves = w + l.moves, a->old = w + l.old;
+  return FA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int fa_tree_mask(const int32_t* parents, const int32_t* cu_nodes, uint32_t* mask, int mask_words, int B, int T,
+                 fa_stream_t stream) {
+  if (B < 0 || T < 0 || mask_words < 1) return FA_ERR_INVALID_ARG;
+  if (B > (1 << 20) || T > (1 << 30) || mask_words > (1 << 20)) return FA_ERR_UNSUPPORTED;
+  if (B == 0 || T == 0) return FA_OK;
+  if (!parents || !cu_nodes || !mask) return FA_ERR_INVALID_ARG;
+  int err = FA_OK;
+  int* status = fa::status_word(&err);
+  if (!status) return err;
+  return fa::launch_pdl("tree_mask_kernel", fa::tree_mask_kernel, dim3(B), dim3(128), 0,
+                        reinterpret_cast<cudaStream_t>(stream), parents, cu_nodes, mask, mask_words, B, T, status);
+}
+
+int fa_cache_append(const fa_rows* k, const fa_rows* v, const fa_pages* cache, const int32_t* start, const int32_t* cu,
+                    const int32_t* rows, int B, int T, int Tkv, int Hkv, int d, fa_stream_t stream) {
+  if (B < 0 || T < 0 || Tkv < 0 || Hkv < 1 || (!rows && T != Tkv)) return FA_ERR_INVALID_ARG;
+  if ((d != 64 && d != 128) || Hkv > 65535 || B > (1 << 20) || T > (1 << 30) || Tkv > (1 << 30)) return FA_ERR_UNSUPPORTED;
+  if (B == 0 || T == 0) return FA_OK;
+  if (Tkv == 0) return FA_ERR_INVALID_ARG;  // rows of nothing
+  if (!cache || !cache->k || !cache->v || !cache->table || !start || !cu) return FA_ERR_INVALID_ARG;
+  if (!aligned16(cache->k) || !aligned16(cache->v)) return FA_ERR_MISALIGNED;
+  for (const fa_rows* r : {k, v}) {
+    if (!r || !r->data) return FA_ERR_INVALID_ARG;
+    if (!aligned16(r->data)) return FA_ERR_MISALIGNED;
+    if (r->token_stride <= 0 || r->token_stride % 8 || r->head_stride <= 0 || r->head_stride % 8) return FA_ERR_INVALID_ARG;
+  }
+  for (int64_t s : {cache->page_stride, cache->head_stride, cache->token_stride})
+    if (s <= 0 || s % 8) return FA_ERR_INVALID_ARG;
+  if (cache->n_pages < 1 || cache->table_width < 1 || cache->table_stride < cache->table_width) return FA_ERR_INVALID_ARG;
+  switch (cache->page_size) {
+    case 16: case 32: case 64: case 128: case 256: break;
+    default: return FA_ERR_UNSUPPORTED;
+  }
+  if ((long long)cache->table_width * cache->page_size > (1 << 30)) return FA_ERR_UNSUPPORTED;
+  fa::AppendArgs a;
+  a.k = static_cast<const uint16_t*>(k->data), a.v = static_cast<const uint16_t*>(v->data);
+  a.k_st = k->token_stride, a.k_sh = k->head_stride, a.v_st = v->token_stride, a.v_sh = v->head_stride;
+  a.kc = static_cast<uint16_t*>(cache->k), a.vc = static_cast<uint16_t*>(cache->v);
+  a.c_sp = cache->page_stride, a.c_sh = cache->head_stride, a.c_st = cache->token_stride;
+  a.n_pages = cache->n_pages;
+  a.page_shift = 0;
+  while ((1 << a.page_shift) < cache->page_size) ++a.page_shift;
+  a.table = cache->table, a.table_stride = cache->table_stride, a.table_width = cache->table_width;
+  a.start = start, a.cu = cu, a.rows = rows;
+  a.B = B, a.T = T, a.Tkv = Tkv, a.Hkv = Hkv;
+  int err = FA_OK;
+  a.status = fa::status_word(&err);
+  if (!a.status) return err;
+  const dim3 grid((T + 3) / 4);
+  const auto st = reinterpret_cast<cudaStream_t>(stream);
+  return d == 64 ? fa::launch_pdl("cache_append_kernel", fa::cache_append_kernel<64>, grid, dim3(128), 0, st, a)
+                 : fa::launch_pdl("cache_append_kernel", fa::cache_append_kernel<128>, grid, dim3(128), 0, st, a);
+}
+
+size_t fa_cache_workspace_size(int n_pages, int slots, int table_width) {
+  if (!pool_sizes_ok(n_pages, slots, table_width)) return 0;
+  return (size_t)pool_layout(n_pages, slots, table_width).total * 4;
+}
+
+int fa_cache_update(const fa_pool* pool, const int32_t* src, const int32_t* new_lens, int32_t* info, void* workspace,
+                    size_t workspace_bytes, fa_stream_t stream) {
+  fa::PoolArgs a = {};
+  int rc = check_pool(pool, info, workspace, workspace_bytes, &a);
+  if (rc != FA_OK) return rc;
+  if (!src || !new_lens) return FA_ERR_INVALID_ARG;
+  a.src = src, a.fresh = new_lens;
+  int sms = 0;
+  if (!fa::sm_count(&sms)) return FA_ERR_CUDA;
+  const auto st = reinterpret_cast<cudaStream_t>(stream);
+  rc = fa::launch_pdl("pool_clear_kernel", fa::pool_clear_kernel, dim3((a.n_pages + 255) / 256), dim3(256), 0, st, a);
+  if (rc == FA_OK) rc = fa::launch_pdl("pool_mark_kernel", fa::pool_mark_kernel<true>, dim3(a.slots), dim3(256), 0, st, a);
+  if (rc == FA_OK) rc = fa::launch_pdl("update_plan_kernel", fa::update_plan_kernel, dim3(1), dim3(1024), 0, st, a);
+  if (rc == FA_OK) rc = fa::launch_pdl("update_apply_kernel", fa::update_apply_kernel, dim3(a.slots), dim3(256), 0, st, a);
+  if (rc == FA_OK) rc = fa::launch_pdl("update_copy_kernel", fa::update_copy_kernel, dim3(8 * sms), dim3(256), 0, st, a);
+  return rc;
+}
+
+int fa_cache_compact(const fa_pool* pool, int32_t* info, void* workspace, size_t workspace_bytes, fa_stream_t stream) {
+  fa::PoolArgs a = {};
+  int rc = check_pool(pool, info, workspace, workspace_bytes, &a);
+  if (rc != FA_OK) return rc;
+  int sms = 0;
+  if (!fa::sm_count(&sms)) return FA_ERR_CUDA;
+  const auto st = reinterpret_cast<cudaStream_t>(stream);
+  rc = fa::launch_pdl("pool_clear_kernel", fa::pool_clear_kernel, dim3((a.n_pages + 255) / 256), dim3(256), 0, st, a);
+  if (rc == FA_OK) rc = fa::launch_pdl("pool_mark_kernel", fa::pool_mark_kernel<false>, dim3(a.slots), dim3(256), 0, st, a);
+  if (rc == FA_OK) rc = fa::launch_pdl("compact_plan_kernel", fa::compact_plan_kernel, dim3(1), dim3(1024), 0, st, a);
+  if (rc == FA_OK) rc = fa::launch_pdl("compact_table_kernel", fa::compact_table_kernel, dim3(a.slots), dim3(256), 0, st, a);
+  if (rc == FA_OK) rc = fa::launch_pdl("compact_copy_kernel", fa::compact_copy_kernel, dim3(8 * sms), dim3(256), 0, st, a);
+  return rc;
+}
+
+}  // extern "C"

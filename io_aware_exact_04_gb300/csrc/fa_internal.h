@@ -84,6 +84,9 @@ int debug_check_slack();
 // (FA_ERR_UNSUPPORTED). FA_OK otherwise.
 int check_common(int B, int H, int Nq, int Nk, int d, float scale, int causal);
 
+// Device address of the current device's status word; null with *err set on failure.
+int* status_word(int* err);
+
 // Device address of a file-scope __device__ variable (`symbol`, its host-side stand-in) on the
 // current device, looked up with cudaGetSymbolAddress on the first call for each (device,
 // context) pair and cached in `cache`. Returns null with *rc set (FA_ERR_UNSUPPORTED for a
