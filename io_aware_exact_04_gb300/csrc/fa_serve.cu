@@ -1,7 +1,5 @@
 // Attention of whole prompts and of drafted trees over a cache in pages: entry points and kernels.
 #include <cuda.h>
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -31,104 +29,854 @@ struct ServeArgs {
   const int* cu;
   int B, T, Hq, Hkv, G;
   float scale_log2;
+  float* part_o;    // workspace: two slots of 256 rows for each CTA, O normalised by its own l
+  float* part_lse;  // their LSEs, base 2 (-inf: no key, O not written)
+  long long part_rows;
   int* status;
 };
 
-template <bool F16>
-__device__ __forceinline__ float to_f32(uint16_t x) {
-  return F16 ? __half2float(__ushort_as_half(x)) : __bfloat162float(__ushort_as_bfloat16(x));
+// Fewest key tiles that a CTA of the tree kernel takes, and rows of a TMA box of new tokens there
+// (a draft seldom fills a tile of 128).
+constexpr int kMinTiles = 2;
+constexpr int kNewBox = 16;
+
+// ---------------------------------------------------------------------------------------------
+// One persistent kernel for prompts and for trees over a cache.
+//
+// Rows: a query tile holds the rows (token, head of the group) of NPT = 128 / G tokens of one
+// key/value head, so that its keys are read once for the whole group. A work item is a pair of
+// such tiles, one for each of two query lanes (warpgroups 0 and 1), over the key tiles of its
+// sequence: first the cached tokens, 128 a tile, then the new ones. Where an item has one query
+// tile only, both lanes take it and alternate key tiles ("dual"), and lane 0 joins the two
+// results out of tensor memory at the end.
+//
+// Roles, 352 threads: warps 0-3 and 4-7 the softmax of lanes 0 and 1 (a thread a row), warp 8
+// the TMA producer and scheduler, warps 9 and 10 the MMA issuers of lanes 0 and 1. The producer
+// runs ahead: it publishes items in a ring of four descriptors, loads Q into two slots and K and
+// V tiles alternately into one ring of NSLOT slots (224 KB with Q). A page is one TMA box, the
+// lanes of the producer warp issuing one each. All rings and barrier phases run on across items.
+//
+// Trees (PAGED): all key tiles of all items form one sequence, of which every CTA takes an equal
+// run, whatever the lengths; an item cut between CTAs leaves fp32 partial results, which
+// serve_join_kernel joins. Prompts: whole items, longest first in the snake order.
+template <int D>
+struct ServeCfg {
+  static constexpr int NSUB = D / 64;
+  static constexpr int SUB_BYTES = 128 * 128;
+  static constexpr int TILE_BYTES = NSUB * SUB_BYTES;
+  static constexpr int NSLOT = D == 64 ? 12 : 5;
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_R = 2 * TILE_BYTES;
+  static constexpr int OFF_BAR = OFF_R + NSLOT * TILE_BYTES;
+  static constexpr int OFF_DESC = OFF_BAR + 400;   // 4 x 16 ints
+  static constexpr int OFF_ML = OFF_BAR + 768;     // m and l of lane 1's rows, for the join of a dual item
+  static constexpr int SMEM_BYTES = OFF_ML + 1024 + 1024;
+  // TMEM columns as in the forward: d = 64 keeps P apart from S, so that S of the next tile can
+  // be formed while P is still read; d = 128 writes P over S.
+  static constexpr bool SEP_P = D == 64;
+  __device__ static constexpr uint32_t tm_s(int t) { return 128u * t; }
+  __device__ static constexpr uint32_t tm_p(int t) { return SEP_P ? 256u + 64u * t : 128u * t; }
+  __device__ static constexpr uint32_t tm_o(int t) { return SEP_P ? 384u + 64u * t : 256u + (uint32_t)D * t; }
+  static constexpr uint32_t TM_COLS = 512;
+  static constexpr int THREADS = 352;
+  // barriers
+  static constexpr int FULL = 0, EMPTY = NSLOT, Q_FULL = 2 * NSLOT, Q_EMPTY = Q_FULL + 2, S_FULL = Q_EMPTY + 2,
+                       P_READY = S_FULL + 2, O_DONE = P_READY + 2, S_FREE = O_DONE + 2, O_FREE = S_FREE + 2,
+                       MERGE = O_FREE + 2, DRAIN = MERGE + 1, D_FULL = DRAIN + 1, D_EMPTY = D_FULL + 4,
+                       BARS = D_EMPTY + 4;
+};
+static_assert(8 * ServeCfg<64>::BARS + 8 <= 400 && 8 * ServeCfg<128>::BARS + 8 <= 400, "barrier area");
+static_assert(400 + 4 * 64 <= 768, "descriptor area");
+static_assert(ServeCfg<64>::SMEM_BYTES <= 232448 && ServeCfg<128>::SMEM_BYTES <= 232448, "shared memory above 227 KB");
+
+enum { SITE_SW_EMPTY = 60, SITE_SW_Q_FULL, SITE_SW_Q_EMPTY, SITE_SW_K_FULL, SITE_SW_V_FULL, SITE_SW_S_FREE,
+       SITE_SW_P_READY, SITE_SW_O_FREE, SITE_SW_S_FULL, SITE_SW_O_DONE, SITE_SW_MERGE, SITE_SW_DESC_FULL,
+       SITE_SW_DESC_EMPTY, SITE_SW_RELEASE };
+
+// A work item (or the part of it that this CTA computes), as the producer publishes it.
+struct ServeItem {
+  int cnt;     // key tiles here; -1: no more items
+  int flags;   // 1: dual, 2: the whole item is here (results go straight to O)
+  int c0, c1;  // key tiles of lanes 0 and 1
+  int j0;      // first key tile, counted from the item's first
+  int nc;      // tiles of cached tokens; tile j >= nc holds the new tokens from 128 (j - nc)
+  int L, n;    // cached and new tokens of the sequence
+  int row0;    // the sequence's first row among the packed tokens
+  int tok0;    // the pair's first token within the sequence
+  int kvh;
+  int slot;    // partial result slot
+};
+enum { ITEM_DUAL = 1, ITEM_WHOLE = 2 };
+
+// Sizes of sequence b's work; record: whether invalid device values are recorded.
+struct SeqWork {
+  int row0, n, L, nc, nk, pairs;
+  long long tiles;  // all heads and pairs, each counted with the nk tiles of the last one
+};
+template <bool PAGED>
+__device__ __forceinline__ SeqWork seq_work(const ServeArgs& a, int b, int npt, bool record) {
+  SeqWork w;
+  const int lo = a.cu[b], hi = a.cu[b + 1];
+  w.row0 = min(max(lo, 0), a.T);
+  const int end = min(max(hi, w.row0), a.T);
+  if (record && (w.row0 != lo || end != hi)) record_check(a.status, SITE_S_OFFSETS);
+  w.n = end - w.row0;
+  w.L = 0;
+  if (PAGED && w.n > 0) {
+    const int len = a.lens[b];
+    w.L = min(max(len, 0), a.table_width << a.page_shift);
+    if (record && w.L != len) record_check(a.status, SITE_S_LENGTH);
+  }
+  w.nc = (w.L + 127) >> 7;
+  w.nk = w.nc + ((w.n + 127) >> 7);
+  w.pairs = (w.n + 2 * npt - 1) / (2 * npt);
+  w.tiles = (long long)w.pairs * a.Hkv * w.nk;
+  return w;
 }
 
-// One block for each (token, query head): keys in tiles of 128, a key a thread.
+__device__ __forceinline__ long long warp_sum(long long x) {
+  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+// Trees: the run of key tiles of CTA c, by a whole warp.
+struct ServeRuns {
+  long long total;
+  int ctas;  // CTAs with work
+  __device__ long long start(int c) const { return total * c / ctas; }
+};
+__device__ __forceinline__ ServeRuns serve_runs(const ServeArgs& a, int npt, int grid, bool record) {
+  ServeRuns r;
+  long long x = 0;
+  for (int b = threadIdx.x & 31; b < a.B; b += 32) x += seq_work<true>(a, b, npt, record).tiles;
+  r.total = warp_sum(x);
+  r.ctas = (int)min((long long)grid, max(1LL, (r.total + kMinTiles - 1) / kMinTiles));
+  return r;
+}
+// The sequence that tile `pos` of all belongs to, and its first tile; by a whole warp. pos < total.
+__device__ __forceinline__ int serve_seek(const ServeArgs& a, int npt, long long pos, long long* first) {
+  const int lane = threadIdx.x & 31;
+  long long base = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 32) {
+    const long long mine = b0 + lane < a.B ? seq_work<true>(a, b0 + lane, npt, false).tiles : 0;
+    long long incl = mine;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, base + incl > pos);
+    if (past) {
+      const int k = __ffs(past) - 1;
+      *first = base + __shfl_sync(0xffffffffu, incl - mine, k);
+      return b0 + k;
+    }
+    base += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  *first = base;
+  return a.B;
+}
+
+// Key tiles that query tile u (tokens [u npt, ..)) of a sequence needs, counted from the first.
+__device__ __forceinline__ int tiles_of(const SeqWork& w, int u, int npt, bool tree) {
+  if (u * npt >= w.n) return 0;
+  return w.nc + ((min(tree ? w.n : (u + 1) * npt, w.n) + 127) >> 7);
+}
+
+// Prompts: item i of all, longest pairs first: level p holds the p-th pairs of all sequences that
+// have one, in the order of the sequences; by a whole warp. False past the last one.
+__device__ __forceinline__ bool prompt_item(const ServeArgs& a, int npt, long long i, int* b, int* pair) {
+  const int lane = threadIdx.x & 31;
+  auto above = [&](int p) {  // pairs of level p and up
+    long long x = 0;
+    for (int s = lane; s < a.B; s += 32) x += max(0, seq_work<false>(a, s, npt, false).pairs - p);
+    return warp_sum(x);
+  };
+  if (i >= above(0)) return false;
+  int lo = 0, hi = (a.T + 2 * npt - 1) / (2 * npt);  // above(lo) > i >= above(hi)
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (above(mid) > i) lo = mid; else hi = mid;
+  }
+  int left = (int)(i - above(lo + 1));
+  *pair = lo;
+  for (int b0 = 0; b0 < a.B; b0 += 32) {
+    const bool has = b0 + lane < a.B && seq_work<false>(a, b0 + lane, npt, false).pairs > lo;
+    unsigned m = __ballot_sync(0xffffffffu, has);
+    const int k = __popc(m);
+    if (left < k) {
+      for (; left; --left) m &= m - 1;
+      *b = b0 + __ffs(m) - 1;
+      return true;
+    }
+    left -= k;
+  }
+  return false;
+}
+
+template <bool F16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  return F16 ? pack_f16x2(lo, hi) : pack_bf16x2(lo, hi);
+}
+
+template <int D, bool F16, bool PAGED>
+__global__ void __launch_bounds__(352, 1)
+    serve_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                 const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_kc,
+                 const __grid_constant__ CUtensorMap tm_vc, ServeArgs a) {
+  using C = ServeCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = align1024(smem_raw);
+  const uint32_t sbase = smem_u32(sm);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t b0 = sbase + C::OFF_BAR;
+  auto BAR = [&](int i) { return b0 + 8u * i; };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::OFF_BAR + 8 * C::BARS);
+  int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
+  DevStatus st{a.status, abort_flag};
+  int* descs = reinterpret_cast<int*>(sm + C::OFF_DESC);
+  const int npt = 128 / a.G;  // tokens of a query tile
+
+  if (warp == 8 && lane == 0) {
+    for (int i = 0; i < C::NSLOT; ++i) {
+      mbar_init(BAR(C::FULL + i), 1);
+      mbar_init(BAR(C::EMPTY + i), 2);  // both issuers
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(BAR(C::Q_FULL + t), 1);
+      mbar_init(BAR(C::Q_EMPTY + t), 2);
+      mbar_init(BAR(C::S_FULL + t), 1);
+      mbar_init(BAR(C::P_READY + t), 4);
+      mbar_init(BAR(C::O_DONE + t), 1);
+      mbar_init(BAR(C::S_FREE + t), 4);
+      mbar_init(BAR(C::O_FREE + t), 4);
+    }
+    mbar_init(BAR(C::MERGE), 4);
+    mbar_init(BAR(C::DRAIN), 2);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(BAR(C::D_FULL + i), 1);
+      mbar_init(BAR(C::D_EMPTY + i), 10);  // softmax warps and issuers
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tmap(&tm_q);
+    prefetch_tmap(&tm_k);
+    prefetch_tmap(&tm_v);
+    if (PAGED) {
+      prefetch_tmap(&tm_kc);
+      prefetch_tmap(&tm_vc);
+    }
+  }
+  if (warp == 9) {
+    tmem_alloc(smem_u32(tmem_slot), C::TM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  griddep_wait();  // before any access to global memory
+  griddep_launch_dependents();
+
+  // Item i of this CTA, for a consumer warp: false when the CTA must give up.
+  auto next_item = [&](int i, ServeItem* it) {
+    if (!wait_warp_sleep(BAR(C::D_FULL + (i & 3)), (i >> 2) & 1, st, SITE_SW_DESC_FULL)) return false;
+    const int4* d = reinterpret_cast<const int4*>(descs + 16 * (i & 3));
+    const int4 x = d[0], y = d[1], z = d[2];
+    it->cnt = x.x, it->flags = x.y, it->c0 = x.z, it->c1 = x.w;
+    it->j0 = y.x, it->nc = y.y, it->L = y.z, it->n = y.w;
+    it->row0 = z.x, it->tok0 = z.y, it->kvh = z.z, it->slot = z.w;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(BAR(C::D_EMPTY + (i & 3)));
+    return true;
+  };
+
+  if (warp == 8) {
+    // ------------------------------------------------------------ scheduler and TMA producer
+    int items = 0, uq = 0, e = 0;  // items published, Q slots and ring entries used
+    bool ok = true;
+    auto publish = [&](const ServeItem& it) {
+      if (!wait_warp(BAR(C::D_EMPTY + (items & 3)), ((items >> 2) & 1) ^ 1, st, SITE_SW_DESC_EMPTY)) return false;
+      if (lane == 0) {
+        int4* d = reinterpret_cast<int4*>(descs + 16 * (items & 3));
+        d[0] = make_int4(it.cnt, it.flags, it.c0, it.c1);
+        d[1] = make_int4(it.j0, it.nc, it.L, it.n);
+        d[2] = make_int4(it.row0, it.tok0, it.kvh, it.slot);
+        mbar_arrive(BAR(C::D_FULL + (items & 3)));
+      }
+      __syncwarp();
+      ++items;
+      return true;
+    };
+    // Loads the item's query tiles and its key tiles [j0, j0 + cnt).
+    auto run_item = [&](const ServeItem& it, int b) {
+      if (!publish(it)) return false;
+      const int nq = (it.flags & ITEM_DUAL) ? 1 : 2;
+      for (int t = 0; t < nq; ++t, ++uq) {
+        const uint32_t qf = BAR(C::Q_FULL + (uq & 1));
+        if (!wait_warp(BAR(C::Q_EMPTY + (uq & 1)), ((uq >> 1) & 1) ^ 1, st, SITE_SW_Q_EMPTY)) return false;
+        if (elect_one()) mbar_arrive_expect_tx(qf, (uint32_t)(npt * a.G * 128 * C::NSUB));
+        __syncwarp();
+        const uint32_t dst = sbase + C::OFF_Q + (uq & 1) * C::TILE_BYTES;
+        if (lane < C::NSUB)
+          tma_load_3d(dst + lane * C::SUB_BYTES, &tm_q, lane * 64, it.kvh * a.G, it.row0 + it.tok0 + t * npt, qf);
+        __syncwarp();
+      }
+      // page ids of a tile: lane (box r, column block c) = r NSUB + c
+      const int prow = min(1 << a.page_shift, 128);  // rows of a page's box
+      const int r = lane / C::NSUB, c = lane % C::NSUB;
+      auto page_of = [&](int j) {
+        const int pg = (j * 128 + r * prow) >> a.page_shift;
+        const bool there = j < it.j0 + it.cnt && j < it.nc && r * prow < 128 && j * 128 + r * prow < it.L;
+        return there ? a.table[b * a.table_stride + pg] : 0;
+      };
+      int id = PAGED ? page_of(it.j0) : 0;
+      for (int j = it.j0; j < it.j0 + it.cnt; ++j) {
+        const int id_next = PAGED ? page_of(j + 1) : 0;
+        const bool cached = PAGED && j < it.nc;
+        const int k0 = cached ? j * 128 : (j - it.nc) * 128;
+        const int rows = min(128, (cached ? it.L : it.n) - k0);
+        const int box = cached ? prow : PAGED ? kNewBox : 128;
+        const int boxes = (rows + box - 1) / box;
+        int page = id;
+        if (cached && lane < boxes * C::NSUB && (id < 0 || id >= a.n_pages)) {
+          record_check(a.status, SITE_S_PAGE);
+          page = a.n_pages;  // outside the tensor: reads as zeros
+        }
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv, ++e) {
+          const int s = e % C::NSLOT;
+          const uint32_t bar = BAR(C::FULL + s);
+          if (!wait_warp(BAR(C::EMPTY + s), ((e / C::NSLOT) & 1) ^ 1, st, SITE_SW_EMPTY)) return false;
+          if (elect_one()) mbar_arrive_expect_tx(bar, (uint32_t)(boxes * box * 128 * C::NSUB));
+          __syncwarp();
+          if (kWithhold && (e >> 1) == 1) continue;  // test build: this copy never arrives
+          const uint32_t dst = sbase + C::OFF_R + s * C::TILE_BYTES + c * C::SUB_BYTES + r * box * 128;
+          if (lane < boxes * C::NSUB &&
+              FA_CHECK(smem_in(dst, box * 128, sbase + C::OFF_R, sbase + C::OFF_BAR), st, DBG_TMA_LOAD)) {
+            if (cached)
+              tma_load_4d(dst, kv ? &tm_vc : &tm_kc, c * 64, k0 & ((1 << a.page_shift) - 1) & ~127, it.kvh, page, bar);
+            else
+              tma_load_3d(dst, kv ? &tm_v : &tm_k, c * 64, it.row0 + k0 + r * box, it.kvh, bar);
+          }
+          __syncwarp();
+        }
+        id = id_next;
+      }
+      return true;
+    };
+    auto make_item = [&](const SeqWork& w, int kvh, int pair, int j0, int j1, ServeItem* it) {
+      const int n0 = tiles_of(w, 2 * pair, npt, a.mask != nullptr), n1 = tiles_of(w, 2 * pair + 1, npt, a.mask != nullptr);
+      const int nmax = max(n0, n1);
+      const bool dual = n1 == 0;
+      j1 = min(j1, nmax);
+      it->cnt = max(0, j1 - j0);
+      it->flags = (dual ? ITEM_DUAL : 0) | (j0 == 0 && j1 == nmax ? ITEM_WHOLE : 0);
+      it->c0 = dual ? (it->cnt + 1) >> 1 : max(0, min(j1, n0) - j0);
+      it->c1 = dual ? it->cnt >> 1 : it->cnt;
+      it->j0 = j0, it->nc = w.nc, it->L = w.L, it->n = w.n, it->row0 = w.row0, it->tok0 = 2 * pair * npt, it->kvh = kvh;
+      it->slot = 2 * blockIdx.x + (j0 == 0);
+    };
+    ServeItem it;
+    if (PAGED) {
+      const ServeRuns runs = serve_runs(a, npt, gridDim.x, blockIdx.x == 0);
+      if ((int)blockIdx.x < runs.ctas && runs.total > 0) {
+        long long pos = runs.start(blockIdx.x), first = 0;
+        const long long end = runs.start(blockIdx.x + 1);
+        int b = serve_seek(a, npt, pos, &first);
+        while (ok && pos < end) {
+          const SeqWork w = seq_work<PAGED>(a, b, npt, false);
+          while (ok && pos < end && pos - first < w.tiles) {
+            const int q = (int)((pos - first) / w.nk), j0 = (int)((pos - first) % w.nk);
+            const int j1 = (int)min((long long)w.nk, j0 + (end - pos));
+            make_item(w, q % a.Hkv, q / a.Hkv, j0, j1, &it);
+            if (it.cnt > 0) ok = run_item(it, b);
+            pos += j1 - j0;
+          }
+          first += w.tiles;
+          ++b;
+        }
+      }
+    } else {
+      if (blockIdx.x == 0)
+        for (int b = lane; b < a.B; b += 32) seq_work<PAGED>(a, b, npt, true);
+      for (long long round = 0; ok; ++round) {
+        const int G = gridDim.x, c = blockIdx.x;
+        const long long i = round * G + ((round & 1) ? G - 1 - c : c);
+        int b = 0, pair = 0;
+        if (!prompt_item(a, npt, i / a.Hkv, &b, &pair)) break;  // later rounds lie past the end too
+        const SeqWork w = seq_work<PAGED>(a, b, npt, false);
+        make_item(w, (int)(i % a.Hkv), pair, 0, w.nk, &it);
+        ok = run_item(it, b);
+      }
+    }
+    if (ok) {
+      it.cnt = -1;
+      ok = publish(it);
+    }
+    if (*(volatile int*)abort_flag) {
+      // let copies already in flight land before the CTA's shared memory is released
+      for (int x = max(0, e - C::NSLOT); x < e; ++x) {
+        const uint64_t t0 = globaltimer_ns();
+        while (!mbar_try_wait(BAR(C::FULL + x % C::NSLOT), (x / C::NSLOT) & 1) && globaltimer_ns() - t0 < 100000000ull) {
+        }
+      }
+      for (int x = max(0, uq - 2); x < uq; ++x) {
+        const uint64_t t0 = globaltimer_ns();
+        while (!mbar_try_wait(BAR(C::Q_FULL + (x & 1)), (x >> 1) & 1) && globaltimer_ns() - t0 < 100000000ull) {
+        }
+      }
+    }
+  } else if (warp >= 9) {
+    // ------------------------------------------------------------ MMA issuer of lane t
+    const int t = warp - 9;
+    constexpr uint32_t IDESC_S = F16 ? idesc_f16_f32(128, 128, 0, 0) : idesc_bf16_f32(128, 128, 0, 0);
+    constexpr uint32_t IDESC_O = F16 ? idesc_f16_f32(128, D, 0, 1) : idesc_bf16_f32(128, D, 0, 1);
+    constexpr uint32_t HI = sdesc_hi(1024), TILE16 = C::TILE_BYTES >> 4;
+    const uint32_t q_lo = sdesc_lo(sbase + C::OFF_Q, 16), k_lo = sdesc_lo(sbase + C::OFF_R, 16);
+    const uint32_t v_lo = sdesc_lo(sbase + C::OFF_R, C::SUB_BYTES);
+    auto commit = [&](uint32_t bar) {
+      if (elect_one()) mma_commit(bar);
+      __syncwarp();
+    };
+    auto full = [&](int x, int site) {  // ring entry x has landed
+      return wait_warp_sleep(BAR(C::FULL + x % C::NSLOT), (x / C::NSLOT) & 1, st, site);
+    };
+    int e0 = 0, uq = 0, ct = 0, used = 0;  // ring tiles before the item, Q slots, this lane's tiles and items so far
+    bool ok = true;
+    for (int i = 0; ok; ++i) {
+      ServeItem it;
+      if (!next_item(i, &it) || it.cnt < 0) break;
+      const bool dual = it.flags & ITEM_DUAL;
+      const int c = t ? it.c1 : it.c0;
+      const int qu = dual ? uq : uq + t;  // this lane's Q slot use
+      const uint32_t qa = q_lo + (qu & 1) * TILE16;
+      auto tile = [&](int kk) { return dual ? 2 * kk + t : kk; };
+      auto issue_s = [&](int kk) {  // S = Q K^T; then K's slot and, after the last one, Q's are done with
+        const int x = 2 * (e0 + tile(kk));
+        if (!full(x, SITE_SW_K_FULL)) return false;
+        if (C::SEP_P && ct + kk > 0 &&
+            !wait_warp_sleep(BAR(C::S_FREE + t), (ct + kk - 1) & 1, st, SITE_SW_S_FREE))
+          return false;
+        tc_fence_after();
+        const uint32_t ka = k_lo + (x % C::NSLOT) * TILE16, d = tmem + C::tm_s(t);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = ((k >> 2) * C::SUB_BYTES + (k & 3) * 32) >> 4;
+          if (elect_one()) mma_ss(d, sdesc_join(qa + off, HI), sdesc_join(ka + off, HI), IDESC_S, k > 0);
+        }
+        commit(BAR(C::S_FULL + t));
+        commit(BAR(C::EMPTY + x % C::NSLOT));
+        if (kk == c - 1) commit(BAR(C::Q_EMPTY + (qu & 1)));
+        return true;
+      };
+      auto issue_pv = [&](int kk) {  // O += P V
+        const int x = 2 * (e0 + tile(kk)) + 1, s = x % C::NSLOT;
+        if (!full(x, SITE_SW_V_FULL)) return false;
+        const int j = it.j0 + tile(kk);
+        const int rows = j < it.nc ? it.L - j * 128 : it.n - (j - it.nc) * 128;
+        if (rows < 128) {
+          // rows past the sequence may hold anything; P is 0 there, but 0 x NaN is not
+          uint8_t* v = sm + C::OFF_R + s * C::TILE_BYTES;
+          for (int z = lane; z < (128 - rows) * 8 * C::NSUB; z += 32) {
+            const int cb = z / ((128 - rows) * 8), w = z % ((128 - rows) * 8);
+            *reinterpret_cast<uint4*>(v + cb * C::SUB_BYTES + rows * 128 + w * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        if (!wait_warp_sleep(BAR(C::P_READY + t), (ct + kk) & 1, st, SITE_SW_P_READY)) return false;
+        if (kk == 0 && used > 0 && !wait_warp_sleep(BAR(C::O_FREE + t), (used - 1) & 1, st, SITE_SW_O_FREE)) return false;
+        tc_fence_after();
+        const uint32_t va = v_lo + s * TILE16, d = tmem + C::tm_o(t), pa = tmem + C::tm_p(t);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (elect_one()) mma_ts(d, pa + k * 8, sdesc_join(va + k * (2048 >> 4), HI), IDESC_O, (kk | k) != 0);
+        commit(BAR(C::O_DONE + t));
+        commit(BAR(C::EMPTY + s));
+        return true;
+      };
+      auto release = [&](uint32_t full_bar, uint32_t parity, uint32_t empty_bar) {  // what this lane does not read
+        if (!wait_warp_sleep(full_bar, parity, st, SITE_SW_RELEASE)) return false;
+        if (elect_one()) mbar_arrive(empty_bar);
+        __syncwarp();
+        return true;
+      };
+      if (c > 0)
+        ok = wait_warp_sleep(BAR(C::Q_FULL + (qu & 1)), (qu >> 1) & 1, st, SITE_SW_Q_FULL) && issue_s(0);
+      int kk = 0;
+      for (int j = 0; ok && j < it.cnt; ++j) {
+        if (kk < c && tile(kk) == j) {
+          if (C::SEP_P && kk + 1 < c && !(ok = issue_s(kk + 1))) break;
+          if (!(ok = issue_pv(kk))) break;
+          if (!C::SEP_P && kk + 1 < c && !(ok = issue_s(kk + 1))) break;
+          ++kk;
+        } else {
+          const int x = 2 * (e0 + j);
+          ok = release(BAR(C::FULL + x % C::NSLOT), (x / C::NSLOT) & 1, BAR(C::EMPTY + x % C::NSLOT)) &&
+               release(BAR(C::FULL + (x + 1) % C::NSLOT), ((x + 1) / C::NSLOT) & 1, BAR(C::EMPTY + (x + 1) % C::NSLOT));
+        }
+      }
+      // Q slots that this lane did not read
+      for (int u = uq; ok && u < uq + (dual ? 1 : 2); ++u)
+        if (u != qu || c == 0)
+          ok = release(BAR(C::Q_FULL + (u & 1)), (u >> 1) & 1, BAR(C::Q_EMPTY + (u & 1)));
+      e0 += it.cnt;
+      uq += dual ? 1 : 2;
+      ct += c;
+      used += c > 0;
+    }
+    // every MMA issued has completed before TMEM is released
+    commit(BAR(C::DRAIN));
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(BAR(C::DRAIN), 0) && globaltimer_ns() - t0 < kWaitLimitNs) {
+    }
+  } else {
+    // ------------------------------------------------------------ softmax of lane t
+    const int t = warp >> 2, wq = warp & 3;
+    const int row = wq * 32 + lane;
+    const int rn = row / a.G, rg = row - rn * a.G;  // token and head of the row within its tile
+    const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
+    const uint32_t tS = tmem + lane_off + C::tm_s(t), tP = tmem + lane_off + C::tm_p(t);
+    const float sl2 = a.scale_log2;
+    float* ml = reinterpret_cast<float*>(sm + C::OFF_ML);
+    int ct0 = 0, ct1 = 0, merges = 0;  // tiles of both lanes and joins of dual items so far
+    for (int i = 0;; ++i) {
+      ServeItem it;
+      if (!next_item(i, &it) || it.cnt < 0) break;
+      const bool dual = it.flags & ITEM_DUAL, whole = it.flags & ITEM_WHOLE;
+      const int c = t ? it.c1 : it.c0, ct = t ? ct1 : ct0;
+      const int tok = it.tok0 + (dual ? 0 : t * npt) + rn;
+      const bool valid = rn < npt && tok < it.n;
+      const bool any = __any_sync(0xffffffffu, valid);
+      float m_run = -INFINITY, l_run = 0.f;
+      bool ok = true;
+      for (int kk = 0; kk < c; ++kk) {
+        if (!(ok = wait_warp_sleep(BAR(C::S_FULL + t), (ct + kk) & 1, st, SITE_SW_S_FULL))) break;
+        if (!any) {  // no row here: P stays what it is, its rows of O are nobody's
+          __syncwarp();
+          if (C::SEP_P) {
+            if (lane == 0) mbar_arrive(BAR(C::S_FREE + t));
+            // S of this tile may be there before the other warps have written P of the one before:
+            // an arrival now would count for that one
+            if (kk > 0 && !(ok = wait_warp_sleep(BAR(C::O_DONE + t), (ct + kk - 1) & 1, st, SITE_SW_O_DONE))) break;
+          }
+          if (lane == 0) mbar_arrive(BAR(C::P_READY + t));
+          continue;
+        }
+        tc_fence_after();
+        float sv[128];
+        {
+          uint32_t r[4][32];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) tmem_ld32(tS + q * 32, r[q]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int x = 0; x < 32; ++x) sv[q * 32 + x] = __uint_as_float(r[q][x]);
+        }
+        if (C::SEP_P) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(BAR(C::S_FREE + t));
+        }
+        const int j = it.j0 + (dual ? 2 * kk + t : kk);
+        if (PAGED && a.mask && j >= it.nc) {
+          const int k0 = (j - it.nc) * 128;
+          const uint32_t* words = a.mask + (long long)(it.row0 + tok) * a.words;
+          uint32_t w[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int left = it.n - k0 - 32 * q;  // nodes from this word on
+            w[q] = valid && left > 0 && (k0 >> 5) + q < a.words ? words[(k0 >> 5) + q] : 0u;
+            if (left > 0 && left < 32) w[q] &= (1u << left) - 1;
+          }
+#pragma unroll
+          for (int x = 0; x < 128; ++x)
+            if (!(w[x >> 5] >> (x & 31) & 1)) sv[x] = -INFINITY;
+        } else {
+          // keys [0, lim) of the tile are seen
+          const int lim = (PAGED && j < it.nc) ? it.L - j * 128 : min(it.n, tok + 1) - (j - it.nc) * 128;
+          if (__any_sync(0xffffffffu, lim < 128)) {
+#pragma unroll
+            for (int x = 0; x < 128; ++x)
+              if (x >= lim) sv[x] = -INFINITY;
+          }
+        }
+        float pm[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) pm[u] = sv[u];
+#pragma unroll
+        for (int x = 4; x < 124; x += 8)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) pm[u] = fmax3(pm[u], sv[x + 2 * u], sv[x + 2 * u + 1]);
+        const float mx = fmax3(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3]), fmax3(sv[124], sv[125], fmaxf(sv[126], sv[127])));
+        const float m_tile = mx * sl2;
+        // the reference maximum moves only when it grows by more than 2^8; O and l share it
+        float f = 1.f;
+        bool rescale_warp = false;
+        if (kk == 0) {
+          m_run = m_tile;
+        } else {
+          const bool grow = valid && m_tile > m_run + 8.0f;
+          rescale_warp = __any_sync(0xffffffffu, grow);
+          if (grow) {
+            f = ex2_approx(m_run - m_tile);
+            m_run = m_tile;
+          }
+        }
+        const float base = (m_run == -INFINITY) ? 0.f : m_run;
+        const uint64_t sl2x2 = f2_pack(sl2, sl2), nbase2 = f2_pack(-base, -base);
+        uint64_t ps2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+        uint32_t pk[4][16];
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+#pragma unroll
+          for (int x = 0; x < 16; ++x) {
+            float x0, x1;
+            f2_unpack(f2_fma(f2_pack(sv[h * 32 + 2 * x], sv[h * 32 + 2 * x + 1]), sl2x2, nbase2), x0, x1);
+            const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+            ps2[x & 1] = f2_add(ps2[x & 1], f2_pack(p0, p1));
+            pk[h][x] = pack2<F16>(p0, p1);
+          }
+          if (C::SEP_P && h == 1) {
+            if (kk > 0) {  // PV of the tile before has read P (across items its epilogue waited for that)
+              if (!(ok = wait_warp_sleep(BAR(C::O_DONE + t), (ct + kk - 1) & 1, st, SITE_SW_O_DONE))) break;
+              tc_fence_after();
+            }
+            tmem_st16(tP, pk[0]);
+            tmem_st16(tP + 16, pk[1]);
+          }
+          if (!C::SEP_P || h >= 2) tmem_st16(tP + h * 16, pk[h]);
+        }
+        if (!ok) break;
+        float ps[4];
+        f2_unpack(ps2[0], ps[0], ps[1]);
+        f2_unpack(ps2[1], ps[2], ps[3]);
+        l_run = l_run * f + ((ps[0] + ps[1]) + (ps[2] + ps[3]));
+        if (rescale_warp) {
+          if (!C::SEP_P) {
+            if (!(ok = wait_warp_sleep(BAR(C::O_DONE + t), (ct + kk - 1) & 1, st, SITE_SW_O_DONE))) break;
+            tc_fence_after();
+          }
+          const uint32_t tO = tmem + lane_off + C::tm_o(t);
+          uint32_t r[32];
+#pragma unroll
+          for (int q = 0; q < D / 32; ++q) {
+            tmem_ld32(tO + q * 32, r);
+            tmem_wait_ld();
+#pragma unroll
+            for (int x = 0; x < 32; ++x) r[x] = __float_as_uint(__uint_as_float(r[x]) * f);
+            tmem_st32(tO + q * 32, r);
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(C::P_READY + t));
+      }
+      if (ok && c > 0) ok = wait_warp_sleep(BAR(C::O_DONE + t), (ct + c - 1) & 1, st, SITE_SW_O_DONE);
+      if (!ok) break;
+      tc_fence_after();
+      const bool join = dual && it.c1 > 0;
+      float f0 = 1.f, f1 = 0.f;
+      if (join) {
+        if (t == 1) {
+          ml[row] = m_run;
+          ml[128 + row] = l_run;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(BAR(C::MERGE));
+        } else {
+          if (!wait_warp_sleep(BAR(C::MERGE), merges & 1, st, SITE_SW_MERGE) ||
+              !wait_warp_sleep(BAR(C::O_DONE + 1), (ct1 + it.c1 - 1) & 1, st, SITE_SW_O_DONE))
+            break;
+          tc_fence_after();
+          const float m1 = ml[row], m = fmaxf(m_run, m1), base = m == -INFINITY ? 0.f : m;
+          f0 = ex2_approx(m_run - base);
+          f1 = ex2_approx(m1 - base);
+          l_run = l_run * f0 + ml[128 + row] * f1;
+          m_run = m;
+        }
+        ++merges;
+      }
+      ct0 += it.c0;
+      ct1 += it.c1;
+      if (dual && t == 1) continue;  // lane 0 writes the results
+      // l = 0: no key; NaN stays NaN
+      const float inv = l_run != 0.f ? 1.f / l_run : 0.f;
+      const float lse2 = l_run != 0.f ? m_run + lg2_approx(l_run) : -INFINITY;
+      const long long part = (long long)it.slot * 256 + (dual ? 0 : t * 128) + row;
+      if (c == 0) {  // (a cut item only) none of this part's keys concerns this tile
+        if (valid && FA_CHECK(in_range(part, a.part_rows), st, DBG_GLOBAL_STORE)) a.part_lse[part] = -INFINITY;
+        continue;
+      }
+      const int h = it.kvh * a.G + rg;
+      const long long token = it.row0 + tok;
+      f0 *= inv;
+      f1 *= inv;
+      const bool write = valid && FA_CHECK(whole ? in_range(token, a.T) : in_range(part, a.part_rows), st, DBG_GLOBAL_STORE);
+      uint16_t* orow = a.o + token * a.o_st + h * a.o_sh;
+      float4* prow = reinterpret_cast<float4*>(a.part_o + part * D);
+      if (any) {
+#pragma unroll
+        for (int q = 0; q < D / 32; ++q) {
+          uint32_t r[32];
+          float v[32];
+          tmem_ld32(tmem + lane_off + C::tm_o(t) + q * 32, r);
+          tmem_wait_ld();
+#pragma unroll
+          for (int x = 0; x < 32; ++x) v[x] = __uint_as_float(r[x]) * f0;
+          if (join) {
+            tmem_ld32(tmem + lane_off + C::tm_o(1) + q * 32, r);
+            tmem_wait_ld();
+#pragma unroll
+            for (int x = 0; x < 32; ++x) v[x] = fmaf(__uint_as_float(r[x]), f1, v[x]);
+          }
+          if (q == D / 32 - 1) {  // O is in registers: the issuers may write it again
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(BAR(C::O_FREE + t));
+              if (join) mbar_arrive(BAR(C::O_FREE + 1));
+            }
+          }
+          if (write && whole) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              *reinterpret_cast<uint4*>(orow + q * 32 + x * 8) =
+                  make_uint4(pack2<F16>(v[8 * x], v[8 * x + 1]), pack2<F16>(v[8 * x + 2], v[8 * x + 3]),
+                             pack2<F16>(v[8 * x + 4], v[8 * x + 5]), pack2<F16>(v[8 * x + 6], v[8 * x + 7]));
+          } else if (write) {
+#pragma unroll
+            for (int x = 0; x < 8; ++x) prow[q * 8 + x] = make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
+          }
+        }
+        if (write && !whole) a.part_lse[part] = lse2;
+        if (write && whole && a.lse) a.lse[(long long)h * a.T + token] = lse2 * 0.6931471805599453f;
+      } else if (lane == 0) {
+        mbar_arrive(BAR(C::O_FREE + t));
+        if (join) mbar_arrive(BAR(C::O_FREE + 1));
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TM_COLS);
+  }
+}
+
+// Joins the partial results of the items that CTA boundaries cut: block (x, y) takes rows
+// [32 y, 32 y + 32) of the item that boundary x + 1 is the first to cut. A warp a row at d = 128,
+// half a warp at d = 64; the parts' weights come from their LSEs, as between key tiles.
 template <int D, bool F16>
-__global__ void __launch_bounds__(128) serve_rows_kernel(ServeArgs a) {
+__global__ void __launch_bounds__(256) serve_join_kernel(ServeArgs a, int grid) {
   griddep_wait();
   griddep_launch_dependents();
-  __shared__ float qs[D], ps[128], red[4];
-  const int t = blockIdx.x, h = blockIdx.y, tid = threadIdx.x;
-  if (t == 0 && h == 0) check_offsets(a.cu, a.B, a.T, a.status);
-  const int b = find_sequence(a.cu, a.B, t);
-  if (b < 0) return;
-  const SeqRange r = seq_range(a.cu, b, a.T, a.status);
-  if (t < r.lo || t >= r.hi) return;
-  const int kvh = h / a.G, node = t - r.lo, n = r.hi - r.lo;
-  int ctx = 0;
-  if (a.table) {
-    const int cap = a.table_width << a.page_shift;
-    ctx = min(max(a.lens[b], 0), cap);
-    if (ctx != a.lens[b]) record_check(a.status, SITE_S_LENGTH);
+  __shared__ int info[8];  // parts, tokens, row0, tok0, kvh
+  const int npt = 128 / a.G, c = blockIdx.x + 1;
+  if (threadIdx.x < 32) {
+    int parts = 0;
+    const ServeRuns runs = serve_runs(a, npt, grid, false);
+    SeqWork w = {};
+    int q = 0;
+    if (c < runs.ctas && runs.total > 0) {
+      const long long pos = runs.start(c);
+      long long first;
+      const int b = serve_seek(a, npt, pos, &first);
+      w = seq_work<true>(a, b, npt, false);
+      q = (int)((pos - first) / w.nk);
+      const long long item = first + (long long)q * w.nk;
+      const int pair = q / a.Hkv;
+      const int nmax = max(tiles_of(w, 2 * pair, npt, a.mask != nullptr), tiles_of(w, 2 * pair + 1, npt, a.mask != nullptr));
+      if (runs.start(c - 1) <= item && pos > item)
+        for (int k = c; k < runs.ctas && runs.start(k) < item + nmax; ++k) ++parts;
+    }
+    if (threadIdx.x == 0) {
+      info[0] = parts;
+      info[1] = w.n, info[2] = w.row0, info[3] = q / a.Hkv * 2 * npt, info[4] = q % a.Hkv;
+    }
   }
-  if (tid < D) qs[tid] = to_f32<F16>(a.q[t * a.q_st + h * a.q_sh + tid]) * a.scale_log2;
   __syncthreads();
-  const int total = ctx + (a.mask ? n : node + 1);
-  float m = -INFINITY, l = 0.f, acc = 0.f;
-  for (int j0 = 0; j0 < total; j0 += 128) {
-    const int j = j0 + tid;
-    bool seen = j < total;
-    const uint16_t *kr = nullptr, *vr = nullptr;
-    if (seen && j < ctx) {
-      const int id = a.table[b * a.table_stride + (j >> a.page_shift)];
-      if (id < 0 || id >= a.n_pages) {
-        record_check(a.status, SITE_S_PAGE);
-      } else {
-        const long long off = id * a.c_sp + kvh * a.c_sh + (j & ((1 << a.page_shift) - 1)) * a.c_st;
-        kr = a.kc + off;
-        vr = a.vc + off;
-      }
-    } else if (seen) {
-      const int i = j - ctx;
-      if (a.mask) seen = i < 32 * a.words && (a.mask[(long long)t * a.words + (i >> 5)] >> (i & 31) & 1);
-      kr = a.k + (r.lo + i) * a.k_st + kvh * a.k_sh;
-      vr = a.v + (r.lo + i) * a.v_st + kvh * a.v_sh;
+  const int parts = info[0] + 1;  // part 0: CTA c - 1's last item; then the first items of c, c + 1, ..
+  if (parts == 1) return;
+  constexpr int LPR = D / 4;  // lanes a row
+  const int sub = threadIdx.x % LPR;
+  for (int row = blockIdx.y * 32 + threadIdx.x / LPR; row < blockIdx.y * 32 + 32; row += 256 / LPR) {
+    const int rr = row & 127, rn = rr / a.G, rg = rr - rn * a.G;
+    const int tok = info[3] + (row >> 7) * npt + rn;
+    if (rn >= npt || tok >= info[1]) continue;
+    auto at = [&](int k) { return (long long)(k == 0 ? 2 * (c - 1) + 1 : 2 * (c - 1 + k)) * 256 + row; };
+    float m = -INFINITY;
+    for (int k = 0; k < parts; ++k) m = fmaxf(m, a.part_lse[at(k)]);
+    const float base = m == -INFINITY ? 0.f : m;
+    float l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < parts; ++k) {
+      const float s = a.part_lse[at(k)];
+      if (s == -INFINITY) continue;  // nothing was written there
+      const float w = ex2_approx(s - base);
+      const float4 x = *reinterpret_cast<const float4*>(a.part_o + at(k) * D + 4 * sub);
+      l += w;
+      o.x = fmaf(w, x.x, o.x), o.y = fmaf(w, x.y, o.y), o.z = fmaf(w, x.z, o.z), o.w = fmaf(w, x.w, o.w);
     }
-    float s = -INFINITY;
-    if (seen) {
-      s = 0.f;
-      if (kr)
-        for (int c = 0; c < D; ++c) s = fmaf(qs[c], to_f32<F16>(kr[c]), s);
-    }
-    float mx = s;
-    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    if ((tid & 31) == 0) red[tid >> 5] = mx;
-    __syncthreads();
-    const float mn = fmaxf(m, fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])));
-    const float base = mn == -INFINITY ? 0.f : mn;
-    ps[tid] = exp2f(s - base);
-    const float f = exp2f((m == -INFINITY ? base : m) - base);
-    __syncthreads();
-    l *= f;
-    acc *= f;
-    m = mn;
-    for (int i = 0; i < 128 && j0 + i < total; ++i) {
-      const float p = ps[i];
-      l += p;
-      if (p == 0.f || tid >= D) continue;
-      const int jj = j0 + i;
-      const uint16_t* row;
-      if (jj < ctx) {
-        const int id = a.table[b * a.table_stride + (jj >> a.page_shift)];
-        if (id < 0 || id >= a.n_pages) continue;
-        row = a.vc + id * a.c_sp + kvh * a.c_sh + (jj & ((1 << a.page_shift) - 1)) * a.c_st;
-      } else {
-        row = a.v + (r.lo + jj - ctx) * a.v_st + kvh * a.v_sh;
-      }
-      acc = fmaf(p, to_f32<F16>(row[tid]), acc);
-    }
-    __syncthreads();
+    const float inv = l != 0.f ? 1.f / l : 0.f;
+    const int h = info[4] * a.G + rg;
+    const long long token = info[2] + tok;
+    *reinterpret_cast<uint2*>(a.o + token * a.o_st + h * a.o_sh + 4 * sub) =
+        make_uint2(pack2<F16>(o.x * inv, o.y * inv), pack2<F16>(o.z * inv, o.w * inv));
+    if (sub == 0 && a.lse)
+      a.lse[(long long)h * a.T + token] = (l != 0.f ? m + lg2_approx(l) : -INFINITY) * 0.6931471805599453f;
   }
-  const float o = l != 0.f ? acc / l : 0.f;  // NaN stays NaN
-  if (tid < D)
-    a.o[t * a.o_st + h * a.o_sh + tid] =
-        F16 ? __half_as_ushort(__float2half_rn(o)) : __bfloat16_as_ushort(__float2bfloat16_rn(o));
-  if (tid == 0 && a.lse) a.lse[(long long)h * a.T + t] = l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+}
+
+template <int D, bool F16, bool PAGED>
+static int launch_serve_d(ServeArgs a, cudaStream_t stream) {
+  using C = ServeCfg<D>;
+  const auto type = F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  CUtensorMap mq, mk, mv, mkc = {}, mvc = {};
+  auto map3 = [&](CUtensorMap* m, const uint16_t* p, long long st, long long sh, bool heads_inner, int heads, int box1,
+                  int box2) {
+    const cuuint64_t T = (cuuint64_t)a.T, H = (cuuint64_t)heads, sT = (cuuint64_t)st * 2, sH = (cuuint64_t)sh * 2;
+    const cuuint64_t dims[3] = {D, heads_inner ? H : T, heads_inner ? T : H};
+    const cuuint64_t strides[2] = {heads_inner ? sH : sT, heads_inner ? sT : sH};
+    const cuuint32_t box[3] = {64, (cuuint32_t)box1, (cuuint32_t)box2};
+    return make_tmap_strided(m, p, type, 3, dims, strides, box);
+  };
+  auto map4 = [&](CUtensorMap* m, const uint16_t* p) {
+    const int page = 1 << a.page_shift;
+    const cuuint64_t dims[4] = {D, (cuuint64_t)page, (cuuint64_t)a.Hkv, (cuuint64_t)a.n_pages};
+    const cuuint64_t strides[3] = {(cuuint64_t)a.c_st * 2, (cuuint64_t)a.c_sh * 2, (cuuint64_t)a.c_sp * 2};
+    const cuuint32_t box[4] = {64, (cuuint32_t)std::min(page, 128), 1, 1};
+    return make_tmap_strided(m, p, type, 4, dims, strides, box);
+  };
+  const int box = PAGED ? kNewBox : 128;
+  if (!map3(&mq, a.q, a.q_st, a.q_sh, true, a.Hq, a.G, 128 / a.G) || !map3(&mk, a.k, a.k_st, a.k_sh, false, a.Hkv, box, 1) ||
+      !map3(&mv, a.v, a.v_st, a.v_sh, false, a.Hkv, box, 1) || (PAGED && (!map4(&mkc, a.kc) || !map4(&mvc, a.vc))))
+    return cuda_fail("cuTensorMapEncodeTiled", 0, "tensor map rejected");
+  const auto kernel = serve_kernel<D, F16, PAGED>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+  if (e != cudaSuccess) return cuda_fail("cudaFuncSetAttribute", (int)e, cudaGetErrorName(e));
+  int sms = 0;
+  if (!sm_count(&sms)) return FA_ERR_CUDA;
+  int grid = sms;
+  if (!PAGED) {  // no more CTAs than items could exist
+    const long long pairs = ((long long)a.T * a.G + 255) / 256 + a.B;  // G rows a token; a pair has at least 129 of them
+    grid = (int)std::min<long long>(sms, std::max<long long>(1, 2 * pairs * a.Hkv));
+  }
+  int rc = launch_pdl("serve_kernel", kernel, dim3(grid), dim3(C::THREADS), C::SMEM_BYTES, stream, mq, mk, mv, mkc, mvc, a);
+  if (rc != FA_OK || !PAGED || grid < 2) return rc;
+  return launch_pdl("serve_join_kernel", serve_join_kernel<D, F16>, dim3(grid - 1, 8), dim3(256), 0, stream, a, grid);
 }
 
 static int launch_serve(const ServeArgs& a, int d, int dtype, cudaStream_t stream) {
-  const dim3 grid(a.T, a.Hq), block(128);
-  if (d == 64) return dtype == FA_FP16 ? launch_pdl("serve_rows_kernel", serve_rows_kernel<64, true>, grid, block, 0, stream, a)
-                                       : launch_pdl("serve_rows_kernel", serve_rows_kernel<64, false>, grid, block, 0, stream, a);
-  return dtype == FA_FP16 ? launch_pdl("serve_rows_kernel", serve_rows_kernel<128, true>, grid, block, 0, stream, a)
-                          : launch_pdl("serve_rows_kernel", serve_rows_kernel<128, false>, grid, block, 0, stream, a);
+  const bool f16 = dtype == FA_FP16, paged = a.table != nullptr;
+#define FA_SERVE(DD, FF) (paged ? launch_serve_d<DD, FF, true>(a, stream) : launch_serve_d<DD, FF, false>(a, stream))
+  if (d == 64) return f16 ? FA_SERVE(64, true) : FA_SERVE(64, false);
+  return f16 ? FA_SERVE(128, true) : FA_SERVE(128, false);
+#undef FA_SERVE
 }
 
 }  // namespace fa
@@ -217,6 +965,11 @@ int forward(const fa_rows* q, const fa_rows* k, const fa_rows* v, const fa_rows*
   a.cu = cu;
   a.B = B, a.T = T, a.Hq = Hq, a.Hkv = Hkv, a.G = Hq / Hkv;
   a.scale_log2 = scale * 1.4426950408889634f;
+  int sms = 0;
+  if (!fa::sm_count(&sms)) return FA_ERR_CUDA;
+  a.part_rows = 2LL * sms * 256;
+  a.part_o = static_cast<float*>(workspace);
+  a.part_lse = a.part_o + a.part_rows * d;
   a.status = status;
   return fa::launch_serve(a, d, dtype, reinterpret_cast<cudaStream_t>(stream));
 }

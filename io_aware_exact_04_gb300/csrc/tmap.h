@@ -52,4 +52,16 @@ inline bool make_tmap_2d(CUtensorMap* map, const void* base, CUtensorMapDataType
   return r == CUDA_SUCCESS;
 }
 
+// Map of any rank over 16-bit elements with 128-byte swizzling: dims, strides (in bytes, of the
+// dimensions 1 ..) and box as cuTensorMapEncodeTiled takes them; zero outside the dims.
+inline bool make_tmap_strided(CUtensorMap* map, const void* base, CUtensorMapDataType dtype, int rank,
+                              const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box) {
+  auto enc = tmap_encoder();
+  if (!enc) return false;
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  CUresult r = enc(map, dtype, rank, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 }  // namespace fa
