@@ -293,10 +293,10 @@ typedef struct {
  * does not reach its results, whatever it holds; a NaN or infinity in a token of
  * the sequence itself may reach its earlier tokens within 128 keys of it.
  * Decreasing offsets or ones past T record FA_ERR_DEVICE_CHECK; the sequence is
- * then cut to the tokens that exist. workspace as for fa_forward_tree. */
+ * then cut to the tokens that exist. */
 FA_API int fa_forward_prompt(const fa_rows* q, const fa_rows* k, const fa_rows* v, const fa_rows* o, float* lse,
                              const int32_t* cu_seqlens, int B, int T, int Hq, int Hkv, int d, int dtype, float scale,
-                             void* workspace, size_t workspace_bytes, fa_stream_t stream);
+                             fa_stream_t stream);
 
 /* Attention of drafted tokens ("nodes") over a cache in pages and over each
  * other. Sequence b has lens[b] tokens in the cache (device int32 [B]) and the
@@ -324,8 +324,8 @@ FA_API int fa_forward_tree(const fa_rows* q, const fa_rows* k, const fa_rows* v,
                            int mask_words, int B, int T, int Hq, int Hkv, int d, int dtype, float scale,
                            void* workspace, size_t workspace_bytes, fa_stream_t stream);
 
-/* Workspace bytes of fa_forward_tree and fa_forward_prompt on the current
- * device: two partial results of 256 rows for each SM. 0 for an unsupported d. */
+/* Workspace bytes of fa_forward_tree on the current device: two partial results
+ * of 256 rows for each SM. 0 for an unsupported d. */
 FA_API size_t fa_forward_tree_workspace_size(int d);
 
 /* Which nodes a node of a tree sees: itself and its ancestors. parents: device

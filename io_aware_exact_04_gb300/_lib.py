@@ -49,7 +49,7 @@ _pool = ctypes.POINTER(Pool)
 
 SIGNATURES = {
     "libfa.so": {
-        "fa_forward_prompt": (_i, [_rows, _rows, _rows, _rows, _vp, _vp, _i, _i, _i, _i, _i, _i, _f, _vp, _sz, _vp]),
+        "fa_forward_prompt": (_i, [_rows, _rows, _rows, _rows, _vp, _vp, _i, _i, _i, _i, _i, _i, _f, _vp]),
         "fa_forward_tree": (_i, [_rows, _rows, _rows, _rows, _vp, _pages, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i,
                                  _f, _vp, _sz, _vp]),
         "fa_forward_tree_workspace_size": (_sz, [_i]),

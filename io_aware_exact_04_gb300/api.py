@@ -203,93 +203,126 @@ def device_status(device=None):
 
 # ------------------------------------------------------------------ serving
 # Prompts, drafted trees over a cache in pages, and the cache's own work (include/fa.h, "serving").
+# Their smallest calls take a few microseconds on the GPU, so the checks here are written to cost
+# little where nothing is wrong: one condition a tensor, the reasons worked out only after it fails.
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1}  # fa_dtype
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_FP32, _INT32, _UINT8 = torch.float32, torch.int32, torch.uint8
 
 
-def _rows(name: str, t: torch.Tensor, like: Optional[torch.Tensor], heads: Optional[int] = None,
-          tokens: Optional[int] = None) -> _lib.Rows:
+def _call(name: str, index: int, *args) -> None:
+    """One entry point on device `index` and its current stream."""
+    fn = getattr(_lib.load("libfa.so"), name)
+    if torch.cuda.current_device() == index:
+        rc = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, _raw_stream(index))
+    if rc:
+        _lib.check(rc, name)
+
+
+def _first(name: str, t: torch.Tensor, dim: int) -> int:
+    """The device of the tensor that the others of a call go by, once its type is one that is served."""
+    if not t.is_cuda or t.dtype not in _DTYPES or t.dim() != dim:
+        raise ValueError(f"{name} must be a bfloat16 or float16 CUDA tensor of {dim} dimensions")
+    return t.get_device()
+
+
+def _rows(name: str, t: torch.Tensor, index: int, dtype, T: int, H: int, d: int) -> _lib.Rows:
     """fa_rows of a [T, H, d] tensor: d contiguous, the other strides positive multiples of 8."""
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [T, H, d], is {tuple(t.shape)}")
-    T, H, d = t.shape
-    if not t.is_cuda or t.dtype not in _DTYPES:
-        raise ValueError(f"{name} must be a bfloat16 or float16 CUDA tensor")
-    if like is not None and (t.dtype != like.dtype or t.device != like.device or d != like.shape[2]):
-        raise ValueError(f"{name} must have q's (k's) dtype, device and head dim")
-    if (heads is not None and H != heads) or (tokens is not None and T != tokens):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(tokens, heads, d)}")
+    if not t.is_cuda or t.get_device() != index or t.dtype is not dtype or t.shape != (T, H, d):
+        raise ValueError(f"{name} must be a {dtype} tensor {(T, H, d)} on cuda:{index}, is {t.dtype} {tuple(t.shape)} on {t.device}")
     st, sh, sd = t.stride()
     # the stride of a dimension of one element is never used: any valid value will do
-    st, sh = (st if T > 1 else 8), (sh if H > 1 else 8)
-    if (sd != 1 and d > 1) or st <= 0 or sh <= 0 or st % 8 or sh % 8:
+    if T <= 1:
+        st = 8
+    if H <= 1:
+        sh = 8
+    if (sd != 1 and d > 1) or st <= 0 or sh <= 0 or (st | sh) & 7:
         raise ValueError(f"{name} has strides {t.stride()}: the last must be 1, the others positive multiples of 8")
     return _lib.Rows(t.data_ptr(), st, sh)
 
 
-def _int32(name: str, t: torch.Tensor, device, shape=None, dim: int = 1) -> torch.Tensor:
-    if t.dtype != torch.int32 or t.dim() != dim or not t.is_contiguous() or t.device != device:
-        raise ValueError(f"{name} must be a contiguous int32 tensor of {dim} dimension(s) on {device}")
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
-    return t
+def _ints(name: str, t: torch.Tensor, index: int, shape) -> int:
+    """The address of a contiguous int32 tensor of a given shape."""
+    if t.dtype is not _INT32 or t.shape != shape or not t.is_cuda or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor {tuple(shape)} on cuda:{index}, is {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
 
 
-def _cu_of(cu: torch.Tensor, device) -> int:
-    """The number of sequences of token offsets."""
-    _int32("cu", cu, device)
-    if cu.numel() < 1:
-        raise ValueError("cu holds the offsets of B sequences and the end: at least one entry")
-    return cu.numel() - 1
+def _offsets(cu: torch.Tensor, index: int):
+    """The address of token offsets and how many sequences they bound."""
+    if cu.dim() != 1 or cu.shape[0] < 1:
+        raise ValueError("cu holds the offsets of B sequences and the end: int32 [B + 1]")
+    B = cu.shape[0] - 1
+    return _ints("cu", cu, index, (B + 1,)), B
 
 
-def _pages_of(k_cache: torch.Tensor, v_cache: torch.Tensor, table: torch.Tensor, like: torch.Tensor, hkv: int,
-              B: int) -> _lib.Pages:
+def _workspace(workspace, need: int, index: int):
+    if workspace is None:
+        return torch.empty(need, dtype=_UINT8, device=index)
+    if workspace.dtype is not _UINT8 or not workspace.is_cuda or workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on cuda:{index}")
+    return workspace
+
+
+def _pages(k_cache: torch.Tensor, v_cache: torch.Tensor, table: torch.Tensor, index: int, dtype, H: int, d: int,
+           B: int) -> _lib.Pages:
     """fa_pages of [n_pages, Hkv, page_size, d] caches and an int32 [>= B, width] table."""
-    for name, c in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if c.dim() != 4 or c.dtype != like.dtype or c.device != like.device:
-            raise ValueError(f"{name} must be [n_pages, Hkv, page_size, d] with k's dtype and device")
-        if c.shape[0] < 1 or c.shape[1] != hkv or c.shape[3] != like.shape[2]:
-            raise ValueError(f"{name} has shape {tuple(c.shape)}: {hkv} heads of {like.shape[2]} are expected")
-    if k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
-        raise ValueError("k_cache and v_cache must have the same shape and strides")
-    n, H, page, d = k_cache.shape
-    sp, sh, st, sd = k_cache.stride()
-    sp, sh = (sp if n > 1 else 8), (sh if H > 1 else 8)
-    if sd != 1 or min(sp, sh, st) <= 0 or sp % 8 or sh % 8 or st % 8:
-        raise ValueError(f"the cache has strides {k_cache.stride()}: the last must be 1, the others positive multiples of 8")
-    if table.dtype != torch.int32 or table.dim() != 2 or table.device != like.device or table.shape[0] < B or table.shape[1] < 1:
-        raise ValueError(f"table must be an int32 [slots, width] tensor on {like.device} with at least {B} rows")
-    ts = table.stride(0) if table.shape[0] > 1 else table.shape[1]
-    if (table.stride(1) != 1 and table.shape[1] > 1) or ts < table.shape[1]:
-        raise ValueError("table must have contiguous rows that do not overlap")
-    return _lib.Pages(k_cache.data_ptr(), v_cache.data_ptr(), sp, sh, st, n, page, table.data_ptr(), ts, table.shape[1])
+    shape, strides = k_cache.shape, k_cache.stride()
+    if k_cache.dim() != 4 or v_cache.shape != shape or v_cache.stride() != strides or shape[1] != H or shape[3] != d or shape[0] < 1:
+        raise ValueError(f"k_cache and v_cache must be [n_pages, {H}, page_size, {d}] with the same shape and strides, are "
+                         f"{tuple(shape)} {strides} and {tuple(v_cache.shape)} {v_cache.stride()}")
+    if (k_cache.dtype is not dtype or v_cache.dtype is not dtype or not k_cache.is_cuda or not v_cache.is_cuda or
+            k_cache.get_device() != index or v_cache.get_device() != index):
+        raise ValueError(f"k_cache and v_cache must be {dtype} tensors on cuda:{index}")
+    n, _, page, _ = shape
+    sp, sh, st, sd = strides
+    if n == 1:
+        sp = 8
+    if H == 1:
+        sh = 8
+    if sd != 1 or sp <= 0 or sh <= 0 or st <= 0 or (sp | sh | st) & 7:
+        raise ValueError(f"the cache has strides {strides}: the last must be 1, the others positive multiples of 8")
+    if table.dim() != 2 or table.dtype is not _INT32 or not table.is_cuda or table.get_device() != index:
+        raise ValueError(f"table must be an int32 [slots, width] tensor on cuda:{index}")
+    slots, width = table.shape
+    ts, tw = table.stride()
+    if slots <= 1:
+        ts = width
+    if slots < B or width < 1 or (tw != 1 and width > 1) or ts < width:
+        raise ValueError(f"table must have contiguous rows that do not overlap, {B} of them at least: is {(slots, width)} "
+                         f"with strides {table.stride()}")
+    return _lib.Pages(k_cache.data_ptr(), v_cache.data_ptr(), sp, sh, st, n, page, table.data_ptr(), ts, width)
 
 
-def _serve(q, k, v, cu, scale, out, lse, workspace):
+def _serve(q, k, v, cu, scale, out, lse):
     """What forward_prompt and forward_tree share: the rows, the sizes and the outputs."""
-    rq = _rows("q", q, None)
+    index, dtype = _first("q", q, 3), q.dtype
     T, Hq, d = q.shape
-    rk, rv = _rows("k", k, q, tokens=T), _rows("v", v, q, heads=k.shape[1], tokens=T)
+    if k.dim() != 3:
+        raise ValueError(f"k must be [T, Hkv, d], is {tuple(k.shape)}")
     Hkv = k.shape[1]
-    if Hkv < 1 or Hq % Hkv:
+    if Hkv < 1 or Hq < 1 or Hq % Hkv:
         raise ValueError(f"{Hq} query heads do not share {Hkv} key/value heads evenly")
-    B = _cu_of(cu, q.device)
+    at, B = _offsets(cu, index)
     if out is None:
-        out = torch.empty((T, Hq, d), dtype=q.dtype, device=q.device)
-    ro = _rows("out", out, q, heads=Hq, tokens=T)
+        out = torch.empty((T, Hq, d), dtype=dtype, device=index)
     if lse is None:
-        lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device)
+        lse = torch.empty((Hq, T), dtype=_FP32, device=index)
     elif lse is False:
         lse = None
-    elif lse.dtype != torch.float32 or tuple(lse.shape) != (Hq, T) or not lse.is_contiguous() or lse.device != q.device:
-        raise ValueError("lse must be a contiguous float32 [Hq, T] tensor on q's device")
-    if workspace is None:
-        workspace = torch.empty(max(_tree_workspace(q.device.index, d), 1), dtype=torch.uint8, device=q.device)
-    elif workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != q.device:
-        raise ValueError("workspace must be a contiguous uint8 tensor on q's device")
-    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    return rq, rk, rv, ro, out, lse, workspace, (B, T, Hq, Hkv, d, _DTYPES[q.dtype], scale)
+    elif lse.dtype is not _FP32 or lse.shape != (Hq, T) or not lse.is_contiguous() or not lse.is_cuda or lse.get_device() != index:
+        raise ValueError(f"lse must be a contiguous float32 tensor {(Hq, T)} on cuda:{index}")
+    rows = (_rows("q", q, index, dtype, T, Hq, d), _rows("k", k, index, dtype, T, Hkv, d),
+            _rows("v", v, index, dtype, T, Hkv, d), _rows("out", out, index, dtype, T, Hq, d),
+            None if lse is None else lse.data_ptr())
+    sizes = (B, T, Hq, Hkv, d, _DTYPES[dtype], 1.0 / math.sqrt(d) if scale is None else float(scale))
+    return index, rows, at, sizes, out, lse
 
 
 _workspace_sizes = {}
@@ -299,19 +332,16 @@ def _tree_workspace(index: int, d: int) -> int:
     """fa_forward_tree_workspace_size on a device: the same for every call."""
     if (index, d) not in _workspace_sizes:
         with torch.cuda.device(index):
-            _workspace_sizes[index, d] = int(_lib_fa().fa_forward_tree_workspace_size(d))
+            _workspace_sizes[index, d] = max(int(_lib_fa().fa_forward_tree_workspace_size(d)), 1)
     return _workspace_sizes[index, d]
 
 
-def forward_prompt(q, k, v, cu_seqlens, scale: Optional[float] = None, out=None, lse=None, workspace=None):
+def forward_prompt(q, k, v, cu_seqlens, scale: Optional[float] = None, out=None, lse=None):
     """O, LSE of causal attention over whole prompts packed back to back (include/fa.h:
     fa_forward_prompt): q [T, Hq, d], k and v [T, Hkv, d] bfloat16 or float16, strided views of one
     projection welcome; cu_seqlens int32 [B + 1]; lse [Hq, T] (lse=False: none is written)."""
-    rq, rk, rv, ro, out, lse, workspace, sizes = _serve(q, k, v, cu_seqlens, scale, out, lse, workspace)
-    with torch.cuda.device(q.device):
-        rc = _lib_fa().fa_forward_prompt(rq, rk, rv, ro, _p(lse), _p(cu_seqlens), *sizes, _p(workspace),
-                                         workspace.numel(), _stream(q.device))
-    _lib.check(rc, "fa_forward_prompt")
+    index, rows, at, sizes, out, lse = _serve(q, k, v, cu_seqlens, scale, out, lse)
+    _call("fa_forward_prompt", index, *rows, at, *sizes)
     return out, lse
 
 
@@ -322,19 +352,18 @@ def forward_tree(q, k, v, k_cache, v_cache, table, lens, cu_nodes, mask=None, sc
     [n_pages, Hkv, page_size, d], table int32 [slots, width], lens int32 [B] cached tokens, cu_nodes
     int32 [B + 1]. mask: int32 [T, words] from tree_mask, or None for a chain (one token a
     sequence is plain decoding). lse [Hq, T] (lse=False: none is written)."""
-    rq, rk, rv, ro, out, lse, workspace, sizes = _serve(q, k, v, cu_nodes, scale, out, lse, workspace)
-    pages = _pages_of(k_cache, v_cache, table, k, k.shape[1], sizes[0])
-    _int32("lens", lens, q.device, (sizes[0],))
-    words = 0
+    index, rows, at, sizes, out, lse = _serve(q, k, v, cu_nodes, scale, out, lse)
+    B, T, _, Hkv, d = sizes[:5]
+    pages = _pages(k_cache, v_cache, table, index, q.dtype, Hkv, d, B)
+    bits, words = None, 0
     if mask is not None:
-        _int32("mask", mask, q.device, dim=2)
+        if mask.dim() != 2 or mask.shape[1] < 1:
+            raise ValueError(f"mask must be int32 [T, words], is {tuple(mask.shape)}")
         words = mask.shape[1]
-        if mask.shape[0] != q.shape[0] or words < 1:
-            raise ValueError(f"mask has shape {tuple(mask.shape)}, expected ({q.shape[0]}, words >= 1)")
-    with torch.cuda.device(q.device):
-        rc = _lib_fa().fa_forward_tree(rq, rk, rv, ro, _p(lse), pages, _p(lens), _p(cu_nodes), _p(mask), words, *sizes,
-                                       _p(workspace), workspace.numel(), _stream(q.device))
-    _lib.check(rc, "fa_forward_tree")
+        bits = _ints("mask", mask, index, (T, words))
+    workspace = _workspace(workspace, _tree_workspace(index, d), index)
+    _call("fa_forward_tree", index, *rows, pages, _ints("lens", lens, index, (B,)), at, bits, words, *sizes,
+          workspace.data_ptr(), workspace.numel())
     return out, lse
 
 
@@ -342,18 +371,16 @@ def tree_mask(parents, cu_nodes, words: int, out=None) -> torch.Tensor:
     """Which nodes each node of a tree sees, itself and its ancestors, as bits (include/fa.h:
     fa_tree_mask): parents int32 [T] (index within the sequence, negative for a root), cu_nodes int32
     [B + 1]; int32 [T, words], 32 nodes a word. One mask serves every layer."""
-    if not parents.is_cuda:
-        raise ValueError("parents must be a CUDA tensor")
-    _int32("parents", parents, parents.device)
-    B, T, words = _cu_of(cu_nodes, parents.device), parents.numel(), int(words)
+    if not parents.is_cuda or parents.dim() != 1:
+        raise ValueError("parents must be an int32 CUDA tensor [T]")
+    index, T, words = parents.get_device(), parents.shape[0], int(words)
+    at, B = _offsets(cu_nodes, index)
     if words < 1:
         raise ValueError("words must be at least 1")
     if out is None:
-        out = torch.empty((T, words), dtype=torch.int32, device=parents.device)
-    _int32("out", out, parents.device, (T, words), dim=2)
-    with torch.cuda.device(parents.device):
-        rc = _lib_fa().fa_tree_mask(_p(parents), _p(cu_nodes), _p(out), words, B, T, _stream(parents.device))
-    _lib.check(rc, "fa_tree_mask")
+        out = torch.empty((T, words), dtype=_INT32, device=index)
+    _call("fa_tree_mask", index, _ints("parents", parents, index, (T,)), at, _ints("out", out, index, (T, words)), words,
+          B, T)
     return out
 
 
@@ -361,38 +388,40 @@ def cache_append(k, v, k_cache, v_cache, table, start, cu, rows=None) -> None:
     """Writes tokens into their pages (include/fa.h: fa_cache_append): token i of sequence b goes to
     position start[b] + i. k and v [Tkv, Hkv, d]; with rows (int32 [T]) token cu[b] + i is row
     rows[cu[b] + i] of them, else row cu[b] + i."""
-    rk = _rows("k", k, None)
-    T, Hkv, d = k.shape
-    rv = _rows("v", v, k, heads=Hkv, tokens=T)
-    B = _cu_of(cu, k.device)
-    pages = _pages_of(k_cache, v_cache, table, k, Hkv, B)
-    _int32("start", start, k.device, (B,))
-    n = T
+    index, dtype = _first("k", k, 3), k.dtype
+    Tkv, H, d = k.shape
+    at, B = _offsets(cu, index)
+    pages = _pages(k_cache, v_cache, table, index, dtype, H, d, B)
+    T, pick = Tkv, None
     if rows is not None:
-        n = _int32("rows", rows, k.device).numel()
-    with torch.cuda.device(k.device):
-        rc = _lib_fa().fa_cache_append(rk, rv, pages, _p(start), _p(cu), _p(rows), B, n, T, Hkv, d, _stream(k.device))
-    _lib.check(rc, "fa_cache_append")
+        T = rows.shape[0] if rows.dim() == 1 else -1
+        pick = _ints("rows", rows, index, (T,))
+    _call("fa_cache_append", index, _rows("k", k, index, dtype, Tkv, H, d), _rows("v", v, index, dtype, Tkv, H, d), pages,
+          _ints("start", start, index, (B,)), at, pick, B, T, Tkv, H, d)
 
 
-def _pool_of(kv: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, workspace):
-    if not kv.is_cuda or kv.dtype not in _DTYPES or kv.dim() != 5 or kv.numel() == 0:
-        raise ValueError("kv must be a bfloat16 or float16 CUDA tensor [planes, n_pages, Hkv, page_size, d]")
-    if not kv[0].is_contiguous() or (kv.shape[0] > 1 and kv.stride(0) < kv[0].numel()):
-        raise ValueError("each plane of kv must be contiguous, and apart from the others")
-    _int32("table", table, kv.device, dim=2)
-    if table.numel() == 0:
-        raise ValueError("table must have at least one slot and one column")
-    _int32("lens", lens, kv.device, (table.shape[0],))
+def _pool(kv: torch.Tensor, table: torch.Tensor, lens: torch.Tensor):
+    index = _first("kv", kv, 5)
     x, n, H, page, d = kv.shape
-    pool = _lib.Pool(kv.data_ptr(), kv.stride(0) if x > 1 else 0, x, n, H, page, d, table.data_ptr(), lens.data_ptr(),
-                     table.shape[0], table.shape[1])
-    if workspace is None:
-        need = int(_lib_fa().fa_cache_workspace_size(n, *table.shape))
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=kv.device)
-    elif workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != kv.device:
-        raise ValueError("workspace must be a contiguous uint8 tensor on kv's device")
-    return pool, workspace
+    sx, sn, sh, st, sd = kv.stride()
+    plane = n * H * page * d
+    if plane == 0 or x == 0:
+        raise ValueError("kv must have at least one plane, page, head and token")
+    if x == 1:
+        sx = 0
+    if ((n > 1 and sn != H * page * d) or (H > 1 and sh != page * d) or (page > 1 and st != d) or (d > 1 and sd != 1) or
+            (x > 1 and sx < plane)):
+        raise ValueError(f"each plane of kv must be contiguous, and apart from the others: strides {kv.stride()}")
+    if table.dim() != 2 or table.shape[0] < 1 or table.shape[1] < 1:
+        raise ValueError("table must be int32 [slots, width] with at least one slot and one column")
+    slots, width = table.shape
+    return index, slots, _lib.Pool(kv.data_ptr(), sx, x, n, H, page, d, _ints("table", table, index, (slots, width)),
+                                   _ints("lens", lens, index, (slots,)), slots, width), (n, slots, width)
+
+
+def _pool_workspace(workspace, sizes, index: int):
+    need = 1 if workspace is not None else max(int(_lib_fa().fa_cache_workspace_size(*sizes)), 1)
+    return _workspace(workspace, need, index)
 
 
 def cache_update(kv, table, lens, src, new_lens, workspace=None) -> torch.Tensor:
@@ -401,25 +430,21 @@ def cache_update(kv, table, lens, src, new_lens, workspace=None) -> torch.Tensor
     kv [planes, n_pages, Hkv, page_size, d] holds K and V of every layer; table int32 [slots, width] and
     lens int32 [slots] are updated in place. Returns info, int32 [2]: the pages needed and the pages
     free (where more are needed than free, nothing has changed; -1, -1: invalid tables)."""
-    pool, workspace = _pool_of(kv, table, lens, workspace)
-    for name, t in (("src", src), ("new_lens", new_lens)):
-        _int32(name, t, kv.device, (table.shape[0],))
-    info = torch.empty(2, dtype=torch.int32, device=kv.device)
-    with torch.cuda.device(kv.device):
-        rc = _lib_fa().fa_cache_update(pool, _p(src), _p(new_lens), _p(info), _p(workspace), workspace.numel(),
-                                       _stream(kv.device))
-    _lib.check(rc, "fa_cache_update")
+    index, slots, pool, sizes = _pool(kv, table, lens)
+    workspace = _pool_workspace(workspace, sizes, index)
+    info = torch.empty(2, dtype=_INT32, device=index)
+    _call("fa_cache_update", index, pool, _ints("src", src, index, (slots,)), _ints("new_lens", new_lens, index, (slots,)),
+          info.data_ptr(), workspace.data_ptr(), workspace.numel())
     return info
 
 
 def cache_compact(kv, table, lens, workspace=None) -> torch.Tensor:
     """Moves the pages in use to the lowest ids, in every plane, and the table with them (include/fa.h:
     fa_cache_compact). Returns info, int32 [2]: the pages in use and the pages moved."""
-    pool, workspace = _pool_of(kv, table, lens, workspace)
-    info = torch.empty(2, dtype=torch.int32, device=kv.device)
-    with torch.cuda.device(kv.device):
-        rc = _lib_fa().fa_cache_compact(pool, _p(info), _p(workspace), workspace.numel(), _stream(kv.device))
-    _lib.check(rc, "fa_cache_compact")
+    index, _, pool, sizes = _pool(kv, table, lens)
+    workspace = _pool_workspace(workspace, sizes, index)
+    info = torch.empty(2, dtype=_INT32, device=index)
+    _call("fa_cache_compact", index, pool, info.data_ptr(), workspace.data_ptr(), workspace.numel())
     return info
 
 

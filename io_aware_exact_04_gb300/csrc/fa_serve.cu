@@ -933,9 +933,9 @@ int forward(const fa_rows* q, const fa_rows* k, const fa_rows* v, const fa_rows*
             int dtype, float scale, void* workspace, size_t workspace_bytes, fa_stream_t stream) {
   for (const fa_rows* r : {q, k, v, o})
     if (const int rc = check_rows(r); rc != FA_OK) return rc;
-  if (!cu || !workspace || (lse && !aligned16(lse))) return !cu || !workspace ? FA_ERR_INVALID_ARG : FA_ERR_MISALIGNED;
-  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return FA_ERR_MISALIGNED;
-  if (workspace_bytes < fa_forward_tree_workspace_size(d)) return FA_ERR_INVALID_ARG;
+  if (!cu || (cache && !workspace)) return FA_ERR_INVALID_ARG;
+  if ((lse && !aligned16(lse)) || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return FA_ERR_MISALIGNED;
+  if (cache && workspace_bytes < fa_forward_tree_workspace_size(d)) return FA_ERR_INVALID_ARG;
   int err = FA_OK;
   int* status = fa::status_word(&err);
   if (!status) return err;
@@ -987,12 +987,12 @@ size_t fa_forward_tree_workspace_size(int d) {
 
 int fa_forward_prompt(const fa_rows* q, const fa_rows* k, const fa_rows* v, const fa_rows* o, float* lse,
                       const int32_t* cu_seqlens, int B, int T, int Hq, int Hkv, int d, int dtype, float scale,
-                      void* workspace, size_t workspace_bytes, fa_stream_t stream) {
+                      fa_stream_t stream) {
   const int rc = check_sizes(B, T, Hq, Hkv, d, dtype, scale);
   if (rc != FA_OK) return rc;
   if (B == 0 || T == 0) return FA_OK;
-  return forward(q, k, v, o, lse, nullptr, nullptr, cu_seqlens, nullptr, 0, B, T, Hq, Hkv, d, dtype, scale, workspace,
-                 workspace_bytes, stream);
+  return forward(q, k, v, o, lse, nullptr, nullptr, cu_seqlens, nullptr, 0, B, T, Hq, Hkv, d, dtype, scale, nullptr, 0,
+                 stream);
 }
 
 int fa_forward_tree(const fa_rows* q, const fa_rows* k, const fa_rows* v, const fa_rows* o, float* lse,
