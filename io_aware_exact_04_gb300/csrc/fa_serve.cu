@@ -68,25 +68,30 @@ struct ServeCfg {
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_R = 2 * TILE_BYTES;
   static constexpr int OFF_BAR = OFF_R + NSLOT * TILE_BYTES;
-  static constexpr int OFF_DESC = OFF_BAR + 400;   // 4 x 16 ints
+  static constexpr int OFF_DESC = OFF_BAR + 512;   // 4 x 16 ints
   static constexpr int OFF_ML = OFF_BAR + 768;     // m and l of lane 1's rows, for the join of a dual item
   static constexpr int SMEM_BYTES = OFF_ML + 1024 + 1024;
-  // TMEM columns as in the forward: d = 64 keeps P apart from S, so that S of the next tile can
-  // be formed while P is still read; d = 128 writes P over S.
+  // A key tile is taken in HPT steps of KT keys. The softmax must find S of the next step ready
+  // when it ends one, so S may not wait for PV of the step before. TMEM has room for that in two
+  // ways: d = 64 keeps P apart from S (one step a tile; S is free once it is in registers);
+  // d = 128, where O takes half the columns, takes a tile as two halves; even and odd steps of a
+  // lane have a buffer each, P over its own S, and S is formed two steps ahead.
   static constexpr bool SEP_P = D == 64;
-  __device__ static constexpr uint32_t tm_s(int t) { return 128u * t; }
-  __device__ static constexpr uint32_t tm_p(int t) { return SEP_P ? 256u + 64u * t : 128u * t; }
+  static constexpr int KT = SEP_P ? 128 : 64, HPT = 128 / KT;
+  __device__ static constexpr int buf(int g) { return SEP_P ? 0 : g & 1; }            // of a lane's step g
+  __device__ static constexpr uint32_t phase(int g) { return (SEP_P ? g : g >> 1) & 1; }  // of its barriers
+  __device__ static constexpr uint32_t tm_s(int t, int u) { return 128u * t + 64u * u; }
+  __device__ static constexpr uint32_t tm_p(int t, int u) { return SEP_P ? 256u + 64u * t : tm_s(t, u); }
   __device__ static constexpr uint32_t tm_o(int t) { return SEP_P ? 384u + 64u * t : 256u + (uint32_t)D * t; }
   static constexpr uint32_t TM_COLS = 512;
   static constexpr int THREADS = 352;
   // barriers
   static constexpr int FULL = 0, EMPTY = NSLOT, Q_FULL = 2 * NSLOT, Q_EMPTY = Q_FULL + 2, S_FULL = Q_EMPTY + 2,
-                       P_READY = S_FULL + 2, O_DONE = P_READY + 2, S_FREE = O_DONE + 2, O_FREE = S_FREE + 2,
+                       P_READY = S_FULL + 4, O_DONE = P_READY + 4, S_FREE = O_DONE + 2, O_FREE = S_FREE + 2,
                        MERGE = O_FREE + 2, DRAIN = MERGE + 1, D_FULL = DRAIN + 1, D_EMPTY = D_FULL + 4,
                        BARS = D_EMPTY + 4;
 };
-static_assert(8 * ServeCfg<64>::BARS + 8 <= 400 && 8 * ServeCfg<128>::BARS + 8 <= 400, "barrier area");
-static_assert(400 + 4 * 64 <= 768, "descriptor area");
+static_assert(8 * ServeCfg<64>::BARS + 8 <= 512 && 8 * ServeCfg<128>::BARS + 8 <= 512, "barrier area");
 static_assert(ServeCfg<64>::SMEM_BYTES <= 232448 && ServeCfg<128>::SMEM_BYTES <= 232448, "shared memory above 227 KB");
 
 enum { SITE_SW_EMPTY = 60, SITE_SW_Q_FULL, SITE_SW_Q_EMPTY, SITE_SW_K_FULL, SITE_SW_V_FULL, SITE_SW_S_FREE,
@@ -105,6 +110,7 @@ struct ServeItem {
   int tok0;    // the pair's first token within the sequence
   int kvh;
   int slot;    // partial result slot
+  int s0, s1;  // steps of lanes 0 and 1 (a half of a tile with no key in it is no step)
 };
 enum { ITEM_DUAL = 1, ITEM_WHOLE = 2 };
 
@@ -244,8 +250,10 @@ __global__ void __launch_bounds__(352, 1)
     for (int t = 0; t < 2; ++t) {
       mbar_init(BAR(C::Q_FULL + t), 1);
       mbar_init(BAR(C::Q_EMPTY + t), 2);
-      mbar_init(BAR(C::S_FULL + t), 1);
-      mbar_init(BAR(C::P_READY + t), 4);
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(BAR(C::S_FULL + 2 * t + h), 1);
+        mbar_init(BAR(C::P_READY + 2 * t + h), 4);
+      }
       mbar_init(BAR(C::O_DONE + t), 1);
       mbar_init(BAR(C::S_FREE + t), 4);
       mbar_init(BAR(C::O_FREE + t), 4);
@@ -277,14 +285,25 @@ __global__ void __launch_bounds__(352, 1)
   griddep_wait();  // before any access to global memory
   griddep_launch_dependents();
 
+  // Steps that lane t takes in the item's tile j: those halves in which some row of its query tile
+  // sees a key.
+  const bool tree = PAGED && a.mask != nullptr;
+  auto steps_in = [&](const ServeItem& it, int t, int j) {
+    if (C::HPT == 1) return 1;
+    const int last = it.tok0 + ((it.flags & ITEM_DUAL) ? 1 : t + 1) * npt;  // past the lane's last token
+    const int keys = j < it.nc ? it.L - j * 128 : (tree ? it.n : min(it.n, last)) - (j - it.nc) * 128;
+    return keys > C::KT ? 2 : 1;
+  };
+
   // Item i of this CTA, for a consumer warp: false when the CTA must give up.
   auto next_item = [&](int i, ServeItem* it) {
     if (!wait_warp_sleep(BAR(C::D_FULL + (i & 3)), (i >> 2) & 1, st, SITE_SW_DESC_FULL)) return false;
     const int4* d = reinterpret_cast<const int4*>(descs + 16 * (i & 3));
-    const int4 x = d[0], y = d[1], z = d[2];
+    const int4 x = d[0], y = d[1], z = d[2], w = d[3];
     it->cnt = x.x, it->flags = x.y, it->c0 = x.z, it->c1 = x.w;
     it->j0 = y.x, it->nc = y.y, it->L = y.z, it->n = y.w;
     it->row0 = z.x, it->tok0 = z.y, it->kvh = z.z, it->slot = z.w;
+    it->s0 = w.x, it->s1 = w.y;
     __syncwarp();
     if (lane == 0) mbar_arrive(BAR(C::D_EMPTY + (i & 3)));
     return true;
@@ -301,6 +320,7 @@ __global__ void __launch_bounds__(352, 1)
         d[0] = make_int4(it.cnt, it.flags, it.c0, it.c1);
         d[1] = make_int4(it.j0, it.nc, it.L, it.n);
         d[2] = make_int4(it.row0, it.tok0, it.kvh, it.slot);
+        d[3] = make_int4(it.s0, it.s1, 0, 0);
         mbar_arrive(BAR(C::D_FULL + (items & 3)));
       }
       __syncwarp();
@@ -375,6 +395,17 @@ __global__ void __launch_bounds__(352, 1)
       it->c1 = dual ? it->cnt >> 1 : it->cnt;
       it->j0 = j0, it->nc = w.nc, it->L = w.L, it->n = w.n, it->row0 = w.row0, it->tok0 = 2 * pair * npt, it->kvh = kvh;
       it->slot = 2 * blockIdx.x + (j0 == 0);
+      it->s0 = it->c0 * C::HPT, it->s1 = it->c1 * C::HPT;
+      if (C::HPT > 1) {  // only the last cached tile and a lane's last tile may have a half less
+        for (int t = 0; t < 2; ++t) {
+          int* steps = t ? &it->s1 : &it->s0;
+          const int end = dual ? j0 + it->cnt : j0 + (t ? it->c1 : it->c0);  // past the lane's tiles
+          auto mine = [&](int j) { return j >= j0 && j < end && (!dual || ((j - j0) & 1) == t); };
+          const int lc = w.nc - 1, ln = (dual || t == 0 ? n0 : n1) - 1;
+          if (mine(lc)) *steps -= 2 - steps_in(*it, t, lc);
+          if (ln != lc && mine(ln)) *steps -= 2 - steps_in(*it, t, ln);
+        }
+      }
     };
     ServeItem it;
     if (PAGED) {
@@ -429,9 +460,9 @@ __global__ void __launch_bounds__(352, 1)
   } else if (warp >= 9) {
     // ------------------------------------------------------------ MMA issuer of lane t
     const int t = warp - 9;
-    constexpr uint32_t IDESC_S = F16 ? idesc_f16_f32(128, 128, 0, 0) : idesc_bf16_f32(128, 128, 0, 0);
+    constexpr uint32_t IDESC_S = F16 ? idesc_f16_f32(128, C::KT, 0, 0) : idesc_bf16_f32(128, C::KT, 0, 0);
     constexpr uint32_t IDESC_O = F16 ? idesc_f16_f32(128, D, 0, 1) : idesc_bf16_f32(128, D, 0, 1);
-    constexpr uint32_t HI = sdesc_hi(1024), TILE16 = C::TILE_BYTES >> 4;
+    constexpr uint32_t HI = sdesc_hi(1024), TILE16 = C::TILE_BYTES >> 4, HALF16 = (C::KT * 128) >> 4;
     const uint32_t q_lo = sdesc_lo(sbase + C::OFF_Q, 16), k_lo = sdesc_lo(sbase + C::OFF_R, 16);
     const uint32_t v_lo = sdesc_lo(sbase + C::OFF_R, C::SUB_BYTES);
     auto commit = [&](uint32_t bar) {
@@ -441,89 +472,107 @@ __global__ void __launch_bounds__(352, 1)
     auto full = [&](int x, int site) {  // ring entry x has landed
       return wait_warp_sleep(BAR(C::FULL + x % C::NSLOT), (x / C::NSLOT) & 1, st, site);
     };
-    int e0 = 0, uq = 0, ct = 0, used = 0;  // ring tiles before the item, Q slots, this lane's tiles and items so far
+    auto release = [&](uint32_t full_bar, uint32_t parity, uint32_t empty_bar) {  // what this lane does not read
+      if (!wait_warp_sleep(full_bar, parity, st, SITE_SW_RELEASE)) return false;
+      if (elect_one()) mbar_arrive(empty_bar);
+      __syncwarp();
+      return true;
+    };
+    int e0 = 0, uq = 0, used = 0;  // ring tiles and Q slots before the item, this lane's items so far
+    int g_s = 0, g_p = 0;  // S and PV steps issued so far
     bool ok = true;
     for (int i = 0; ok; ++i) {
       ServeItem it;
       if (!next_item(i, &it) || it.cnt < 0) break;
       const bool dual = it.flags & ITEM_DUAL;
-      const int c = t ? it.c1 : it.c0;
+      const int steps = t ? it.s1 : it.s0;
       const int qu = dual ? uq : uq + t;  // this lane's Q slot use
       const uint32_t qa = q_lo + (qu & 1) * TILE16;
       auto tile = [&](int kk) { return dual ? 2 * kk + t : kk; };
-      auto issue_s = [&](int kk) {  // S = Q K^T; then K's slot and, after the last one, Q's are done with
-        const int x = 2 * (e0 + tile(kk));
+      int sk = 0, sh = 0, left = steps;  // the next S step: tile and half
+      auto issue_s = [&]() {  // S = Q K^T; then K's slot and, after the last one, Q's are done with
+        const int x = 2 * (e0 + tile(sk)), h = sh;
         if (!full(x, SITE_SW_K_FULL)) return false;
-        if (C::SEP_P && ct + kk > 0 &&
-            !wait_warp_sleep(BAR(C::S_FREE + t), (ct + kk - 1) & 1, st, SITE_SW_S_FREE))
-          return false;
+        if (C::SEP_P && g_s > 0 && !wait_warp_sleep(BAR(C::S_FREE + t), (g_s - 1) & 1, st, SITE_SW_S_FREE)) return false;
         tc_fence_after();
-        const uint32_t ka = k_lo + (x % C::NSLOT) * TILE16, d = tmem + C::tm_s(t);
+        const uint32_t ka = k_lo + (x % C::NSLOT) * TILE16 + h * HALF16, d = tmem + C::tm_s(t, C::buf(g_s));
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const uint32_t off = ((k >> 2) * C::SUB_BYTES + (k & 3) * 32) >> 4;
           if (elect_one()) mma_ss(d, sdesc_join(qa + off, HI), sdesc_join(ka + off, HI), IDESC_S, k > 0);
         }
-        commit(BAR(C::S_FULL + t));
-        commit(BAR(C::EMPTY + x % C::NSLOT));
-        if (kk == c - 1) commit(BAR(C::Q_EMPTY + (qu & 1)));
+        commit(BAR(C::S_FULL + 2 * t + C::buf(g_s)));
+        ++g_s;
+        if (h + 1 == steps_in(it, t, it.j0 + tile(sk))) {
+          commit(BAR(C::EMPTY + x % C::NSLOT));
+          ++sk;
+          sh = 0;
+        } else {
+          ++sh;
+        }
+        if (--left == 0) commit(BAR(C::Q_EMPTY + (qu & 1)));
         return true;
       };
-      auto issue_pv = [&](int kk) {  // O += P V
-        const int x = 2 * (e0 + tile(kk)) + 1, s = x % C::NSLOT;
+      int pk = 0, ph = 0, freed = 0;  // the next PV step; ring tiles that this lane is done with
+      auto pass_by = [&](int to) {  // releases the tiles before ring tile `to` that are the other lane's
+        for (; freed < to; ++freed) {
+          if (dual ? (freed & 1) == t : freed < (t ? it.c1 : it.c0)) continue;
+          const int x = 2 * (e0 + freed), y = x + 1;
+          if (!release(BAR(C::FULL + x % C::NSLOT), (x / C::NSLOT) & 1, BAR(C::EMPTY + x % C::NSLOT)) ||
+              !release(BAR(C::FULL + y % C::NSLOT), (y / C::NSLOT) & 1, BAR(C::EMPTY + y % C::NSLOT)))
+            return false;
+        }
+        return true;
+      };
+      auto issue_pv = [&](bool first) {  // O += P V
+        const int x = 2 * (e0 + tile(pk)) + 1, s = x % C::NSLOT, h = ph, j = it.j0 + tile(pk);
         if (!full(x, SITE_SW_V_FULL)) return false;
-        const int j = it.j0 + tile(kk);
-        const int rows = j < it.nc ? it.L - j * 128 : it.n - (j - it.nc) * 128;
-        if (rows < 128) {
+        const int rows = (j < it.nc ? it.L - j * 128 : it.n - (j - it.nc) * 128) - h * C::KT;
+        if (rows < C::KT) {
           // rows past the sequence may hold anything; P is 0 there, but 0 x NaN is not
-          uint8_t* v = sm + C::OFF_R + s * C::TILE_BYTES;
-          for (int z = lane; z < (128 - rows) * 8 * C::NSUB; z += 32) {
-            const int cb = z / ((128 - rows) * 8), w = z % ((128 - rows) * 8);
-            *reinterpret_cast<uint4*>(v + cb * C::SUB_BYTES + rows * 128 + w * 16) = make_uint4(0, 0, 0, 0);
-          }
+          uint8_t* v = sm + C::OFF_R + s * C::TILE_BYTES + (h * C::KT + rows) * 128;
+          const int chunks = (C::KT - rows) * 8;
+          for (int z = lane; z < chunks * C::NSUB; z += 32)
+            *reinterpret_cast<uint4*>(v + z / chunks * C::SUB_BYTES + z % chunks * 16) = make_uint4(0, 0, 0, 0);
           fence_proxy_async_smem();
           __syncwarp();
         }
-        if (!wait_warp_sleep(BAR(C::P_READY + t), (ct + kk) & 1, st, SITE_SW_P_READY)) return false;
-        if (kk == 0 && used > 0 && !wait_warp_sleep(BAR(C::O_FREE + t), (used - 1) & 1, st, SITE_SW_O_FREE)) return false;
+        const int u = C::buf(g_p);
+        if (!wait_warp_sleep(BAR(C::P_READY + 2 * t + u), C::phase(g_p), st, SITE_SW_P_READY)) return false;
+        if (first && used > 0 && !wait_warp_sleep(BAR(C::O_FREE + t), (used - 1) & 1, st, SITE_SW_O_FREE)) return false;
         tc_fence_after();
-        const uint32_t va = v_lo + s * TILE16, d = tmem + C::tm_o(t), pa = tmem + C::tm_p(t);
+        const uint32_t va = v_lo + s * TILE16 + h * HALF16, d = tmem + C::tm_o(t), pa = tmem + C::tm_p(t, u);
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (elect_one()) mma_ts(d, pa + k * 8, sdesc_join(va + k * (2048 >> 4), HI), IDESC_O, (kk | k) != 0);
+        for (int k = 0; k < C::KT / 16; ++k)
+          if (elect_one()) mma_ts(d, pa + k * 8, sdesc_join(va + k * (2048 >> 4), HI), IDESC_O, !first || k > 0);
         commit(BAR(C::O_DONE + t));
-        commit(BAR(C::EMPTY + s));
-        return true;
-      };
-      auto release = [&](uint32_t full_bar, uint32_t parity, uint32_t empty_bar) {  // what this lane does not read
-        if (!wait_warp_sleep(full_bar, parity, st, SITE_SW_RELEASE)) return false;
-        if (elect_one()) mbar_arrive(empty_bar);
-        __syncwarp();
-        return true;
-      };
-      if (c > 0)
-        ok = wait_warp_sleep(BAR(C::Q_FULL + (qu & 1)), (qu >> 1) & 1, st, SITE_SW_Q_FULL) && issue_s(0);
-      int kk = 0;
-      for (int j = 0; ok && j < it.cnt; ++j) {
-        if (kk < c && tile(kk) == j) {
-          if (C::SEP_P && kk + 1 < c && !(ok = issue_s(kk + 1))) break;
-          if (!(ok = issue_pv(kk))) break;
-          if (!C::SEP_P && kk + 1 < c && !(ok = issue_s(kk + 1))) break;
-          ++kk;
+        ++g_p;
+        if (h + 1 == steps_in(it, t, j)) {
+          commit(BAR(C::EMPTY + s));
+          ++pk;
+          ph = 0;
         } else {
-          const int x = 2 * (e0 + j);
-          ok = release(BAR(C::FULL + x % C::NSLOT), (x / C::NSLOT) & 1, BAR(C::EMPTY + x % C::NSLOT)) &&
-               release(BAR(C::FULL + (x + 1) % C::NSLOT), ((x + 1) / C::NSLOT) & 1, BAR(C::EMPTY + (x + 1) % C::NSLOT));
+          ++ph;
         }
+        return true;
+      };
+      if (steps > 0) {
+        ok = wait_warp_sleep(BAR(C::Q_FULL + (qu & 1)), (qu >> 1) & 1, st, SITE_SW_Q_FULL) && issue_s();
+        if (ok && !C::SEP_P && left > 0) ok = issue_s();
       }
+      for (int s = 0; ok && s < steps; ++s) {
+        if (C::SEP_P && left > 0 && !(ok = issue_s())) break;
+        if (!(ok = pass_by(tile(pk)) && issue_pv(s == 0))) break;
+        if (!C::SEP_P && left > 0) ok = issue_s();
+      }
+      if (ok) ok = pass_by(it.cnt);
       // Q slots that this lane did not read
       for (int u = uq; ok && u < uq + (dual ? 1 : 2); ++u)
-        if (u != qu || c == 0)
+        if (u != qu || steps == 0)
           ok = release(BAR(C::Q_FULL + (u & 1)), (u >> 1) & 1, BAR(C::Q_EMPTY + (u & 1)));
       e0 += it.cnt;
       uq += dual ? 1 : 2;
-      ct += c;
-      used += c > 0;
+      used += steps > 0;
     }
     // every MMA issued has completed before TMEM is released
     commit(BAR(C::DRAIN));
@@ -536,42 +585,53 @@ __global__ void __launch_bounds__(352, 1)
     const int row = wq * 32 + lane;
     const int rn = row / a.G, rg = row - rn * a.G;  // token and head of the row within its tile
     const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
-    const uint32_t tS = tmem + lane_off + C::tm_s(t), tP = tmem + lane_off + C::tm_p(t);
     const float sl2 = a.scale_log2;
     float* ml = reinterpret_cast<float*>(sm + C::OFF_ML);
-    int ct0 = 0, ct1 = 0, merges = 0;  // tiles of both lanes and joins of dual items so far
+    int st0 = 0, st1 = 0, merges = 0;  // steps of both lanes and joins of dual items so far
     for (int i = 0;; ++i) {
       ServeItem it;
       if (!next_item(i, &it) || it.cnt < 0) break;
       const bool dual = it.flags & ITEM_DUAL, whole = it.flags & ITEM_WHOLE;
-      const int c = t ? it.c1 : it.c0, ct = t ? ct1 : ct0;
+      const int steps = t ? it.s1 : it.s0, before = t ? st1 : st0;
       const int tok = it.tok0 + (dual ? 0 : t * npt) + rn;
       const bool valid = rn < npt && tok < it.n;
       const bool any = __any_sync(0xffffffffu, valid);
       float m_run = -INFINITY, l_run = 0.f;
       bool ok = true;
-      for (int kk = 0; kk < c; ++kk) {
-        if (!(ok = wait_warp_sleep(BAR(C::S_FULL + t), (ct + kk) & 1, st, SITE_SW_S_FULL))) break;
+      int j = it.j0 + (dual ? t : 0), h = 0;  // the step's key tile and half
+      for (int s = 0; s < steps; ++s) {
+        const int hs = h, js = j;
+        if (h + 1 < steps_in(it, t, j)) {
+          ++h;
+        } else {
+          h = 0;
+          j += dual ? 2 : 1;
+        }
+        const int u = C::buf(before + s);
+        if (!(ok = wait_warp_sleep(BAR(C::S_FULL + 2 * t + u), C::phase(before + s), st, SITE_SW_S_FULL))) break;
         if (!any) {  // no row here: P stays what it is, its rows of O are nobody's
           __syncwarp();
           if (C::SEP_P) {
             if (lane == 0) mbar_arrive(BAR(C::S_FREE + t));
-            // S of this tile may be there before the other warps have written P of the one before:
-            // an arrival now would count for that one
-            if (kk > 0 && !(ok = wait_warp_sleep(BAR(C::O_DONE + t), (ct + kk - 1) & 1, st, SITE_SW_O_DONE))) break;
           }
-          if (lane == 0) mbar_arrive(BAR(C::P_READY + t));
+          // d = 64: S of this tile may be there before the other warps have written P of the one
+          // before: an arrival now would count for that one. d = 128: see below
+          if (s > 0 && (C::SEP_P || s == steps - 1) &&
+              !(ok = wait_warp_sleep(BAR(C::O_DONE + t), (before + s - 1) & 1, st, SITE_SW_O_DONE)))
+            break;
+          if (lane == 0) mbar_arrive(BAR(C::P_READY + 2 * t + u));
           continue;
         }
         tc_fence_after();
-        float sv[128];
+        constexpr int KT = C::KT;
+        float sv[KT];
         {
-          uint32_t r[4][32];
+          uint32_t r[KT / 32][32];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) tmem_ld32(tS + q * 32, r[q]);
+          for (int q = 0; q < KT / 32; ++q) tmem_ld32(tmem + lane_off + C::tm_s(t, u) + q * 32, r[q]);
           tmem_wait_ld();
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
+          for (int q = 0; q < KT / 32; ++q)
 #pragma unroll
             for (int x = 0; x < 32; ++x) sv[q * 32 + x] = __uint_as_float(r[q][x]);
         }
@@ -580,42 +640,42 @@ __global__ void __launch_bounds__(352, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(BAR(C::S_FREE + t));
         }
-        const int j = it.j0 + (dual ? 2 * kk + t : kk);
-        if (PAGED && a.mask && j >= it.nc) {
-          const int k0 = (j - it.nc) * 128;
+        if (tree && js >= it.nc) {
+          const int k0 = (js - it.nc) * 128 + hs * KT;
           const uint32_t* words = a.mask + (long long)(it.row0 + tok) * a.words;
-          uint32_t w[4];
+          uint32_t w[KT / 32];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
+          for (int q = 0; q < KT / 32; ++q) {
             const int left = it.n - k0 - 32 * q;  // nodes from this word on
             w[q] = valid && left > 0 && (k0 >> 5) + q < a.words ? words[(k0 >> 5) + q] : 0u;
             if (left > 0 && left < 32) w[q] &= (1u << left) - 1;
           }
 #pragma unroll
-          for (int x = 0; x < 128; ++x)
+          for (int x = 0; x < KT; ++x)
             if (!(w[x >> 5] >> (x & 31) & 1)) sv[x] = -INFINITY;
         } else {
-          // keys [0, lim) of the tile are seen
-          const int lim = (PAGED && j < it.nc) ? it.L - j * 128 : min(it.n, tok + 1) - (j - it.nc) * 128;
-          if (__any_sync(0xffffffffu, lim < 128)) {
+          // keys [0, lim) of the step are seen
+          const int lim = (js < it.nc ? it.L - js * 128 : min(it.n, tok + 1) - (js - it.nc) * 128) - hs * KT;
+          if (__any_sync(0xffffffffu, lim < KT)) {
 #pragma unroll
-            for (int x = 0; x < 128; ++x)
+            for (int x = 0; x < KT; ++x)
               if (x >= lim) sv[x] = -INFINITY;
           }
         }
         float pm[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) pm[u] = sv[u];
+        for (int y = 0; y < 4; ++y) pm[y] = sv[y];
 #pragma unroll
-        for (int x = 4; x < 124; x += 8)
+        for (int x = 4; x < KT - 4; x += 8)
 #pragma unroll
-          for (int u = 0; u < 4; ++u) pm[u] = fmax3(pm[u], sv[x + 2 * u], sv[x + 2 * u + 1]);
-        const float mx = fmax3(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3]), fmax3(sv[124], sv[125], fmaxf(sv[126], sv[127])));
+          for (int y = 0; y < 4; ++y) pm[y] = fmax3(pm[y], sv[x + 2 * y], sv[x + 2 * y + 1]);
+        const float mx = fmax3(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3]),
+                               fmax3(sv[KT - 4], sv[KT - 3], fmaxf(sv[KT - 2], sv[KT - 1])));
         const float m_tile = mx * sl2;
         // the reference maximum moves only when it grows by more than 2^8; O and l share it
         float f = 1.f;
         bool rescale_warp = false;
-        if (kk == 0) {
+        if (s == 0) {
           m_run = m_tile;
         } else {
           const bool grow = valid && m_tile > m_run + 8.0f;
@@ -628,37 +688,41 @@ __global__ void __launch_bounds__(352, 1)
         const float base = (m_run == -INFINITY) ? 0.f : m_run;
         const uint64_t sl2x2 = f2_pack(sl2, sl2), nbase2 = f2_pack(-base, -base);
         uint64_t ps2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
-        uint32_t pk[4][16];
+        uint32_t pk[KT / 32][16];
+        const uint32_t tP = tmem + lane_off + C::tm_p(t, u);
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
+        for (int q = 0; q < KT / 32; ++q) {
 #pragma unroll
           for (int x = 0; x < 16; ++x) {
             float x0, x1;
-            f2_unpack(f2_fma(f2_pack(sv[h * 32 + 2 * x], sv[h * 32 + 2 * x + 1]), sl2x2, nbase2), x0, x1);
+            f2_unpack(f2_fma(f2_pack(sv[q * 32 + 2 * x], sv[q * 32 + 2 * x + 1]), sl2x2, nbase2), x0, x1);
             const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
             ps2[x & 1] = f2_add(ps2[x & 1], f2_pack(p0, p1));
-            pk[h][x] = pack2<F16>(p0, p1);
+            pk[q][x] = pack2<F16>(p0, p1);
           }
-          if (C::SEP_P && h == 1) {
-            if (kk > 0) {  // PV of the tile before has read P (across items its epilogue waited for that)
-              if (!(ok = wait_warp_sleep(BAR(C::O_DONE + t), (ct + kk - 1) & 1, st, SITE_SW_O_DONE))) break;
+          if (C::SEP_P && q == 1) {
+            if (s > 0) {  // PV of the tile before has read P (across items its epilogue waited for that)
+              if (!(ok = wait_warp_sleep(BAR(C::O_DONE + t), (before + s - 1) & 1, st, SITE_SW_O_DONE))) break;
               tc_fence_after();
             }
             tmem_st16(tP, pk[0]);
             tmem_st16(tP + 16, pk[1]);
           }
-          if (!C::SEP_P || h >= 2) tmem_st16(tP + h * 16, pk[h]);
+          if (!C::SEP_P || q >= 2) tmem_st16(tP + q * 16, pk[q]);
         }
         if (!ok) break;
         float ps[4];
         f2_unpack(ps2[0], ps[0], ps[1]);
         f2_unpack(ps2[1], ps[2], ps[3]);
         l_run = l_run * f + ((ps[0] + ps[1]) + (ps[2] + ps[3]));
+        // d = 128: S of this step was formed behind PV of the last step but one, so that the phase of the
+        // last one is the one this wait can meet. It is waited for before O is rescaled, and before
+        // the last P is published: the wait for the last PV below would else take that phase for its own.
+        if (!C::SEP_P && s > 0 && (rescale_warp || s == steps - 1)) {
+          if (!(ok = wait_warp_sleep(BAR(C::O_DONE + t), (before + s - 1) & 1, st, SITE_SW_O_DONE))) break;
+          tc_fence_after();
+        }
         if (rescale_warp) {
-          if (!C::SEP_P) {
-            if (!(ok = wait_warp_sleep(BAR(C::O_DONE + t), (ct + kk - 1) & 1, st, SITE_SW_O_DONE))) break;
-            tc_fence_after();
-          }
           const uint32_t tO = tmem + lane_off + C::tm_o(t);
           uint32_t r[32];
 #pragma unroll
@@ -673,9 +737,9 @@ __global__ void __launch_bounds__(352, 1)
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(BAR(C::P_READY + t));
+        if (lane == 0) mbar_arrive(BAR(C::P_READY + 2 * t + u));
       }
-      if (ok && c > 0) ok = wait_warp_sleep(BAR(C::O_DONE + t), (ct + c - 1) & 1, st, SITE_SW_O_DONE);
+      if (ok && steps > 0) ok = wait_warp_sleep(BAR(C::O_DONE + t), (before + steps - 1) & 1, st, SITE_SW_O_DONE);
       if (!ok) break;
       tc_fence_after();
       const bool join = dual && it.c1 > 0;
@@ -688,7 +752,7 @@ __global__ void __launch_bounds__(352, 1)
           if (lane == 0) mbar_arrive(BAR(C::MERGE));
         } else {
           if (!wait_warp_sleep(BAR(C::MERGE), merges & 1, st, SITE_SW_MERGE) ||
-              !wait_warp_sleep(BAR(C::O_DONE + 1), (ct1 + it.c1 - 1) & 1, st, SITE_SW_O_DONE))
+              !wait_warp_sleep(BAR(C::O_DONE + 1), (st1 + it.s1 - 1) & 1, st, SITE_SW_O_DONE))
             break;
           tc_fence_after();
           const float m1 = ml[row], m = fmaxf(m_run, m1), base = m == -INFINITY ? 0.f : m;
@@ -699,23 +763,23 @@ __global__ void __launch_bounds__(352, 1)
         }
         ++merges;
       }
-      ct0 += it.c0;
-      ct1 += it.c1;
+      st0 += it.s0;
+      st1 += it.s1;
       if (dual && t == 1) continue;  // lane 0 writes the results
       // l = 0: no key; NaN stays NaN
       const float inv = l_run != 0.f ? 1.f / l_run : 0.f;
       const float lse2 = l_run != 0.f ? m_run + lg2_approx(l_run) : -INFINITY;
       const long long part = (long long)it.slot * 256 + (dual ? 0 : t * 128) + row;
-      if (c == 0) {  // (a cut item only) none of this part's keys concerns this tile
+      if (steps == 0) {  // (a cut item only) none of this part's keys concerns this tile
         if (valid && FA_CHECK(in_range(part, a.part_rows), st, DBG_GLOBAL_STORE)) a.part_lse[part] = -INFINITY;
         continue;
       }
-      const int h = it.kvh * a.G + rg;
+      const int head = it.kvh * a.G + rg;
       const long long token = it.row0 + tok;
       f0 *= inv;
       f1 *= inv;
       const bool write = valid && FA_CHECK(whole ? in_range(token, a.T) : in_range(part, a.part_rows), st, DBG_GLOBAL_STORE);
-      uint16_t* orow = a.o + token * a.o_st + h * a.o_sh;
+      uint16_t* orow = a.o + token * a.o_st + head * a.o_sh;
       float4* prow = reinterpret_cast<float4*>(a.part_o + part * D);
       if (any) {
 #pragma unroll
@@ -752,7 +816,7 @@ __global__ void __launch_bounds__(352, 1)
           }
         }
         if (write && !whole) a.part_lse[part] = lse2;
-        if (write && whole && a.lse) a.lse[(long long)h * a.T + token] = lse2 * 0.6931471805599453f;
+        if (write && whole && a.lse) a.lse[(long long)head * a.T + token] = lse2 * 0.6931471805599453f;
       } else if (lane == 0) {
         mbar_arrive(BAR(C::O_FREE + t));
         if (join) mbar_arrive(BAR(C::O_FREE + 1));
