@@ -469,33 +469,54 @@ __global__ void __launch_bounds__(352, 1)
       if (elect_one()) mma_commit(bar);
       __syncwarp();
     };
-    auto full = [&](int x, int site) {  // ring entry x has landed
-      return wait_warp_sleep(BAR(C::FULL + x % C::NSLOT), (x / C::NSLOT) & 1, st, site);
+    // A place in the ring of K and V tiles.
+    struct Place {
+      int slot;
+      uint32_t parity;
+      __device__ void skip(int entries) {  // fewer than NSLOT
+        slot += entries;
+        if (slot >= C::NSLOT) slot -= C::NSLOT, parity ^= 1;
+      }
+      __device__ void skip_tiles(int tiles) {
+        const int x = slot + 2 * tiles;
+        slot = x % C::NSLOT;
+        parity ^= (uint32_t)(x / C::NSLOT) & 1;
+      }
     };
     auto release = [&](uint32_t full_bar, uint32_t parity, uint32_t empty_bar) {  // what this lane does not read
-      if (!wait_warp_sleep(full_bar, parity, st, SITE_SW_RELEASE)) return false;
+      if (!wait_warp_fast(full_bar, parity, st, SITE_SW_RELEASE)) return false;
       if (elect_one()) mbar_arrive(empty_bar);
       __syncwarp();
       return true;
     };
-    int e0 = 0, uq = 0, used = 0;  // ring tiles and Q slots before the item, this lane's items so far
-    int g_s = 0, g_p = 0;  // S and PV steps issued so far
+    auto pass_by = [&](Place p) {  // releases a whole tile of the other lane
+      if (!release(BAR(C::FULL + p.slot), p.parity, BAR(C::EMPTY + p.slot))) return false;
+      p.skip(1);
+      return release(BAR(C::FULL + p.slot), p.parity, BAR(C::EMPTY + p.slot));
+    };
+    Place ring = {0, 0};                // the item's first K
+    int uq = 0, used = 0, g_s = 0, g_p = 0;  // Q slots and this lane's items before; S and PV steps issued so far
     bool ok = true;
     for (int i = 0; ok; ++i) {
       ServeItem it;
       if (!next_item(i, &it) || it.cnt < 0) break;
       const bool dual = it.flags & ITEM_DUAL;
-      const int steps = t ? it.s1 : it.s0;
+      const int steps = t ? it.s1 : it.s0, tiles = t ? it.c1 : it.c0;
       const int qu = dual ? uq : uq + t;  // this lane's Q slot use
       const uint32_t qa = q_lo + (qu & 1) * TILE16;
-      auto tile = [&](int kk) { return dual ? 2 * kk + t : kk; };
-      int sk = 0, sh = 0, left = steps;  // the next S step: tile and half
+      const int stride = dual ? 2 : 1;    // tiles from one of the lane's to the next
+      Place ks = ring, vs = ring;         // the next S step's K, the next PV step's V
+      vs.skip(1);
+      if (dual && t == 1) ks.skip(2), vs.skip(2);
+      int js = it.j0 + (dual ? t : 0), jp = js;
+      int hs = 0, left = steps;           // half of the next S step, S steps to issue
       auto issue_s = [&]() {  // S = Q K^T; then K's slot and, after the last one, Q's are done with
-        const int x = 2 * (e0 + tile(sk)), h = sh;
-        if (!full(x, SITE_SW_K_FULL)) return false;
-        if (C::SEP_P && g_s > 0 && !wait_warp_sleep(BAR(C::S_FREE + t), (g_s - 1) & 1, st, SITE_SW_S_FREE)) return false;
-        tc_fence_after();
-        const uint32_t ka = k_lo + (x % C::NSLOT) * TILE16 + h * HALF16, d = tmem + C::tm_s(t, C::buf(g_s));
+        if (hs == 0 && !wait_warp_fast(BAR(C::FULL + ks.slot), ks.parity, st, SITE_SW_K_FULL)) return false;
+        if (C::SEP_P) {
+          if (g_s > 0 && !wait_warp_fast(BAR(C::S_FREE + t), (g_s - 1) & 1, st, SITE_SW_S_FREE)) return false;
+          tc_fence_after();
+        }
+        const uint32_t ka = k_lo + ks.slot * TILE16 + hs * HALF16, d = tmem + C::tm_s(t, C::buf(g_s));
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const uint32_t off = ((k >> 2) * C::SUB_BYTES + (k & 3) * 32) >> 4;
@@ -503,74 +524,79 @@ __global__ void __launch_bounds__(352, 1)
         }
         commit(BAR(C::S_FULL + 2 * t + C::buf(g_s)));
         ++g_s;
-        if (h + 1 == steps_in(it, t, it.j0 + tile(sk))) {
-          commit(BAR(C::EMPTY + x % C::NSLOT));
-          ++sk;
-          sh = 0;
+        --left;
+        if (C::HPT == 1 || hs + 1 == steps_in(it, t, js)) {
+          commit(BAR(C::EMPTY + ks.slot));
+          if (left == 0) commit(BAR(C::Q_EMPTY + (qu & 1)));
+          ks.skip(2 * stride);
+          js += stride;
+          hs = 0;
         } else {
-          ++sh;
-        }
-        if (--left == 0) commit(BAR(C::Q_EMPTY + (qu & 1)));
-        return true;
-      };
-      int pk = 0, ph = 0, freed = 0;  // the next PV step; ring tiles that this lane is done with
-      auto pass_by = [&](int to) {  // releases the tiles before ring tile `to` that are the other lane's
-        for (; freed < to; ++freed) {
-          if (dual ? (freed & 1) == t : freed < (t ? it.c1 : it.c0)) continue;
-          const int x = 2 * (e0 + freed), y = x + 1;
-          if (!release(BAR(C::FULL + x % C::NSLOT), (x / C::NSLOT) & 1, BAR(C::EMPTY + x % C::NSLOT)) ||
-              !release(BAR(C::FULL + y % C::NSLOT), (y / C::NSLOT) & 1, BAR(C::EMPTY + y % C::NSLOT)))
-            return false;
+          hs = 1;
         }
         return true;
       };
-      auto issue_pv = [&](bool first) {  // O += P V
-        const int x = 2 * (e0 + tile(pk)) + 1, s = x % C::NSLOT, h = ph, j = it.j0 + tile(pk);
-        if (!full(x, SITE_SW_V_FULL)) return false;
-        const int rows = (j < it.nc ? it.L - j * 128 : it.n - (j - it.nc) * 128) - h * C::KT;
-        if (rows < C::KT) {
+      if (steps > 0) {
+        ok = wait_warp_fast(BAR(C::Q_FULL + (qu & 1)), (qu >> 1) & 1, st, SITE_SW_Q_FULL) && issue_s();
+        if (ok && !C::SEP_P && left > 0) ok = issue_s();
+      }
+      for (int kk = 0, s = 0; ok && kk < tiles; ++kk, jp += stride) {
+        if (C::SEP_P && left > 0 && !(ok = issue_s())) break;
+        if (dual && t == 1) {  // the tile before is lane 0's
+          Place p = vs;
+          p.skip(C::NSLOT - 3);
+          p.parity ^= 1;
+          if (!(ok = pass_by(p))) break;
+        }
+        if (!(ok = wait_warp_fast(BAR(C::FULL + vs.slot), vs.parity, st, SITE_SW_V_FULL))) break;
+        const int rows = jp < it.nc ? it.L - jp * 128 : it.n - (jp - it.nc) * 128;
+        const int halves = steps_in(it, t, jp);
+        if (rows < halves * C::KT) {
           // rows past the sequence may hold anything; P is 0 there, but 0 x NaN is not
-          uint8_t* v = sm + C::OFF_R + s * C::TILE_BYTES + (h * C::KT + rows) * 128;
-          const int chunks = (C::KT - rows) * 8;
+          uint8_t* v = sm + C::OFF_R + vs.slot * C::TILE_BYTES + rows * 128;
+          const int chunks = (halves * C::KT - rows) * 8;
           for (int z = lane; z < chunks * C::NSUB; z += 32)
             *reinterpret_cast<uint4*>(v + z / chunks * C::SUB_BYTES + z % chunks * 16) = make_uint4(0, 0, 0, 0);
           fence_proxy_async_smem();
           __syncwarp();
         }
-        const int u = C::buf(g_p);
-        if (!wait_warp_sleep(BAR(C::P_READY + 2 * t + u), C::phase(g_p), st, SITE_SW_P_READY)) return false;
-        if (first && used > 0 && !wait_warp_sleep(BAR(C::O_FREE + t), (used - 1) & 1, st, SITE_SW_O_FREE)) return false;
-        tc_fence_after();
-        const uint32_t va = v_lo + s * TILE16 + h * HALF16, d = tmem + C::tm_o(t), pa = tmem + C::tm_p(t, u);
+        for (int h = 0; h < halves; ++h, ++s) {  // O += P V
+          if (!(ok = wait_warp_fast(BAR(C::P_READY + 2 * t + C::buf(g_p)), C::phase(g_p), st, SITE_SW_P_READY))) break;
+          if (s == 0 && used > 0 && !(ok = wait_warp_fast(BAR(C::O_FREE + t), (used - 1) & 1, st, SITE_SW_O_FREE))) break;
+          tc_fence_after();
+          const uint32_t va = v_lo + vs.slot * TILE16 + h * HALF16, d = tmem + C::tm_o(t), pa = tmem + C::tm_p(t, C::buf(g_p));
 #pragma unroll
-        for (int k = 0; k < C::KT / 16; ++k)
-          if (elect_one()) mma_ts(d, pa + k * 8, sdesc_join(va + k * (2048 >> 4), HI), IDESC_O, !first || k > 0);
-        commit(BAR(C::O_DONE + t));
-        ++g_p;
-        if (h + 1 == steps_in(it, t, j)) {
-          commit(BAR(C::EMPTY + s));
-          ++pk;
-          ph = 0;
-        } else {
-          ++ph;
+          for (int k = 0; k < C::KT / 16; ++k)
+            if (elect_one()) mma_ts(d, pa + k * 8, sdesc_join(va + k * (2048 >> 4), HI), IDESC_O, s > 0 || k > 0);
+          ++g_p;
+          // d = 128: the softmax learns from S of the step after next that PV is done, but for the
+          // last two steps, which have none
+          if (C::SEP_P || s + 2 >= steps) commit(BAR(C::O_DONE + t));
+          if (h + 1 == halves) commit(BAR(C::EMPTY + vs.slot));
+          if (!C::SEP_P && left > 0 && !(ok = issue_s())) break;
         }
-        return true;
-      };
-      if (steps > 0) {
-        ok = wait_warp_sleep(BAR(C::Q_FULL + (qu & 1)), (qu >> 1) & 1, st, SITE_SW_Q_FULL) && issue_s();
-        if (ok && !C::SEP_P && left > 0) ok = issue_s();
+        if (!ok) break;
+        Place p = vs;
+        vs.skip(2 * stride);
+        if (dual && t == 0 && 2 * kk + 1 < it.cnt) {  // the tile behind is lane 1's
+          p.skip(1);
+          ok = pass_by(p);
+        }
       }
-      for (int s = 0; ok && s < steps; ++s) {
-        if (C::SEP_P && left > 0 && !(ok = issue_s())) break;
-        if (!(ok = pass_by(tile(pk)) && issue_pv(s == 0))) break;
-        if (!C::SEP_P && left > 0) ok = issue_s();
+      // what is left of the ring and of Q that this lane did not read
+      if (dual && t == 1 && (it.cnt & 1)) {
+        Place p = ring;
+        p.skip_tiles(it.cnt - 1);
+        ok = ok && pass_by(p);
+      } else if (!dual) {
+        Place p = ring;
+        p.skip_tiles(tiles);
+        for (int k = tiles; ok && k < it.cnt; ++k, p.skip(2)) ok = pass_by(p);
       }
-      if (ok) ok = pass_by(it.cnt);
-      // Q slots that this lane did not read
       for (int u = uq; ok && u < uq + (dual ? 1 : 2); ++u)
         if (u != qu || steps == 0)
           ok = release(BAR(C::Q_FULL + (u & 1)), (u >> 1) & 1, BAR(C::Q_EMPTY + (u & 1)));
-      e0 += it.cnt;
+      ring.skip_tiles(it.cnt);
       uq += dual ? 1 : 2;
       used += steps > 0;
     }
@@ -587,28 +613,32 @@ __global__ void __launch_bounds__(352, 1)
     const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
     const float sl2 = a.scale_log2;
     float* ml = reinterpret_cast<float*>(sm + C::OFF_ML);
-    int st0 = 0, st1 = 0, merges = 0;  // steps of both lanes and joins of dual items so far
+    // steps of both lanes, those of them that O_DONE counts, and joins of dual items so far
+    int st0 = 0, st1 = 0, so0 = 0, so1 = 0, merges = 0;
     for (int i = 0;; ++i) {
       ServeItem it;
       if (!next_item(i, &it) || it.cnt < 0) break;
       const bool dual = it.flags & ITEM_DUAL, whole = it.flags & ITEM_WHOLE;
       const int steps = t ? it.s1 : it.s0, before = t ? st1 : st0;
+      const int before_o = t ? so1 : so0;
       const int tok = it.tok0 + (dual ? 0 : t * npt) + rn;
       const bool valid = rn < npt && tok < it.n;
       const bool any = __any_sync(0xffffffffu, valid);
       float m_run = -INFINITY, l_run = 0.f;
       bool ok = true;
-      int j = it.j0 + (dual ? t : 0), h = 0;  // the step's key tile and half
-      for (int s = 0; s < steps; ++s) {
-        const int hs = h, js = j;
-        if (h + 1 < steps_in(it, t, j)) {
-          ++h;
-        } else {
-          h = 0;
-          j += dual ? 2 : 1;
+      const int tok_first = __shfl_sync(0xffffffffu, tok, 0);  // the warp's tokens ascend with its rows
+      const int last = steps - 1;
+      const int od = before_o - (C::SEP_P ? 0 : steps - min(steps, 2));  // O_DONE phase of step 0, were it counted
+      const int stride = dual ? 2 : 1;
+      int js = it.j0 + (dual ? t : 0), hs = 0, halves = steps_in(it, t, js);  // the step's key tile and half
+      for (int s = 0; s < steps; ++s, ++hs) {
+        if (hs == halves) {
+          hs = 0;
+          js += stride;
+          halves = steps_in(it, t, js);
         }
         const int u = C::buf(before + s);
-        if (!(ok = wait_warp_sleep(BAR(C::S_FULL + 2 * t + u), C::phase(before + s), st, SITE_SW_S_FULL))) break;
+        if (!(ok = wait_warp_fast(BAR(C::S_FULL + 2 * t + u), C::phase(before + s), st, SITE_SW_S_FULL))) break;
         if (!any) {  // no row here: P stays what it is, its rows of O are nobody's
           __syncwarp();
           if (C::SEP_P) {
@@ -616,8 +646,8 @@ __global__ void __launch_bounds__(352, 1)
           }
           // d = 64: S of this tile may be there before the other warps have written P of the one
           // before: an arrival now would count for that one. d = 128: see below
-          if (s > 0 && (C::SEP_P || s == steps - 1) &&
-              !(ok = wait_warp_sleep(BAR(C::O_DONE + t), (before + s - 1) & 1, st, SITE_SW_O_DONE)))
+          if (s > 0 && (C::SEP_P || s == last) &&
+              !(ok = wait_warp_fast(BAR(C::O_DONE + t), (od + s - 1) & 1, st, SITE_SW_O_DONE)))
             break;
           if (lane == 0) mbar_arrive(BAR(C::P_READY + 2 * t + u));
           continue;
@@ -654,9 +684,10 @@ __global__ void __launch_bounds__(352, 1)
           for (int x = 0; x < KT; ++x)
             if (!(w[x >> 5] >> (x & 31) & 1)) sv[x] = -INFINITY;
         } else {
-          // keys [0, lim) of the step are seen
-          const int lim = (js < it.nc ? it.L - js * 128 : min(it.n, tok + 1) - (js - it.nc) * 128) - hs * KT;
-          if (__any_sync(0xffffffffu, lim < KT)) {
+          // keys [0, lim) of the step are seen, by the warp's first row fewest
+          const int k0 = js * 128 + hs * KT - (js < it.nc ? it.L : it.nc * 128);
+          if (js < it.nc ? k0 > -KT : min(it.n, tok_first + 1) < k0 + KT) {
+            const int lim = js < it.nc ? -k0 : min(it.n, tok + 1) - k0;
 #pragma unroll
             for (int x = 0; x < KT; ++x)
               if (x >= lim) sv[x] = -INFINITY;
@@ -702,7 +733,7 @@ __global__ void __launch_bounds__(352, 1)
           }
           if (C::SEP_P && q == 1) {
             if (s > 0) {  // PV of the tile before has read P (across items its epilogue waited for that)
-              if (!(ok = wait_warp_sleep(BAR(C::O_DONE + t), (before + s - 1) & 1, st, SITE_SW_O_DONE))) break;
+              if (!(ok = wait_warp_fast(BAR(C::O_DONE + t), (od + s - 1) & 1, st, SITE_SW_O_DONE))) break;
               tc_fence_after();
             }
             tmem_st16(tP, pk[0]);
@@ -715,11 +746,14 @@ __global__ void __launch_bounds__(352, 1)
         f2_unpack(ps2[0], ps[0], ps[1]);
         f2_unpack(ps2[1], ps[2], ps[3]);
         l_run = l_run * f + ((ps[0] + ps[1]) + (ps[2] + ps[3]));
-        // d = 128: S of this step was formed behind PV of the last step but one, so that the phase of the
-        // last one is the one this wait can meet. It is waited for before O is rescaled, and before
-        // the last P is published: the wait for the last PV below would else take that phase for its own.
-        if (!C::SEP_P && s > 0 && (rescale_warp || s == steps - 1)) {
-          if (!(ok = wait_warp_sleep(BAR(C::O_DONE + t), (before + s - 1) & 1, st, SITE_SW_O_DONE))) break;
+        // d = 128: S of this step was formed behind PV of the last step but one. PV of the last step is
+        // waited for before O is rescaled (S of the next step was formed behind it), and before the
+        // last P is published: the wait for the last PV below would else take its phase for its own.
+        if (!C::SEP_P && s > 0 && (rescale_warp || s == last)) {
+          const int v = C::buf(before + s + 1);
+          ok = s == last ? wait_warp_fast(BAR(C::O_DONE + t), (od + s - 1) & 1, st, SITE_SW_O_DONE)
+                         : wait_warp_fast(BAR(C::S_FULL + 2 * t + v), C::phase(before + s + 1), st, SITE_SW_S_FULL);
+          if (!ok) break;
           tc_fence_after();
         }
         if (rescale_warp) {
@@ -739,7 +773,7 @@ __global__ void __launch_bounds__(352, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(BAR(C::P_READY + 2 * t + u));
       }
-      if (ok && steps > 0) ok = wait_warp_sleep(BAR(C::O_DONE + t), (before + steps - 1) & 1, st, SITE_SW_O_DONE);
+      if (ok && steps > 0) ok = wait_warp_fast(BAR(C::O_DONE + t), (od + last) & 1, st, SITE_SW_O_DONE);
       if (!ok) break;
       tc_fence_after();
       const bool join = dual && it.c1 > 0;
@@ -752,7 +786,7 @@ __global__ void __launch_bounds__(352, 1)
           if (lane == 0) mbar_arrive(BAR(C::MERGE));
         } else {
           if (!wait_warp_sleep(BAR(C::MERGE), merges & 1, st, SITE_SW_MERGE) ||
-              !wait_warp_sleep(BAR(C::O_DONE + 1), (st1 + it.s1 - 1) & 1, st, SITE_SW_O_DONE))
+              !wait_warp_sleep(BAR(C::O_DONE + 1), (so1 + (C::SEP_P ? it.s1 : min(it.s1, 2)) - 1) & 1, st, SITE_SW_O_DONE))
             break;
           tc_fence_after();
           const float m1 = ml[row], m = fmaxf(m_run, m1), base = m == -INFINITY ? 0.f : m;
@@ -765,6 +799,8 @@ __global__ void __launch_bounds__(352, 1)
       }
       st0 += it.s0;
       st1 += it.s1;
+      so0 += C::SEP_P ? it.s0 : min(it.s0, 2);
+      so1 += C::SEP_P ? it.s1 : min(it.s1, 2);
       if (dual && t == 1) continue;  // lane 0 writes the results
       // l = 0: no key; NaN stays NaN
       const float inv = l_run != 0.f ? 1.f / l_run : 0.f;
