@@ -50,8 +50,10 @@ constexpr int kNewBox = 16;
 // tile only, both lanes take it and alternate key tiles ("dual"), and lane 0 joins the two
 // results out of tensor memory at the end.
 //
-// Roles, 352 threads: warps 0-3 and 4-7 the softmax of lanes 0 and 1 (a thread a row), warp 8
-// the TMA producer and scheduler, warps 9 and 10 the MMA issuers of lanes 0 and 1. The producer
+// Roles, 384 threads: warps 0-3 and 4-7 the softmax of lanes 0 and 1 (a thread a row), warp 8
+// the TMA producer and scheduler, warps 9 and 10 the issuers of O += P V of lanes 0 and 1, warp
+// 11 the issuer of S = Q K^T of both. (One issuer a lane for both products measured 215 us on
+// the long prompts: its own instructions took longer than the products.) The producer
 // runs ahead: it publishes items in a ring of four descriptors, loads Q into two slots and K and
 // V tiles alternately into one ring of NSLOT slots (224 KB with Q). A page is one TMA box, the
 // lanes of the producer warp issuing one each. All rings and barrier phases run on across items.
@@ -84,10 +86,10 @@ struct ServeCfg {
   __device__ static constexpr uint32_t tm_p(int t, int u) { return SEP_P ? 256u + 64u * t : tm_s(t, u); }
   __device__ static constexpr uint32_t tm_o(int t) { return SEP_P ? 384u + 64u * t : 256u + (uint32_t)D * t; }
   static constexpr uint32_t TM_COLS = 512;
-  static constexpr int THREADS = 352;
+  static constexpr int THREADS = 384;
   // barriers
   static constexpr int FULL = 0, EMPTY = NSLOT, Q_FULL = 2 * NSLOT, Q_EMPTY = Q_FULL + 2, S_FULL = Q_EMPTY + 2,
-                       P_READY = S_FULL + 4, O_DONE = P_READY + 4, S_FREE = O_DONE + 2, O_FREE = S_FREE + 2,
+                       P_READY = S_FULL + 4, O_DONE = P_READY + 4, S_FREE = O_DONE + 4, O_FREE = S_FREE + 2,
                        MERGE = O_FREE + 2, DRAIN = MERGE + 1, D_FULL = DRAIN + 1, D_EMPTY = D_FULL + 4,
                        BARS = D_EMPTY + 4;
 };
@@ -96,7 +98,7 @@ static_assert(ServeCfg<64>::SMEM_BYTES <= 232448 && ServeCfg<128>::SMEM_BYTES <=
 
 enum { SITE_SW_EMPTY = 60, SITE_SW_Q_FULL, SITE_SW_Q_EMPTY, SITE_SW_K_FULL, SITE_SW_V_FULL, SITE_SW_S_FREE,
        SITE_SW_P_READY, SITE_SW_O_FREE, SITE_SW_S_FULL, SITE_SW_O_DONE, SITE_SW_MERGE, SITE_SW_DESC_FULL,
-       SITE_SW_DESC_EMPTY, SITE_SW_RELEASE };
+       SITE_SW_DESC_EMPTY };
 
 // A work item (or the part of it that this CTA computes), as the producer publishes it.
 struct ServeItem {
@@ -225,7 +227,7 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 }
 
 template <int D, bool F16, bool PAGED>
-__global__ void __launch_bounds__(352, 1)
+__global__ void __launch_bounds__(384, 1)
     serve_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                  const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_kc,
                  const __grid_constant__ CUtensorMap tm_vc, ServeArgs a) {
@@ -245,24 +247,24 @@ __global__ void __launch_bounds__(352, 1)
   if (warp == 8 && lane == 0) {
     for (int i = 0; i < C::NSLOT; ++i) {
       mbar_init(BAR(C::FULL + i), 1);
-      mbar_init(BAR(C::EMPTY + i), 2);  // both issuers
+      mbar_init(BAR(C::EMPTY + i), 2);  // V: both issuers; K: its issuer twice
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(BAR(C::Q_FULL + t), 1);
-      mbar_init(BAR(C::Q_EMPTY + t), 2);
+      mbar_init(BAR(C::Q_EMPTY + t), 1);
       for (int h = 0; h < 2; ++h) {
         mbar_init(BAR(C::S_FULL + 2 * t + h), 1);
         mbar_init(BAR(C::P_READY + 2 * t + h), 4);
+        mbar_init(BAR(C::O_DONE + 2 * t + h), 1);
       }
-      mbar_init(BAR(C::O_DONE + t), 1);
       mbar_init(BAR(C::S_FREE + t), 4);
       mbar_init(BAR(C::O_FREE + t), 4);
     }
     mbar_init(BAR(C::MERGE), 4);
-    mbar_init(BAR(C::DRAIN), 2);
+    mbar_init(BAR(C::DRAIN), 3);
     for (int i = 0; i < 4; ++i) {
       mbar_init(BAR(C::D_FULL + i), 1);
-      mbar_init(BAR(C::D_EMPTY + i), 10);  // softmax warps and issuers
+      mbar_init(BAR(C::D_EMPTY + i), 11);  // softmax warps and issuers
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -458,13 +460,10 @@ __global__ void __launch_bounds__(352, 1)
       }
     }
   } else if (warp >= 9) {
-    // ------------------------------------------------------------ MMA issuer of lane t
-    const int t = warp - 9;
+    // ------------------------------------------------------------ MMA issuers
     constexpr uint32_t IDESC_S = F16 ? idesc_f16_f32(128, C::KT, 0, 0) : idesc_bf16_f32(128, C::KT, 0, 0);
     constexpr uint32_t IDESC_O = F16 ? idesc_f16_f32(128, D, 0, 1) : idesc_bf16_f32(128, D, 0, 1);
     constexpr uint32_t HI = sdesc_hi(1024), TILE16 = C::TILE_BYTES >> 4, HALF16 = (C::KT * 128) >> 4;
-    const uint32_t q_lo = sdesc_lo(sbase + C::OFF_Q, 16), k_lo = sdesc_lo(sbase + C::OFF_R, 16);
-    const uint32_t v_lo = sdesc_lo(sbase + C::OFF_R, C::SUB_BYTES);
     auto commit = [&](uint32_t bar) {
       if (elect_one()) mma_commit(bar);
       __syncwarp();
@@ -477,128 +476,104 @@ __global__ void __launch_bounds__(352, 1)
         slot += entries;
         if (slot >= C::NSLOT) slot -= C::NSLOT, parity ^= 1;
       }
-      __device__ void skip_tiles(int tiles) {
-        const int x = slot + 2 * tiles;
-        slot = x % C::NSLOT;
-        parity ^= (uint32_t)(x / C::NSLOT) & 1;
-      }
     };
-    auto release = [&](uint32_t full_bar, uint32_t parity, uint32_t empty_bar) {  // what this lane does not read
-      if (!wait_warp_fast(full_bar, parity, st, SITE_SW_RELEASE)) return false;
-      if (elect_one()) mbar_arrive(empty_bar);
-      __syncwarp();
-      return true;
-    };
-    auto pass_by = [&](Place p) {  // releases a whole tile of the other lane
-      if (!release(BAR(C::FULL + p.slot), p.parity, BAR(C::EMPTY + p.slot))) return false;
-      p.skip(1);
-      return release(BAR(C::FULL + p.slot), p.parity, BAR(C::EMPTY + p.slot));
-    };
-    Place ring = {0, 0};                // the item's first K
-    int uq = 0, used = 0, g_s = 0, g_p = 0;  // Q slots and this lane's items before; S and PV steps issued so far
     bool ok = true;
-    for (int i = 0; ok; ++i) {
-      ServeItem it;
-      if (!next_item(i, &it) || it.cnt < 0) break;
-      const bool dual = it.flags & ITEM_DUAL;
-      const int steps = t ? it.s1 : it.s0, tiles = t ? it.c1 : it.c0;
-      const int qu = dual ? uq : uq + t;  // this lane's Q slot use
-      const uint32_t qa = q_lo + (qu & 1) * TILE16;
-      const int stride = dual ? 2 : 1;    // tiles from one of the lane's to the next
-      Place ks = ring, vs = ring;         // the next S step's K, the next PV step's V
-      vs.skip(1);
-      if (dual && t == 1) ks.skip(2), vs.skip(2);
-      int js = it.j0 + (dual ? t : 0), jp = js;
-      int hs = 0, left = steps;           // half of the next S step, S steps to issue
-      auto issue_s = [&]() {  // S = Q K^T; then K's slot and, after the last one, Q's are done with
-        if (hs == 0 && !wait_warp_fast(BAR(C::FULL + ks.slot), ks.parity, st, SITE_SW_K_FULL)) return false;
-        if (C::SEP_P) {
-          if (g_s > 0 && !wait_warp_fast(BAR(C::S_FREE + t), (g_s - 1) & 1, st, SITE_SW_S_FREE)) return false;
+    if (warp == 11) {
+      // S = Q K^T of both lanes, tile after tile in the order of the ring
+      const uint32_t q_lo = sdesc_lo(sbase + C::OFF_Q, 16), k_lo = sdesc_lo(sbase + C::OFF_R, 16);
+      Place ks = {0, 0};
+      int uq = 0, g0 = 0, g1 = 0;  // Q slots and steps of both lanes so far
+      for (int i = 0; ok; ++i) {
+        ServeItem it;
+        if (!next_item(i, &it) || it.cnt < 0) break;
+        const bool dual = it.flags & ITEM_DUAL;
+        const int nq = dual ? 1 : 2;
+        for (int u = uq; ok && u < uq + nq; ++u)
+          ok = wait_warp_fast(BAR(C::Q_FULL + (u & 1)), (u >> 1) & 1, st, SITE_SW_Q_FULL);
+        const uint32_t qa0 = q_lo + (uq & 1) * TILE16, qa1 = q_lo + ((uq + nq - 1) & 1) * TILE16;
+        auto issue_s = [&](int t, int g, uint32_t qa, uint32_t ka) {
+          // S(g) goes over S(g - 1), once it is in registers (d = 64), or over P(g - 2), once PV has read it
+          if (C::SEP_P ? g > 0 : g > 1) {
+            if (C::SEP_P ? !wait_warp_fast(BAR(C::S_FREE + t), (g - 1) & 1, st, SITE_SW_S_FREE)
+                         : !wait_warp_fast(BAR(C::O_DONE + 2 * t + C::buf(g)), C::phase(g - 2), st, SITE_SW_O_DONE))
+              return false;
+          }
           tc_fence_after();
-        }
-        const uint32_t ka = k_lo + ks.slot * TILE16 + hs * HALF16, d = tmem + C::tm_s(t, C::buf(g_s));
+          const uint32_t d = tmem + C::tm_s(t, C::buf(g));
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = ((k >> 2) * C::SUB_BYTES + (k & 3) * 32) >> 4;
-          if (elect_one()) mma_ss(d, sdesc_join(qa + off, HI), sdesc_join(ka + off, HI), IDESC_S, k > 0);
-        }
-        commit(BAR(C::S_FULL + 2 * t + C::buf(g_s)));
-        ++g_s;
-        --left;
-        if (C::HPT == 1 || hs + 1 == steps_in(it, t, js)) {
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = ((k >> 2) * C::SUB_BYTES + (k & 3) * 32) >> 4;
+            if (elect_one()) mma_ss(d, sdesc_join(qa + off, HI), sdesc_join(ka + off, HI), IDESC_S, k > 0);
+          }
+          commit(BAR(C::S_FULL + 2 * t + C::buf(g)));
+          return true;
+        };
+        for (int k = 0; ok && k < it.cnt; ++k) {
+          if (!(ok = wait_warp_fast(BAR(C::FULL + ks.slot), ks.parity, st, SITE_SW_K_FULL))) break;
+          const int j = it.j0 + k;
+          const int h0 = (dual ? (k & 1) : k >= it.c0) ? 0 : steps_in(it, 0, j);
+          const int h1 = (dual ? !(k & 1) : k >= it.c1) ? 0 : steps_in(it, 1, j);
+          const uint32_t ka = k_lo + ks.slot * TILE16;
+          for (int h = 0; ok && h < max(h0, h1); ++h) {
+            if (h < h0) ok = issue_s(0, g0++, qa0, ka + h * HALF16);
+            if (ok && h < h1) ok = issue_s(1, g1++, qa1, ka + h * HALF16);
+          }
           commit(BAR(C::EMPTY + ks.slot));
-          if (left == 0) commit(BAR(C::Q_EMPTY + (qu & 1)));
-          ks.skip(2 * stride);
-          js += stride;
-          hs = 0;
-        } else {
-          hs = 1;
+          commit(BAR(C::EMPTY + ks.slot));
+          ks.skip(2);
         }
-        return true;
-      };
-      if (steps > 0) {
-        ok = wait_warp_fast(BAR(C::Q_FULL + (qu & 1)), (qu >> 1) & 1, st, SITE_SW_Q_FULL) && issue_s();
-        if (ok && !C::SEP_P && left > 0) ok = issue_s();
+        for (int u = uq; u < uq + nq; ++u) commit(BAR(C::Q_EMPTY + (u & 1)));
+        uq += nq;
       }
-      for (int kk = 0, s = 0; ok && kk < tiles; ++kk, jp += stride) {
-        if (C::SEP_P && left > 0 && !(ok = issue_s())) break;
-        if (dual && t == 1) {  // the tile before is lane 0's
-          Place p = vs;
-          p.skip(C::NSLOT - 3);
-          p.parity ^= 1;
-          if (!(ok = pass_by(p))) break;
-        }
-        if (!(ok = wait_warp_fast(BAR(C::FULL + vs.slot), vs.parity, st, SITE_SW_V_FULL))) break;
-        const int rows = jp < it.nc ? it.L - jp * 128 : it.n - (jp - it.nc) * 128;
-        const int halves = steps_in(it, t, jp);
-        if (rows < halves * C::KT) {
-          // rows past the sequence may hold anything; P is 0 there, but 0 x NaN is not
-          uint8_t* v = sm + C::OFF_R + vs.slot * C::TILE_BYTES + rows * 128;
-          const int chunks = (halves * C::KT - rows) * 8;
-          for (int z = lane; z < chunks * C::NSUB; z += 32)
-            *reinterpret_cast<uint4*>(v + z / chunks * C::SUB_BYTES + z % chunks * 16) = make_uint4(0, 0, 0, 0);
-          fence_proxy_async_smem();
-          __syncwarp();
-        }
-        for (int h = 0; h < halves; ++h, ++s) {  // O += P V
-          if (!(ok = wait_warp_fast(BAR(C::P_READY + 2 * t + C::buf(g_p)), C::phase(g_p), st, SITE_SW_P_READY))) break;
-          if (s == 0 && used > 0 && !(ok = wait_warp_fast(BAR(C::O_FREE + t), (used - 1) & 1, st, SITE_SW_O_FREE))) break;
-          tc_fence_after();
-          const uint32_t va = v_lo + vs.slot * TILE16 + h * HALF16, d = tmem + C::tm_o(t), pa = tmem + C::tm_p(t, C::buf(g_p));
+    } else {
+      // O += P V of lane t
+      const int t = warp - 9;
+      const uint32_t v_lo = sdesc_lo(sbase + C::OFF_R, C::SUB_BYTES);
+      Place vs = {1, 0};
+      int used = 0, g = 0;  // this lane's items and steps so far
+      for (int i = 0; ok; ++i) {
+        ServeItem it;
+        if (!next_item(i, &it) || it.cnt < 0) break;
+        const bool dual = it.flags & ITEM_DUAL;
+        const int tiles = t ? it.c1 : it.c0;
+        bool first = true;
+        for (int k = 0; ok && k < it.cnt; ++k) {
+          if (!(ok = wait_warp_fast(BAR(C::FULL + vs.slot), vs.parity, st, SITE_SW_V_FULL))) break;
+          if (dual ? (k & 1) != t : k >= tiles) {  // the other lane's
+            if (elect_one()) mbar_arrive(BAR(C::EMPTY + vs.slot));
+            __syncwarp();
+            vs.skip(2);
+            continue;
+          }
+          const int j = it.j0 + k;
+          const int rows = j < it.nc ? it.L - j * 128 : it.n - (j - it.nc) * 128;
+          const int halves = steps_in(it, t, j);
+          if (rows < halves * C::KT) {
+            // rows past the sequence may hold anything; P is 0 there, but 0 x NaN is not
+            uint8_t* v = sm + C::OFF_R + vs.slot * C::TILE_BYTES + rows * 128;
+            const int chunks = (halves * C::KT - rows) * 8;
+            for (int z = lane; z < chunks * C::NSUB; z += 32)
+              *reinterpret_cast<uint4*>(v + z / chunks * C::SUB_BYTES + z % chunks * 16) = make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+          for (int h = 0; h < halves; ++h, ++g, first = false) {
+            if (!(ok = wait_warp_fast(BAR(C::P_READY + 2 * t + C::buf(g)), C::phase(g), st, SITE_SW_P_READY))) break;
+            if (first && used > 0 && !(ok = wait_warp_fast(BAR(C::O_FREE + t), (used - 1) & 1, st, SITE_SW_O_FREE))) break;
+            tc_fence_after();
+            const uint32_t va = v_lo + vs.slot * TILE16 + h * HALF16;
+            const uint32_t d = tmem + C::tm_o(t), pa = tmem + C::tm_p(t, C::buf(g));
 #pragma unroll
-          for (int k = 0; k < C::KT / 16; ++k)
-            if (elect_one()) mma_ts(d, pa + k * 8, sdesc_join(va + k * (2048 >> 4), HI), IDESC_O, s > 0 || k > 0);
-          ++g_p;
-          // d = 128: the softmax learns from S of the step after next that PV is done, but for the
-          // last two steps, which have none
-          if (C::SEP_P || s + 2 >= steps) commit(BAR(C::O_DONE + t));
-          if (h + 1 == halves) commit(BAR(C::EMPTY + vs.slot));
-          if (!C::SEP_P && left > 0 && !(ok = issue_s())) break;
+            for (int q = 0; q < C::KT / 16; ++q)
+              if (elect_one()) mma_ts(d, pa + q * 8, sdesc_join(va + q * (2048 >> 4), HI), IDESC_O, !first || q > 0);
+            commit(BAR(C::O_DONE + 2 * t + C::buf(g)));
+          }
+          if (!ok) break;
+          commit(BAR(C::EMPTY + vs.slot));
+          vs.skip(2);
         }
-        if (!ok) break;
-        Place p = vs;
-        vs.skip(2 * stride);
-        if (dual && t == 0 && 2 * kk + 1 < it.cnt) {  // the tile behind is lane 1's
-          p.skip(1);
-          ok = pass_by(p);
-        }
+        used += tiles > 0;
       }
-      // what is left of the ring and of Q that this lane did not read
-      if (dual && t == 1 && (it.cnt & 1)) {
-        Place p = ring;
-        p.skip_tiles(it.cnt - 1);
-        ok = ok && pass_by(p);
-      } else if (!dual) {
-        Place p = ring;
-        p.skip_tiles(tiles);
-        for (int k = tiles; ok && k < it.cnt; ++k, p.skip(2)) ok = pass_by(p);
-      }
-      for (int u = uq; ok && u < uq + (dual ? 1 : 2); ++u)
-        if (u != qu || steps == 0)
-          ok = release(BAR(C::Q_FULL + (u & 1)), (u >> 1) & 1, BAR(C::Q_EMPTY + (u & 1)));
-      ring.skip_tiles(it.cnt);
-      uq += dual ? 1 : 2;
-      used += steps > 0;
     }
     // every MMA issued has completed before TMEM is released
     commit(BAR(C::DRAIN));
@@ -613,22 +588,21 @@ __global__ void __launch_bounds__(352, 1)
     const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
     const float sl2 = a.scale_log2;
     float* ml = reinterpret_cast<float*>(sm + C::OFF_ML);
-    // steps of both lanes, those of them that O_DONE counts, and joins of dual items so far
-    int st0 = 0, st1 = 0, so0 = 0, so1 = 0, merges = 0;
+    int st0 = 0, st1 = 0, merges = 0;  // steps of both lanes and joins of dual items so far
     for (int i = 0;; ++i) {
       ServeItem it;
       if (!next_item(i, &it) || it.cnt < 0) break;
       const bool dual = it.flags & ITEM_DUAL, whole = it.flags & ITEM_WHOLE;
       const int steps = t ? it.s1 : it.s0, before = t ? st1 : st0;
-      const int before_o = t ? so1 : so0;
-      const int tok = it.tok0 + (dual ? 0 : t * npt) + rn;
+            const int tok = it.tok0 + (dual ? 0 : t * npt) + rn;
       const bool valid = rn < npt && tok < it.n;
       const bool any = __any_sync(0xffffffffu, valid);
       float m_run = -INFINITY, l_run = 0.f;
       bool ok = true;
       const int tok_first = __shfl_sync(0xffffffffu, tok, 0);  // the warp's tokens ascend with its rows
-      const int last = steps - 1;
-      const int od = before_o - (C::SEP_P ? 0 : steps - min(steps, 2));  // O_DONE phase of step 0, were it counted
+      auto wait_pv = [&](int lane_t, int g) {  // PV of that lane's step g has landed in O
+        return wait_warp_fast(BAR(C::O_DONE + 2 * lane_t + C::buf(g)), C::phase(g), st, SITE_SW_O_DONE);
+      };
       const int stride = dual ? 2 : 1;
       int js = it.j0 + (dual ? t : 0), hs = 0, halves = steps_in(it, t, js);  // the step's key tile and half
       for (int s = 0; s < steps; ++s, ++hs) {
@@ -645,10 +619,8 @@ __global__ void __launch_bounds__(352, 1)
             if (lane == 0) mbar_arrive(BAR(C::S_FREE + t));
           }
           // d = 64: S of this tile may be there before the other warps have written P of the one
-          // before: an arrival now would count for that one. d = 128: see below
-          if (s > 0 && (C::SEP_P || s == last) &&
-              !(ok = wait_warp_fast(BAR(C::O_DONE + t), (od + s - 1) & 1, st, SITE_SW_O_DONE)))
-            break;
+          // before: an arrival now would count for that one
+          if (C::SEP_P && s > 0 && !(ok = wait_pv(t, before + s - 1))) break;
           if (lane == 0) mbar_arrive(BAR(C::P_READY + 2 * t + u));
           continue;
         }
@@ -733,7 +705,7 @@ __global__ void __launch_bounds__(352, 1)
           }
           if (C::SEP_P && q == 1) {
             if (s > 0) {  // PV of the tile before has read P (across items its epilogue waited for that)
-              if (!(ok = wait_warp_fast(BAR(C::O_DONE + t), (od + s - 1) & 1, st, SITE_SW_O_DONE))) break;
+              if (!(ok = wait_pv(t, before + s - 1))) break;
               tc_fence_after();
             }
             tmem_st16(tP, pk[0]);
@@ -746,17 +718,11 @@ __global__ void __launch_bounds__(352, 1)
         f2_unpack(ps2[0], ps[0], ps[1]);
         f2_unpack(ps2[1], ps[2], ps[3]);
         l_run = l_run * f + ((ps[0] + ps[1]) + (ps[2] + ps[3]));
-        // d = 128: S of this step was formed behind PV of the last step but one. PV of the last step is
-        // waited for before O is rescaled (S of the next step was formed behind it), and before the
-        // last P is published: the wait for the last PV below would else take its phase for its own.
-        if (!C::SEP_P && s > 0 && (rescale_warp || s == last)) {
-          const int v = C::buf(before + s + 1);
-          ok = s == last ? wait_warp_fast(BAR(C::O_DONE + t), (od + s - 1) & 1, st, SITE_SW_O_DONE)
-                         : wait_warp_fast(BAR(C::S_FULL + 2 * t + v), C::phase(before + s + 1), st, SITE_SW_S_FULL);
-          if (!ok) break;
-          tc_fence_after();
-        }
         if (rescale_warp) {
+          if (!C::SEP_P) {
+            if (!(ok = wait_pv(t, before + s - 1))) break;
+            tc_fence_after();
+          }
           const uint32_t tO = tmem + lane_off + C::tm_o(t);
           uint32_t r[32];
 #pragma unroll
@@ -773,7 +739,7 @@ __global__ void __launch_bounds__(352, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(BAR(C::P_READY + 2 * t + u));
       }
-      if (ok && steps > 0) ok = wait_warp_fast(BAR(C::O_DONE + t), (od + last) & 1, st, SITE_SW_O_DONE);
+      if (ok && steps > 0) ok = wait_pv(t, before + steps - 1);
       if (!ok) break;
       tc_fence_after();
       const bool join = dual && it.c1 > 0;
@@ -786,7 +752,7 @@ __global__ void __launch_bounds__(352, 1)
           if (lane == 0) mbar_arrive(BAR(C::MERGE));
         } else {
           if (!wait_warp_sleep(BAR(C::MERGE), merges & 1, st, SITE_SW_MERGE) ||
-              !wait_warp_sleep(BAR(C::O_DONE + 1), (so1 + (C::SEP_P ? it.s1 : min(it.s1, 2)) - 1) & 1, st, SITE_SW_O_DONE))
+              !wait_pv(1, st1 + it.s1 - 1))
             break;
           tc_fence_after();
           const float m1 = ml[row], m = fmaxf(m_run, m1), base = m == -INFINITY ? 0.f : m;
@@ -799,8 +765,6 @@ __global__ void __launch_bounds__(352, 1)
       }
       st0 += it.s0;
       st1 += it.s1;
-      so0 += C::SEP_P ? it.s0 : min(it.s0, 2);
-      so1 += C::SEP_P ? it.s1 : min(it.s1, 2);
       if (dual && t == 1) continue;  // lane 0 writes the results
       // l = 0: no key; NaN stays NaN
       const float inv = l_run != 0.f ? 1.f / l_run : 0.f;
