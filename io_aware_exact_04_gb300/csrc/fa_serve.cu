@@ -116,13 +116,14 @@ struct ServeItem {
 };
 enum { ITEM_DUAL = 1, ITEM_WHOLE = 2 };
 
-// Sizes of sequence b's work; record: whether invalid device values are recorded.
+// Sizes of sequence b's work, in items of `unit` tokens; record: whether invalid device values are
+// recorded.
 struct SeqWork {
-  int row0, n, L, nc, nk, pairs;
-  long long tiles;  // all heads and pairs, each counted with the nk tiles of the last one
+  int row0, n, L, nc, nk, units;
+  long long tiles;  // all heads and units, each counted with the nk tiles of the last one
 };
 template <bool PAGED>
-__device__ __forceinline__ SeqWork seq_work(const ServeArgs& a, int b, int npt, bool record) {
+__device__ __forceinline__ SeqWork seq_work(const ServeArgs& a, int b, int unit, bool record) {
   SeqWork w;
   const int lo = a.cu[b], hi = a.cu[b + 1];
   w.row0 = min(max(lo, 0), a.T);
@@ -137,8 +138,8 @@ __device__ __forceinline__ SeqWork seq_work(const ServeArgs& a, int b, int npt, 
   }
   w.nc = (w.L + 127) >> 7;
   w.nk = w.nc + ((w.n + 127) >> 7);
-  w.pairs = (w.n + 2 * npt - 1) / (2 * npt);
-  w.tiles = (long long)w.pairs * a.Hkv * w.nk;
+  w.units = (w.n + unit - 1) / unit;
+  w.tiles = (long long)w.units * a.Hkv * w.nk;
   return w;
 }
 
@@ -153,20 +154,20 @@ struct ServeRuns {
   int ctas;  // CTAs with work
   __device__ long long start(int c) const { return total * c / ctas; }
 };
-__device__ __forceinline__ ServeRuns serve_runs(const ServeArgs& a, int npt, int grid, bool record) {
+__device__ __forceinline__ ServeRuns serve_runs(const ServeArgs& a, int unit, int grid, bool record) {
   ServeRuns r;
   long long x = 0;
-  for (int b = threadIdx.x & 31; b < a.B; b += 32) x += seq_work<true>(a, b, npt, record).tiles;
+  for (int b = threadIdx.x & 31; b < a.B; b += 32) x += seq_work<true>(a, b, unit, record).tiles;
   r.total = warp_sum(x);
   r.ctas = (int)min((long long)grid, max(1LL, (r.total + kMinTiles - 1) / kMinTiles));
   return r;
 }
 // The sequence that tile `pos` of all belongs to, and its first tile; by a whole warp. pos < total.
-__device__ __forceinline__ int serve_seek(const ServeArgs& a, int npt, long long pos, long long* first) {
+__device__ __forceinline__ int serve_seek(const ServeArgs& a, int unit, long long pos, long long* first) {
   const int lane = threadIdx.x & 31;
   long long base = 0;
   for (int b0 = 0; b0 < a.B; b0 += 32) {
-    const long long mine = b0 + lane < a.B ? seq_work<true>(a, b0 + lane, npt, false).tiles : 0;
+    const long long mine = b0 + lane < a.B ? seq_work<true>(a, b0 + lane, unit, false).tiles : 0;
     long long incl = mine;
     for (int o = 1; o < 32; o <<= 1) {
       const long long y = __shfl_up_sync(0xffffffffu, incl, o);
@@ -190,25 +191,41 @@ __device__ __forceinline__ int tiles_of(const SeqWork& w, int u, int npt, bool t
   return w.nc + ((min(tree ? w.n : (u + 1) * npt, w.n) + 127) >> 7);
 }
 
-// Prompts: item i of all, longest pairs first: level p holds the p-th pairs of all sequences that
-// have one, in the order of the sequences; by a whole warp. False past the last one.
-__device__ __forceinline__ bool prompt_item(const ServeArgs& a, int npt, long long i, int* b, int* pair) {
+// Prompts: the tokens of an item, by a whole warp. Two query tiles share the keys that an item loads;
+// but with few items the longest one alone may outlast the even share of all key tiles, and items
+// of one tile, whose keys both lanes divide, take half as long (prompt_batch: 37 -> 21 us; long
+// prompts, where the share is longer than any item, lose a tenth by it).
+__device__ __forceinline__ int prompt_unit(const ServeArgs& a, int npt, int grid, bool record) {
+  long long tiles = 0;
+  int longest = 0;
+  for (int b = threadIdx.x & 31; b < a.B; b += 32) {
+    const SeqWork w = seq_work<false>(a, b, 2 * npt, record);
+    tiles += (w.tiles + (long long)w.units * a.Hkv) / 2;  // item p of a sequence has about (p + 1) nk / units
+    longest = max(longest, w.nk);
+  }
+  tiles = warp_sum(tiles);
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  return tiles < (long long)longest * grid ? npt : 2 * npt;
+}
+// Item i of all, longest first: level p holds the p-th items of all sequences that have one, in
+// the order of the sequences; by a whole warp. False past the last one.
+__device__ __forceinline__ bool prompt_item(const ServeArgs& a, int unit, long long i, int* b, int* p) {
   const int lane = threadIdx.x & 31;
-  auto above = [&](int p) {  // pairs of level p and up
+  auto above = [&](int level) {  // items of that level and up
     long long x = 0;
-    for (int s = lane; s < a.B; s += 32) x += max(0, seq_work<false>(a, s, npt, false).pairs - p);
+    for (int s = lane; s < a.B; s += 32) x += max(0, seq_work<false>(a, s, unit, false).units - level);
     return warp_sum(x);
   };
   if (i >= above(0)) return false;
-  int lo = 0, hi = (a.T + 2 * npt - 1) / (2 * npt);  // above(lo) > i >= above(hi)
+  int lo = 0, hi = (a.T + unit - 1) / unit;  // above(lo) > i >= above(hi)
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (above(mid) > i) lo = mid; else hi = mid;
   }
   int left = (int)(i - above(lo + 1));
-  *pair = lo;
+  *p = lo;
   for (int b0 = 0; b0 < a.B; b0 += 32) {
-    const bool has = b0 + lane < a.B && seq_work<false>(a, b0 + lane, npt, false).pairs > lo;
+    const bool has = b0 + lane < a.B && seq_work<false>(a, b0 + lane, unit, false).units > lo;
     unsigned m = __ballot_sync(0xffffffffu, has);
     const int k = __popc(m);
     if (left < k) {
@@ -386,8 +403,9 @@ __global__ void __launch_bounds__(384, 1)
       }
       return true;
     };
-    auto make_item = [&](const SeqWork& w, int kvh, int pair, int j0, int j1, ServeItem* it) {
-      const int n0 = tiles_of(w, 2 * pair, npt, a.mask != nullptr), n1 = tiles_of(w, 2 * pair + 1, npt, a.mask != nullptr);
+    auto make_item = [&](const SeqWork& w, int unit, int kvh, int p, int j0, int j1, ServeItem* it) {
+      const int u = unit == npt ? p : 2 * p;  // first query tile
+      const int n0 = tiles_of(w, u, npt, tree), n1 = unit == npt ? 0 : tiles_of(w, u + 1, npt, tree);
       const int nmax = max(n0, n1);
       const bool dual = n1 == 0;
       j1 = min(j1, nmax);
@@ -395,7 +413,7 @@ __global__ void __launch_bounds__(384, 1)
       it->flags = (dual ? ITEM_DUAL : 0) | (j0 == 0 && j1 == nmax ? ITEM_WHOLE : 0);
       it->c0 = dual ? (it->cnt + 1) >> 1 : max(0, min(j1, n0) - j0);
       it->c1 = dual ? it->cnt >> 1 : it->cnt;
-      it->j0 = j0, it->nc = w.nc, it->L = w.L, it->n = w.n, it->row0 = w.row0, it->tok0 = 2 * pair * npt, it->kvh = kvh;
+      it->j0 = j0, it->nc = w.nc, it->L = w.L, it->n = w.n, it->row0 = w.row0, it->tok0 = p * unit, it->kvh = kvh;
       it->slot = 2 * blockIdx.x + (j0 == 0);
       it->s0 = it->c0 * C::HPT, it->s1 = it->c1 * C::HPT;
       if (C::HPT > 1) {  // only the last cached tile and a lane's last tile may have a half less
@@ -411,17 +429,18 @@ __global__ void __launch_bounds__(384, 1)
     };
     ServeItem it;
     if (PAGED) {
-      const ServeRuns runs = serve_runs(a, npt, gridDim.x, blockIdx.x == 0);
+      const int unit = 2 * npt;
+      const ServeRuns runs = serve_runs(a, unit, gridDim.x, blockIdx.x == 0);
       if ((int)blockIdx.x < runs.ctas && runs.total > 0) {
         long long pos = runs.start(blockIdx.x), first = 0;
         const long long end = runs.start(blockIdx.x + 1);
-        int b = serve_seek(a, npt, pos, &first);
+        int b = serve_seek(a, unit, pos, &first);
         while (ok && pos < end) {
-          const SeqWork w = seq_work<PAGED>(a, b, npt, false);
+          const SeqWork w = seq_work<PAGED>(a, b, unit, false);
           while (ok && pos < end && pos - first < w.tiles) {
             const int q = (int)((pos - first) / w.nk), j0 = (int)((pos - first) % w.nk);
             const int j1 = (int)min((long long)w.nk, j0 + (end - pos));
-            make_item(w, q % a.Hkv, q / a.Hkv, j0, j1, &it);
+            make_item(w, unit, q % a.Hkv, q / a.Hkv, j0, j1, &it);
             if (it.cnt > 0) ok = run_item(it, b);
             pos += j1 - j0;
           }
@@ -430,15 +449,14 @@ __global__ void __launch_bounds__(384, 1)
         }
       }
     } else {
-      if (blockIdx.x == 0)
-        for (int b = lane; b < a.B; b += 32) seq_work<PAGED>(a, b, npt, true);
+      const int unit = prompt_unit(a, npt, gridDim.x, blockIdx.x == 0);
       for (long long round = 0; ok; ++round) {
         const int G = gridDim.x, c = blockIdx.x;
         const long long i = round * G + ((round & 1) ? G - 1 - c : c);
-        int b = 0, pair = 0;
-        if (!prompt_item(a, npt, i / a.Hkv, &b, &pair)) break;  // later rounds lie past the end too
-        const SeqWork w = seq_work<PAGED>(a, b, npt, false);
-        make_item(w, (int)(i % a.Hkv), pair, 0, w.nk, &it);
+        int b = 0, p = 0;
+        if (!prompt_item(a, unit, i / a.Hkv, &b, &p)) break;  // later rounds lie past the end too
+        const SeqWork w = seq_work<PAGED>(a, b, unit, false);
+        make_item(w, unit, (int)(i % a.Hkv), p, 0, w.nk, &it);
         ok = run_item(it, b);
       }
     }
@@ -843,14 +861,14 @@ __global__ void __launch_bounds__(256) serve_join_kernel(ServeArgs a, int grid) 
   const int npt = 128 / a.G, c = blockIdx.x + 1;
   if (threadIdx.x < 32) {
     int parts = 0;
-    const ServeRuns runs = serve_runs(a, npt, grid, false);
+    const ServeRuns runs = serve_runs(a, 2 * npt, grid, false);
     SeqWork w = {};
     int q = 0;
     if (c < runs.ctas && runs.total > 0) {
       const long long pos = runs.start(c);
       long long first;
-      const int b = serve_seek(a, npt, pos, &first);
-      w = seq_work<true>(a, b, npt, false);
+      const int b = serve_seek(a, 2 * npt, pos, &first);
+      w = seq_work<true>(a, b, 2 * npt, false);
       q = (int)((pos - first) / w.nk);
       const long long item = first + (long long)q * w.nk;
       const int pair = q / a.Hkv;
@@ -926,9 +944,9 @@ static int launch_serve_d(ServeArgs a, cudaStream_t stream) {
   int sms = 0;
   if (!sm_count(&sms)) return FA_ERR_CUDA;
   int grid = sms;
-  if (!PAGED) {  // no more CTAs than items could exist
-    const long long pairs = ((long long)a.T * a.G + 255) / 256 + a.B;  // G rows a token; a pair has at least 129 of them
-    grid = (int)std::min<long long>(sms, std::max<long long>(1, 2 * pairs * a.Hkv));
+  if (!PAGED) {  // no more CTAs than there may be items of one query tile
+    const int npt = 128 / a.G;
+    grid = (int)std::min<long long>(sms, ((a.T + npt - 1) / npt + (long long)a.B) * a.Hkv);
   }
   int rc = launch_pdl("serve_kernel", kernel, dim3(grid), dim3(C::THREADS), C::SMEM_BYTES, stream, mq, mk, mv, mkc, mvc, a);
   if (rc != FA_OK || !PAGED || grid < 2) return rc;
