@@ -207,36 +207,56 @@ __device__ __forceinline__ int prompt_unit(const ServeArgs& a, int npt, int grid
   longest = __reduce_max_sync(0xffffffffu, longest);
   return tiles < (long long)longest * grid ? npt : 2 * npt;
 }
-// Item i of all, longest first: level p holds the p-th items of all sequences that have one, in
-// the order of the sequences; by a whole warp. False past the last one.
-__device__ __forceinline__ bool prompt_item(const ServeArgs& a, int unit, long long i, int* b, int* p) {
-  const int lane = threadIdx.x & 31;
-  auto above = [&](int level) {  // items of that level and up
-    long long x = 0;
-    for (int s = lane; s < a.B; s += 32) x += max(0, seq_work<false>(a, s, unit, false).units - level);
-    return warp_sum(x);
-  };
-  if (i >= above(0)) return false;
-  int lo = 0, hi = (a.T + unit - 1) / unit;  // above(lo) > i >= above(hi)
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (above(mid) > i) lo = mid; else hi = mid;
+// The items of all prompts, longest first: level p holds the p-th items of all sequences that have
+// one, in the order of the sequences. Used by a whole warp; the item counts of the first 128
+// sequences stay in registers (read again for every item, they made the search longer than an
+// ordinary item's work).
+struct PromptItems {
+  static constexpr int KEPT = 4;
+  const ServeArgs& a;
+  int unit, total, mine[KEPT];
+  __device__ PromptItems(const ServeArgs& args, int u) : a(args), unit(u) {
+#pragma unroll
+    for (int k = 0; k < KEPT; ++k) mine[k] = units(32 * k);
+    total = above(0);
   }
-  int left = (int)(i - above(lo + 1));
-  *p = lo;
-  for (int b0 = 0; b0 < a.B; b0 += 32) {
-    const bool has = b0 + lane < a.B && seq_work<false>(a, b0 + lane, unit, false).units > lo;
-    unsigned m = __ballot_sync(0xffffffffu, has);
-    const int k = __popc(m);
-    if (left < k) {
-      for (; left; --left) m &= m - 1;
-      *b = b0 + __ffs(m) - 1;
-      return true;
+  __device__ int units(int b0) const {
+    const int b = b0 + (threadIdx.x & 31);
+    return b < a.B ? seq_work<false>(a, b, unit, false).units : 0;
+  }
+  __device__ int above(int level) const {  // items of that level and up
+    int x = 0;
+#pragma unroll
+    for (int k = 0; k < KEPT; ++k) x += max(0, mine[k] - level);
+    for (int b0 = 32 * KEPT; b0 < a.B; b0 += 32) x += max(0, units(b0) - level);
+    return __reduce_add_sync(0xffffffffu, x);
+  }
+  // Sequence and level of item i < total.
+  __device__ void find(int i, int* b, int* level) const {
+    int lo = 0, hi = (a.T + unit - 1) / unit;  // above(lo) > i >= above(hi)
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (above(mid) > i) lo = mid; else hi = mid;
     }
-    left -= k;
+    int left = i - above(lo + 1);
+    *level = lo;
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+      int u = 0;
+#pragma unroll
+      for (int k = 0; k < KEPT; ++k)
+        if (b0 == 32 * k) u = mine[k];
+      if (b0 >= 32 * KEPT) u = units(b0);
+      unsigned m = __ballot_sync(0xffffffffu, u > lo);
+      const int k = __popc(m);
+      if (left < k) {
+        for (; left; --left) m &= m - 1;
+        *b = b0 + __ffs(m) - 1;
+        return;
+      }
+      left -= k;
+    }
   }
-  return false;
-}
+};
 
 template <bool F16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -450,11 +470,13 @@ __global__ void __launch_bounds__(384, 1)
       }
     } else {
       const int unit = prompt_unit(a, npt, gridDim.x, blockIdx.x == 0);
+      const PromptItems items_of(a, unit);
       for (long long round = 0; ok; ++round) {
         const int G = gridDim.x, c = blockIdx.x;
         const long long i = round * G + ((round & 1) ? G - 1 - c : c);
         int b = 0, p = 0;
-        if (!prompt_item(a, unit, i / a.Hkv, &b, &p)) break;  // later rounds lie past the end too
+        if (i >= (long long)items_of.total * a.Hkv) break;  // later rounds lie past the end too
+        items_of.find((int)(i / a.Hkv), &b, &p);
         const SeqWork w = seq_work<PAGED>(a, b, unit, false);
         make_item(w, unit, (int)(i % a.Hkv), p, 0, w.nk, &it);
         ok = run_item(it, b);
