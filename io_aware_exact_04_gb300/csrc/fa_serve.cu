@@ -93,7 +93,7 @@ struct ServeCfg {
                        MERGE = O_FREE + 2, DRAIN = MERGE + 1, D_FULL = DRAIN + 1, D_EMPTY = D_FULL + 4,
                        BARS = D_EMPTY + 4;
 };
-static_assert(8 * ServeCfg<64>::BARS + 8 <= 512 && 8 * ServeCfg<128>::BARS + 8 <= 512, "barrier area");
+static_assert(8 * ServeCfg<64>::BARS + 12 <= 512 && 8 * ServeCfg<128>::BARS + 12 <= 512, "barrier area");
 static_assert(ServeCfg<64>::SMEM_BYTES <= 232448 && ServeCfg<128>::SMEM_BYTES <= 232448, "shared memory above 227 KB");
 
 enum { SITE_SW_EMPTY = 60, SITE_SW_Q_FULL, SITE_SW_Q_EMPTY, SITE_SW_K_FULL, SITE_SW_V_FULL, SITE_SW_S_FREE,
@@ -277,6 +277,7 @@ __global__ void __launch_bounds__(384, 1)
   auto BAR = [&](int i) { return b0 + 8u * i; };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::OFF_BAR + 8 * C::BARS);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
+  volatile int* loading = reinterpret_cast<int*>(tmem_slot + 2);  // ring entries whose loads have begun
   DevStatus st{a.status, abort_flag};
   int* descs = reinterpret_cast<int*>(sm + C::OFF_DESC);
   const int npt = 128 / a.G;  // tokens of a query tile
@@ -304,6 +305,7 @@ __global__ void __launch_bounds__(384, 1)
       mbar_init(BAR(C::D_EMPTY + i), 11);  // softmax warps and issuers
     }
     *abort_flag = 0;
+    *loading = 0;
     fence_mbar_init();
     prefetch_tmap(&tm_q);
     prefetch_tmap(&tm_k);
@@ -406,7 +408,10 @@ __global__ void __launch_bounds__(384, 1)
           const int s = e % C::NSLOT;
           const uint32_t bar = BAR(C::FULL + s);
           if (!wait_warp(BAR(C::EMPTY + s), ((e / C::NSLOT) & 1) ^ 1, st, SITE_SW_EMPTY)) return false;
-          if (elect_one()) mbar_arrive_expect_tx(bar, (uint32_t)(boxes * box * 128 * C::NSUB));
+          if (elect_one()) {
+            *loading = e + 1;
+            mbar_arrive_expect_tx(bar, (uint32_t)(boxes * box * 128 * C::NSUB));
+          }
           __syncwarp();
           if (kWithhold && (e >> 1) == 1) continue;  // test build: this copy never arrives
           const uint32_t dst = sbase + C::OFF_R + s * C::TILE_BYTES + c * C::SUB_BYTES + r * box * 128;
@@ -508,20 +513,48 @@ __global__ void __launch_bounds__(384, 1)
       if (elect_one()) mma_commit(bar);
       __syncwarp();
     };
-    // A place in the ring of K and V tiles.
+    // A place in the ring of K and V tiles. A barrier's parity tells two uses of a slot apart, not
+    // three: a warp that releases only K or only V, which take turns in a slot at d = 128, may wait for
+    // a use only when the slot's use before it has landed. Within an item that follows from the steps
+    // before (the use before lies two or three tiles back, and this warp has waited for a product
+    // that reads it); for an item's first tiles, and for those of which its lane computes nothing,
+    // `landed` looks whether the load has begun, which it does once that use is over.
     struct Place {
-      int slot;
+      int entry, slot;
       uint32_t parity;
       __device__ void skip(int entries) {  // fewer than NSLOT
+        entry += entries;
         slot += entries;
         if (slot >= C::NSLOT) slot -= C::NSLOT, parity ^= 1;
       }
+    };
+    int begun = 0;  // of `loading`, when last looked at
+    auto landed = [&](const Place& p, bool steady, int site) {
+      if (!steady && begun <= p.entry) {
+        const uint64_t t0 = globaltimer_ns();
+        for (uint32_t spins = 1;; ++spins) {
+          begun = *loading;
+          if (__all_sync(0xffffffffu, begun > p.entry)) break;
+          bool give_up = false;
+          if ((spins & 63u) == 0) {
+            if (*(volatile int*)abort_flag || *(volatile int*)st.word != 0) {
+              *(volatile int*)abort_flag = 1;
+              give_up = true;
+            } else if (globaltimer_ns() - t0 > kWaitLimitNs) {
+              record_error(st, FA_ERR_TIMEOUT, site);
+              give_up = true;
+            }
+          }
+          if (__any_sync(0xffffffffu, give_up)) return false;
+        }
+      }
+      return wait_warp_fast(BAR(C::FULL + p.slot), p.parity, st, site);
     };
     bool ok = true;
     if (warp == 11) {
       // S = Q K^T of both lanes, tile after tile in the order of the ring
       const uint32_t q_lo = sdesc_lo(sbase + C::OFF_Q, 16), k_lo = sdesc_lo(sbase + C::OFF_R, 16);
-      Place ks = {0, 0};
+      Place ks = {0, 0, 0};
       int uq = 0, g0 = 0, g1 = 0;  // Q slots and steps of both lanes so far
       for (int i = 0; ok; ++i) {
         ServeItem it;
@@ -549,7 +582,7 @@ __global__ void __launch_bounds__(384, 1)
           return true;
         };
         for (int k = 0; ok && k < it.cnt; ++k) {
-          if (!(ok = wait_warp_fast(BAR(C::FULL + ks.slot), ks.parity, st, SITE_SW_K_FULL))) break;
+          if (!(ok = landed(ks, k >= 4, SITE_SW_K_FULL))) break;
           const int j = it.j0 + k;
           const int h0 = (dual ? (k & 1) : k >= it.c0) ? 0 : steps_in(it, 0, j);
           const int h1 = (dual ? !(k & 1) : k >= it.c1) ? 0 : steps_in(it, 1, j);
@@ -569,7 +602,7 @@ __global__ void __launch_bounds__(384, 1)
       // O += P V of lane t
       const int t = warp - 9;
       const uint32_t v_lo = sdesc_lo(sbase + C::OFF_R, C::SUB_BYTES);
-      Place vs = {1, 0};
+      Place vs = {1, 1, 0};
       int used = 0, g = 0;  // this lane's items and steps so far
       for (int i = 0; ok; ++i) {
         ServeItem it;
@@ -578,7 +611,7 @@ __global__ void __launch_bounds__(384, 1)
         const int tiles = t ? it.c1 : it.c0;
         bool first = true;
         for (int k = 0; ok && k < it.cnt; ++k) {
-          if (!(ok = wait_warp_fast(BAR(C::FULL + vs.slot), vs.parity, st, SITE_SW_V_FULL))) break;
+          if (!(ok = landed(vs, k >= 4 && (dual || k < tiles), SITE_SW_V_FULL))) break;
           if (dual ? (k & 1) != t : k >= tiles) {  // the other lane's
             if (elect_one()) mbar_arrive(BAR(C::EMPTY + vs.slot));
             __syncwarp();
