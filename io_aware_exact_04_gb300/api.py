@@ -214,7 +214,7 @@ _FP32, _INT32, _UINT8 = torch.float32, torch.int32, torch.uint8
 
 def _call(name: str, index: int, *args) -> None:
     """One entry point on device `index` and its current stream."""
-    fn = getattr(_lib.load("libfa.so"), name)
+    fn = getattr(_lib_fa(), name)
     if torch.cuda.current_device() == index:
         rc = fn(*args, _raw_stream(index))
     else:

@@ -160,17 +160,6 @@ __device__ __forceinline__ bool wait_warp_sleep(uint32_t bar, uint32_t parity, D
   return __all_sync(0xffffffffu, ok);
 }
 
-// The same with the waiting part out of line: a warp that mostly finds its phase complete (an MMA
-// issuer's) then runs through less code. Every softmax warp shares its instruction caches, and the
-// issuer's own time per step bounds the forward of the serving kernels.
-__device__ __noinline__ inline bool wait_warp_slow(uint32_t bar, uint32_t parity, DevStatus st, int site) {
-  return wait_warp_sleep(bar, parity, st, site);
-}
-__device__ __forceinline__ bool wait_warp_fast(uint32_t bar, uint32_t parity, DevStatus st, int site) {
-  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-  return wait_warp_slow(bar, parity, st, site);
-}
-
 // Byte offset of 16-byte chunk `chunk` (0..7) of row `row` inside a tile whose
 // rows are 128 bytes and which TMA fills with 128-byte swizzling (1024-byte atoms).
 __device__ __forceinline__ uint32_t sw128_offset(uint32_t row, uint32_t chunk) {

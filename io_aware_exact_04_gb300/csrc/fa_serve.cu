@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(384, 1)
 
   // Item i of this CTA, for a consumer warp: false when the CTA must give up.
   auto next_item = [&](int i, ServeItem* it) {
-    if (!wait_warp_sleep(BAR(C::D_FULL + (i & 3)), (i >> 2) & 1, st, SITE_SW_DESC_FULL)) return false;
+    if (!wait_phase(BAR(C::D_FULL + (i & 3)), (i >> 2) & 1, st, SITE_SW_DESC_FULL)) return false;
     const int4* d = reinterpret_cast<const int4*>(descs + 16 * (i & 3));
     const int4 x = d[0], y = d[1], z = d[2], w = d[3];
     it->cnt = x.x, it->flags = x.y, it->c0 = x.z, it->c1 = x.w;
@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(384, 1)
     int items = 0, uq = 0, e = 0;  // items published, Q slots and ring entries used
     bool ok = true;
     auto publish = [&](const ServeItem& it) {
-      if (!wait_warp(BAR(C::D_EMPTY + (items & 3)), ((items >> 2) & 1) ^ 1, st, SITE_SW_DESC_EMPTY)) return false;
+      if (!wait_phase(BAR(C::D_EMPTY + (items & 3)), ((items >> 2) & 1) ^ 1, st, SITE_SW_DESC_EMPTY)) return false;
       if (lane == 0) {
         int4* d = reinterpret_cast<int4*>(descs + 16 * (items & 3));
         d[0] = make_int4(it.cnt, it.flags, it.c0, it.c1);
@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(384, 1)
       const int nq = (it.flags & ITEM_DUAL) ? 1 : 2;
       for (int t = 0; t < nq; ++t, ++uq) {
         const uint32_t qf = BAR(C::Q_FULL + (uq & 1));
-        if (!wait_warp(BAR(C::Q_EMPTY + (uq & 1)), ((uq >> 1) & 1) ^ 1, st, SITE_SW_Q_EMPTY)) return false;
+        if (!wait_phase(BAR(C::Q_EMPTY + (uq & 1)), ((uq >> 1) & 1) ^ 1, st, SITE_SW_Q_EMPTY)) return false;
         if (elect_one()) mbar_arrive_expect_tx(qf, (uint32_t)(npt * a.G * 128 * C::NSUB));
         __syncwarp();
         const uint32_t dst = sbase + C::OFF_Q + (uq & 1) * C::TILE_BYTES;
@@ -407,7 +407,7 @@ __global__ void __launch_bounds__(384, 1)
         for (int kv = 0; kv < 2; ++kv, ++e) {
           const int s = e % C::NSLOT;
           const uint32_t bar = BAR(C::FULL + s);
-          if (!wait_warp(BAR(C::EMPTY + s), ((e / C::NSLOT) & 1) ^ 1, st, SITE_SW_EMPTY)) return false;
+          if (!wait_phase(BAR(C::EMPTY + s), ((e / C::NSLOT) & 1) ^ 1, st, SITE_SW_EMPTY)) return false;
           if (elect_one()) {
             *loading = e + 1;
             mbar_arrive_expect_tx(bar, (uint32_t)(boxes * box * 128 * C::NSUB));
@@ -537,7 +537,7 @@ __global__ void __launch_bounds__(384, 1)
           if (__all_sync(0xffffffffu, begun > p.entry)) break;
           bool give_up = false;
           if ((spins & 63u) == 0) {
-            if (*(volatile int*)abort_flag || *(volatile int*)st.word != 0) {
+            if (*(volatile int*)abort_flag || *(volatile int*)st.word == FA_ERR_TIMEOUT) {
               *(volatile int*)abort_flag = 1;
               give_up = true;
             } else if (globaltimer_ns() - t0 > kWaitLimitNs) {
@@ -548,7 +548,7 @@ __global__ void __launch_bounds__(384, 1)
           if (__any_sync(0xffffffffu, give_up)) return false;
         }
       }
-      return wait_warp_fast(BAR(C::FULL + p.slot), p.parity, st, site);
+      return wait_phase(BAR(C::FULL + p.slot), p.parity, st, site);
     };
     bool ok = true;
     if (warp == 11) {
@@ -562,13 +562,13 @@ __global__ void __launch_bounds__(384, 1)
         const bool dual = it.flags & ITEM_DUAL;
         const int nq = dual ? 1 : 2;
         for (int u = uq; ok && u < uq + nq; ++u)
-          ok = wait_warp_fast(BAR(C::Q_FULL + (u & 1)), (u >> 1) & 1, st, SITE_SW_Q_FULL);
+          ok = wait_phase(BAR(C::Q_FULL + (u & 1)), (u >> 1) & 1, st, SITE_SW_Q_FULL);
         const uint32_t qa0 = q_lo + (uq & 1) * TILE16, qa1 = q_lo + ((uq + nq - 1) & 1) * TILE16;
         auto issue_s = [&](int t, int g, uint32_t qa, uint32_t ka) {
           // S(g) goes over S(g - 1), once it is in registers (d = 64), or over P(g - 2), once PV has read it
           if (C::SEP_P ? g > 0 : g > 1) {
-            if (C::SEP_P ? !wait_warp_fast(BAR(C::S_FREE + t), (g - 1) & 1, st, SITE_SW_S_FREE)
-                         : !wait_warp_fast(BAR(C::O_DONE + 2 * t + C::buf(g)), C::phase(g - 2), st, SITE_SW_O_DONE))
+            if (C::SEP_P ? !wait_phase(BAR(C::S_FREE + t), (g - 1) & 1, st, SITE_SW_S_FREE)
+                         : !wait_phase(BAR(C::O_DONE + 2 * t + C::buf(g)), C::phase(g - 2), st, SITE_SW_O_DONE))
               return false;
           }
           tc_fence_after();
@@ -631,8 +631,8 @@ __global__ void __launch_bounds__(384, 1)
             __syncwarp();
           }
           for (int h = 0; h < halves; ++h, ++g, first = false) {
-            if (!(ok = wait_warp_fast(BAR(C::P_READY + 2 * t + C::buf(g)), C::phase(g), st, SITE_SW_P_READY))) break;
-            if (first && used > 0 && !(ok = wait_warp_fast(BAR(C::O_FREE + t), (used - 1) & 1, st, SITE_SW_O_FREE))) break;
+            if (!(ok = wait_phase(BAR(C::P_READY + 2 * t + C::buf(g)), C::phase(g), st, SITE_SW_P_READY))) break;
+            if (first && used > 0 && !(ok = wait_phase(BAR(C::O_FREE + t), (used - 1) & 1, st, SITE_SW_O_FREE))) break;
             tc_fence_after();
             const uint32_t va = v_lo + vs.slot * TILE16 + h * HALF16;
             const uint32_t d = tmem + C::tm_o(t), pa = tmem + C::tm_p(t, C::buf(g));
@@ -674,7 +674,7 @@ __global__ void __launch_bounds__(384, 1)
       bool ok = true;
       const int tok_first = __shfl_sync(0xffffffffu, tok, 0);  // the warp's tokens ascend with its rows
       auto wait_pv = [&](int lane_t, int g) {  // PV of that lane's step g has landed in O
-        return wait_warp_fast(BAR(C::O_DONE + 2 * lane_t + C::buf(g)), C::phase(g), st, SITE_SW_O_DONE);
+        return wait_phase(BAR(C::O_DONE + 2 * lane_t + C::buf(g)), C::phase(g), st, SITE_SW_O_DONE);
       };
       const int stride = dual ? 2 : 1;
       int js = it.j0 + (dual ? t : 0), hs = 0, halves = steps_in(it, t, js);  // the step's key tile and half
@@ -685,7 +685,7 @@ __global__ void __launch_bounds__(384, 1)
           halves = steps_in(it, t, js);
         }
         const int u = C::buf(before + s);
-        if (!(ok = wait_warp_fast(BAR(C::S_FULL + 2 * t + u), C::phase(before + s), st, SITE_SW_S_FULL))) break;
+        if (!(ok = wait_phase(BAR(C::S_FULL + 2 * t + u), C::phase(before + s), st, SITE_SW_S_FULL))) break;
         if (!any) {  // no row here: P stays what it is, its rows of O are nobody's
           __syncwarp();
           if (C::SEP_P) {
@@ -824,7 +824,7 @@ __global__ void __launch_bounds__(384, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(BAR(C::MERGE));
         } else {
-          if (!wait_warp_sleep(BAR(C::MERGE), merges & 1, st, SITE_SW_MERGE) ||
+          if (!wait_phase(BAR(C::MERGE), merges & 1, st, SITE_SW_MERGE) ||
               !wait_pv(1, st1 + it.s1 - 1))
             break;
           tc_fence_after();

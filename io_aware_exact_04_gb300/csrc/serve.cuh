@@ -9,6 +9,33 @@ namespace fa {
 // Check sites recorded with FA_ERR_DEVICE_CHECK by the serving kernels.
 enum { SITE_S_OFFSETS = 40, SITE_S_LENGTH, SITE_S_PAGE, SITE_S_ROW, SITE_S_PARENT, SITE_S_WORDS, SITE_S_SLOT };
 
+// Bounded waits of the serving kernels, by a whole warp. They give up after kWaitLimitNs, as the
+// other kernels' do, and when another CTA has; not when a check was recorded, as these kernels
+// carry on past the values that they check. The waiting part is out of line: a warp that mostly
+// finds its phase complete then runs through less code, and the issuing warps' own time bounds
+// the steps of these kernels.
+__device__ __noinline__ inline bool wait_slow(uint32_t bar, uint32_t parity, DevStatus st, int site) {
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t spins = 1;; ++spins) {
+    if (__all_sync(0xffffffffu, mbar_try_wait_sleep(bar, parity, 20000u))) return true;
+    if ((spins & 7u) != 0) continue;
+    bool give_up = *(volatile int*)st.abort_smem != 0;
+    if (!give_up && *(volatile int*)st.word == FA_ERR_TIMEOUT) {
+      *(volatile int*)st.abort_smem = 1;
+      give_up = true;
+    }
+    if (!give_up && globaltimer_ns() - t0 > kWaitLimitNs) {
+      record_error(st, FA_ERR_TIMEOUT, site);
+      give_up = true;
+    }
+    if (__any_sync(0xffffffffu, give_up)) return false;
+  }
+}
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, DevStatus st, int site) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return wait_slow(bar, parity, st, site);
+}
+
 // The tokens [lo, hi) of sequence b, cut to [0, T): offsets are the caller's device data.
 struct SeqRange {
   int lo, hi;
