@@ -80,8 +80,11 @@ __global__ void __launch_bounds__(128) cache_append_kernel(AppendArgs a) {
 }
 
 // ---------------------------------------------------------------------------------------------
-// Slots and pages. Workspace, in ints: head [8], uses [n_pages], pages [n_pages] (new pages, or
-// where a page goes), slots [slots] x 4, copies [slots] x 3, moves [n_pages] x 2, the old table.
+// Slots and pages: a plan, made by one cluster of eight CTAs (the counts of all pages have to be
+// complete before the free ones are numbered; a cluster's barrier costs less than another launch:
+// five launches took update_beams 79 us of host time, two take 45), and its execution by the whole
+// GPU. Workspace, in ints: head [64], uses [n_pages], pages [n_pages] (new pages, or where a page
+// goes), slots [slots] x 2, copies [slots] x 3, moves [n_pages] x 2, the table as it was.
 struct PoolArgs {
   uint8_t* data;
   long long plane_bytes;
@@ -93,52 +96,21 @@ struct PoolArgs {
   int* status;
   int *head, *uses, *pages, *slot, *copies, *moves, *old;
 };
-enum { H_ERR = 0, H_NEED, H_FREE, H_COPIES, H_MOVES };
+constexpr int kPlanCtas = 8, kPlanThreads = 1024;
+enum { H_ERR = 0, H_NEED, H_FREE, H_COPIES, H_MOVES, H_COUNT = 8, H_HOLES = 16, H_HIGH = 24 };  // the last three: one a CTA
 constexpr int kWasUsed = 1 << 30;
 
 __device__ __forceinline__ int pages_of(int tokens, int shift) { return (tokens + (1 << shift) - 1) >> shift; }
 
-__global__ void __launch_bounds__(256) pool_clear_kernel(PoolArgs a) {
-  griddep_wait();
-  griddep_launch_dependents();
-  const int i = blockIdx.x * 256 + threadIdx.x;
-  if (i < a.n_pages) a.uses[i] = 0;
-  if (i < 8) a.head[i] = 0;
+// All CTAs of the cluster, and what they wrote to global memory.
+__device__ __forceinline__ void cluster_sync() {
+  __threadfence();
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
 __device__ __forceinline__ void pool_error(const PoolArgs& a, int site) {
   a.head[H_ERR] = 1;
   record_check(a.status, site);
-}
-
-// A block for each slot: which pages were in use, and how often each is kept.
-template <bool UPDATE>
-__global__ void __launch_bounds__(256) pool_mark_kernel(PoolArgs a) {
-  griddep_wait();
-  griddep_launch_dependents();
-  const int s = blockIdx.x, cap = a.width << a.page_shift;
-  const int len = a.lens[s];
-  if (len < 0 || len > cap) return pool_error(a, SITE_S_LENGTH);
-  const int n = pages_of(len, a.page_shift);
-  for (int j = threadIdx.x; j < n; j += 256) {
-    const int id = a.table[(long long)s * a.width + j];
-    a.old[(long long)s * a.width + j] = id;
-    if (id < 0 || id >= a.n_pages) {
-      pool_error(a, SITE_S_PAGE);
-      continue;
-    }
-    atomicOr(&a.uses[id], kWasUsed);
-  }
-  if (!UPDATE) return;
-  const int t = a.src[s], want = a.fresh[s];
-  if (t < 0 || t >= a.slots) return pool_error(a, SITE_S_SLOT);
-  if (want < 0 || want > cap) return pool_error(a, SITE_S_LENGTH);
-  const int keep = min(want, min(max(a.lens[t], 0), cap));
-  const int shared = (keep >> a.page_shift) + (t == s && (keep & ((1 << a.page_shift) - 1)) != 0);
-  for (int j = threadIdx.x; j < shared; j += 256) {
-    const int id = a.table[(long long)t * a.width + j];
-    if (id >= 0 && id < a.n_pages) atomicAdd(&a.uses[id], 1);
-  }
 }
 
 // The sum over the block's threads below this one, and the block's total.
@@ -166,152 +138,248 @@ __device__ __forceinline__ int block_scan(int x, int* total, int* sh) {
   return before;
 }
 
-__global__ void __launch_bounds__(1024) update_plan_kernel(PoolArgs a) {
-  griddep_wait();
-  griddep_launch_dependents();
-  __shared__ int sh[32];
-  const int tid = threadIdx.x;
-  if (a.head[H_ERR]) {
-    if (tid < 2) a.info[tid] = -1;
-    return;
+// Of slot s, by a warp: its pages are marked as used, its table row is kept and, for an update,
+// the pages that it will share are counted.
+template <bool UPDATE>
+__device__ void mark_slot(const PoolArgs& a, int s) {
+  const int lane = threadIdx.x & 31, cap = a.width << a.page_shift;
+  const int len = a.lens[s];
+  if (len < 0 || len > cap) return pool_error(a, SITE_S_LENGTH);
+  const int n = pages_of(len, a.page_shift);
+  for (int j = lane; j < n; j += 32) {
+    const int id = a.table[(long long)s * a.width + j];
+    if (UPDATE) a.old[(long long)s * a.width + j] = id;
+    if (id < 0 || id >= a.n_pages) {
+      pool_error(a, SITE_S_PAGE);
+      continue;
+    }
+    atomicOr(&a.uses[id], kWasUsed);
   }
+  if (!UPDATE) return;
+  const int t = a.src[s], want = a.fresh[s];
+  if (t < 0 || t >= a.slots) return pool_error(a, SITE_S_SLOT);
+  if (want < 0 || want > cap) return pool_error(a, SITE_S_LENGTH);
+  const int keep = min(want, min(max(a.lens[t], 0), cap));
+  const int shared = (keep >> a.page_shift) + (t == s && (keep & ((1 << a.page_shift) - 1)) != 0);
+  for (int j = lane; j < shared; j += 32) {
+    const int id = a.table[(long long)t * a.width + j];
+    if (id >= 0 && id < a.n_pages) atomicAdd(&a.uses[id], 1);
+  }
+}
+
+// How many pages each slot keeps, where its new ones start, and which partly kept pages are copied;
+// by one CTA.
+__device__ void plan_slots(const PoolArgs& a, int* sh) {
   int need = 0, copies = 0, total;
-  for (int s0 = 0; s0 < a.slots; s0 += 1024) {
-    const int s = s0 + tid;
-    int mine = 0, copy = 0, kept = 0, keep = 0, part = 0, page = 0;
+  for (int s0 = 0; s0 < a.slots; s0 += kPlanThreads) {
+    const int s = s0 + threadIdx.x;
+    int mine = 0, copy = 0, kept = 0, part = 0, page = 0;
     if (s < a.slots) {
-      const int t = a.src[s];
-      keep = min(a.fresh[s], a.lens[t]);
+      const int t = a.src[s], keep = min(a.fresh[s], a.lens[t]);
       part = keep & ((1 << a.page_shift) - 1);
       kept = keep >> a.page_shift;
       if (part) {
-        page = a.old[(long long)t * a.width + kept];
-        copy = !(t == s && (a.uses[page] & (kWasUsed - 1)) == 1);
+        page = a.table[(long long)t * a.width + kept];
+        copy = !(t == s && (__ldcg(&a.uses[page]) & (kWasUsed - 1)) == 1);
         kept += !copy;
       }
       mine = pages_of(a.fresh[s], a.page_shift) - kept;
     }
     const int before = block_scan(mine, &total, sh);
     if (s < a.slots) {
-      a.slot[4 * s] = kept;
-      a.slot[4 * s + 1] = need + before;
+      a.slot[2 * s] = kept;
+      a.slot[2 * s + 1] = need + before;
     }
     need += total;  // at most slots x width
     const int at = block_scan(copy, &total, sh);
     if (copy) {
-      a.copies[3 * (copies + at)] = s;
-      a.copies[3 * (copies + at) + 1] = page;
-      a.copies[3 * (copies + at) + 2] = part;
+      int* c = a.copies + 3 * (copies + at);
+      c[0] = s, c[1] = page, c[2] = part;
     }
     copies += total;
   }
-  int free = 0;
-  for (int p0 = 0; p0 < a.n_pages; p0 += 1024) {
-    const int p = p0 + tid;
-    const int is_free = p < a.n_pages && a.uses[p] == 0;
-    const int before = block_scan(is_free, &total, sh);
-    if (is_free) a.pages[free + before] = p;
-    free += total;
-  }
-  if (tid == 0) {
+  if (threadIdx.x == 0) {
     a.info[0] = need;
-    a.info[1] = free;
     a.head[H_NEED] = need;
-    a.head[H_FREE] = free;
     a.head[H_COPIES] = copies;
   }
 }
 
-// Table rows (a block each), then the copies of partly kept pages.
+template <bool UPDATE>
+__global__ void __launch_bounds__(kPlanThreads) pool_plan_kernel(PoolArgs a) {
+  griddep_wait();
+  griddep_launch_dependents();
+  __shared__ int sh[32];
+  const int tid = threadIdx.x, rank = blockIdx.x, warp = tid >> 5;  // the grid is one cluster
+  // this CTA's share of the pages
+  const int chunk = (a.n_pages + kPlanCtas - 1) / kPlanCtas;
+  const int lo = min(a.n_pages, rank * chunk), hi = min(a.n_pages, lo + chunk);
+  for (int p = lo + tid; p < hi; p += kPlanThreads) a.uses[p] = 0;
+  if (rank == 0 && tid < 8) a.head[tid] = 0;
+  cluster_sync();
+  for (int s = rank * 32 + warp; s < a.slots; s += 32 * kPlanCtas) mark_slot<UPDATE>(a, s);
+  cluster_sync();
+  if (__ldcg(&a.head[H_ERR])) {  // (the same for every CTA)
+    if (rank == 0 && tid < 2) a.info[tid] = -1;
+    return;
+  }
+  // pages in use of each share, then what lies before this one
+  int total, n = 0;
+  for (int p0 = lo; p0 < hi; p0 += kPlanThreads) {
+    const int p = p0 + tid;
+    n += __syncthreads_count(p < hi && __ldcg(&a.uses[p]) != 0);
+  }
+  if (tid == 0) a.head[H_COUNT + rank] = n;
+  if (UPDATE && rank == kPlanCtas - 1) plan_slots(a, sh);
+  cluster_sync();
+  int used = 0, used_before = 0;
+  for (int r = 0; r < kPlanCtas; ++r) {
+    const int x = __ldcg(&a.head[H_COUNT + r]);
+    used += x;
+    used_before += r < rank ? x : 0;
+  }
+  if (UPDATE) {  // the free pages, ascending
+    int at = lo - used_before;
+    for (int p0 = lo; p0 < hi; p0 += kPlanThreads) {
+      const int p = p0 + tid;
+      const int is_free = p < hi && __ldcg(&a.uses[p]) == 0;
+      const int before = block_scan(is_free, &total, sh);
+      if (is_free) a.pages[at + before] = p;
+      at += total;
+    }
+    if (rank == 0 && tid == 0) a.info[1] = a.head[H_FREE] = a.n_pages - used;
+    return;
+  }
+  // compaction: pages in use at or past `used` move to free ones below it
+  int holes = 0, high = 0;
+  for (int p0 = lo; p0 < hi; p0 += kPlanThreads) {
+    const int p = p0 + tid;
+    const bool in_use = p < hi && __ldcg(&a.uses[p]) != 0;
+    holes += __syncthreads_count(p < hi && p < used && !in_use);
+    high += __syncthreads_count(p >= used && in_use);
+  }
+  if (tid == 0) a.head[H_HOLES + rank] = holes, a.head[H_HIGH + rank] = high;
+  cluster_sync();
+  int at_hole = 0, at_high = 0, moves = 0;
+  for (int r = 0; r < kPlanCtas; ++r) {
+    const int x = __ldcg(&a.head[H_HOLES + r]), y = __ldcg(&a.head[H_HIGH + r]);
+    at_hole += r < rank ? x : 0;
+    at_high += r < rank ? y : 0;
+    moves += y;
+  }
+  for (int p0 = lo; p0 < hi; p0 += kPlanThreads) {
+    const int p = p0 + tid;
+    const bool in_use = p < hi && __ldcg(&a.uses[p]) != 0;
+    const int hole = p < hi && p < used && !in_use, goes = p >= used && in_use;
+    int before = block_scan(hole, &total, sh);
+    if (hole) a.moves[2 * (at_hole + before) + 1] = p;
+    at_hole += total;
+    before = block_scan(goes, &total, sh);
+    if (goes) a.moves[2 * (at_high + before)] = p;
+    if (p < hi) a.pages[p] = goes ? -1 - (at_high + before) : p;
+    at_high += total;
+  }
+  if (rank == 0 && tid == 0) {
+    a.info[0] = used;
+    a.info[1] = moves;
+    a.head[H_MOVES] = moves;
+  }
+}
+
+// A warp copies up to kCopyChunks x 512 bytes, all loads before the stores: with four blocks of eight
+// warps an SM, 128 KB of loads in flight there.
+constexpr int kCopyChunks = 8, kCopyBytes = kCopyChunks * 512;
+__device__ __forceinline__ void warp_copy(uint8_t* to, const uint8_t* from, int bytes) {
+  const int lane = threadIdx.x & 31, n = bytes / 16;
+  const uint4* f = reinterpret_cast<const uint4*>(from);
+  uint4* t = reinterpret_cast<uint4*>(to);
+  uint4 x[kCopyChunks];
+#pragma unroll
+  for (int c = 0; c < kCopyChunks; ++c)
+    if (c * 32 + lane < n) x[c] = __ldcs(f + c * 32 + lane);
+#pragma unroll
+  for (int c = 0; c < kCopyChunks; ++c)
+    if (c * 32 + lane < n) __stcs(t + c * 32 + lane, x[c]);
+}
+
+// The table rows (a warp each), then the kept rows of the pages that are copied: a warp a plane, head
+// and kCopyBytes.
 __global__ void __launch_bounds__(256) update_apply_kernel(PoolArgs a) {
   griddep_wait();
   griddep_launch_dependents();
   if (a.head[H_ERR] || a.head[H_NEED] > a.head[H_FREE]) return;
-  const int s = blockIdx.x;
-  const int kept = a.slot[4 * s], off = a.slot[4 * s + 1], want = a.fresh[s], n = pages_of(want, a.page_shift);
-  for (int j = threadIdx.x; j < a.width; j += 256)
-    a.table[(long long)s * a.width + j] =
-        j < kept ? a.old[(long long)a.src[s] * a.width + j] : j < n ? a.pages[off + j - kept] : -1;
-  if (threadIdx.x == 0) a.lens[s] = want;
-}
-
-__global__ void __launch_bounds__(256) update_copy_kernel(PoolArgs a) {
-  griddep_wait();
-  griddep_launch_dependents();
-  if (a.head[H_ERR] || a.head[H_NEED] > a.head[H_FREE]) return;
-  const long long units = (long long)a.head[H_COPIES] * a.planes * a.Hkv;
-  const long long head_bytes = (long long)a.row_bytes << a.page_shift;
-  for (long long u = blockIdx.x; u < units; u += gridDim.x) {
-    const int h = (int)(u % a.Hkv), x = (int)(u / a.Hkv % a.planes), c = (int)(u / a.Hkv / a.planes);
-    const int s = a.copies[3 * c], of = a.copies[3 * c + 1], rows = a.copies[3 * c + 2];
-    const int to = a.pages[a.slot[4 * s + 1]];  // the slot's first new page
-    uint8_t* plane = a.data + x * a.plane_bytes;
-    const uint4* from = reinterpret_cast<const uint4*>(plane + ((long long)of * a.Hkv + h) * head_bytes);
-    uint4* dest = reinterpret_cast<uint4*>(plane + ((long long)to * a.Hkv + h) * head_bytes);
-    for (int i = threadIdx.x; i < rows * (a.row_bytes / 16); i += 256) dest[i] = from[i];
+  const int lane = threadIdx.x & 31, warps = gridDim.x * 8;
+  const int warp = blockIdx.x * 8 + (threadIdx.x >> 5);
+  for (int s = warp; s < a.slots; s += warps) {
+    const int kept = a.slot[2 * s], off = a.slot[2 * s + 1], want = a.fresh[s], n = pages_of(want, a.page_shift);
+    const int* row = a.old + (long long)a.src[s] * a.width;
+    for (int j = lane; j < a.width; j += 32)
+      a.table[(long long)s * a.width + j] = j < kept ? row[j] : j < n ? a.pages[off + j - kept] : -1;
+    if (lane == 0) a.lens[s] = want;
+  }
+  const int head_bytes = a.row_bytes << a.page_shift;  // one head's rows of a page: at most 64 KB
+  const int parts = (head_bytes + kCopyBytes - 1) / kCopyBytes;
+  const long long units = (long long)a.head[H_COPIES] * a.planes * a.Hkv * parts;
+  for (long long u = warp; u < units; u += warps) {
+    const int part = (int)(u % parts), h = (int)(u / parts % a.Hkv);
+    const long long v = u / parts / a.Hkv;
+    const int x = (int)(v % a.planes), c = (int)(v / a.planes);
+    const int s = a.copies[3 * c], of = a.copies[3 * c + 1], bytes = a.copies[3 * c + 2] * a.row_bytes - part * kCopyBytes;
+    if (bytes <= 0) continue;
+    const int to = a.pages[a.slot[2 * s + 1]];  // the slot's first new page
+    uint8_t* plane = a.data + x * a.plane_bytes + part * kCopyBytes;
+    warp_copy(plane + ((long long)to * a.Hkv + h) * head_bytes, plane + ((long long)of * a.Hkv + h) * head_bytes,
+              min(bytes, kCopyBytes));
   }
 }
 
-__global__ void __launch_bounds__(1024) compact_plan_kernel(PoolArgs a) {
-  griddep_wait();
-  griddep_launch_dependents();
-  __shared__ int sh[32];
-  const int tid = threadIdx.x;
-  if (a.head[H_ERR]) {
-    if (tid < 2) a.info[tid] = -1;
-    return;
-  }
-  int n = 0, total;
-  for (int p0 = 0; p0 < a.n_pages; p0 += 1024) {
-    const int p = p0 + tid;
-    block_scan(p < a.n_pages && a.uses[p] != 0, &total, sh);
-    n += total;
-  }
-  int holes = 0, high = 0;
-  for (int p0 = 0; p0 < a.n_pages; p0 += 1024) {
-    const int p = p0 + tid;
-    const bool used = p < a.n_pages && a.uses[p] != 0;
-    const int hole = p < n && !used, moves = p >= n && used;
-    int at = block_scan(hole, &total, sh);
-    if (hole) a.moves[2 * (holes + at) + 1] = p;
-    holes += total;
-    at = block_scan(moves, &total, sh);
-    if (moves) a.moves[2 * (high + at)] = p;
-    high += total;
-    if (p < a.n_pages) a.pages[p] = moves ? -1 - (high - total + at) : p;
-  }
-  if (tid == 0) {
-    a.info[0] = n;
-    a.info[1] = high;
-    a.head[H_MOVES] = high;
-  }
-}
-
-__global__ void __launch_bounds__(256) compact_table_kernel(PoolArgs a) {
+__global__ void __launch_bounds__(256) compact_apply_kernel(PoolArgs a) {
   griddep_wait();
   griddep_launch_dependents();
   if (a.head[H_ERR]) return;
-  const int s = blockIdx.x, n = pages_of(a.lens[s], a.page_shift);
-  for (int j = threadIdx.x; j < n; j += 256) {
-    int* e = &a.table[(long long)s * a.width + j];
-    const int g = a.pages[*e];
-    if (g < 0) *e = a.moves[2 * (-1 - g) + 1];
+  const int lane = threadIdx.x & 31, warps = gridDim.x * 8;
+  const int warp = blockIdx.x * 8 + (threadIdx.x >> 5);
+  for (int s = warp; s < a.slots; s += warps) {
+    const int n = pages_of(a.lens[s], a.page_shift);
+    for (int j = lane; j < n; j += 32) {
+      int* e = &a.table[(long long)s * a.width + j];
+      const int g = a.pages[*e];
+      if (g < 0) *e = a.moves[2 * (-1 - g) + 1];
+    }
   }
-}
-
-__global__ void __launch_bounds__(256) compact_copy_kernel(PoolArgs a) {
-  griddep_wait();
-  griddep_launch_dependents();
-  if (a.head[H_ERR]) return;
-  const long long units = (long long)a.head[H_MOVES] * a.planes;
   const long long page_bytes = ((long long)a.row_bytes << a.page_shift) * a.Hkv;
-  for (long long u = blockIdx.x; u < units; u += gridDim.x) {
-    const int x = (int)(u % a.planes), m = (int)(u / a.planes);
-    uint8_t* plane = a.data + x * a.plane_bytes;
-    const uint4* from = reinterpret_cast<const uint4*>(plane + a.moves[2 * m] * page_bytes);
-    uint4* dest = reinterpret_cast<uint4*>(plane + a.moves[2 * m + 1] * page_bytes);
-    for (long long i = threadIdx.x; i < page_bytes / 16; i += 256) dest[i] = from[i];
+  const long long parts = (page_bytes + kCopyBytes - 1) / kCopyBytes;
+  const long long units = a.head[H_MOVES] * parts * a.planes;
+  for (long long u = warp; u < units; u += warps) {
+    const long long part = u % parts, v = u / parts;
+    const int x = (int)(v % a.planes), m = (int)(v / a.planes);
+    uint8_t* plane = a.data + x * a.plane_bytes + part * kCopyBytes;
+    warp_copy(plane + a.moves[2 * m + 1] * page_bytes, plane + a.moves[2 * m] * page_bytes,
+              (int)min(page_bytes - part * kCopyBytes, (long long)kCopyBytes));
   }
+}
+
+static int launch_pool(bool update, const PoolArgs& a, cudaStream_t stream) {
+  int sms = 0;
+  if (!sm_count(&sms)) return FA_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kPlanCtas);
+  cfg.blockDim = dim3(kPlanThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kPlanCtas;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  const cudaError_t e = update ? cudaLaunchKernelEx(&cfg, pool_plan_kernel<true>, a) : cudaLaunchKernelEx(&cfg, pool_plan_kernel<false>, a);
+  if (e != cudaSuccess) return cuda_fail("pool_plan_kernel", (int)e, cudaGetErrorName(e));
+  const int rc = check_launch("pool_plan_kernel");
+  if (rc != FA_OK) return rc;
+  return update ? launch_pdl("update_apply_kernel", update_apply_kernel, dim3(4 * sms), dim3(256), 0, stream, a)
+                : launch_pdl("compact_apply_kernel", compact_apply_kernel, dim3(4 * sms), dim3(256), 0, stream, a);
 }
 
 }  // namespace fa
@@ -328,7 +396,7 @@ PoolLayout pool_layout(long long n_pages, long long slots, long long width) {
   l.uses = 64;
   l.pages = l.uses + (n_pages + 63) / 64 * 64;
   l.slot = l.pages + (n_pages + 63) / 64 * 64;
-  l.copies = l.slot + 4 * slots;
+  l.copies = l.slot + 2 * slots;
   l.moves = l.copies + 3 * slots;
   l.old = l.moves + 2 * n_pages;
   l.total = l.old + slots * width;
@@ -439,34 +507,17 @@ size_t fa_cache_workspace_size(int n_pages, int slots, int table_width) {
 int fa_cache_update(const fa_pool* pool, const int32_t* src, const int32_t* new_lens, int32_t* info, void* workspace,
                     size_t workspace_bytes, fa_stream_t stream) {
   fa::PoolArgs a = {};
-  int rc = check_pool(pool, info, workspace, workspace_bytes, &a);
+  const int rc = check_pool(pool, info, workspace, workspace_bytes, &a);
   if (rc != FA_OK) return rc;
   if (!src || !new_lens) return FA_ERR_INVALID_ARG;
   a.src = src, a.fresh = new_lens;
-  int sms = 0;
-  if (!fa::sm_count(&sms)) return FA_ERR_CUDA;
-  const auto st = reinterpret_cast<cudaStream_t>(stream);
-  rc = fa::launch_pdl("pool_clear_kernel", fa::pool_clear_kernel, dim3((a.n_pages + 255) / 256), dim3(256), 0, st, a);
-  if (rc == FA_OK) rc = fa::launch_pdl("pool_mark_kernel", fa::pool_mark_kernel<true>, dim3(a.slots), dim3(256), 0, st, a);
-  if (rc == FA_OK) rc = fa::launch_pdl("update_plan_kernel", fa::update_plan_kernel, dim3(1), dim3(1024), 0, st, a);
-  if (rc == FA_OK) rc = fa::launch_pdl("update_apply_kernel", fa::update_apply_kernel, dim3(a.slots), dim3(256), 0, st, a);
-  if (rc == FA_OK) rc = fa::launch_pdl("update_copy_kernel", fa::update_copy_kernel, dim3(8 * sms), dim3(256), 0, st, a);
-  return rc;
+  return fa::launch_pool(true, a, reinterpret_cast<cudaStream_t>(stream));
 }
 
 int fa_cache_compact(const fa_pool* pool, int32_t* info, void* workspace, size_t workspace_bytes, fa_stream_t stream) {
   fa::PoolArgs a = {};
-  int rc = check_pool(pool, info, workspace, workspace_bytes, &a);
-  if (rc != FA_OK) return rc;
-  int sms = 0;
-  if (!fa::sm_count(&sms)) return FA_ERR_CUDA;
-  const auto st = reinterpret_cast<cudaStream_t>(stream);
-  rc = fa::launch_pdl("pool_clear_kernel", fa::pool_clear_kernel, dim3((a.n_pages + 255) / 256), dim3(256), 0, st, a);
-  if (rc == FA_OK) rc = fa::launch_pdl("pool_mark_kernel", fa::pool_mark_kernel<false>, dim3(a.slots), dim3(256), 0, st, a);
-  if (rc == FA_OK) rc = fa::launch_pdl("compact_plan_kernel", fa::compact_plan_kernel, dim3(1), dim3(1024), 0, st, a);
-  if (rc == FA_OK) rc = fa::launch_pdl("compact_table_kernel", fa::compact_table_kernel, dim3(a.slots), dim3(256), 0, st, a);
-  if (rc == FA_OK) rc = fa::launch_pdl("compact_copy_kernel", fa::compact_copy_kernel, dim3(8 * sms), dim3(256), 0, st, a);
-  return rc;
+  const int rc = check_pool(pool, info, workspace, workspace_bytes, &a);
+  return rc != FA_OK ? rc : fa::launch_pool(false, a, reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"
