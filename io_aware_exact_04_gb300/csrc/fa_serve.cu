@@ -16,6 +16,7 @@ struct ServeArgs {
   uint16_t* o;
   long long q_st, q_sh, k_st, k_sh, v_st, v_sh, o_st, o_sh;  // token and head strides, elements
   float* lse;  // [Hq, T] or null
+  int o_wide;  // every row of o is 32-byte aligned
   // the cache; prompts have none (table null)
   const uint16_t *kc, *vc;
   long long c_sp, c_sh, c_st;
@@ -47,8 +48,8 @@ constexpr int kNewBox = 16;
 // key/value head, so that its keys are read once for the whole group. A work item is a pair of
 // such tiles, one for each of two query lanes (warpgroups 0 and 1), over the key tiles of its
 // sequence: first the cached tokens, 128 a tile, then the new ones. Where an item has one query
-// tile only, both lanes take it and alternate key tiles ("dual"), and lane 0 joins the two
-// results out of tensor memory at the end.
+// tile only, both lanes take it and alternate key tiles ("dual"), and join the two results out of
+// tensor memory at the end, each for half of the columns.
 //
 // Roles, 384 threads: warps 0-3 and 4-7 the softmax of lanes 0 and 1 (a thread a row), warp 8
 // the TMA producer and scheduler, warps 9 and 10 the issuers of O += P V of lanes 0 and 1, warp
@@ -71,8 +72,8 @@ struct ServeCfg {
   static constexpr int OFF_R = 2 * TILE_BYTES;
   static constexpr int OFF_BAR = OFF_R + NSLOT * TILE_BYTES;
   static constexpr int OFF_DESC = OFF_BAR + 512;   // 4 x 16 ints
-  static constexpr int OFF_ML = OFF_BAR + 768;     // m and l of lane 1's rows, for the join of a dual item
-  static constexpr int SMEM_BYTES = OFF_ML + 1024 + 1024;
+  static constexpr int OFF_ML = OFF_BAR + 768;     // m and l of both lanes' rows, for the join of a dual item
+  static constexpr int SMEM_BYTES = OFF_ML + 2048;
   // A key tile is taken in HPT steps of KT keys. The softmax must find S of the next step ready
   // when it ends one, so S may not wait for PV of the step before. TMEM has room for that in two
   // ways: d = 64 keeps P apart from S (one step a tile; S is free once it is in registers);
@@ -269,9 +270,13 @@ __global__ void __launch_bounds__(384, 1)
                  const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_kc,
                  const __grid_constant__ CUtensorMap tm_vc, ServeArgs a) {
   using C = ServeCfg<D>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* sm = align1024(smem_raw);
+  // 1024-byte aligned, as the swizzled tiles have to be: there is no room to round the address up
+  extern __shared__ __align__(1024) uint8_t sm[];
   const uint32_t sbase = smem_u32(sm);
+  if (sbase & 1023u) {  // (never seen: the kernel has no static shared memory)
+    if (threadIdx.x == 0) record_check(a.status, SITE_S_SMEM);
+    return;
+  }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t b0 = sbase + C::OFF_BAR;
   auto BAR = [&](int i) { return b0 + 8u * i; };
@@ -296,9 +301,9 @@ __global__ void __launch_bounds__(384, 1)
         mbar_init(BAR(C::O_DONE + 2 * t + h), 1);
       }
       mbar_init(BAR(C::S_FREE + t), 4);
-      mbar_init(BAR(C::O_FREE + t), 4);
+      mbar_init(BAR(C::O_FREE + t), 8);  // four warps twice, or all eight in a join
     }
-    mbar_init(BAR(C::MERGE), 4);
+    mbar_init(BAR(C::MERGE), 8);
     mbar_init(BAR(C::DRAIN), 3);
     for (int i = 0; i < 4; ++i) {
       mbar_init(BAR(C::D_FULL + i), 1);
@@ -816,29 +821,27 @@ __global__ void __launch_bounds__(384, 1)
       if (!ok) break;
       tc_fence_after();
       const bool join = dual && it.c1 > 0;
-      float f0 = 1.f, f1 = 0.f;
+      float f0 = 1.f, f1 = 0.f;  // weights of this lane's O and of the other's
       if (join) {
-        if (t == 1) {
-          ml[row] = m_run;
-          ml[128 + row] = l_run;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(BAR(C::MERGE));
-        } else {
-          if (!wait_phase(BAR(C::MERGE), merges & 1, st, SITE_SW_MERGE) ||
-              !wait_pv(1, st1 + it.s1 - 1))
-            break;
-          tc_fence_after();
-          const float m1 = ml[row], m = fmaxf(m_run, m1), base = m == -INFINITY ? 0.f : m;
-          f0 = ex2_approx(m_run - base);
-          f1 = ex2_approx(m1 - base);
-          l_run = l_run * f0 + ml[128 + row] * f1;
-          m_run = m;
-        }
+        ml[256 * t + row] = m_run;
+        ml[256 * t + 128 + row] = l_run;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(C::MERGE));
+        if (!wait_phase(BAR(C::MERGE), merges & 1, st, SITE_SW_MERGE) ||
+            !wait_pv(t ^ 1, t ? st0 + it.s0 - 1 : st1 + it.s1 - 1))
+          break;
+        tc_fence_after();
+        const float* other = ml + 256 * (t ^ 1) + row;
+        const float m = fmaxf(m_run, other[0]), base = m == -INFINITY ? 0.f : m;
+        f0 = ex2_approx(m_run - base);
+        f1 = ex2_approx(other[0] - base);
+        l_run = l_run * f0 + other[128] * f1;
+        m_run = m;
         ++merges;
       }
       st0 += it.s0;
       st1 += it.s1;
-      if (dual && t == 1) continue;  // lane 0 writes the results
+      if (dual && t == 1 && !join) continue;  // lane 0 has all of them
       // l = 0: no key; NaN stays NaN
       const float inv = l_run != 0.f ? 1.f / l_run : 0.f;
       const float lse2 = l_run != 0.f ? m_run + lg2_approx(l_run) : -INFINITY;
@@ -853,10 +856,12 @@ __global__ void __launch_bounds__(384, 1)
       f1 *= inv;
       const bool write = valid && FA_CHECK(whole ? in_range(token, a.T) : in_range(part, a.part_rows), st, DBG_GLOBAL_STORE);
       uint16_t* orow = a.o + token * a.o_st + head * a.o_sh;
-      float4* prow = reinterpret_cast<float4*>(a.part_o + part * D);
+      float* prow = a.part_o + part * D;
+      // in a join each lane takes half of the columns
+      const int q0 = join ? t * (D / 64) : 0, q1 = join ? q0 + D / 64 : D / 32;
       if (any) {
-#pragma unroll
-        for (int q = 0; q < D / 32; ++q) {
+#pragma unroll 1
+        for (int q = q0; q < q1; ++q) {
           uint32_t r[32];
           float v[32];
           tmem_ld32(tmem + lane_off + C::tm_o(t) + q * 32, r);
@@ -864,35 +869,53 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
           for (int x = 0; x < 32; ++x) v[x] = __uint_as_float(r[x]) * f0;
           if (join) {
-            tmem_ld32(tmem + lane_off + C::tm_o(1) + q * 32, r);
+            tmem_ld32(tmem + lane_off + C::tm_o(t ^ 1) + q * 32, r);
             tmem_wait_ld();
 #pragma unroll
             for (int x = 0; x < 32; ++x) v[x] = fmaf(__uint_as_float(r[x]), f1, v[x]);
           }
-          if (q == D / 32 - 1) {  // O is in registers: the issuers may write it again
+          if (q == q1 - 1) {  // O is in registers: the issuers may write it again
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
-              mbar_arrive(BAR(C::O_FREE + t));
-              if (join) mbar_arrive(BAR(C::O_FREE + 1));
+              mbar_arrive_n(BAR(C::O_FREE + t), join ? 1 : 2);
+              if (join) mbar_arrive(BAR(C::O_FREE + (t ^ 1)));
             }
           }
+          // a thread writes a row: whole sectors where the rows allow it
           if (write && whole) {
+            uint32_t y[2][8];
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
-              *reinterpret_cast<uint4*>(orow + q * 32 + x * 8) =
-                  make_uint4(pack2<F16>(v[8 * x], v[8 * x + 1]), pack2<F16>(v[8 * x + 2], v[8 * x + 3]),
-                             pack2<F16>(v[8 * x + 4], v[8 * x + 5]), pack2<F16>(v[8 * x + 6], v[8 * x + 7]));
+            for (int x = 0; x < 16; ++x) y[x >> 3][x & 7] = pack2<F16>(v[2 * x], v[2 * x + 1]);
+            if (a.o_wide) {
+              store_32b(orow + q * 32, y[0]);
+              store_32b(orow + q * 32 + 16, y[1]);
+            } else {
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                *reinterpret_cast<uint4*>(orow + q * 32 + x * 8) =
+                    make_uint4(y[x >> 1][(x & 1) * 4], y[x >> 1][(x & 1) * 4 + 1], y[x >> 1][(x & 1) * 4 + 2],
+                               y[x >> 1][(x & 1) * 4 + 3]);
+            }
           } else if (write) {
 #pragma unroll
-            for (int x = 0; x < 8; ++x) prow[q * 8 + x] = make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
+            for (int x = 0; x < 4; ++x) {
+              uint32_t y[8];
+#pragma unroll
+              for (int z = 0; z < 8; ++z) y[z] = __float_as_uint(v[8 * x + z]);
+              store_32b(prow + q * 32 + x * 8, y);
+            }
           }
         }
-        if (write && !whole) a.part_lse[part] = lse2;
-        if (write && whole && a.lse) a.lse[(long long)head * a.T + token] = lse2 * 0.6931471805599453f;
+        if (write && q0 == 0) {
+          if (!whole)
+            a.part_lse[part] = lse2;
+          else if (a.lse)
+            a.lse[(long long)head * a.T + token] = lse2 * 0.6931471805599453f;
+        }
       } else if (lane == 0) {
-        mbar_arrive(BAR(C::O_FREE + t));
-        if (join) mbar_arrive(BAR(C::O_FREE + 1));
+        mbar_arrive_n(BAR(C::O_FREE + t), join ? 1 : 2);
+        if (join) mbar_arrive(BAR(C::O_FREE + (t ^ 1)));
       }
     }
   }
@@ -1086,6 +1109,7 @@ int forward(const fa_rows* q, const fa_rows* k, const fa_rows* v, const fa_rows*
   a.v_st = v->token_stride, a.v_sh = v->head_stride;
   a.o_st = o->token_stride, a.o_sh = o->head_stride;
   a.lse = lse;
+  a.o_wide = (reinterpret_cast<uintptr_t>(o->data) & 31u) == 0 && o->token_stride % 16 == 0 && o->head_stride % 16 == 0;
   if (cache) {
     a.kc = static_cast<const uint16_t*>(cache->k);
     a.vc = static_cast<const uint16_t*>(cache->v);
