@@ -325,7 +325,7 @@ FA_API int fa_forward_tree(const fa_rows* q, const fa_rows* k, const fa_rows* v,
                            void* workspace, size_t workspace_bytes, fa_stream_t stream);
 
 /* Workspace bytes of fa_forward_tree on the current device: two partial results
- * of 256 rows for each SM. 0 for an unsupported d. */
+ * of 256 rows, and 32 bytes, for each SM. 0 for an unsupported d. */
 FA_API size_t fa_forward_tree_workspace_size(int d);
 
 /* Which nodes a node of a tree sees: itself and its ancestors. parents: device

@@ -11,28 +11,36 @@ namespace fa {
 
 // ---------------------------------------------------------------------------------------------
 // Bits of a tree: node i sees itself and what its parent sees. A thread walks the chain of one
-// node; every step goes to a smaller index, so that the walk ends whatever the parents are.
+// node; every step goes to a smaller index, so that the walk ends whatever the parents are. The
+// parents of the first nodes lie in shared memory: a step of the walk waits for the one before.
+constexpr int kParents = 1024;
 __global__ void __launch_bounds__(128) tree_mask_kernel(const int* parents, const int* cu, uint32_t* mask, int words, int B,
                                                         int T, int* status) {
   griddep_wait();
   griddep_launch_dependents();
+  __shared__ int near_root[kParents];
   const int b = blockIdx.x;
   const SeqRange r = seq_range(cu, b, T, status);
   const int n = r.hi - r.lo;
   if (n > 32 * words && threadIdx.x == 0) record_check(status, SITE_S_WORDS);
+  for (int i = threadIdx.x; i < min(n, kParents); i += blockDim.x) near_root[i] = parents[r.lo + i];
+  __syncthreads();
   for (int i = threadIdx.x; i < n; i += blockDim.x) {
     uint32_t* row = mask + (long long)(r.lo + i) * words;
-    for (int w = 0; w < words; ++w) row[w] = 0;
+    uint32_t bits = 0;
+    int word = i >> 5;  // the word that `bits` belongs to; the walk meets the words from the last to the first
+    for (int w = words - 1; w > word; --w) row[w] = 0;
     for (int j = i;;) {
-      if (j < 32 * words) row[j >> 5] |= 1u << (j & 31);
-      const int p = parents[r.lo + j];
-      if (p < 0) break;
-      if (p >= j) {
-        record_check(status, SITE_S_PARENT);
-        break;
-      }
+      for (; (j >> 5) != word; --word, bits = 0)
+        if (word < words) row[word] = bits;
+      bits |= 1u << (j & 31);
+      const int p = j < kParents ? near_root[j] : parents[r.lo + j];
+      if (p >= j) record_check(status, SITE_S_PARENT);
+      if (p < 0 || p >= j) break;
       j = p;
     }
+    for (; word >= 0; --word, bits = 0)
+      if (word < words) row[word] = bits;
   }
 }
 

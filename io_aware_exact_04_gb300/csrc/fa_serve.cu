@@ -33,6 +33,7 @@ struct ServeArgs {
   float* part_o;    // workspace: two slots of 256 rows for each CTA, O normalised by its own l
   float* part_lse;  // their LSEs, base 2 (-inf: no key, O not written)
   long long part_rows;
+  int4* cuts;       // two for each CTA: the item that its first tile cuts, if it is the first to (ServeCut)
   int* status;
 };
 
@@ -114,6 +115,7 @@ struct ServeItem {
   int kvh;
   int slot;    // partial result slot
   int s0, s1;  // steps of lanes 0 and 1 (a half of a tile with no key in it is no step)
+  int cnt_all; // (not published) key tiles of the whole item
 };
 enum { ITEM_DUAL = 1, ITEM_WHOLE = 2 };
 
@@ -151,24 +153,30 @@ __device__ __forceinline__ long long warp_sum(long long x) {
 
 // Trees: the run of key tiles of CTA c, by a whole warp.
 struct ServeRuns {
-  long long total;
-  int ctas;  // CTAs with work
-  __device__ long long start(int c) const { return total * c / ctas; }
+  long long total, base;
+  int ctas, rest;        // CTAs with work; the first `rest` of them take a tile more
+  long long mine;        // this lane's sequence among the first 32: its tiles
+  __device__ long long start(int c) const { return base * c + min(c, rest); }
 };
 __device__ __forceinline__ ServeRuns serve_runs(const ServeArgs& a, int unit, int grid, bool record) {
   ServeRuns r;
-  long long x = 0;
-  for (int b = threadIdx.x & 31; b < a.B; b += 32) x += seq_work<true>(a, b, unit, record).tiles;
+  const int lane = threadIdx.x & 31;
+  r.mine = lane < a.B ? seq_work<true>(a, lane, unit, record).tiles : 0;
+  long long x = r.mine;
+  for (int b = lane + 32; b < a.B; b += 32) x += seq_work<true>(a, b, unit, record).tiles;
   r.total = warp_sum(x);
-  r.ctas = (int)min((long long)grid, max(1LL, (r.total + kMinTiles - 1) / kMinTiles));
+  r.ctas = r.total < (long long)grid * kMinTiles ? max(1, ((int)r.total + kMinTiles - 1) / kMinTiles) : grid;
+  r.base = r.total < (1LL << 31) ? (int)r.total / r.ctas : r.total / r.ctas;  // the short division costs a fifth
+  r.rest = (int)(r.total - r.base * r.ctas);
   return r;
 }
 // The sequence that tile `pos` of all belongs to, and its first tile; by a whole warp. pos < total.
-__device__ __forceinline__ int serve_seek(const ServeArgs& a, int unit, long long pos, long long* first) {
+__device__ __forceinline__ int serve_seek(const ServeArgs& a, int unit, const ServeRuns& runs, long long pos,
+                                          long long* first) {
   const int lane = threadIdx.x & 31;
   long long base = 0;
   for (int b0 = 0; b0 < a.B; b0 += 32) {
-    const long long mine = b0 + lane < a.B ? seq_work<true>(a, b0 + lane, unit, false).tiles : 0;
+    const long long mine = b0 == 0 ? runs.mine : b0 + lane < a.B ? seq_work<true>(a, b0 + lane, unit, false).tiles : 0;
     long long incl = mine;
     for (int o = 1; o < 32; o <<= 1) {
       const long long y = __shfl_up_sync(0xffffffffu, incl, o);
@@ -440,6 +448,7 @@ __global__ void __launch_bounds__(384, 1)
       const bool dual = n1 == 0;
       j1 = min(j1, nmax);
       it->cnt = max(0, j1 - j0);
+      it->cnt_all = nmax;
       it->flags = (dual ? ITEM_DUAL : 0) | (j0 == 0 && j1 == nmax ? ITEM_WHOLE : 0);
       it->c0 = dual ? (it->cnt + 1) >> 1 : max(0, min(j1, n0) - j0);
       it->c1 = dual ? it->cnt >> 1 : it->cnt;
@@ -461,22 +470,36 @@ __global__ void __launch_bounds__(384, 1)
     if (PAGED) {
       const int unit = 2 * npt;
       const ServeRuns runs = serve_runs(a, unit, gridDim.x, blockIdx.x == 0);
+      int parts = 0;  // of the item that this CTA is the first to cut
+      int4 cut = make_int4(0, 0, 0, 0);
       if ((int)blockIdx.x < runs.ctas && runs.total > 0) {
         long long pos = runs.start(blockIdx.x), first = 0;
         const long long end = runs.start(blockIdx.x + 1);
-        int b = serve_seek(a, unit, pos, &first);
+        int b = serve_seek(a, unit, runs, pos, &first);
         while (ok && pos < end) {
           const SeqWork w = seq_work<PAGED>(a, b, unit, false);
           while (ok && pos < end && pos - first < w.tiles) {
-            const int q = (int)((pos - first) / w.nk), j0 = (int)((pos - first) % w.nk);
+            const long long at = pos - first;
+            const int q = at < (1LL << 31) ? (int)at / w.nk : (int)(at / w.nk), j0 = (int)(at - (long long)q * w.nk);
             const int j1 = (int)min((long long)w.nk, j0 + (end - pos));
             make_item(w, unit, q % a.Hkv, q / a.Hkv, j0, j1, &it);
+            if (j0 > 0 && it.cnt > 0 && runs.start(blockIdx.x - 1) <= pos - j0) {
+              // (the first item only) how many CTAs, this one included, hold later parts of it
+              const long long end_of_item = pos + it.cnt_all - j0;
+              for (int k = blockIdx.x + lane; __any_sync(0xffffffffu, k < runs.ctas); k += 32)
+                parts += __popc(__ballot_sync(0xffffffffu, k < runs.ctas && runs.start(k) < end_of_item));
+              cut = make_int4(it.n, it.row0, it.tok0, it.kvh);
+            }
             if (it.cnt > 0) ok = run_item(it, b);
             pos += j1 - j0;
           }
           first += w.tiles;
           ++b;
         }
+      }
+      if (lane == 0) {
+        a.cuts[2 * blockIdx.x] = make_int4(parts, 0, 0, 0);
+        a.cuts[2 * blockIdx.x + 1] = cut;
       }
     } else {
       const int unit = prompt_unit(a, npt, gridDim.x, blockIdx.x == 0);
@@ -932,42 +955,19 @@ __global__ void __launch_bounds__(384, 1)
 // [32 y, 32 y + 32) of the item that boundary x + 1 is the first to cut. A warp a row at d = 128,
 // half a warp at d = 64; the parts' weights come from their LSEs, as between key tiles.
 template <int D, bool F16>
-__global__ void __launch_bounds__(256) serve_join_kernel(ServeArgs a, int grid) {
+__global__ void __launch_bounds__(256) serve_join_kernel(ServeArgs a) {
   griddep_wait();
   griddep_launch_dependents();
-  __shared__ int info[8];  // parts, tokens, row0, tok0, kvh
   const int npt = 128 / a.G, c = blockIdx.x + 1;
-  if (threadIdx.x < 32) {
-    int parts = 0;
-    const ServeRuns runs = serve_runs(a, 2 * npt, grid, false);
-    SeqWork w = {};
-    int q = 0;
-    if (c < runs.ctas && runs.total > 0) {
-      const long long pos = runs.start(c);
-      long long first;
-      const int b = serve_seek(a, 2 * npt, pos, &first);
-      w = seq_work<true>(a, b, 2 * npt, false);
-      q = (int)((pos - first) / w.nk);
-      const long long item = first + (long long)q * w.nk;
-      const int pair = q / a.Hkv;
-      const int nmax = max(tiles_of(w, 2 * pair, npt, a.mask != nullptr), tiles_of(w, 2 * pair + 1, npt, a.mask != nullptr));
-      if (runs.start(c - 1) <= item && pos > item)
-        for (int k = c; k < runs.ctas && runs.start(k) < item + nmax; ++k) ++parts;
-    }
-    if (threadIdx.x == 0) {
-      info[0] = parts;
-      info[1] = w.n, info[2] = w.row0, info[3] = q / a.Hkv * 2 * npt, info[4] = q % a.Hkv;
-    }
-  }
-  __syncthreads();
-  const int parts = info[0] + 1;  // part 0: CTA c - 1's last item; then the first items of c, c + 1, ..
+  const int parts = a.cuts[2 * c].x + 1;  // part 0: CTA c - 1's last item; then the first items of c, c + 1, ..
   if (parts == 1) return;
+  const int4 cut = a.cuts[2 * c + 1];  // tokens of the sequence, its first row, the item's first token, head
   constexpr int LPR = D / 4;  // lanes a row
   const int sub = threadIdx.x % LPR;
   for (int row = blockIdx.y * 32 + threadIdx.x / LPR; row < blockIdx.y * 32 + 32; row += 256 / LPR) {
     const int rr = row & 127, rn = rr / a.G, rg = rr - rn * a.G;
-    const int tok = info[3] + (row >> 7) * npt + rn;
-    if (rn >= npt || tok >= info[1]) continue;
+    const int tok = cut.z + (row >> 7) * npt + rn;
+    if (rn >= npt || tok >= cut.x) continue;
     auto at = [&](int k) { return (long long)(k == 0 ? 2 * (c - 1) + 1 : 2 * (c - 1 + k)) * 256 + row; };
     float m = -INFINITY;
     for (int k = 0; k < parts; ++k) m = fmaxf(m, a.part_lse[at(k)]);
@@ -983,8 +983,8 @@ __global__ void __launch_bounds__(256) serve_join_kernel(ServeArgs a, int grid) 
       o.x = fmaf(w, x.x, o.x), o.y = fmaf(w, x.y, o.y), o.z = fmaf(w, x.z, o.z), o.w = fmaf(w, x.w, o.w);
     }
     const float inv = l != 0.f ? 1.f / l : 0.f;
-    const int h = info[4] * a.G + rg;
-    const long long token = info[2] + tok;
+    const int h = cut.w * a.G + rg;
+    const long long token = cut.y + tok;
     *reinterpret_cast<uint2*>(a.o + token * a.o_st + h * a.o_sh + 4 * sub) =
         make_uint2(pack2<F16>(o.x * inv, o.y * inv), pack2<F16>(o.z * inv, o.w * inv));
     if (sub == 0 && a.lse)
@@ -1028,7 +1028,7 @@ static int launch_serve_d(ServeArgs a, cudaStream_t stream) {
   }
   int rc = launch_pdl("serve_kernel", kernel, dim3(grid), dim3(C::THREADS), C::SMEM_BYTES, stream, mq, mk, mv, mkc, mvc, a);
   if (rc != FA_OK || !PAGED || grid < 2) return rc;
-  return launch_pdl("serve_join_kernel", serve_join_kernel<D, F16>, dim3(grid - 1, 8), dim3(256), 0, stream, a, grid);
+  return launch_pdl("serve_join_kernel", serve_join_kernel<D, F16>, dim3(grid - 1, 8), dim3(256), 0, stream, a);
 }
 
 static int launch_serve(const ServeArgs& a, int d, int dtype, cudaStream_t stream) {
@@ -1131,6 +1131,7 @@ int forward(const fa_rows* q, const fa_rows* k, const fa_rows* v, const fa_rows*
   a.part_rows = 2LL * sms * 256;
   a.part_o = static_cast<float*>(workspace);
   a.part_lse = a.part_o + a.part_rows * d;
+  a.cuts = reinterpret_cast<int4*>(a.part_lse + a.part_rows);
   a.status = status;
   return fa::launch_serve(a, d, dtype, reinterpret_cast<cudaStream_t>(stream));
 }
@@ -1143,7 +1144,7 @@ size_t fa_forward_tree_workspace_size(int d) {
   if (d != 64 && d != 128) return 0;
   int sms = 0;
   if (!fa::sm_count(&sms)) return 0;
-  return (size_t)2 * sms * 256 * (d + 1) * 4;
+  return (size_t)2 * sms * 256 * (d + 1) * 4 + (size_t)sms * 2 * sizeof(int4);
 }
 
 int fa_forward_prompt(const fa_rows* q, const fa_rows* k, const fa_rows* v, const fa_rows* o, float* lse,
