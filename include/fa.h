@@ -261,7 +261,9 @@ FA_API size_t fa_backward_noalloc_max_bytes(void);
  *  - A value that only the kernels can check (an offset that decreases or passes
  *    T, a length that passes the page table, a page id outside the cache) records
  *    FA_ERR_DEVICE_CHECK in the device status word. Nothing outside the given
- *    tensors is read or written; what the call says below happens instead. */
+ *    tensors is read or written; what the call says below happens instead.
+ *    Where offsets decrease, rows that two sequences claim hold either's result.
+ *  - Each entry point is called once on a device before it is captured there. */
 typedef enum { FA_BF16 = 0, FA_FP16 = 1 } fa_dtype;
 
 /* Rows of [T, H, d] tokens: d contiguous, strides in elements, both positive
@@ -310,6 +312,8 @@ FA_API int fa_forward_prompt(const fa_rows* q, const fa_rows* k, const fa_rows* 
  *    sequence (fa_tree_mask makes it from parents). Any bits may be set; those at
  *    or past the sequence's number of nodes, and nodes past 32 mask_words, count
  *    as not set.
+ * As for prompts, a NaN or infinity in a node's own value may reach nodes of its
+ * sequence that do not see it.
  * A node that sees nothing gets O = 0 and LSE = -inf. o is [T, Hq, d], lse
  * [Hq, T] fp32 (NULL: not written). A sequence without nodes writes nothing, and
  * its length and pages are not looked at. What lies in the cache past lens[b]
