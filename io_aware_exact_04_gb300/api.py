@@ -233,7 +233,7 @@ def _first(name: str, t: torch.Tensor, dim: int) -> int:
 
 def _rows(name: str, t: torch.Tensor, index: int, dtype, T: int, H: int, d: int) -> _lib.Rows:
     """fa_rows of a [T, H, d] tensor: d contiguous, the other strides positive multiples of 8."""
-    if not t.is_cuda or t.get_device() != index or t.dtype is not dtype or t.shape != (T, H, d):
+    if t.dtype is not dtype or t.get_device() != index or t.shape != (T, H, d):  # (a CPU tensor's device is -1)
         raise ValueError(f"{name} must be a {dtype} tensor {(T, H, d)} on cuda:{index}, is {t.dtype} {tuple(t.shape)} on {t.device}")
     st, sh, sd = t.stride()
     # the stride of a dimension of one element is never used: any valid value will do
@@ -248,7 +248,7 @@ def _rows(name: str, t: torch.Tensor, index: int, dtype, T: int, H: int, d: int)
 
 def _ints(name: str, t: torch.Tensor, index: int, shape) -> int:
     """The address of a contiguous int32 tensor of a given shape."""
-    if t.dtype is not _INT32 or t.shape != shape or not t.is_cuda or t.get_device() != index or not t.is_contiguous():
+    if t.dtype is not _INT32 or t.get_device() != index or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 tensor {tuple(shape)} on cuda:{index}, is {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
     return t.data_ptr()
@@ -256,16 +256,16 @@ def _ints(name: str, t: torch.Tensor, index: int, shape) -> int:
 
 def _offsets(cu: torch.Tensor, index: int):
     """The address of token offsets and how many sequences they bound."""
-    if cu.dim() != 1 or cu.shape[0] < 1:
+    n = cu.numel()
+    if n < 1:
         raise ValueError("cu holds the offsets of B sequences and the end: int32 [B + 1]")
-    B = cu.shape[0] - 1
-    return _ints("cu", cu, index, (B + 1,)), B
+    return _ints("cu", cu, index, (n,)), n - 1
 
 
 def _workspace(workspace, need: int, index: int):
     if workspace is None:
         return torch.empty(need, dtype=_UINT8, device=index)
-    if workspace.dtype is not _UINT8 or not workspace.is_cuda or workspace.get_device() != index or not workspace.is_contiguous():
+    if workspace.dtype is not _UINT8 or workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous uint8 tensor on cuda:{index}")
     return workspace
 
@@ -274,11 +274,11 @@ def _pages(k_cache: torch.Tensor, v_cache: torch.Tensor, table: torch.Tensor, in
            B: int) -> _lib.Pages:
     """fa_pages of [n_pages, Hkv, page_size, d] caches and an int32 [>= B, width] table."""
     shape, strides = k_cache.shape, k_cache.stride()
-    if k_cache.dim() != 4 or v_cache.shape != shape or v_cache.stride() != strides or shape[1] != H or shape[3] != d or shape[0] < 1:
+    if len(shape) != 4 or v_cache.shape != shape or v_cache.stride() != strides or shape[1] != H or shape[3] != d or shape[0] < 1:
         raise ValueError(f"k_cache and v_cache must be [n_pages, {H}, page_size, {d}] with the same shape and strides, are "
                          f"{tuple(shape)} {strides} and {tuple(v_cache.shape)} {v_cache.stride()}")
-    if (k_cache.dtype is not dtype or v_cache.dtype is not dtype or not k_cache.is_cuda or not v_cache.is_cuda or
-            k_cache.get_device() != index or v_cache.get_device() != index):
+    if (k_cache.dtype is not dtype or v_cache.dtype is not dtype or k_cache.get_device() != index or
+            v_cache.get_device() != index):
         raise ValueError(f"k_cache and v_cache must be {dtype} tensors on cuda:{index}")
     n, _, page, _ = shape
     sp, sh, st, sd = strides
@@ -288,7 +288,7 @@ def _pages(k_cache: torch.Tensor, v_cache: torch.Tensor, table: torch.Tensor, in
         sh = 8
     if sd != 1 or sp <= 0 or sh <= 0 or st <= 0 or (sp | sh | st) & 7:
         raise ValueError(f"the cache has strides {strides}: the last must be 1, the others positive multiples of 8")
-    if table.dim() != 2 or table.dtype is not _INT32 or not table.is_cuda or table.get_device() != index:
+    if table.dtype is not _INT32 or table.get_device() != index or table.dim() != 2:
         raise ValueError(f"table must be an int32 [slots, width] tensor on cuda:{index}")
     slots, width = table.shape
     ts, tw = table.stride()
@@ -316,7 +316,7 @@ def _serve(q, k, v, cu, scale, out, lse):
         lse = torch.empty((Hq, T), dtype=_FP32, device=index)
     elif lse is False:
         lse = None
-    elif lse.dtype is not _FP32 or lse.shape != (Hq, T) or not lse.is_contiguous() or not lse.is_cuda or lse.get_device() != index:
+    elif lse.dtype is not _FP32 or lse.get_device() != index or lse.shape != (Hq, T) or not lse.is_contiguous():
         raise ValueError(f"lse must be a contiguous float32 tensor {(Hq, T)} on cuda:{index}")
     rows = (_rows("q", q, index, dtype, T, Hq, d), _rows("k", k, index, dtype, T, Hkv, d),
             _rows("v", v, index, dtype, T, Hkv, d), _rows("out", out, index, dtype, T, Hq, d),
