@@ -59,7 +59,9 @@ struct AppendArgs {
   int* status;
 };
 
-// A warp for each token.
+// A warp for each token: its head rows are whole lines on both sides, 16 bytes a lane. The longest
+// prompts (72 MB moved) take 10.3 us, the measured copy rate; a step's accepted tokens 3.5 us, the
+// latency of finding the sequence, its page and the row.
 template <int D>
 __global__ void __launch_bounds__(128) cache_append_kernel(AppendArgs a) {
   griddep_wait();
@@ -90,9 +92,10 @@ __global__ void __launch_bounds__(128) cache_append_kernel(AppendArgs a) {
 // ---------------------------------------------------------------------------------------------
 // Slots and pages: a plan, made by one cluster of eight CTAs (the counts of all pages have to be
 // complete before the free ones are numbered; a cluster's barrier costs less than another launch:
-// five launches took update_beams 79 us of host time, two take 45), and its execution by the whole
-// GPU. Workspace, in ints: head [64], uses [n_pages], pages [n_pages] (new pages, or where a page
-// goes), slots [slots] x 2, copies [slots] x 3, moves [n_pages] x 2, the table as it was.
+// compacting a small pool took 44 us of the host with five launches and takes 39 with two), and its
+// execution by the whole GPU. Each phase of the plan waits for L2: 10-12 us in all. Workspace, in
+// ints: head [64], uses [n_pages], pages [n_pages] (new pages, or where a page goes), slots [slots] x 2,
+// copies [slots] x 3, moves [n_pages] x 2, the table as it was.
 struct PoolArgs {
   uint8_t* data;
   long long plane_bytes;
@@ -311,7 +314,7 @@ __device__ __forceinline__ void warp_copy(uint8_t* to, const uint8_t* from, int 
 }
 
 // The table rows (a warp each), then the kept rows of the pages that are copied: a warp a plane, head
-// and kCopyBytes.
+// and kCopyBytes. Memory bounds it where much is copied: 256 slots and 51 MB in 11 us.
 __global__ void __launch_bounds__(256) update_apply_kernel(PoolArgs a) {
   griddep_wait();
   griddep_launch_dependents();
@@ -341,6 +344,8 @@ __global__ void __launch_bounds__(256) update_apply_kernel(PoolArgs a) {
   }
 }
 
+// The table, then the moved pages, a warp a plane and kCopyBytes: 4.04 GB in 641 us, 93 % of the measured
+// copy rate (one 16-byte load in flight a thread: 717 us).
 __global__ void __launch_bounds__(256) compact_apply_kernel(PoolArgs a) {
   griddep_wait();
   griddep_launch_dependents();
