@@ -606,6 +606,15 @@ __global__ void __launch_bounds__(384, 1)
         for (int u = uq; ok && u < uq + nq; ++u)
           ok = wait_phase(BAR(C::Q_FULL + (u & 1)), (u >> 1) & 1, st, SITE_SW_Q_FULL);
         const uint32_t qa0 = q_lo + (uq & 1) * TILE16, qa1 = q_lo + ((uq + nq - 1) & 1) * TILE16;
+        auto form_s = [&](int t, int g, uint32_t qa, uint32_t ka) {
+          const uint32_t d = tmem + C::tm_s(t, C::buf(g));
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = ((k >> 2) * C::SUB_BYTES + (k & 3) * 32) >> 4;
+            if (elect_one()) mma_ss(d, sdesc_join(qa + off, HI), sdesc_join(ka + off, HI), IDESC_S, k > 0);
+          }
+          commit(BAR(C::S_FULL + 2 * t + C::buf(g)));
+        };
         auto issue_s = [&](int t, int g, uint32_t qa, uint32_t ka) {
           // S(g) goes over S(g - 1), once it is in registers (d = 64), or over P(g - 2), once PV has read it
           if (C::SEP_P ? g > 0 : g > 1) {
@@ -614,13 +623,7 @@ __global__ void __launch_bounds__(384, 1)
               return false;
           }
           tc_fence_after();
-          const uint32_t d = tmem + C::tm_s(t, C::buf(g));
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t off = ((k >> 2) * C::SUB_BYTES + (k & 3) * 32) >> 4;
-            if (elect_one()) mma_ss(d, sdesc_join(qa + off, HI), sdesc_join(ka + off, HI), IDESC_S, k > 0);
-          }
-          commit(BAR(C::S_FULL + 2 * t + C::buf(g)));
+          form_s(t, g, qa, ka);
           return true;
         };
         for (int k = 0; ok && k < it.cnt; ++k) {
@@ -629,12 +632,30 @@ __global__ void __launch_bounds__(384, 1)
           const int h0 = (dual ? (k & 1) : k >= it.c0) ? 0 : steps_in(it, 0, j);
           const int h1 = (dual ? !(k & 1) : k >= it.c1) ? 0 : steps_in(it, 1, j);
           const uint32_t ka = k_lo + ks.slot * TILE16;
-          for (int h = 0; ok && h < max(h0, h1); ++h) {
-            if (h < h0) ok = issue_s(0, g0++, qa0, ka + h * HALF16);
-            if (ok && h < h1) ok = issue_s(1, g1++, qa1, ka + h * HALF16);
+          if (!C::SEP_P && h0 == 2 && h1 == 2 && min(g0, g1) > 1) {
+            // the ordinary tile of two lanes, with few instructions and one wait for both lanes
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t b0 = BAR(C::O_DONE + C::buf(g0)), b1 = BAR(C::O_DONE + 2 + C::buf(g1));
+              if (!__all_sync(0xffffffffu, mbar_try_wait(b0, C::phase(g0 - 2)) && mbar_try_wait(b1, C::phase(g1 - 2))))
+                if (!(ok = wait_slow(b0, C::phase(g0 - 2), st, SITE_SW_O_DONE) &&
+                           wait_slow(b1, C::phase(g1 - 2), st, SITE_SW_O_DONE)))
+                  break;
+              tc_fence_after();
+              form_s(0, g0++, qa0, ka + h * HALF16);
+              form_s(1, g1++, qa1, ka + h * HALF16);
+            }
+          } else {
+            for (int h = 0; ok && h < max(h0, h1); ++h) {
+              if (h < h0) ok = issue_s(0, g0++, qa0, ka + h * HALF16);
+              if (ok && h < h1) ok = issue_s(1, g1++, qa1, ka + h * HALF16);
+            }
           }
-          commit(BAR(C::EMPTY + ks.slot));
-          commit(BAR(C::EMPTY + ks.slot));
+          if (elect_one()) {
+            mma_commit(BAR(C::EMPTY + ks.slot));
+            mbar_arrive(BAR(C::EMPTY + ks.slot));
+          }
+          __syncwarp();
           ks.skip(2);
         }
         for (int u = uq; u < uq + nq; ++u) commit(BAR(C::Q_EMPTY + (u & 1)));
