@@ -626,26 +626,31 @@ __global__ void __launch_bounds__(384, 1)
           form_s(t, g, qa, ka);
           return true;
         };
+        // up to three phases at once: a wait for each costs some 200 cycles even where all have completed
+        auto wait_for = [&](uint32_t x, uint32_t px, uint32_t y, uint32_t py, uint32_t z, uint32_t pz) {
+          if (__all_sync(0xffffffffu, mbar_try_wait(x, px) && mbar_try_wait(y, py) && mbar_try_wait(z, pz))) return true;
+          return wait_slow(x, px, st, SITE_SW_K_FULL) && wait_slow(y, py, st, SITE_SW_O_DONE) &&
+                 wait_slow(z, pz, st, SITE_SW_O_DONE);
+        };
         for (int k = 0; ok && k < it.cnt; ++k) {
-          if (!(ok = landed(ks, k >= 4, SITE_SW_K_FULL))) break;
           const int j = it.j0 + k;
           const int h0 = (dual ? (k & 1) : k >= it.c0) ? 0 : steps_in(it, 0, j);
           const int h1 = (dual ? !(k & 1) : k >= it.c1) ? 0 : steps_in(it, 1, j);
-          const uint32_t ka = k_lo + ks.slot * TILE16;
-          if (!C::SEP_P && h0 == 2 && h1 == 2 && min(g0, g1) > 1) {
-            // the ordinary tile of two lanes, with few instructions and one wait for both lanes
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t b0 = BAR(C::O_DONE + C::buf(g0)), b1 = BAR(C::O_DONE + 2 + C::buf(g1));
-              if (!__all_sync(0xffffffffu, mbar_try_wait(b0, C::phase(g0 - 2)) && mbar_try_wait(b1, C::phase(g1 - 2))))
-                if (!(ok = wait_slow(b0, C::phase(g0 - 2), st, SITE_SW_O_DONE) &&
-                           wait_slow(b1, C::phase(g1 - 2), st, SITE_SW_O_DONE)))
-                  break;
-              tc_fence_after();
-              form_s(0, g0++, qa0, ka + h * HALF16);
-              form_s(1, g1++, qa1, ka + h * HALF16);
-            }
+          const uint32_t ka = k_lo + ks.slot * TILE16, kb = BAR(C::FULL + ks.slot);
+          const uint32_t o0 = BAR(C::O_DONE + C::buf(g0)), o1 = BAR(C::O_DONE + 2 + C::buf(g1));
+          if (!C::SEP_P && k >= 4 && h0 == 2 && h1 == 2) {
+            // the ordinary tile of two lanes
+            if (!(ok = wait_for(kb, ks.parity, o0, C::phase(g0 - 2), o1, C::phase(g1 - 2)))) break;
+            tc_fence_after();
+            form_s(0, g0++, qa0, ka);
+            form_s(1, g1++, qa1, ka);
+            const uint32_t n0 = BAR(C::O_DONE + C::buf(g0)), n1 = BAR(C::O_DONE + 2 + C::buf(g1));
+            if (!(ok = wait_for(n0, C::phase(g0 - 2), n0, C::phase(g0 - 2), n1, C::phase(g1 - 2)))) break;
+            tc_fence_after();
+            form_s(0, g0++, qa0, ka + HALF16);
+            form_s(1, g1++, qa1, ka + HALF16);
           } else {
+            if (!(ok = landed(ks, k >= 4, SITE_SW_K_FULL))) break;
             for (int h = 0; ok && h < max(h0, h1); ++h) {
               if (h < h0) ok = issue_s(0, g0++, qa0, ka + h * HALF16);
               if (ok && h < h1) ok = issue_s(1, g1++, qa1, ka + h * HALF16);
