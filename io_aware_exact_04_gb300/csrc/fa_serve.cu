@@ -53,8 +53,8 @@ constexpr int kNewBox = 16;
 // tile only, both lanes take it and alternate key tiles ("dual"), and join the two results out of
 // tensor memory at the end, each for half of the columns.
 //
-// Roles, 384 threads: warps 0-3 and 4-7 the softmax of lanes 0 and 1 (a thread a row), warp 8
-// the TMA producer and scheduler, warps 9 and 10 the issuers of O += P V of lanes 0 and 1, warp
+// Roles, 384 threads: warps 0-3 and 4-7 the softmax of lanes 0 and 1 (a thread a row), warp 9
+// the TMA producer and scheduler, warps 8 and 10 the issuers of O += P V of lanes 0 and 1, warp
 // 11 the issuer of S = Q K^T of both (with one issuer a lane for both products, decoding 64
 // sequences over up to 8192 tokens took 210 us instead of 176). The producer
 // runs ahead: it publishes items in a ring of four descriptors, loads Q into two slots and K and
@@ -99,6 +99,8 @@ struct ServeCfg {
   __device__ static constexpr uint32_t tm_o(int t) { return SEP_P ? 384u + 64u * t : 256u + (uint32_t)D * t; }
   static constexpr uint32_t TM_COLS = 512;
   static constexpr int THREADS = 384;
+  // with few rows the softmax is warps 0 and 4, on the scheduler of warp 8: the least busy role there
+  static constexpr int PV0 = 8, PRODUCER = 9, PV1 = 10, S_BOTH = 11;
   // barriers
   static constexpr int FULL = 0, EMPTY = NSLOT, Q_FULL = 2 * NSLOT, Q_EMPTY = Q_FULL + 2, S_FULL = Q_EMPTY + 2,
                        P_READY = S_FULL + 4, O_DONE = P_READY + 4, S_FREE = O_DONE + 4, O_FREE = S_FREE + 2,
@@ -309,7 +311,7 @@ __global__ void __launch_bounds__(384, 1)
   int* descs = reinterpret_cast<int*>(sm + C::OFF_DESC);
   const int npt = 128 / a.G;  // tokens of a query tile
 
-  if (warp == 8 && lane == 0) {
+  if (warp == C::PRODUCER && lane == 0) {
     for (int i = 0; i < C::NSLOT; ++i) {
       mbar_init(BAR(C::FULL + i), 1);
       mbar_init(BAR(C::EMPTY + i), 2);  // V: both issuers; K: its issuer twice
@@ -342,7 +344,7 @@ __global__ void __launch_bounds__(384, 1)
       prefetch_tmap(&tm_vc);
     }
   }
-  if (warp == 9) {
+  if (warp == C::PV0) {
     tmem_alloc(smem_u32(tmem_slot), C::TM_COLS);
     tmem_relinquish();
   }
@@ -377,7 +379,7 @@ __global__ void __launch_bounds__(384, 1)
     return true;
   };
 
-  if (warp == 8) {
+  if (warp == C::PRODUCER) {
     // ------------------------------------------------------------ scheduler and TMA producer
     int items = 0, uq = 0, e = 0;  // items published, Q slots and ring entries used
     bool ok = true;
@@ -546,7 +548,7 @@ __global__ void __launch_bounds__(384, 1)
         }
       }
     }
-  } else if (warp >= 9) {
+  } else if (warp >= 8) {
     // ------------------------------------------------------------ MMA issuers
     constexpr uint32_t IDESC_S = F16 ? idesc_f16_f32(128, C::KT, 0, 0) : idesc_bf16_f32(128, C::KT, 0, 0);
     constexpr uint32_t IDESC_O = F16 ? idesc_f16_f32(128, D, 0, 1) : idesc_bf16_f32(128, D, 0, 1);
@@ -593,7 +595,7 @@ __global__ void __launch_bounds__(384, 1)
       return wait_phase(BAR(C::FULL + p.slot), p.parity, st, site);
     };
     bool ok = true;
-    if (warp == 11) {
+    if (warp == C::S_BOTH) {
       // S = Q K^T of both lanes, tile after tile in the order of the ring
       const uint32_t q_lo = sdesc_lo(sbase + C::OFF_Q, 16), k_lo = sdesc_lo(sbase + C::OFF_R, 16);
       Place ks = {0, 0, 0};
@@ -668,7 +670,7 @@ __global__ void __launch_bounds__(384, 1)
       }
     } else {
       // O += P V of lane t
-      const int t = warp - 9;
+      const int t = warp == C::PV1;
       const uint32_t v_lo = sdesc_lo(sbase + C::OFF_R, C::SUB_BYTES);
       Place vs = {1, 1, 0};
       int used = 0, g = 0;  // this lane's items and steps so far
@@ -985,7 +987,7 @@ __global__ void __launch_bounds__(384, 1)
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == C::PV0) {
     tc_fence_after();
     tmem_dealloc(tmem, C::TM_COLS);
   }
