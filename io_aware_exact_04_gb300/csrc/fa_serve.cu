@@ -68,11 +68,12 @@ constexpr int kNewBox = 16;
 // Rounding: scores, maxima, sums and O are fp32; P is rounded to the inputs' type for the product
 // with V (the tensor core takes both operands in one type), its sum is not; O is rounded once.
 //
-// Measured on one GB300: prompts of 8192 + 590 + 13 tokens, 16 heads over 2 of 128: 209 us, 1320
-// TFLOP/s, 70 % of the measured bf16 peak, the tensor pipe busy 76 % of the cycles; decoding 64
-// sequences over up to 8192 tokens, 32 heads over 8 of 128: 169 us, 6.4 TB/s, 94 % of the measured
-// copy rate; 64 trees of up to 64 nodes over up to 32768 tokens: 982-1035 us, bound by the tensor
-// pipe (80 % busy) beside memory at 70 %.
+// Measured on one GB300: prompts of 8192 + 590 + 13 tokens, 16 heads over 2 of 128: 197 us, 1400
+// TFLOP/s, 74 % of the measured bf16 peak, the tensor pipe busy 78 % of the cycles; decoding 64
+// sequences over up to 8192 tokens, 32 heads over 8 of 128: 171 us, 6.3 TB/s, 93 % of the measured
+// copy rate (116 us, 69 %, at d = 64, where the softmax of the few rows bounds it; 191 us with pages of
+// 16 tokens, sixteen copies a tile); 64 trees of up to 64 nodes over up to 32768 tokens: 1000 us, bound
+// by the tensor pipe (84 % busy) beside memory at 73 %.
 template <int D>
 struct ServeCfg {
   static constexpr int NSUB = D / 64;
