@@ -232,50 +232,75 @@ __device__ __forceinline__ int prompt_unit(const ServeArgs& a, int npt, int grid
 // The items of all prompts, longest first: level p holds the p-th items of all sequences that have
 // one, in the order of the sequences. Used by a whole warp; the item counts of the first 128
 // sequences stay in registers (read again for every item, they made the search longer than an
-// ordinary item's work).
+// ordinary item's work). A CTA asks for ascending items, so that a search goes on where the last one
+// ended; starting anew each time, 1024 prompts of up to 200 tokens took 2925 us instead of 329.
 struct PromptItems {
   static constexpr int KEPT = 4;
   const ServeArgs& a;
   int unit, total, mine[KEPT];
+  int level, end;   // the last item's level, and the items of that level and up
+  int b0, before;   // the block of sequences that holds it, and the items before that block's
   __device__ PromptItems(const ServeArgs& args, int u) : a(args), unit(u) {
+    int most = 0;
 #pragma unroll
-    for (int k = 0; k < KEPT; ++k) mine[k] = units(32 * k);
-    total = above(0);
+    for (int k = 0; k < KEPT; ++k) {
+      mine[k] = units(32 * k);
+      most = max(most, mine[k]);
+    }
+    int x = 0;
+    for (int b = 32 * KEPT; b < a.B; b += 32) {
+      const int n = units(b);
+      x += n;
+      most = max(most, n);
+    }
+#pragma unroll
+    for (int k = 0; k < KEPT; ++k) x += mine[k];
+    total = __reduce_add_sync(0xffffffffu, x);
+    level = __reduce_max_sync(0xffffffffu, most);  // above the first item's
+    end = b0 = before = 0;
   }
-  __device__ int units(int b0) const {
-    const int b = b0 + (threadIdx.x & 31);
+  __device__ int units(int from) const {
+    const int b = from + (threadIdx.x & 31);
     return b < a.B ? seq_work<false>(a, b, unit, false).units : 0;
   }
-  __device__ int above(int level) const {  // items of that level and up
+  __device__ int above(int l) const {  // items of that level and up
     int x = 0;
 #pragma unroll
-    for (int k = 0; k < KEPT; ++k) x += max(0, mine[k] - level);
-    for (int b0 = 32 * KEPT; b0 < a.B; b0 += 32) x += max(0, units(b0) - level);
+    for (int k = 0; k < KEPT; ++k) x += max(0, mine[k] - l);
+    for (int b = 32 * KEPT; b < a.B; b += 32) x += max(0, units(b) - l);
     return __reduce_add_sync(0xffffffffu, x);
   }
-  // Sequence and level of item i < total.
-  __device__ void find(int i, int* b, int* level) const {
-    int lo = 0, hi = (a.T + unit - 1) / unit;  // above(lo) > i >= above(hi)
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (above(mid) > i) lo = mid; else hi = mid;
+  // Sequence and level of item i < total, not before the last one asked for.
+  __device__ void find(int i, int* b, int* l) {
+    if (i >= end) {  // a lower level: doubling steps down to above(lo) > i >= above(hi), then halves
+      int hi = level, lo = level, n_hi = end, n_lo = end;
+      for (int step = 1; n_lo <= i && lo > 0; step *= 2) {
+        hi = lo, n_hi = n_lo;
+        lo = max(0, lo - step);
+        n_lo = above(lo);
+      }
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1, n = above(mid);
+        if (n > i) lo = mid, n_lo = n; else hi = mid, n_hi = n;
+      }
+      level = lo, end = n_lo;
+      b0 = 0, before = n_hi;
     }
-    int left = i - above(lo + 1);
-    *level = lo;
-    for (int b0 = 0; b0 < a.B; b0 += 32) {
+    *l = level;
+    for (; b0 < a.B; b0 += 32) {
       int u = 0;
 #pragma unroll
       for (int k = 0; k < KEPT; ++k)
         if (b0 == 32 * k) u = mine[k];
       if (b0 >= 32 * KEPT) u = units(b0);
-      unsigned m = __ballot_sync(0xffffffffu, u > lo);
+      unsigned m = __ballot_sync(0xffffffffu, u > level);
       const int k = __popc(m);
-      if (left < k) {
-        for (; left; --left) m &= m - 1;
+      if (i - before < k) {
+        for (int left = i - before; left; --left) m &= m - 1;
         *b = b0 + __ffs(m) - 1;
         return;
       }
-      left -= k;
+      before += k;
     }
   }
 };
@@ -520,7 +545,7 @@ __global__ void __launch_bounds__(384, 1)
       }
     } else {
       const int unit = prompt_unit(a, npt, gridDim.x, blockIdx.x == 0);
-      const PromptItems items_of(a, unit);
+      PromptItems items_of(a, unit);
       for (long long round = 0; ok; ++round) {
         const int G = gridDim.x, c = blockIdx.x;
         const long long i = round * G + ((round & 1) ? G - 1 - c : c);

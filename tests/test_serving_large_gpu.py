@@ -1,8 +1,11 @@
-"""The serving operators where an element's offset passes 31 and 32 bits, and inside CUDA graphs.
+"""The serving operators where an element's offset passes 31 and 32 bits, with many sequences, and inside
+CUDA graphs.
 
 Where the data lies does not enter the arithmetic: the same tokens in other pages, or in rows
 further apart, give the same bits.
 """
+
+import random
 
 import pytest
 import torch
@@ -145,3 +148,22 @@ def test_pool_replayed_with_other_slots(gpu):
         for x, y in zip(infos, want):
             assert torch.equal(x, y)
         assert plain[2].tolist() == new
+
+
+@pytest.mark.parametrize("count,Hq,Hkv,d", [(129, 2, 1, 64), (300, 6, 3, 128), (1000, 1, 1, 64), (200, 20, 5, 128)])
+def test_many_sequences(gpu, count, Hq, Hkv, d):
+    """Hundreds of sequences: mostly short, some empty, a few long."""
+    r = random.Random(count)
+    lens = [r.choice([0, 1, r.randrange(2, 40), r.randrange(2, 40), 129]) for _ in range(count)]
+    for b in (0, count // 2, count - 1):
+        lens[b] = r.randrange(700, 900)
+    T = sum(lens)
+    q, k, v = rows_like("fused", T, Hq, Hkv, d, torch.bfloat16, gpu, seed=count)
+    cu = ints(ref.offsets(lens), gpu)
+    o, lse = api.forward_prompt(q, k, v, cu)
+    ok(gpu)
+    ref.assert_close(o, lse, ref.forward(q, k, v, lens, d ** -0.5), T)
+    c = Cache([r.choice([0, r.randrange(300)]) for _ in lens], Hkv, 32, d, torch.bfloat16, gpu)
+    o, lse = api.forward_tree(q, k, v, c.kv[0], c.kv[1], c.table, c.lens, cu)
+    ok(gpu)
+    ref.assert_close(o, lse, ref.forward(q, k, v, lens, d ** -0.5, ctx=c.ctx), T)
