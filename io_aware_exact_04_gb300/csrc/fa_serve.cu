@@ -774,122 +774,26 @@ __global__ void __launch_bounds__(384, 1)
       };
       const int stride = dual ? 2 : 1;
       int js = it.j0 + (dual ? t : 0), hs = 0, halves = steps_in(it, t, js);  // the step's key tile and half
-      for (int s = 0; s < steps; ++s, ++hs) {
-        if (hs == halves) {
+      constexpr int KT = C::KT;
+      auto begin_step = [&](int s) {  // its key tile and half; S is there
+        if (C::HPT == 1 ? s > 0 && ++hs == halves : hs == halves) {
           hs = 0;
           js += stride;
           halves = steps_in(it, t, js);
         }
-        const int u = C::buf(before + s);
-        if (!(ok = wait_phase(BAR(C::S_FULL + 2 * t + u), C::phase(before + s), st, SITE_SW_S_FULL))) break;
-        if (!any) {  // no row here: P stays what it is, its rows of O are nobody's
-          __syncwarp();
-          if (C::SEP_P) {
-            if (lane == 0) mbar_arrive(BAR(C::S_FREE + t));
-          }
-          // d = 64: S of this tile may be there before the other warps have written P of the one
-          // before: an arrival now would count for that one
-          if (C::SEP_P && s > 0 && !(ok = wait_pv(t, before + s - 1))) break;
-          if (lane == 0) mbar_arrive(BAR(C::P_READY + 2 * t + u));
-          continue;
-        }
-        tc_fence_after();
-        constexpr int KT = C::KT;
-        float sv[KT];
-        {
-          uint32_t r[KT / 32][32];
-#pragma unroll
-          for (int q = 0; q < KT / 32; ++q) tmem_ld32(tmem + lane_off + C::tm_s(t, u) + q * 32, r[q]);
-          tmem_wait_ld();
-#pragma unroll
-          for (int q = 0; q < KT / 32; ++q)
-#pragma unroll
-            for (int x = 0; x < 32; ++x) sv[q * 32 + x] = __uint_as_float(r[q][x]);
-        }
+        return wait_phase(BAR(C::S_FULL + 2 * t + C::buf(before + s)), C::phase(before + s), st, SITE_SW_S_FULL);
+      };
+      auto s_in_registers = [&] {
         if (C::SEP_P) {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(BAR(C::S_FREE + t));
         }
-        if (tree && js >= it.nc) {
-          const int k0 = (js - it.nc) * 128 + hs * KT;
-          const uint32_t* words = a.mask + (long long)(it.row0 + tok) * a.words;
-          uint32_t w[KT / 32];
-#pragma unroll
-          for (int q = 0; q < KT / 32; ++q) {
-            const int left = it.n - k0 - 32 * q;  // nodes from this word on
-            w[q] = valid && left > 0 && (k0 >> 5) + q < a.words ? words[(k0 >> 5) + q] : 0u;
-            if (left > 0 && left < 32) w[q] &= (1u << left) - 1;
-          }
-#pragma unroll
-          for (int x = 0; x < KT; ++x)
-            if (!(w[x >> 5] >> (x & 31) & 1)) sv[x] = -INFINITY;
-        } else {
-          // keys [0, lim) of the step are seen, by the warp's first row fewest
-          const int k0 = js * 128 + hs * KT - (js < it.nc ? it.L : it.nc * 128);
-          if (js < it.nc ? k0 > -KT : min(it.n, tok_first + 1) < k0 + KT) {
-            const int lim = js < it.nc ? -k0 : min(it.n, tok + 1) - k0;
-#pragma unroll
-            for (int x = 0; x < KT; ++x)
-              if (x >= lim) sv[x] = -INFINITY;
-          }
-        }
-        float pm[4];
-#pragma unroll
-        for (int y = 0; y < 4; ++y) pm[y] = sv[y];
-#pragma unroll
-        for (int x = 4; x < KT - 4; x += 8)
-#pragma unroll
-          for (int y = 0; y < 4; ++y) pm[y] = fmax3(pm[y], sv[x + 2 * y], sv[x + 2 * y + 1]);
-        const float mx = fmax3(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3]),
-                               fmax3(sv[KT - 4], sv[KT - 3], fmaxf(sv[KT - 2], sv[KT - 1])));
-        const float m_tile = mx * sl2;
-        // the reference maximum moves only when it grows by more than 2^8; O and l share it
-        float f = 1.f;
-        bool rescale_warp = false;
-        if (s == 0) {
-          m_run = m_tile;
-        } else {
-          const bool grow = valid && m_tile > m_run + 8.0f;
-          rescale_warp = __any_sync(0xffffffffu, grow);
-          if (grow) {
-            f = ex2_approx(m_run - m_tile);
-            m_run = m_tile;
-          }
-        }
-        const float base = (m_run == -INFINITY) ? 0.f : m_run;
-        const uint64_t sl2x2 = f2_pack(sl2, sl2), nbase2 = f2_pack(-base, -base);
-        uint64_t ps2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
-        uint32_t pk[KT / 32][16];
-        const uint32_t tP = tmem + lane_off + C::tm_p(t, u);
-#pragma unroll
-        for (int q = 0; q < KT / 32; ++q) {
-#pragma unroll
-          for (int x = 0; x < 16; ++x) {
-            float x0, x1;
-            f2_unpack(f2_fma(f2_pack(sv[q * 32 + 2 * x], sv[q * 32 + 2 * x + 1]), sl2x2, nbase2), x0, x1);
-            const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-            ps2[x & 1] = f2_add(ps2[x & 1], f2_pack(p0, p1));
-            pk[q][x] = pack2<F16>(p0, p1);
-          }
-          if (C::SEP_P && q == 1) {
-            if (s > 0) {  // PV of the tile before has read P (across items its epilogue waited for that)
-              if (!(ok = wait_pv(t, before + s - 1))) break;
-              tc_fence_after();
-            }
-            tmem_st16(tP, pk[0]);
-            tmem_st16(tP + 16, pk[1]);
-          }
-          if (!C::SEP_P || q >= 2) tmem_st16(tP + q * 16, pk[q]);
-        }
-        if (!ok) break;
-        float ps[4];
-        f2_unpack(ps2[0], ps[0], ps[1]);
-        f2_unpack(ps2[1], ps[2], ps[3]);
-        l_run = l_run * f + ((ps[0] + ps[1]) + (ps[2] + ps[3]));
-        if (rescale_warp) {
+      };
+      auto end_step = [&](int s, bool rescale, float f) {  // P is on its way; O of row `lane` takes the factor f
+        if (rescale) {
           if (!C::SEP_P) {
-            if (!(ok = wait_pv(t, before + s - 1))) break;
+            if (!wait_pv(t, before + s - 1)) return false;
             tc_fence_after();
           }
           const uint32_t tO = tmem + lane_off + C::tm_o(t);
@@ -906,7 +810,221 @@ __global__ void __launch_bounds__(384, 1)
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(BAR(C::P_READY + 2 * t + u));
+        if (lane == 0) mbar_arrive(BAR(C::P_READY + 2 * t + C::buf(before + s)));
+        return true;
+      };
+      if (!(PAGED && any && it.n <= 16 && it.n * a.G <= 16)) {
+        for (int s = 0; s < steps; ++s, hs += C::HPT > 1) {
+          const int u = C::buf(before + s);
+          if (!(ok = begin_step(s))) break;
+          if (!any) {  // no row here: P stays what it is, its rows of O are nobody's
+            __syncwarp();
+            if (C::SEP_P) {
+              if (lane == 0) mbar_arrive(BAR(C::S_FREE + t));
+            }
+            // d = 64: S of this tile may be there before the other warps have written P of the one
+            // before: an arrival now would count for that one
+            if (C::SEP_P && s > 0 && !(ok = wait_pv(t, before + s - 1))) break;
+            if (lane == 0) mbar_arrive(BAR(C::P_READY + 2 * t + u));
+            continue;
+          }
+          tc_fence_after();
+          float f = 1.f;
+          bool rescale = false;
+          float sv[KT];
+          {
+            uint32_t r[KT / 32][32];
+#pragma unroll
+            for (int q = 0; q < KT / 32; ++q) tmem_ld32(tmem + lane_off + C::tm_s(t, u) + q * 32, r[q]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int q = 0; q < KT / 32; ++q)
+#pragma unroll
+              for (int x = 0; x < 32; ++x) sv[q * 32 + x] = __uint_as_float(r[q][x]);
+          }
+          s_in_registers();
+          if (tree && js >= it.nc) {
+            const int k0 = (js - it.nc) * 128 + hs * KT;
+            const uint32_t* words = a.mask + (long long)(it.row0 + tok) * a.words;
+            uint32_t w[KT / 32];
+#pragma unroll
+            for (int q = 0; q < KT / 32; ++q) {
+              const int left = it.n - k0 - 32 * q;  // nodes from this word on
+              w[q] = valid && left > 0 && (k0 >> 5) + q < a.words ? words[(k0 >> 5) + q] : 0u;
+              if (left > 0 && left < 32) w[q] &= (1u << left) - 1;
+            }
+#pragma unroll
+            for (int x = 0; x < KT; ++x)
+              if (!(w[x >> 5] >> (x & 31) & 1)) sv[x] = -INFINITY;
+          } else {
+            // keys [0, lim) of the step are seen, by the warp's first row fewest
+            const int k0 = js * 128 + hs * KT - (js < it.nc ? it.L : it.nc * 128);
+            if (js < it.nc ? k0 > -KT : min(it.n, tok_first + 1) < k0 + KT) {
+              const int lim = js < it.nc ? -k0 : min(it.n, tok + 1) - k0;
+#pragma unroll
+              for (int x = 0; x < KT; ++x)
+                if (x >= lim) sv[x] = -INFINITY;
+            }
+          }
+          float pm[4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) pm[y] = sv[y];
+#pragma unroll
+          for (int x = 4; x < KT - 4; x += 8)
+#pragma unroll
+            for (int y = 0; y < 4; ++y) pm[y] = fmax3(pm[y], sv[x + 2 * y], sv[x + 2 * y + 1]);
+          const float mx = fmax3(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3]),
+                                 fmax3(sv[KT - 4], sv[KT - 3], fmaxf(sv[KT - 2], sv[KT - 1])));
+          const float m_tile = mx * sl2;
+          // the reference maximum moves only when it grows by more than 2^8; O and l share it
+          if (s == 0) {
+            m_run = m_tile;
+          } else {
+            const bool grow = valid && m_tile > m_run + 8.0f;
+            rescale = __any_sync(0xffffffffu, grow);
+            if (grow) {
+              f = ex2_approx(m_run - m_tile);
+              m_run = m_tile;
+            }
+          }
+          const float base = (m_run == -INFINITY) ? 0.f : m_run;
+          const uint64_t sl2x2 = f2_pack(sl2, sl2), nbase2 = f2_pack(-base, -base);
+          uint64_t ps2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+          uint32_t pk[KT / 32][16];
+          const uint32_t tP = tmem + lane_off + C::tm_p(t, u);
+#pragma unroll
+          for (int q = 0; q < KT / 32; ++q) {
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+              float x0, x1;
+              f2_unpack(f2_fma(f2_pack(sv[q * 32 + 2 * x], sv[q * 32 + 2 * x + 1]), sl2x2, nbase2), x0, x1);
+              const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+              ps2[x & 1] = f2_add(ps2[x & 1], f2_pack(p0, p1));
+              pk[q][x] = pack2<F16>(p0, p1);
+            }
+            if (C::SEP_P && q == 1) {
+              if (s > 0) {  // PV of the tile before has read P (across items its epilogue waited for that)
+                if (!(ok = wait_pv(t, before + s - 1))) break;
+                tc_fence_after();
+              }
+              tmem_st16(tP, pk[0]);
+              tmem_st16(tP + 16, pk[1]);
+            }
+            if (!C::SEP_P || q >= 2) tmem_st16(tP + q * 16, pk[q]);
+          }
+          if (!ok) break;
+          float ps[4];
+          f2_unpack(ps2[0], ps[0], ps[1]);
+          f2_unpack(ps2[1], ps[2], ps[3]);
+          l_run = l_run * f + ((ps[0] + ps[1]) + (ps[2] + ps[3]));
+          if (!(ok = end_step(s, rescale, f))) break;
+        }
+      } else {
+        // Decoding and small drafts: up to 16 rows, in the first warp's lanes. A thread of it takes a quarter
+        // of the keys of rows lane / 4 and lane / 4 + 8 rather than all of row `lane`: with the exponentials
+        // of 32 rows a warp, decoding 512 sequences of up to 500 tokens took 332 us at d = 64 (12 heads)
+        // instead of 255, and 217 at d = 128 (32 / 8 heads) instead of 209.
+        const int tok_few[2] = {(lane >> 2) / a.G, ((lane >> 2) + 8) / a.G};
+        float m_few[2] = {-INFINITY, -INFINITY}, l_few[2] = {0.f, 0.f};
+        for (int s = 0; s < steps; ++s, hs += C::HPT > 1) {
+          const int u = C::buf(before + s);
+          if (!(ok = begin_step(s))) break;
+          tc_fence_after();
+          uint32_t r[KT / 64][32];
+#pragma unroll
+          for (int q = 0; q < KT / 64; ++q) tmem_ld_rows16(tmem + lane_off + C::tm_s(t, u) + q * 64, r[q]);
+          tmem_wait_ld();
+          s_in_registers();
+          uint32_t pk[KT / 64][16];
+          float fh[2] = {1.f, 1.f};
+          bool grow = false;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (h == 1 && it.n * a.G <= 8) {
+#pragma unroll
+              for (int y = 0; y < KT / 8; ++y) pk[y >> 3][2 * (y & 7) + 1] = 0;
+              break;
+            }
+            float x[KT / 4];
+#pragma unroll
+            for (int y = 0; y < KT / 8; ++y) {
+              x[2 * y] = __uint_as_float(r[y >> 3][4 * (y & 7) + 2 * h]);
+              x[2 * y + 1] = __uint_as_float(r[y >> 3][4 * (y & 7) + 2 * h + 1]);
+            }
+            const int token = tok_few[h], c0 = 2 * (lane & 3);
+            if (js >= it.nc) {  // at most 16 new tokens
+              uint32_t seen = tree ? (token < it.n ? a.mask[(long long)(it.row0 + token) * a.words] : 0u)
+                                   : (2u << min(token, 30)) - 1;
+              seen &= (1u << it.n) - 1;
+#pragma unroll
+              for (int y = 0; y < KT / 8; ++y)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                  if (y >= 4 || !(seen >> (8 * y + c0 + e) & 1)) x[2 * y + e] = -INFINITY;
+            } else if (it.L - js * 128 - hs * KT < KT) {
+              const int lim = it.L - js * 128 - hs * KT - c0;
+#pragma unroll
+              for (int y = 0; y < KT / 8; ++y)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                  if (8 * y + e >= lim) x[2 * y + e] = -INFINITY;
+            }
+            float pm[2] = {x[0], x[1]};
+#pragma unroll
+            for (int y = 2; y < KT / 4 - 2; y += 4)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) pm[e] = fmax3(pm[e], x[y + 2 * e], x[y + 2 * e + 1]);
+            float mx = fmax3(fmaxf(pm[0], pm[1]), x[KT / 4 - 2], x[KT / 4 - 1]);
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            const float m_tile = mx * sl2;
+            float& m = m_few[h];
+            if (s == 0) {
+              m = m_tile;
+            } else if (token < it.n && m_tile > m + 8.0f) {
+              grow = true;
+              fh[h] = ex2_approx(m - m_tile);
+              m = m_tile;
+            }
+            const float base = m == -INFINITY ? 0.f : m;
+            const uint64_t sl2x2 = f2_pack(sl2, sl2), nbase2 = f2_pack(-base, -base);
+            uint64_t ps2 = f2_pack(0.f, 0.f);
+#pragma unroll
+            for (int y = 0; y < KT / 8; ++y) {
+              float x0, x1;
+              f2_unpack(f2_fma(f2_pack(x[2 * y], x[2 * y + 1]), sl2x2, nbase2), x0, x1);
+              const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+              ps2 = f2_add(ps2, f2_pack(p0, p1));
+              pk[y >> 3][2 * (y & 7) + h] = pack2<F16>(p0, p1);
+            }
+            float ps0, ps1;
+            f2_unpack(ps2, ps0, ps1);
+            l_few[h] = l_few[h] * fh[h] + (ps0 + ps1);
+          }
+          if (C::SEP_P && s > 0) {
+            if (!(ok = wait_pv(t, before + s - 1))) break;
+            tc_fence_after();
+          }
+#pragma unroll
+          for (int q = 0; q < KT / 64; ++q) tmem_st_rows16(tmem + lane_off + C::tm_p(t, u) + q * 32, pk[q]);
+          const bool rescale = __any_sync(0xffffffffu, grow);
+          float f = 1.f;
+          if (rescale) {
+            const float fa = __shfl_sync(0xffffffffu, fh[0], 4 * (lane & 7));
+            const float fb = __shfl_sync(0xffffffffu, fh[1], 4 * (lane & 7));
+            f = lane < 8 ? fa : fb;
+          }
+          if (!(ok = end_step(s, rescale, f))) break;
+        }
+        // maximum and sum of row `lane`
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float l = l_few[h];
+          l += __shfl_xor_sync(0xffffffffu, l, 1);
+          l += __shfl_xor_sync(0xffffffffu, l, 2);
+          const float mr = __shfl_sync(0xffffffffu, m_few[h], 4 * (lane & 7)), lr = __shfl_sync(0xffffffffu, l, 4 * (lane & 7));
+          if ((lane >> 3) == h) m_run = mr, l_run = lr;
+        }
       }
       if (ok && steps > 0) ok = wait_pv(t, before + steps - 1);
       if (!ok) break;

@@ -12,7 +12,7 @@ import torch
 
 import serving_ref as ref
 from io_aware_exact_04_gb300 import api
-from test_serving_gpu import Cache, ints, normal, ok, rows_like
+from test_serving_gpu import Cache, ints, masks_of, normal, ok, rows_like
 
 pytestmark = pytest.mark.gpu
 
@@ -167,3 +167,33 @@ def test_many_sequences(gpu, count, Hq, Hkv, d):
     o, lse = api.forward_tree(q, k, v, c.kv[0], c.kv[1], c.table, c.lens, cu)
     ok(gpu)
     ref.assert_close(o, lse, ref.forward(q, k, v, lens, d ** -0.5, ctx=c.ctx), T)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("nodes,Hq,Hkv", [(1, 7, 1), (1, 16, 2), (1, 9, 1), (8, 2, 2), (9, 1, 1), (5, 3, 1), (16, 1, 1), (17, 1, 1),
+                                          (4, 16, 4), (1, 17, 1), (2, 16, 2)])
+def test_few_rows(gpu, nodes, Hq, Hkv, d, dtype):
+    """Around 8 and 16 rows a key/value head; scores that grow along the keys, so that the running
+    maximum moves; trees and chains."""
+    lens = [0, 1, 63, 64, 65, 127, 129, 400, 1000]
+    T = nodes * len(lens)
+    q, k, v = rows_like("fused", T, Hq, Hkv, d, dtype, gpu, seed=nodes)
+    c = Cache(lens, Hkv, 32, d, dtype, gpu, seed=d)
+    for b, n in enumerate(lens):  # keys grow tenfold along a sequence
+        grown = (c.rows[b][0].float() * torch.linspace(0.5, 5, max(n, 1), device=gpu)[:n, None, None]).to(dtype)
+        c.rows[b] = torch.stack([grown, c.rows[b][1]])
+        for j in range(-(-n // 32)):
+            part = grown[32 * j:32 * j + 32]
+            c.kv[0, int(c.table[b, j]), :, :part.shape[0]] = part.transpose(0, 1)
+    cu = ints(ref.offsets([nodes] * len(lens)), gpu)
+    o, lse = api.forward_tree(q, k, v, c.kv[0], c.kv[1], c.table, c.lens, cu)
+    ok(gpu)
+    ref.assert_close(o, lse, ref.forward(q, k, v, [nodes] * len(lens), d ** -0.5, ctx=c.ctx), T)
+    for kind in ("tree", "random"):
+        words, bits, _ = masks_of(kind, [nodes] * len(lens), 3)
+        mask = torch.cat([ref.pack_bits(s, words) for s in bits]).to(gpu)
+        o, lse = api.forward_tree(q, k, v, c.kv[0], c.kv[1], c.table, c.lens, cu, mask=mask)
+        ok(gpu)
+        ref.assert_close(o, lse, ref.forward(q, k, v, [nodes] * len(lens), d ** -0.5, ctx=c.ctx,
+                                             seen_nodes=lambda b, n: bits[b][:, :n]), T)
