@@ -139,16 +139,14 @@ struct SeqWork {
   long long tiles;  // all heads and units, each counted with the nk tiles of the last one
 };
 template <bool PAGED>
-__device__ __forceinline__ SeqWork seq_work(const ServeArgs& a, int b, int unit, bool record) {
+__device__ __forceinline__ SeqWork seq_sizes(const ServeArgs& a, int lo, int hi, int len, int unit, bool record) {
   SeqWork w;
-  const int lo = a.cu[b], hi = a.cu[b + 1];
   w.row0 = min(max(lo, 0), a.T);
   const int end = min(max(hi, w.row0), a.T);
   if (record && (w.row0 != lo || end != hi)) record_check(a.status, SITE_S_OFFSETS);
   w.n = end - w.row0;
   w.L = 0;
   if (PAGED && w.n > 0) {
-    const int len = a.lens[b];
     w.L = min(max(len, 0), a.table_width << a.page_shift);
     if (record && w.L != len) record_check(a.status, SITE_S_LENGTH);
   }
@@ -158,52 +156,74 @@ __device__ __forceinline__ SeqWork seq_work(const ServeArgs& a, int b, int unit,
   w.tiles = (long long)w.units * a.Hkv * w.nk;
   return w;
 }
+template <bool PAGED>
+__device__ __forceinline__ SeqWork seq_work(const ServeArgs& a, int b, int unit, bool record) {
+  return seq_sizes<PAGED>(a, a.cu[b], a.cu[b + 1], PAGED ? a.lens[b] : 0, unit, record);
+}
 
 __device__ __forceinline__ long long warp_sum(long long x) {
   for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
 }
 
-// Trees: the run of key tiles of CTA c, by a whole warp.
+// Trees: the run of key tiles of CTA c, by a whole warp. Each lane counts the tiles of `chunk` sequences
+// that follow each other, four sequences' loads at a time, so that the search below looks at a lane's
+// sequences only (a block of 32 sequences after the other, both took up to 15 us for 512 sequences).
 struct ServeRuns {
   long long total, base;
   int ctas, rest;        // CTAs with work; the first `rest` of them take a tile more
-  long long mine;        // this lane's sequence among the first 32: its tiles
+  long long mine;        // this lane's tiles
+  int chunk;
   __device__ long long start(int c) const { return base * c + min(c, rest); }
 };
 __device__ __forceinline__ ServeRuns serve_runs(const ServeArgs& a, int unit, int grid, bool record) {
   ServeRuns r;
   const int lane = threadIdx.x & 31;
-  r.mine = lane < a.B ? seq_work<true>(a, lane, unit, record).tiles : 0;
-  long long x = r.mine;
-  for (int b = lane + 32; b < a.B; b += 32) x += seq_work<true>(a, b, unit, record).tiles;
-  r.total = warp_sum(x);
+  r.chunk = (a.B + 31) >> 5;
+  r.mine = 0;
+  const int end = min(a.B, (lane + 1) * r.chunk);
+  for (int b = lane * r.chunk; b < end; b += 4) {
+    int at[5], len[4];
+#pragma unroll
+    for (int k = 0; k < 5; ++k) at[k] = a.cu[min(b + k, end)];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) len[k] = a.lens[min(b + k, end - 1)];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (b + k < end) r.mine += seq_sizes<true>(a, at[k], at[k + 1], len[k], unit, record).tiles;
+  }
+  r.total = warp_sum(r.mine);
   r.ctas = r.total < (long long)grid * kMinTiles ? max(1, ((int)r.total + kMinTiles - 1) / kMinTiles) : grid;
   r.base = r.total < (1LL << 31) ? (int)r.total / r.ctas : r.total / r.ctas;  // the short division costs a fifth
   r.rest = (int)(r.total - r.base * r.ctas);
   return r;
 }
+// The lane whose own tiles hold tile `pos` of all, and their first one; 32: past the end.
+__device__ __forceinline__ int lane_of(long long mine, long long pos, long long* first) {
+  const int lane = threadIdx.x & 31;
+  long long incl = mine;
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  const unsigned past = __ballot_sync(0xffffffffu, *first + incl > pos);
+  const int k = past ? __ffs(past) - 1 : 32;
+  *first += __shfl_sync(0xffffffffu, k < 32 ? incl - mine : incl, k < 32 ? k : 31);
+  return k;
+}
 // The sequence that tile `pos` of all belongs to, and its first tile; by a whole warp. pos < total.
 __device__ __forceinline__ int serve_seek(const ServeArgs& a, int unit, const ServeRuns& runs, long long pos,
                                           long long* first) {
-  const int lane = threadIdx.x & 31;
-  long long base = 0;
-  for (int b0 = 0; b0 < a.B; b0 += 32) {
-    const long long mine = b0 == 0 ? runs.mine : b0 + lane < a.B ? seq_work<true>(a, b0 + lane, unit, false).tiles : 0;
-    long long incl = mine;
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
-    }
-    const unsigned past = __ballot_sync(0xffffffffu, base + incl > pos);
-    if (past) {
-      const int k = __ffs(past) - 1;
-      *first = base + __shfl_sync(0xffffffffu, incl - mine, k);
-      return b0 + k;
-    }
-    base += __shfl_sync(0xffffffffu, incl, 31);
+  *first = 0;
+  const int k = lane_of(runs.mine, pos, first);
+  if (k == 32) return a.B;
+  if (runs.chunk == 1) return k;
+  const int end = min(a.B, (k + 1) * runs.chunk);
+  for (int b0 = k * runs.chunk; b0 < end; b0 += 32) {
+    const int b = b0 + (threadIdx.x & 31);
+    const int x = lane_of(b < end ? seq_work<true>(a, b, unit, false).tiles : 0, pos, first);
+    if (x < 32) return b0 + x;
   }
-  *first = base;
   return a.B;
 }
 
@@ -220,10 +240,20 @@ __device__ __forceinline__ int tiles_of(const SeqWork& w, int u, int npt, bool t
 __device__ __forceinline__ int prompt_unit(const ServeArgs& a, int npt, int grid, bool record) {
   long long tiles = 0;
   int longest = 0;
-  for (int b = threadIdx.x & 31; b < a.B; b += 32) {
-    const SeqWork w = seq_work<false>(a, b, 2 * npt, record);
-    tiles += (w.tiles + (long long)w.units * a.Hkv) / 2;  // item p of a sequence has about (p + 1) nk / units
-    longest = max(longest, w.nk);
+  for (int b0 = threadIdx.x & 31; b0 < a.B; b0 += 128) {  // four sequences' loads at a time
+    int lo[4], hi[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int b = min(b0 + 32 * k, a.B - 1);
+      lo[k] = a.cu[b], hi[k] = a.cu[b + 1];
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (b0 + 32 * k >= a.B) break;
+      const SeqWork w = seq_sizes<false>(a, lo[k], hi[k], 0, 2 * npt, record);
+      tiles += (w.tiles + (long long)w.units * a.Hkv) / 2;  // item p of a sequence has about (p + 1) nk / units
+      longest = max(longest, w.nk);
+    }
   }
   tiles = warp_sum(tiles);
   longest = __reduce_max_sync(0xffffffffu, longest);
@@ -248,6 +278,7 @@ struct PromptItems {
       most = max(most, mine[k]);
     }
     int x = 0;
+#pragma unroll 4
     for (int b = 32 * KEPT; b < a.B; b += 32) {
       const int n = units(b);
       x += n;
@@ -267,6 +298,7 @@ struct PromptItems {
     int x = 0;
 #pragma unroll
     for (int k = 0; k < KEPT; ++k) x += max(0, mine[k] - l);
+#pragma unroll 4
     for (int b = 32 * KEPT; b < a.B; b += 32) x += max(0, units(b) - l);
     return __reduce_add_sync(0xffffffffu, x);
   }
