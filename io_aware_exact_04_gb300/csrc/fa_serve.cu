@@ -458,6 +458,15 @@ __global__ void __launch_bounds__(384, 1)
     // Loads the item's query tiles and its key tiles [j0, j0 + cnt).
     auto run_item = [&](const ServeItem& it, int b) {
       if (!publish(it)) return false;
+      // page ids of a tile: lane (box r, column block c) = r NSUB + c
+      const int prow = min(1 << a.page_shift, 128);  // rows of a page's box
+      const int r = lane / C::NSUB, c = lane % C::NSUB;
+      auto page_of = [&](int j) {
+        const int pg = (j * 128 + r * prow) >> a.page_shift;
+        const bool there = j < it.j0 + it.cnt && j < it.nc && r * prow < 128 && j * 128 + r * prow < it.L;
+        return there ? a.table[b * a.table_stride + pg] : 0;
+      };
+      int id = PAGED ? page_of(it.j0) : 0;
       const int nq = (it.flags & ITEM_DUAL) ? 1 : 2;
       for (int t = 0; t < nq; ++t, ++uq) {
         const uint32_t qf = BAR(C::Q_FULL + (uq & 1));
@@ -469,15 +478,6 @@ __global__ void __launch_bounds__(384, 1)
           tma_load_3d(dst + lane * C::SUB_BYTES, &tm_q, lane * 64, it.kvh * a.G, it.row0 + it.tok0 + t * npt, qf);
         __syncwarp();
       }
-      // page ids of a tile: lane (box r, column block c) = r NSUB + c
-      const int prow = min(1 << a.page_shift, 128);  // rows of a page's box
-      const int r = lane / C::NSUB, c = lane % C::NSUB;
-      auto page_of = [&](int j) {
-        const int pg = (j * 128 + r * prow) >> a.page_shift;
-        const bool there = j < it.j0 + it.cnt && j < it.nc && r * prow < 128 && j * 128 + r * prow < it.L;
-        return there ? a.table[b * a.table_stride + pg] : 0;
-      };
-      int id = PAGED ? page_of(it.j0) : 0;
       for (int j = it.j0; j < it.j0 + it.cnt; ++j) {
         const int id_next = PAGED ? page_of(j + 1) : 0;
         const bool cached = PAGED && j < it.nc;
@@ -552,11 +552,17 @@ __global__ void __launch_bounds__(384, 1)
         int b = serve_seek(a, unit, runs, pos, &first);
         while (ok && pos < end) {
           const SeqWork w = seq_work<PAGED>(a, b, unit, false);
+          // the first item may be cut; from then on they start with their first tile
+          const long long at = pos - first;
+          const int q = at < (1LL << 31) ? (int)at / max(w.nk, 1) : (int)(at / w.nk);
+          int p = q / a.Hkv, kvh = q - p * a.Hkv, j0 = (int)(at - (long long)q * w.nk);
+          bool again = false;  // the last item was whole, and this one differs in its head only
           while (ok && pos < end && pos - first < w.tiles) {
-            const long long at = pos - first;
-            const int q = at < (1LL << 31) ? (int)at / w.nk : (int)(at / w.nk), j0 = (int)(at - (long long)q * w.nk);
             const int j1 = (int)min((long long)w.nk, j0 + (end - pos));
-            make_item(w, unit, q % a.Hkv, q / a.Hkv, j0, j1, &it);
+            if (again && j1 == w.nk)
+              it.kvh = kvh;
+            else
+              make_item(w, unit, kvh, p, j0, j1, &it);
             if (j0 > 0 && it.cnt > 0 && runs.start(blockIdx.x - 1) <= pos - j0) {
               // (the first item only) how many CTAs, this one included, hold later parts of it
               const long long end_of_item = pos + it.cnt_all - j0;
@@ -566,6 +572,9 @@ __global__ void __launch_bounds__(384, 1)
             }
             if (it.cnt > 0) ok = run_item(it, b);
             pos += j1 - j0;
+            again = j0 == 0 && j1 == w.nk;
+            j0 = 0;
+            if (++kvh == a.Hkv) kvh = 0, ++p, again = false;
           }
           first += w.tiles;
           ++b;
