@@ -458,9 +458,9 @@ __global__ void __launch_bounds__(384, 1)
     // Loads the item's query tiles and its key tiles [j0, j0 + cnt).
     auto run_item = [&](const ServeItem& it, int b) {
       if (!publish(it)) return false;
-      // page ids of a tile: lane (box r, column block c) = r NSUB + c
+      // page ids of a tile: lane (box r, column block c) = r NSUB + c, and lane 16 + r NSUB + c
       const int prow = min(1 << a.page_shift, 128);  // rows of a page's box
-      const int r = lane / C::NSUB, c = lane % C::NSUB;
+      const int r = (lane & 15) / C::NSUB, c = lane % C::NSUB;
       auto page_of = [&](int j) {
         const int pg = (j * 128 + r * prow) >> a.page_shift;
         const bool there = j < it.j0 + it.cnt && j < it.nc && r * prow < 128 && j * 128 + r * prow < it.L;
@@ -478,7 +478,40 @@ __global__ void __launch_bounds__(384, 1)
           tma_load_3d(dst + lane * C::SUB_BYTES, &tm_q, lane * 64, it.kvh * a.G, it.row0 + it.tok0 + t * npt, qf);
         __syncwarp();
       }
-      for (int j = it.j0; j < it.j0 + it.cnt; ++j) {
+      int j = it.j0;
+      // With few rows and small boxes this warp is the slowest: K and V of a tile in one go then, a lane for
+      // each box (decoding 64 sequences of up to 8192 tokens took 112 us a slot at a time and takes 100 at
+      // d = 64, 190 and 177 at d = 128 with pages of 16 tokens). Few tiles an item gain nothing by it, nor
+      // do larger boxes at d = 128, where the ring has five slots and is full.
+      if (PAGED && (D == 64 || a.page_shift == 4) && it.cnt >= 8 && it.n <= 16 && it.n * a.G <= 16) {
+        for (; j < min(it.j0 + it.cnt, it.nc); ++j, e += 2) {
+          const int id_next = page_of(j + 1), boxes = (min(128, it.L - j * 128) + prow - 1) / prow;
+          const bool mine = (lane & 15) < boxes * C::NSUB;
+          int page = id;
+          if (mine && (id < 0 || id >= a.n_pages)) {
+            record_check(a.status, SITE_S_PAGE);
+            page = a.n_pages;
+          }
+          const int s0 = e % C::NSLOT, s1 = (e + 1) % C::NSLOT, s = lane < 16 ? s0 : s1;
+          if (!wait_phase(BAR(C::EMPTY + s0), ((e / C::NSLOT) & 1) ^ 1, st, SITE_SW_EMPTY) ||
+              !wait_phase(BAR(C::EMPTY + s1), (((e + 1) / C::NSLOT) & 1) ^ 1, st, SITE_SW_EMPTY))
+            return false;
+          if (elect_one()) {
+            *loading = e + 2;
+            mbar_arrive_expect_tx(BAR(C::FULL + s0), (uint32_t)(boxes * prow * 128 * C::NSUB));
+            mbar_arrive_expect_tx(BAR(C::FULL + s1), (uint32_t)(boxes * prow * 128 * C::NSUB));
+          }
+          __syncwarp();
+          const uint32_t dst = sbase + C::OFF_R + s * C::TILE_BYTES + c * C::SUB_BYTES + r * prow * 128;
+          if (mine && !(kWithhold && (e >> 1) == 1) &&
+              FA_CHECK(smem_in(dst, prow * 128, sbase + C::OFF_R, sbase + C::OFF_BAR), st, DBG_TMA_LOAD))
+            tma_load_4d(dst, lane < 16 ? &tm_kc : &tm_vc, c * 64, j * 128 & ((1 << a.page_shift) - 1) & ~127, it.kvh, page,
+                        BAR(C::FULL + s));
+          __syncwarp();
+          id = id_next;
+        }
+      }
+      for (; j < it.j0 + it.cnt; ++j) {
         const int id_next = PAGED ? page_of(j + 1) : 0;
         const bool cached = PAGED && j < it.nc;
         const int k0 = cached ? j * 128 : (j - it.nc) * 128;
