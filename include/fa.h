@@ -398,8 +398,8 @@ FA_API size_t fa_cache_workspace_size(int n_pages, int slots, int table_width);
 FA_API const char* fa_status_string(int status);
 
 /* Synchronises `stream`, then returns and clears the current device's status
- * word: FA_OK if no kernel recorded an error, else the first error a kernel
- * recorded (FA_ERR_TIMEOUT or FA_ERR_DEVICE_CHECK). A failure of the CUDA
+ * word: FA_OK if no kernel recorded an error, else FA_ERR_TIMEOUT if some wait
+ * ran out, else FA_ERR_DEVICE_CHECK. A failure of the CUDA
  * calls this makes returns FA_ERR_CUDA (fa_last_error_detail names it); a
  * device ordinal of 64 or more returns FA_ERR_UNSUPPORTED. The word's device
  * address is looked up once per device and context; after cudaDeviceReset the
@@ -407,7 +407,7 @@ FA_API const char* fa_status_string(int status);
 FA_API int fa_get_last_device_status(fa_stream_t stream);
 
 /* As fa_get_last_device_status; if detail is non-NULL it also receives 4 ints
- * describing the first recorded error: code, site (which wait or check),
+ * describing the first recorded error of that code: code, site (which wait or check),
  * blockIdx.x, blockIdx.y (all 0 when none was recorded). */
 FA_API int fa_get_last_device_status_detail(fa_stream_t stream, int* detail);
 

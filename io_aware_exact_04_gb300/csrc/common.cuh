@@ -30,14 +30,21 @@ constexpr bool kWithhold = true;
 constexpr bool kWithhold = false;
 #endif
 
-// status[0]: first error code, status[1]: wait site, status[2..3]: block index.
+// status[0]: error code, status[1]: wait or check site, status[2..3]: block index; of the first error,
+// but a timeout takes the place of a check: after a check the kernels' results are defined, after a
+// timeout they are not, and the other CTAs' waits look for it.
 struct DevStatus {
   int* word;        // global, 4 ints
   int* abort_smem;  // this CTA's abort flag
 };
 
 __device__ __forceinline__ void record_error(const DevStatus& st, int code, int site) {
-  if (atomicCAS(st.word, 0, code) == 0) {
+  int seen = atomicCAS(st.word, 0, code);
+  if (seen == FA_ERR_DEVICE_CHECK && code == FA_ERR_TIMEOUT) {
+    seen = atomicCAS(st.word, FA_ERR_DEVICE_CHECK, code);
+    if (seen == FA_ERR_DEVICE_CHECK) seen = 0;
+  }
+  if (seen == 0) {
     st.word[1] = site;
     st.word[2] = blockIdx.x;
     st.word[3] = blockIdx.y;
