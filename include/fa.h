@@ -36,7 +36,9 @@
  *    also says where). An argument that only the kernels can
  *    check (a packed sequence longer than max_seqlen) records
  *    FA_ERR_DEVICE_CHECK there; so does a failed bounds check in the
- *    bounds-checked build of this library (fa_debug.h).
+ *    bounds-checked build of this library (fa_debug.h). A recorded check does
+ *    not affect other calls; a recorded timeout makes kernels give up at their
+ *    next long wait until the word is read.
  *  - Entry points are reentrant; calls that share output buffers race.
  */
 #ifndef IO_AWARE_EXACT_FA_H

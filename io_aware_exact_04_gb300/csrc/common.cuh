@@ -130,7 +130,9 @@ __device__ __forceinline__ bool tmem_in(uint32_t taddr, uint32_t cols, uint32_t 
   return lane < 128 && (lane & 31) == 0 && col >= c0 && col + cols <= c0 + ncols;
 }
 
-// Single-thread bounded wait. Returns false if the CTA must abort. SLEEP: after the first
+// Single-thread bounded wait. Returns false if the CTA must abort: its own wait ran out, or its flag
+// is up (another wait of the CTA ran out, a check of the debug build failed), or some wait on the
+// device ran out. A recorded check of another call is no reason to stop. SLEEP: after the first
 // test, each poll may suspend the thread in hardware for up to 20 us (it resumes as soon as the
 // phase completes), so a waiting warp takes no issue slots from the warps still computing.
 template <bool SLEEP = false>
@@ -142,7 +144,7 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, DevS
     if (SLEEP ? mbar_try_wait_sleep(bar, parity, 20000u) : mbar_try_wait(bar, parity)) return true;
     if ((spins & (SLEEP ? 7u : 63u)) == 0) {
       if (*(volatile int*)st.abort_smem) return false;
-      if (*(volatile int*)st.word != 0) {
+      if (*(volatile int*)st.word == FA_ERR_TIMEOUT) {
         *(volatile int*)st.abort_smem = 1;
         return false;
       }

@@ -1196,7 +1196,7 @@ __global__ void __launch_bounds__(480, 1)
           if (lane == 0) {
             const uint64_t t0 = globaltimer_ns();
             while (smem_ld_acquire(ds0_count) < need) {
-              if (*(volatile int*)abort_flag || *(volatile int*)a.status != 0) {
+              if (*(volatile int*)abort_flag || *(volatile int*)a.status == FA_ERR_TIMEOUT) {
                 *(volatile int*)abort_flag = 1;
                 ok = false;
                 break;
