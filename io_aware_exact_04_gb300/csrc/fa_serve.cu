@@ -67,6 +67,12 @@ constexpr int kNewBox = 16;
 //
 // Rounding: scores, maxima, sums and O are fp32; P is rounded to the inputs' type for the product
 // with V (the tensor core takes both operands in one type), its sum is not; O is rounded once.
+// fp16 has all its bits down to 2^-14 and none below 2^-25, so there P is formed 2^9 times its value,
+// and the reference maximum moves when it grows by 2^6 (bf16: 2^8), so that P stays within 2^15: a
+// probability keeps its bits down to 2^-23 of the row's largest and is off by 2^-34 of it at most below that
+// (2^-25 without the factor: 8000 keys with 3e-4 of the weight beside one of value 0 gave O off by a fifth).
+// A factor of 2^11 with a growth of 2^4 costs fp16 1-3 % where queries are four times as large, this one 0-1 %.
+// l carries the factor with it, O = P V / l does not, and the LSE takes it off.
 //
 // Measured on one GB300: prompts of 8192 + 590 + 13 tokens, 16 heads over 2 of 128: 197 us, 1400
 // TFLOP/s, 74 % of the measured bf16 peak, the tensor pipe busy 78 % of the cycles; decoding 64
@@ -348,6 +354,7 @@ __global__ void __launch_bounds__(384, 1)
                  const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_kc,
                  const __grid_constant__ CUtensorMap tm_vc, ServeArgs a) {
   using C = ServeCfg<D>;
+  constexpr float P_LOG2 = F16 ? 9.f : 0.f, LAG_LOG2 = F16 ? 6.f : 8.f;
   // 1024-byte aligned, as the swizzled tiles have to be: there is no room to round the address up
   extern __shared__ __align__(1024) uint8_t sm[];
   const uint32_t sbase = smem_u32(sm);
@@ -950,19 +957,19 @@ __global__ void __launch_bounds__(384, 1)
           const float mx = fmax3(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3]),
                                  fmax3(sv[KT - 4], sv[KT - 3], fmaxf(sv[KT - 2], sv[KT - 1])));
           const float m_tile = mx * sl2;
-          // the reference maximum moves only when it grows by more than 2^8; O and l share it
+          // the reference maximum moves only when it grows by more than 2^LAG_LOG2; O and l share it
           if (s == 0) {
             m_run = m_tile;
           } else {
-            const bool grow = valid && m_tile > m_run + 8.0f;
+            const bool grow = valid && m_tile > m_run + LAG_LOG2;
             rescale = __any_sync(0xffffffffu, grow);
             if (grow) {
               f = ex2_approx(m_run - m_tile);
               m_run = m_tile;
             }
           }
-          const float base = (m_run == -INFINITY) ? 0.f : m_run;
-          const uint64_t sl2x2 = f2_pack(sl2, sl2), nbase2 = f2_pack(-base, -base);
+          const float nbase = P_LOG2 - (m_run == -INFINITY ? 0.f : m_run);
+          const uint64_t sl2x2 = f2_pack(sl2, sl2), nbase2 = f2_pack(nbase, nbase);
           uint64_t ps2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
           uint32_t pk[KT / 32][16];
           const uint32_t tP = tmem + lane_off + C::tm_p(t, u);
@@ -1055,13 +1062,13 @@ __global__ void __launch_bounds__(384, 1)
             float& m = m_few[h];
             if (s == 0) {
               m = m_tile;
-            } else if (token < it.n && m_tile > m + 8.0f) {
+            } else if (token < it.n && m_tile > m + LAG_LOG2) {
               grow = true;
               fh[h] = ex2_approx(m - m_tile);
               m = m_tile;
             }
-            const float base = m == -INFINITY ? 0.f : m;
-            const uint64_t sl2x2 = f2_pack(sl2, sl2), nbase2 = f2_pack(-base, -base);
+            const float nbase = P_LOG2 - (m == -INFINITY ? 0.f : m);
+            const uint64_t sl2x2 = f2_pack(sl2, sl2), nbase2 = f2_pack(nbase, nbase);
             uint64_t ps2 = f2_pack(0.f, 0.f);
 #pragma unroll
             for (int y = 0; y < KT / 8; ++y) {
@@ -1127,7 +1134,7 @@ __global__ void __launch_bounds__(384, 1)
       if (dual && t == 1 && !join) continue;  // lane 0 has all of them
       // l = 0: no key; NaN stays NaN
       const float inv = l_run != 0.f ? 1.f / l_run : 0.f;
-      const float lse2 = l_run != 0.f ? m_run + lg2_approx(l_run) : -INFINITY;
+      const float lse2 = l_run != 0.f ? m_run - P_LOG2 + lg2_approx(l_run) : -INFINITY;
       const long long part = (long long)it.slot * 256 + (dual ? 0 : t * 128) + row;
       if (steps == 0) {  // (a cut item only) none of this part's keys concerns this tile
         if (valid && FA_CHECK(in_range(part, a.part_rows), st, DBG_GLOBAL_STORE)) a.part_lse[part] = -INFINITY;
