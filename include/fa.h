@@ -294,8 +294,9 @@ typedef struct {
  * j <= i of the same sequence. q and o are [T, Hq, d], k and v [T, Hkv, d], lse
  * [Hq, T] fp32 (NULL: not written). Sequences may have any length, 0 and 1 too.
  * What lies in rows of k and v behind a sequence's end (other sequences, padding)
- * does not reach its results, whatever it holds; a NaN or infinity in a token of
- * the sequence itself may reach its earlier tokens within 128 keys of it.
+ * does not reach its results, whatever it holds; a NaN or infinity in V of a token
+ * of the sequence itself may reach earlier tokens of the same key/value head, those
+ * less than 128 + 128 Hkv / Hq (rounded down) before it.
  * Decreasing offsets or ones past T record FA_ERR_DEVICE_CHECK; the sequence is
  * then cut to the tokens that exist. */
 FA_API int fa_forward_prompt(const fa_rows* q, const fa_rows* k, const fa_rows* v, const fa_rows* o, float* lse,
@@ -314,8 +315,8 @@ FA_API int fa_forward_prompt(const fa_rows* q, const fa_rows* k, const fa_rows* 
  *    sequence (fa_tree_mask makes it from parents). Any bits may be set; those at
  *    or past the sequence's number of nodes, and nodes past 32 mask_words, count
  *    as not set.
- * As for prompts, a NaN or infinity in a node's own value may reach nodes of its
- * sequence that do not see it.
+ * A NaN or infinity in V of a node may reach nodes of its sequence, of the same
+ * key/value head, that do not see it.
  * A node that sees nothing gets O = 0 and LSE = -inf. o is [T, Hq, d], lse
  * [Hq, T] fp32 (NULL: not written). A sequence without nodes writes nothing, and
  * its length and pages are not looked at. What lies in the cache past lens[b]
