@@ -32,6 +32,8 @@
 
 namespace fa {
 
+enum { SITE_B_SEQLEN = 40 };  // a packed sequence longer than max_seqlen
+
 #ifdef FA_DEBUG
 // Extents that the debug build checks the backward's accesses against, each less the check
 // slack. Per tensor-map head: rows of Q / O / dO / dQ, of K / V / dK / dV and of the dQ
@@ -161,7 +163,7 @@ __global__ void __launch_bounds__(256) bwd_pre_varlen_kernel(BwdArgs a, int B) {
   const int rb = vl_cu(a)[b];
   const int len = vl_cu(a)[b + 1] - rb;
   const int base = (rb + 4 * b) & ~3;
-  if (len > vl_maxlen(a) && blockIdx.x == 0 && threadIdx.x == 0) record_check(a.status, 40);  // grid too small
+  if (len > vl_maxlen(a) && blockIdx.x == 0 && threadIdx.x == 0) record_check(a.status, SITE_B_SEQLEN);
   const int slots = (b + 1 < B) ? (((vl_cu(a)[b + 1] + 4 * (b + 1)) & ~3) - base) : (vl_Lpad(a) - base);
   const bool valid = n < len;
   float acc = 0.f;

@@ -7,7 +7,7 @@
 namespace fa {
 
 // Check sites recorded with FA_ERR_DEVICE_CHECK by the serving kernels.
-enum { SITE_S_OFFSETS = 40, SITE_S_LENGTH, SITE_S_PAGE, SITE_S_ROW, SITE_S_PARENT, SITE_S_WORDS, SITE_S_SLOT,
+enum { SITE_S_OFFSETS = 50, SITE_S_LENGTH, SITE_S_PAGE, SITE_S_ROW, SITE_S_PARENT, SITE_S_WORDS, SITE_S_SLOT,
        SITE_S_SMEM };
 
 // Bounded waits of the serving kernels, by a whole warp. They give up after kWaitLimitNs, as the

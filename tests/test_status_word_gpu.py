@@ -127,3 +127,20 @@ def test_a_timeout_of_the_forward_replaces_a_recorded_check(gpu, monkeypatch, d)
     torch.cuda.synchronize(gpu)
     assert api.device_status(gpu)[0] == 0
     assert torch.equal(got, o) and torch.equal(glse, lse)
+
+
+def test_the_detail_tells_checks_apart(gpu):
+    """A serving call's bad offsets and a packed backward's sequence that is too long."""
+    q = normal(300, 2, 64, dtype=torch.bfloat16, device=gpu)
+    api.device_status(gpu)
+    api.forward_prompt(q, q, q, ints([0, 200, 100], gpu))
+    torch.cuda.synchronize(gpu)
+    code, serving = api.device_status(gpu)
+    assert code == CHECK
+    x = q.transpose(0, 1).contiguous()  # [H, T, d]
+    cu = ints([0, 300], gpu)
+    o, lse = api.forward_varlen(x, x, x, cu, 300)
+    api.backward_varlen(x, x, x, o, x, lse, cu, 200)
+    torch.cuda.synchronize(gpu)
+    code, packed = api.device_status(gpu)
+    assert code == CHECK and packed[1] != serving[1], (packed, serving)
