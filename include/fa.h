@@ -255,6 +255,10 @@ FA_API size_t fa_backward_noalloc_max_bytes(void);
  *  - Types: FA_BF16 or FA_FP16, the same for every tensor of a call.
  *  - Grouped heads: Hq query heads share Hkv key/value heads, Hq a multiple of
  *    Hkv and Hq / Hkv <= 128; query head h reads key/value head h / (Hq / Hkv).
+ *  - Rounding: scores, maxima, sums, LSE and O are fp32, O is rounded once to the
+ *    type; the probabilities are rounded to the type before their product with V
+ *    (each by half a step, eps / 2 of itself; in fp16 below 2^-23 of the row's
+ *    largest by up to 2^-34 of that one), the sum that divides O is not.
  *  - Tokens of all sequences are packed back to back: sequence b has the tokens
  *    [cu[b], cu[b + 1]), cu a device int32 [B + 1], non-decreasing from 0. cu[B]
  *    may be less than T: the rows behind it are neither read for a result nor

@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(128) cache_append_kernel(AppendArgs a) {
 // ---------------------------------------------------------------------------------------------
 // Slots and pages: a plan, made by one cluster of eight CTAs (the counts of all pages have to be
 // complete before the free ones are numbered; a cluster's barrier costs less than another launch:
-// compacting a small pool took 44 us of the host with five launches and takes 39 with two), and its
+// compacting a small pool took 44 us of the host with five launches and 39 beside it with two), and its
 // execution by the whole GPU. Each phase of the plan waits for L2: 10-12 us in all. Workspace, in
 // ints: head [64], uses [n_pages], pages [n_pages] (new pages, or where a page goes), slots [slots] x 2,
 // copies [slots] x 3, moves [n_pages] x 2, the table as it was.

@@ -38,8 +38,8 @@ struct ServeArgs {
   int* status;
 };
 
-// Fewest key tiles that a CTA of the tree kernel takes, and rows of a TMA box of new tokens there
-// (a draft seldom fills a tile of 128).
+// Key tiles that a CTA of the tree kernel takes where there are few (the last one may take one less), and
+// rows of a TMA box of new tokens there (a draft seldom fills a tile of 128).
 constexpr int kMinTiles = 2;
 constexpr int kNewBox = 16;
 
@@ -74,12 +74,14 @@ constexpr int kNewBox = 16;
 // A factor of 2^11 with a growth of 2^4 costs fp16 1-3 % where queries are four times as large, this one 0-1 %.
 // l carries the factor with it, O = P V / l does not, and the LSE takes it off.
 //
-// Measured on one GB300: prompts of 8192 + 590 + 13 tokens, 16 heads over 2 of 128: 197 us, 1400
-// TFLOP/s, 74 % of the measured bf16 peak, the tensor pipe busy 78 % of the cycles; decoding 64
-// sequences over up to 8192 tokens, 32 heads over 8 of 128: 171 us, 6.3 TB/s, 93 % of the measured
-// copy rate (116 us, 69 %, at d = 64, where the softmax of the few rows bounds it; 191 us with pages of
-// 16 tokens, sixteen copies a tile); 64 trees of up to 64 nodes over up to 32768 tokens: 1000 us, bound
-// by the tensor pipe (84 % busy) beside memory at 73 %.
+// Measured on one GB300, in a graph: prompts of 8192 + 590 + 13 tokens, 16 heads over 2 of 128: 186 us,
+// 1480 TFLOP/s, 77 % of the measured bf16 peak, the tensor pipe busy 78 % of the cycles (16 over 4 of 64:
+// 142 us, 970 TFLOP/s, busy 51 %: a lane's one score buffer makes softmax and S wait for each other);
+// decoding 64 sequences over up to 8192 tokens, 32 heads over 8 of 128: 169 us, 6.4 TB/s, 95 % of the
+// measured copy rate (97 us, 82 %, at d = 64 and 174 us, 92 %, with pages of 16 tokens, where the
+// producer's issue bounds it); 512 sequences over up to 500 tokens: 194 us, 44 % (12 heads of 64: 239 us, 27 %):
+// an item's start and end; 64 trees of up to 64 nodes over up to 32768 tokens: 960 us, bound by the
+// tensor pipe (81-84 % busy) beside memory at 76 %.
 template <int D>
 struct ServeCfg {
   static constexpr int NSUB = D / 64;
@@ -241,8 +243,9 @@ __device__ __forceinline__ int tiles_of(const SeqWork& w, int u, int npt, bool t
 
 // Prompts: the tokens of an item, by a whole warp. Two query tiles share the keys that an item loads;
 // but with few items the longest one alone may outlast the even share of all key tiles, and items
-// of one tile, whose keys both lanes divide, take half as long (prompt_batch: 37 -> 21 us; long
-// prompts, where the share is longer than any item, lose a tenth by it).
+// of one tile, whose keys both lanes divide, take half as long: 16 prompts of up to 2048 tokens, 16 / 8
+// heads of 128, take 30 us so and 31.4 in pairs, four of up to 200, 12 heads of 64, 6.6 and 7.5; prompts
+// of 8192 + 590 + 13, 16 / 2 heads, where the share is longer than any item, 249 and 186.
 __device__ __forceinline__ int prompt_unit(const ServeArgs& a, int npt, int grid, bool record) {
   long long tiles = 0;
   int longest = 0;
