@@ -401,6 +401,98 @@ FA_API int fa_cache_compact(const fa_pool* pool, int32_t* info, void* workspace,
 /* Workspace bytes of fa_cache_update and fa_cache_compact. 0 for invalid sizes. */
 FA_API size_t fa_cache_workspace_size(int n_pages, int slots, int table_width);
 
+/* ---- a cache in 8 bits
+ * K and V of a cache in pages (fa_pages) as e4m3, strides in elements, positive
+ * multiples of 16, with a positive fp32 scale for each block of `block` tokens of a
+ * page and head (16, 32, 64, 128 or 256, at most the page size): an element stands
+ * for its value times scale[page * page_stride + head * head_stride + i], i = place
+ * in the page / block. The same strides for k and v. */
+typedef struct {
+  float *k, *v;
+  int64_t page_stride, head_stride;
+  int32_t block;
+} fa_scales;
+
+/* fa_forward_tree over a cache in 8 bits: the queries, the nodes' keys and values
+ * and O are of the type `dtype`, the cached ones e4m3 with their blocks' scales.
+ * As there otherwise, but for what is said here.
+ *  - Rounding: e4m3 values, their products with q and all sums are exact or fp32; see
+ *    there for the probabilities.
+ *  - A page id outside the cache counts as a page of zeros.
+ *  - An infinity or NaN in a query makes its row NaN.
+ * workspace: fa_forward_tree_8bit_workspace_size bytes, 256-byte aligned. */
+FA_API int fa_forward_tree_8bit(const fa_rows* q, const fa_rows* k, const fa_rows* v, const fa_rows* o, float* lse,
+                                const fa_pages* cache, const fa_scales* scales, const int32_t* lens,
+                                const int32_t* cu_nodes, const uint32_t* mask, int mask_words, int B, int T, int Hq,
+                                int Hkv, int d, int dtype, float scale, void* workspace, size_t workspace_bytes,
+                                fa_stream_t stream);
+
+/* Workspace bytes of fa_forward_tree_8bit on the current device. 0 for an unsupported d. */
+FA_API size_t fa_forward_tree_8bit_workspace_size(int d);
+
+/* fa_cache_append into a cache in 8 bits: k and v of the type `dtype`. How a token is
+ * held: in a block none of whose tokens lies before the call's first one there, the
+ * scale becomes 2^i with the least i >= -118 that brings the largest magnitude of the
+ * block's new tokens (of that head, of K or of V) to 448 at most. Where tokens lie
+ * before it they stay, and the scale s becomes 2^i s with the least such i >= 0; for
+ * i > 0 their elements are rounded again, to 2^-i of themselves. (A scale there that
+ * is no positive, normal number is taken as none; those elements stay as they are.) An
+ * element is rounded once, from its value times the reciprocal of the scale, to the
+ * nearest e4m3, ties to even. NaN and infinities become NaN and count for no scale.
+ * Other elements of the pages and other blocks' scales are left as they are. A
+ * sequence's blocks that the call touches must belong to no other sequence of it. */
+FA_API int fa_cache_append_8bit(const fa_rows* k, const fa_rows* v, const fa_pages* cache, const fa_scales* scales,
+                                const int32_t* start, const int32_t* cu, const int32_t* rows, int B, int T, int Tkv,
+                                int Hkv, int d, int dtype, fa_stream_t stream);
+
+/* The rotation of queries and keys by the angles of their positions. angles: fp32,
+ * `positions` rows of `dim` values (row_stride apart, a multiple of 4; 16-byte aligned):
+ * the cosines of the position's dim / 2 angles, then their sines. dim is a multiple
+ * of 16, at most d. With pair j of a head being elements (j, j + dim / 2), or
+ * (2j, 2j + 1) if interleaved,
+ *   (x1, x2) -> (x1 cos - x2 sin, x2 cos + x1 sin)
+ * in fp32, each product and sum rounded; elements from dim on stay. at: device int32
+ * [T], each token's position for the angles, or NULL: its position in the cache. */
+typedef struct {
+  const float* angles;
+  int64_t row_stride;
+  int32_t positions, dim, interleaved;
+  const int32_t* at;
+} fa_rotary;
+
+/* The rotation of new tokens, and their way into the cache, in one pass. q [T, Hq, d]
+ * (NULL: none, with q_out NULL) and k [T, Hkv, d] are rotated and rounded once to the
+ * type, into q_out and k_out (k_out may be NULL; either may be its input, and must not
+ * overlap it otherwise); the rotated keys and v [T, Hkv, d] go into the pages as
+ * fa_cache_append (scales NULL) or fa_cache_append_8bit (from the rotated keys in fp32)
+ * writes them: token i of sequence b to position start[b] + i. cache NULL: only
+ * the rotation; v, scales, start are not looked at then, rotary->at is needed, and
+ * cu may be NULL (every row is a token).
+ * A token whose position lies outside the angles is left out altogether and records
+ * FA_ERR_DEVICE_CHECK; one whose position or page in the cache lies outside is still
+ * rotated. Rows behind cu[B] are left as they are. */
+FA_API int fa_rotary_append(const fa_rows* q, const fa_rows* k, const fa_rows* v, const fa_rows* q_out,
+                            const fa_rows* k_out, const fa_pages* cache, const fa_scales* scales,
+                            const fa_rotary* rotary, const int32_t* start, const int32_t* cu, int B, int T, int Hq,
+                            int Hkv, int d, int dtype, fa_stream_t stream);
+
+/* The scales of a pool in 8 bits: plane x's lie plane_stride elements after plane 0's,
+ * each [n_pages, Hkv, blocks] fp32, contiguous. */
+typedef struct {
+  float* data;
+  int64_t plane_stride;
+  int32_t blocks; /* page_size / block */
+} fa_pool_scales;
+
+/* fa_cache_update and fa_cache_compact of a pool whose elements have 8 bits
+ * (plane_stride a multiple of 16): pages are copied and moved with their scales. A
+ * page of which some tokens are copied takes the scales of the blocks that hold them. */
+FA_API int fa_cache_update_8bit(const fa_pool* pool, const fa_pool_scales* scales, const int32_t* src,
+                                const int32_t* new_lens, int32_t* info, void* workspace, size_t workspace_bytes,
+                                fa_stream_t stream);
+FA_API int fa_cache_compact_8bit(const fa_pool* pool, const fa_pool_scales* scales, int32_t* info, void* workspace,
+                                 size_t workspace_bytes, fa_stream_t stream);
+
 /* Static text for an fa_status value. */
 FA_API const char* fa_status_string(int status);
 

@@ -35,6 +35,23 @@ class Pages(ctypes.Structure):
                 ("table", _vp), ("table_stride", ctypes.c_int64), ("table_width", ctypes.c_int32)]
 
 
+class Scales(ctypes.Structure):
+    """fa_scales: the scales of a cache in 8 bits."""
+    _fields_ = [("k", _vp), ("v", _vp), ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("block", ctypes.c_int32)]
+
+
+class Rotary(ctypes.Structure):
+    """fa_rotary: the angles of positions."""
+    _fields_ = [("angles", _vp), ("row_stride", ctypes.c_int64), ("positions", ctypes.c_int32), ("dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("at", _vp)]
+
+
+class PoolScales(ctypes.Structure):
+    """fa_pool_scales: the scales of all planes of a cache in 8 bits."""
+    _fields_ = [("data", _vp), ("plane_stride", ctypes.c_int64), ("blocks", ctypes.c_int32)]
+
+
 class Pool(ctypes.Structure):
     """fa_pool: all planes of a cache with the slots' page tables and lengths."""
     _fields_ = [("data", _vp), ("plane_stride", ctypes.c_int64), ("planes", ctypes.c_int32),
@@ -46,6 +63,9 @@ class Pool(ctypes.Structure):
 _rows = ctypes.POINTER(Rows)
 _pages = ctypes.POINTER(Pages)
 _pool = ctypes.POINTER(Pool)
+_scales = ctypes.POINTER(Scales)
+_rotary = ctypes.POINTER(Rotary)
+_pool_scales = ctypes.POINTER(PoolScales)
 
 SIGNATURES = {
     "libfa.so": {
@@ -58,6 +78,14 @@ SIGNATURES = {
         "fa_cache_update": (_i, [_pool, _vp, _vp, _vp, _vp, _sz, _vp]),
         "fa_cache_compact": (_i, [_pool, _vp, _vp, _sz, _vp]),
         "fa_cache_workspace_size": (_sz, [_i, _i, _i]),
+        "fa_forward_tree_8bit": (_i, [_rows, _rows, _rows, _rows, _vp, _pages, _scales, _vp, _vp, _vp, _i, _i, _i, _i, _i,
+                                      _i, _i, _f, _vp, _sz, _vp]),
+        "fa_forward_tree_8bit_workspace_size": (_sz, [_i]),
+        "fa_cache_append_8bit": (_i, [_rows, _rows, _pages, _scales, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp]),
+        "fa_rotary_append": (_i, [_rows, _rows, _rows, _rows, _rows, _pages, _scales, _rotary, _vp, _vp, _i, _i, _i, _i,
+                                  _i, _i, _vp]),
+        "fa_cache_update_8bit": (_i, [_pool, _pool_scales, _vp, _vp, _vp, _vp, _sz, _vp]),
+        "fa_cache_compact_8bit": (_i, [_pool, _pool_scales, _vp, _vp, _sz, _vp]),
         "fa_forward": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _f, _i, _vp]),
         "fa_forward_ex": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _f, _i, _vp, _vp]),
         "fa_forward_qk": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _f, _i, _vp, _vp]),
@@ -86,6 +114,7 @@ SIGNATURES = {
     "libfa_debug.so": {"fa_debug_set_check_slack": (_i, [_i])},  # include/fa_debug.h
     "libfa_selftest.so": {
         "fa_selftest_mma": (_i, [_vp, _vp, _vp, _i, _i, _i, _vp, _vp]),
+        "fa_selftest_mma8": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _vp, _vp]),
         "fa_selftest_wait_timeout": (_i, [_vp, ctypes.c_uint, _vp]),
     },
 }

@@ -271,8 +271,8 @@ def _workspace(workspace, need: int, index: int):
 
 
 def _pages(k_cache: torch.Tensor, v_cache: torch.Tensor, table: torch.Tensor, index: int, dtype, H: int, d: int,
-           B: int) -> _lib.Pages:
-    """fa_pages of [n_pages, Hkv, page_size, d] caches and an int32 [>= B, width] table."""
+           B: int, unit: int = 8) -> _lib.Pages:
+    """fa_pages of [n_pages, Hkv, page_size, d] caches, `unit` elements in 16 bytes, and an int32 [>= B, width] table."""
     shape, strides = k_cache.shape, k_cache.stride()
     if len(shape) != 4 or v_cache.shape != shape or v_cache.stride() != strides or shape[1] != H or shape[3] != d or shape[0] < 1:
         raise ValueError(f"k_cache and v_cache must be [n_pages, {H}, page_size, {d}] with the same shape and strides, are "
@@ -283,11 +283,11 @@ def _pages(k_cache: torch.Tensor, v_cache: torch.Tensor, table: torch.Tensor, in
     n, _, page, _ = shape
     sp, sh, st, sd = strides
     if n == 1:
-        sp = 8
+        sp = unit
     if H == 1:
-        sh = 8
-    if sd != 1 or sp <= 0 or sh <= 0 or st <= 0 or (sp | sh | st) & 7:
-        raise ValueError(f"the cache has strides {strides}: the last must be 1, the others positive multiples of 8")
+        sh = unit
+    if sd != 1 or sp <= 0 or sh <= 0 or st <= 0 or (sp | sh | st) & (unit - 1):
+        raise ValueError(f"the cache has strides {strides}: the last must be 1, the others positive multiples of {unit}")
     if table.dtype is not _INT32 or table.get_device() != index or table.dim() != 2:
         raise ValueError(f"table must be an int32 [slots, width] tensor on cuda:{index}")
     slots, width = table.shape
@@ -298,6 +298,39 @@ def _pages(k_cache: torch.Tensor, v_cache: torch.Tensor, table: torch.Tensor, in
         raise ValueError(f"table must have contiguous rows that do not overlap, {B} of them at least: is {(slots, width)} "
                          f"with strides {table.stride()}")
     return _lib.Pages(k_cache.data_ptr(), v_cache.data_ptr(), sp, sh, st, n, page, table.data_ptr(), ts, width)
+
+
+_E4M3 = torch.float8_e4m3fn
+
+
+def _cache(k_cache, v_cache, k_scale, v_scale, table, index: int, dtype, H: int, d: int, B: int):
+    """fa_pages of a cache in 16 bits and None, or of one in 8 bits and its fa_scales: k_scale and v_scale float32
+    [n_pages, Hkv, blocks], a block being page_size / blocks tokens."""
+    if k_cache.dtype is not _E4M3:
+        if k_scale is not None or v_scale is not None:
+            raise ValueError(f"k_scale and v_scale belong to a cache of {_E4M3}, this one is {k_cache.dtype}")
+        return _pages(k_cache, v_cache, table, index, dtype, H, d, B), None
+    if k_scale is None or v_scale is None:
+        raise ValueError("a cache in 8 bits needs k_scale and v_scale")
+    pages = _pages(k_cache, v_cache, table, index, _E4M3, H, d, B, 16)
+    n, page = k_cache.shape[0], k_cache.shape[2]
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        if t.dtype is not _FP32 or t.get_device() != index or t.dim() != 3 or t.shape[:2] != (n, H) or t.shape != k_scale.shape:
+            raise ValueError(f"{name} must be a float32 tensor ({n}, {H}, blocks) on cuda:{index}, is {t.dtype} "
+                             f"{tuple(t.shape)} on {t.device}")
+    blocks = k_scale.shape[2]
+    sp, sh, sb = k_scale.stride()
+    if blocks < 1 or page % blocks or page // blocks not in (16, 32, 64, 128, 256):
+        raise ValueError(f"{blocks} blocks of a page of {page} tokens: a block has 16, 32, 64, 128 or 256 of them")
+    if v_scale.stride() != k_scale.stride() or (sb != 1 and blocks > 1):
+        raise ValueError(f"k_scale and v_scale must have the same strides, the last 1: {k_scale.stride()}, {v_scale.stride()}")
+    if n == 1:
+        sp = 1
+    if H == 1:
+        sh = 1
+    if sp < 1 or sh < 1:
+        raise ValueError(f"the scales have strides {k_scale.stride()}: they must be positive")
+    return pages, _lib.Scales(k_scale.data_ptr(), v_scale.data_ptr(), sp, sh, page // blocks)
 
 
 def _serve(q, k, v, cu, scale, out, lse):
@@ -328,12 +361,12 @@ def _serve(q, k, v, cu, scale, out, lse):
 _workspace_sizes = {}
 
 
-def _tree_workspace(index: int, d: int) -> int:
-    """fa_forward_tree_workspace_size on a device: the same for every call."""
-    if (index, d) not in _workspace_sizes:
+def _tree_workspace(index: int, d: int, name: str = "fa_forward_tree") -> int:
+    """The workspace size of an entry point on a device: the same for every call."""
+    if (name, index, d) not in _workspace_sizes:
         with torch.cuda.device(index):
-            _workspace_sizes[index, d] = max(int(_lib_fa().fa_forward_tree_workspace_size(d)), 1)
-    return _workspace_sizes[index, d]
+            _workspace_sizes[name, index, d] = max(int(getattr(_lib_fa(), name + "_workspace_size")(d)), 1)
+    return _workspace_sizes[name, index, d]
 
 
 def forward_prompt(q, k, v, cu_seqlens, scale: Optional[float] = None, out=None, lse=None):
@@ -346,24 +379,26 @@ def forward_prompt(q, k, v, cu_seqlens, scale: Optional[float] = None, out=None,
 
 
 def forward_tree(q, k, v, k_cache, v_cache, table, lens, cu_nodes, mask=None, scale: Optional[float] = None, out=None,
-                 lse=None, workspace=None):
+                 lse=None, workspace=None, k_scale=None, v_scale=None):
     """O, LSE of drafted tokens over a cache in pages and over each other (include/fa.h:
-    fa_forward_tree): q [T, Hq, d], k and v [T, Hkv, d] of the drafted tokens, k_cache and v_cache
-    [n_pages, Hkv, page_size, d], table int32 [slots, width], lens int32 [B] cached tokens, cu_nodes
-    int32 [B + 1]. mask: int32 [T, words] from tree_mask, or None for a chain (one token a
+    fa_forward_tree, fa_forward_tree_8bit): q [T, Hq, d], k and v [T, Hkv, d] of the drafted tokens,
+    k_cache and v_cache [n_pages, Hkv, page_size, d] of the same type, or float8_e4m3fn with k_scale and
+    v_scale float32 [n_pages, Hkv, blocks]; table int32 [slots, width], lens int32 [B] cached tokens,
+    cu_nodes int32 [B + 1]. mask: int32 [T, words] from tree_mask, or None for a chain (one token a
     sequence is plain decoding). lse [Hq, T] (lse=False: none is written)."""
     index, rows, at, sizes, out, lse = _serve(q, k, v, cu_nodes, scale, out, lse)
     B, T, _, Hkv, d = sizes[:5]
-    pages = _pages(k_cache, v_cache, table, index, q.dtype, Hkv, d, B)
+    pages, scales = _cache(k_cache, v_cache, k_scale, v_scale, table, index, q.dtype, Hkv, d, B)
     bits, words = None, 0
     if mask is not None:
         if mask.dim() != 2 or mask.shape[1] < 1:
             raise ValueError(f"mask must be int32 [T, words], is {tuple(mask.shape)}")
         words = mask.shape[1]
         bits = _ints("mask", mask, index, (T, words))
-    workspace = _workspace(workspace, _tree_workspace(index, d), index)
-    _call("fa_forward_tree", index, *rows, pages, _ints("lens", lens, index, (B,)), at, bits, words, *sizes,
-          workspace.data_ptr(), workspace.numel())
+    name, cache = ("fa_forward_tree", (pages,)) if scales is None else ("fa_forward_tree_8bit", (pages, scales))
+    workspace = _workspace(workspace, _tree_workspace(index, d, name), index)
+    _call(name, index, *rows, *cache, _ints("lens", lens, index, (B,)), at, bits, words, *sizes, workspace.data_ptr(),
+          workspace.numel())
     return out, lse
 
 
@@ -384,24 +419,111 @@ def tree_mask(parents, cu_nodes, words: int, out=None) -> torch.Tensor:
     return out
 
 
-def cache_append(k, v, k_cache, v_cache, table, start, cu, rows=None) -> None:
-    """Writes tokens into their pages (include/fa.h: fa_cache_append): token i of sequence b goes to
-    position start[b] + i. k and v [Tkv, Hkv, d]; with rows (int32 [T]) token cu[b] + i is row
-    rows[cu[b] + i] of them, else row cu[b] + i."""
+def cache_append(k, v, k_cache, v_cache, table, start, cu, rows=None, k_scale=None, v_scale=None) -> None:
+    """Writes tokens into their pages (include/fa.h: fa_cache_append, fa_cache_append_8bit): token i of
+    sequence b goes to position start[b] + i. k and v [Tkv, Hkv, d]; with rows (int32 [T]) token cu[b] + i
+    is row rows[cu[b] + i] of them, else row cu[b] + i. A cache of float8_e4m3fn takes k_scale and v_scale,
+    which are updated with it."""
     index, dtype = _first("k", k, 3), k.dtype
     Tkv, H, d = k.shape
     at, B = _offsets(cu, index)
-    pages = _pages(k_cache, v_cache, table, index, dtype, H, d, B)
+    pages, scales = _cache(k_cache, v_cache, k_scale, v_scale, table, index, dtype, H, d, B)
     T, pick = Tkv, None
     if rows is not None:
         T = rows.shape[0] if rows.dim() == 1 else -1
         pick = _ints("rows", rows, index, (T,))
-    _call("fa_cache_append", index, _rows("k", k, index, dtype, Tkv, H, d), _rows("v", v, index, dtype, Tkv, H, d), pages,
-          _ints("start", start, index, (B,)), at, pick, B, T, Tkv, H, d)
+    given = (_rows("k", k, index, dtype, Tkv, H, d), _rows("v", v, index, dtype, Tkv, H, d), pages)
+    where = (_ints("start", start, index, (B,)), at, pick, B, T, Tkv, H, d)
+    if scales is None:
+        _call("fa_cache_append", index, *given, *where)
+    else:
+        _call("fa_cache_append_8bit", index, *given, scales, *where, _DTYPES[dtype])
 
 
-def _pool(kv: torch.Tensor, table: torch.Tensor, lens: torch.Tensor):
-    index = _first("kv", kv, 5)
+def rotary_angles(positions: int, dim: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
+    """float32 [positions, dim]: the cosines of position i's angles i base^(-2 j / dim), j < dim / 2, then
+    their sines, formed in 64 bits."""
+    if dim < 2 or dim % 2 or positions < 1:
+        raise ValueError(f"{positions} positions of {dim} elements: dim must be even, both positive")
+    f = base ** (-torch.arange(0, dim, 2, dtype=torch.float64, device=device) / dim)
+    x = torch.arange(positions, dtype=torch.float64, device=device)[:, None] * f
+    return torch.cat([torch.cos(x), torch.sin(x)], 1).float()
+
+
+def _angles(angles: torch.Tensor, positions, interleaved: bool, index: int, T: int) -> _lib.Rotary:
+    if angles.dtype is not _FP32 or angles.get_device() != index or angles.dim() != 2 or angles.shape[0] < 1:
+        raise ValueError(f"angles must be a float32 tensor [positions, dim] on cuda:{index}")
+    count, dim = angles.shape
+    st, se = angles.stride()
+    if count == 1:
+        st = dim
+    if se != 1 or st < dim or st % 4 or dim < 16 or dim % 16:
+        raise ValueError(f"angles {tuple(angles.shape)} with strides {angles.stride()}: dim must be a multiple of 16, rows "
+                         f"contiguous, apart, a multiple of 4 between them")
+    at = None if positions is None else _ints("positions", positions, index, (T,))
+    return _lib.Rotary(angles.data_ptr(), st, count, dim, int(bool(interleaved)), at)
+
+
+def _rotated(name: str, t, out, index: int, dtype, T: int, H: int, d: int):
+    """fa_rows of a tensor to rotate and of its result (None: a new one)."""
+    if out is None:
+        out = torch.empty((T, H, d), dtype=dtype, device=index)
+    return _rows(name, t, index, dtype, T, H, d), _rows(name + "_out", out, index, dtype, T, H, d), out
+
+
+def rotary(q, k, angles, positions, interleaved: bool = False, q_out=None, k_out=None):
+    """Queries [T, Hq, d] and keys [T, Hkv, d] rotated by the angles (rotary_angles) of their positions,
+    int32 [T] (include/fa.h: fa_rotary_append without a cache): the nodes of a draft, say. Returns both;
+    q_out=q, k_out=k rotates in place."""
+    index, dtype = _first("q", q, 3), q.dtype
+    T, Hq, d = q.shape
+    if k.dim() != 3:
+        raise ValueError(f"k must be [T, Hkv, d], is {tuple(k.shape)}")
+    Hkv = k.shape[1]
+    if Hkv < 1 or Hq < 1 or Hq % Hkv:
+        raise ValueError(f"{Hq} query heads do not share {Hkv} key/value heads evenly")
+    if positions is None:
+        raise ValueError("positions are needed without a cache")
+    turn = _angles(angles, positions, interleaved, index, T)
+    rq, ro, q_out = _rotated("q", q, q_out, index, dtype, T, Hq, d)
+    rk, rko, k_out = _rotated("k", k, k_out, index, dtype, T, Hkv, d)
+    _call("fa_rotary_append", index, rq, rk, None, ro, rko, None, None, turn, None, None, 0, T, Hq, Hkv, d, _DTYPES[dtype])
+    return q_out, k_out
+
+
+def rotary_append(q, k, v, k_cache, v_cache, table, start, cu, angles, positions=None, interleaved: bool = False, q_out=None,
+                  k_out=None, k_scale=None, v_scale=None):
+    """Rotates the queries [T, Hq, d] and keys [T, Hkv, d] of new tokens by the angles (rotary_angles) of their
+    positions and writes the rotated keys and v [T, Hkv, d] into their pages, in one pass (include/fa.h:
+    fa_rotary_append): token i of sequence b goes to position start[b] + i, which is its position for the
+    angles too unless positions (int32 [T]) says another. Caches as for cache_append. Returns the rotated
+    q and k, for forward_prompt or forward_tree; q_out=q, k_out=k rotates in place."""
+    index, dtype = _first("q", q, 3), q.dtype
+    T, Hq, d = q.shape
+    if k.dim() != 3:
+        raise ValueError(f"k must be [T, Hkv, d], is {tuple(k.shape)}")
+    Hkv = k.shape[1]
+    if Hkv < 1 or Hq < 1 or Hq % Hkv:
+        raise ValueError(f"{Hq} query heads do not share {Hkv} key/value heads evenly")
+    at, B = _offsets(cu, index)
+    pages, scales = _cache(k_cache, v_cache, k_scale, v_scale, table, index, dtype, Hkv, d, B)
+    turn = _angles(angles, positions, interleaved, index, T)
+    rq, ro, q_out = _rotated("q", q, q_out, index, dtype, T, Hq, d)
+    rk, rko, k_out = _rotated("k", k, k_out, index, dtype, T, Hkv, d)
+    _call("fa_rotary_append", index, rq, rk, _rows("v", v, index, dtype, T, Hkv, d), ro, rko, pages, scales, turn,
+          _ints("start", start, index, (B,)), at, B, T, Hq, Hkv, d, _DTYPES[dtype])
+    return q_out, k_out
+
+
+def _pool(kv: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, scales):
+    if kv.dtype is not _E4M3:
+        index, more = _first("kv", kv, 5), ()
+        if scales is not None:
+            raise ValueError(f"scales belong to a pool of {_E4M3}, this one is {kv.dtype}")
+    elif kv.dim() != 5 or not kv.is_cuda:
+        raise ValueError("kv must be a CUDA tensor of 5 dimensions")
+    else:
+        index, more = kv.get_device(), (_pool_scales(kv, scales),)
     x, n, H, page, d = kv.shape
     sx, sn, sh, st, sd = kv.stride()
     plane = n * H * page * d
@@ -415,8 +537,24 @@ def _pool(kv: torch.Tensor, table: torch.Tensor, lens: torch.Tensor):
     if table.dim() != 2 or table.shape[0] < 1 or table.shape[1] < 1:
         raise ValueError("table must be int32 [slots, width] with at least one slot and one column")
     slots, width = table.shape
-    return index, slots, _lib.Pool(kv.data_ptr(), sx, x, n, H, page, d, _ints("table", table, index, (slots, width)),
-                                   _ints("lens", lens, index, (slots,)), slots, width), (n, slots, width)
+    pool = _lib.Pool(kv.data_ptr(), sx, x, n, H, page, d, _ints("table", table, index, (slots, width)),
+                     _ints("lens", lens, index, (slots,)), slots, width)
+    return index, slots, (pool, *more), (n, slots, width)
+
+
+def _pool_scales(kv: torch.Tensor, scales) -> _lib.PoolScales:
+    """fa_pool_scales of a pool of e4m3: float32 [planes, n_pages, Hkv, blocks], every plane contiguous."""
+    x, n, H, page, _ = kv.shape
+    if (scales is None or scales.dtype is not _FP32 or scales.device != kv.device or scales.dim() != 4 or
+            scales.shape[:3] != (x, n, H) or scales.shape[3] < 1):
+        raise ValueError(f"a pool in 8 bits needs scales, a float32 tensor {(x, n, H)} + (blocks,) on {kv.device}")
+    blocks = scales.shape[3]
+    sx, sn, sh, sb = scales.stride()
+    if x == 1:
+        sx = 0
+    if (n > 1 and sn != H * blocks) or (H > 1 and sh != blocks) or (blocks > 1 and sb != 1) or (x > 1 and sx < n * H * blocks):
+        raise ValueError(f"each plane of the scales must be contiguous, and apart from the others: strides {scales.stride()}")
+    return _lib.PoolScales(scales.data_ptr(), sx, blocks)
 
 
 def _pool_workspace(workspace, sizes, index: int):
@@ -424,27 +562,27 @@ def _pool_workspace(workspace, sizes, index: int):
     return _workspace(workspace, need, index)
 
 
-def cache_update(kv, table, lens, src, new_lens, workspace=None) -> torch.Tensor:
+def cache_update(kv, table, lens, src, new_lens, workspace=None, scales=None) -> torch.Tensor:
     """Every slot s becomes the first min(new_lens[s], lens[src[s]]) tokens of slot src[s], with pages
     for new_lens[s] tokens (include/fa.h: fa_cache_update): forks, reorders, trims, frees and grows.
-    kv [planes, n_pages, Hkv, page_size, d] holds K and V of every layer; table int32 [slots, width] and
-    lens int32 [slots] are updated in place. Returns info, int32 [2]: the pages needed and the pages
+    kv [planes, n_pages, Hkv, page_size, d] holds K and V of every layer (float8_e4m3fn: with scales, float32
+    [planes, n_pages, Hkv, blocks]); table int32 [slots, width] and lens int32 [slots] are updated in place. Returns info, int32 [2]: the pages needed and the pages
     free (where more are needed than free, nothing has changed; -1, -1: invalid tables)."""
-    index, slots, pool, sizes = _pool(kv, table, lens)
+    index, slots, pool, sizes = _pool(kv, table, lens, scales)
     workspace = _pool_workspace(workspace, sizes, index)
     info = torch.empty(2, dtype=_INT32, device=index)
-    _call("fa_cache_update", index, pool, _ints("src", src, index, (slots,)), _ints("new_lens", new_lens, index, (slots,)),
+    _call("fa_cache_update" if len(pool) == 1 else "fa_cache_update_8bit", index, *pool, _ints("src", src, index, (slots,)), _ints("new_lens", new_lens, index, (slots,)),
           info.data_ptr(), workspace.data_ptr(), workspace.numel())
     return info
 
 
-def cache_compact(kv, table, lens, workspace=None) -> torch.Tensor:
-    """Moves the pages in use to the lowest ids, in every plane, and the table with them (include/fa.h:
-    fa_cache_compact). Returns info, int32 [2]: the pages in use and the pages moved."""
-    index, _, pool, sizes = _pool(kv, table, lens)
+def cache_compact(kv, table, lens, workspace=None, scales=None) -> torch.Tensor:
+    """Moves the pages in use to the lowest ids, in every plane (with its scales, as for cache_update), and the
+    table with them (include/fa.h: fa_cache_compact). Returns info, int32 [2]: the pages in use and the pages moved."""
+    index, _, pool, sizes = _pool(kv, table, lens, scales)
     workspace = _pool_workspace(workspace, sizes, index)
     info = torch.empty(2, dtype=_INT32, device=index)
-    _call("fa_cache_compact", index, pool, info.data_ptr(), workspace.data_ptr(), workspace.numel())
+    _call("fa_cache_compact" if len(pool) == 1 else "fa_cache_compact_8bit", index, *pool, info.data_ptr(), workspace.data_ptr(), workspace.numel())
     return info
 
 

@@ -32,10 +32,13 @@ FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", 
          "-I" + INCLUDE, "-I" + CSRC]
 
 LIBS = {
-    "libfa.so": ["fa_api.cu", "fa_fwd.cu", "fa_bwd.cu", "fa_noalloc.cu", "fa_serve.cu", "fa_cache.cu"],
+    "libfa.so": ["fa_api.cu", "fa_fwd.cu", "fa_bwd.cu", "fa_noalloc.cu", "fa_serve.cu", "fa_serve8.cu",
+              "fa_cache.cu", "fa_rotary.cu"],
     "libfa_selftest.so": ["selftest.cu"],
-    "libfa_withhold.so": ["fa_api.cu", "fa_fwd.cu", "fa_bwd.cu", "fa_noalloc.cu", "fa_serve.cu", "fa_cache.cu"],
-    "libfa_debug.so": ["fa_api.cu", "fa_fwd.cu", "fa_bwd.cu", "fa_noalloc.cu", "fa_serve.cu", "fa_cache.cu"],
+    "libfa_withhold.so": ["fa_api.cu", "fa_fwd.cu", "fa_bwd.cu", "fa_noalloc.cu", "fa_serve.cu", "fa_serve8.cu",
+              "fa_cache.cu", "fa_rotary.cu"],
+    "libfa_debug.so": ["fa_api.cu", "fa_fwd.cu", "fa_bwd.cu", "fa_noalloc.cu", "fa_serve.cu", "fa_serve8.cu",
+              "fa_cache.cu", "fa_rotary.cu"],
 }
 # extra preprocessor definitions (and a separate object directory) per library
 DEFINES = {

@@ -136,6 +136,9 @@ struct PoolArgs {
   int* info;
   int* status;
   int *head, *uses, *pages, *slot, *copies, *moves, *old;
+  float* scales;  // of a pool in 8 bits, else null: [planes][n_pages][Hkv][blocks]
+  long long scale_plane;
+  int blocks, block_shift;
 };
 constexpr int kPlanCtas = 8, kPlanThreads = 1024;
 enum { H_ERR = 0, H_NEED, H_FREE, H_COPIES, H_MOVES, H_COUNT = 8, H_HOLES = 16, H_HIGH = 24 };  // the last three: one a CTA
@@ -371,6 +374,11 @@ __global__ void __launch_bounds__(256) update_apply_kernel(PoolArgs a) {
     uint8_t* plane = a.data + x * a.plane_bytes + part * kCopyBytes;
     warp_copy(plane + ((long long)to * a.Hkv + h) * head_bytes, plane + ((long long)of * a.Hkv + h) * head_bytes,
               min(bytes, kCopyBytes));
+    if (part == 0 && a.scales) {  // of the blocks that hold kept tokens: at most 16
+      float* x8 = a.scales + x * a.scale_plane;
+      if (lane <= (a.copies[3 * c + 2] - 1) >> a.block_shift)
+        x8[((long long)to * a.Hkv + h) * a.blocks + lane] = x8[((long long)of * a.Hkv + h) * a.blocks + lane];
+    }
   }
 }
 
@@ -399,6 +407,11 @@ __global__ void __launch_bounds__(256) compact_apply_kernel(PoolArgs a) {
     uint8_t* plane = a.data + x * a.plane_bytes + part * kCopyBytes;
     warp_copy(plane + a.moves[2 * m + 1] * page_bytes, plane + a.moves[2 * m] * page_bytes,
               (int)min(page_bytes - part * kCopyBytes, (long long)kCopyBytes));
+    if (part == 0 && a.scales) {
+      const long long n = (long long)a.Hkv * a.blocks;
+      float* x8 = a.scales + x * a.scale_plane;
+      for (long long i = lane; i < n; i += 32) x8[a.moves[2 * m + 1] * n + i] = x8[a.moves[2 * m] * n + i];
+    }
   }
 }
 
@@ -451,7 +464,8 @@ bool pool_sizes_ok(long long n_pages, long long slots, long long width) {
          slots * width <= (1 << 28);
 }
 
-int check_pool(const fa_pool* p, const int32_t* info, const void* workspace, size_t bytes, fa::PoolArgs* a) {
+int check_pool(const fa_pool* p, const fa_pool_scales* scales, int elem, const int32_t* info, const void* workspace,
+               size_t bytes, fa::PoolArgs* a) {
   if (!p || !p->data || !p->table || !p->lens || !info || !workspace) return FA_ERR_INVALID_ARG;
   if (!aligned16(p->data)) return FA_ERR_MISALIGNED;
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return FA_ERR_MISALIGNED;
@@ -465,14 +479,23 @@ int check_pool(const fa_pool* p, const int32_t* info, const void* workspace, siz
   if (!pool_sizes_ok(p->n_pages, p->slots, p->table_width) || (long long)p->table_width * p->page_size > (1 << 30))
     return FA_ERR_UNSUPPORTED;
   const long long plane = (long long)p->n_pages * p->Hkv * p->page_size * p->d;
-  if (p->plane_stride % 8 != 0 || (p->planes > 1 && p->plane_stride < plane)) return FA_ERR_INVALID_ARG;
+  if (p->plane_stride % (16 / elem) != 0 || (p->planes > 1 && p->plane_stride < plane)) return FA_ERR_INVALID_ARG;
+  if (elem == 1) {
+    if (!scales || !scales->data || scales->blocks < 1 || scales->plane_stride < 0) return FA_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(scales->data) & 3u) != 0) return FA_ERR_MISALIGNED;
+    a->block_shift = 4;
+    while ((p->page_size >> a->block_shift) > scales->blocks) ++a->block_shift;
+    if (scales->blocks << a->block_shift != p->page_size) return FA_ERR_UNSUPPORTED;
+    if (p->planes > 1 && scales->plane_stride < (long long)p->n_pages * p->Hkv * scales->blocks) return FA_ERR_INVALID_ARG;
+    a->scales = scales->data, a->scale_plane = scales->plane_stride, a->blocks = scales->blocks;
+  }
   if (bytes < fa_cache_workspace_size(p->n_pages, p->slots, p->table_width)) return FA_ERR_INVALID_ARG;
   int err = FA_OK;
   a->status = fa::status_word(&err);
   if (!a->status) return err;
   a->data = static_cast<uint8_t*>(p->data);
-  a->plane_bytes = p->plane_stride * 2;
-  a->planes = p->planes, a->n_pages = p->n_pages, a->Hkv = p->Hkv, a->row_bytes = 2 * p->d;
+  a->plane_bytes = p->plane_stride * elem;
+  a->planes = p->planes, a->n_pages = p->n_pages, a->Hkv = p->Hkv, a->row_bytes = elem * p->d;
   a->page_shift = 0;
   while ((1 << a->page_shift) < p->page_size) ++a->page_shift;
   a->table = p->table, a->lens = p->lens, a->slots = p->slots, a->width = p->table_width;
@@ -482,6 +505,23 @@ int check_pool(const fa_pool* p, const int32_t* info, const void* workspace, siz
   a->head = w, a->uses = w + l.uses, a->pages = w + l.pages, a->slot = w + l.slot, a->copies = w + l.copies;
   a->moves = w + l.moves, a->old = w + l.old;
   return FA_OK;
+}
+
+int update_pool(const fa_pool* pool, const fa_pool_scales* scales, int elem, const int32_t* src, const int32_t* new_lens,
+                int32_t* info, void* workspace, size_t workspace_bytes, fa_stream_t stream) {
+  fa::PoolArgs a = {};
+  const int rc = check_pool(pool, scales, elem, info, workspace, workspace_bytes, &a);
+  if (rc != FA_OK) return rc;
+  if (!src || !new_lens) return FA_ERR_INVALID_ARG;
+  a.src = src, a.fresh = new_lens;
+  return fa::launch_pool(true, a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int compact_pool(const fa_pool* pool, const fa_pool_scales* scales, int elem, int32_t* info, void* workspace,
+                 size_t workspace_bytes, fa_stream_t stream) {
+  fa::PoolArgs a = {};
+  const int rc = check_pool(pool, scales, elem, info, workspace, workspace_bytes, &a);
+  return rc != FA_OK ? rc : fa::launch_pool(false, a, reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // namespace
@@ -549,18 +589,21 @@ size_t fa_cache_workspace_size(int n_pages, int slots, int table_width) {
 
 int fa_cache_update(const fa_pool* pool, const int32_t* src, const int32_t* new_lens, int32_t* info, void* workspace,
                     size_t workspace_bytes, fa_stream_t stream) {
-  fa::PoolArgs a = {};
-  const int rc = check_pool(pool, info, workspace, workspace_bytes, &a);
-  if (rc != FA_OK) return rc;
-  if (!src || !new_lens) return FA_ERR_INVALID_ARG;
-  a.src = src, a.fresh = new_lens;
-  return fa::launch_pool(true, a, reinterpret_cast<cudaStream_t>(stream));
+  return update_pool(pool, nullptr, 2, src, new_lens, info, workspace, workspace_bytes, stream);
 }
 
 int fa_cache_compact(const fa_pool* pool, int32_t* info, void* workspace, size_t workspace_bytes, fa_stream_t stream) {
-  fa::PoolArgs a = {};
-  const int rc = check_pool(pool, info, workspace, workspace_bytes, &a);
-  return rc != FA_OK ? rc : fa::launch_pool(false, a, reinterpret_cast<cudaStream_t>(stream));
+  return compact_pool(pool, nullptr, 2, info, workspace, workspace_bytes, stream);
+}
+
+int fa_cache_update_8bit(const fa_pool* pool, const fa_pool_scales* scales, const int32_t* src, const int32_t* new_lens,
+                         int32_t* info, void* workspace, size_t workspace_bytes, fa_stream_t stream) {
+  return update_pool(pool, scales, 1, src, new_lens, info, workspace, workspace_bytes, stream);
+}
+
+int fa_cache_compact_8bit(const fa_pool* pool, const fa_pool_scales* scales, int32_t* info, void* workspace,
+                          size_t workspace_bytes, fa_stream_t stream) {
+  return compact_pool(pool, scales, 1, info, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

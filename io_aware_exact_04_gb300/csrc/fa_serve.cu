@@ -7,6 +7,7 @@
 
 #include "fa_internal.h"
 #include "serve.cuh"
+#include "serve_args.h"
 #include "tmap.h"
 
 namespace fa {
@@ -1315,50 +1316,7 @@ static int launch_serve(const ServeArgs& a, int d, int dtype, cudaStream_t strea
 
 namespace {
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-// The largest stride in elements that a tensor map takes (2^40 bytes, exclusive).
-constexpr long long kMaxStride = (1LL << 39) - 8;
-
-int check_stride(int64_t s) {
-  if (s <= 0 || s % 8 != 0) return FA_ERR_INVALID_ARG;
-  return s <= kMaxStride ? FA_OK : FA_ERR_UNSUPPORTED;
-}
-
-int check_rows(const fa_rows* r) {
-  if (!r || !r->data) return FA_ERR_INVALID_ARG;
-  if (!aligned16(r->data)) return FA_ERR_MISALIGNED;
-  const int rc = check_stride(r->token_stride);
-  return rc != FA_OK ? rc : check_stride(r->head_stride);
-}
-
-int check_sizes(int B, int T, int Hq, int Hkv, int d, int dtype, float scale) {
-  if (B < 0 || T < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0) return FA_ERR_INVALID_ARG;
-  if (dtype != FA_BF16 && dtype != FA_FP16) return FA_ERR_INVALID_ARG;
-  if (!(scale > 0.f) || !std::isfinite(scale)) return FA_ERR_INVALID_ARG;
-  if ((d != 64 && d != 128) || Hq / Hkv > 128 || Hq > 65535 || B > (1 << 20) || T > (1 << 30)) return FA_ERR_UNSUPPORTED;
-  return FA_OK;
-}
-
-int check_pages(const fa_pages* c) {
-  if (!c || !c->k || !c->v || !c->table) return FA_ERR_INVALID_ARG;
-  if (!aligned16(c->k) || !aligned16(c->v)) return FA_ERR_MISALIGNED;
-  for (int64_t s : {c->page_stride, c->head_stride, c->token_stride})
-    if (const int rc = check_stride(s); rc != FA_OK) return rc;
-  if (c->n_pages < 1 || c->table_width < 1 || c->table_stride < c->table_width) return FA_ERR_INVALID_ARG;
-  switch (c->page_size) {
-    case 16: case 32: case 64: case 128: case 256: break;
-    default: return FA_ERR_UNSUPPORTED;
-  }
-  if ((long long)c->table_width * c->page_size > (1 << 30)) return FA_ERR_UNSUPPORTED;
-  return FA_OK;
-}
-
-int log2_of(int x) {
-  int s = 0;
-  while ((1 << s) < x) ++s;
-  return s;
-}
+using namespace fa::host;
 
 int forward(const fa_rows* q, const fa_rows* k, const fa_rows* v, const fa_rows* o, float* lse, const fa_pages* cache,
             const int32_t* lens, const int32_t* cu, const uint32_t* mask, int words, int B, int T, int Hq, int Hkv, int d,

@@ -270,6 +270,11 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(uint32_t M, uint32_t N, uin
   return idesc_bf16_f32(M, N, a_mn_major, b_mn_major) & ~((1u << 7) | (1u << 10));
 }
 
+// kind::f8f6f4, fp32 accumulator, A e4m3; B e4m3, or e5m2 (formats 0 and 1). K = 32 an instruction.
+__host__ __device__ constexpr uint32_t idesc_e4m3_f32(uint32_t M, uint32_t N, uint32_t b_e5m2, uint32_t a_mn_major) {
+  return (1u << 4) | (b_e5m2 << 10) | (a_mn_major << 15) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+
 // Shared-memory matrix descriptor for a 128-byte-swizzled operand.
 //   [0,14) start >> 4   [16,30) leading byte offset >> 4   [32,46) stride byte offset >> 4
 //   [46,48) version = 1   [49,52) base offset = 0   [61,64) layout (2 = 128-byte swizzle)
@@ -291,6 +296,10 @@ __host__ __device__ constexpr uint32_t sdesc_lo(uint32_t saddr, uint32_t lbo) {
 __host__ __device__ constexpr uint32_t sdesc_hi(uint32_t sbo) {
   return ((sbo >> 4) & 0x3FFFu) | (1u << 14) | (2u << 29);
 }
+// The high word for 64-byte swizzling: 8-row atoms of 512 B.
+__host__ __device__ constexpr uint32_t sdesc_hi_sw64(uint32_t sbo) {
+  return ((sbo >> 4) & 0x3FFFu) | (1u << 14) | (4u << 29);
+}
 __device__ __forceinline__ uint64_t sdesc_join(uint32_t lo, uint32_t hi) { return ((uint64_t)hi << 32) | lo; }
 
 // D[tmem] (+)= A[smem] * B[smem]
@@ -311,6 +320,16 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_
       "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// The 8-bit kinds of mma_ss.
+__device__ __forceinline__ void mma8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 // Arrive once on `bar` when every tcgen05 async op issued so far by this thread completes.

@@ -124,6 +124,80 @@ __global__ void __launch_bounds__(128, 1)
   }
 }
 
+struct Gemm8Args {
+  float* out;
+  int N, d, a_mn, e5m2;
+  int* status;
+};
+
+// A in [128][d] bytes at A0 (16 KB), B in [N][K] bytes behind it (32 KB), 64- or 128-byte swizzled.
+__global__ void __launch_bounds__(128, 1)
+    selftest_gemm8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b, Gemm8Args g) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = align1024(smem_raw);
+  const uint32_t sbase = smem_u32(sm);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int N = g.N, K = g.a_mn ? 128 : g.d;
+  const uint32_t A0 = sbase, B0 = sbase + 16384;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + 49152);
+  const uint32_t load_bar = smem_u32(bars), mma_bar = smem_u32(bars + 1);
+  uint32_t* slot = reinterpret_cast<uint32_t*>(bars + 2);
+  int* abort_flag = reinterpret_cast<int*>(slot + 1);
+  DevStatus st{g.status, abort_flag};
+  for (int i = threadIdx.x; i < 16384 / 4; i += 128) reinterpret_cast<uint32_t*>(sm)[i] = 0;  // d = 64: the half behind A
+  fence_proxy_async_smem();
+  if (threadIdx.x == 0) {
+    mbar_init(load_bar, 1);
+    mbar_init(mma_bar, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(smem_u32(slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *slot;
+  bool ok = true;
+  if (threadIdx.x == 0) {
+    mbar_arrive_expect_tx(load_bar, 128 * g.d + N * K);
+    tma_load_2d(A0, &tm_a, 0, 0, load_bar);
+    tma_load_2d(B0, &tm_b, 0, 0, load_bar);
+    ok = wait_bounded(load_bar, 0, st, 100);
+    if (ok) {
+      tc_fence_after();
+      const uint32_t idesc = idesc_e4m3_f32(128, N, g.e5m2, g.a_mn);
+      const uint32_t row = g.d, hi_a = row == 64 ? sdesc_hi_sw64(512) : sdesc_hi(1024);
+      const uint32_t hi_b = K == 64 ? sdesc_hi_sw64(512) : sdesc_hi(1024);
+      for (int k = 0; k < K / 32; ++k) {
+        const uint32_t lo_a = sdesc_lo(A0 + (g.a_mn ? k * 32 * row : k * 32), g.a_mn ? 8192 : 16);
+        mma8_ss(tmem, sdesc_join(lo_a, hi_a), sdesc_join(sdesc_lo(B0 + k * 32, 16), hi_b), idesc, k > 0);
+      }
+      mma_commit(mma_bar);
+    }
+  }
+  __syncwarp();
+  ok = wait_warp(mma_bar, 0, st, 101) && ok;
+  if (__all_sync(0xffffffffu, ok)) {
+    tc_fence_after();
+    const int r = warp * 32 + lane;
+    for (int c = 0; c < N; c += 32) {
+      uint32_t v[32];
+      tmem_ld32(tmem + ((uint32_t)(warp * 32) << 16) + c, v);
+      tmem_wait_ld();
+      for (int i = 0; i < 32; ++i) g.out[(size_t)r * N + c + i] = __uint_as_float(v[i]);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
 __global__ void selftest_wait_kernel(int* status, unsigned long long limit_ns) {
   __shared__ __align__(8) uint64_t bar;
   __shared__ int abort_flag;
@@ -169,6 +243,24 @@ int fa_selftest_mma(const void* a, const void* b, float* d, int N, int K, int mo
     return FA_ERR_CUDA;
   fa::GemmArgs g{static_cast<const uint32_t*>(a), d, N, K, mode, status};
   fa::selftest_gemm_kernel<<<1, 128, smem, reinterpret_cast<cudaStream_t>(stream)>>>(ma, mb, g);
+  return cudaPeekAtLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+int fa_selftest_mma8(const void* a, const void* b, float* d_out, int N, int d, int a_mn, int e5m2, int* status,
+                     fa_stream_t stream) {
+  if (!a || !b || !d_out || !status) return FA_ERR_INVALID_ARG;
+  if (N < 32 || N > 256 || N % 32 || (d != 64 && d != 128) || (a_mn | e5m2) & ~1) return FA_ERR_UNSUPPORTED;
+  const int K = a_mn ? 128 : d;
+  const auto U8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  CUtensorMap ma, mb;
+  if (!fa::make_tmap_2d(&ma, a, U8, 1, d, 128, d, 128, d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !fa::make_tmap_2d(&mb, b, U8, 1, K, N, K, N, K == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B))
+    return FA_ERR_CUDA;
+  const int smem = 49152 + 256 + 1024;
+  if (cudaFuncSetAttribute(fa::selftest_gemm8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return FA_ERR_CUDA;
+  fa::Gemm8Args g{d_out, N, d, a_mn, e5m2, status};
+  fa::selftest_gemm8_kernel<<<1, 128, smem, reinterpret_cast<cudaStream_t>(stream)>>>(ma, mb, g);
   return cudaPeekAtLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 

@@ -8,7 +8,7 @@ namespace fa {
 
 // Check sites recorded with FA_ERR_DEVICE_CHECK by the serving kernels.
 enum { SITE_S_OFFSETS = 50, SITE_S_LENGTH, SITE_S_PAGE, SITE_S_ROW, SITE_S_PARENT, SITE_S_WORDS, SITE_S_SLOT,
-       SITE_S_SMEM };
+       SITE_S_SMEM, SITE_S_ANGLE };
 
 // Bounded waits of the serving kernels, by a whole warp. They give up after kWaitLimitNs, as the
 // other kernels' do, and when another CTA has; not when a check was recorded, as these kernels
