@@ -27,9 +27,11 @@ FA_API int fa_selftest_mma(const void* a, const void* b, float* d, int N, int K,
 /* The same in 8 bits, D[128 x N] (fp32): a is e4m3, b e4m3 or (e5m2 = 1) e5m2, b stored
  * [N][K]. a_mn = 0: a stored [128][d], K = d; a_mn = 1: a stored [128][d] as well, but
  * taken as K rows of d elements of M (rows d and up of D mean nothing), K = 128.
- * d = 64 or 128 (64- or 128-byte swizzle); N a multiple of 32, at most 256. */
-FA_API int fa_selftest_mma8(const void* a, const void* b, float* d_out, int N, int d, int a_mn, int e5m2, int* status,
-                            fa_stream_t stream);
+ * d = 64 or 128 (64- or 128-byte swizzle); N a multiple of 16, at most 256.
+ * b_mn: 0, or (a_mn = 1) the bytes of a row, 64 or 128, of b stored [128][b_mn], of which
+ * the N from b_from (a multiple of 16) are taken. */
+FA_API int fa_selftest_mma8(const void* a, const void* b, float* d_out, int N, int d, int a_mn, int e5m2, int b_mn,
+                            int b_from, int* status, fa_stream_t stream);
 
 /* Launches one thread that waits on a shared-memory barrier nothing arrives
  * on, with a limit of limit_us microseconds (1 .. 5e6). Afterwards status[0]

@@ -114,7 +114,7 @@ SIGNATURES = {
     "libfa_debug.so": {"fa_debug_set_check_slack": (_i, [_i])},  # include/fa_debug.h
     "libfa_selftest.so": {
         "fa_selftest_mma": (_i, [_vp, _vp, _vp, _i, _i, _i, _vp, _vp]),
-        "fa_selftest_mma8": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _vp, _vp]),
+        "fa_selftest_mma8": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _vp]),
         "fa_selftest_wait_timeout": (_i, [_vp, ctypes.c_uint, _vp]),
     },
 }

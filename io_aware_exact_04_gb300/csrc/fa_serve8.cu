@@ -7,20 +7,18 @@
 #include "fa_internal.h"
 #include "serve.cuh"
 #include "serve_args.h"
+#include "tmap.h"
 
 namespace fa {
 
 struct Serve8Args {
-  const uint16_t *q, *k, *v;
+  const uint16_t* q;
   uint16_t* o;
-  long long q_st, q_sh, k_st, k_sh, v_st, v_sh, o_st, o_sh;  // token and head strides, elements
+  long long q_st, q_sh, o_st, o_sh;  // token and head strides, elements
   float* lse;  // [Hq, T] or null
-  const uint8_t *kc, *vc;
-  long long c_sp, c_sh, c_st;
   const float *ks, *vs;
   long long s_sp, s_sh;
-  int block_shift;
-  int n_pages, page_shift;
+  int block_shift, page_shift, n_pages;
   const int* table;
   long long table_stride;
   int table_width;
@@ -28,109 +26,1103 @@ struct Serve8Args {
   const uint32_t* mask;  // null: a chain
   int words;
   const int* cu;
-  int B, T, Hq, Hkv, G;
-  float scale;
+  int B, T, Hkv, G;
+  float scale_log2;
+  float* part_o;    // workspace: two slots of 2 R rows for each CTA, O normalised by its own l
+  float* part_lse;  // their LSEs, base 2 (-inf: no key, O not written)
+  int4* cuts;       // two for each CTA, of the item that it is the first to cut: {later parts (0: none), ..},
+                    // {rows of the sequence, its first token, the item's first row, key/value head}
+  long long part_rows;
   int* status;
 };
 
-template <bool F16>
-__device__ __forceinline__ float to_float(uint16_t x) {
-  float f;
-  if (F16)
-    asm("cvt.f32.f16 %0, %1;" : "=f"(f) : "h"(x));
-  else
-    f = __uint_as_float((uint32_t)x << 16);
-  return f;
+// ---------------------------------------------------------------------------------------------
+// Few rows against many keys: everything is transposed. S^T = K Q^T and O^T = V^T P^T have the keys, or
+// the columns of V, as the 128 rows of the tensor core's tile and the query rows as its columns, so that
+// decoding does not pay for 128 query rows, and K and V go from the pages through shared memory into the
+// tensor core as they are, in 8 bits: no element of the cache is ever converted, which would cost more
+// shared-memory traffic than the copy from memory itself.
+//
+// The other operand is split into 8-bit parts instead, which costs columns of a narrow tile:
+//  - q, brought to [2^7, 2^8) by a power of two a row, is q1 + q2 / 16 (+ q3 / 16 in fp16), each the e4m3
+//    nearest to what the ones before leave: 8 bits with two parts, all that bf16 has, 11 with three
+//    (elements below 2^-10 of the row's largest keep bits down to 2^-21 of that one). q1 K and
+//    (q2 + q3) K have columns of their own, as the factor 16 must stay outside.
+//  - P, formed 2^11 times its value in fp16 (11 bits; below 2^-25 of the largest, steps of 2^-35 of it), is
+//    p1 + p2 + (p3 + p4) / 64, each the e5m2 nearest to what is left (bf16 does without p4). With the
+//    range of e5m2, 2^-16 to 2^15, three parts round a probability by half a step of 2^-8 of itself
+//    (2^-9), four by 2^-12, and either by no more than 2^-34 of the row's largest. (e4m3 would need as
+//    many parts and end at 2^-26.) The reference maximum moves when it grows by 2^4, so that P stays
+//    within 2^15.
+//  - The scale of a key's block multiplies its scores, that of its values its probability, which is kept
+//    in range by a reference of its own (vref, at least each scale that was met).
+//
+// The new tokens, in 16 bits, take the same way as tiles of 64 keys: kind::f16 products with Q and P in
+// 16 bits, into the same accumulators (O is brought to vref = 1 before).
+//
+// Rows: a row is (token, head of the group), numbered token * G + head; a lane (four warps) has R of
+// them. A work item is 2 R rows of a sequence and key/value head, R for each of two lanes, over the same
+// tiles of 128 keys; where there are R rows or fewer both lanes take them and alternate tiles ("dual"),
+// and join their results at the end. All tiles of all items form one sequence, of which every CTA
+// takes an equal run; items cut between CTAs leave fp32 partial results for serve8_join_kernel.
+//
+// Roles, 448 threads: warps 0-3 and 4-7 the softmax of lanes 0 and 1 (a thread a key; with all 16 rows of
+// a step in registers, a maximum over the keys is needed only where some score passes the reference,
+// which one barrier's vote decides), warp 8 the TMA producer and scheduler, 9 the issuer of S, 10 and 11
+// those of O, 12 and 13 split Q.
+template <int D, int R, bool F16>
+struct Serve8Cfg {
+  static constexpr int ROW = D;                      // bytes of a cached row
+  static constexpr int KV = 128 * ROW, ENTRY = 2 * KV;
+  static constexpr int NEW = 64;                     // keys of a tile of new tokens
+  static constexpr int NSUB = D / 64;                // 64-column halves of their rows
+  static constexpr int QPARTS = F16 ? 3 : 2;
+  static constexpr int Q16 = QPARTS * R * D, QSLOT = Q16 + R * D * 2;
+  static constexpr int NQ = R == 16 ? 4 : R == 32 ? 3 : 2;
+  // P: [key][p1 | p3] and [p2 | p4] of R bytes each; one 64- or 128-byte row a key where they fit
+  static constexpr int PX = R == 16 ? 64 : 128;      // bytes of a key's row
+  static constexpr int PY = R == 64 && !F16 ? 64 : PX;
+  static constexpr int OFF_Y = R == 64 ? 128 * PX : 2 * R;  // of [p2 | p4] against [p1 | p3]
+  static constexpr int PBYTES = R == 64 ? 128 * (PX + PY) : 128 * PX;
+  static constexpr int MISC = 512 + 256 + 12 * 64 + NQ * R * 4 + 2 * R * (8 + 8 + 8 + 4) + 2 * 4 * (R + 4) * 4 + 64;
+  static constexpr int FIXED = 2 * PBYTES + NQ * QSLOT + MISC;
+  static constexpr int NT = (232448 - FIXED) / ENTRY < 12 ? (232448 - FIXED) / ENTRY : 12;
+  static constexpr int OFF_P = NT * ENTRY, OFF_Q = OFF_P + 2 * PBYTES, OFF_BAR = OFF_Q + NQ * QSLOT;
+  static constexpr int OFF_DESC = OFF_BAR + 512, OFF_SC = OFF_DESC + 256, OFF_QS = OFF_SC + 12 * 64;
+  static constexpr int OFF_ROWC = OFF_QS + NQ * R * 4, OFF_OROW = OFF_ROWC + 2 * R * 8, OFF_ML = OFF_OROW + 2 * R * 8;
+  static constexpr int OFF_TOK = OFF_ML + 2 * R * 8, OFF_RED = OFF_TOK + 2 * R * 4, OFF_VREF = OFF_RED + 2 * 4 * (R + 4) * 4;
+  static constexpr int SMEM_BYTES = OFF_VREF + 64;
+  __device__ static constexpr uint32_t tm_s(int t) { return 2u * R * t; }
+  __device__ static constexpr uint32_t tm_o(int t) { return 4u * R + 2u * R * t; }
+  static constexpr uint32_t TM_COLS = 8 * R;
+  static constexpr int THREADS = 448, PRODUCER = 8, S_BOTH = 9, PV0 = 10, PV1 = 11, SPLIT = 12;
+  // barriers
+  static constexpr int FULL = 0, EMPTY = NT, Q_FULL = 2 * NT, Q_EMPTY = Q_FULL + NQ, S_FULL = Q_EMPTY + NQ, S_FREE = S_FULL + 2,
+                       P_READY = S_FREE + 2, O_DONE = P_READY + 2, O_FREE = O_DONE + 2, MERGE = O_FREE + 2, DRAIN = MERGE + 1,
+                       D_FULL = DRAIN + 1, D_EMPTY = D_FULL + 4, BARS = D_EMPTY + 4;
+  static_assert(8 * BARS + 12 <= 512, "barrier area");
+  static_assert(NT >= 2 && SMEM_BYTES <= 232448, "shared memory");
+  static_assert(OFF_P % 1024 == 0 && OFF_Q % 1024 == 0 && QSLOT % 1024 == 0 && Q16 % 1024 == 0 && OFF_BAR % 16 == 0, "alignment");
+};
+
+enum { SITE_T8_EMPTY = 80, SITE_T8_FULL, SITE_T8_Q_FULL, SITE_T8_Q_EMPTY, SITE_T8_S_FULL, SITE_T8_S_FREE, SITE_T8_P_READY,
+       SITE_T8_O_DONE, SITE_T8_O_FREE, SITE_T8_MERGE, SITE_T8_DESC_FULL, SITE_T8_DESC_EMPTY, SITE_T8_V_FULL };
+
+constexpr float kNoKey = -1e30f;     // reference maximum of a row that has met no key
+constexpr float kPLog2 = 11.f, kLagLog2 = 4.f;
+constexpr int kMinTiles8 = 2;        // tiles of a CTA where there are few
+constexpr int kNewBox8 = 16;         // rows of a TMA box of new tokens
+
+// A work item (or the part of it that this CTA computes), as the producer publishes it.
+struct Item8 {
+  int cnt;     // tiles here; -1: no more items
+  int flags;   // 1: dual, 2: the whole item is here (results go straight to O)
+  int c0, c1;  // tiles of lanes 0 and 1
+  int j0;      // first tile, counted from the item's first
+  int nc;      // tiles of cached tokens; tile j >= nc holds the new tokens from 64 (j - nc)
+  int L, n;    // cached and new tokens of the sequence
+  int row0;    // the sequence's first token among the packed ones
+  int r0;      // the item's first row
+  int kvh;
+  int slot;    // partial result slot
+};
+enum { ITEM8_DUAL = 1, ITEM8_WHOLE = 2 };
+
+// Sizes of sequence b's work, in items of `unit` rows; record: whether invalid device values are recorded.
+struct SeqWork8 {
+  int row0, n, L, nc, nk, units;
+  long long tiles;  // all heads and units, each counted with the nk tiles of the last one
+};
+__device__ __forceinline__ SeqWork8 seq_work8(const Serve8Args& a, int lo, int hi, int len, int unit, bool record) {
+  SeqWork8 w;
+  w.row0 = min(max(lo, 0), a.T);
+  const int end = min(max(hi, w.row0), a.T);
+  if (record && (w.row0 != lo || end != hi)) record_check(a.status, SITE_S_OFFSETS);
+  w.n = end - w.row0;
+  w.L = 0;
+  if (w.n > 0) {
+    w.L = min(max(len, 0), a.table_width << a.page_shift);
+    if (record && w.L != len) record_check(a.status, SITE_S_LENGTH);
+  }
+  w.nc = (w.L + 127) >> 7;
+  w.nk = w.nc + ((w.n + 63) >> 6);
+  w.units = (w.n * a.G + unit - 1) / unit;
+  w.tiles = (long long)w.units * a.Hkv * w.nk;
+  return w;
 }
-__device__ __forceinline__ float e4m3_float(uint8_t x) {
-  float f;
-  asm("{\n\t.reg .b32 t;\n\t.reg .b16 l, h;\n\tcvt.rn.f16x2.e4m3x2 t, %1;\n\tmov.b32 {l, h}, t;\n\tcvt.f32.f16 %0, l;\n\t}"
-      : "=f"(f)
-      : "h"((uint16_t)x));
-  return f;
+__device__ __forceinline__ SeqWork8 seq_work8(const Serve8Args& a, int b, int unit, bool record) {
+  return seq_work8(a, a.cu[b], a.cu[b + 1], a.lens[b], unit, record);
 }
 
-// A warp for each row (token, query head): 32 keys at a time, a key a lane for the scores, D / 32 columns
-// a lane for O.
-template <int D, bool F16>
-__global__ void __launch_bounds__(128) tree8_kernel(Serve8Args a) {
-  griddep_wait();
-  griddep_launch_dependents();
-  __shared__ float qs[4][D];
-  if (blockIdx.x == 0 && blockIdx.y == 0) check_offsets(a.cu, a.B, a.T, a.status);
+// The run of tiles of CTA c, by a whole warp. Each lane counts the tiles of `chunk` sequences that follow
+// each other, four sequences' loads at a time, so that a search looks at one lane's sequences only.
+struct Runs8 {
+  long long total, base;
+  int ctas, rest;  // CTAs with work; the first `rest` of them take a tile more
+  long long mine;  // this lane's tiles
+  int chunk;
+  __device__ long long start(int c) const { return base * c + min(c, rest); }
+};
+__device__ __forceinline__ Runs8 runs8(const Serve8Args& a, int unit, int grid, bool record) {
+  Runs8 r;
+  const int lane = threadIdx.x & 31;
+  r.chunk = (a.B + 31) >> 5;
+  r.mine = 0;
+  const int end = min(a.B, (lane + 1) * r.chunk);
+  for (int b = lane * r.chunk; b < end; b += 4) {
+    int at[5], len[4];
+#pragma unroll
+    for (int k = 0; k < 5; ++k) at[k] = a.cu[min(b + k, end)];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) len[k] = a.lens[min(b + k, end - 1)];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (b + k < end) r.mine += seq_work8(a, at[k], at[k + 1], len[k], unit, record).tiles;
+  }
+  r.total = r.mine;
+  for (int o = 16; o; o >>= 1) r.total += __shfl_xor_sync(0xffffffffu, r.total, o);
+  r.ctas = r.total < (long long)grid * kMinTiles8 ? max(1, ((int)r.total + kMinTiles8 - 1) / kMinTiles8) : grid;
+  r.base = r.total < (1LL << 31) ? (int)r.total / r.ctas : r.total / r.ctas;
+  r.rest = (int)(r.total - r.base * r.ctas);
+  return r;
+}
+// The lane whose own tiles hold tile `pos` of all, and their first one; 32: past the end.
+__device__ __forceinline__ int lane_with(long long mine, long long pos, long long* first) {
+  const int lane = threadIdx.x & 31;
+  long long incl = mine;
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  const unsigned past = __ballot_sync(0xffffffffu, *first + incl > pos);
+  const int k = past ? __ffs(past) - 1 : 32;
+  *first += __shfl_sync(0xffffffffu, k < 32 ? incl - mine : incl, k < 32 ? k : 31);
+  return k;
+}
+// The sequence that tile `pos` of all belongs to, and its first tile; by a whole warp. pos < total.
+__device__ __forceinline__ int seek8(const Serve8Args& a, int unit, const Runs8& runs, long long pos, long long* first) {
+  *first = 0;
+  const int k = lane_with(runs.mine, pos, first);
+  if (k == 32) return a.B;
+  if (runs.chunk == 1) return k;
+  const int end = min(a.B, (k + 1) * runs.chunk);
+  for (int b0 = k * runs.chunk; b0 < end; b0 += 32) {
+    const int b = b0 + (threadIdx.x & 31);
+    const int x = lane_with(b < end ? seq_work8(a, b, unit, false).tiles : 0, pos, first);
+    if (x < 32) return b0 + x;
+  }
+  return a.B;
+}
+
+// Tiles that the rows [r, r + R) of a sequence need, counted from the first.
+__device__ __forceinline__ int tiles_of_rows(const Serve8Args& a, const SeqWork8& w, int r, int R) {
+  const int rows = w.n * a.G;
+  if (r >= rows) return 0;
+  return w.nc + (((a.mask ? w.n : min(w.n, (min(r + R, rows) - 1) / a.G + 1)) + 63) >> 6);
+}
+
+__device__ __forceinline__ float warp_max(float x) {
+  float m;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(x));
+  return m;
+}
+__device__ __forceinline__ bool bar_or(uint32_t id, bool x) { return !named_bar_and(id, 128, !x); }
+__device__ __forceinline__ uint32_t h2_sub(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t h2_mul64(uint32_t a) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(0x54005400u));  // 64, 64
+  return r;
+}
+// The two e5m2 nearest to two fp16, as fp16 with the low bytes zero: half a step up in the magnitude's
+// bits, and the low bytes off (e5m2 is the upper byte of fp16; ties go away from zero).
+__device__ __forceinline__ uint32_t to_e5m2(uint32_t x) { return (x + 0x00800080u) & 0xff00ff00u; }
+// The upper bytes of four fp16.
+__device__ __forceinline__ uint32_t upper_bytes(uint32_t lo, uint32_t hi) { return __byte_perm(lo, hi, 0x7531); }
+__device__ __forceinline__ void sts128(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+__device__ __forceinline__ void sts64(uint32_t at, uint32_t x, uint32_t y) {
+  asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(x), "r"(y) : "memory");
+}
+// The offset of 16-byte chunk c of row r in rows of PITCH (64 or 128) bytes, swizzled as TMA and the tensor
+// core do: address bits 7 .. exchange with bits 4 ...
+template <int PITCH>
+__device__ __forceinline__ uint32_t swizzled(uint32_t r, uint32_t c) {
+  return PITCH == 128 ? r * 128u + ((c ^ (r & 7u)) << 4) : r * 64u + ((c ^ ((r >> 1) & 3u)) << 4);
+}
+template <int PITCH>
+__host__ __device__ constexpr uint32_t desc_hi() {
+  return PITCH == 128 ? sdesc_hi(1024) : sdesc_hi_sw64(512);
+}
+__device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ void e4m3_floats(uint32_t x, float& lo, float& hi) {
+  asm("{\n\t.reg .b32 t;\n\t.reg .b16 l, h;\n\tcvt.rn.f16x2.e4m3x2 t, %2;\n\tmov.b32 {l, h}, t;\n\t"
+      "cvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
+      : "=f"(lo), "=f"(hi)
+      : "h"((uint16_t)x));
+}
+template <bool F16>
+__device__ __forceinline__ void halves(uint32_t w, float& lo, float& hi) {
+  if (F16) {
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
+        : "=f"(lo), "=f"(hi)
+        : "r"(w));
+  } else {
+    lo = __uint_as_float(w << 16), hi = __uint_as_float(w & 0xffff0000u);
+  }
+}
+template <bool F16>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+  return F16 ? pack_f16x2(lo, hi) : pack_bf16x2(lo, hi);
+}
+
+template <int D, int R, bool F16>
+__global__ void __launch_bounds__(448, 1)
+    serve8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                  const __grid_constant__ CUtensorMap tm_kc, const __grid_constant__ CUtensorMap tm_vc, Serve8Args a) {
+  using C = Serve8Cfg<D, R, F16>;
+  constexpr int NT = C::NT, NQ = C::NQ, CH = R / 16;
+  // 1024-byte aligned, as the swizzled tiles have to be: there is no room to round the address up
+  extern __shared__ __align__(1024) uint8_t sm[];
+  const uint32_t sbase = smem_u32(sm);
+  if (sbase & 1023u) {  // (never seen: the kernel has no static shared memory)
+    griddep_wait();
+    if (threadIdx.x == 0) {
+      record_check(a.status, SITE_S_SMEM);
+      a.cuts[2 * blockIdx.x] = make_int4(0, 0, 0, 0);  // nothing for the join to read
+    }
+    return;
+  }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int t = blockIdx.x * 4 + warp, head = blockIdx.y, kvh = head / a.G;
-  if (t >= a.T) return;
-  const int b = find_sequence(a.cu, a.B, t);
-  if (b < 0) return;
-  const SeqRange r = seq_range(a.cu, b, a.T, a.status);
-  if (t < r.lo || t >= r.hi) return;
-  const int len = a.lens[b], L = min(max(len, 0), a.table_width << a.page_shift), n = r.hi - r.lo, me = t - r.lo;
-  if (L != len && lane == 0) record_check(a.status, SITE_S_LENGTH);
-  for (int c = lane; c < D; c += 32) qs[warp][c] = to_float<F16>(a.q[t * a.q_st + head * a.q_sh + c]);
-  __syncwarp();
-  float m = -INFINITY, l = 0.f, o[D / 32] = {};
-  for (int j0 = 0; j0 < L + n; j0 = j0 < L ? min(L, j0 + 32) : j0 + 32) {
-    const bool cached = j0 < L;
-    const int j = j0 + lane;
-    bool seen;
-    float s = 0.f, vscale = 1.f;
-    const uint8_t* v8 = nullptr;
-    if (cached) {
-      seen = j < L;
-      const int id = seen ? a.table[b * a.table_stride + (j >> a.page_shift)] : 0;
-      const int in_page = j & ((1 << a.page_shift) - 1);
-      if (seen && (id < 0 || id >= a.n_pages)) {
-        record_check(a.status, SITE_S_PAGE);
-      } else if (seen) {
-        const uint8_t* k8 = a.kc + id * a.c_sp + kvh * a.c_sh + in_page * a.c_st;
-        const long long at = id * a.s_sp + kvh * a.s_sh + (in_page >> a.block_shift);
-        for (int c = 0; c < D; ++c) s = fmaf(qs[warp][c], e4m3_float(k8[c]), s);
-        s *= a.ks[at];
-        vscale = a.vs[at];
-        v8 = a.vc + id * a.c_sp + kvh * a.c_sh + in_page * a.c_st;
+  const uint32_t b0 = sbase + C::OFF_BAR;
+  auto BAR = [&](int i) { return b0 + 8u * i; };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::OFF_BAR + 8 * C::BARS);
+  int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
+  DevStatus st{a.status, abort_flag};
+  int* descs = reinterpret_cast<int*>(sm + C::OFF_DESC);
+  float* scales = reinterpret_cast<float*>(sm + C::OFF_SC);  // [entry][K of 8 groups of 16 keys, V of 8]
+  float* qscale = reinterpret_cast<float*>(sm + C::OFF_QS);  // [slot][row]
+
+  if (warp == C::PRODUCER && lane == 0) {
+    for (int i = 0; i < NT; ++i) {
+      mbar_init(BAR(C::FULL + i), 17);  // the copies, and each of 16 lanes' scale
+      mbar_init(BAR(C::EMPTY + i), 2);  // both lanes, or one twice
+    }
+    for (int i = 0; i < NQ; ++i) {
+      mbar_init(BAR(C::Q_FULL + i), 2);
+      mbar_init(BAR(C::Q_EMPTY + i), 3);  // the issuer of S, and both lanes' rows, or one's twice
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(BAR(C::S_FULL + t), 1);
+      mbar_init(BAR(C::S_FREE + t), 4);
+      mbar_init(BAR(C::P_READY + t), 4);
+      mbar_init(BAR(C::O_DONE + t), 1);
+      mbar_init(BAR(C::O_FREE + t), 8);  // four warps twice, or all eight in a join
+    }
+    mbar_init(BAR(C::MERGE), 8);
+    mbar_init(BAR(C::DRAIN), 3);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(BAR(C::D_FULL + i), 1);
+      mbar_init(BAR(C::D_EMPTY + i), 13);  // softmax warps, issuers, splitters
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tmap(&tm_k);
+    prefetch_tmap(&tm_v);
+    prefetch_tmap(&tm_kc);
+    prefetch_tmap(&tm_vc);
+  }
+  if (warp == C::PV0) {
+    tmem_alloc(smem_u32(tmem_slot), C::TM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  griddep_wait();  // before any access to global memory
+  griddep_launch_dependents();
+
+  // Item i of this CTA, for a consumer warp: false when the CTA must give up.
+  auto next_item = [&](int i, Item8* it) {
+    if (!wait_phase(BAR(C::D_FULL + (i & 3)), (i >> 2) & 1, st, SITE_T8_DESC_FULL)) return false;
+    const int4* d = reinterpret_cast<const int4*>(descs + 16 * (i & 3));
+    const int4 x = d[0], y = d[1], z = d[2];
+    it->cnt = x.x, it->flags = x.y, it->c0 = x.z, it->c1 = x.w;
+    it->j0 = y.x, it->nc = y.y, it->L = y.z, it->n = y.w;
+    it->row0 = z.x, it->r0 = z.y, it->kvh = z.z, it->slot = z.w;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(BAR(C::D_EMPTY + (i & 3)));
+    return true;
+  };
+  auto rows_here = [&](const Item8& it, int j) {  // keys of tile j
+    return j < it.nc ? min(128, it.L - j * 128) : min(C::NEW, it.n - (j - it.nc) * C::NEW);
+  };
+
+  if (warp == C::PRODUCER) {
+    // ------------------------------------------------------------ scheduler and TMA producer
+    int items = 0, e = 0;  // items published, ring entries used
+    bool ok = true;
+    auto publish = [&](const Item8& it) {
+      if (!wait_phase(BAR(C::D_EMPTY + (items & 3)), ((items >> 2) & 1) ^ 1, st, SITE_T8_DESC_EMPTY)) return false;
+      if (lane == 0) {
+        int4* d = reinterpret_cast<int4*>(descs + 16 * (items & 3));
+        d[0] = make_int4(it.cnt, it.flags, it.c0, it.c1);
+        d[1] = make_int4(it.j0, it.nc, it.L, it.n);
+        d[2] = make_int4(it.row0, it.r0, it.kvh, it.slot);
+        mbar_arrive(BAR(C::D_FULL + (items & 3)));
+      }
+      __syncwarp();
+      ++items;
+      return true;
+    };
+    // Loads the item's tiles. Lane (kv, g) = 8 kv + g looks after 16 keys: their scale, and, where a page's
+    // box begins with them, the box.
+    const int kv = (lane >> 3) & 1, g = lane & 7;
+    const int page = 1 << a.page_shift, prow = min(page, 128);
+    const float* sc = kv ? a.vs : a.ks;
+    auto run_item = [&](const Item8& it, int b) {
+      if (!publish(it)) return false;
+      auto page_of = [&](int j) {
+        const int t0 = j * 128 + g * 16;
+        return lane < 16 && j < min(it.j0 + it.cnt, it.nc) && t0 < it.L ? a.table[b * a.table_stride + (t0 >> a.page_shift)] : 0;
+      };
+      int id = page_of(it.j0);
+      for (int j = it.j0; j < it.j0 + it.cnt; ++j, ++e) {
+        const int id_next = page_of(j + 1);
+        const bool cached = j < it.nc;
+        const int s = e % NT, rows = rows_here(it, j);
+        const uint32_t bar = BAR(C::FULL + s), dst0 = sbase + s * C::ENTRY;
+        const int box = cached ? prow : kNewBox8, boxes = (rows + box - 1) / box;
+        if (!wait_phase(BAR(C::EMPTY + s), ((e / NT) & 1) ^ 1, st, SITE_T8_EMPTY)) return false;
+        if (elect_one()) mbar_arrive_expect_tx(bar, (uint32_t)(2 * boxes * box * (cached ? C::ROW : 2 * D)));
+        __syncwarp();
+        if (cached) {
+          const int t0 = j * 128 + g * 16, in_page = t0 & (page - 1);
+          const bool mine = lane < 16 && g * 16 < rows;
+          const bool there = id >= 0 && id < a.n_pages;
+          if (mine && !there) record_check(a.status, SITE_S_PAGE);
+          float* to = scales + s * 16 + lane;
+          if (mine && there) {
+            const float* from = sc + id * a.s_sp + it.kvh * a.s_sh + (in_page >> a.block_shift);
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+          } else if (lane < 16) {
+            *to = 1.f;
+            mbar_arrive(bar);
+          }
+          const uint32_t dst = dst0 + kv * C::KV + g * 16 * C::ROW;
+          if (mine && (g * 16 & (prow - 1)) == 0 && !(kWithhold && e == 1) &&
+              FA_CHECK(smem_in(dst, prow * C::ROW, sbase, sbase + C::OFF_P), st, DBG_TMA_LOAD))
+            tma_load_4d(dst, kv ? &tm_vc : &tm_kc, 0, in_page, it.kvh, there ? id : a.n_pages, bar);  // outside: zeros
+        } else {
+          if (lane == 0) mbar_arrive_n(bar, 16);
+          const int r = g / C::NSUB, c = g % C::NSUB;
+          const uint32_t dst = dst0 + kv * C::KV + c * (C::NEW * 128) + r * kNewBox8 * 128;
+          if (lane < 16 && r < boxes && !(kWithhold && e == 1) &&
+              FA_CHECK(smem_in(dst, kNewBox8 * 128, sbase, sbase + C::OFF_P), st, DBG_TMA_LOAD))
+            tma_load_3d(dst, kv ? &tm_v : &tm_k, c * 64, it.row0 + (j - it.nc) * C::NEW + r * kNewBox8, it.kvh, bar);
+        }
+        __syncwarp();
+        id = id_next;
+      }
+      return true;
+    };
+    Item8 it;
+    const int unit = 2 * R;
+    const Runs8 runs = runs8(a, unit, gridDim.x, blockIdx.x == 0);
+    int parts = 0;  // of the item that this CTA is the first to cut
+    int4 cut = make_int4(0, 0, 0, 0);
+    if ((int)blockIdx.x < runs.ctas && runs.total > 0) {
+      long long pos = runs.start(blockIdx.x), first = 0;
+      const long long end = runs.start(blockIdx.x + 1);
+      int b = seek8(a, unit, runs, pos, &first);
+      while (ok && pos < end) {
+        const SeqWork8 w = seq_work8(a, b, unit, false);
+        // the first item may be cut; from then on they start with their first tile
+        const long long at = pos - first;
+        const int q = at < (1LL << 31) ? (int)at / max(w.nk, 1) : (int)(at / w.nk);
+        int p = q / a.Hkv, kvh = q - p * a.Hkv, j0 = (int)(at - (long long)q * w.nk);
+        while (ok && pos < end && pos - first < w.tiles) {
+          int j1 = (int)min((long long)w.nk, j0 + (end - pos));
+          const int taken = j1 - j0;
+          const int n0 = tiles_of_rows(a, w, p * unit, R), n1 = tiles_of_rows(a, w, p * unit + R, R), most = max(n0, n1);
+          const bool dual = n1 == 0;
+          j1 = min(j1, most);
+          it.cnt = max(0, j1 - j0);
+          it.flags = (dual ? ITEM8_DUAL : 0) | (j0 == 0 && j1 == most ? ITEM8_WHOLE : 0);
+          it.c0 = dual ? (it.cnt + 1) >> 1 : max(0, min(j1, n0) - j0);
+          it.c1 = dual ? it.cnt >> 1 : it.cnt;
+          it.j0 = j0, it.nc = w.nc, it.L = w.L, it.n = w.n, it.row0 = w.row0, it.r0 = p * unit, it.kvh = kvh;
+          it.slot = 2 * blockIdx.x + (j0 == 0);
+          if (j0 > 0 && it.cnt > 0 && runs.start(blockIdx.x - 1) <= pos - j0) {
+            // (the first item only) how many CTAs, this one included, hold later parts of it
+            const long long end_of_item = pos + most - j0;
+            for (int k = blockIdx.x + lane; __any_sync(0xffffffffu, k < runs.ctas); k += 32)
+              parts += __popc(__ballot_sync(0xffffffffu, k < runs.ctas && runs.start(k) < end_of_item));
+            cut = make_int4(it.n * a.G, it.row0, it.r0, it.kvh);
+          }
+          if (it.cnt > 0) ok = run_item(it, b);
+          pos += taken;
+          j0 = 0;
+          if (++kvh == a.Hkv) kvh = 0, ++p;
+        }
+        first += w.tiles;
+        ++b;
+      }
+    }
+    if (lane == 0) {
+      a.cuts[2 * blockIdx.x] = make_int4(parts, 0, 0, 0);
+      a.cuts[2 * blockIdx.x + 1] = cut;
+    }
+    if (ok) {
+      it.cnt = -1;
+      ok = publish(it);
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (*(volatile int*)abort_flag) {
+      // let copies already in flight land before the CTA's shared memory is released
+      for (int x = max(0, e - NT); x < e; ++x) {
+        const uint64_t t0 = globaltimer_ns();
+        while (!mbar_try_wait(BAR(C::FULL + x % NT), (x / NT) & 1) && globaltimer_ns() - t0 < 100000000ull) {
+        }
+      }
+    }
+  } else if (warp >= C::SPLIT) {
+    // ------------------------------------------------------------ Q in parts
+    constexpr int LPR = D / 8, RPI = 32 / LPR, STEPS = R / 2 / RPI;  // lanes a row, rows and steps of a warp
+    const int half = warp - C::SPLIT, sub = lane / LPR, c = lane % LPR;
+    int uq = 0;
+    for (int i = 0;; ++i) {
+      Item8 it;
+      if (!next_item(i, &it) || it.cnt < 0) break;
+      const int nq = (it.flags & ITEM8_DUAL) ? 1 : 2, rows = it.n * a.G;
+      bool ok = true;
+      for (int t = 0; ok && t < nq; ++t, ++uq) {
+        const int s = uq % NQ;
+        uint4 x[STEPS];
+#pragma unroll
+        for (int k = 0; k < STEPS; ++k) {
+          const int rr = it.r0 + t * R + half * (R / 2) + k * RPI + sub, tok = rr / a.G;
+          x[k] = make_uint4(0, 0, 0, 0);
+          if (rr < rows)
+            x[k] = *reinterpret_cast<const uint4*>(a.q + (long long)(it.row0 + tok) * a.q_st +
+                                                   (long long)(it.kvh * a.G + rr - tok * a.G) * a.q_sh + 8 * c);
+        }
+        if (!(ok = wait_phase(BAR(C::Q_EMPTY + s), ((uq / NQ) & 1) ^ 1, st, SITE_T8_Q_EMPTY))) break;
+        const uint32_t q8 = sbase + C::OFF_Q + s * C::QSLOT, q16 = q8 + C::Q16;
+#pragma unroll
+        for (int k = 0; k < STEPS; ++k) {
+          const uint32_t r = half * (R / 2) + k * RPI + sub;
+          sts128(q16 + (c >> 3) * (R * 128) + swizzled<128>(r, c & 7), x[k].x, x[k].y, x[k].z, x[k].w);
+          const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+          float f[8], most = 0.f;
+#pragma unroll
+          for (int y = 0; y < 4; ++y) halves<F16>(w[y], f[2 * y], f[2 * y + 1]);
+#pragma unroll
+          for (int y = 0; y < 8; ++y) {
+            // infinities count as NaN: the parts have none
+            if (!(fabsf(f[y]) <= 3.4028235e38f)) f[y] = NAN;
+            most = fmaxf(most, fabsf(f[y]));
+          }
+#pragma unroll
+          for (int o = LPR / 2; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+          // most 2^-x in [2^7, 2^8)
+          const int x2 = max((int)(__float_as_uint(most) >> 23) - 127, -100) - 7;
+          const float down = __uint_as_float((uint32_t)(127 - x2) << 23), up = __uint_as_float((uint32_t)(127 + x2) << 23);
+          uint32_t part[3][4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            float lo = f[2 * y] * down, hi = f[2 * y + 1] * down, bl, bh;
+            part[0][y] = e4m3_pair(lo, hi);
+            e4m3_floats(part[0][y], bl, bh);
+            lo = (lo - bl) * 16.f, hi = (hi - bh) * 16.f;
+            part[1][y] = e4m3_pair(lo, hi);
+            e4m3_floats(part[1][y], bl, bh);
+            part[2][y] = e4m3_pair(lo - bl, hi - bh);
+          }
+#pragma unroll
+          for (int z = 0; z < C::QPARTS; ++z)
+            sts64(q8 + swizzled<C::ROW>(z * R + r, c >> 1) + (c & 1) * 8, part[z][0] | part[z][1] << 16,
+                  part[z][2] | part[z][3] << 16);
+          if (c == 0) qscale[s * R + r] = up;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(C::Q_FULL + s));
+      }
+      if (!ok) break;
+    }
+  } else if (warp >= C::S_BOTH) {
+    // ------------------------------------------------------------ MMA issuers
+    auto commit = [&](uint32_t bar) {
+      if (elect_one()) mma_commit(bar);
+      __syncwarp();
+    };
+    bool ok = true;
+    int e = 0;
+    if (warp == C::S_BOTH) {
+      // S^T = K Q^T of both lanes, tile after tile in the order of the ring
+      constexpr uint32_t I8 = idesc_e4m3_f32(128, 2 * R, 0, 0), I8X = idesc_e4m3_f32(128, R, 0, 0);
+      constexpr uint32_t I16 = F16 ? idesc_f16_f32(128, R, 0, 0) : idesc_bf16_f32(128, R, 0, 0);
+      constexpr uint32_t HI = desc_hi<C::ROW>(), HI16 = sdesc_hi(1024);
+      int uq = 0, used[2] = {0, 0};
+      for (int i = 0; ok; ++i) {
+        Item8 it;
+        if (!next_item(i, &it) || it.cnt < 0) break;
+        const bool dual = it.flags & ITEM8_DUAL;
+        const int nq = dual ? 1 : 2;
+        for (int u = uq; ok && u < uq + nq; ++u)
+          ok = wait_phase(BAR(C::Q_FULL + u % NQ), (u / NQ) & 1, st, SITE_T8_Q_FULL);
+        for (int k = 0; ok && k < it.cnt; ++k, ++e) {
+          const int j = it.j0 + k, s = e % NT;
+          if (!(ok = wait_phase(BAR(C::FULL + s), (e / NT) & 1, st, SITE_T8_FULL))) break;
+          const uint32_t ka = sdesc_lo(sbase + s * C::ENTRY, 16);
+          for (int t = 0; t < 2; ++t) {
+            if (dual ? (k & 1) != t : k >= (t ? it.c1 : it.c0)) continue;
+            // S of the tile before is in registers
+            if (used[t] > 0 && !(ok = wait_phase(BAR(C::S_FREE + t), (used[t] - 1) & 1, st, SITE_T8_S_FREE))) break;
+            ++used[t];
+            tc_fence_after();
+            const uint32_t d = tmem + C::tm_s(t), slot = sbase + C::OFF_Q + (uq + (dual ? 0 : t)) % NQ * C::QSLOT;
+            if (j < it.nc) {
+              const uint32_t qb = sdesc_lo(slot, 16);
+#pragma unroll
+              for (int x = 0; x < D / 32; ++x)
+                if (elect_one()) mma8_ss(d, sdesc_join(ka + 2 * x, HI), sdesc_join(qb + 2 * x, HI), I8, x > 0);
+              if (F16) {
+                const uint32_t qc = sdesc_lo(slot + 2 * R * D, 16);
+#pragma unroll
+                for (int x = 0; x < D / 32; ++x)
+                  if (elect_one()) mma8_ss(d + R, sdesc_join(ka + 2 * x, HI), sdesc_join(qc + 2 * x, HI), I8X, 1);
+              }
+            } else {
+              const uint32_t qb = sdesc_lo(slot + C::Q16, 16);
+#pragma unroll
+              for (int x = 0; x < D / 16; ++x) {
+                const uint32_t ko = ((x >> 2) * (C::NEW * 128) + (x & 3) * 32) >> 4, qo = ((x >> 2) * (R * 128) + (x & 3) * 32) >> 4;
+                if (elect_one()) mma_ss(d, sdesc_join(ka + ko, HI16), sdesc_join(qb + qo, HI16), I16, x > 0);
+              }
+            }
+            commit(BAR(C::S_FULL + t));
+          }
+          if (!ok) break;
+        }
+        for (int u = uq; u < uq + nq; ++u) commit(BAR(C::Q_EMPTY + u % NQ));
+        uq += nq;
       }
     } else {
-      const int i = j - L;
-      seen = i < n && (a.mask ? (i >> 5) < a.words && (a.mask[(long long)t * a.words + (i >> 5)] >> (i & 31) & 1) : i <= me);
-      if (seen) {
-        const uint16_t* k = a.k + (r.lo + i) * a.k_st + kvh * a.k_sh;
-        for (int c = 0; c < D; ++c) s = fmaf(qs[warp][c], to_float<F16>(k[c]), s);
+      // O^T += V^T P^T of lane t
+      const int t = warp == C::PV1;
+      constexpr uint32_t IX = idesc_e4m3_f32(128, 2 * R, 1, 1) | 1u << 16;                  // [p1 | p3]
+      constexpr uint32_t IY = idesc_e4m3_f32(128, F16 ? 2 * R : R, 1, 1) | 1u << 16;        // [p2 | p4], [p2]
+      constexpr uint32_t I16 = F16 ? idesc_f16_f32(128, R, 1, 1) : idesc_bf16_f32(128, R, 1, 1);
+      constexpr uint32_t HIV = desc_hi<C::ROW>(), HIX = desc_hi<C::PX>(), HIY = desc_hi<C::PY>(), HI16 = sdesc_hi(1024);
+      const uint32_t d = tmem + C::tm_o(t), p0 = sbase + C::OFF_P + t * C::PBYTES;
+      int used = 0, items = 0;
+      for (int i = 0; ok; ++i) {
+        Item8 it;
+        if (!next_item(i, &it) || it.cnt < 0) break;
+        const bool dual = it.flags & ITEM8_DUAL;
+        const int tiles = t ? it.c1 : it.c0;
+        bool first = true;
+        for (int k = 0; ok && k < it.cnt; ++k, ++e) {
+          const int s = e % NT;
+          // waited for also where the other lane's: the arrival below must not count for an earlier use
+          if (!(ok = wait_phase(BAR(C::FULL + s), (e / NT) & 1, st, SITE_T8_V_FULL))) break;
+          if (dual ? (k & 1) != t : k >= tiles) {
+            if (!dual && elect_one()) mbar_arrive(BAR(C::EMPTY + s));
+            __syncwarp();
+            continue;
+          }
+          const int j = it.j0 + k, rows = rows_here(it, j);
+          const bool cached = j < it.nc;
+          const int step = cached ? 32 : 16, steps = (rows + step - 1) / step;
+          uint8_t* v = sm + s * C::ENTRY + C::KV;
+          if (rows < steps * step) {
+            // rows past the sequence may hold anything; P is 0 there, but 0 x NaN is not
+            const int pitch = cached ? C::ROW : 128, chunks = (steps * step - rows) * pitch / 16;
+            for (int z = lane; z < chunks * (cached ? 1 : C::NSUB); z += 32)
+              *reinterpret_cast<uint4*>(v + rows * pitch + z / chunks * (C::NEW * 128) + z % chunks * 16) = make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+          if (!(ok = wait_phase(BAR(C::P_READY + t), used & 1, st, SITE_T8_P_READY))) break;
+          if (first && items > 0 && !(ok = wait_phase(BAR(C::O_FREE + t), (items - 1) & 1, st, SITE_T8_O_FREE))) break;
+          ++used;
+          tc_fence_after();
+          const uint32_t va = smem_u32(v);
+          if (cached) {
+            for (int x = 0; x < steps; ++x) {
+              const uint64_t av = sdesc_join(sdesc_lo(va + x * 32 * C::ROW, 8192), HIV);
+              if (elect_one()) mma8_ss(d, av, sdesc_join(sdesc_lo(p0 + x * 32 * C::PX, 8192), HIX), IX, !first || x > 0);
+              if (elect_one()) mma8_ss(d, av, sdesc_join(sdesc_lo(p0 + C::OFF_Y + x * 32 * C::PY, 8192), HIY), IY, 1);
+            }
+          } else {
+            for (int x = 0; x < steps; ++x) {
+              const uint64_t av = sdesc_join(sdesc_lo(va + x * 2048, C::NEW * 128), HI16);
+              if (elect_one()) mma_ss(d, av, sdesc_join(sdesc_lo(p0 + x * 16 * C::PX, 8192), HIX), I16 , !first || x > 0);
+            }
+          }
+          commit(BAR(C::O_DONE + t));
+          commit(BAR(C::EMPTY + s));
+          if (dual) commit(BAR(C::EMPTY + s));
+          first = false;
+        }
+        items += tiles > 0;
       }
     }
-    s = seen ? s * a.scale : -INFINITY;
-    float top = s;
-    for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-    top = fmaxf(top, m);
-    const float base = top == -INFINITY ? 0.f : top, f = expf(m - base);
-    const float p = seen ? expf(s - base) : 0.f;
-    m = top;
-    l = l * f + p;
-    for (int c = 0; c < D / 32; ++c) o[c] *= f;
-    for (int x = 0; x < 32; ++x) {
-      const float px = __shfl_sync(0xffffffffu, p * vscale, x);
-      const unsigned long long row = __shfl_sync(0xffffffffu, (unsigned long long)v8, x);
-      if (!__shfl_sync(0xffffffffu, (int)seen, x)) continue;
-      if (cached && !row) continue;
-      for (int c = 0; c < D / 32; ++c)
-        o[c] = fmaf(px, cached ? e4m3_float(reinterpret_cast<const uint8_t*>(row)[lane + 32 * c])
-                               : to_float<F16>(a.v[(r.lo + j0 + x - L) * a.v_st + kvh * a.v_sh + lane + 32 * c]), o[c]);
+    // every MMA issued has completed before TMEM is released
+    commit(BAR(C::DRAIN));
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(BAR(C::DRAIN), 0) && globaltimer_ns() - t0 < kWaitLimitNs) {
+    }
+  } else {
+    // ------------------------------------------------------------ softmax of lane t, a thread a key
+    // The four warps meet at named barriers, which know no limit: a warp whose wait has run out goes on to
+    // the next of them (without further waits) and says so there, and all four leave together.
+    const int t = warp >> 2, wq = warp & 3, key = wq * 32 + lane;
+    const uint32_t bar_id = 1 + t, tlane = (uint32_t)(wq * 32) << 16;
+    const float sl2 = a.scale_log2;
+    float2* rowc = reinterpret_cast<float2*>(sm + C::OFF_ROWC) + t * R;  // {factor of a row's scores, 11 - its reference}
+    long long* orow = reinterpret_cast<long long*>(sm + C::OFF_OROW) + t * R;  // head << 40 | token, or -1
+    int* tok = reinterpret_cast<int*>(sm + C::OFF_TOK) + t * R;
+    float* red = reinterpret_cast<float*>(sm + C::OFF_RED) + t * 4 * (R + 4);
+    float2* ml = reinterpret_cast<float2*>(sm + C::OFF_ML);
+    float* vrefs = reinterpret_cast<float*>(sm + C::OFF_VREF);
+    const uint32_t pbuf = sbase + C::OFF_P + t * C::PBYTES;
+    int uq = 0, e0 = 0, used = 0, merges = 0;
+    for (int i = 0;; ++i) {
+      Item8 it;
+      bool ok = next_item(i, &it);
+      const bool dual = it.flags & ITEM8_DUAL;
+      const int slot = (uq + (dual ? 0 : t)) % NQ;
+      if (ok && it.cnt >= 0) ok = wait_phase(BAR(C::Q_FULL + slot), ((uq + (dual ? 0 : t)) / NQ) & 1, st, SITE_T8_Q_FULL);
+      // (also: all four warps are done with the rows of the item before)
+      if (bar_or(bar_id, !ok) || it.cnt < 0) break;
+      {
+        const int rr = it.r0 + (dual ? 0 : t * R) + key;
+        if (key < R) {
+          const bool there = rr < it.n * a.G;
+          const int tk = rr / a.G;
+          rowc[key] = make_float2(there ? qscale[slot * R + key] * sl2 : 0.f, there ? kPLog2 - kNoKey : kNoKey);
+          orow[key] = there ? (long long)(it.kvh * a.G + rr - tk * a.G) << 40 | (long long)(it.row0 + tk) : -1;
+          tok[key] = there ? tk : -1;
+        }
+      }
+      named_bar_sync(bar_id, 128);
+      if (wq == 0 && lane == 0) mbar_arrive_n(BAR(C::Q_EMPTY + slot), dual ? 1 : 2);
+      uq += dual ? 1 : 2;
+      const int steps = t ? it.c1 : it.c0;
+      float l[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r) l[r] = 0.f;
+      float vref = 1.1754944e-38f;
+      bool give_up = false;
+      for (int s = 0; s < steps; ++s, ++used) {
+        const int k = dual ? 2 * s + t : s, j = it.j0 + k, es = (e0 + k) % NT;
+        const bool cached = j < it.nc;
+        ok = ok && wait_phase(BAR(C::S_FULL + t), used & 1, st, SITE_T8_S_FULL);
+        tc_fence_after();
+        const bool there = key < rows_here(it, j);
+        const float kscale = cached ? scales[es * 16 + (key >> 4)] : 1.f;
+        const float vscale = cached ? scales[es * 16 + 8 + (key >> 4)] : 1.f;
+        const int nkey = (j - it.nc) * C::NEW + key;  // of a new token, within its sequence
+        bool pv_waited = s == 0;  // (its P has been read; across items the epilogue waited for that)
+        auto wait_pv = [&] {
+          if (!pv_waited) ok = ok && wait_phase(BAR(C::O_DONE + t), (used - 1) & 1, st, SITE_T8_O_DONE);
+          pv_waited = true;
+          tc_fence_after();
+        };
+        const bool to_one = !cached && vref != 1.f;
+        float w = 0.f;
+#pragma unroll
+        for (int ch = 0; ch < CH; ++ch) {
+          float y[16];
+          {
+            uint32_t x0[16], x1[16];
+            tmem_ld16(tmem + tlane + C::tm_s(t) + ch * 16, x0);
+            if (cached) tmem_ld16(tmem + tlane + C::tm_s(t) + R + ch * 16, x1);
+            tmem_wait_ld();
+            const float k16 = kscale * 0.0625f;
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+              y[r] = cached ? fmaf(__uint_as_float(x1[r]), k16, __uint_as_float(x0[r]) * kscale) : __uint_as_float(x0[r]);
+          }
+          if (ch == CH - 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(BAR(C::S_FREE + t));
+          }
+          uint32_t seen = there ? 0xffffu : 0u;
+          if (!cached && there) {
+            seen = 0;
+#pragma unroll 1
+            for (int r = 0; r < 16; ++r) {
+              const int tk = tok[ch * 16 + r];
+              bool sees = nkey <= tk;
+              if (a.mask)
+                sees = tk >= 0 && (nkey >> 5) < a.words &&
+                       (a.mask[(long long)(it.row0 + tk) * a.words + (nkey >> 5)] >> (nkey & 31) & 1);
+              seen |= (uint32_t)sees << r;
+            }
+          }
+          float tt[16], top = -INFINITY;
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const float2 rc = rowc[ch * 16 + r];
+            const float x = fmaf(y[r], cached ? rc.x : sl2, rc.y);
+            tt[r] = (seen >> r & 1) ? x : -INFINITY;
+            top = fmaxf(top, tt[r]);
+          }
+          const bool grows = top > kPLog2 + kLagLog2 || (ch == 0 && ((there && cached && vscale > vref) || to_one));
+          if (bar_or(bar_id, grows || !ok)) {
+            // a reference moves: the largest score of each row over the tile
+            if (bar_or(bar_id, !ok)) {
+              give_up = true;
+              break;
+            }
+            float mine = 0.f;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+              const float2 rc = rowc[ch * 16 + r];
+              const float m = warp_max((seen >> r & 1) ? y[r] * (cached ? rc.x : sl2) : -INFINITY);
+              if (lane == r) mine = m;
+            }
+            if (lane < 16) red[wq * (R + 4) + ch * 16 + lane] = mine;
+            const float vm = warp_max(there && cached ? vscale : 0.f);
+            if (lane == 0) red[wq * (R + 4) + R] = vm;
+            named_bar_sync(bar_id, 128);
+            float fv = 1.f;  // of all rows, as the reference of the values' scales moves
+            if (ch == 0) {
+              float v = 0.f;
+#pragma unroll
+              for (int x = 0; x < 4; ++x) v = fmaxf(v, red[x * (R + 4) + R]);
+              const float to = to_one ? 1.f : v > vref ? 2.f * v : vref;
+              fv = vref / to;
+              vref = to;
+            }
+            if (s > 0) wait_pv();
+            const int c0 = ch, c1 = fv != 1.f ? CH : ch + 1;
+            uint32_t moved = 0;
+#pragma unroll 1
+            for (int c = c0; c < c1; ++c) {
+              float f[16];
+#pragma unroll
+              for (int r = 0; r < 16; ++r) {
+                f[r] = fv;
+                if (c != ch) continue;
+                float m = -INFINITY;
+#pragma unroll
+                for (int x = 0; x < 4; ++x) m = fmaxf(m, red[x * (R + 4) + ch * 16 + r]);
+                const float ref = kPLog2 - rowc[ch * 16 + r].y;
+                if (tok[ch * 16 + r] >= 0 && m > ref + kLagLog2) {
+                  moved |= 1u << r;
+                  f[r] *= ex2_approx(ref - m);
+                }
+              }
+              if (s > 0) {
+                uint32_t x[16];
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                  const uint32_t at = tmem + tlane + C::tm_o(t) + half * R + c * 16;
+                  tmem_ld16(at, x);
+                  tmem_wait_ld();
+#pragma unroll
+                  for (int r = 0; r < 16; ++r) x[r] = __float_as_uint(__uint_as_float(x[r]) * f[r]);
+                  tmem_st16(at, x);
+                }
+                tmem_wait_st();
+              }
+            }
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+              if (!(moved >> r & 1)) continue;
+              float m = -INFINITY;
+#pragma unroll
+              for (int x = 0; x < 4; ++x) m = fmaxf(m, red[x * (R + 4) + ch * 16 + r]);
+              l[ch * 16 + r] *= ex2_approx(kPLog2 - rowc[ch * 16 + r].y - m);
+            }
+            named_bar_sync(bar_id, 128);  // the references have been read
+            if (wq == 0 && lane < 16 && (moved >> lane & 1)) {
+              float m = -INFINITY;
+#pragma unroll
+              for (int x = 0; x < 4; ++x) m = fmaxf(m, red[x * (R + 4) + ch * 16 + lane]);
+              rowc[ch * 16 + lane].y = kPLog2 - m;
+            }
+            named_bar_sync(bar_id, 128);
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+              const float2 rc = rowc[ch * 16 + r];
+              tt[r] = (seen >> r & 1) ? fmaf(y[r], cached ? rc.x : sl2, rc.y) : -INFINITY;
+            }
+          }
+          if (ch == 0) w = vscale / vref;
+          uint32_t x[8], x16[8];
+#pragma unroll
+          for (int r = 0; r < 8; ++r) {
+            const float p = ex2_approx(tt[2 * r]), q = ex2_approx(tt[2 * r + 1]);
+            l[ch * 16 + 2 * r] += p;
+            l[ch * 16 + 2 * r + 1] += q;
+            if (cached)
+              x[r] = pack_f16x2(p * w, q * w);
+            else
+              x16[r] = pack16<F16>(p, q);
+          }
+          wait_pv();
+          if (cached) {
+            uint32_t part[4][4];
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                const uint32_t lo = to_e5m2(x[2 * r]), hi = to_e5m2(x[2 * r + 1]);
+                part[z][r] = upper_bytes(lo, hi);
+                x[2 * r] = h2_sub(x[2 * r], lo);
+                x[2 * r + 1] = h2_sub(x[2 * r + 1], hi);
+                if (z == 1) x[2 * r] = h2_mul64(x[2 * r]), x[2 * r + 1] = h2_mul64(x[2 * r + 1]);
+              }
+              if (z == 2 && !F16) break;
+            }
+            auto put = [&](int z, int at) { sts128(at, part[z][0], part[z][1], part[z][2], part[z][3]); };
+            constexpr int RC = R / 16;  // chunks of 16 rows
+            const uint32_t py = pbuf + (R == 64 ? C::OFF_Y : 0);
+            constexpr int Y0 = R == 64 ? 0 : 2 * RC;
+            put(0, pbuf + swizzled<C::PX>(key, ch));
+            put(2, pbuf + swizzled<C::PX>(key, RC + ch));
+            put(1, py + swizzled<C::PY>(key, Y0 + ch));
+            if (F16) put(3, py + swizzled<C::PY>(key, Y0 + RC + ch));
+          } else if (key < C::NEW) {
+            sts128(pbuf + swizzled<C::PX>(key, 2 * ch), x16[0], x16[1], x16[2], x16[3]);
+            sts128(pbuf + swizzled<C::PX>(key, 2 * ch + 1), x16[4], x16[5], x16[6], x16[7]);
+          }
+        }
+        if (give_up) break;
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(C::P_READY + t));
+      }
+      if (give_up) break;
+      if (steps > 0) ok = ok && wait_phase(BAR(C::O_DONE + t), (used - 1) & 1, st, SITE_T8_O_DONE);
+      tc_fence_after();
+      // sums over the keys: of 16 rows at a time, lane pairs end with a row each
+#pragma unroll
+      for (int ch = 0; ch < CH; ++ch) {
+        float v[16];
+#pragma unroll
+        for (int r = 0; r < 16; ++r) v[r] = l[ch * 16 + r];
+#pragma unroll
+        for (int o = 16, n = 8; o > 1; o >>= 1, n >>= 1)
+#pragma unroll
+          for (int r = 0; r < n; ++r) {
+            const bool up = lane & o;
+            const float send = up ? v[r] : v[r + n], keep = up ? v[r + n] : v[r];
+            v[r] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+          }
+        v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
+        if (!(lane & 1)) red[wq * (R + 4) + ch * 16 + (lane >> 1)] = v[0];
+      }
+      if (bar_or(bar_id, !ok)) break;
+      if (key < R && steps > 0) {  // (without steps nobody reads them, and the other lane may still read the last ones)
+        float sum = 0.f;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) sum += red[x * (R + 4) + key];
+        ml[t * R + key] = make_float2(tok[key] < 0 ? kNoKey : kPLog2 - rowc[key].y, sum);
+      }
+      if (key == 0 && steps > 0) vrefs[t] = vref;
+      const bool join = dual && it.c1 > 0, whole = it.flags & ITEM8_WHOLE;
+      e0 += it.cnt;
+      if (join) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(C::MERGE));
+        ok = wait_phase(BAR(C::MERGE), merges & 1, st, SITE_T8_MERGE);
+        tc_fence_after();
+        ++merges;
+      }
+      // The other lane's results stay as they are: it writes the next ones after a product into O, which waits for
+      // this lane's arrival below.
+      if (bar_or(bar_id, !ok)) break;
+      if (dual && t == 1 && !join) continue;  // lane 0 has all of them
+      const long long part0 = (long long)it.slot * (2 * R) + (dual ? 0 : t * R);
+      if (steps == 0) {  // (a cut item only) none of this part's keys concerns these rows
+        if (key < R && tok[key] >= 0 && FA_CHECK(in_range(part0 + key, a.part_rows), st, DBG_GLOBAL_STORE))
+          a.part_lse[part0 + key] = -INFINITY;
+        continue;
+      }
+      // rows [ra, rb): in a join each lane takes half of them
+      const int ra = join ? t * (R / 2) : 0, rb = join ? ra + R / 2 : R;
+      if (key >= ra && key < rb && orow[key] >= 0) {
+        const float2 x = ml[(join ? 0 : t * R) + key], z = join ? ml[R + key] : make_float2(kNoKey, 0.f);
+        const float m = fmaxf(x.x, z.x), sum = x.y * ex2_approx(x.x - m) + z.y * ex2_approx(z.x - m);
+        const float lse2 = sum != 0.f ? m - kPLog2 + lg2_approx(sum) : -INFINITY;
+        const long long token = orow[key] & 0xffffffffffll, head = orow[key] >> 40;
+        if (!whole) {
+          if (FA_CHECK(in_range(part0 + key, a.part_rows), st, DBG_GLOBAL_STORE)) a.part_lse[part0 + key] = lse2;
+        } else if (a.lse && FA_CHECK(in_range(token, a.T), st, DBG_GLOBAL_STORE)) {
+          a.lse[head * a.T + token] = lse2 * 0.6931471805599453f;
+        }
+      }
+      const float v0 = vrefs[join ? 0 : t], v1 = join ? vrefs[1] : 0.f;
+#pragma unroll 1
+      for (int r0 = ra; r0 < rb; r0 += 8) {
+        float o[8];
+        if (key < D) {
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            if (u == 1 && !join) break;
+            uint32_t x[8], z[8];
+            const uint32_t at = tmem + tlane + C::tm_o(join ? u : t) + r0;
+            // (tiles of new tokens alone leave the columns of p3 and p4 unwritten)
+            const bool parts = it.j0 + (dual ? (join ? u : t) : 0) < it.nc;
+            tmem_ld8(at, x);
+            tmem_ld8(at + R, z);
+            tmem_wait_ld();
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+              const float2 p = ml[(join ? 0 : t * R) + r0 + r], q = join ? ml[R + r0 + r] : make_float2(kNoKey, 0.f);
+              const float m = fmaxf(p.x, q.x), f0 = ex2_approx(p.x - m), f1 = ex2_approx(q.x - m);
+              const float sum = p.y * f0 + q.y * f1, inv = sum != 0.f ? 1.f / sum : 0.f;
+              const float v = fmaf(parts ? __uint_as_float(z[r]) : 0.f, 0.015625f, __uint_as_float(x[r])) * ((u ? f1 * v1 : f0 * v0) * inv);
+              o[r] = u ? o[r] + v : v;
+            }
+          }
+        }
+        if (r0 + 8 >= rb) {  // O is in registers: the issuers may write it again
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive_n(BAR(C::O_FREE + t), join ? 1 : 2);
+            if (join) mbar_arrive(BAR(C::O_FREE + (t ^ 1)));
+          }
+        }
+        if (key >= D) continue;
+        if (whole) {
+          // even threads write the even rows of two columns each, odd threads the odd rows
+#pragma unroll
+          for (int r = 0; r < 8; r += 2) {
+            const float got = __shfl_xor_sync(0xffffffffu, (lane & 1) ? o[r] : o[r + 1], 1);
+            const uint32_t y = (lane & 1) ? pack16<F16>(got, o[r + 1]) : pack16<F16>(o[r], got);
+            const long long to = orow[r0 + r + (lane & 1)];
+            const long long token = to & 0xffffffffffll;
+            if (to >= 0 && FA_CHECK(in_range(token, a.T), st, DBG_GLOBAL_STORE))
+              *reinterpret_cast<uint32_t*>(a.o + token * a.o_st + (to >> 40) * a.o_sh + (key & ~1)) = y;
+          }
+        } else {
+#pragma unroll
+          for (int r = 0; r < 8; ++r)
+            if (orow[r0 + r] >= 0 && FA_CHECK(in_range(part0 + r0 + r, a.part_rows), st, DBG_GLOBAL_STORE))
+              a.part_o[(part0 + r0 + r) * D + key] = o[r];
+        }
+      }
     }
   }
-  for (int x = 16; x; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
-  const float inv = l != 0.f ? 1.f / l : 0.f;
-  for (int c = 0; c < D / 32; ++c) {
-    const float x = o[c] * inv;
-    a.o[t * a.o_st + head * a.o_sh + lane + 32 * c] = (uint16_t)(F16 ? pack_f16x2(x, x) : pack_bf16x2(x, x));
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == C::PV0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TM_COLS);
   }
-  if (lane == 0 && a.lse) a.lse[(long long)head * a.T + t] = l != 0.f ? m + logf(l) : -INFINITY;
 }
 
-static int launch_serve8(const Serve8Args& a, int d, int dtype, cudaStream_t stream) {
-  const dim3 grid((a.T + 3) / 4, a.Hq);
-  const auto go = [&](auto kernel) { return launch_pdl("tree8_kernel", kernel, grid, dim3(128), 0, stream, a); };
-  if (d == 64) return dtype == FA_FP16 ? go(tree8_kernel<64, true>) : go(tree8_kernel<64, false>);
-  return dtype == FA_FP16 ? go(tree8_kernel<128, true>) : go(tree8_kernel<128, false>);
+// Joins the partial results of the items that CTA boundaries cut: block (x, y) takes rows
+// [16 y, 16 y + 16) of the item that boundary x + 1 is the first to cut, a group of D / 4 threads a row.
+template <int D, int R, bool F16>
+__global__ void __launch_bounds__(4 * D) serve8_join_kernel(Serve8Args a) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int c = blockIdx.x + 1;
+  const int parts = a.cuts[2 * c].x + 1;  // part 0: CTA c - 1's last item; then the first items of c, c + 1, ..
+  if (parts == 1) return;
+  const int4 cut = a.cuts[2 * c + 1];  // rows of the sequence, its first token, the item's first row, head
+  constexpr int LPR = D / 4;
+  const int sub = threadIdx.x % LPR, row = blockIdx.y * 16 + threadIdx.x / LPR, rr = cut.z + row;
+  if (rr >= cut.x) return;
+  auto at = [&](int k) { return (long long)(k == 0 ? 2 * (c - 1) + 1 : 2 * (c - 1 + k)) * (2 * R) + row; };
+  float m = -INFINITY;
+  for (int k = 0; k < parts; ++k) m = fmaxf(m, a.part_lse[at(k)]);
+  const float base = m == -INFINITY ? 0.f : m;
+  float l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k = 0; k < parts; ++k) {
+    const float s = a.part_lse[at(k)];
+    if (s == -INFINITY) continue;  // nothing was written there
+    const float w = ex2_approx(s - base);
+    const float4 x = *reinterpret_cast<const float4*>(a.part_o + at(k) * D + 4 * sub);
+    l += w;
+    o.x = fmaf(w, x.x, o.x), o.y = fmaf(w, x.y, o.y), o.z = fmaf(w, x.z, o.z), o.w = fmaf(w, x.w, o.w);
+  }
+  const float inv = l != 0.f ? 1.f / l : 0.f;
+  const int tok = rr / a.G, h = cut.w * a.G + rr - tok * a.G;
+  const long long token = cut.y + tok;
+  *reinterpret_cast<uint2*>(a.o + token * a.o_st + h * a.o_sh + 4 * sub) =
+      make_uint2(pack16<F16>(o.x * inv, o.y * inv), pack16<F16>(o.z * inv, o.w * inv));
+  if (sub == 0 && a.lse)
+    a.lse[(long long)h * a.T + token] = (l != 0.f ? m + lg2_approx(l) : -INFINITY) * 0.6931471805599453f;
+}
+
+struct Serve8Tensors {
+  const fa_rows *k, *v;
+  const fa_pages* cache;
+};
+
+template <int D, int R, bool F16>
+static int launch_serve8_r(const Serve8Tensors& x, Serve8Args a, cudaStream_t stream) {
+  using C = Serve8Cfg<D, R, F16>;
+  const auto type = F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  CUtensorMap mk, mv, mkc, mvc;
+  auto map3 = [&](CUtensorMap* m, const fa_rows* r) {
+    const cuuint64_t dims[3] = {D, (cuuint64_t)a.T, (cuuint64_t)a.Hkv};
+    const cuuint64_t strides[2] = {(cuuint64_t)r->token_stride * 2, (cuuint64_t)r->head_stride * 2};
+    const cuuint32_t box[3] = {64, kNewBox8, 1};
+    return make_tmap_strided(m, r->data, type, 3, dims, strides, box);
+  };
+  auto map4 = [&](CUtensorMap* m, const void* p) {
+    const fa_pages* c = x.cache;
+    const cuuint64_t dims[4] = {D, (cuuint64_t)c->page_size, (cuuint64_t)a.Hkv, (cuuint64_t)c->n_pages};
+    const cuuint64_t strides[3] = {(cuuint64_t)c->token_stride, (cuuint64_t)c->head_stride, (cuuint64_t)c->page_stride};
+    const cuuint32_t box[4] = {D, (cuuint32_t)std::min(c->page_size, 128), 1, 1};
+    return make_tmap_strided(m, p, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, dims, strides, box,
+                             D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
+  };
+  if (!map3(&mk, x.k) || !map3(&mv, x.v) || !map4(&mkc, x.cache->k) || !map4(&mvc, x.cache->v))
+    return cuda_fail("cuTensorMapEncodeTiled", 0, "tensor map rejected");
+  const auto kernel = serve8_kernel<D, R, F16>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+  if (e != cudaSuccess) return cuda_fail("cudaFuncSetAttribute", (int)e, cudaGetErrorName(e));
+  int sms = 0;
+  if (!sm_count(&sms)) return FA_ERR_CUDA;
+  a.part_rows = 2LL * sms * 2 * R;
+  a.part_lse = a.part_o + a.part_rows * D;
+  a.cuts = reinterpret_cast<int4*>(a.part_lse + a.part_rows);
+  const int rc = launch_pdl("serve8_kernel", kernel, dim3(sms), dim3(C::THREADS), C::SMEM_BYTES, stream, mk, mv, mkc, mvc, a);
+  if (rc != FA_OK || sms < 2) return rc;
+  return launch_pdl("serve8_join_kernel", serve8_join_kernel<D, R, F16>, dim3(sms - 1, 2 * R / 16), dim3(4 * D), 0, stream, a);
+}
+
+// Rows of a lane by the average rows of a sequence (the lengths are on the device): a lane of 16 fits
+// decoding and small drafts; with more rows than two lanes hold the keys are read again for the rest.
+template <int D, bool F16>
+static int launch_serve8_d(const Serve8Tensors& x, const Serve8Args& a, cudaStream_t stream) {
+  const long long rows = (long long)a.T * a.G;
+  if (rows <= 16LL * a.B) return launch_serve8_r<D, 16, F16>(x, a, stream);
+  if (rows <= 64LL * a.B) return launch_serve8_r<D, 32, F16>(x, a, stream);
+  return launch_serve8_r<D, 64, F16>(x, a, stream);
+}
+static int launch_serve8(const Serve8Tensors& x, const Serve8Args& a, int d, int dtype, cudaStream_t stream) {
+  const bool f16 = dtype == FA_FP16;
+  if (d == 64) return f16 ? launch_serve8_d<64, true>(x, a, stream) : launch_serve8_d<64, false>(x, a, stream);
+  return f16 ? launch_serve8_d<128, true>(x, a, stream) : launch_serve8_d<128, false>(x, a, stream);
 }
 
 }  // namespace fa
@@ -140,7 +1132,10 @@ using namespace fa::host;
 extern "C" {
 
 size_t fa_forward_tree_8bit_workspace_size(int d) {
-  return d == 64 || d == 128 ? 256 : 0;
+  if (d != 64 && d != 128) return 0;
+  int sms = 0;
+  if (!fa::sm_count(&sms)) return 0;
+  return (size_t)2 * sms * 128 * (d + 1) * 4 + (size_t)sms * 2 * sizeof(int4);
 }
 
 int fa_forward_tree_8bit(const fa_rows* q, const fa_rows* k, const fa_rows* v, const fa_rows* o, float* lse,
@@ -150,6 +1145,7 @@ int fa_forward_tree_8bit(const fa_rows* q, const fa_rows* k, const fa_rows* v, c
   int rc = check_sizes(B, T, Hq, Hkv, d, dtype, scale);
   if (rc != FA_OK) return rc;
   if (mask && (mask_words < 1 || mask_words > (1 << 20))) return mask_words < 1 ? FA_ERR_INVALID_ARG : FA_ERR_UNSUPPORTED;
+  if ((long long)T * (Hq / Hkv) > (1 << 30)) return FA_ERR_UNSUPPORTED;
   if (B == 0 || T == 0) return FA_OK;
   if ((rc = check_pages(cache, 16)) != FA_OK || (rc = check_scales(scales, cache->page_size)) != FA_OK) return rc;
   for (const fa_rows* r : {q, k, v, o})
@@ -162,25 +1158,20 @@ int fa_forward_tree_8bit(const fa_rows* q, const fa_rows* k, const fa_rows* v, c
   if (!status) return err;
   fa::Serve8Args a = {};
   a.q = static_cast<const uint16_t*>(q->data);
-  a.k = static_cast<const uint16_t*>(k->data);
-  a.v = static_cast<const uint16_t*>(v->data);
   a.o = static_cast<uint16_t*>(o->data);
   a.q_st = q->token_stride, a.q_sh = q->head_stride;
-  a.k_st = k->token_stride, a.k_sh = k->head_stride;
-  a.v_st = v->token_stride, a.v_sh = v->head_stride;
   a.o_st = o->token_stride, a.o_sh = o->head_stride;
   a.lse = lse;
-  a.kc = static_cast<const uint8_t*>(cache->k), a.vc = static_cast<const uint8_t*>(cache->v);
-  a.c_sp = cache->page_stride, a.c_sh = cache->head_stride, a.c_st = cache->token_stride;
   a.ks = scales->k, a.vs = scales->v, a.s_sp = scales->page_stride, a.s_sh = scales->head_stride;
   a.block_shift = log2_of(scales->block);
   a.n_pages = cache->n_pages, a.page_shift = log2_of(cache->page_size);
   a.table = cache->table, a.table_stride = cache->table_stride, a.table_width = cache->table_width;
   a.lens = lens, a.mask = mask, a.words = mask_words, a.cu = cu_nodes;
-  a.B = B, a.T = T, a.Hq = Hq, a.Hkv = Hkv, a.G = Hq / Hkv;
-  a.scale = scale;
+  a.B = B, a.T = T, a.Hkv = Hkv, a.G = Hq / Hkv;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.part_o = static_cast<float*>(workspace);
   a.status = status;
-  return fa::launch_serve8(a, d, dtype, reinterpret_cast<cudaStream_t>(stream));
+  return fa::launch_serve8({k, v, cache}, a, d, dtype, reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

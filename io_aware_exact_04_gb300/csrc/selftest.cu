@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(128, 1)
 
 struct Gemm8Args {
   float* out;
-  int N, d, a_mn, e5m2;
+  int N, d, a_mn, e5m2, b_mn, b_from;
   int* status;
 };
 
@@ -162,18 +162,19 @@ __global__ void __launch_bounds__(128, 1)
   const uint32_t tmem = *slot;
   bool ok = true;
   if (threadIdx.x == 0) {
-    mbar_arrive_expect_tx(load_bar, 128 * g.d + N * K);
+    mbar_arrive_expect_tx(load_bar, 128 * g.d + (g.b_mn ? 128 * g.b_mn : N * K));
     tma_load_2d(A0, &tm_a, 0, 0, load_bar);
     tma_load_2d(B0, &tm_b, 0, 0, load_bar);
     ok = wait_bounded(load_bar, 0, st, 100);
     if (ok) {
       tc_fence_after();
-      const uint32_t idesc = idesc_e4m3_f32(128, N, g.e5m2, g.a_mn);
+      const uint32_t idesc = idesc_e4m3_f32(128, N, g.e5m2, g.a_mn) | (g.b_mn ? 1u << 16 : 0u);
       const uint32_t row = g.d, hi_a = row == 64 ? sdesc_hi_sw64(512) : sdesc_hi(1024);
-      const uint32_t hi_b = K == 64 ? sdesc_hi_sw64(512) : sdesc_hi(1024);
+      const uint32_t hi_b = (g.b_mn ? g.b_mn : K) == 64 ? sdesc_hi_sw64(512) : sdesc_hi(1024);
       for (int k = 0; k < K / 32; ++k) {
         const uint32_t lo_a = sdesc_lo(A0 + (g.a_mn ? k * 32 * row : k * 32), g.a_mn ? 8192 : 16);
-        mma8_ss(tmem, sdesc_join(lo_a, hi_a), sdesc_join(sdesc_lo(B0 + k * 32, 16), hi_b), idesc, k > 0);
+        const uint32_t lo_b = sdesc_lo(B0 + (g.b_mn ? g.b_from + k * 32 * g.b_mn : k * 32), g.b_mn ? 8192 : 16);
+        mma8_ss(tmem, sdesc_join(lo_a, hi_a), sdesc_join(lo_b, hi_b), idesc, k > 0);
       }
       mma_commit(mma_bar);
     }
@@ -183,11 +184,11 @@ __global__ void __launch_bounds__(128, 1)
   if (__all_sync(0xffffffffu, ok)) {
     tc_fence_after();
     const int r = warp * 32 + lane;
-    for (int c = 0; c < N; c += 32) {
-      uint32_t v[32];
-      tmem_ld32(tmem + ((uint32_t)(warp * 32) << 16) + c, v);
+    for (int c = 0; c < N; c += 16) {
+      uint32_t v[16];
+      tmem_ld16(tmem + ((uint32_t)(warp * 32) << 16) + c, v);
       tmem_wait_ld();
-      for (int i = 0; i < 32; ++i) g.out[(size_t)r * N + c + i] = __uint_as_float(v[i]);
+      for (int i = 0; i < 16; ++i) g.out[(size_t)r * N + c + i] = __uint_as_float(v[i]);
     }
   }
   tc_fence_before();
@@ -246,20 +247,21 @@ int fa_selftest_mma(const void* a, const void* b, float* d, int N, int K, int mo
   return cudaPeekAtLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
-int fa_selftest_mma8(const void* a, const void* b, float* d_out, int N, int d, int a_mn, int e5m2, int* status,
-                     fa_stream_t stream) {
+int fa_selftest_mma8(const void* a, const void* b, float* d_out, int N, int d, int a_mn, int e5m2, int b_mn, int b_from,
+                     int* status, fa_stream_t stream) {
   if (!a || !b || !d_out || !status) return FA_ERR_INVALID_ARG;
-  if (N < 32 || N > 256 || N % 32 || (d != 64 && d != 128) || (a_mn | e5m2) & ~1) return FA_ERR_UNSUPPORTED;
+  if (b_mn && (!a_mn || (b_mn != 64 && b_mn != 128) || b_from < 0 || b_from % 16 || b_from + N > b_mn)) return FA_ERR_UNSUPPORTED;
+  if (N < 16 || N > 256 || N % 16 || (d != 64 && d != 128) || (a_mn | e5m2) & ~1) return FA_ERR_UNSUPPORTED;
   const int K = a_mn ? 128 : d;
   const auto U8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
   CUtensorMap ma, mb;
   if (!fa::make_tmap_2d(&ma, a, U8, 1, d, 128, d, 128, d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !fa::make_tmap_2d(&mb, b, U8, 1, K, N, K, N, K == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B))
+      !fa::make_tmap_2d(&mb, b, U8, 1, b_mn ? b_mn : K, b_mn ? 128 : N, b_mn ? b_mn : K, b_mn ? 128 : N, (b_mn ? b_mn : K) == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B))
     return FA_ERR_CUDA;
   const int smem = 49152 + 256 + 1024;
   if (cudaFuncSetAttribute(fa::selftest_gemm8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return FA_ERR_CUDA;
-  fa::Gemm8Args g{d_out, N, d, a_mn, e5m2, status};
+  fa::Gemm8Args g{d_out, N, d, a_mn, e5m2, b_mn, b_from, status};
   fa::selftest_gemm8_kernel<<<1, 128, smem, reinterpret_cast<cudaStream_t>(stream)>>>(ma, mb, g);
   return cudaPeekAtLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
