@@ -52,8 +52,9 @@ struct Serve8Args {
 //    p1 + p2 + (p3 + p4) / 64, each the e5m2 nearest to what is left (bf16 does without p4). With the
 //    range of e5m2, 2^-16 to 2^15, three parts round a probability by half a step of 2^-8 of itself
 //    (2^-9), four by 2^-12, and either by no more than 2^-34 of the row's largest. (e4m3 would need as
-//    many parts and end at 2^-26.) The reference maximum moves when it grows by 2^4, so that P stays
-//    within 2^15.
+//    many parts and end at 2^-26.) Each has columns of O of its own: one product of N = 3 R or 4 R columns
+//    takes 40 to 58 cycles, one of 16 takes 36. The reference maximum moves when it grows by 2^4, so
+//    that P stays within 2^15.
 //  - The scale of a key's block multiplies its scores, that of its values its probability, which is kept
 //    in range by a reference of its own (vref, at least each scale that was met).
 //
@@ -66,10 +67,15 @@ struct Serve8Args {
 // and join their results at the end. All tiles of all items form one sequence, of which every CTA
 // takes an equal run; items cut between CTAs leave fp32 partial results for serve8_join_kernel.
 //
-// Roles, 448 threads: warps 0-3 and 4-7 the softmax of lanes 0 and 1 (a thread a key; with all 16 rows of
-// a step in registers, a maximum over the keys is needed only where some score passes the reference,
-// which one barrier's vote decides), warp 8 the TMA producer and scheduler, 9 the issuer of S, 10 and 11
-// those of O, 12 and 13 split Q.
+// Roles, 448 threads: warps 0-3 and 4-7 the softmax of lanes 0 and 1, a thread a key, warp 8 the TMA
+// producer and scheduler, 9 the issuer of S, 10 and 11 those of O, 12 and 13 split Q.
+//
+// The softmax needs a maximum over the keys, across its threads, only where a reference moves: for the
+// first tile of an item, and where some score passes the reference by more than it may. A vote of the four
+// warps says so, taken while P is formed as if nothing moved (with four warps in step, latency bounds a
+// tile: a wait costs 100 to 200 cycles, also where its phase has completed). S has two buffers, so that the next one is
+// formed meanwhile, and so has P with lanes of 16 rows. Rows come in classes of 4, 8, 16 (or 16, 32): the
+// columns of others are never looked at, and what stands in them stays in them.
 template <int D, int R, bool F16>
 struct Serve8Cfg {
   static constexpr int ROW = D;                      // bytes of a cached row
@@ -78,35 +84,36 @@ struct Serve8Cfg {
   static constexpr int NSUB = D / 64;                // 64-column halves of their rows
   static constexpr int QPARTS = F16 ? 3 : 2;
   static constexpr int Q16 = QPARTS * R * D, QSLOT = Q16 + R * D * 2;
-  static constexpr int NQ = R == 16 ? 4 : R == 32 ? 3 : 2;
-  // P: [key][p1 | p3] and [p2 | p4] of R bytes each; one 64- or 128-byte row a key where they fit
-  static constexpr int PX = R == 16 ? 64 : 128;      // bytes of a key's row
-  static constexpr int PY = R == 64 && !F16 ? 64 : PX;
-  static constexpr int OFF_Y = R == 64 ? 128 * PX : 2 * R;  // of [p2 | p4] against [p1 | p3]
-  static constexpr int PBYTES = R == 64 ? 128 * (PX + PY) : 128 * PX;
-  static constexpr int MISC = 512 + 256 + 12 * 64 + NQ * R * 4 + 2 * R * (8 + 8 + 8 + 4) + 2 * 4 * (R + 4) * 4 + 64;
-  static constexpr int FIXED = 2 * PBYTES + NQ * QSLOT + MISC;
+  static constexpr int NQ = R == 16 ? 4 : 3;
+  static constexpr int PPARTS = F16 ? 4 : 3;
+  static constexpr int PX = 4 * R;                   // P: bytes of a key's row, [p1 | p2 | p3 | p4] of R bytes each
+  static constexpr int NP = R == 16 ? 2 : 1;         // buffers of P
+  static constexpr int PBYTES = 128 * PX;
+  static constexpr int QROW = 16;                    // of a row of Q: factor of its scores, token, place in O (8 bytes)
+  static constexpr int MISC = 512 + 256 + 12 * 64 + NQ * R * QROW + 2 * (R + R + R + 4 * R + 4 * (R + 4)) * 4 + 64;
+  static constexpr int FIXED = 2 * NP * PBYTES + NQ * QSLOT + MISC;
   static constexpr int NT = (232448 - FIXED) / ENTRY < 12 ? (232448 - FIXED) / ENTRY : 12;
-  static constexpr int OFF_P = NT * ENTRY, OFF_Q = OFF_P + 2 * PBYTES, OFF_BAR = OFF_Q + NQ * QSLOT;
-  static constexpr int OFF_DESC = OFF_BAR + 512, OFF_SC = OFF_DESC + 256, OFF_QS = OFF_SC + 12 * 64;
-  static constexpr int OFF_ROWC = OFF_QS + NQ * R * 4, OFF_OROW = OFF_ROWC + 2 * R * 8, OFF_ML = OFF_OROW + 2 * R * 8;
-  static constexpr int OFF_TOK = OFF_ML + 2 * R * 8, OFF_RED = OFF_TOK + 2 * R * 4, OFF_VREF = OFF_RED + 2 * 4 * (R + 4) * 4;
-  static constexpr int SMEM_BYTES = OFF_VREF + 64;
-  __device__ static constexpr uint32_t tm_s(int t) { return 2u * R * t; }
-  __device__ static constexpr uint32_t tm_o(int t) { return 4u * R + 2u * R * t; }
-  static constexpr uint32_t TM_COLS = 8 * R;
+  static constexpr int OFF_P = NT * ENTRY, OFF_Q = OFF_P + 2 * NP * PBYTES, OFF_BAR = OFF_Q + NQ * QSLOT;
+  static constexpr int OFF_DESC = OFF_BAR + 512, OFF_SC = OFF_DESC + 256, OFF_QROW = OFF_SC + 12 * 64;
+  // of each lane: 11 - reference of each row, factors of a move; of the item before: reference, sums of each warp
+  static constexpr int OFF_NB = OFF_QROW + NQ * R * QROW, OFF_FAC = OFF_NB + 2 * R * 4, OFF_REF = OFF_FAC + 2 * R * 4;
+  static constexpr int OFF_SUM = OFF_REF + 2 * R * 4, OFF_RED = OFF_SUM + 2 * 4 * R * 4;
+  static constexpr int OFF_FLAG = OFF_RED + 2 * 4 * (R + 4) * 4, SMEM_BYTES = OFF_FLAG + 64;
+  __device__ static constexpr uint32_t tm_s(int t, int u) { return 4u * R * t + 2u * R * u; }
+  __device__ static constexpr uint32_t tm_o(int t) { return 8u * R + 4u * R * t; }
+  static constexpr uint32_t TM_COLS = 16 * R;
   static constexpr int THREADS = 448, PRODUCER = 8, S_BOTH = 9, PV0 = 10, PV1 = 11, SPLIT = 12;
   // barriers
-  static constexpr int FULL = 0, EMPTY = NT, Q_FULL = 2 * NT, Q_EMPTY = Q_FULL + NQ, S_FULL = Q_EMPTY + NQ, S_FREE = S_FULL + 2,
-                       P_READY = S_FREE + 2, O_DONE = P_READY + 2, O_FREE = O_DONE + 2, MERGE = O_FREE + 2, DRAIN = MERGE + 1,
-                       D_FULL = DRAIN + 1, D_EMPTY = D_FULL + 4, BARS = D_EMPTY + 4;
+  static constexpr int FULL = 0, EMPTY = NT, Q_FULL = 2 * NT, Q_EMPTY = Q_FULL + NQ, S_FULL = Q_EMPTY + NQ, S_FREE = S_FULL + 4,
+                       P_READY = S_FREE + 4, O_DONE = P_READY + 2, O_FREE = O_DONE + 4, MERGE = O_FREE + 2, DRAIN = MERGE + 1,
+                       GROUP = DRAIN + 1, D_FULL = GROUP + 2, D_EMPTY = D_FULL + 4, BARS = D_EMPTY + 4;
   static_assert(8 * BARS + 12 <= 512, "barrier area");
   static_assert(NT >= 2 && SMEM_BYTES <= 232448, "shared memory");
   static_assert(OFF_P % 1024 == 0 && OFF_Q % 1024 == 0 && QSLOT % 1024 == 0 && Q16 % 1024 == 0 && OFF_BAR % 16 == 0, "alignment");
 };
 
 enum { SITE_T8_EMPTY = 80, SITE_T8_FULL, SITE_T8_Q_FULL, SITE_T8_Q_EMPTY, SITE_T8_S_FULL, SITE_T8_S_FREE, SITE_T8_P_READY,
-       SITE_T8_O_DONE, SITE_T8_O_FREE, SITE_T8_MERGE, SITE_T8_DESC_FULL, SITE_T8_DESC_EMPTY, SITE_T8_V_FULL };
+       SITE_T8_O_DONE, SITE_T8_O_FREE, SITE_T8_MERGE, SITE_T8_DESC_FULL, SITE_T8_DESC_EMPTY, SITE_T8_V_FULL, SITE_T8_GROUP };
 
 constexpr float kNoKey = -1e30f;     // reference maximum of a row that has met no key
 constexpr float kPLog2 = 11.f, kLagLog2 = 4.f;
@@ -226,7 +233,6 @@ __device__ __forceinline__ float warp_max(float x) {
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(x));
   return m;
 }
-__device__ __forceinline__ bool bar_or(uint32_t id, bool x) { return !named_bar_and(id, 128, !x); }
 __device__ __forceinline__ uint32_t h2_sub(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -244,6 +250,9 @@ __device__ __forceinline__ uint32_t to_e5m2(uint32_t x) { return (x + 0x00800080
 __device__ __forceinline__ uint32_t upper_bytes(uint32_t lo, uint32_t hi) { return __byte_perm(lo, hi, 0x7531); }
 __device__ __forceinline__ void sts128(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+__device__ __forceinline__ void sts32(uint32_t at, uint32_t x) {
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(x) : "memory");
 }
 __device__ __forceinline__ void sts64(uint32_t at, uint32_t x, uint32_t y) {
   asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(x), "r"(y) : "memory");
@@ -279,6 +288,33 @@ __device__ __forceinline__ void halves(uint32_t w, float& lo, float& hi) {
     lo = __uint_as_float(w << 16), hi = __uint_as_float(w & 0xffff0000u);
   }
 }
+// N columns of the warp's 32 lanes.
+template <int N>
+__device__ __forceinline__ void tmem_ldn(uint32_t taddr, uint32_t (&r)[N]) {
+  static_assert(N == 2 || N == 4 || N == 8 || N == 16, "");
+  if constexpr (N == 2)
+    tmem_ld2(taddr, r);
+  else if constexpr (N == 4)
+    tmem_ld4(taddr, r);
+  else if constexpr (N == 8)
+    tmem_ld8(taddr, r);
+  else
+    tmem_ld16(taddr, r);
+}
+template <int N>
+__device__ __forceinline__ void tmem_stn(uint32_t taddr, const uint32_t (&r)[N]) {
+  static_assert(N == 4 || N == 8 || N == 16, "");
+  if constexpr (N == 4)
+    tmem_st4(taddr, r);
+  else if constexpr (N == 8)
+    tmem_st8(taddr, r);
+  else
+    tmem_st16(taddr, r);
+}
+template <int N>
+struct Rows8 {
+  static constexpr int value = N;
+};
 template <bool F16>
 __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
   return F16 ? pack_f16x2(lo, hi) : pack_bf16x2(lo, hi);
@@ -289,7 +325,7 @@ __global__ void __launch_bounds__(448, 1)
     serve8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                   const __grid_constant__ CUtensorMap tm_kc, const __grid_constant__ CUtensorMap tm_vc, Serve8Args a) {
   using C = Serve8Cfg<D, R, F16>;
-  constexpr int NT = C::NT, NQ = C::NQ, CH = R / 16;
+  constexpr int NT = C::NT, NQ = C::NQ;
   // 1024-byte aligned, as the swizzled tiles have to be: there is no room to round the address up
   extern __shared__ __align__(1024) uint8_t sm[];
   const uint32_t sbase = smem_u32(sm);
@@ -309,7 +345,12 @@ __global__ void __launch_bounds__(448, 1)
   DevStatus st{a.status, abort_flag};
   int* descs = reinterpret_cast<int*>(sm + C::OFF_DESC);
   float* scales = reinterpret_cast<float*>(sm + C::OFF_SC);  // [entry][K of 8 groups of 16 keys, V of 8]
-  float* qscale = reinterpret_cast<float*>(sm + C::OFF_QS);  // [slot][row]
+  struct __align__(16) QRow {
+    float factor;  // of the row's scores, to base 2
+    int tok;       // its token within the sequence; -1: no row
+    long long to;  // head << 40 | packed token
+  };
+  QRow* qrows = reinterpret_cast<QRow*>(sm + C::OFF_QROW);  // [slot][row]
 
   if (warp == C::PRODUCER && lane == 0) {
     for (int i = 0; i < NT; ++i) {
@@ -318,14 +359,17 @@ __global__ void __launch_bounds__(448, 1)
     }
     for (int i = 0; i < NQ; ++i) {
       mbar_init(BAR(C::Q_FULL + i), 2);
-      mbar_init(BAR(C::Q_EMPTY + i), 3);  // the issuer of S, and both lanes' rows, or one's twice
+      mbar_init(BAR(C::Q_EMPTY + i), 9);  // the issuer of S, and both lanes' warps, or one's twice
     }
     for (int t = 0; t < 2; ++t) {
-      mbar_init(BAR(C::S_FULL + t), 1);
-      mbar_init(BAR(C::S_FREE + t), 4);
+      for (int u = 0; u < 2; ++u) {
+        mbar_init(BAR(C::S_FULL + 2 * t + u), 1);
+        mbar_init(BAR(C::S_FREE + 2 * t + u), 4);
+        mbar_init(BAR(C::O_DONE + 2 * t + u), 1);
+      }
       mbar_init(BAR(C::P_READY + t), 4);
-      mbar_init(BAR(C::O_DONE + t), 1);
       mbar_init(BAR(C::O_FREE + t), 8);  // four warps twice, or all eight in a join
+      mbar_init(BAR(C::GROUP + t), 4);
     }
     mbar_init(BAR(C::MERGE), 8);
     mbar_init(BAR(C::DRAIN), 3);
@@ -553,7 +597,13 @@ __global__ void __launch_bounds__(448, 1)
           for (int z = 0; z < C::QPARTS; ++z)
             sts64(q8 + swizzled<C::ROW>(z * R + r, c >> 1) + (c & 1) * 8, part[z][0] | part[z][1] << 16,
                   part[z][2] | part[z][3] << 16);
-          if (c == 0) qscale[s * R + r] = up;
+          if (c == 0) {
+            const int rr = it.r0 + t * R + r, tok = rr / a.G;
+            QRow* to = qrows + s * R + r;
+            to->factor = rr < rows ? up * a.scale_log2 : 0.f;
+            to->tok = rr < rows ? tok : -1;
+            to->to = (long long)(it.kvh * a.G + rr - tok * a.G) << 40 | (long long)(it.row0 + tok);
+          }
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -574,45 +624,46 @@ __global__ void __launch_bounds__(448, 1)
       constexpr uint32_t I8 = idesc_e4m3_f32(128, 2 * R, 0, 0), I8X = idesc_e4m3_f32(128, R, 0, 0);
       constexpr uint32_t I16 = F16 ? idesc_f16_f32(128, R, 0, 0) : idesc_bf16_f32(128, R, 0, 0);
       constexpr uint32_t HI = desc_hi<C::ROW>(), HI16 = sdesc_hi(1024);
+      const uint32_t ring_lo = sdesc_lo(sbase, 16), q_lo = sdesc_lo(sbase + C::OFF_Q, 16);
       int uq = 0, used[2] = {0, 0};
       for (int i = 0; ok; ++i) {
         Item8 it;
         if (!next_item(i, &it) || it.cnt < 0) break;
         const bool dual = it.flags & ITEM8_DUAL;
         const int nq = dual ? 1 : 2;
+        const int slot0 = uq % NQ, slot1 = (uq + 1) % NQ;
         for (int u = uq; ok && u < uq + nq; ++u)
           ok = wait_phase(BAR(C::Q_FULL + u % NQ), (u / NQ) & 1, st, SITE_T8_Q_FULL);
         for (int k = 0; ok && k < it.cnt; ++k, ++e) {
           const int j = it.j0 + k, s = e % NT;
           if (!(ok = wait_phase(BAR(C::FULL + s), (e / NT) & 1, st, SITE_T8_FULL))) break;
-          const uint32_t ka = sdesc_lo(sbase + s * C::ENTRY, 16);
+          const uint32_t ka = ring_lo + s * (C::ENTRY >> 4);
+#pragma unroll
           for (int t = 0; t < 2; ++t) {
             if (dual ? (k & 1) != t : k >= (t ? it.c1 : it.c0)) continue;
-            // S of the tile before is in registers
-            if (used[t] > 0 && !(ok = wait_phase(BAR(C::S_FREE + t), (used[t] - 1) & 1, st, SITE_T8_S_FREE))) break;
-            ++used[t];
+            const int g = used[t]++, u = g & 1;
+            // S of two tiles before is in registers
+            if (g > 1 && !(ok = wait_phase(BAR(C::S_FREE + 2 * t + u), ((g >> 1) - 1) & 1, st, SITE_T8_S_FREE))) break;
             tc_fence_after();
-            const uint32_t d = tmem + C::tm_s(t), slot = sbase + C::OFF_Q + (uq + (dual ? 0 : t)) % NQ * C::QSLOT;
+            const uint32_t d = tmem + C::tm_s(t, u), qb = q_lo + (t && !dual ? slot1 : slot0) * (C::QSLOT >> 4);
             if (j < it.nc) {
-              const uint32_t qb = sdesc_lo(slot, 16);
 #pragma unroll
               for (int x = 0; x < D / 32; ++x)
                 if (elect_one()) mma8_ss(d, sdesc_join(ka + 2 * x, HI), sdesc_join(qb + 2 * x, HI), I8, x > 0);
               if (F16) {
-                const uint32_t qc = sdesc_lo(slot + 2 * R * D, 16);
 #pragma unroll
                 for (int x = 0; x < D / 32; ++x)
-                  if (elect_one()) mma8_ss(d + R, sdesc_join(ka + 2 * x, HI), sdesc_join(qc + 2 * x, HI), I8X, 1);
+                  if (elect_one()) mma8_ss(d + R, sdesc_join(ka + 2 * x, HI), sdesc_join(qb + (2 * R * D >> 4) + 2 * x, HI), I8X, 1);
               }
             } else {
-              const uint32_t qb = sdesc_lo(slot + C::Q16, 16);
 #pragma unroll
               for (int x = 0; x < D / 16; ++x) {
-                const uint32_t ko = ((x >> 2) * (C::NEW * 128) + (x & 3) * 32) >> 4, qo = ((x >> 2) * (R * 128) + (x & 3) * 32) >> 4;
+                const uint32_t ko = ((x >> 2) * (C::NEW * 128) + (x & 3) * 32) >> 4;
+                const uint32_t qo = (C::Q16 + (x >> 2) * (R * 128) + (x & 3) * 32) >> 4;
                 if (elect_one()) mma_ss(d, sdesc_join(ka + ko, HI16), sdesc_join(qb + qo, HI16), I16, x > 0);
               }
             }
-            commit(BAR(C::S_FULL + t));
+            commit(BAR(C::S_FULL + 2 * t + u));
           }
           if (!ok) break;
         }
@@ -622,12 +673,12 @@ __global__ void __launch_bounds__(448, 1)
     } else {
       // O^T += V^T P^T of lane t
       const int t = warp == C::PV1;
-      constexpr uint32_t IX = idesc_e4m3_f32(128, 2 * R, 1, 1) | 1u << 16;                  // [p1 | p3]
-      constexpr uint32_t IY = idesc_e4m3_f32(128, F16 ? 2 * R : R, 1, 1) | 1u << 16;        // [p2 | p4], [p2]
+      constexpr uint32_t I8 = idesc_e4m3_f32(128, C::PPARTS * R, 1, 1) | 1u << 16;
       constexpr uint32_t I16 = F16 ? idesc_f16_f32(128, R, 1, 1) : idesc_bf16_f32(128, R, 1, 1);
-      constexpr uint32_t HIV = desc_hi<C::ROW>(), HIX = desc_hi<C::PX>(), HIY = desc_hi<C::PY>(), HI16 = sdesc_hi(1024);
-      const uint32_t d = tmem + C::tm_o(t), p0 = sbase + C::OFF_P + t * C::PBYTES;
-      int used = 0, items = 0;
+      constexpr uint32_t HIV = desc_hi<C::ROW>(), HIP = desc_hi<C::PX>(), HI16 = sdesc_hi(1024);
+      const uint32_t d = tmem + C::tm_o(t), p_lo = sdesc_lo(sbase + C::OFF_P + t * C::NP * C::PBYTES, 8192);
+      const uint32_t v_lo = sdesc_lo(sbase + C::KV, 8192);
+      int g = 0, items = 0;
       for (int i = 0; ok; ++i) {
         Item8 it;
         if (!next_item(i, &it) || it.cnt < 0) break;
@@ -645,37 +696,36 @@ __global__ void __launch_bounds__(448, 1)
           }
           const int j = it.j0 + k, rows = rows_here(it, j);
           const bool cached = j < it.nc;
-          const int step = cached ? 32 : 16, steps = (rows + step - 1) / step;
-          uint8_t* v = sm + s * C::ENTRY + C::KV;
-          if (rows < steps * step) {
+          if (rows < (cached ? 128 : C::NEW)) {
             // rows past the sequence may hold anything; P is 0 there, but 0 x NaN is not
-            const int pitch = cached ? C::ROW : 128, chunks = (steps * step - rows) * pitch / 16;
+            uint8_t* v = sm + s * C::ENTRY + C::KV;
+            const int pitch = cached ? C::ROW : 128, chunks = ((cached ? 128 : C::NEW) - rows) * pitch / 16;
             for (int z = lane; z < chunks * (cached ? 1 : C::NSUB); z += 32)
               *reinterpret_cast<uint4*>(v + rows * pitch + z / chunks * (C::NEW * 128) + z % chunks * 16) = make_uint4(0, 0, 0, 0);
             fence_proxy_async_smem();
             __syncwarp();
           }
-          if (!(ok = wait_phase(BAR(C::P_READY + t), used & 1, st, SITE_T8_P_READY))) break;
+          if (!(ok = wait_phase(BAR(C::P_READY + t), g & 1, st, SITE_T8_P_READY))) break;
           if (first && items > 0 && !(ok = wait_phase(BAR(C::O_FREE + t), (items - 1) & 1, st, SITE_T8_O_FREE))) break;
-          ++used;
           tc_fence_after();
-          const uint32_t va = smem_u32(v);
-          if (cached) {
-            for (int x = 0; x < steps; ++x) {
-              const uint64_t av = sdesc_join(sdesc_lo(va + x * 32 * C::ROW, 8192), HIV);
-              if (elect_one()) mma8_ss(d, av, sdesc_join(sdesc_lo(p0 + x * 32 * C::PX, 8192), HIX), IX, !first || x > 0);
-              if (elect_one()) mma8_ss(d, av, sdesc_join(sdesc_lo(p0 + C::OFF_Y + x * 32 * C::PY, 8192), HIY), IY, 1);
-            }
-          } else {
-            for (int x = 0; x < steps; ++x) {
-              const uint64_t av = sdesc_join(sdesc_lo(va + x * 2048, C::NEW * 128), HI16);
-              if (elect_one()) mma_ss(d, av, sdesc_join(sdesc_lo(p0 + x * 16 * C::PX, 8192), HIX), I16 , !first || x > 0);
-            }
+          const uint32_t va = v_lo + s * (C::ENTRY >> 4), pa = p_lo + (C::NP == 2 ? (g & 1) * (C::PBYTES >> 4) : 0);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            if (!elect_one()) continue;
+            if (cached)
+              mma8_ss(d, sdesc_join(va + x * (32 * C::ROW >> 4), HIV), sdesc_join(pa + x * (32 * C::PX >> 4), HIP), I8, !first || x > 0);
+            else
+              mma_ss(d, sdesc_join(va + x * (2048 >> 4), HI16), sdesc_join(pa + x * (16 * C::PX >> 4), HIP), I16, !first || x > 0);
           }
-          commit(BAR(C::O_DONE + t));
-          commit(BAR(C::EMPTY + s));
-          if (dual) commit(BAR(C::EMPTY + s));
+          __syncwarp();
+          if (elect_one()) {
+            mma_commit(BAR(C::O_DONE + 2 * t + (g & 1)));
+            mma_commit(BAR(C::EMPTY + s));
+            if (dual) mma_commit(BAR(C::EMPTY + s));
+          }
+          __syncwarp();
           first = false;
+          ++g;
         }
         items += tiles > 0;
       }
@@ -687,343 +737,372 @@ __global__ void __launch_bounds__(448, 1)
     }
   } else {
     // ------------------------------------------------------------ softmax of lane t, a thread a key
-    // The four warps meet at named barriers, which know no limit: a warp whose wait has run out goes on to
-    // the next of them (without further waits) and says so there, and all four leave together.
     const int t = warp >> 2, wq = warp & 3, key = wq * 32 + lane;
-    const uint32_t bar_id = 1 + t, tlane = (uint32_t)(wq * 32) << 16;
-    const float sl2 = a.scale_log2;
-    float2* rowc = reinterpret_cast<float2*>(sm + C::OFF_ROWC) + t * R;  // {factor of a row's scores, 11 - its reference}
-    long long* orow = reinterpret_cast<long long*>(sm + C::OFF_OROW) + t * R;  // head << 40 | token, or -1
-    int* tok = reinterpret_cast<int*>(sm + C::OFF_TOK) + t * R;
+    const uint32_t tlane = (uint32_t)(wq * 32) << 16;
+    float* nbs = reinterpret_cast<float*>(sm + C::OFF_NB) + t * R;
+    float* facs = reinterpret_cast<float*>(sm + C::OFF_FAC) + t * R;
+    float* refs = reinterpret_cast<float*>(sm + C::OFF_REF);
+    float* sums = reinterpret_cast<float*>(sm + C::OFF_SUM);
     float* red = reinterpret_cast<float*>(sm + C::OFF_RED) + t * 4 * (R + 4);
-    float2* ml = reinterpret_cast<float2*>(sm + C::OFF_ML);
-    float* vrefs = reinterpret_cast<float*>(sm + C::OFF_VREF);
-    const uint32_t pbuf = sbase + C::OFF_P + t * C::PBYTES;
-    int uq = 0, e0 = 0, used = 0, merges = 0;
-    for (int i = 0;; ++i) {
-      Item8 it;
-      bool ok = next_item(i, &it);
+    volatile int* flags = reinterpret_cast<int*>(sm + C::OFF_FLAG) + 2 * t;
+    float* vrefs = reinterpret_cast<float*>(sm + C::OFF_FLAG) + 4;
+    if (lane == 0 && wq == 0) flags[0] = flags[1] = 0;  // (read after a phase of GROUP)
+    int uq = 0, e0 = 0, g = 0, merges = 0, meets = 0;  // Q slots, ring entries, tiles, joins, phases of GROUP so far
+    auto meet_arrive = [&] {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(BAR(C::GROUP + t));
+    };
+    auto meet = [&] {  // the four warps
+      meet_arrive();
+      return wait_phase(BAR(C::GROUP + t), meets++ & 1, st, SITE_T8_GROUP);
+    };
+    auto wait_pv = [&](int x) {  // tile x of the lane is in O, its P is read
+      return wait_phase(BAR(C::O_DONE + 2 * t + (x & 1)), (x >> 1) & 1, st, SITE_T8_O_DONE);
+    };
+    // One item, for lanes of which the first RV rows matter
+    auto run_item = [&](const Item8& it, auto rv) {
+      constexpr int RV = decltype(rv)::value, W = RV < 16 ? RV : 16;  // rows, and rows at a time
       const bool dual = it.flags & ITEM8_DUAL;
-      const int slot = (uq + (dual ? 0 : t)) % NQ;
-      if (ok && it.cnt >= 0) ok = wait_phase(BAR(C::Q_FULL + slot), ((uq + (dual ? 0 : t)) / NQ) & 1, st, SITE_T8_Q_FULL);
-      // (also: all four warps are done with the rows of the item before)
-      if (bar_or(bar_id, !ok) || it.cnt < 0) break;
-      {
-        const int rr = it.r0 + (dual ? 0 : t * R) + key;
-        if (key < R) {
-          const bool there = rr < it.n * a.G;
-          const int tk = rr / a.G;
-          rowc[key] = make_float2(there ? qscale[slot * R + key] * sl2 : 0.f, there ? kPLog2 - kNoKey : kNoKey);
-          orow[key] = there ? (long long)(it.kvh * a.G + rr - tk * a.G) << 40 | (long long)(it.row0 + tk) : -1;
-          tok[key] = there ? tk : -1;
-        }
-      }
-      named_bar_sync(bar_id, 128);
-      if (wq == 0 && lane == 0) mbar_arrive_n(BAR(C::Q_EMPTY + slot), dual ? 1 : 2);
-      uq += dual ? 1 : 2;
-      const int steps = t ? it.c1 : it.c0;
-      float l[R];
+      const int slot = (uq + (dual ? 0 : t)) % NQ, steps = t ? it.c1 : it.c0;
+      const QRow* qr = qrows + slot * R;
+      float l[RV];
 #pragma unroll
-      for (int r = 0; r < R; ++r) l[r] = 0.f;
+      for (int r = 0; r < RV; ++r) l[r] = 0.f;
       float vref = 1.1754944e-38f;
-      bool give_up = false;
-      for (int s = 0; s < steps; ++s, ++used) {
+      for (int s = 0; s < steps; ++s, ++g) {
         const int k = dual ? 2 * s + t : s, j = it.j0 + k, es = (e0 + k) % NT;
         const bool cached = j < it.nc;
-        ok = ok && wait_phase(BAR(C::S_FULL + t), used & 1, st, SITE_T8_S_FULL);
+        if (!wait_phase(BAR(C::S_FULL + 2 * t + (g & 1)), (g >> 1) & 1, st, SITE_T8_S_FULL)) return false;
         tc_fence_after();
         const bool there = key < rows_here(it, j);
         const float kscale = cached ? scales[es * 16 + (key >> 4)] : 1.f;
         const float vscale = cached ? scales[es * 16 + 8 + (key >> 4)] : 1.f;
-        const int nkey = (j - it.nc) * C::NEW + key;  // of a new token, within its sequence
-        bool pv_waited = s == 0;  // (its P has been read; across items the epilogue waited for that)
-        auto wait_pv = [&] {
-          if (!pv_waited) ok = ok && wait_phase(BAR(C::O_DONE + t), (used - 1) & 1, st, SITE_T8_O_DONE);
-          pv_waited = true;
-          tc_fence_after();
-        };
-        const bool to_one = !cached && vref != 1.f;
-        float w = 0.f;
-#pragma unroll
-        for (int ch = 0; ch < CH; ++ch) {
-          float y[16];
-          {
-            uint32_t x0[16], x1[16];
-            tmem_ld16(tmem + tlane + C::tm_s(t) + ch * 16, x0);
-            if (cached) tmem_ld16(tmem + tlane + C::tm_s(t) + R + ch * 16, x1);
-            tmem_wait_ld();
-            const float k16 = kscale * 0.0625f;
-#pragma unroll
-            for (int r = 0; r < 16; ++r)
-              y[r] = cached ? fmaf(__uint_as_float(x1[r]), k16, __uint_as_float(x0[r]) * kscale) : __uint_as_float(x0[r]);
-          }
-          if (ch == CH - 1) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(BAR(C::S_FREE + t));
-          }
-          uint32_t seen = there ? 0xffffu : 0u;
-          if (!cached && there) {
-            seen = 0;
+        const uint32_t ts = tmem + tlane + C::tm_s(t, g & 1);
+        uint32_t seen = there ? 0xffffffffu : 0u;  // of the rows
+        if (!cached && there) {
+          const int nkey = (j - it.nc) * C::NEW + key;  // the new token within its sequence
+          seen = 0;
 #pragma unroll 1
-            for (int r = 0; r < 16; ++r) {
-              const int tk = tok[ch * 16 + r];
-              bool sees = nkey <= tk;
-              if (a.mask)
-                sees = tk >= 0 && (nkey >> 5) < a.words &&
-                       (a.mask[(long long)(it.row0 + tk) * a.words + (nkey >> 5)] >> (nkey & 31) & 1);
-              seen |= (uint32_t)sees << r;
-            }
+          for (int r = 0; r < RV; ++r) {
+            const int tk = qr[r].tok;
+            bool sees = nkey <= tk;
+            if (a.mask)
+              sees = tk >= 0 && (nkey >> 5) < a.words &&
+                     (a.mask[(long long)(it.row0 + tk) * a.words + (nkey >> 5)] >> (nkey & 31) & 1);
+            seen |= (uint32_t)sees << r;
           }
-          float tt[16], top = -INFINITY;
+        }
+        // rows [c, c + W): scores to base 2 without their rows' factors
+        auto load_y = [&](int c, float (&y)[W]) {
+          uint32_t x0[W], x1[W];
+          tmem_ldn<W>(ts + c, x0);
+          if (cached) tmem_ldn<W>(ts + R + c, x1);
+          tmem_wait_ld();
+          const float k16 = kscale * 0.0625f;
 #pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            const float2 rc = rowc[ch * 16 + r];
-            const float x = fmaf(y[r], cached ? rc.x : sl2, rc.y);
-            tt[r] = (seen >> r & 1) ? x : -INFINITY;
-            top = fmaxf(top, tt[r]);
-          }
-          const bool grows = top > kPLog2 + kLagLog2 || (ch == 0 && ((there && cached && vscale > vref) || to_one));
-          if (bar_or(bar_id, grows || !ok)) {
-            // a reference moves: the largest score of each row over the tile
-            if (bar_or(bar_id, !ok)) {
-              give_up = true;
-              break;
-            }
-            float mine = 0.f;
+          for (int r = 0; r < W; ++r)
+            y[r] = cached ? fmaf(__uint_as_float(x1[r]), k16, __uint_as_float(x0[r]) * kscale) : __uint_as_float(x0[r]);
+        };
+        // References move: for the first tile, or where a score or a scale has passed its own.
+        auto move = [&] {
+#pragma unroll 1
+          for (int c = 0; c < RV; c += W) {
+            float y[W], mine = 0.f;
+            load_y(c, y);
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-              const float2 rc = rowc[ch * 16 + r];
-              const float m = warp_max((seen >> r & 1) ? y[r] * (cached ? rc.x : sl2) : -INFINITY);
+            for (int r = 0; r < W; ++r) {
+              const float f = cached ? qr[c + r].factor : a.scale_log2;
+              const float m = warp_max((seen >> (c + r) & 1) ? y[r] * f : -INFINITY);
               if (lane == r) mine = m;
             }
-            if (lane < 16) red[wq * (R + 4) + ch * 16 + lane] = mine;
-            const float vm = warp_max(there && cached ? vscale : 0.f);
-            if (lane == 0) red[wq * (R + 4) + R] = vm;
-            named_bar_sync(bar_id, 128);
-            float fv = 1.f;  // of all rows, as the reference of the values' scales moves
-            if (ch == 0) {
-              float v = 0.f;
+            if (lane < W) red[wq * (R + 4) + c + lane] = mine;
+          }
+          const float vm = warp_max(there && cached ? vscale : 0.f);
+          if (lane == 0) red[wq * (R + 4) + R] = vm;
+          if (!meet()) return false;
+          float v = 0.f;
 #pragma unroll
-              for (int x = 0; x < 4; ++x) v = fmaxf(v, red[x * (R + 4) + R]);
-              const float to = to_one ? 1.f : v > vref ? 2.f * v : vref;
-              fv = vref / to;
-              vref = to;
+          for (int x = 0; x < 4; ++x) v = fmaxf(v, red[x * (R + 4) + R]);
+          const float to = !cached ? 1.f : v > vref ? 2.f * v : vref, fv = s == 0 ? 1.f : vref / to;
+          vref = to;
+          if (key < RV) {
+            float m = -INFINITY, f = 1.f;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) m = fmaxf(m, red[x * (R + 4) + key]);
+            const bool row = qr[key].tok >= 0;
+            // a row that is none never moves; one without a key so far does with the first
+            const float nb = s == 0 ? (row ? kPLog2 - kNoKey : kNoKey) : nbs[key], ref = kPLog2 - nb;
+            if (row && m > ref + kLagLog2) {
+              nbs[key] = kPLog2 - m;
+              f = ex2_approx(ref - m);
+            } else if (s == 0) {
+              nbs[key] = nb;
             }
-            if (s > 0) wait_pv();
-            const int c0 = ch, c1 = fv != 1.f ? CH : ch + 1;
-            uint32_t moved = 0;
+            facs[key] = f;
+          }
+          if (!meet()) return false;
+          if (s > 0) {
+            if (!wait_pv(g - 1)) return false;
+            tc_fence_after();
 #pragma unroll 1
-            for (int c = c0; c < c1; ++c) {
-              float f[16];
+            for (int c = 0; c < RV; c += W) {
 #pragma unroll
-              for (int r = 0; r < 16; ++r) {
-                f[r] = fv;
-                if (c != ch) continue;
-                float m = -INFINITY;
+              for (int z = 0; z < C::PPARTS; ++z) {
+                const uint32_t at = tmem + tlane + C::tm_o(t) + z * R + c;
+                uint32_t x[W];
+                tmem_ldn<W>(at, x);
+                tmem_wait_ld();
 #pragma unroll
-                for (int x = 0; x < 4; ++x) m = fmaxf(m, red[x * (R + 4) + ch * 16 + r]);
-                const float ref = kPLog2 - rowc[ch * 16 + r].y;
-                if (tok[ch * 16 + r] >= 0 && m > ref + kLagLog2) {
-                  moved |= 1u << r;
-                  f[r] *= ex2_approx(ref - m);
-                }
-              }
-              if (s > 0) {
-                uint32_t x[16];
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                  const uint32_t at = tmem + tlane + C::tm_o(t) + half * R + c * 16;
-                  tmem_ld16(at, x);
-                  tmem_wait_ld();
-#pragma unroll
-                  for (int r = 0; r < 16; ++r) x[r] = __float_as_uint(__uint_as_float(x[r]) * f[r]);
-                  tmem_st16(at, x);
-                }
-                tmem_wait_st();
+                for (int r = 0; r < W; ++r) x[r] = __float_as_uint(__uint_as_float(x[r]) * (facs[c + r] * fv));
+                tmem_stn<W>(at, x);
               }
             }
+            tmem_wait_st();
+          }
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-              if (!(moved >> r & 1)) continue;
-              float m = -INFINITY;
+          for (int r = 0; r < RV; ++r) l[r] *= facs[r];
+          return true;
+        };
+        bool moves = s == 0 || (!cached && vref != 1.f), vote = !moves;
+        const uint32_t pbuf = sbase + C::OFF_P + (t * C::NP + (C::NP == 2 ? (g & 1) : 0)) * C::PBYTES;
+        for (;;) {
+          if (moves && !move()) return false;
+          uint32_t x[RV / 2];
+          float p[RV], top = -INFINITY;
+          const float w = cached ? vscale / vref : 1.f;
 #pragma unroll
-              for (int x = 0; x < 4; ++x) m = fmaxf(m, red[x * (R + 4) + ch * 16 + r]);
-              l[ch * 16 + r] *= ex2_approx(kPLog2 - rowc[ch * 16 + r].y - m);
-            }
-            named_bar_sync(bar_id, 128);  // the references have been read
-            if (wq == 0 && lane < 16 && (moved >> lane & 1)) {
-              float m = -INFINITY;
+          for (int c = 0; c < RV; c += W) {
+            float y[W];
+            load_y(c, y);
 #pragma unroll
-              for (int x = 0; x < 4; ++x) m = fmaxf(m, red[x * (R + 4) + ch * 16 + lane]);
-              rowc[ch * 16 + lane].y = kPLog2 - m;
-            }
-            named_bar_sync(bar_id, 128);
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-              const float2 rc = rowc[ch * 16 + r];
-              tt[r] = (seen >> r & 1) ? fmaf(y[r], cached ? rc.x : sl2, rc.y) : -INFINITY;
+            for (int r = 0; r < W; ++r) {
+              const float f = cached ? qr[c + r].factor : a.scale_log2;
+              const float tt = (seen >> (c + r) & 1) ? fmaf(y[r], f, nbs[c + r]) : -INFINITY;
+              top = fmaxf(top, tt);
+              p[c + r] = tt;
             }
           }
-          if (ch == 0) w = vscale / vref;
-          uint32_t x[8], x16[8];
-#pragma unroll
-          for (int r = 0; r < 8; ++r) {
-            const float p = ex2_approx(tt[2 * r]), q = ex2_approx(tt[2 * r + 1]);
-            l[ch * 16 + 2 * r] += p;
-            l[ch * 16 + 2 * r + 1] += q;
-            if (cached)
-              x[r] = pack_f16x2(p * w, q * w);
-            else
-              x16[r] = pack16<F16>(p, q);
+          if (vote) {
+            const bool grows = __any_sync(0xffffffffu, top > kPLog2 + kLagLog2 || (there && cached && vscale > vref));
+            if (grows && lane == 0) flags[meets & 1] = meets + 1;
+            meet_arrive();
+          } else {
+            tc_fence_before();  // S is in registers for good
+            __syncwarp();
+            if (lane == 0) mbar_arrive(BAR(C::S_FREE + 2 * t + (g & 1)));
           }
-          wait_pv();
+#pragma unroll
+          for (int r = 0; r < RV / 2; ++r) {
+            p[2 * r] = ex2_approx(p[2 * r]);
+            p[2 * r + 1] = ex2_approx(p[2 * r + 1]);
+            x[r] = cached ? pack_f16x2(p[2 * r] * w, p[2 * r + 1] * w) : pack16<F16>(p[2 * r], p[2 * r + 1]);
+          }
+          if (vote) {
+            const bool ok = wait_phase(BAR(C::GROUP + t), meets & 1, st, SITE_T8_GROUP);
+            const bool grows = flags[meets & 1] == meets + 1;
+            ++meets;
+            if (!ok) return false;
+            if (grows) {
+              moves = true, vote = false;
+              continue;
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(BAR(C::S_FREE + 2 * t + (g & 1)));
+          }
+#pragma unroll
+          for (int r = 0; r < RV; ++r) l[r] += p[r];
+          // P of the tile that had this buffer has been read
+          if (g >= C::NP && !wait_pv(g - C::NP)) return false;
           if (cached) {
-            uint32_t part[4][4];
 #pragma unroll
-            for (int z = 0; z < 4; ++z) {
+            for (int z = 0; z < C::PPARTS; ++z) {
+              uint32_t part[RV / 4];
 #pragma unroll
-              for (int r = 0; r < 4; ++r) {
+              for (int r = 0; r < RV / 4; ++r) {
                 const uint32_t lo = to_e5m2(x[2 * r]), hi = to_e5m2(x[2 * r + 1]);
-                part[z][r] = upper_bytes(lo, hi);
+                part[r] = upper_bytes(lo, hi);
                 x[2 * r] = h2_sub(x[2 * r], lo);
                 x[2 * r + 1] = h2_sub(x[2 * r + 1], hi);
                 if (z == 1) x[2 * r] = h2_mul64(x[2 * r]), x[2 * r + 1] = h2_mul64(x[2 * r + 1]);
               }
-              if (z == 2 && !F16) break;
+              if constexpr (RV >= 16) {
+#pragma unroll
+                for (int c = 0; c < RV / 16; ++c)
+                  sts128(pbuf + swizzled<C::PX>(key, z * (R / 16) + c), part[4 * c], part[4 * c + 1], part[4 * c + 2], part[4 * c + 3]);
+              } else if constexpr (RV == 8) {
+                sts64(pbuf + swizzled<C::PX>(key, z * (R / 16)), part[0], part[1]);
+              } else {
+                sts32(pbuf + swizzled<C::PX>(key, z * (R / 16)), part[0]);
+              }
             }
-            auto put = [&](int z, int at) { sts128(at, part[z][0], part[z][1], part[z][2], part[z][3]); };
-            constexpr int RC = R / 16;  // chunks of 16 rows
-            const uint32_t py = pbuf + (R == 64 ? C::OFF_Y : 0);
-            constexpr int Y0 = R == 64 ? 0 : 2 * RC;
-            put(0, pbuf + swizzled<C::PX>(key, ch));
-            put(2, pbuf + swizzled<C::PX>(key, RC + ch));
-            put(1, py + swizzled<C::PY>(key, Y0 + ch));
-            if (F16) put(3, py + swizzled<C::PY>(key, Y0 + RC + ch));
           } else if (key < C::NEW) {
-            sts128(pbuf + swizzled<C::PX>(key, 2 * ch), x16[0], x16[1], x16[2], x16[3]);
-            sts128(pbuf + swizzled<C::PX>(key, 2 * ch + 1), x16[4], x16[5], x16[6], x16[7]);
+            if constexpr (RV >= 8) {
+#pragma unroll
+              for (int c = 0; c < RV / 8; ++c)
+                sts128(pbuf + swizzled<C::PX>(key, c), x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
+            } else {
+              sts64(pbuf + swizzled<C::PX>(key, 0), x[0], x[1]);
+            }
           }
+          break;
         }
-        if (give_up) break;
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(BAR(C::P_READY + t));
       }
-      if (give_up) break;
-      if (steps > 0) ok = ok && wait_phase(BAR(C::O_DONE + t), (used - 1) & 1, st, SITE_T8_O_DONE);
-      tc_fence_after();
-      // sums over the keys: of 16 rows at a time, lane pairs end with a row each
-#pragma unroll
-      for (int ch = 0; ch < CH; ++ch) {
-        float v[16];
-#pragma unroll
-        for (int r = 0; r < 16; ++r) v[r] = l[ch * 16 + r];
-#pragma unroll
-        for (int o = 16, n = 8; o > 1; o >>= 1, n >>= 1)
-#pragma unroll
-          for (int r = 0; r < n; ++r) {
-            const bool up = lane & o;
-            const float send = up ? v[r] : v[r + n], keep = up ? v[r + n] : v[r];
-            v[r] = keep + __shfl_xor_sync(0xffffffffu, send, o);
-          }
-        v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
-        if (!(lane & 1)) red[wq * (R + 4) + ch * 16 + (lane >> 1)] = v[0];
-      }
-      if (bar_or(bar_id, !ok)) break;
-      if (key < R && steps > 0) {  // (without steps nobody reads them, and the other lane may still read the last ones)
-        float sum = 0.f;
-#pragma unroll
-        for (int x = 0; x < 4; ++x) sum += red[x * (R + 4) + key];
-        ml[t * R + key] = make_float2(tok[key] < 0 ? kNoKey : kPLog2 - rowc[key].y, sum);
-      }
-      if (key == 0 && steps > 0) vrefs[t] = vref;
       const bool join = dual && it.c1 > 0, whole = it.flags & ITEM8_WHOLE;
-      e0 += it.cnt;
-      if (join) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(BAR(C::MERGE));
-        ok = wait_phase(BAR(C::MERGE), merges & 1, st, SITE_T8_MERGE);
-        tc_fence_after();
-        ++merges;
-      }
-      // The other lane's results stay as they are: it writes the next ones after a product into O, which waits for
-      // this lane's arrival below.
-      if (bar_or(bar_id, !ok)) break;
-      if (dual && t == 1 && !join) continue;  // lane 0 has all of them
       const long long part0 = (long long)it.slot * (2 * R) + (dual ? 0 : t * R);
-      if (steps == 0) {  // (a cut item only) none of this part's keys concerns these rows
-        if (key < R && tok[key] >= 0 && FA_CHECK(in_range(part0 + key, a.part_rows), st, DBG_GLOBAL_STORE))
-          a.part_lse[part0 + key] = -INFINITY;
-        continue;
-      }
-      // rows [ra, rb): in a join each lane takes half of them
-      const int ra = join ? t * (R / 2) : 0, rb = join ? ra + R / 2 : R;
-      if (key >= ra && key < rb && orow[key] >= 0) {
-        const float2 x = ml[(join ? 0 : t * R) + key], z = join ? ml[R + key] : make_float2(kNoKey, 0.f);
-        const float m = fmaxf(x.x, z.x), sum = x.y * ex2_approx(x.x - m) + z.y * ex2_approx(z.x - m);
-        const float lse2 = sum != 0.f ? m - kPLog2 + lg2_approx(sum) : -INFINITY;
-        const long long token = orow[key] & 0xffffffffffll, head = orow[key] >> 40;
-        if (!whole) {
-          if (FA_CHECK(in_range(part0 + key, a.part_rows), st, DBG_GLOBAL_STORE)) a.part_lse[part0 + key] = lse2;
-        } else if (a.lse && FA_CHECK(in_range(token, a.T), st, DBG_GLOBAL_STORE)) {
-          a.lse[head * a.T + token] = lse2 * 0.6931471805599453f;
-        }
-      }
-      const float v0 = vrefs[join ? 0 : t], v1 = join ? vrefs[1] : 0.f;
-#pragma unroll 1
-      for (int r0 = ra; r0 < rb; r0 += 8) {
-        float o[8];
-        if (key < D) {
+      if (steps > 0) {
+        if (!wait_pv(g - 1)) return false;
+        tc_fence_after();
+        // Sums over the warp's keys: of W rows at a time, groups of 32 / W lanes end with a row each. Where there are
+        // no steps nothing is written here: the other lane may still read what the item before left.
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            if (u == 1 && !join) break;
-            uint32_t x[8], z[8];
-            const uint32_t at = tmem + tlane + C::tm_o(join ? u : t) + r0;
-            // (tiles of new tokens alone leave the columns of p3 and p4 unwritten)
-            const bool parts = it.j0 + (dual ? (join ? u : t) : 0) < it.nc;
-            tmem_ld8(at, x);
-            tmem_ld8(at + R, z);
-            tmem_wait_ld();
+        for (int c = 0; c < RV; c += W) {
+          float v[W];
 #pragma unroll
-            for (int r = 0; r < 8; ++r) {
-              const float2 p = ml[(join ? 0 : t * R) + r0 + r], q = join ? ml[R + r0 + r] : make_float2(kNoKey, 0.f);
-              const float m = fmaxf(p.x, q.x), f0 = ex2_approx(p.x - m), f1 = ex2_approx(q.x - m);
-              const float sum = p.y * f0 + q.y * f1, inv = sum != 0.f ? 1.f / sum : 0.f;
-              const float v = fmaf(parts ? __uint_as_float(z[r]) : 0.f, 0.015625f, __uint_as_float(x[r])) * ((u ? f1 * v1 : f0 * v0) * inv);
-              o[r] = u ? o[r] + v : v;
+          for (int r = 0; r < W; ++r) v[r] = l[c + r];
+          int row = 0;
+#pragma unroll
+          for (int o = 16, n = W / 2; o; o >>= 1, n >>= 1) {
+            if (n == 0) {
+              v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+              continue;
+            }
+            const bool up = lane & o;
+            row += up ? n : 0;
+#pragma unroll
+            for (int r = 0; r < n; ++r) {
+              const float send = up ? v[r] : v[r + n], keep = up ? v[r + n] : v[r];
+              v[r] = keep + __shfl_xor_sync(0xffffffffu, send, o);
             }
           }
+          if ((lane & (32 / W - 1)) == 0) sums[(t * 4 + wq) * R + c + row] = v[0];
         }
-        if (r0 + 8 >= rb) {  // O is in registers: the issuers may write it again
+        if (key < RV) refs[t * R + key] = kPLog2 - nbs[key];
+        if (key == 0) vrefs[t] = vref;
+        // The other lane's results stay as they are until its next product into O, which waits for this lane's
+        // arrival below.
+        if (join) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) {
-            mbar_arrive_n(BAR(C::O_FREE + t), join ? 1 : 2);
-            if (join) mbar_arrive(BAR(C::O_FREE + (t ^ 1)));
+          if (lane == 0) mbar_arrive(BAR(C::MERGE));
+          if (!wait_phase(BAR(C::MERGE), merges++ & 1, st, SITE_T8_MERGE)) return false;
+          tc_fence_after();
+        } else if (!meet()) {
+          return false;
+        }
+        // rows [ra, rb): in a join each lane takes half of them
+        const int ra = join ? t * (RV / 2) : 0, rb = join ? ra + RV / 2 : RV;
+        auto weights = [&](int r, float* f0, float* f1) {  // of both lanes' O; returns the row's LSE to base 2
+          const float m0 = refs[(join ? 0 : t) * R + r], m1 = join ? refs[R + r] : kNoKey;
+          float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            l0 += sums[((join ? 0 : t) * 4 + x) * R + r];
+            if (join) l1 += sums[(4 + x) * R + r];
+          }
+          const float m = fmaxf(m0, m1);
+          *f0 = ex2_approx(m0 - m), *f1 = ex2_approx(m1 - m);
+          const float sum = l0 * *f0 + l1 * *f1, inv = sum != 0.f ? 1.f / sum : 0.f;  // 0: no key; NaN stays NaN
+          *f0 *= inv, *f1 *= inv;
+          return sum != 0.f ? m - kPLog2 + lg2_approx(sum) : -INFINITY;
+        };
+        if (key >= ra && key < rb && qr[key].tok >= 0) {
+          float f0, f1;
+          const float lse2 = weights(key, &f0, &f1);
+          const long long token = qr[key].to & 0xffffffffffll, head = qr[key].to >> 40;
+          if (!whole) {
+            if (FA_CHECK(in_range(part0 + key, a.part_rows), st, DBG_GLOBAL_STORE)) a.part_lse[part0 + key] = lse2;
+          } else if (a.lse && FA_CHECK(in_range(token, a.T), st, DBG_GLOBAL_STORE)) {
+            a.lse[head * a.T + token] = lse2 * 0.6931471805599453f;
           }
         }
-        if (key >= D) continue;
-        if (whole) {
-          // even threads write the even rows of two columns each, odd threads the odd rows
+        const float v0 = vrefs[join ? 0 : t], v1 = join ? vrefs[1] : 0.f;
+        constexpr int WO = RV < 16 ? RV / 2 : 8;  // rows at a time
+#pragma unroll 1
+        for (int r0 = ra; r0 < rb; r0 += WO) {
+          float o[WO];
+          if (key < D) {
 #pragma unroll
-          for (int r = 0; r < 8; r += 2) {
-            const float got = __shfl_xor_sync(0xffffffffu, (lane & 1) ? o[r] : o[r + 1], 1);
-            const uint32_t y = (lane & 1) ? pack16<F16>(got, o[r + 1]) : pack16<F16>(o[r], got);
-            const long long to = orow[r0 + r + (lane & 1)];
-            const long long token = to & 0xffffffffffll;
-            if (to >= 0 && FA_CHECK(in_range(token, a.T), st, DBG_GLOBAL_STORE))
-              *reinterpret_cast<uint32_t*>(a.o + token * a.o_st + (to >> 40) * a.o_sh + (key & ~1)) = y;
+            for (int r = 0; r < WO; ++r) o[r] = 0.f;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              if (u == 1 && !join) break;
+              uint32_t x[C::PPARTS][WO];
+              const uint32_t at = tmem + tlane + C::tm_o(join ? u : t) + r0;
+              // (tiles of new tokens alone write the first part's columns only)
+              const bool parts = it.j0 + (dual ? (join ? u : t) : 0) < it.nc;
+#pragma unroll
+              for (int z = 0; z < C::PPARTS; ++z) tmem_ldn<WO>(at + z * R, x[z]);
+              tmem_wait_ld();
+#pragma unroll
+              for (int r = 0; r < WO; ++r) {
+                float f0, f1, v = __uint_as_float(x[0][r]);
+                weights(r0 + r, &f0, &f1);
+                if (parts) {
+                  float low = __uint_as_float(x[2][r]);
+                  if (F16) low += __uint_as_float(x[C::PPARTS - 1][r]);
+                  v = fmaf(low, 0.015625f, v + __uint_as_float(x[1][r]));
+                }
+                o[r] = fmaf(v, u ? f1 * v1 : f0 * v0, o[r]);
+              }
+            }
           }
-        } else {
+          if (r0 + WO >= rb) {  // O is in registers: the issuers may write it again
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive_n(BAR(C::O_FREE + t), join ? 1 : 2);
+              if (join) mbar_arrive(BAR(C::O_FREE + (t ^ 1)));
+            }
+          }
+          if (key >= D) continue;
+          if (whole) {
+            // even threads write the even rows of two columns each, odd threads the odd rows
 #pragma unroll
-          for (int r = 0; r < 8; ++r)
-            if (orow[r0 + r] >= 0 && FA_CHECK(in_range(part0 + r0 + r, a.part_rows), st, DBG_GLOBAL_STORE))
-              a.part_o[(part0 + r0 + r) * D + key] = o[r];
+            for (int r = 0; r < WO; r += 2) {
+              const float got = __shfl_xor_sync(0xffffffffu, (lane & 1) ? o[r] : o[r + 1], 1);
+              const uint32_t y = (lane & 1) ? pack16<F16>(got, o[r + 1]) : pack16<F16>(o[r], got);
+              const QRow& q = qr[r0 + r + (lane & 1)];
+              const long long token = q.to & 0xffffffffffll;
+              if (q.tok >= 0 && FA_CHECK(in_range(token, a.T), st, DBG_GLOBAL_STORE))
+                *reinterpret_cast<uint32_t*>(a.o + token * a.o_st + (q.to >> 40) * a.o_sh + (key & ~1)) = y;
+            }
+          } else {
+#pragma unroll
+            for (int r = 0; r < WO; ++r)
+              if (qr[r0 + r].tok >= 0 && FA_CHECK(in_range(part0 + r0 + r, a.part_rows), st, DBG_GLOBAL_STORE))
+                a.part_o[(part0 + r0 + r) * D + key] = o[r];
+          }
         }
+      } else if (!dual && key < RV && qr[key].tok >= 0 && FA_CHECK(in_range(part0 + key, a.part_rows), st, DBG_GLOBAL_STORE)) {
+        a.part_lse[part0 + key] = -INFINITY;  // (a cut item only) none of this part's keys concerns these rows
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive_n(BAR(C::Q_EMPTY + slot), dual ? 1 : 2);
+      return true;
+    };
+    for (int i = 0;; ++i) {
+      Item8 it;
+      if (!next_item(i, &it) || it.cnt < 0) break;
+      const bool dual = it.flags & ITEM8_DUAL;
+      const int rows = it.n * a.G - it.r0 - (dual ? 0 : t * R);
+      // both slots of a pair: a barrier's parity tells two uses of a slot apart, not three, so none may be left out
+      bool ok = true;
+      for (int u = uq; ok && u < uq + (dual ? 1 : 2); ++u)
+        ok = wait_phase(BAR(C::Q_FULL + u % NQ), (u / NQ) & 1, st, SITE_T8_Q_FULL);
+      if (!ok) break;
+      if constexpr (R == 16) {
+        ok = rows <= 4 ? run_item(it, Rows8<4>()) : rows <= 8 ? run_item(it, Rows8<8>()) : run_item(it, Rows8<16>());
+      } else {
+        ok = rows <= 16 ? run_item(it, Rows8<16>()) : run_item(it, Rows8<32>());
+      }
+      if (!ok) break;
+      uq += dual ? 1 : 2;
+      e0 += it.cnt;
     }
   }
 
@@ -1115,9 +1194,7 @@ static int launch_serve8_r(const Serve8Tensors& x, Serve8Args a, cudaStream_t st
 template <int D, bool F16>
 static int launch_serve8_d(const Serve8Tensors& x, const Serve8Args& a, cudaStream_t stream) {
   const long long rows = (long long)a.T * a.G;
-  if (rows <= 16LL * a.B) return launch_serve8_r<D, 16, F16>(x, a, stream);
-  if (rows <= 64LL * a.B) return launch_serve8_r<D, 32, F16>(x, a, stream);
-  return launch_serve8_r<D, 64, F16>(x, a, stream);
+  return rows <= 16LL * a.B ? launch_serve8_r<D, 16, F16>(x, a, stream) : launch_serve8_r<D, 32, F16>(x, a, stream);
 }
 static int launch_serve8(const Serve8Tensors& x, const Serve8Args& a, int d, int dtype, cudaStream_t stream) {
   const bool f16 = dtype == FA_FP16;
@@ -1135,7 +1212,7 @@ size_t fa_forward_tree_8bit_workspace_size(int d) {
   if (d != 64 && d != 128) return 0;
   int sms = 0;
   if (!fa::sm_count(&sms)) return 0;
-  return (size_t)2 * sms * 128 * (d + 1) * 4 + (size_t)sms * 2 * sizeof(int4);
+  return (size_t)2 * sms * 64 * (d + 1) * 4 + (size_t)sms * 2 * sizeof(int4);
 }
 
 int fa_forward_tree_8bit(const fa_rows* q, const fa_rows* k, const fa_rows* v, const fa_rows* o, float* lse,

@@ -139,3 +139,21 @@ def test_random_shapes(gpu):
             nodes[0] = 1
         Made(gpu, lens, nodes, G * H, H, r.choice([64, 128]), page, block, r.choice([BF16, FP16]), seed=seed,
              tree=r.random() < 0.5).check()
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("most", [3, 14, 40])
+def test_many_items_of_both_kinds(gpu, dtype, d, most):
+    """More items than CTAs, some of one lane's rows and some of two, in turn: every ring goes round several times,
+    with slots that one lane skips."""
+    import random
+    r = random.Random(most)
+    lens = [r.choice([0, 5, 130, 300, r.randrange(1, 700)]) for _ in range(40)]
+    nodes = [r.choice([1, 2, most, r.randrange(0, most + 1)]) for _ in range(40)]
+    m = Made(gpu, lens, nodes, 24, 6, d, 64, 32, dtype, seed=most, tree=most == 14)
+    first = m.check()
+    for _ in range(3):  # no atomics, one order of sums: the same bits
+        again = m.call()
+        assert all(torch.equal(x[..., : m.T] if x.dim() == 2 else x[: m.T], y[..., : m.T] if y.dim() == 2 else y[: m.T])
+                   for x, y in zip(first, again))
