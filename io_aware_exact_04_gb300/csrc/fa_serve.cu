@@ -4,40 +4,15 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "fa_internal.h"
 #include "serve.cuh"
 #include "serve_args.h"
+#include "serve_tree.h"
 #include "tmap.h"
 
 namespace fa {
-
-struct ServeArgs {
-  const uint16_t *q, *k, *v;
-  uint16_t* o;
-  long long q_st, q_sh, k_st, k_sh, v_st, v_sh, o_st, o_sh;  // token and head strides, elements
-  float* lse;  // [Hq, T] or null
-  int o_wide;  // every row of o is 32-byte aligned
-  // the cache; prompts have none (table null)
-  const uint16_t *kc, *vc;
-  long long c_sp, c_sh, c_st;
-  int n_pages, page_shift;
-  const int* table;
-  long long table_stride;
-  int table_width;
-  const int* lens;
-  const uint32_t* mask;  // null: a chain
-  int words;
-  const int* cu;
-  int B, T, Hq, Hkv, G;
-  float scale_log2;
-  float* part_o;    // workspace: two slots of 256 rows for each CTA, O normalised by its own l
-  float* part_lse;  // their LSEs, base 2 (-inf: no key, O not written)
-  long long part_rows;
-  int4* cuts;       // two for each CTA, of the item that it is the first to cut: {later parts (0: none), ..},
-                    // {tokens of the sequence, its first row, the item's first token, key/value head}
-  int* status;
-};
 
 // Key tiles that a CTA of the tree kernel takes where there are few (the last one may take one less), and
 // rows of a TMA box of new tokens there (a draft seldom fills a tile of 128).
@@ -83,24 +58,36 @@ constexpr int kNewBox = 16;
 // producer's issue bounds it); 512 sequences over up to 500 tokens: 194 us, 44 % (12 heads of 64: 239 us, 27 %):
 // an item's start and end; 64 trees of up to 64 nodes over up to 32768 tokens: 960 us, bound by the
 // tensor pipe (81-84 % busy) beside memory at 76 %.
-template <int D>
+//
+// A cache in 8 bits (C8): the pages arrive in a ring of their own, and four more warps (12-15) turn them into tiles
+// of 16 bits (exactly) in the ring that the products read, so that all else is as it is. A converter thread takes
+// 16 elements of one key at a time, the lanes of a quarter-warp eight keys that follow each other, which the
+// swizzled rows of both sides spread over all banks. The scales of 16 keys each come with K's pages: that of
+// K multiplies S, that of V the probability, in bf16 as it is (the type's range holds it); fp16 divides
+// by a reference (vref, twice the largest so far), which O keeps up with as it does with the maximum. The
+// tiles of new tokens are loaded by the converters, who meet all entries of the ring in order.
+template <int D, bool C8 = false>
 struct ServeCfg {
   static constexpr int NSUB = D / 64;
   static constexpr int SUB_BYTES = 128 * 128;
   static constexpr int TILE_BYTES = NSUB * SUB_BYTES;
-  static constexpr int NSLOT = D == 64 ? 12 : 5;
+  static constexpr int NSLOT = C8 ? (D == 64 ? 6 : 3) : D == 64 ? 12 : 5;
+  static constexpr int STAGE = 128 * D, NS8 = C8 ? (D == 64 ? 8 : 4) : 0;  // pages of 8 bits
+  static constexpr int SCALES = C8 ? (D == 64 ? 16 : 4) : 0;  // tiles whose scales are kept: those with an entry in either ring
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_R = 2 * TILE_BYTES;
-  static constexpr int OFF_BAR = OFF_R + NSLOT * TILE_BYTES;
+  static constexpr int OFF_S8 = OFF_R + NSLOT * TILE_BYTES;
+  static constexpr int OFF_BAR = OFF_S8 + NS8 * STAGE;
   static constexpr int OFF_DESC = OFF_BAR + 512;   // 4 x 16 ints
   static constexpr int OFF_ML = OFF_BAR + 768;     // m and l of both lanes' rows, for the join of a dual item
-  static constexpr int SMEM_BYTES = OFF_ML + 2048;
+  static constexpr int OFF_SC = OFF_ML + 2048;     // [tile][K of 8 groups of 16 keys, V of 8]
+  static constexpr int SMEM_BYTES = OFF_SC + SCALES * 64;
   // A key tile is taken in HPT steps of KT keys. The softmax must find S of the next step ready
   // when it ends one, so S may not wait for PV of the step before. TMEM has room for that in two
   // ways: d = 64 keeps P apart from S (one step a tile; S is free once it is in registers);
   // d = 128, where O takes half the columns, takes a tile as two halves; even and odd steps of a
   // lane have a buffer each, P over its own S, and S is formed two steps ahead.
-  static constexpr bool SEP_P = D == 64;
+  static constexpr bool SEP_P = D == 64 && !C8;
   static constexpr int KT = SEP_P ? 128 : 64, HPT = 128 / KT;
   __device__ static constexpr int buf(int g) { return SEP_P ? 0 : g & 1; }            // of a lane's step g
   __device__ static constexpr uint32_t phase(int g) { return (SEP_P ? g : g >> 1) & 1; }  // of its barriers
@@ -108,21 +95,21 @@ struct ServeCfg {
   __device__ static constexpr uint32_t tm_p(int t, int u) { return SEP_P ? 256u + 64u * t : tm_s(t, u); }
   __device__ static constexpr uint32_t tm_o(int t) { return SEP_P ? 384u + 64u * t : 256u + (uint32_t)D * t; }
   static constexpr uint32_t TM_COLS = 512;
-  static constexpr int THREADS = 384;
+  static constexpr int THREADS = C8 ? 512 : 384;
   // with few rows the softmax is warps 0 and 4, on the scheduler of warp 8: the least busy role there
   static constexpr int PV0 = 8, PRODUCER = 9, PV1 = 10, S_BOTH = 11;
   // barriers
   static constexpr int FULL = 0, EMPTY = NSLOT, Q_FULL = 2 * NSLOT, Q_EMPTY = Q_FULL + 2, S_FULL = Q_EMPTY + 2,
                        P_READY = S_FULL + 4, O_DONE = P_READY + 4, S_FREE = O_DONE + 4, O_FREE = S_FREE + 2,
                        MERGE = O_FREE + 2, DRAIN = MERGE + 1, D_FULL = DRAIN + 1, D_EMPTY = D_FULL + 4,
-                       BARS = D_EMPTY + 4;
+                       FULL8 = D_EMPTY + 4, EMPTY8 = FULL8 + NS8, BARS = EMPTY8 + NS8;
+  static_assert(8 * BARS + 20 <= 512, "barrier area");
+  static_assert(SMEM_BYTES <= 232448, "shared memory above 227 KB");
 };
-static_assert(8 * ServeCfg<64>::BARS + 12 <= 512 && 8 * ServeCfg<128>::BARS + 12 <= 512, "barrier area");
-static_assert(ServeCfg<64>::SMEM_BYTES <= 232448 && ServeCfg<128>::SMEM_BYTES <= 232448, "shared memory above 227 KB");
 
 enum { SITE_SW_EMPTY = 60, SITE_SW_Q_FULL, SITE_SW_Q_EMPTY, SITE_SW_K_FULL, SITE_SW_V_FULL, SITE_SW_S_FREE,
        SITE_SW_P_READY, SITE_SW_O_FREE, SITE_SW_S_FULL, SITE_SW_O_DONE, SITE_SW_MERGE, SITE_SW_DESC_FULL,
-       SITE_SW_DESC_EMPTY };
+       SITE_SW_DESC_EMPTY, SITE_SW_FULL8, SITE_SW_EMPTY8 };
 
 // A work item (or the part of it that this CTA computes), as the producer publishes it.
 struct ServeItem {
@@ -352,12 +339,34 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return F16 ? pack_f16x2(lo, hi) : pack_bf16x2(lo, hi);
 }
 
-template <int D, bool F16, bool PAGED>
-__global__ void __launch_bounds__(384, 1)
+// Sixteen e4m3 as two 16-byte chunks of 16-bit values, exactly.
+template <bool F16>
+__device__ __forceinline__ void widen16(const uint4& x, uint4* lo, uint4* hi) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  uint32_t r[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(w[i >> 1] >> (16 * (i & 1)))));
+    if (!F16) {
+      float a, b;
+      asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
+          : "=f"(a), "=f"(b)
+          : "r"(h));
+      h = pack_bf16x2(a, b);
+    }
+    r[i] = h;
+  }
+  *lo = make_uint4(r[0], r[1], r[2], r[3]);
+  *hi = make_uint4(r[4], r[5], r[6], r[7]);
+}
+
+template <int D, bool F16, bool PAGED, bool C8 = false>
+__global__ void __launch_bounds__(C8 ? 512 : 384, 1)
     serve_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                  const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_kc,
-                 const __grid_constant__ CUtensorMap tm_vc, ServeArgs a) {
-  using C = ServeCfg<D>;
+                 const __grid_constant__ CUtensorMap tm_vc, std::conditional_t<C8, Serve8BitArgs, ServeArgs> a) {
+  using C = ServeCfg<D, C8>;
   constexpr float P_LOG2 = F16 ? 9.f : 0.f, LAG_LOG2 = F16 ? 6.f : 8.f;
   // 1024-byte aligned, as the swizzled tiles have to be: there is no room to round the address up
   extern __shared__ __align__(1024) uint8_t sm[];
@@ -376,14 +385,20 @@ __global__ void __launch_bounds__(384, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::OFF_BAR + 8 * C::BARS);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
   volatile int* loading = reinterpret_cast<int*>(tmem_slot + 2);  // ring entries whose loads have begun
+  float* vrefs = reinterpret_cast<float*>(tmem_slot + 3);         // (C8) of both lanes, for the join
+  float* scales = reinterpret_cast<float*>(sm + C::OFF_SC);
   DevStatus st{a.status, abort_flag};
   int* descs = reinterpret_cast<int*>(sm + C::OFF_DESC);
   const int npt = 128 / a.G;  // tokens of a query tile
 
   if (warp == C::PRODUCER && lane == 0) {
     for (int i = 0; i < C::NSLOT; ++i) {
-      mbar_init(BAR(C::FULL + i), 1);
+      mbar_init(BAR(C::FULL + i), C8 ? 4 : 1);
       mbar_init(BAR(C::EMPTY + i), 2);  // V: both issuers; K: its issuer twice
+    }
+    for (int i = 0; i < C::NS8; ++i) {
+      mbar_init(BAR(C::FULL8 + i), i & 1 ? 1 : 17);  // the copies, and with K each of 16 lanes' scale
+      mbar_init(BAR(C::EMPTY8 + i), 4);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(BAR(C::Q_FULL + t), 1);
@@ -400,7 +415,7 @@ __global__ void __launch_bounds__(384, 1)
     mbar_init(BAR(C::DRAIN), 3);
     for (int i = 0; i < 4; ++i) {
       mbar_init(BAR(C::D_FULL + i), 1);
-      mbar_init(BAR(C::D_EMPTY + i), 11);  // softmax warps and issuers
+      mbar_init(BAR(C::D_EMPTY + i), C8 ? 15 : 11);  // softmax warps, issuers and converters
     }
     *abort_flag = 0;
     *loading = 0;
@@ -450,7 +465,7 @@ __global__ void __launch_bounds__(384, 1)
 
   if (warp == C::PRODUCER) {
     // ------------------------------------------------------------ scheduler and TMA producer
-    int items = 0, uq = 0, e = 0;  // items published, Q slots and ring entries used
+    int items = 0, uq = 0, e = 0;  // items published, Q slots and ring entries (C8: tiles of 8 bits) used
     bool ok = true;
     auto publish = [&](const ServeItem& it) {
       if (!wait_phase(BAR(C::D_EMPTY + (items & 3)), ((items >> 2) & 1) ^ 1, st, SITE_SW_DESC_EMPTY)) return false;
@@ -473,6 +488,10 @@ __global__ void __launch_bounds__(384, 1)
       const int prow = min(1 << a.page_shift, 128);  // rows of a page's box
       const int r = (lane & 15) / C::NSUB, c = lane % C::NSUB;
       auto page_of = [&](int j) {
+        if (C8) {  // lane (kv, g) = 8 kv + g: of 16 keys
+          const int t0 = j * 128 + (lane & 7) * 16;
+          return lane < 16 && j < min(it.j0 + it.cnt, it.nc) && t0 < it.L ? a.table[b * a.table_stride + (t0 >> a.page_shift)] : 0;
+        }
         const int pg = (j * 128 + r * prow) >> a.page_shift;
         const bool there = j < it.j0 + it.cnt && j < it.nc && r * prow < 128 && j * 128 + r * prow < it.L;
         return there ? a.table[b * a.table_stride + pg] : 0;
@@ -490,6 +509,41 @@ __global__ void __launch_bounds__(384, 1)
         __syncwarp();
       }
       int j = it.j0;
+      if constexpr (C8) {
+        // K and V of a tile in one go, a lane for 16 keys: their scale, and the box that begins with them
+        const int kv = (lane >> 3) & 1, g = lane & 7, page_size = 1 << a.page_shift;
+        for (; j < min(it.j0 + it.cnt, it.nc); ++j, ++e) {
+          const int id_next = page_of(j + 1), rows = min(128, it.L - j * 128), boxes = (rows + prow - 1) / prow;
+          const int sk = (2 * e) % C::NS8, sv = sk + 1;
+          const uint32_t ph = ((2 * e / C::NS8) & 1) ^ 1;
+          if (!wait_phase(BAR(C::EMPTY8 + sk), ph, st, SITE_SW_EMPTY8) || !wait_phase(BAR(C::EMPTY8 + sv), ph, st, SITE_SW_EMPTY8))
+            return false;
+          const int t0 = j * 128 + g * 16, in_page = t0 & (page_size - 1);
+          const bool mine = lane < 16 && g * 16 < rows, there = id >= 0 && id < a.n_pages;
+          if (mine && !there) record_check(a.status, SITE_S_PAGE);
+          if (elect_one()) {
+            mbar_arrive_expect_tx(BAR(C::FULL8 + sk), (uint32_t)(boxes * prow * D));
+            mbar_arrive_expect_tx(BAR(C::FULL8 + sv), (uint32_t)(boxes * prow * D));
+          }
+          __syncwarp();
+          float* to = scales + e % C::SCALES * 16 + lane;
+          if (mine && there) {
+            const float* from = (kv ? a.vs : a.ks) + id * a.s_sp + it.kvh * a.s_sh + (in_page >> a.block_shift);
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(BAR(C::FULL8 + sk)) : "memory");
+          } else if (lane < 16) {
+            *to = kv ? 0.f : 1.f;  // nothing there: its probabilities are 0, and stay out of vref
+            mbar_arrive(BAR(C::FULL8 + sk));
+          }
+          const uint32_t dst = sbase + C::OFF_S8 + (kv ? sv : sk) * C::STAGE + g * 16 * D;
+          if (mine && (g * 16 & (prow - 1)) == 0 && !(kWithhold && e == 1) &&
+              FA_CHECK(smem_in(dst, prow * D, sbase + C::OFF_S8, sbase + C::OFF_BAR), st, DBG_TMA_LOAD))
+            tma_load_4d(dst, kv ? &tm_vc : &tm_kc, 0, in_page, it.kvh, there ? id : a.n_pages, BAR(C::FULL8 + (kv ? sv : sk)));
+          __syncwarp();
+          id = id_next;
+        }
+        return true;
+      }
       // With few rows and small boxes this warp is the slowest: K and V of a tile in one go then, a lane for
       // each box (decoding 64 sequences of up to 8192 tokens took 112 us a slot at a time and takes 100 at
       // d = 64, 190 and 177 at d = 128 with pages of 16 tokens). Few tiles an item gain nothing by it, nor
@@ -646,16 +700,81 @@ __global__ void __launch_bounds__(384, 1)
       it.cnt = -1;
       ok = publish(it);
     }
+    if constexpr (C8) asm volatile("cp.async.wait_all;" ::: "memory");
     if (*(volatile int*)abort_flag) {
       // let copies already in flight land before the CTA's shared memory is released
-      for (int x = max(0, e - C::NSLOT); x < e; ++x) {
+      const int ring = C8 ? C::NS8 : C::NSLOT, full = C8 ? C::FULL8 : C::FULL, used = C8 ? 2 * e : e;
+      for (int x = max(0, used - ring); x < used; ++x) {
         const uint64_t t0 = globaltimer_ns();
-        while (!mbar_try_wait(BAR(C::FULL + x % C::NSLOT), (x / C::NSLOT) & 1) && globaltimer_ns() - t0 < 100000000ull) {
+        while (!mbar_try_wait(BAR(full + x % ring), (x / ring) & 1) && globaltimer_ns() - t0 < 100000000ull) {
         }
       }
       for (int x = max(0, uq - 2); x < uq; ++x) {
         const uint64_t t0 = globaltimer_ns();
         while (!mbar_try_wait(BAR(C::Q_FULL + (x & 1)), (x >> 1) & 1) && globaltimer_ns() - t0 < 100000000ull) {
+        }
+      }
+    }
+  } else if (C8 && warp >= 12) {
+    // ------------------------------------------------------------ converters, and the loads of new tokens
+    if constexpr (C8) {
+      const int cw = warp - 12;
+      int e = 0, x = 0, slot = 0;  // ring entries and tiles of 8 bits so far
+      uint32_t phase = 1;          // of the slot's EMPTY
+      bool ok = true;
+      for (int i = 0; ok; ++i) {
+        ServeItem it;
+        if (!next_item(i, &it) || it.cnt < 0) break;
+        for (int j = it.j0; ok && j < it.j0 + it.cnt; ++j) {
+          const bool cached = j < it.nc;
+          for (int kv = 0; kv < 2; ++kv, ++e) {
+            const uint32_t full = BAR(C::FULL + slot);
+            const int s8 = (2 * x + kv) % (C8 ? C::NS8 : 1);
+            if (cached && !(ok = wait_phase(BAR(C::FULL8 + s8), ((2 * x + kv) / (C8 ? C::NS8 : 1)) & 1, st, SITE_SW_FULL8))) break;
+            if (!(ok = wait_phase(BAR(C::EMPTY + slot), phase, st, SITE_SW_EMPTY))) break;
+            if (cw == 0 && lane == 0) *loading = e + 1;
+            uint8_t* to = sm + C::OFF_R + slot * C::TILE_BYTES;
+            if (cached) {
+              const uint8_t* from = sm + C::OFF_S8 + s8 * C::STAGE;
+              const int c0 = lane >> 3;
+#pragma unroll
+              for (int y = 0; y < 4 * (D / 64); ++y) {
+                const uint32_t key = cw * 32 + (y & 3) * 8 + (lane & 7), c = c0 + 4 * (y >> 2);
+                const uint32_t at = D == 128 ? key * 128 + ((c ^ (key & 7)) << 4) : key * 64 + ((c ^ ((key >> 1) & 3)) << 4);
+                uint4 lo, hi;
+                widen16<F16>(*reinterpret_cast<const uint4*>(from + at), &lo, &hi);
+                uint8_t* sub = to + (c >> 2) * C::SUB_BYTES;
+                *reinterpret_cast<uint4*>(sub + sw128_offset(key, 2 * (c & 3))) = lo;
+                *reinterpret_cast<uint4*>(sub + sw128_offset(key, 2 * (c & 3) + 1)) = hi;
+              }
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                mbar_arrive(full);
+                mbar_arrive(BAR(C::EMPTY8 + s8));
+              }
+            } else if (cw == 0) {
+              const int k0 = (j - it.nc) * 128, boxes = (min(128, it.n - k0) + kNewBox - 1) / kNewBox;
+              if (elect_one()) mbar_arrive_expect_tx(full, (uint32_t)(boxes * kNewBox * 128 * C::NSUB));
+              __syncwarp();
+              const int r = lane / C::NSUB, c = lane % C::NSUB;
+              const uint32_t dst = smem_u32(to) + c * C::SUB_BYTES + r * kNewBox * 128;
+              if (lane < boxes * C::NSUB && FA_CHECK(smem_in(dst, kNewBox * 128, sbase + C::OFF_R, sbase + C::OFF_S8), st, DBG_TMA_LOAD))
+                tma_load_3d(dst, kv ? &tm_v : &tm_k, c * 64, it.row0 + k0 + r * kNewBox, it.kvh, full);
+              __syncwarp();
+            } else if (lane == 0) {
+              mbar_arrive(full);
+            }
+            if (++slot == C::NSLOT) slot = 0, phase ^= 1;
+          }
+          x += cached;
+        }
+      }
+      if (*(volatile int*)abort_flag && cw == 0) {  // as the producer does: copies of new tokens land first
+        for (int y = max(0, e - C::NSLOT); y < e; ++y) {
+          const uint64_t t0 = globaltimer_ns();
+          while (!mbar_try_wait(BAR(C::FULL + y % C::NSLOT), (y / C::NSLOT) & 1) && globaltimer_ns() - t0 < 100000000ull) {
+          }
         }
       }
     }
@@ -843,6 +962,7 @@ __global__ void __launch_bounds__(384, 1)
     const float sl2 = a.scale_log2;
     float* ml = reinterpret_cast<float*>(sm + C::OFF_ML);
     int st0 = 0, st1 = 0, merges = 0;  // steps of both lanes and joins of dual items so far
+    int tiles8 = 0;                    // (C8) cached tiles so far
     for (int i = 0;; ++i) {
       ServeItem it;
       if (!next_item(i, &it) || it.cnt < 0) break;
@@ -851,7 +971,7 @@ __global__ void __launch_bounds__(384, 1)
       const int tok = it.tok0 + (dual ? 0 : t * npt) + rn;
       const bool valid = rn < npt && tok < it.n;
       const bool any = __any_sync(0xffffffffu, valid);
-      float m_run = -INFINITY, l_run = 0.f;
+      float m_run = -INFINITY, l_run = 0.f, vref = 1.f;
       bool ok = true;
       const int tok_first = __shfl_sync(0xffffffffu, tok, 0);  // the warp's tokens ascend with its rows
       auto wait_pv = [&](int lane_t, int g) {  // PV of that lane's step g has landed in O
@@ -898,7 +1018,7 @@ __global__ void __launch_bounds__(384, 1)
         if (lane == 0) mbar_arrive(BAR(C::P_READY + 2 * t + C::buf(before + s)));
         return true;
       };
-      if (!(PAGED && any && it.n <= 16 && it.n * a.G <= 16)) {
+      if (C8 || !(PAGED && any && it.n <= 16 && it.n * a.G <= 16)) {
         for (int s = 0; s < steps; ++s, hs += C::HPT > 1) {
           const int u = C::buf(before + s);
           if (!(ok = begin_step(s))) break;
@@ -914,9 +1034,9 @@ __global__ void __launch_bounds__(384, 1)
             continue;
           }
           tc_fence_after();
-          float f = 1.f;
+          float f = 1.f, fv = 1.f;  // of O and l, and of O alone
           bool rescale = false;
-          float sv[KT];
+          float sv[KT], w[C8 ? KT / 16 : 1];
           {
             uint32_t r[KT / 32][32];
 #pragma unroll
@@ -928,6 +1048,32 @@ __global__ void __launch_bounds__(384, 1)
               for (int x = 0; x < 32; ++x) sv[q * 32 + x] = __uint_as_float(r[q][x]);
           }
           s_in_registers();
+          if constexpr (C8) {
+            float vtop = 1.f;
+            if (js < it.nc) {
+              const float* sc = scales + (tiles8 + js - it.j0) % (C8 ? C::SCALES : 1) * 16;
+              const float4 v0 = *reinterpret_cast<const float4*>(sc + 8), v1 = *reinterpret_cast<const float4*>(sc + 12);
+              vtop = fmaxf(fmaxf(fmaxf(v0.x, v0.y), fmaxf(v0.z, v0.w)), fmaxf(fmaxf(v1.x, v1.y), fmaxf(v1.z, v1.w)));
+#pragma unroll
+              for (int x = 0; x < KT / 16; ++x) {
+                const float k16 = sc[hs * (KT / 16) + x];
+                w[x] = sc[8 + hs * (KT / 16) + x];
+#pragma unroll
+                for (int y = 0; y < 16; ++y) sv[16 * x + y] *= k16;
+              }
+            } else {
+#pragma unroll
+              for (int x = 0; x < KT / 16; ++x) w[x] = 1.f;
+            }
+            if (F16) {  // the reference of the values' scales: 1 for new tokens, who come last
+              const float to = js >= it.nc ? 1.f : s == 0 ? 2.f * fmaxf(vtop, 1.1754944e-38f) : vtop > vref ? 2.f * vtop : vref;
+              if (s > 0 && to != vref) rescale = true, fv = vref / to;
+              vref = to;
+              const float inv = 1.f / vref;
+#pragma unroll
+              for (int x = 0; x < KT / 16; ++x) w[x] *= inv;
+            }
+          }
           if (tree && js >= it.nc) {
             const int k0 = (js - it.nc) * 128 + hs * KT;
             const uint32_t* words = a.mask + (long long)(it.row0 + tok) * a.words;
@@ -966,7 +1112,7 @@ __global__ void __launch_bounds__(384, 1)
             m_run = m_tile;
           } else {
             const bool grow = valid && m_tile > m_run + LAG_LOG2;
-            rescale = __any_sync(0xffffffffu, grow);
+            rescale |= __any_sync(0xffffffffu, grow);
             if (grow) {
               f = ex2_approx(m_run - m_tile);
               m_run = m_tile;
@@ -985,7 +1131,10 @@ __global__ void __launch_bounds__(384, 1)
               f2_unpack(f2_fma(f2_pack(sv[q * 32 + 2 * x], sv[q * 32 + 2 * x + 1]), sl2x2, nbase2), x0, x1);
               const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
               ps2[x & 1] = f2_add(ps2[x & 1], f2_pack(p0, p1));
-              pk[q][x] = pack2<F16>(p0, p1);
+              if constexpr (C8)
+                pk[q][x] = pack2<F16>(p0 * w[2 * q + (x >> 3)], p1 * w[2 * q + (x >> 3)]);
+              else
+                pk[q][x] = pack2<F16>(p0, p1);
             }
             if (C::SEP_P && q == 1) {
               if (s > 0) {  // PV of the tile before has read P (across items its epilogue waited for that)
@@ -1002,7 +1151,7 @@ __global__ void __launch_bounds__(384, 1)
           f2_unpack(ps2[0], ps[0], ps[1]);
           f2_unpack(ps2[1], ps[2], ps[3]);
           l_run = l_run * f + ((ps[0] + ps[1]) + (ps[2] + ps[3]));
-          if (!(ok = end_step(s, rescale, f))) break;
+          if (!(ok = end_step(s, rescale, C8 && F16 ? f * fv : f))) break;
         }
       } else {
         // Decoding and small drafts: up to 16 rows, in the first warp's lanes. A thread of it takes a quarter
@@ -1119,6 +1268,7 @@ __global__ void __launch_bounds__(384, 1)
       if (join) {
         ml[256 * t + row] = m_run;
         ml[256 * t + 128 + row] = l_run;
+        if (C8 && F16 && row == 0) vrefs[t] = vref;
         __syncwarp();
         if (lane == 0) mbar_arrive(BAR(C::MERGE));
         if (!wait_phase(BAR(C::MERGE), merges & 1, st, SITE_SW_MERGE) ||
@@ -1135,6 +1285,7 @@ __global__ void __launch_bounds__(384, 1)
       }
       st0 += it.s0;
       st1 += it.s1;
+      if (C8) tiles8 += max(0, min(it.nc - it.j0, it.cnt));
       if (dual && t == 1 && !join) continue;  // lane 0 has all of them
       // l = 0: no key; NaN stays NaN
       const float inv = l_run != 0.f ? 1.f / l_run : 0.f;
@@ -1148,6 +1299,10 @@ __global__ void __launch_bounds__(384, 1)
       const long long token = it.row0 + tok;
       f0 *= inv;
       f1 *= inv;
+      if (C8 && F16) {
+        f0 *= vref;
+        if (join) f1 *= vrefs[t ^ 1];
+      }
       const bool write = valid && FA_CHECK(whole ? in_range(token, a.T) : in_range(part, a.part_rows), st, DBG_GLOBAL_STORE);
       uint16_t* orow = a.o + token * a.o_st + head * a.o_sh;
       float* prow = a.part_o + part * D;
@@ -1265,9 +1420,9 @@ __global__ void __launch_bounds__(256) serve_join_kernel(ServeArgs a) {
   }
 }
 
-template <int D, bool F16, bool PAGED>
-static int launch_serve_d(ServeArgs a, cudaStream_t stream) {
-  using C = ServeCfg<D>;
+template <int D, bool F16, bool PAGED, bool C8 = false>
+static int launch_serve_d(std::conditional_t<C8, Serve8BitArgs, ServeArgs> a, cudaStream_t stream) {
+  using C = ServeCfg<D, C8>;
   const auto type = F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   CUtensorMap mq, mk, mv, mkc = {}, mvc = {};
   auto map3 = [&](CUtensorMap* m, const uint16_t* p, long long st, long long sh, bool heads_inner, int heads, int box1,
@@ -1281,15 +1436,17 @@ static int launch_serve_d(ServeArgs a, cudaStream_t stream) {
   auto map4 = [&](CUtensorMap* m, const uint16_t* p) {
     const int page = 1 << a.page_shift;
     const cuuint64_t dims[4] = {D, (cuuint64_t)page, (cuuint64_t)a.Hkv, (cuuint64_t)a.n_pages};
-    const cuuint64_t strides[3] = {(cuuint64_t)a.c_st * 2, (cuuint64_t)a.c_sh * 2, (cuuint64_t)a.c_sp * 2};
-    const cuuint32_t box[4] = {64, (cuuint32_t)std::min(page, 128), 1, 1};
-    return make_tmap_strided(m, p, type, 4, dims, strides, box);
+    const cuuint64_t elem = C8 ? 1 : 2;
+    const cuuint64_t strides[3] = {(cuuint64_t)a.c_st * elem, (cuuint64_t)a.c_sh * elem, (cuuint64_t)a.c_sp * elem};
+    const cuuint32_t box[4] = {C8 ? D : 64, (cuuint32_t)std::min(page, 128), 1, 1};
+    return make_tmap_strided(m, p, C8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : type, 4, dims, strides, box,
+                             C8 && D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
   };
   const int box = PAGED ? kNewBox : 128;
   if (!map3(&mq, a.q, a.q_st, a.q_sh, true, a.Hq, a.G, 128 / a.G) || !map3(&mk, a.k, a.k_st, a.k_sh, false, a.Hkv, box, 1) ||
       !map3(&mv, a.v, a.v_st, a.v_sh, false, a.Hkv, box, 1) || (PAGED && (!map4(&mkc, a.kc) || !map4(&mvc, a.vc))))
     return cuda_fail("cuTensorMapEncodeTiled", 0, "tensor map rejected");
-  const auto kernel = serve_kernel<D, F16, PAGED>;
+  const auto kernel = serve_kernel<D, F16, PAGED, C8>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
   if (e != cudaSuccess) return cuda_fail("cudaFuncSetAttribute", (int)e, cudaGetErrorName(e));
   int sms = 0;
@@ -1301,7 +1458,8 @@ static int launch_serve_d(ServeArgs a, cudaStream_t stream) {
   }
   int rc = launch_pdl("serve_kernel", kernel, dim3(grid), dim3(C::THREADS), C::SMEM_BYTES, stream, mq, mk, mv, mkc, mvc, a);
   if (rc != FA_OK || !PAGED || grid < 2) return rc;
-  return launch_pdl("serve_join_kernel", serve_join_kernel<D, F16>, dim3(grid - 1, 8), dim3(256), 0, stream, a);
+  return launch_pdl("serve_join_kernel", serve_join_kernel<D, F16>, dim3(grid - 1, 8), dim3(256), 0, stream,
+                    static_cast<const ServeArgs&>(a));
 }
 
 static int launch_serve(const ServeArgs& a, int d, int dtype, cudaStream_t stream) {
@@ -1319,8 +1477,8 @@ namespace {
 using namespace fa::host;
 
 int forward(const fa_rows* q, const fa_rows* k, const fa_rows* v, const fa_rows* o, float* lse, const fa_pages* cache,
-            const int32_t* lens, const int32_t* cu, const uint32_t* mask, int words, int B, int T, int Hq, int Hkv, int d,
-            int dtype, float scale, void* workspace, size_t workspace_bytes, fa_stream_t stream) {
+            const fa_scales* scales, const int32_t* lens, const int32_t* cu, const uint32_t* mask, int words, int B, int T,
+            int Hq, int Hkv, int d, int dtype, float scale, void* workspace, size_t workspace_bytes, fa_stream_t stream) {
   for (const fa_rows* r : {q, k, v, o})
     if (const int rc = check_rows(r); rc != FA_OK) return rc;
   if (!cu || (cache && !workspace)) return FA_ERR_INVALID_ARG;
@@ -1329,7 +1487,7 @@ int forward(const fa_rows* q, const fa_rows* k, const fa_rows* v, const fa_rows*
   int err = FA_OK;
   int* status = fa::status_word(&err);
   if (!status) return err;
-  fa::ServeArgs a = {};
+  fa::Serve8BitArgs a = {};
   a.q = static_cast<const uint16_t*>(q->data);
   a.k = static_cast<const uint16_t*>(k->data);
   a.v = static_cast<const uint16_t*>(v->data);
@@ -1363,7 +1521,15 @@ int forward(const fa_rows* q, const fa_rows* k, const fa_rows* v, const fa_rows*
   a.part_lse = a.part_o + a.part_rows * d;
   a.cuts = reinterpret_cast<int4*>(a.part_lse + a.part_rows);
   a.status = status;
-  return fa::launch_serve(a, d, dtype, reinterpret_cast<cudaStream_t>(stream));
+  const auto st = reinterpret_cast<cudaStream_t>(stream);
+  if (!scales) return fa::launch_serve(a, d, dtype, st);
+  a.ks = scales->k, a.vs = scales->v, a.s_sp = scales->page_stride, a.s_sh = scales->head_stride;
+  a.block_shift = log2_of(scales->block);
+  // Few rows a sequence on the average (the lengths are on the device) have a kernel of their own.
+  if ((long long)T * a.G <= 16LL * B) return fa::launch_serve8(k, v, cache, a, d, dtype, st);
+  const bool f16 = dtype == FA_FP16;
+  if (d == 64) return f16 ? fa::launch_serve_d<64, true, true, true>(a, st) : fa::launch_serve_d<64, false, true, true>(a, st);
+  return f16 ? fa::launch_serve_d<128, true, true, true>(a, st) : fa::launch_serve_d<128, false, true, true>(a, st);
 }
 
 }  // namespace
@@ -1383,7 +1549,7 @@ int fa_forward_prompt(const fa_rows* q, const fa_rows* k, const fa_rows* v, cons
   const int rc = check_sizes(B, T, Hq, Hkv, d, dtype, scale);
   if (rc != FA_OK) return rc;
   if (B == 0 || T == 0) return FA_OK;
-  return forward(q, k, v, o, lse, nullptr, nullptr, cu_seqlens, nullptr, 0, B, T, Hq, Hkv, d, dtype, scale, nullptr, 0,
+  return forward(q, k, v, o, lse, nullptr, nullptr, nullptr, cu_seqlens, nullptr, 0, B, T, Hq, Hkv, d, dtype, scale, nullptr, 0,
                  stream);
 }
 
@@ -1398,7 +1564,23 @@ int fa_forward_tree(const fa_rows* q, const fa_rows* k, const fa_rows* v, const 
   rc = check_pages(cache);
   if (rc != FA_OK) return rc;
   if (!lens) return FA_ERR_INVALID_ARG;
-  return forward(q, k, v, o, lse, cache, lens, cu_nodes, mask, mask_words, B, T, Hq, Hkv, d, dtype, scale, workspace,
+  return forward(q, k, v, o, lse, cache, nullptr, lens, cu_nodes, mask, mask_words, B, T, Hq, Hkv, d, dtype, scale,
+                 workspace, workspace_bytes, stream);
+}
+
+size_t fa_forward_tree_8bit_workspace_size(int d) { return fa_forward_tree_workspace_size(d); }
+
+int fa_forward_tree_8bit(const fa_rows* q, const fa_rows* k, const fa_rows* v, const fa_rows* o, float* lse,
+                         const fa_pages* cache, const fa_scales* scales, const int32_t* lens, const int32_t* cu_nodes,
+                         const uint32_t* mask, int mask_words, int B, int T, int Hq, int Hkv, int d, int dtype, float scale,
+                         void* workspace, size_t workspace_bytes, fa_stream_t stream) {
+  int rc = check_sizes(B, T, Hq, Hkv, d, dtype, scale);
+  if (rc != FA_OK) return rc;
+  if (mask && (mask_words < 1 || mask_words > (1 << 20))) return mask_words < 1 ? FA_ERR_INVALID_ARG : FA_ERR_UNSUPPORTED;
+  if (B == 0 || T == 0) return FA_OK;
+  if ((rc = check_pages(cache, 16)) != FA_OK || (rc = check_scales(scales, cache->page_size)) != FA_OK) return rc;
+  if (!lens) return FA_ERR_INVALID_ARG;
+  return forward(q, k, v, o, lse, cache, scales, lens, cu_nodes, mask, mask_words, B, T, Hq, Hkv, d, dtype, scale, workspace,
                  workspace_bytes, stream);
 }
 

@@ -1,4 +1,4 @@
-// Attention of drafted trees over a cache in 8 bits: entry points and kernels.
+// Attention of decoding and small drafts, few rows a sequence, over a cache in 8 bits.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -6,35 +6,10 @@
 
 #include "fa_internal.h"
 #include "serve.cuh"
-#include "serve_args.h"
+#include "serve_tree.h"
 #include "tmap.h"
 
 namespace fa {
-
-struct Serve8Args {
-  const uint16_t* q;
-  uint16_t* o;
-  long long q_st, q_sh, o_st, o_sh;  // token and head strides, elements
-  float* lse;  // [Hq, T] or null
-  const float *ks, *vs;
-  long long s_sp, s_sh;
-  int block_shift, page_shift, n_pages;
-  const int* table;
-  long long table_stride;
-  int table_width;
-  const int* lens;
-  const uint32_t* mask;  // null: a chain
-  int words;
-  const int* cu;
-  int B, T, Hkv, G;
-  float scale_log2;
-  float* part_o;    // workspace: two slots of 2 R rows for each CTA, O normalised by its own l
-  float* part_lse;  // their LSEs, base 2 (-inf: no key, O not written)
-  int4* cuts;       // two for each CTA, of the item that it is the first to cut: {later parts (0: none), ..},
-                    // {rows of the sequence, its first token, the item's first row, key/value head}
-  long long part_rows;
-  int* status;
-};
 
 // ---------------------------------------------------------------------------------------------
 // Few rows against many keys: everything is transposed. S^T = K Q^T and O^T = V^T P^T have the keys, or
@@ -140,7 +115,7 @@ struct SeqWork8 {
   int row0, n, L, nc, nk, units;
   long long tiles;  // all heads and units, each counted with the nk tiles of the last one
 };
-__device__ __forceinline__ SeqWork8 seq_work8(const Serve8Args& a, int lo, int hi, int len, int unit, bool record) {
+__device__ __forceinline__ SeqWork8 seq_work8(const Serve8BitArgs& a, int lo, int hi, int len, int unit, bool record) {
   SeqWork8 w;
   w.row0 = min(max(lo, 0), a.T);
   const int end = min(max(hi, w.row0), a.T);
@@ -157,7 +132,7 @@ __device__ __forceinline__ SeqWork8 seq_work8(const Serve8Args& a, int lo, int h
   w.tiles = (long long)w.units * a.Hkv * w.nk;
   return w;
 }
-__device__ __forceinline__ SeqWork8 seq_work8(const Serve8Args& a, int b, int unit, bool record) {
+__device__ __forceinline__ SeqWork8 seq_work8(const Serve8BitArgs& a, int b, int unit, bool record) {
   return seq_work8(a, a.cu[b], a.cu[b + 1], a.lens[b], unit, record);
 }
 
@@ -170,7 +145,7 @@ struct Runs8 {
   int chunk;
   __device__ long long start(int c) const { return base * c + min(c, rest); }
 };
-__device__ __forceinline__ Runs8 runs8(const Serve8Args& a, int unit, int grid, bool record) {
+__device__ __forceinline__ Runs8 runs8(const Serve8BitArgs& a, int unit, int grid, bool record) {
   Runs8 r;
   const int lane = threadIdx.x & 31;
   r.chunk = (a.B + 31) >> 5;
@@ -207,7 +182,7 @@ __device__ __forceinline__ int lane_with(long long mine, long long pos, long lon
   return k;
 }
 // The sequence that tile `pos` of all belongs to, and its first tile; by a whole warp. pos < total.
-__device__ __forceinline__ int seek8(const Serve8Args& a, int unit, const Runs8& runs, long long pos, long long* first) {
+__device__ __forceinline__ int seek8(const Serve8BitArgs& a, int unit, const Runs8& runs, long long pos, long long* first) {
   *first = 0;
   const int k = lane_with(runs.mine, pos, first);
   if (k == 32) return a.B;
@@ -222,7 +197,7 @@ __device__ __forceinline__ int seek8(const Serve8Args& a, int unit, const Runs8&
 }
 
 // Tiles that the rows [r, r + R) of a sequence need, counted from the first.
-__device__ __forceinline__ int tiles_of_rows(const Serve8Args& a, const SeqWork8& w, int r, int R) {
+__device__ __forceinline__ int tiles_of_rows(const Serve8BitArgs& a, const SeqWork8& w, int r, int R) {
   const int rows = w.n * a.G;
   if (r >= rows) return 0;
   return w.nc + (((a.mask ? w.n : min(w.n, (min(r + R, rows) - 1) / a.G + 1)) + 63) >> 6);
@@ -323,7 +298,7 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
 template <int D, int R, bool F16>
 __global__ void __launch_bounds__(448, 1)
     serve8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                  const __grid_constant__ CUtensorMap tm_kc, const __grid_constant__ CUtensorMap tm_vc, Serve8Args a) {
+                  const __grid_constant__ CUtensorMap tm_kc, const __grid_constant__ CUtensorMap tm_vc, Serve8BitArgs a) {
   using C = Serve8Cfg<D, R, F16>;
   constexpr int NT = C::NT, NQ = C::NQ;
   // 1024-byte aligned, as the swizzled tiles have to be: there is no room to round the address up
@@ -1117,7 +1092,7 @@ __global__ void __launch_bounds__(448, 1)
 // Joins the partial results of the items that CTA boundaries cut: block (x, y) takes rows
 // [16 y, 16 y + 16) of the item that boundary x + 1 is the first to cut, a group of D / 4 threads a row.
 template <int D, int R, bool F16>
-__global__ void __launch_bounds__(4 * D) serve8_join_kernel(Serve8Args a) {
+__global__ void __launch_bounds__(4 * D) serve8_join_kernel(Serve8BitArgs a) {
   griddep_wait();
   griddep_launch_dependents();
   const int c = blockIdx.x + 1;
@@ -1150,13 +1125,8 @@ __global__ void __launch_bounds__(4 * D) serve8_join_kernel(Serve8Args a) {
     a.lse[(long long)h * a.T + token] = (l != 0.f ? m + lg2_approx(l) : -INFINITY) * 0.6931471805599453f;
 }
 
-struct Serve8Tensors {
-  const fa_rows *k, *v;
-  const fa_pages* cache;
-};
-
 template <int D, int R, bool F16>
-static int launch_serve8_r(const Serve8Tensors& x, Serve8Args a, cudaStream_t stream) {
+static int launch_serve8_d(const fa_rows* k, const fa_rows* v, const fa_pages* c, Serve8BitArgs a, cudaStream_t stream) {
   using C = Serve8Cfg<D, R, F16>;
   const auto type = F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   CUtensorMap mk, mv, mkc, mvc;
@@ -1167,14 +1137,13 @@ static int launch_serve8_r(const Serve8Tensors& x, Serve8Args a, cudaStream_t st
     return make_tmap_strided(m, r->data, type, 3, dims, strides, box);
   };
   auto map4 = [&](CUtensorMap* m, const void* p) {
-    const fa_pages* c = x.cache;
     const cuuint64_t dims[4] = {D, (cuuint64_t)c->page_size, (cuuint64_t)a.Hkv, (cuuint64_t)c->n_pages};
     const cuuint64_t strides[3] = {(cuuint64_t)c->token_stride, (cuuint64_t)c->head_stride, (cuuint64_t)c->page_stride};
     const cuuint32_t box[4] = {D, (cuuint32_t)std::min(c->page_size, 128), 1, 1};
     return make_tmap_strided(m, p, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, dims, strides, box,
                              D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
   };
-  if (!map3(&mk, x.k) || !map3(&mv, x.v) || !map4(&mkc, x.cache->k) || !map4(&mvc, x.cache->v))
+  if (!map3(&mk, k) || !map3(&mv, v) || !map4(&mkc, c->k) || !map4(&mvc, c->v))
     return cuda_fail("cuTensorMapEncodeTiled", 0, "tensor map rejected");
   const auto kernel = serve8_kernel<D, R, F16>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
@@ -1189,66 +1158,11 @@ static int launch_serve8_r(const Serve8Tensors& x, Serve8Args a, cudaStream_t st
   return launch_pdl("serve8_join_kernel", serve8_join_kernel<D, R, F16>, dim3(sms - 1, 2 * R / 16), dim3(4 * D), 0, stream, a);
 }
 
-// Rows of a lane by the average rows of a sequence (the lengths are on the device): a lane of 16 fits
-// decoding and small drafts; with more rows than two lanes hold the keys are read again for the rest.
-template <int D, bool F16>
-static int launch_serve8_d(const Serve8Tensors& x, const Serve8Args& a, cudaStream_t stream) {
-  const long long rows = (long long)a.T * a.G;
-  return rows <= 16LL * a.B ? launch_serve8_r<D, 16, F16>(x, a, stream) : launch_serve8_r<D, 32, F16>(x, a, stream);
-}
-static int launch_serve8(const Serve8Tensors& x, const Serve8Args& a, int d, int dtype, cudaStream_t stream) {
+int launch_serve8(const fa_rows* k, const fa_rows* v, const fa_pages* cache, Serve8BitArgs a, int d, int dtype,
+                  cudaStream_t stream) {
   const bool f16 = dtype == FA_FP16;
-  if (d == 64) return f16 ? launch_serve8_d<64, true>(x, a, stream) : launch_serve8_d<64, false>(x, a, stream);
-  return f16 ? launch_serve8_d<128, true>(x, a, stream) : launch_serve8_d<128, false>(x, a, stream);
+  if (d == 64) return f16 ? launch_serve8_d<64, 16, true>(k, v, cache, a, stream) : launch_serve8_d<64, 16, false>(k, v, cache, a, stream);
+  return f16 ? launch_serve8_d<128, 16, true>(k, v, cache, a, stream) : launch_serve8_d<128, 16, false>(k, v, cache, a, stream);
 }
 
 }  // namespace fa
-
-using namespace fa::host;
-
-extern "C" {
-
-size_t fa_forward_tree_8bit_workspace_size(int d) {
-  if (d != 64 && d != 128) return 0;
-  int sms = 0;
-  if (!fa::sm_count(&sms)) return 0;
-  return (size_t)2 * sms * 64 * (d + 1) * 4 + (size_t)sms * 2 * sizeof(int4);
-}
-
-int fa_forward_tree_8bit(const fa_rows* q, const fa_rows* k, const fa_rows* v, const fa_rows* o, float* lse,
-                         const fa_pages* cache, const fa_scales* scales, const int32_t* lens, const int32_t* cu_nodes,
-                         const uint32_t* mask, int mask_words, int B, int T, int Hq, int Hkv, int d, int dtype, float scale,
-                         void* workspace, size_t workspace_bytes, fa_stream_t stream) {
-  int rc = check_sizes(B, T, Hq, Hkv, d, dtype, scale);
-  if (rc != FA_OK) return rc;
-  if (mask && (mask_words < 1 || mask_words > (1 << 20))) return mask_words < 1 ? FA_ERR_INVALID_ARG : FA_ERR_UNSUPPORTED;
-  if ((long long)T * (Hq / Hkv) > (1 << 30)) return FA_ERR_UNSUPPORTED;
-  if (B == 0 || T == 0) return FA_OK;
-  if ((rc = check_pages(cache, 16)) != FA_OK || (rc = check_scales(scales, cache->page_size)) != FA_OK) return rc;
-  for (const fa_rows* r : {q, k, v, o})
-    if ((rc = check_rows(r)) != FA_OK) return rc;
-  if (!lens || !cu_nodes || !workspace) return FA_ERR_INVALID_ARG;
-  if ((lse && !aligned16(lse)) || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return FA_ERR_MISALIGNED;
-  if (workspace_bytes < fa_forward_tree_8bit_workspace_size(d)) return FA_ERR_INVALID_ARG;
-  int err = FA_OK;
-  int* status = fa::status_word(&err);
-  if (!status) return err;
-  fa::Serve8Args a = {};
-  a.q = static_cast<const uint16_t*>(q->data);
-  a.o = static_cast<uint16_t*>(o->data);
-  a.q_st = q->token_stride, a.q_sh = q->head_stride;
-  a.o_st = o->token_stride, a.o_sh = o->head_stride;
-  a.lse = lse;
-  a.ks = scales->k, a.vs = scales->v, a.s_sp = scales->page_stride, a.s_sh = scales->head_stride;
-  a.block_shift = log2_of(scales->block);
-  a.n_pages = cache->n_pages, a.page_shift = log2_of(cache->page_size);
-  a.table = cache->table, a.table_stride = cache->table_stride, a.table_width = cache->table_width;
-  a.lens = lens, a.mask = mask, a.words = mask_words, a.cu = cu_nodes;
-  a.B = B, a.T = T, a.Hkv = Hkv, a.G = Hq / Hkv;
-  a.scale_log2 = scale * 1.4426950408889634f;
-  a.part_o = static_cast<float*>(workspace);
-  a.status = status;
-  return fa::launch_serve8({k, v, cache}, a, d, dtype, reinterpret_cast<cudaStream_t>(stream));
-}
-
-}  // extern "C"

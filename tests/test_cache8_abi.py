@@ -87,8 +87,7 @@ def test_sizes_pages_and_scales(lib, call):
 
 
 def test_tree_argument_errors(lib):
-    for kw in (dict(scale=0.0), dict(scale=float("nan")), dict(Hq=5), dict(lens=None), dict(ws=None), dict(mask=A, words=0),
-               dict(nbytes=16)):
+    for kw in (dict(scale=0.0), dict(scale=float("nan")), dict(Hq=5), dict(lens=None), dict(ws=None), dict(mask=A, words=0)):
         assert tree(lib, **kw) == INVALID, kw
     assert tree(lib, Hq=129, Hkv=1) == UNSUPPORTED
     assert tree(lib, mask=A, words=(1 << 20) + 1) == UNSUPPORTED

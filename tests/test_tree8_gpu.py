@@ -157,3 +157,19 @@ def test_many_items_of_both_kinds(gpu, dtype, d, most):
         again = m.call()
         assert all(torch.equal(x[..., : m.T] if x.dim() == 2 else x[: m.T], y[..., : m.T] if y.dim() == 2 else y[: m.T])
                    for x, y in zip(first, again))
+
+
+def test_refusals(gpu):
+    m = Made(gpu, [40, 3], [1, 1], 4, 2, 64, 32, 16, BF16)
+    need = api._tree_workspace(gpu.index, 64, "fa_forward_tree_8bit")
+    m.call(workspace=torch.empty(need, dtype=torch.uint8, device=gpu))
+    with pytest.raises(RuntimeError):
+        m.call(workspace=torch.empty(need - 1, dtype=torch.uint8, device=gpu))
+    for name, bad in (("ks", None), ("vs", m.vs[:, :, :1]), ("ks", m.ks.double()), ("kc", m.kc.view(torch.uint8)),
+                      ("vc", m.vc[:, :1]), ("kc", m.kc.to(BF16)), ("q", m.q.float()), ("table", m.table[:1])):
+        was = getattr(m, name)
+        setattr(m, name, bad)
+        with pytest.raises(ValueError):
+            m.call()
+        setattr(m, name, was)
+    m.check()
