@@ -60,35 +60,42 @@ constexpr int kNewBox = 16;
 // tensor pipe (81-84 % busy) beside memory at 76 %.
 //
 // A cache in 8 bits (C8): the pages arrive in a ring of their own, and four more warps (12-15) turn them into tiles
-// of 16 bits (exactly) in the ring that the products read, so that all else is as it is. A converter thread takes
+// of fp16 (exactly) in the ring that the products read, so that all else is as it is. A converter thread takes
 // 16 elements of one key at a time, the lanes of a quarter-warp eight keys that follow each other, which the
-// swizzled rows of both sides spread over all banks. The scales of 16 keys each come with K's pages: that of
-// K multiplies S, that of V the probability, in bf16 as it is (the type's range holds it); fp16 divides
-// by a reference (vref, twice the largest so far), which O keeps up with as it does with the maximum. The
-// tiles of new tokens are loaded by the converters, who meet all entries of the ring in order.
+// swizzled rows of both sides spread over all banks. The products are fp16 for bf16 queries too: e4m3 to fp16 is one
+// instruction for two elements, to bf16 four (with it, full trees of 64 nodes took 398 us). The converters bring the
+// queries, and the keys and values of new tokens, to fp16 with a power of two for each 32 rows that takes their
+// largest element to [2^14, 2^15): elements keep their bits down to 2^-28 of that one. They load the new tokens
+// too, as they meet all entries of the ring in order.
+// Scales: that of a key's block of 16 multiplies its scores within the exponential's argument, and the block's
+// maximum; that of a value's adds its logarithm there, so that P is formed with it, and the sum l takes it out
+// again by blocks. A reference (vref, twice the largest so far) keeps P in range; O keeps up with it as it does
+// with the maximum.
 template <int D, bool C8 = false>
 struct ServeCfg {
   static constexpr int NSUB = D / 64;
-  static constexpr int SUB_BYTES = 128 * 128;
-  static constexpr int TILE_BYTES = NSUB * SUB_BYTES;
-  static constexpr int NSLOT = C8 ? (D == 64 ? 6 : 3) : D == 64 ? 12 : 5;
-  static constexpr int STAGE = 128 * D, NS8 = C8 ? (D == 64 ? 8 : 4) : 0;  // pages of 8 bits
-  static constexpr int SCALES = C8 ? (D == 64 ? 16 : 4) : 0;  // tiles whose scales are kept: those with an entry in either ring
+  static constexpr int SUB_BYTES = 128 * 128, Q_BYTES = NSUB * SUB_BYTES;
+  static constexpr int TK = C8 ? 64 : 128, TK_LOG2 = C8 ? 6 : 7;  // keys of a tile
+  static constexpr int KSUB_BYTES = TK * 128, TILE_BYTES = NSUB * KSUB_BYTES;
+  static constexpr int NSLOT = C8 ? (D == 64 ? 10 : 6) : D == 64 ? 12 : 5;
+  static constexpr int STAGE = TK * D, NS8 = C8 ? (D == 64 ? 12 : 6) : 0;  // pages of 8 bits
+  // tiles whose scales are kept: more than have an entry in either ring, or have not been met by the softmax
+  static constexpr int SCALES = C8 ? 16 : 0;
   static constexpr int OFF_Q = 0;
-  static constexpr int OFF_R = 2 * TILE_BYTES;
+  static constexpr int OFF_R = 2 * Q_BYTES;
   static constexpr int OFF_S8 = OFF_R + NSLOT * TILE_BYTES;
-  static constexpr int OFF_BAR = OFF_S8 + NS8 * STAGE;
-  static constexpr int OFF_DESC = OFF_BAR + 512;   // 4 x 16 ints
-  static constexpr int OFF_ML = OFF_BAR + 768;     // m and l of both lanes' rows, for the join of a dual item
-  static constexpr int OFF_SC = OFF_ML + 2048;     // [tile][K of 8 groups of 16 keys, V of 8]
-  static constexpr int SMEM_BYTES = OFF_SC + SCALES * 64;
+  static constexpr int OFF_BAR = OFF_S8 + NS8 * STAGE, BAR_AREA = C8 ? 2048 : 512;
+  static constexpr int OFF_DESC = OFF_BAR + BAR_AREA;  // 4 x 16 ints
+  static constexpr int OFF_ML = OFF_DESC + 256;    // m and l of both lanes' rows, for the join of a dual item
+  static constexpr int OFF_SC = OFF_ML + 2048;     // [tile][K of 4 groups of 16 keys, V of 4]
+  static constexpr int SMEM_BYTES = OFF_SC + SCALES * 32;
   // A key tile is taken in HPT steps of KT keys. The softmax must find S of the next step ready
   // when it ends one, so S may not wait for PV of the step before. TMEM has room for that in two
   // ways: d = 64 keeps P apart from S (one step a tile; S is free once it is in registers);
   // d = 128, where O takes half the columns, takes a tile as two halves; even and odd steps of a
   // lane have a buffer each, P over its own S, and S is formed two steps ahead.
   static constexpr bool SEP_P = D == 64 && !C8;
-  static constexpr int KT = SEP_P ? 128 : 64, HPT = 128 / KT;
+  static constexpr int KT = SEP_P ? 128 : 64, HPT = TK / KT;
   __device__ static constexpr int buf(int g) { return SEP_P ? 0 : g & 1; }            // of a lane's step g
   __device__ static constexpr uint32_t phase(int g) { return (SEP_P ? g : g >> 1) & 1; }  // of its barriers
   __device__ static constexpr uint32_t tm_s(int t, int u) { return 128u * t + 64u * u; }
@@ -102,8 +109,13 @@ struct ServeCfg {
   static constexpr int FULL = 0, EMPTY = NSLOT, Q_FULL = 2 * NSLOT, Q_EMPTY = Q_FULL + 2, S_FULL = Q_EMPTY + 2,
                        P_READY = S_FULL + 4, O_DONE = P_READY + 4, S_FREE = O_DONE + 4, O_FREE = S_FREE + 2,
                        MERGE = O_FREE + 2, DRAIN = MERGE + 1, D_FULL = DRAIN + 1, D_EMPTY = D_FULL + 4,
-                       FULL8 = D_EMPTY + 4, EMPTY8 = FULL8 + NS8, BARS = EMPTY8 + NS8;
-  static_assert(8 * BARS + 20 <= 512, "barrier area");
+                       FULL8 = D_EMPTY + 4, EMPTY8 = FULL8 + NS8, Q_RAW = EMPTY8 + NS8, NEW_RAW = Q_RAW + 2 * C8,
+                       BARS = NEW_RAW + NSLOT * C8;
+  // behind the barriers: three words, and with C8 vref of both lanes, the factors of 32 rows of each Q slot, and
+  // those of 32 keys, K and V, of the last new tiles
+  static constexpr int OFF_VREF = 8 * BARS + 12, OFF_QF = OFF_VREF + 8, OFF_NSC = (OFF_QF + 32 + 15) / 16 * 16;
+  static_assert((C8 ? OFF_NSC + SCALES * 16 : 8 * BARS + 12) <= BAR_AREA, "barrier area");
+  static_assert(!C8 || (NSLOT % 2 == 0 && NS8 % 2 == 0), "K and V have slots of their own");
   static_assert(SMEM_BYTES <= 232448, "shared memory above 227 KB");
 };
 
@@ -134,7 +146,7 @@ struct SeqWork {
   int row0, n, L, nc, nk, units;
   long long tiles;  // all heads and units, each counted with the nk tiles of the last one
 };
-template <bool PAGED>
+template <bool PAGED, int TL>
 __device__ __forceinline__ SeqWork seq_sizes(const ServeArgs& a, int lo, int hi, int len, int unit, bool record) {
   SeqWork w;
   w.row0 = min(max(lo, 0), a.T);
@@ -146,15 +158,15 @@ __device__ __forceinline__ SeqWork seq_sizes(const ServeArgs& a, int lo, int hi,
     w.L = min(max(len, 0), a.table_width << a.page_shift);
     if (record && w.L != len) record_check(a.status, SITE_S_LENGTH);
   }
-  w.nc = (w.L + 127) >> 7;
-  w.nk = w.nc + ((w.n + 127) >> 7);
+  w.nc = (w.L + (1 << TL) - 1) >> TL;
+  w.nk = w.nc + ((w.n + (1 << TL) - 1) >> TL);
   w.units = (w.n + unit - 1) / unit;
   w.tiles = (long long)w.units * a.Hkv * w.nk;
   return w;
 }
-template <bool PAGED>
+template <bool PAGED, int TL>
 __device__ __forceinline__ SeqWork seq_work(const ServeArgs& a, int b, int unit, bool record) {
-  return seq_sizes<PAGED>(a, a.cu[b], a.cu[b + 1], PAGED ? a.lens[b] : 0, unit, record);
+  return seq_sizes<PAGED, TL>(a, a.cu[b], a.cu[b + 1], PAGED ? a.lens[b] : 0, unit, record);
 }
 
 __device__ __forceinline__ long long warp_sum(long long x) {
@@ -172,6 +184,7 @@ struct ServeRuns {
   int chunk;
   __device__ long long start(int c) const { return base * c + min(c, rest); }
 };
+template <int TL>
 __device__ __forceinline__ ServeRuns serve_runs(const ServeArgs& a, int unit, int grid, bool record) {
   ServeRuns r;
   const int lane = threadIdx.x & 31;
@@ -186,7 +199,7 @@ __device__ __forceinline__ ServeRuns serve_runs(const ServeArgs& a, int unit, in
     for (int k = 0; k < 4; ++k) len[k] = a.lens[min(b + k, end - 1)];
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      if (b + k < end) r.mine += seq_sizes<true>(a, at[k], at[k + 1], len[k], unit, record).tiles;
+      if (b + k < end) r.mine += seq_sizes<true, TL>(a, at[k], at[k + 1], len[k], unit, record).tiles;
   }
   r.total = warp_sum(r.mine);
   r.ctas = r.total < (long long)grid * kMinTiles ? max(1, ((int)r.total + kMinTiles - 1) / kMinTiles) : grid;
@@ -208,6 +221,7 @@ __device__ __forceinline__ int lane_of(long long mine, long long pos, long long*
   return k;
 }
 // The sequence that tile `pos` of all belongs to, and its first tile; by a whole warp. pos < total.
+template <int TL>
 __device__ __forceinline__ int serve_seek(const ServeArgs& a, int unit, const ServeRuns& runs, long long pos,
                                           long long* first) {
   *first = 0;
@@ -217,16 +231,17 @@ __device__ __forceinline__ int serve_seek(const ServeArgs& a, int unit, const Se
   const int end = min(a.B, (k + 1) * runs.chunk);
   for (int b0 = k * runs.chunk; b0 < end; b0 += 32) {
     const int b = b0 + (threadIdx.x & 31);
-    const int x = lane_of(b < end ? seq_work<true>(a, b, unit, false).tiles : 0, pos, first);
+    const int x = lane_of(b < end ? seq_work<true, TL>(a, b, unit, false).tiles : 0, pos, first);
     if (x < 32) return b0 + x;
   }
   return a.B;
 }
 
 // Key tiles that query tile u (tokens [u npt, ..)) of a sequence needs, counted from the first.
+template <int TL>
 __device__ __forceinline__ int tiles_of(const SeqWork& w, int u, int npt, bool tree) {
   if (u * npt >= w.n) return 0;
-  return w.nc + ((min(tree ? w.n : (u + 1) * npt, w.n) + 127) >> 7);
+  return w.nc + ((min(tree ? w.n : (u + 1) * npt, w.n) + (1 << TL) - 1) >> TL);
 }
 
 // Prompts: the tokens of an item, by a whole warp. Two query tiles share the keys that an item loads;
@@ -247,7 +262,7 @@ __device__ __forceinline__ int prompt_unit(const ServeArgs& a, int npt, int grid
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       if (b0 + 32 * k >= a.B) break;
-      const SeqWork w = seq_sizes<false>(a, lo[k], hi[k], 0, 2 * npt, record);
+      const SeqWork w = seq_sizes<false, 7>(a, lo[k], hi[k], 0, 2 * npt, record);
       tiles += (w.tiles + (long long)w.units * a.Hkv) / 2;  // item p of a sequence has about (p + 1) nk / units
       longest = max(longest, w.nk);
     }
@@ -289,7 +304,7 @@ struct PromptItems {
   }
   __device__ int units(int from) const {
     const int b = from + (threadIdx.x & 31);
-    return b < a.B ? seq_work<false>(a, b, unit, false).units : 0;
+    return b < a.B ? seq_work<false, 7>(a, b, unit, false).units : 0;
   }
   __device__ int above(int l) const {  // items of that level and up
     int x = 0;
@@ -339,26 +354,50 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return F16 ? pack_f16x2(lo, hi) : pack_bf16x2(lo, hi);
 }
 
-// Sixteen e4m3 as two 16-byte chunks of 16-bit values, exactly.
-template <bool F16>
+// Sixteen e4m3 as two 16-byte chunks of fp16, exactly.
 __device__ __forceinline__ void widen16(const uint4& x, uint4* lo, uint4* hi) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
   uint32_t r[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(w[i >> 1] >> (16 * (i & 1)))));
-    if (!F16) {
-      float a, b;
-      asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
-          : "=f"(a), "=f"(b)
-          : "r"(h));
-      h = pack_bf16x2(a, b);
-    }
-    r[i] = h;
-  }
+  for (int i = 0; i < 8; ++i)
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r[i]) : "h"((uint16_t)(w[i >> 1] >> (16 * (i & 1)))));
   *lo = make_uint4(r[0], r[1], r[2], r[3]);
   *hi = make_uint4(r[4], r[5], r[6], r[7]);
+}
+// Rows [row0, min(row0 + 32, rows)) of bf16 in swizzled tiles of 64 columns to fp16 in place, by a warp: times a power of
+// two that takes the largest finite element to [2^14, 2^15). Returns what undoes the factor. (Rows behind them
+// are nobody's, or masked, or, of V, zeroed before the product.)
+// Loops of few instructions: the code runs once an item, and fetching it anew is what it takes (unrolled, 32 rows of
+// 128 columns took 10000 cycles between the loops of the products, against 2600 at the start).
+template <int NSUB, int SUB_BYTES>
+__device__ __forceinline__ float to_fp16_rows(uint8_t* tile, int row0, int rows) {
+  const int lane = threadIdx.x & 31, steps = max(0, (min(32, rows - row0) + 3) >> 2) * NSUB;  // of 4 rows, 8 chunks each
+  auto place = [&](int y) {
+    return reinterpret_cast<uint4*>(tile + y % NSUB * SUB_BYTES + sw128_offset(row0 + y / NSUB * 4 + (lane >> 3), lane & 7));
+  };
+  uint32_t most2 = 0;  // two magnitudes, as whole numbers
+#pragma unroll 1
+  for (int y = 0; y < steps; ++y) {
+    const uint4 x = *place(y);
+    if (row0 + y / NSUB * 4 + (lane >> 3) >= rows) continue;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t w = (i == 0 ? x.x : i == 1 ? x.y : i == 2 ? x.z : x.w) & 0x7fff7fffu;
+      most2 = __vmaxu2(most2, w & __vcmpltu2(w, 0x7f807f80u));
+    }
+  }
+  const uint32_t most = __reduce_max_sync(0xffffffffu, max(most2 & 0xffffu, most2 >> 16));
+  const int e = max((int)(most >> 7) - 127, -100) - 14;  // 2^-e times the largest lies in [2^14, 2^15)
+  const float down = __uint_as_float((uint32_t)(127 - e) << 23), up = __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll 1
+  for (int y = 0; y < steps; ++y) {
+    uint4* at = place(y);
+    uint4 x = *at;
+    auto half2 = [&](uint32_t w) { return pack_f16x2(__uint_as_float(w << 16) * down, __uint_as_float(w & 0xffff0000u) * down); };
+    x.x = half2(x.x), x.y = half2(x.y), x.z = half2(x.z), x.w = half2(x.w);
+    *at = x;
+  }
+  return up;
 }
 
 template <int D, bool F16, bool PAGED, bool C8 = false>
@@ -367,7 +406,9 @@ __global__ void __launch_bounds__(C8 ? 512 : 384, 1)
                  const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_kc,
                  const __grid_constant__ CUtensorMap tm_vc, std::conditional_t<C8, Serve8BitArgs, ServeArgs> a) {
   using C = ServeCfg<D, C8>;
-  constexpr float P_LOG2 = F16 ? 9.f : 0.f, LAG_LOG2 = F16 ? 6.f : 8.f;
+  constexpr bool H = C8 || F16;         // the products are fp16
+  constexpr bool TURN = C8 && !F16;     // the converters bring Q, and K and V of new tokens, to fp16
+  constexpr float P_LOG2 = H ? 9.f : 0.f, LAG_LOG2 = H ? 6.f : 8.f;
   // 1024-byte aligned, as the swizzled tiles have to be: there is no room to round the address up
   extern __shared__ __align__(1024) uint8_t sm[];
   const uint32_t sbase = smem_u32(sm);
@@ -385,7 +426,9 @@ __global__ void __launch_bounds__(C8 ? 512 : 384, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::OFF_BAR + 8 * C::BARS);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
   volatile int* loading = reinterpret_cast<int*>(tmem_slot + 2);  // ring entries whose loads have begun
-  float* vrefs = reinterpret_cast<float*>(tmem_slot + 3);         // (C8) of both lanes, for the join
+  float* vrefs = reinterpret_cast<float*>(sm + C::OFF_BAR + C::OFF_VREF);  // (C8) of both lanes, for the join
+  float* qfs = reinterpret_cast<float*>(sm + C::OFF_BAR + C::OFF_QF);      // [slot][32 rows each]
+  float* nscales = reinterpret_cast<float*>(sm + C::OFF_BAR + C::OFF_NSC);  // [new tile][K of 32 keys each, V]
   float* scales = reinterpret_cast<float*>(sm + C::OFF_SC);
   DevStatus st{a.status, abort_flag};
   int* descs = reinterpret_cast<int*>(sm + C::OFF_DESC);
@@ -393,16 +436,17 @@ __global__ void __launch_bounds__(C8 ? 512 : 384, 1)
 
   if (warp == C::PRODUCER && lane == 0) {
     for (int i = 0; i < C::NSLOT; ++i) {
-      mbar_init(BAR(C::FULL + i), C8 ? 4 : 1);
+      mbar_init(BAR(C::FULL + i), C8 ? 4 : 1);  // (two converters twice, or, of K of new tokens, all four)
       mbar_init(BAR(C::EMPTY + i), 2);  // V: both issuers; K: its issuer twice
     }
     for (int i = 0; i < C::NS8; ++i) {
-      mbar_init(BAR(C::FULL8 + i), i & 1 ? 1 : 17);  // the copies, and with K each of 16 lanes' scale
-      mbar_init(BAR(C::EMPTY8 + i), 4);
+      mbar_init(BAR(C::FULL8 + i), i & 1 ? 1 : 9);  // the copies, and with K each of 8 lanes' scale
+      mbar_init(BAR(C::EMPTY8 + i), 2);
     }
     for (int t = 0; t < 2; ++t) {
-      mbar_init(BAR(C::Q_FULL + t), 1);
-      mbar_init(BAR(C::Q_EMPTY + t), 1);
+      mbar_init(BAR(C::Q_FULL + t), TURN ? 4 : 1);
+      if (C8) mbar_init(BAR(C::Q_RAW + t), 1);
+      mbar_init(BAR(C::Q_EMPTY + t), TURN ? 9 : 1);  // the issuer of S (and all softmax warps, or a lane's twice: its factors)
       for (int h = 0; h < 2; ++h) {
         mbar_init(BAR(C::S_FULL + 2 * t + h), 1);
         mbar_init(BAR(C::P_READY + 2 * t + h), 4);
@@ -411,6 +455,7 @@ __global__ void __launch_bounds__(C8 ? 512 : 384, 1)
       mbar_init(BAR(C::S_FREE + t), 4);
       mbar_init(BAR(C::O_FREE + t), 8);  // four warps twice, or all eight in a join
     }
+    for (int i = 0; i < (C8 ? C::NSLOT : 0); ++i) mbar_init(BAR(C::NEW_RAW + i), 1);
     mbar_init(BAR(C::MERGE), 8);
     mbar_init(BAR(C::DRAIN), 3);
     for (int i = 0; i < 4; ++i) {
@@ -485,12 +530,12 @@ __global__ void __launch_bounds__(C8 ? 512 : 384, 1)
     auto run_item = [&](const ServeItem& it, int b) {
       if (!publish(it)) return false;
       // page ids of a tile: lane (box r, column block c) = r NSUB + c, and lane 16 + r NSUB + c
-      const int prow = min(1 << a.page_shift, 128);  // rows of a page's box
+      const int prow = min(1 << a.page_shift, C::TK);  // rows of a page's box
       const int r = (lane & 15) / C::NSUB, c = lane % C::NSUB;
       auto page_of = [&](int j) {
-        if (C8) {  // lane (kv, g) = 8 kv + g: of 16 keys
-          const int t0 = j * 128 + (lane & 7) * 16;
-          return lane < 16 && j < min(it.j0 + it.cnt, it.nc) && t0 < it.L ? a.table[b * a.table_stride + (t0 >> a.page_shift)] : 0;
+        if (C8) {  // lane (kv, g) = 4 kv + g: of 16 keys
+          const int t0 = j * 64 + (lane & 3) * 16;
+          return lane < 8 && j < min(it.j0 + it.cnt, it.nc) && t0 < it.L ? a.table[b * a.table_stride + (t0 >> a.page_shift)] : 0;
         }
         const int pg = (j * 128 + r * prow) >> a.page_shift;
         const bool there = j < it.j0 + it.cnt && j < it.nc && r * prow < 128 && j * 128 + r * prow < it.L;
@@ -499,11 +544,11 @@ __global__ void __launch_bounds__(C8 ? 512 : 384, 1)
       int id = PAGED ? page_of(it.j0) : 0;
       const int nq = (it.flags & ITEM_DUAL) ? 1 : 2;
       for (int t = 0; t < nq; ++t, ++uq) {
-        const uint32_t qf = BAR(C::Q_FULL + (uq & 1));
+        const uint32_t qf = BAR((TURN ? C::Q_RAW : C::Q_FULL) + (uq & 1));
         if (!wait_phase(BAR(C::Q_EMPTY + (uq & 1)), ((uq >> 1) & 1) ^ 1, st, SITE_SW_Q_EMPTY)) return false;
         if (elect_one()) mbar_arrive_expect_tx(qf, (uint32_t)(npt * a.G * 128 * C::NSUB));
         __syncwarp();
-        const uint32_t dst = sbase + C::OFF_Q + (uq & 1) * C::TILE_BYTES;
+        const uint32_t dst = sbase + C::OFF_Q + (uq & 1) * C::Q_BYTES;
         if (lane < C::NSUB)
           tma_load_3d(dst + lane * C::SUB_BYTES, &tm_q, lane * 64, it.kvh * a.G, it.row0 + it.tok0 + t * npt, qf);
         __syncwarp();
@@ -511,27 +556,27 @@ __global__ void __launch_bounds__(C8 ? 512 : 384, 1)
       int j = it.j0;
       if constexpr (C8) {
         // K and V of a tile in one go, a lane for 16 keys: their scale, and the box that begins with them
-        const int kv = (lane >> 3) & 1, g = lane & 7, page_size = 1 << a.page_shift;
+        const int kv = (lane >> 2) & 1, g = lane & 3, page_size = 1 << a.page_shift;
         for (; j < min(it.j0 + it.cnt, it.nc); ++j, ++e) {
-          const int id_next = page_of(j + 1), rows = min(128, it.L - j * 128), boxes = (rows + prow - 1) / prow;
+          const int id_next = page_of(j + 1), rows = min(64, it.L - j * 64), boxes = (rows + prow - 1) / prow;
           const int sk = (2 * e) % C::NS8, sv = sk + 1;
           const uint32_t ph = ((2 * e / C::NS8) & 1) ^ 1;
           if (!wait_phase(BAR(C::EMPTY8 + sk), ph, st, SITE_SW_EMPTY8) || !wait_phase(BAR(C::EMPTY8 + sv), ph, st, SITE_SW_EMPTY8))
             return false;
-          const int t0 = j * 128 + g * 16, in_page = t0 & (page_size - 1);
-          const bool mine = lane < 16 && g * 16 < rows, there = id >= 0 && id < a.n_pages;
+          const int t0 = j * 64 + g * 16, in_page = t0 & (page_size - 1);
+          const bool mine = lane < 8 && g * 16 < rows, there = id >= 0 && id < a.n_pages;
           if (mine && !there) record_check(a.status, SITE_S_PAGE);
           if (elect_one()) {
             mbar_arrive_expect_tx(BAR(C::FULL8 + sk), (uint32_t)(boxes * prow * D));
             mbar_arrive_expect_tx(BAR(C::FULL8 + sv), (uint32_t)(boxes * prow * D));
           }
           __syncwarp();
-          float* to = scales + e % C::SCALES * 16 + lane;
+          float* to = scales + e % C::SCALES * 8 + lane;
           if (mine && there) {
             const float* from = (kv ? a.vs : a.ks) + id * a.s_sp + it.kvh * a.s_sh + (in_page >> a.block_shift);
             asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(to)), "l"(from) : "memory");
             asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(BAR(C::FULL8 + sk)) : "memory");
-          } else if (lane < 16) {
+          } else if (lane < 8) {
             *to = kv ? 0.f : 1.f;  // nothing there: its probabilities are 0, and stay out of vref
             mbar_arrive(BAR(C::FULL8 + sk));
           }
@@ -567,7 +612,7 @@ __global__ void __launch_bounds__(C8 ? 512 : 384, 1)
             mbar_arrive_expect_tx(BAR(C::FULL + s1), (uint32_t)(boxes * prow * 128 * C::NSUB));
           }
           __syncwarp();
-          const uint32_t dst = sbase + C::OFF_R + s * C::TILE_BYTES + c * C::SUB_BYTES + r * prow * 128;
+          const uint32_t dst = sbase + C::OFF_R + s * C::TILE_BYTES + c * C::KSUB_BYTES + r * prow * 128;
           if (mine && !(kWithhold && (e >> 1) == 1) &&
               FA_CHECK(smem_in(dst, prow * 128, sbase + C::OFF_R, sbase + C::OFF_BAR), st, DBG_TMA_LOAD))
             tma_load_4d(dst, lane < 16 ? &tm_kc : &tm_vc, c * 64, j * 128 & ((1 << a.page_shift) - 1) & ~127, it.kvh, page,
@@ -599,7 +644,7 @@ __global__ void __launch_bounds__(C8 ? 512 : 384, 1)
           }
           __syncwarp();
           if (kWithhold && (e >> 1) == 1) continue;  // test build: this copy never arrives
-          const uint32_t dst = sbase + C::OFF_R + s * C::TILE_BYTES + c * C::SUB_BYTES + r * box * 128;
+          const uint32_t dst = sbase + C::OFF_R + s * C::TILE_BYTES + c * C::KSUB_BYTES + r * box * 128;
           if (lane < boxes * C::NSUB &&
               FA_CHECK(smem_in(dst, box * 128, sbase + C::OFF_R, sbase + C::OFF_BAR), st, DBG_TMA_LOAD)) {
             if (cached)
@@ -615,7 +660,7 @@ __global__ void __launch_bounds__(C8 ? 512 : 384, 1)
     };
     auto make_item = [&](const SeqWork& w, int unit, int kvh, int p, int j0, int j1, ServeItem* it) {
       const int u = unit == npt ? p : 2 * p;  // first query tile
-      const int n0 = tiles_of(w, u, npt, tree), n1 = unit == npt ? 0 : tiles_of(w, u + 1, npt, tree);
+      const int n0 = tiles_of<C::TK_LOG2>(w, u, npt, tree), n1 = unit == npt ? 0 : tiles_of<C::TK_LOG2>(w, u + 1, npt, tree);
       const int nmax = max(n0, n1);
       const bool dual = n1 == 0;
       j1 = min(j1, nmax);
@@ -641,15 +686,15 @@ __global__ void __launch_bounds__(C8 ? 512 : 384, 1)
     ServeItem it;
     if (PAGED) {
       const int unit = 2 * npt;
-      const ServeRuns runs = serve_runs(a, unit, gridDim.x, blockIdx.x == 0);
+      const ServeRuns runs = serve_runs<C::TK_LOG2>(a, unit, gridDim.x, blockIdx.x == 0);
       int parts = 0;  // of the item that this CTA is the first to cut
       int4 cut = make_int4(0, 0, 0, 0);
       if ((int)blockIdx.x < runs.ctas && runs.total > 0) {
         long long pos = runs.start(blockIdx.x), first = 0;
         const long long end = runs.start(blockIdx.x + 1);
-        int b = serve_seek(a, unit, runs, pos, &first);
+        int b = serve_seek<C::TK_LOG2>(a, unit, runs, pos, &first);
         while (ok && pos < end) {
-          const SeqWork w = seq_work<PAGED>(a, b, unit, false);
+          const SeqWork w = seq_work<PAGED, C::TK_LOG2>(a, b, unit, false);
           // the first item may be cut; from then on they start with their first tile
           const long long at = pos - first;
           const int q = at < (1LL << 31) ? (int)at / max(w.nk, 1) : (int)(at / w.nk);
@@ -691,7 +736,7 @@ __global__ void __launch_bounds__(C8 ? 512 : 384, 1)
         int b = 0, p = 0;
         if (i >= (long long)items_of.total * a.Hkv) break;  // later rounds lie past the end too
         items_of.find((int)(i / a.Hkv), &b, &p);
-        const SeqWork w = seq_work<PAGED>(a, b, unit, false);
+        const SeqWork w = seq_work<PAGED, C::TK_LOG2>(a, b, unit, false);
         make_item(w, unit, (int)(i % a.Hkv), p, 0, w.nk, &it);
         ok = run_item(it, b);
       }
@@ -711,7 +756,7 @@ __global__ void __launch_bounds__(C8 ? 512 : 384, 1)
       }
       for (int x = max(0, uq - 2); x < uq; ++x) {
         const uint64_t t0 = globaltimer_ns();
-        while (!mbar_try_wait(BAR(C::Q_FULL + (x & 1)), (x >> 1) & 1) && globaltimer_ns() - t0 < 100000000ull) {
+        while (!mbar_try_wait(BAR((TURN ? C::Q_RAW : C::Q_FULL) + (x & 1)), (x >> 1) & 1) && globaltimer_ns() - t0 < 100000000ull) {
         }
       }
     }
@@ -719,70 +764,100 @@ __global__ void __launch_bounds__(C8 ? 512 : 384, 1)
     // ------------------------------------------------------------ converters, and the loads of new tokens
     if constexpr (C8) {
       const int cw = warp - 12;
-      int e = 0, x = 0, slot = 0;  // ring entries and tiles of 8 bits so far
-      uint32_t phase = 1;          // of the slot's EMPTY
+      // Warps 12 and 13 take K, 14 and 15 V, half of the keys each: the slots of K (even) and V are rings of their own.
+      constexpr int NS8 = C8 ? C::NS8 : 2;
+      const int kv = cw >> 1, half = cw & 1;
+      int x = 0, uq = 0, news = 0, slot = kv;  // tiles of 8 bits, Q slots and new tiles so far
+      uint32_t phase = 1, raw = 0;             // of the slot's EMPTY; of each slot's NEW_RAW
       bool ok = true;
       for (int i = 0; ok; ++i) {
         ServeItem it;
         if (!next_item(i, &it) || it.cnt < 0) break;
+        if (TURN) {
+          const int nq = (it.flags & ITEM_DUAL) ? 1 : 2;
+          for (int t = 0; ok && t < nq; ++t, ++uq) {
+            if (!(ok = wait_phase(BAR(C::Q_RAW + (uq & 1)), (uq >> 1) & 1, st, SITE_SW_Q_FULL))) break;
+            const int toks = min(npt, it.n - it.tok0 - t * npt);  // (rows behind them may be other sequences')
+            const float up = to_fp16_rows<C::NSUB, C::SUB_BYTES>(sm + C::OFF_Q + (uq & 1) * C::Q_BYTES, cw * 32, toks * a.G);
+            if (lane == 0) qfs[(uq & 1) * 4 + cw] = up;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(BAR(C::Q_FULL + (uq & 1)));
+          }
+        }
         for (int j = it.j0; ok && j < it.j0 + it.cnt; ++j) {
-          const bool cached = j < it.nc;
-          for (int kv = 0; kv < 2; ++kv, ++e) {
-            const uint32_t full = BAR(C::FULL + slot);
-            const int s8 = (2 * x + kv) % (C8 ? C::NS8 : 1);
-            if (cached && !(ok = wait_phase(BAR(C::FULL8 + s8), ((2 * x + kv) / (C8 ? C::NS8 : 1)) & 1, st, SITE_SW_FULL8))) break;
+          const uint32_t full = BAR(C::FULL + slot);
+          uint8_t* to = sm + C::OFF_R + slot * C::TILE_BYTES;
+          if (j < it.nc) {
+            const int s8 = (2 * x + kv) % NS8;
+            if (!(ok = wait_phase(BAR(C::FULL8 + s8), ((2 * x + kv) / NS8) & 1, st, SITE_SW_FULL8))) break;
             if (!(ok = wait_phase(BAR(C::EMPTY + slot), phase, st, SITE_SW_EMPTY))) break;
-            if (cw == 0 && lane == 0) *loading = e + 1;
-            uint8_t* to = sm + C::OFF_R + slot * C::TILE_BYTES;
-            if (cached) {
-              const uint8_t* from = sm + C::OFF_S8 + s8 * C::STAGE;
-              const int c0 = lane >> 3;
+            const uint8_t* from = sm + C::OFF_S8 + s8 * C::STAGE;
+            const int c0 = lane >> 3;
 #pragma unroll
-              for (int y = 0; y < 4 * (D / 64); ++y) {
-                const uint32_t key = cw * 32 + (y & 3) * 8 + (lane & 7), c = c0 + 4 * (y >> 2);
-                const uint32_t at = D == 128 ? key * 128 + ((c ^ (key & 7)) << 4) : key * 64 + ((c ^ ((key >> 1) & 3)) << 4);
-                uint4 lo, hi;
-                widen16<F16>(*reinterpret_cast<const uint4*>(from + at), &lo, &hi);
-                uint8_t* sub = to + (c >> 2) * C::SUB_BYTES;
-                *reinterpret_cast<uint4*>(sub + sw128_offset(key, 2 * (c & 3))) = lo;
-                *reinterpret_cast<uint4*>(sub + sw128_offset(key, 2 * (c & 3) + 1)) = hi;
-              }
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) {
-                mbar_arrive(full);
-                mbar_arrive(BAR(C::EMPTY8 + s8));
-              }
-            } else if (cw == 0) {
-              const int k0 = (j - it.nc) * 128, boxes = (min(128, it.n - k0) + kNewBox - 1) / kNewBox;
-              if (elect_one()) mbar_arrive_expect_tx(full, (uint32_t)(boxes * kNewBox * 128 * C::NSUB));
+            for (int y = 0; y < 4 * (D / 64); ++y) {
+              const uint32_t key = half * 32 + (y & 3) * 8 + (lane & 7), c = c0 + 4 * (y >> 2);
+              const uint32_t at = D == 128 ? key * 128 + ((c ^ (key & 7)) << 4) : key * 64 + ((c ^ ((key >> 1) & 3)) << 4);
+              uint4 lo, hi;
+              widen16(*reinterpret_cast<const uint4*>(from + at), &lo, &hi);
+              uint8_t* sub = to + (c >> 2) * C::KSUB_BYTES;
+              *reinterpret_cast<uint4*>(sub + sw128_offset(key, 2 * (c & 3))) = lo;
+              *reinterpret_cast<uint4*>(sub + sw128_offset(key, 2 * (c & 3) + 1)) = hi;
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive_n(full, 2);
+              mbar_arrive(BAR(C::EMPTY8 + s8));
+            }
+            ++x;
+          } else {
+            const int k0 = (j - it.nc) * 64, rows = min(64, it.n - k0), boxes = (rows + kNewBox - 1) / kNewBox;
+            if (!(ok = wait_phase(BAR(C::EMPTY + slot), phase, st, SITE_SW_EMPTY))) break;
+            const uint32_t landed = BAR(C::NEW_RAW + slot);
+            if (half == 0) {
+              if (elect_one()) mbar_arrive_expect_tx(landed, (uint32_t)(boxes * kNewBox * 128 * C::NSUB));
               __syncwarp();
               const int r = lane / C::NSUB, c = lane % C::NSUB;
-              const uint32_t dst = smem_u32(to) + c * C::SUB_BYTES + r * kNewBox * 128;
+              const uint32_t dst = smem_u32(to) + c * C::KSUB_BYTES + r * kNewBox * 128;
               if (lane < boxes * C::NSUB && FA_CHECK(smem_in(dst, kNewBox * 128, sbase + C::OFF_R, sbase + C::OFF_S8), st, DBG_TMA_LOAD))
-                tma_load_3d(dst, kv ? &tm_v : &tm_k, c * 64, it.row0 + k0 + r * kNewBox, it.kvh, full);
+                tma_load_3d(dst, kv ? &tm_v : &tm_k, c * 64, it.row0 + k0 + r * kNewBox, it.kvh, landed);
               __syncwarp();
-            } else if (lane == 0) {
-              mbar_arrive(full);
             }
-            if (++slot == C::NSLOT) slot = 0, phase ^= 1;
+            if (!(ok = wait_phase(landed, raw >> slot & 1, st, SITE_SW_FULL8))) break;
+            raw ^= 1u << slot;
+            if (TURN) {
+              const float up = to_fp16_rows<C::NSUB, C::KSUB_BYTES>(to, half * 32, rows);
+              if (lane == 0) nscales[news % C::SCALES * 4 + kv * 2 + half] = up;
+              fence_proxy_async_smem();
+              __syncwarp();
+            }
+            // S of the tile finds the factors of both: K's entry is full when V is there too (K's slot has been given up
+            // by the tile that had V's before, as this one has been waited for)
+            if (lane == 0) {
+              mbar_arrive_n(full, kv ? 2 : 1);
+              if (kv) mbar_arrive(BAR(C::FULL + slot - 1));
+            }
+            ++news;
           }
-          x += cached;
+          slot += 2;
+          if (slot >= C::NSLOT) slot = kv, phase ^= 1;
         }
       }
-      if (*(volatile int*)abort_flag && cw == 0) {  // as the producer does: copies of new tokens land first
-        for (int y = max(0, e - C::NSLOT); y < e; ++y) {
+      if (*(volatile int*)abort_flag && half == 0) {  // as the producer does: copies of new tokens land first
+        // (those whose waits gave up; where another wait did, none is in flight)
+        for (int y = kv; y < C::NSLOT; y += 2) {
           const uint64_t t0 = globaltimer_ns();
-          while (!mbar_try_wait(BAR(C::FULL + y % C::NSLOT), (y / C::NSLOT) & 1) && globaltimer_ns() - t0 < 100000000ull) {
+          while (!mbar_try_wait(BAR(C::NEW_RAW + y), raw >> y & 1) && globaltimer_ns() - t0 < 10000000ull) {
           }
         }
       }
     }
   } else if (warp >= 8) {
     // ------------------------------------------------------------ MMA issuers
-    constexpr uint32_t IDESC_S = F16 ? idesc_f16_f32(128, C::KT, 0, 0) : idesc_bf16_f32(128, C::KT, 0, 0);
-    constexpr uint32_t IDESC_O = F16 ? idesc_f16_f32(128, D, 0, 1) : idesc_bf16_f32(128, D, 0, 1);
-    constexpr uint32_t HI = sdesc_hi(1024), TILE16 = C::TILE_BYTES >> 4, HALF16 = (C::KT * 128) >> 4;
+    constexpr uint32_t IDESC_S = H ? idesc_f16_f32(128, C::KT, 0, 0) : idesc_bf16_f32(128, C::KT, 0, 0);
+    constexpr uint32_t IDESC_O = H ? idesc_f16_f32(128, D, 0, 1) : idesc_bf16_f32(128, D, 0, 1);
+    constexpr uint32_t HI = sdesc_hi(1024), TILE16 = C::TILE_BYTES >> 4, Q16 = C::Q_BYTES >> 4, HALF16 = (C::KT * 128) >> 4;
     auto commit = [&](uint32_t bar) {
       if (elect_one()) mma_commit(bar);
       __syncwarp();
@@ -803,8 +878,9 @@ __global__ void __launch_bounds__(C8 ? 512 : 384, 1)
       }
     };
     int begun = 0;  // of `loading`, when last looked at
+    // (C8: K and V have slots of their own, and every warp waits for all uses in order.)
     auto landed = [&](const Place& p, bool steady, int site) {
-      if (!steady && begun <= p.entry) {
+      if (!C8 && !steady && begun <= p.entry) {
         const uint64_t t0 = globaltimer_ns();
         for (uint32_t spins = 1;; ++spins) {
           begun = *loading;
@@ -837,13 +913,13 @@ __global__ void __launch_bounds__(C8 ? 512 : 384, 1)
         const int nq = dual ? 1 : 2;
         for (int u = uq; ok && u < uq + nq; ++u)
           ok = wait_phase(BAR(C::Q_FULL + (u & 1)), (u >> 1) & 1, st, SITE_SW_Q_FULL);
-        const uint32_t qa0 = q_lo + (uq & 1) * TILE16, qa1 = q_lo + ((uq + nq - 1) & 1) * TILE16;
+        const uint32_t qa0 = q_lo + (uq & 1) * Q16, qa1 = q_lo + ((uq + nq - 1) & 1) * Q16;
         auto form_s = [&](int t, int g, uint32_t qa, uint32_t ka) {
           const uint32_t d = tmem + C::tm_s(t, C::buf(g));
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
-            const uint32_t off = ((k >> 2) * C::SUB_BYTES + (k & 3) * 32) >> 4;
-            if (elect_one()) mma_ss(d, sdesc_join(qa + off, HI), sdesc_join(ka + off, HI), IDESC_S, k > 0);
+            const uint32_t off = ((k >> 2) * C::SUB_BYTES + (k & 3) * 32) >> 4, koff = ((k >> 2) * C::KSUB_BYTES + (k & 3) * 32) >> 4;
+            if (elect_one()) mma_ss(d, sdesc_join(qa + off, HI), sdesc_join(ka + koff, HI), IDESC_S, k > 0);
           }
           commit(BAR(C::S_FULL + 2 * t + C::buf(g)));
         };
@@ -901,7 +977,7 @@ __global__ void __launch_bounds__(C8 ? 512 : 384, 1)
     } else {
       // O += P V of lane t
       const int t = warp == C::PV1;
-      const uint32_t v_lo = sdesc_lo(sbase + C::OFF_R, C::SUB_BYTES);
+      const uint32_t v_lo = sdesc_lo(sbase + C::OFF_R, C::KSUB_BYTES);
       Place vs = {1, 1, 0};
       int used = 0, g = 0;  // this lane's items and steps so far
       for (int i = 0; ok; ++i) {
@@ -919,14 +995,14 @@ __global__ void __launch_bounds__(C8 ? 512 : 384, 1)
             continue;
           }
           const int j = it.j0 + k;
-          const int rows = j < it.nc ? it.L - j * 128 : it.n - (j - it.nc) * 128;
+          const int rows = j < it.nc ? it.L - j * C::TK : it.n - (j - it.nc) * C::TK;
           const int halves = steps_in(it, t, j);
           if (rows < halves * C::KT) {
             // rows past the sequence may hold anything; P is 0 there, but 0 x NaN is not
             uint8_t* v = sm + C::OFF_R + vs.slot * C::TILE_BYTES + rows * 128;
             const int chunks = (halves * C::KT - rows) * 8;
             for (int z = lane; z < chunks * C::NSUB; z += 32)
-              *reinterpret_cast<uint4*>(v + z / chunks * C::SUB_BYTES + z % chunks * 16) = make_uint4(0, 0, 0, 0);
+              *reinterpret_cast<uint4*>(v + z / chunks * C::KSUB_BYTES + z % chunks * 16) = make_uint4(0, 0, 0, 0);
             fence_proxy_async_smem();
             __syncwarp();
           }
@@ -962,7 +1038,7 @@ __global__ void __launch_bounds__(C8 ? 512 : 384, 1)
     const float sl2 = a.scale_log2;
     float* ml = reinterpret_cast<float*>(sm + C::OFF_ML);
     int st0 = 0, st1 = 0, merges = 0;  // steps of both lanes and joins of dual items so far
-    int tiles8 = 0;                    // (C8) cached tiles so far
+    int tiles8 = 0, news = 0, uq = 0;  // (C8) cached and new tiles, Q slots so far
     for (int i = 0;; ++i) {
       ServeItem it;
       if (!next_item(i, &it) || it.cnt < 0) break;
@@ -971,8 +1047,22 @@ __global__ void __launch_bounds__(C8 ? 512 : 384, 1)
       const int tok = it.tok0 + (dual ? 0 : t * npt) + rn;
       const bool valid = rn < npt && tok < it.n;
       const bool any = __any_sync(0xffffffffu, valid);
-      float m_run = -INFINITY, l_run = 0.f, vref = 1.f;
+      float m_run = -INFINITY, l_run = 0.f, vref = 0.f;  // vref: (C8) to base 2
       bool ok = true;
+      // (C8) of scores: what undoes the factor of the row's Q; there with the first S, and kept until this arrival
+      float qf = 1.f;
+      const int qslot = (uq + (dual ? 0 : t)) & 1;
+      auto q_read = [&] {
+        __syncwarp();
+        if (lane == 0) mbar_arrive_n(BAR(C::Q_EMPTY + qslot), dual ? 1 : 2);
+      };
+      // Every use of the slots is waited for, in order: the arrival that releases one may not count for the one before.
+      if (TURN) {
+        for (int y = uq; ok && y < uq + (dual ? 1 : 2); ++y)
+          ok = wait_phase(BAR(C::Q_FULL + (y & 1)), (y >> 1) & 1, st, SITE_SW_Q_FULL);
+        if (!ok) break;
+        if (steps == 0) q_read();
+      }
       const int tok_first = __shfl_sync(0xffffffffu, tok, 0);  // the warp's tokens ascend with its rows
       auto wait_pv = [&](int lane_t, int g) {  // PV of that lane's step g has landed in O
         return wait_phase(BAR(C::O_DONE + 2 * lane_t + C::buf(g)), C::phase(g), st, SITE_SW_O_DONE);
@@ -1022,6 +1112,10 @@ __global__ void __launch_bounds__(C8 ? 512 : 384, 1)
         for (int s = 0; s < steps; ++s, hs += C::HPT > 1) {
           const int u = C::buf(before + s);
           if (!(ok = begin_step(s))) break;
+          if (TURN && s == 0) {
+            qf = qfs[qslot * 4 + wq];
+            q_read();
+          }
           if (!any) {  // no row here: P stays what it is, its rows of O are nobody's
             __syncwarp();
             if (C::SEP_P) {
@@ -1036,7 +1130,7 @@ __global__ void __launch_bounds__(C8 ? 512 : 384, 1)
           tc_fence_after();
           float f = 1.f, fv = 1.f;  // of O and l, and of O alone
           bool rescale = false;
-          float sv[KT], w[C8 ? KT / 16 : 1];
+          float sv[KT], ks[C8 ? KT / 16 : 1], w[C8 ? KT / 16 : 1];
           {
             uint32_t r[KT / 32][32];
 #pragma unroll
@@ -1049,33 +1143,37 @@ __global__ void __launch_bounds__(C8 ? 512 : 384, 1)
           }
           s_in_registers();
           if constexpr (C8) {
-            float vtop = 1.f;
+            constexpr int GR = KT / 16;  // (4)
+            float vs[GR];
             if (js < it.nc) {
-              const float* sc = scales + (tiles8 + js - it.j0) % (C8 ? C::SCALES : 1) * 16;
-              const float4 v0 = *reinterpret_cast<const float4*>(sc + 8), v1 = *reinterpret_cast<const float4*>(sc + 12);
-              vtop = fmaxf(fmaxf(fmaxf(v0.x, v0.y), fmaxf(v0.z, v0.w)), fmaxf(fmaxf(v1.x, v1.y), fmaxf(v1.z, v1.w)));
-#pragma unroll
-              for (int x = 0; x < KT / 16; ++x) {
-                const float k16 = sc[hs * (KT / 16) + x];
-                w[x] = sc[8 + hs * (KT / 16) + x];
-#pragma unroll
-                for (int y = 0; y < 16; ++y) sv[16 * x + y] *= k16;
-              }
+              const float4* sc = reinterpret_cast<const float4*>(scales + (tiles8 + js - it.j0) % C::SCALES * 8);
+              const float4 k4 = sc[0], v4 = sc[1];
+              ks[0] = k4.x, ks[1] = k4.y, ks[2] = k4.z, ks[3] = k4.w;
+              vs[0] = v4.x, vs[1] = v4.y, vs[2] = v4.z, vs[3] = v4.w;
+            } else if (TURN) {
+              const float4 f4 = reinterpret_cast<const float4*>(nscales)[(news + js - max(it.nc, it.j0)) % C::SCALES];
+              ks[0] = ks[1] = f4.x, ks[2] = ks[3] = f4.y, vs[0] = vs[1] = f4.z, vs[2] = vs[3] = f4.w;
             } else {
 #pragma unroll
-              for (int x = 0; x < KT / 16; ++x) w[x] = 1.f;
+              for (int x = 0; x < GR; ++x) ks[x] = vs[x] = 1.f;
             }
-            if (F16) {  // the reference of the values' scales: 1 for new tokens, who come last
-              const float to = js >= it.nc ? 1.f : s == 0 ? 2.f * fmaxf(vtop, 1.1754944e-38f) : vtop > vref ? 2.f * vtop : vref;
-              if (s > 0 && to != vref) rescale = true, fv = vref / to;
-              vref = to;
-              const float inv = 1.f / vref;
+            // the reference of the values' scales, to base 2
+            const float vtop = lg2_approx(fmax3(fmaxf(vs[0], vs[1]), fmaxf(vs[2], vs[3]), 1.1754944e-38f));
+            if (s == 0) {
+              vref = vtop + 1.f;
+            } else if (vtop > vref) {
+              rescale = true, fv = ex2_approx(vref - (vtop + 1.f));
+              vref = vtop + 1.f;
+            }
 #pragma unroll
-              for (int x = 0; x < KT / 16; ++x) w[x] *= inv;
+            for (int x = 0; x < GR; ++x) {
+              ks[x] = fmaxf(ks[x], 1.1754944e-38f) * (sl2 * qf);  // (not 0: -inf times it stays -inf)
+              // not below 2^-40: what is that small adds nothing to O, but to the sum
+              w[x] = fmaxf(lg2_approx(vs[x]) - vref, -40.f);
             }
           }
           if (tree && js >= it.nc) {
-            const int k0 = (js - it.nc) * 128 + hs * KT;
+            const int k0 = (js - it.nc) * C::TK + hs * KT;
             const uint32_t* words = a.mask + (long long)(it.row0 + tok) * a.words;
             uint32_t w[KT / 32];
 #pragma unroll
@@ -1089,7 +1187,7 @@ __global__ void __launch_bounds__(C8 ? 512 : 384, 1)
               if (!(w[x >> 5] >> (x & 31) & 1)) sv[x] = -INFINITY;
           } else {
             // keys [0, lim) of the step are seen, by the warp's first row fewest
-            const int k0 = js * 128 + hs * KT - (js < it.nc ? it.L : it.nc * 128);
+            const int k0 = js * C::TK + hs * KT - (js < it.nc ? it.L : it.nc * C::TK);
             if (js < it.nc ? k0 > -KT : min(it.n, tok_first + 1) < k0 + KT) {
               const int lim = js < it.nc ? -k0 : min(it.n, tok + 1) - k0;
 #pragma unroll
@@ -1097,7 +1195,21 @@ __global__ void __launch_bounds__(C8 ? 512 : 384, 1)
                 if (x >= lim) sv[x] = -INFINITY;
             }
           }
-          float pm[4];
+          float m_tile;
+          if constexpr (C8) {
+            m_tile = -INFINITY;
+#pragma unroll
+            for (int x = 0; x < KT / 16; ++x) {
+              float pm[2] = {fmax3(sv[16 * x], sv[16 * x + 1], sv[16 * x + 2]), fmax3(sv[16 * x + 3], sv[16 * x + 4], sv[16 * x + 5])};
+#pragma unroll
+              for (int y = 6; y < 14; y += 4) {
+                pm[0] = fmax3(pm[0], sv[16 * x + y], sv[16 * x + y + 1]);
+                pm[1] = fmax3(pm[1], sv[16 * x + y + 2], sv[16 * x + y + 3]);
+              }
+              m_tile = fmaxf(m_tile, ks[x] * fmax3(fmaxf(pm[0], pm[1]), sv[16 * x + 14], sv[16 * x + 15]));
+            }
+          } else {
+            float pm[4];
 #pragma unroll
           for (int y = 0; y < 4; ++y) pm[y] = sv[y];
 #pragma unroll
@@ -1106,7 +1218,8 @@ __global__ void __launch_bounds__(C8 ? 512 : 384, 1)
             for (int y = 0; y < 4; ++y) pm[y] = fmax3(pm[y], sv[x + 2 * y], sv[x + 2 * y + 1]);
           const float mx = fmax3(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3]),
                                  fmax3(sv[KT - 4], sv[KT - 3], fmaxf(sv[KT - 2], sv[KT - 1])));
-          const float m_tile = mx * sl2;
+          m_tile = mx * sl2;
+          }
           // the reference maximum moves only when it grows by more than 2^LAG_LOG2; O and l share it
           if (s == 0) {
             m_run = m_tile;
@@ -1120,6 +1233,8 @@ __global__ void __launch_bounds__(C8 ? 512 : 384, 1)
           }
           const float nbase = P_LOG2 - (m_run == -INFINITY ? 0.f : m_run);
           const uint64_t sl2x2 = f2_pack(sl2, sl2), nbase2 = f2_pack(nbase, nbase);
+          [[maybe_unused]] uint64_t ks2, nb2, sum16;
+          [[maybe_unused]] float l_step = 0.f;
           uint64_t ps2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
           uint32_t pk[KT / 32][16];
           const uint32_t tP = tmem + lane_off + C::tm_p(t, u);
@@ -1128,13 +1243,28 @@ __global__ void __launch_bounds__(C8 ? 512 : 384, 1)
 #pragma unroll
             for (int x = 0; x < 16; ++x) {
               float x0, x1;
-              f2_unpack(f2_fma(f2_pack(sv[q * 32 + 2 * x], sv[q * 32 + 2 * x + 1]), sl2x2, nbase2), x0, x1);
+              if constexpr (C8) {  // w P, whose sums over 16 keys are divided by w again
+                if ((x & 7) == 0) {
+                  const float nb = nbase + w[2 * q + (x >> 3)];
+                  ks2 = f2_pack(ks[2 * q + (x >> 3)], ks[2 * q + (x >> 3)]);
+                  nb2 = f2_pack(nb, nb);
+                }
+                f2_unpack(f2_fma(f2_pack(sv[q * 32 + 2 * x], sv[q * 32 + 2 * x + 1]), ks2, nb2), x0, x1);
+              } else {
+                f2_unpack(f2_fma(f2_pack(sv[q * 32 + 2 * x], sv[q * 32 + 2 * x + 1]), sl2x2, nbase2), x0, x1);
+              }
               const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-              ps2[x & 1] = f2_add(ps2[x & 1], f2_pack(p0, p1));
-              if constexpr (C8)
-                pk[q][x] = pack2<F16>(p0 * w[2 * q + (x >> 3)], p1 * w[2 * q + (x >> 3)]);
-              else
-                pk[q][x] = pack2<F16>(p0, p1);
+              if constexpr (C8) {
+                sum16 = (x & 7) == 0 ? f2_pack(p0, p1) : f2_add(sum16, f2_pack(p0, p1));
+                if ((x & 7) == 7) {
+                  float lo, hi;
+                  f2_unpack(sum16, lo, hi);
+                  l_step = fmaf(lo + hi, ex2_approx(-w[2 * q + (x >> 3)]), l_step);
+                }
+              } else {
+                ps2[x & 1] = f2_add(ps2[x & 1], f2_pack(p0, p1));
+              }
+              pk[q][x] = pack2<H>(p0, p1);
             }
             if (C::SEP_P && q == 1) {
               if (s > 0) {  // PV of the tile before has read P (across items its epilogue waited for that)
@@ -1150,8 +1280,8 @@ __global__ void __launch_bounds__(C8 ? 512 : 384, 1)
           float ps[4];
           f2_unpack(ps2[0], ps[0], ps[1]);
           f2_unpack(ps2[1], ps[2], ps[3]);
-          l_run = l_run * f + ((ps[0] + ps[1]) + (ps[2] + ps[3]));
-          if (!(ok = end_step(s, rescale, C8 && F16 ? f * fv : f))) break;
+          l_run = l_run * f + (C8 ? l_step : (ps[0] + ps[1]) + (ps[2] + ps[3]));
+          if (!(ok = end_step(s, rescale, C8 ? f * fv : f))) break;
         }
       } else {
         // Decoding and small drafts: up to 16 rows, in the first warp's lanes. A thread of it takes a quarter
@@ -1268,7 +1398,7 @@ __global__ void __launch_bounds__(C8 ? 512 : 384, 1)
       if (join) {
         ml[256 * t + row] = m_run;
         ml[256 * t + 128 + row] = l_run;
-        if (C8 && F16 && row == 0) vrefs[t] = vref;
+        if (C8 && row == 0) vrefs[t] = vref;
         __syncwarp();
         if (lane == 0) mbar_arrive(BAR(C::MERGE));
         if (!wait_phase(BAR(C::MERGE), merges & 1, st, SITE_SW_MERGE) ||
@@ -1285,7 +1415,10 @@ __global__ void __launch_bounds__(C8 ? 512 : 384, 1)
       }
       st0 += it.s0;
       st1 += it.s1;
-      if (C8) tiles8 += max(0, min(it.nc - it.j0, it.cnt));
+      if (C8) {
+        const int here = max(0, min(it.nc - it.j0, it.cnt));
+        tiles8 += here, news += it.cnt - here, uq += dual ? 1 : 2;
+      }
       if (dual && t == 1 && !join) continue;  // lane 0 has all of them
       // l = 0: no key; NaN stays NaN
       const float inv = l_run != 0.f ? 1.f / l_run : 0.f;
@@ -1299,9 +1432,9 @@ __global__ void __launch_bounds__(C8 ? 512 : 384, 1)
       const long long token = it.row0 + tok;
       f0 *= inv;
       f1 *= inv;
-      if (C8 && F16) {
-        f0 *= vref;
-        if (join) f1 *= vrefs[t ^ 1];
+      if (C8) {
+        f0 *= exp2f(vref);
+        if (join) f1 *= exp2f(vrefs[t ^ 1]);
       }
       const bool write = valid && FA_CHECK(whole ? in_range(token, a.T) : in_range(part, a.part_rows), st, DBG_GLOBAL_STORE);
       uint16_t* orow = a.o + token * a.o_st + head * a.o_sh;
@@ -1438,7 +1571,7 @@ static int launch_serve_d(std::conditional_t<C8, Serve8BitArgs, ServeArgs> a, cu
     const cuuint64_t dims[4] = {D, (cuuint64_t)page, (cuuint64_t)a.Hkv, (cuuint64_t)a.n_pages};
     const cuuint64_t elem = C8 ? 1 : 2;
     const cuuint64_t strides[3] = {(cuuint64_t)a.c_st * elem, (cuuint64_t)a.c_sh * elem, (cuuint64_t)a.c_sp * elem};
-    const cuuint32_t box[4] = {C8 ? D : 64, (cuuint32_t)std::min(page, 128), 1, 1};
+    const cuuint32_t box[4] = {C8 ? D : 64, (cuuint32_t)std::min(page, C::TK), 1, 1};
     return make_tmap_strided(m, p, C8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : type, 4, dims, strides, box,
                              C8 && D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
   };

@@ -80,7 +80,7 @@ struct Serve8Cfg {
   static constexpr int THREADS = 448, PRODUCER = 8, S_BOTH = 9, PV0 = 10, PV1 = 11, SPLIT = 12;
   // barriers
   static constexpr int FULL = 0, EMPTY = NT, Q_FULL = 2 * NT, Q_EMPTY = Q_FULL + NQ, S_FULL = Q_EMPTY + NQ, S_FREE = S_FULL + 4,
-                       P_READY = S_FREE + 4, O_DONE = P_READY + 2, O_FREE = O_DONE + 4, MERGE = O_FREE + 2, DRAIN = MERGE + 1,
+                       P_READY = S_FREE + 4, O_DONE = P_READY + 4, O_FREE = O_DONE + 4, MERGE = O_FREE + 2, DRAIN = MERGE + 1,
                        GROUP = DRAIN + 1, D_FULL = GROUP + 2, D_EMPTY = D_FULL + 4, BARS = D_EMPTY + 4;
   static_assert(8 * BARS + 12 <= 512, "barrier area");
   static_assert(NT >= 2 && SMEM_BYTES <= 232448, "shared memory");
@@ -340,9 +340,9 @@ __global__ void __launch_bounds__(448, 1)
       for (int u = 0; u < 2; ++u) {
         mbar_init(BAR(C::S_FULL + 2 * t + u), 1);
         mbar_init(BAR(C::S_FREE + 2 * t + u), 4);
+        mbar_init(BAR(C::P_READY + 2 * t + u), 4);
         mbar_init(BAR(C::O_DONE + 2 * t + u), 1);
       }
-      mbar_init(BAR(C::P_READY + t), 4);
       mbar_init(BAR(C::O_FREE + t), 8);  // four warps twice, or all eight in a join
       mbar_init(BAR(C::GROUP + t), 4);
     }
@@ -680,7 +680,7 @@ __global__ void __launch_bounds__(448, 1)
             fence_proxy_async_smem();
             __syncwarp();
           }
-          if (!(ok = wait_phase(BAR(C::P_READY + t), g & 1, st, SITE_T8_P_READY))) break;
+          if (!(ok = wait_phase(BAR(C::P_READY + 2 * t + (g & 1)), (g >> 1) & 1, st, SITE_T8_P_READY))) break;
           if (first && items > 0 && !(ok = wait_phase(BAR(C::O_FREE + t), (items - 1) & 1, st, SITE_T8_O_FREE))) break;
           tc_fence_after();
           const uint32_t va = v_lo + s * (C::ENTRY >> 4), pa = p_lo + (C::NP == 2 ? (g & 1) * (C::PBYTES >> 4) : 0);
@@ -925,7 +925,7 @@ __global__ void __launch_bounds__(448, 1)
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(BAR(C::P_READY + t));
+        if (lane == 0) mbar_arrive(BAR(C::P_READY + 2 * t + (g & 1)));  // (two: P may be two tiles ahead of its product)
       }
       const bool join = dual && it.c1 > 0, whole = it.flags & ITEM8_WHOLE;
       const long long part0 = (long long)it.slot * (2 * R) + (dual ? 0 : t * R);

@@ -173,3 +173,16 @@ def test_refusals(gpu):
             m.call()
         setattr(m, name, was)
     m.check()
+
+
+@pytest.mark.parametrize("Hq,H,d,dtype", [(12, 12, 64, FP16), (32, 8, 128, BF16), (16, 2, 128, FP16), (20, 4, 64, BF16)])
+def test_many_calls_in_a_row(gpu, Hq, H, d, dtype):
+    """Long contexts, many items, calls that follow each other without a wait, from a cold start: every product may lag
+    behind by as much as the buffers allow. No wait runs out, and all calls give the same bits."""
+    lens = [5000 - 37 * i for i in range(64)]
+    m = Made(gpu, lens, [1] * 64, Hq, H, d, 32, 16, dtype, seed=2)
+    outs = [m.call() for _ in range(30)]
+    assert api.device_status(gpu)[0] == 0
+    for o, lse in outs[1:]:
+        assert torch.equal(o[: m.T], outs[0][0][: m.T]) and torch.equal(lse[:, : m.T], outs[0][1][:, : m.T])
+    m.check(outs[-1])
