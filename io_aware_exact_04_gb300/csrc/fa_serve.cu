@@ -364,22 +364,23 @@ __device__ __forceinline__ void widen16(const uint4& x, uint4* lo, uint4* hi) {
   *lo = make_uint4(r[0], r[1], r[2], r[3]);
   *hi = make_uint4(r[4], r[5], r[6], r[7]);
 }
-// Rows [row0, min(row0 + 32, rows)) of bf16 in swizzled tiles of 64 columns to fp16 in place, by a warp: times a power of
-// two that takes the largest finite element to [2^14, 2^15). Returns what undoes the factor. (Rows behind them
-// are nobody's, or masked, or, of V, zeroed before the product.)
+// Rows of bf16 in swizzled tiles of 64 columns to fp16 in place, by a warp: eight from `first` on, and eight more every
+// `stride`, below `end`; times a power of two that takes their largest finite element to [2^14, 2^15). Returns what
+// undoes the factor. (Rows behind them are nobody's, or masked, or, of V, zeroed before the product.)
 // Loops of few instructions: the code runs once an item, and fetching it anew is what it takes (unrolled, 32 rows of
 // 128 columns took 10000 cycles between the loops of the products, against 2600 at the start).
 template <int NSUB, int SUB_BYTES>
-__device__ __forceinline__ float to_fp16_rows(uint8_t* tile, int row0, int rows) {
-  const int lane = threadIdx.x & 31, steps = max(0, (min(32, rows - row0) + 3) >> 2) * NSUB;  // of 4 rows, 8 chunks each
-  auto place = [&](int y) {
-    return reinterpret_cast<uint4*>(tile + y % NSUB * SUB_BYTES + sw128_offset(row0 + y / NSUB * 4 + (lane >> 3), lane & 7));
-  };
+__device__ __forceinline__ float to_fp16_rows(uint8_t* tile, int first, int stride, int end) {
+  const int lane = threadIdx.x & 31;
+  // a step: 4 rows, 8 chunks each; two steps and NSUB columns of them, then the next eight rows
+  const int steps = (max(0, end - first) + stride - 1) / stride * 2 * NSUB;
+  auto row_of = [&](int y) { return first + stride * (y / (2 * NSUB)) + y / NSUB % 2 * 4 + (lane >> 3); };
+  auto place = [&](int y) { return reinterpret_cast<uint4*>(tile + y % NSUB * SUB_BYTES + sw128_offset(row_of(y), lane & 7)); };
   uint32_t most2 = 0;  // two magnitudes, as whole numbers
 #pragma unroll 1
   for (int y = 0; y < steps; ++y) {
     const uint4 x = *place(y);
-    if (row0 + y / NSUB * 4 + (lane >> 3) >= rows) continue;
+    if (row_of(y) >= end) continue;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t w = (i == 0 ? x.x : i == 1 ? x.y : i == 2 ? x.z : x.w) & 0x7fff7fffu;
@@ -778,7 +779,7 @@ __global__ void __launch_bounds__(C8 ? 512 : 384, 1)
           for (int t = 0; ok && t < nq; ++t, ++uq) {
             if (!(ok = wait_phase(BAR(C::Q_RAW + (uq & 1)), (uq >> 1) & 1, st, SITE_SW_Q_FULL))) break;
             const int toks = min(npt, it.n - it.tok0 - t * npt);  // (rows behind them may be other sequences')
-            const float up = to_fp16_rows<C::NSUB, C::SUB_BYTES>(sm + C::OFF_Q + (uq & 1) * C::Q_BYTES, cw * 32, toks * a.G);
+            const float up = to_fp16_rows<C::NSUB, C::SUB_BYTES>(sm + C::OFF_Q + (uq & 1) * C::Q_BYTES, 8 * cw, 32, toks * a.G);
             if (lane == 0) qfs[(uq & 1) * 4 + cw] = up;
             fence_proxy_async_smem();
             __syncwarp();
@@ -827,7 +828,7 @@ __global__ void __launch_bounds__(C8 ? 512 : 384, 1)
             if (!(ok = wait_phase(landed, raw >> slot & 1, st, SITE_SW_FULL8))) break;
             raw ^= 1u << slot;
             if (TURN) {
-              const float up = to_fp16_rows<C::NSUB, C::KSUB_BYTES>(to, half * 32, rows);
+              const float up = to_fp16_rows<C::NSUB, C::KSUB_BYTES>(to, half * 32, 8, min(rows, half * 32 + 32));
               if (lane == 0) nscales[news % C::SCALES * 4 + kv * 2 + half] = up;
               fence_proxy_async_smem();
               __syncwarp();
@@ -1113,7 +1114,7 @@ __global__ void __launch_bounds__(C8 ? 512 : 384, 1)
           const int u = C::buf(before + s);
           if (!(ok = begin_step(s))) break;
           if (TURN && s == 0) {
-            qf = qfs[qslot * 4 + wq];
+            qf = qfs[qslot * 4 + (row >> 3 & 3)];
             q_read();
           }
           if (!any) {  // no row here: P stays what it is, its rows of O are nobody's

@@ -3,6 +3,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "fa_internal.h"
 #include "serve.cuh"
@@ -42,8 +43,9 @@ namespace fa {
 // and join their results at the end. All tiles of all items form one sequence, of which every CTA
 // takes an equal run; items cut between CTAs leave fp32 partial results for serve8_join_kernel.
 //
-// Roles, 448 threads: warps 0-3 and 4-7 the softmax of lanes 0 and 1, a thread a key, warp 8 the TMA
-// producer and scheduler, 9 the issuer of S, 10 and 11 those of O, 12 and 13 split Q.
+// Roles, 512 threads: warps 0-3 and 4-7 the softmax of lanes 0 and 1, a thread a key, warp 8 the scheduler,
+// which loads the pages of K, 14 loads those of V and 15 the scales (one warp for all three took 1100 cycles
+// a tile, more than memory does at d = 64), 9 issues S, 10 and 11 O, 12 and 13 split Q.
 //
 // The softmax needs a maximum over the keys, across its threads, only where a reference moves: for the
 // first tile of an item, and where some score passes the reference by more than it may. A vote of the four
@@ -65,19 +67,20 @@ struct Serve8Cfg {
   static constexpr int NP = R == 16 ? 2 : 1;         // buffers of P
   static constexpr int PBYTES = 128 * PX;
   static constexpr int QROW = 16;                    // of a row of Q: factor of its scores, token, place in O (8 bytes)
-  static constexpr int MISC = 512 + 256 + 12 * 64 + NQ * R * QROW + 2 * (R + R + R + 4 * R + 4 * (R + 4)) * 4 + 64;
+  static constexpr int MISC = 512 + 256 + 12 * 64 + NQ * R * QROW + 2 * (2 * R + R + R + 4 * R + 4 * (R + 4)) * 4 + 64;
   static constexpr int FIXED = 2 * NP * PBYTES + NQ * QSLOT + MISC;
   static constexpr int NT = (232448 - FIXED) / ENTRY < 12 ? (232448 - FIXED) / ENTRY : 12;
   static constexpr int OFF_P = NT * ENTRY, OFF_Q = OFF_P + 2 * NP * PBYTES, OFF_BAR = OFF_Q + NQ * QSLOT;
   static constexpr int OFF_DESC = OFF_BAR + 512, OFF_SC = OFF_DESC + 256, OFF_QROW = OFF_SC + 12 * 64;
-  // of each lane: 11 - reference of each row, factors of a move; of the item before: reference, sums of each warp
-  static constexpr int OFF_NB = OFF_QROW + NQ * R * QROW, OFF_FAC = OFF_NB + 2 * R * 4, OFF_REF = OFF_FAC + 2 * R * 4;
+  // of each lane: factor of each row's scores and 11 - its reference, factors of a move; of the item before: reference,
+  // sums of each warp
+  static constexpr int OFF_ROWC = OFF_QROW + NQ * R * QROW, OFF_FAC = OFF_ROWC + 2 * R * 8, OFF_REF = OFF_FAC + 2 * R * 4;
   static constexpr int OFF_SUM = OFF_REF + 2 * R * 4, OFF_RED = OFF_SUM + 2 * 4 * R * 4;
   static constexpr int OFF_FLAG = OFF_RED + 2 * 4 * (R + 4) * 4, SMEM_BYTES = OFF_FLAG + 64;
   __device__ static constexpr uint32_t tm_s(int t, int u) { return 4u * R * t + 2u * R * u; }
   __device__ static constexpr uint32_t tm_o(int t) { return 8u * R + 4u * R * t; }
   static constexpr uint32_t TM_COLS = 16 * R;
-  static constexpr int THREADS = 448, PRODUCER = 8, S_BOTH = 9, PV0 = 10, PV1 = 11, SPLIT = 12;
+  static constexpr int THREADS = 512, PRODUCER = 8, S_BOTH = 9, PV0 = 10, PV1 = 11, SPLIT = 12, LOAD_V = 14, SCALES = 15;
   // barriers
   static constexpr int FULL = 0, EMPTY = NT, Q_FULL = 2 * NT, Q_EMPTY = Q_FULL + NQ, S_FULL = Q_EMPTY + NQ, S_FREE = S_FULL + 4,
                        P_READY = S_FREE + 4, O_DONE = P_READY + 4, O_FREE = O_DONE + 4, MERGE = O_FREE + 2, DRAIN = MERGE + 1,
@@ -107,6 +110,7 @@ struct Item8 {
   int r0;      // the item's first row
   int kvh;
   int slot;    // partial result slot
+  int b;       // the sequence
 };
 enum { ITEM8_DUAL = 1, ITEM8_WHOLE = 2 };
 
@@ -296,7 +300,7 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
 }
 
 template <int D, int R, bool F16>
-__global__ void __launch_bounds__(448, 1)
+__global__ void __launch_bounds__(512, 1)
     serve8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                   const __grid_constant__ CUtensorMap tm_kc, const __grid_constant__ CUtensorMap tm_vc, Serve8BitArgs a) {
   using C = Serve8Cfg<D, R, F16>;
@@ -329,7 +333,7 @@ __global__ void __launch_bounds__(448, 1)
 
   if (warp == C::PRODUCER && lane == 0) {
     for (int i = 0; i < NT; ++i) {
-      mbar_init(BAR(C::FULL + i), 17);  // the copies, and each of 16 lanes' scale
+      mbar_init(BAR(C::FULL + i), 10);  // K's and V's copies, and each of 8 lanes' scales
       mbar_init(BAR(C::EMPTY + i), 2);  // both lanes, or one twice
     }
     for (int i = 0; i < NQ; ++i) {
@@ -350,7 +354,7 @@ __global__ void __launch_bounds__(448, 1)
     mbar_init(BAR(C::DRAIN), 3);
     for (int i = 0; i < 4; ++i) {
       mbar_init(BAR(C::D_FULL + i), 1);
-      mbar_init(BAR(C::D_EMPTY + i), 13);  // softmax warps, issuers, splitters
+      mbar_init(BAR(C::D_EMPTY + i), 15);  // softmax warps, issuers, splitters, loaders
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -375,6 +379,7 @@ __global__ void __launch_bounds__(448, 1)
     if (!wait_phase(BAR(C::D_FULL + (i & 3)), (i >> 2) & 1, st, SITE_T8_DESC_FULL)) return false;
     const int4* d = reinterpret_cast<const int4*>(descs + 16 * (i & 3));
     const int4 x = d[0], y = d[1], z = d[2];
+    it->b = reinterpret_cast<const int*>(d)[12];
     it->cnt = x.x, it->flags = x.y, it->c0 = x.z, it->c1 = x.w;
     it->j0 = y.x, it->nc = y.y, it->L = y.z, it->n = y.w;
     it->row0 = z.x, it->r0 = z.y, it->kvh = z.z, it->slot = z.w;
@@ -386,8 +391,52 @@ __global__ void __launch_bounds__(448, 1)
     return j < it.nc ? min(128, it.L - j * 128) : min(C::NEW, it.n - (j - it.nc) * C::NEW);
   };
 
+  // Loaders: an item's tiles, in the order of the ring. Lane 8 x + g looks after keys 16 g .. of the x-th of four
+  // tiles, whose page ids are fetched four tiles ahead.
+  const int page = 1 << a.page_shift, prow = min(page, 128), g8 = lane & 7, x8 = lane >> 3;
+  auto page_ids = [&](const Item8& it, int k) {  // of the tiles k .. k + 3 of the item's part
+    const int j = it.j0 + k + x8, t0 = j * 128 + g8 * 16;
+    return j < min(it.j0 + it.cnt, it.nc) && t0 < it.L ? a.table[it.b * a.table_stride + (t0 >> a.page_shift)] : 0;
+  };
+  // K's (kv = 0) or V's copies of the item's tiles, the ring's entries from e on.
+  auto load_tiles = [&](const Item8& it, int kv, int* e) {
+    int id = page_ids(it, 0), id_next = page_ids(it, 4);
+    for (int k = 0; k < it.cnt; ++k, ++*e) {
+      if (k && !(k & 3)) id = id_next, id_next = page_ids(it, k + 4);
+      const int j = it.j0 + k, s = *e % NT, rows = rows_here(it, j);
+      const bool cached = j < it.nc;
+      const uint32_t bar = BAR(C::FULL + s), dst0 = sbase + s * C::ENTRY + kv * C::KV;
+      const int box = cached ? prow : kNewBox8, boxes = (rows + box - 1) / box;
+      if (!wait_phase(BAR(C::EMPTY + s), ((*e / NT) & 1) ^ 1, st, SITE_T8_EMPTY)) return false;
+      if (elect_one()) mbar_arrive_expect_tx(bar, (uint32_t)(boxes * box * (cached ? C::ROW : 2 * D)));
+      __syncwarp();
+      if (cached) {
+        const int in_page = (j * 128 + g8 * 16) & (page - 1);
+        const uint32_t dst = dst0 + g8 * 16 * C::ROW;
+        if (x8 == (k & 3) && g8 * 16 < rows && (g8 * 16 & (prow - 1)) == 0 && !(kWithhold && *e == 1) &&
+            FA_CHECK(smem_in(dst, prow * C::ROW, sbase, sbase + C::OFF_P), st, DBG_TMA_LOAD))
+          tma_load_4d(dst, kv ? &tm_vc : &tm_kc, 0, in_page, it.kvh, id >= 0 && id < a.n_pages ? id : a.n_pages, bar);  // outside: zeros
+      } else {
+        const int r = lane / C::NSUB, c = lane % C::NSUB;
+        const uint32_t dst = dst0 + c * (C::NEW * 128) + r * kNewBox8 * 128;
+        if (r < boxes && !(kWithhold && *e == 1) && FA_CHECK(smem_in(dst, kNewBox8 * 128, sbase, sbase + C::OFF_P), st, DBG_TMA_LOAD))
+          tma_load_3d(dst, kv ? &tm_v : &tm_k, c * 64, it.row0 + (j - it.nc) * C::NEW + r * kNewBox8, it.kvh, bar);
+      }
+      __syncwarp();
+    }
+    return true;
+  };
+  auto let_land = [&](int e) {  // copies in flight, before a CTA that gives up releases its shared memory
+    if (!*(volatile int*)abort_flag) return;
+    for (int x = max(0, e - NT); x < e; ++x) {
+      const uint64_t t0 = globaltimer_ns();
+      while (!mbar_try_wait(BAR(C::FULL + x % NT), (x / NT) & 1) && globaltimer_ns() - t0 < 100000000ull) {
+      }
+    }
+  };
+
   if (warp == C::PRODUCER) {
-    // ------------------------------------------------------------ scheduler and TMA producer
+    // ------------------------------------------------------------ scheduler, and the loads of K
     int items = 0, e = 0;  // items published, ring entries used
     bool ok = true;
     auto publish = [&](const Item8& it) {
@@ -397,62 +446,11 @@ __global__ void __launch_bounds__(448, 1)
         d[0] = make_int4(it.cnt, it.flags, it.c0, it.c1);
         d[1] = make_int4(it.j0, it.nc, it.L, it.n);
         d[2] = make_int4(it.row0, it.r0, it.kvh, it.slot);
+        reinterpret_cast<int*>(d)[12] = it.b;
         mbar_arrive(BAR(C::D_FULL + (items & 3)));
       }
       __syncwarp();
       ++items;
-      return true;
-    };
-    // Loads the item's tiles. Lane (kv, g) = 8 kv + g looks after 16 keys: their scale, and, where a page's
-    // box begins with them, the box.
-    const int kv = (lane >> 3) & 1, g = lane & 7;
-    const int page = 1 << a.page_shift, prow = min(page, 128);
-    const float* sc = kv ? a.vs : a.ks;
-    auto run_item = [&](const Item8& it, int b) {
-      if (!publish(it)) return false;
-      auto page_of = [&](int j) {
-        const int t0 = j * 128 + g * 16;
-        return lane < 16 && j < min(it.j0 + it.cnt, it.nc) && t0 < it.L ? a.table[b * a.table_stride + (t0 >> a.page_shift)] : 0;
-      };
-      int id = page_of(it.j0);
-      for (int j = it.j0; j < it.j0 + it.cnt; ++j, ++e) {
-        const int id_next = page_of(j + 1);
-        const bool cached = j < it.nc;
-        const int s = e % NT, rows = rows_here(it, j);
-        const uint32_t bar = BAR(C::FULL + s), dst0 = sbase + s * C::ENTRY;
-        const int box = cached ? prow : kNewBox8, boxes = (rows + box - 1) / box;
-        if (!wait_phase(BAR(C::EMPTY + s), ((e / NT) & 1) ^ 1, st, SITE_T8_EMPTY)) return false;
-        if (elect_one()) mbar_arrive_expect_tx(bar, (uint32_t)(2 * boxes * box * (cached ? C::ROW : 2 * D)));
-        __syncwarp();
-        if (cached) {
-          const int t0 = j * 128 + g * 16, in_page = t0 & (page - 1);
-          const bool mine = lane < 16 && g * 16 < rows;
-          const bool there = id >= 0 && id < a.n_pages;
-          if (mine && !there) record_check(a.status, SITE_S_PAGE);
-          float* to = scales + s * 16 + lane;
-          if (mine && there) {
-            const float* from = sc + id * a.s_sp + it.kvh * a.s_sh + (in_page >> a.block_shift);
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(to)), "l"(from) : "memory");
-            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-          } else if (lane < 16) {
-            *to = 1.f;
-            mbar_arrive(bar);
-          }
-          const uint32_t dst = dst0 + kv * C::KV + g * 16 * C::ROW;
-          if (mine && (g * 16 & (prow - 1)) == 0 && !(kWithhold && e == 1) &&
-              FA_CHECK(smem_in(dst, prow * C::ROW, sbase, sbase + C::OFF_P), st, DBG_TMA_LOAD))
-            tma_load_4d(dst, kv ? &tm_vc : &tm_kc, 0, in_page, it.kvh, there ? id : a.n_pages, bar);  // outside: zeros
-        } else {
-          if (lane == 0) mbar_arrive_n(bar, 16);
-          const int r = g / C::NSUB, c = g % C::NSUB;
-          const uint32_t dst = dst0 + kv * C::KV + c * (C::NEW * 128) + r * kNewBox8 * 128;
-          if (lane < 16 && r < boxes && !(kWithhold && e == 1) &&
-              FA_CHECK(smem_in(dst, kNewBox8 * 128, sbase, sbase + C::OFF_P), st, DBG_TMA_LOAD))
-            tma_load_3d(dst, kv ? &tm_v : &tm_k, c * 64, it.row0 + (j - it.nc) * C::NEW + r * kNewBox8, it.kvh, bar);
-        }
-        __syncwarp();
-        id = id_next;
-      }
       return true;
     };
     Item8 it;
@@ -482,6 +480,7 @@ __global__ void __launch_bounds__(448, 1)
           it.c1 = dual ? it.cnt >> 1 : it.cnt;
           it.j0 = j0, it.nc = w.nc, it.L = w.L, it.n = w.n, it.row0 = w.row0, it.r0 = p * unit, it.kvh = kvh;
           it.slot = 2 * blockIdx.x + (j0 == 0);
+          it.b = b;
           if (j0 > 0 && it.cnt > 0 && runs.start(blockIdx.x - 1) <= pos - j0) {
             // (the first item only) how many CTAs, this one included, hold later parts of it
             const long long end_of_item = pos + most - j0;
@@ -489,7 +488,7 @@ __global__ void __launch_bounds__(448, 1)
               parts += __popc(__ballot_sync(0xffffffffu, k < runs.ctas && runs.start(k) < end_of_item));
             cut = make_int4(it.n * a.G, it.row0, it.r0, it.kvh);
           }
-          if (it.cnt > 0) ok = run_item(it, b);
+          if (it.cnt > 0) ok = publish(it) && load_tiles(it, 0, &e);
           pos += taken;
           j0 = 0;
           if (++kvh == a.Hkv) kvh = 0, ++p;
@@ -506,15 +505,49 @@ __global__ void __launch_bounds__(448, 1)
       it.cnt = -1;
       ok = publish(it);
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
-    if (*(volatile int*)abort_flag) {
-      // let copies already in flight land before the CTA's shared memory is released
-      for (int x = max(0, e - NT); x < e; ++x) {
-        const uint64_t t0 = globaltimer_ns();
-        while (!mbar_try_wait(BAR(C::FULL + x % NT), (x / NT) & 1) && globaltimer_ns() - t0 < 100000000ull) {
+    let_land(e);
+  } else if (warp == C::LOAD_V) {
+    // ------------------------------------------------------------ the loads of V
+    int e = 0;
+    for (int i = 0;; ++i) {
+      Item8 it;
+      if (!next_item(i, &it) || it.cnt < 0 || !load_tiles(it, 1, &e)) break;
+    }
+    let_land(e);
+  } else if (warp == C::SCALES) {
+    // ------------------------------------------------------------ the loads of the scales
+    int e = 0;
+    bool ok = true;
+    for (int i = 0; ok; ++i) {
+      Item8 it;
+      if (!next_item(i, &it) || it.cnt < 0) break;
+      int id = page_ids(it, 0), id_next = page_ids(it, 4);
+      for (int k = 0; k < it.cnt; ++k, ++e) {
+        if (k && !(k & 3)) id = id_next, id_next = page_ids(it, k + 4);
+        const int j = it.j0 + k, s = e % NT;
+        const uint32_t bar = BAR(C::FULL + s);
+        if (!(ok = wait_phase(BAR(C::EMPTY + s), ((e / NT) & 1) ^ 1, st, SITE_T8_EMPTY))) break;
+        if (j >= it.nc) {
+          if (lane == 0) mbar_arrive_n(bar, 8);
+        } else if (x8 == (k & 3)) {
+          const int t0 = j * 128 + g8 * 16;
+          const bool mine = t0 < it.L, there = id >= 0 && id < a.n_pages;
+          if (mine && !there) record_check(a.status, SITE_S_PAGE);
+          float* to = scales + s * 16 + g8;
+          if (mine && there) {
+            const long long from = id * a.s_sp + it.kvh * a.s_sh + ((t0 & (page - 1)) >> a.block_shift);
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(to)), "l"(a.ks + from) : "memory");
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(to + 8)), "l"(a.vs + from) : "memory");
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+          } else {
+            to[0] = to[8] = 1.f;
+            mbar_arrive(bar);
+          }
         }
+        __syncwarp();
       }
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp >= C::SPLIT) {
     // ------------------------------------------------------------ Q in parts
     constexpr int LPR = D / 8, RPI = 32 / LPR, STEPS = R / 2 / RPI;  // lanes a row, rows and steps of a warp
@@ -621,24 +654,26 @@ __global__ void __launch_bounds__(448, 1)
             if (g > 1 && !(ok = wait_phase(BAR(C::S_FREE + 2 * t + u), ((g >> 1) - 1) & 1, st, SITE_T8_S_FREE))) break;
             tc_fence_after();
             const uint32_t d = tmem + C::tm_s(t, u), qb = q_lo + (t && !dual ? slot1 : slot0) * (C::QSLOT >> 4);
-            if (j < it.nc) {
+            if (elect_one()) {
+              if (j < it.nc) {
 #pragma unroll
-              for (int x = 0; x < D / 32; ++x)
-                if (elect_one()) mma8_ss(d, sdesc_join(ka + 2 * x, HI), sdesc_join(qb + 2 * x, HI), I8, x > 0);
-              if (F16) {
+                for (int x = 0; x < D / 32; ++x) mma8_ss(d, sdesc_join(ka + 2 * x, HI), sdesc_join(qb + 2 * x, HI), I8, x > 0);
+                if (F16) {
 #pragma unroll
-                for (int x = 0; x < D / 32; ++x)
-                  if (elect_one()) mma8_ss(d + R, sdesc_join(ka + 2 * x, HI), sdesc_join(qb + (2 * R * D >> 4) + 2 * x, HI), I8X, 1);
+                  for (int x = 0; x < D / 32; ++x)
+                    mma8_ss(d + R, sdesc_join(ka + 2 * x, HI), sdesc_join(qb + (2 * R * D >> 4) + 2 * x, HI), I8X, 1);
+                }
+              } else {
+#pragma unroll
+                for (int x = 0; x < D / 16; ++x) {
+                  const uint32_t ko = ((x >> 2) * (C::NEW * 128) + (x & 3) * 32) >> 4;
+                  const uint32_t qo = (C::Q16 + (x >> 2) * (R * 128) + (x & 3) * 32) >> 4;
+                  mma_ss(d, sdesc_join(ka + ko, HI16), sdesc_join(qb + qo, HI16), I16, x > 0);
+                }
               }
-            } else {
-#pragma unroll
-              for (int x = 0; x < D / 16; ++x) {
-                const uint32_t ko = ((x >> 2) * (C::NEW * 128) + (x & 3) * 32) >> 4;
-                const uint32_t qo = (C::Q16 + (x >> 2) * (R * 128) + (x & 3) * 32) >> 4;
-                if (elect_one()) mma_ss(d, sdesc_join(ka + ko, HI16), sdesc_join(qb + qo, HI16), I16, x > 0);
-              }
+              mma_commit(BAR(C::S_FULL + 2 * t + u));
             }
-            commit(BAR(C::S_FULL + 2 * t + u));
+            __syncwarp();
           }
           if (!ok) break;
         }
@@ -684,16 +719,16 @@ __global__ void __launch_bounds__(448, 1)
           if (first && items > 0 && !(ok = wait_phase(BAR(C::O_FREE + t), (items - 1) & 1, st, SITE_T8_O_FREE))) break;
           tc_fence_after();
           const uint32_t va = v_lo + s * (C::ENTRY >> 4), pa = p_lo + (C::NP == 2 ? (g & 1) * (C::PBYTES >> 4) : 0);
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            if (!elect_one()) continue;
-            if (cached)
-              mma8_ss(d, sdesc_join(va + x * (32 * C::ROW >> 4), HIV), sdesc_join(pa + x * (32 * C::PX >> 4), HIP), I8, !first || x > 0);
-            else
-              mma_ss(d, sdesc_join(va + x * (2048 >> 4), HI16), sdesc_join(pa + x * (16 * C::PX >> 4), HIP), I16, !first || x > 0);
-          }
-          __syncwarp();
           if (elect_one()) {
+            if (cached) {
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                mma8_ss(d, sdesc_join(va + x * (32 * C::ROW >> 4), HIV), sdesc_join(pa + x * (32 * C::PX >> 4), HIP), I8, !first || x > 0);
+            } else {
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                mma_ss(d, sdesc_join(va + x * (2048 >> 4), HI16), sdesc_join(pa + x * (16 * C::PX >> 4), HIP), I16, !first || x > 0);
+            }
             mma_commit(BAR(C::O_DONE + 2 * t + (g & 1)));
             mma_commit(BAR(C::EMPTY + s));
             if (dual) mma_commit(BAR(C::EMPTY + s));
@@ -714,7 +749,7 @@ __global__ void __launch_bounds__(448, 1)
     // ------------------------------------------------------------ softmax of lane t, a thread a key
     const int t = warp >> 2, wq = warp & 3, key = wq * 32 + lane;
     const uint32_t tlane = (uint32_t)(wq * 32) << 16;
-    float* nbs = reinterpret_cast<float*>(sm + C::OFF_NB) + t * R;
+    float2* rowc = reinterpret_cast<float2*>(sm + C::OFF_ROWC) + t * R;
     float* facs = reinterpret_cast<float*>(sm + C::OFF_FAC) + t * R;
     float* refs = reinterpret_cast<float*>(sm + C::OFF_REF);
     float* sums = reinterpret_cast<float*>(sm + C::OFF_SUM);
@@ -744,10 +779,20 @@ __global__ void __launch_bounds__(448, 1)
 #pragma unroll
       for (int r = 0; r < RV; ++r) l[r] = 0.f;
       float vref = 1.1754944e-38f;
-      for (int s = 0; s < steps; ++s, ++g) {
-        const int k = dual ? 2 * s + t : s, j = it.j0 + k, es = (e0 + k) % NT;
-        const bool cached = j < it.nc;
-        if (!wait_phase(BAR(C::S_FULL + 2 * t + (g & 1)), (g >> 1) & 1, st, SITE_T8_S_FULL)) return false;
+      const int stride = dual ? 2 : 1, ahead = dual ? t : 0;
+      const int cached_steps = min(steps, max(0, it.nc - it.j0 - ahead + stride - 1) / stride);
+      int es = (e0 + ahead) % NT, s = 0;
+      auto step = [&](auto of_cache) {
+        constexpr bool cached = decltype(of_cache)::value;
+        const int j = it.j0 + ahead + s * stride;
+        // S is there, and P of the tile that had its buffer before has been read
+        const uint32_t s_bar = BAR(C::S_FULL + 2 * t + (g & 1)), p_bar = BAR(C::O_DONE + 2 * t + ((g - C::NP) & 1));
+        const uint32_t s_ph = (g >> 1) & 1, p_ph = ((g - C::NP) >> 1) & 1;
+        if (g < C::NP) {
+          if (!wait_phase(s_bar, s_ph, st, SITE_T8_S_FULL)) return false;
+        } else if (!__all_sync(0xffffffffu, mbar_try_wait(s_bar, s_ph) && mbar_try_wait(p_bar, p_ph))) {
+          if (!wait_slow(s_bar, s_ph, st, SITE_T8_S_FULL) || !wait_slow(p_bar, p_ph, st, SITE_T8_O_DONE)) return false;
+        }
         tc_fence_after();
         const bool there = key < rows_here(it, j);
         const float kscale = cached ? scales[es * 16 + (key >> 4)] : 1.f;
@@ -806,12 +851,12 @@ __global__ void __launch_bounds__(448, 1)
             for (int x = 0; x < 4; ++x) m = fmaxf(m, red[x * (R + 4) + key]);
             const bool row = qr[key].tok >= 0;
             // a row that is none never moves; one without a key so far does with the first
-            const float nb = s == 0 ? (row ? kPLog2 - kNoKey : kNoKey) : nbs[key], ref = kPLog2 - nb;
+            const float nb = s == 0 ? (row ? kPLog2 - kNoKey : kNoKey) : rowc[key].y, ref = kPLog2 - nb;
             if (row && m > ref + kLagLog2) {
-              nbs[key] = kPLog2 - m;
+              rowc[key] = make_float2(qr[key].factor, kPLog2 - m);
               f = ex2_approx(ref - m);
             } else if (s == 0) {
-              nbs[key] = nb;
+              rowc[key] = make_float2(qr[key].factor, nb);
             }
             facs[key] = f;
           }
@@ -851,8 +896,9 @@ __global__ void __launch_bounds__(448, 1)
             load_y(c, y);
 #pragma unroll
             for (int r = 0; r < W; ++r) {
-              const float f = cached ? qr[c + r].factor : a.scale_log2;
-              const float tt = (seen >> (c + r) & 1) ? fmaf(y[r], f, nbs[c + r]) : -INFINITY;
+              const float2 rc = rowc[c + r];
+              float tt = fmaf(y[r], cached ? rc.x : a.scale_log2, rc.y);
+              if (!(cached ? there : (seen >> (c + r) & 1))) tt = -INFINITY;
               top = fmaxf(top, tt);
               p[c + r] = tt;
             }
@@ -887,8 +933,6 @@ __global__ void __launch_bounds__(448, 1)
           }
 #pragma unroll
           for (int r = 0; r < RV; ++r) l[r] += p[r];
-          // P of the tile that had this buffer has been read
-          if (g >= C::NP && !wait_pv(g - C::NP)) return false;
           if (cached) {
 #pragma unroll
             for (int z = 0; z < C::PPARTS; ++z) {
@@ -926,9 +970,15 @@ __global__ void __launch_bounds__(448, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(BAR(C::P_READY + 2 * t + (g & 1)));  // (two: P may be two tiles ahead of its product)
-      }
-      const bool join = dual && it.c1 > 0, whole = it.flags & ITEM8_WHOLE;
-      const long long part0 = (long long)it.slot * (2 * R) + (dual ? 0 : t * R);
+        ++s, ++g;
+        es += stride;
+        if (es >= NT) es -= NT;
+        return true;
+      };
+      while (s < cached_steps)
+        if (!step(std::true_type())) return false;
+      while (s < steps)
+        if (!step(std::false_type())) return false;
       if (steps > 0) {
         if (!wait_pv(g - 1)) return false;
         tc_fence_after();
@@ -956,8 +1006,19 @@ __global__ void __launch_bounds__(448, 1)
           }
           if ((lane & (32 / W - 1)) == 0) sums[(t * 4 + wq) * R + c + row] = v[0];
         }
-        if (key < RV) refs[t * R + key] = kPLog2 - nbs[key];
+        if (key < RV) refs[t * R + key] = kPLog2 - rowc[key].y;
         if (key == 0) vrefs[t] = vref;
+      }
+      return true;
+    };
+    // What becomes of an item's results, for all classes: code that runs once an item has to be fetched anew
+    auto finish = [&](const Item8& it) {
+      const bool dual = it.flags & ITEM8_DUAL, join = dual && it.c1 > 0, whole = it.flags & ITEM8_WHOLE;
+      const int slot = (uq + (dual ? 0 : t)) % NQ, steps = t ? it.c1 : it.c0;
+      const QRow* qr = qrows + slot * R;
+      const long long part0 = (long long)it.slot * (2 * R) + (dual ? 0 : t * R);
+      const int rows = min(R, it.n * a.G - it.r0 - (dual ? 0 : t * R));  // 1 at least, where there are steps
+      if (steps > 0) {
         // The other lane's results stay as they are until its next product into O, which waits for this lane's
         // arrival below.
         if (join) {
@@ -969,91 +1030,86 @@ __global__ void __launch_bounds__(448, 1)
         } else if (!meet()) {
           return false;
         }
-        // rows [ra, rb): in a join each lane takes half of them
-        const int ra = join ? t * (RV / 2) : 0, rb = join ? ra + RV / 2 : RV;
-        auto weights = [&](int r, float* f0, float* f1) {  // of both lanes' O; returns the row's LSE to base 2
-          const float m0 = refs[(join ? 0 : t) * R + r], m1 = join ? refs[R + r] : kNoKey;
+        // rows [ra, rb), four at a time: in a join each lane takes half of them
+        const int half = (rows + 7) / 8 * 4, ra = join ? t * half : 0, rb = join && t == 0 ? half : rows;
+        const float v0 = vrefs[join ? 0 : t], v1 = join ? vrefs[1] : 0.f;
+        auto o_free = [&] {  // O is in registers: the issuers may write it again
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive_n(BAR(C::O_FREE + t), join ? 1 : 2);
+            if (join) mbar_arrive(BAR(C::O_FREE + (t ^ 1)));
+          }
+        };
+        if (ra >= rb) o_free();
+#pragma unroll 1
+        for (int r0 = ra; r0 < rb; r0 += 4) {
+          // weights of both lanes' O for row r0 + lane % 4, and its LSE to base 2
+          const int rr = r0 + (lane & 3);
+          const float m0 = refs[(join ? 0 : t) * R + rr], m1 = join ? refs[R + rr] : kNoKey, m = fmaxf(m0, m1);
           float l0 = 0.f, l1 = 0.f;
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            l0 += sums[((join ? 0 : t) * 4 + x) * R + r];
-            if (join) l1 += sums[(4 + x) * R + r];
+            l0 += sums[((join ? 0 : t) * 4 + x) * R + rr];
+            if (join) l1 += sums[(4 + x) * R + rr];
           }
-          const float m = fmaxf(m0, m1);
-          *f0 = ex2_approx(m0 - m), *f1 = ex2_approx(m1 - m);
-          const float sum = l0 * *f0 + l1 * *f1, inv = sum != 0.f ? 1.f / sum : 0.f;  // 0: no key; NaN stays NaN
-          *f0 *= inv, *f1 *= inv;
-          return sum != 0.f ? m - kPLog2 + lg2_approx(sum) : -INFINITY;
-        };
-        if (key >= ra && key < rb && qr[key].tok >= 0) {
-          float f0, f1;
-          const float lse2 = weights(key, &f0, &f1);
-          const long long token = qr[key].to & 0xffffffffffll, head = qr[key].to >> 40;
-          if (!whole) {
-            if (FA_CHECK(in_range(part0 + key, a.part_rows), st, DBG_GLOBAL_STORE)) a.part_lse[part0 + key] = lse2;
-          } else if (a.lse && FA_CHECK(in_range(token, a.T), st, DBG_GLOBAL_STORE)) {
-            a.lse[head * a.T + token] = lse2 * 0.6931471805599453f;
+          float f0 = ex2_approx(m0 - m), f1 = ex2_approx(m1 - m);
+          const float sum = l0 * f0 + l1 * f1, inv = sum != 0.f ? 1.f / sum : 0.f;  // 0: no key; NaN stays NaN
+          f0 *= inv * v0, f1 *= inv * v1;
+          const int tok = qr[rr].tok;
+          const long long token = qr[rr].to & 0xffffffffffll, head = qr[rr].to >> 40;
+          if (wq == 0 && lane < 4 && rr < rb && tok >= 0) {
+            const float lse2 = sum != 0.f ? m - kPLog2 + lg2_approx(sum) : -INFINITY;
+            if (!whole) {
+              if (FA_CHECK(in_range(part0 + rr, a.part_rows), st, DBG_GLOBAL_STORE)) a.part_lse[part0 + rr] = lse2;
+            } else if (a.lse && FA_CHECK(in_range(token, a.T), st, DBG_GLOBAL_STORE)) {
+              a.lse[head * a.T + token] = lse2 * 0.6931471805599453f;
+            }
           }
-        }
-        const float v0 = vrefs[join ? 0 : t], v1 = join ? vrefs[1] : 0.f;
-        constexpr int WO = RV < 16 ? RV / 2 : 8;  // rows at a time
-#pragma unroll 1
-        for (int r0 = ra; r0 < rb; r0 += WO) {
-          float o[WO];
+          float o[4] = {};
           if (key < D) {
-#pragma unroll
-            for (int r = 0; r < WO; ++r) o[r] = 0.f;
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              if (u == 1 && !join) break;
-              uint32_t x[C::PPARTS][WO];
+#pragma unroll 1
+            for (int u = 0; u < 1 + join; ++u) {
+              uint32_t x[C::PPARTS][4];
               const uint32_t at = tmem + tlane + C::tm_o(join ? u : t) + r0;
               // (tiles of new tokens alone write the first part's columns only)
               const bool parts = it.j0 + (dual ? (join ? u : t) : 0) < it.nc;
 #pragma unroll
-              for (int z = 0; z < C::PPARTS; ++z) tmem_ldn<WO>(at + z * R, x[z]);
+              for (int z = 0; z < C::PPARTS; ++z) tmem_ldn<4>(at + z * R, x[z]);
               tmem_wait_ld();
 #pragma unroll
-              for (int r = 0; r < WO; ++r) {
-                float f0, f1, v = __uint_as_float(x[0][r]);
-                weights(r0 + r, &f0, &f1);
+              for (int r = 0; r < 4; ++r) {
+                float v = __uint_as_float(x[0][r]);
                 if (parts) {
                   float low = __uint_as_float(x[2][r]);
                   if (F16) low += __uint_as_float(x[C::PPARTS - 1][r]);
                   v = fmaf(low, 0.015625f, v + __uint_as_float(x[1][r]));
                 }
-                o[r] = fmaf(v, u ? f1 * v1 : f0 * v0, o[r]);
+                o[r] = fmaf(v, __shfl_sync(0xffffffffu, u ? f1 : f0, r), o[r]);
               }
             }
           }
-          if (r0 + WO >= rb) {  // O is in registers: the issuers may write it again
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-              mbar_arrive_n(BAR(C::O_FREE + t), join ? 1 : 2);
-              if (join) mbar_arrive(BAR(C::O_FREE + (t ^ 1)));
-            }
-          }
+          if (r0 + 4 >= rb) o_free();
           if (key >= D) continue;
           if (whole) {
             // even threads write the even rows of two columns each, odd threads the odd rows
+            uint16_t* const row = a.o + token * a.o_st + head * a.o_sh;  // of this lane's rr
+            const long long mine = tok >= 0 && FA_CHECK(in_range(token, a.T), st, DBG_GLOBAL_STORE) ? (long long)row : 0;
 #pragma unroll
-            for (int r = 0; r < WO; r += 2) {
+            for (int r = 0; r < 4; r += 2) {
               const float got = __shfl_xor_sync(0xffffffffu, (lane & 1) ? o[r] : o[r + 1], 1);
               const uint32_t y = (lane & 1) ? pack16<F16>(got, o[r + 1]) : pack16<F16>(o[r], got);
-              const QRow& q = qr[r0 + r + (lane & 1)];
-              const long long token = q.to & 0xffffffffffll;
-              if (q.tok >= 0 && FA_CHECK(in_range(token, a.T), st, DBG_GLOBAL_STORE))
-                *reinterpret_cast<uint32_t*>(a.o + token * a.o_st + (q.to >> 40) * a.o_sh + (key & ~1)) = y;
+              const long long to = __shfl_sync(0xffffffffu, mine, r + (lane & 1));
+              if (to) *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(to) + (key & ~1)) = y;
             }
           } else {
 #pragma unroll
-            for (int r = 0; r < WO; ++r)
-              if (qr[r0 + r].tok >= 0 && FA_CHECK(in_range(part0 + r0 + r, a.part_rows), st, DBG_GLOBAL_STORE))
+            for (int r = 0; r < 4; ++r)
+              if (__shfl_sync(0xffffffffu, tok, r) >= 0 && FA_CHECK(in_range(part0 + r0 + r, a.part_rows), st, DBG_GLOBAL_STORE))
                 a.part_o[(part0 + r0 + r) * D + key] = o[r];
           }
         }
-      } else if (!dual && key < RV && qr[key].tok >= 0 && FA_CHECK(in_range(part0 + key, a.part_rows), st, DBG_GLOBAL_STORE)) {
+      } else if (!dual && key < R && qr[key].tok >= 0 && FA_CHECK(in_range(part0 + key, a.part_rows), st, DBG_GLOBAL_STORE)) {
         a.part_lse[part0 + key] = -INFINITY;  // (a cut item only) none of this part's keys concerns these rows
       }
       __syncwarp();
@@ -1075,7 +1131,7 @@ __global__ void __launch_bounds__(448, 1)
       } else {
         ok = rows <= 16 ? run_item(it, Rows8<16>()) : run_item(it, Rows8<32>());
       }
-      if (!ok) break;
+      if (!ok || !finish(it)) break;
       uq += dual ? 1 : 2;
       e0 += it.cnt;
     }
