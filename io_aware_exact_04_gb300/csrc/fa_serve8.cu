@@ -35,7 +35,7 @@ namespace fa {
 //    in range by a reference of its own (vref, at least each scale that was met).
 //
 // The new tokens, in 16 bits, take the same way as tiles of 64 keys: kind::f16 products with Q and P in
-// 16 bits, into the same accumulators (O is brought to vref = 1 before).
+// 16 bits, into columns of O of their own (vref = 1 there).
 //
 // Rows: a row is (token, head of the group), numbered token * G + head; a lane (four warps) has R of
 // them. A work item is 2 R rows of a sequence and key/value head, R for each of two lanes, over the same
@@ -79,7 +79,9 @@ struct Serve8Cfg {
   static constexpr int OFF_FLAG = OFF_RED + 2 * 4 * (R + 4) * 4, SMEM_BYTES = OFF_FLAG + 64;
   __device__ static constexpr uint32_t tm_s(int t, int u) { return 4u * R * t + 2u * R * u; }
   __device__ static constexpr uint32_t tm_o(int t) { return 8u * R + 4u * R * t; }
-  static constexpr uint32_t TM_COLS = 16 * R;
+  __device__ static constexpr uint32_t tm_n(int t) { return 16u * R + R * t; }  // O of the new tokens
+  static constexpr uint32_t TM_COLS = 512;
+  static_assert(18 * R <= 512, "tensor memory");
   static constexpr int THREADS = 512, PRODUCER = 8, S_BOTH = 9, PV0 = 10, PV1 = 11, SPLIT = 12, LOAD_V = 14, SCALES = 15;
   // barriers
   static constexpr int FULL = 0, EMPTY = NT, Q_FULL = 2 * NT, Q_EMPTY = Q_FULL + NQ, S_FULL = Q_EMPTY + NQ, S_FREE = S_FULL + 4,
@@ -96,6 +98,10 @@ enum { SITE_T8_EMPTY = 80, SITE_T8_FULL, SITE_T8_Q_FULL, SITE_T8_Q_EMPTY, SITE_T
 constexpr float kNoKey = -1e30f;     // reference maximum of a row that has met no key
 constexpr float kPLog2 = 11.f, kLagLog2 = 4.f;
 constexpr int kMinTiles8 = 2;        // tiles of a CTA where there are few
+// An item's start and end cost a CTA as much as some tiles do (2.2 us and 0.6 a tile at d = 128, 4.0 and 0.5 at d = 64): the
+// runs are balanced with that many more for each.
+template <int D>
+constexpr int kItemTiles = D == 64 ? 8 : 4;
 constexpr int kNewBox8 = 16;         // rows of a TMA box of new tokens
 
 // A work item (or the part of it that this CTA computes), as the producer publishes it.
@@ -117,8 +123,9 @@ enum { ITEM8_DUAL = 1, ITEM8_WHOLE = 2 };
 // Sizes of sequence b's work, in items of `unit` rows; record: whether invalid device values are recorded.
 struct SeqWork8 {
   int row0, n, L, nc, nk, units;
-  long long tiles;  // all heads and units, each counted with the nk tiles of the last one
+  long long tiles;  // all heads and units, each counted with the nk tiles of the last one, and what an item costs
 };
+template <int D>
 __device__ __forceinline__ SeqWork8 seq_work8(const Serve8BitArgs& a, int lo, int hi, int len, int unit, bool record) {
   SeqWork8 w;
   w.row0 = min(max(lo, 0), a.T);
@@ -133,11 +140,12 @@ __device__ __forceinline__ SeqWork8 seq_work8(const Serve8BitArgs& a, int lo, in
   w.nc = (w.L + 127) >> 7;
   w.nk = w.nc + ((w.n + 63) >> 6);
   w.units = (w.n * a.G + unit - 1) / unit;
-  w.tiles = (long long)w.units * a.Hkv * w.nk;
+  w.tiles = (long long)w.units * a.Hkv * (w.nk + kItemTiles<D>);
   return w;
 }
+template <int D>
 __device__ __forceinline__ SeqWork8 seq_work8(const Serve8BitArgs& a, int b, int unit, bool record) {
-  return seq_work8(a, a.cu[b], a.cu[b + 1], a.lens[b], unit, record);
+  return seq_work8<D>(a, a.cu[b], a.cu[b + 1], a.lens[b], unit, record);
 }
 
 // The run of tiles of CTA c, by a whole warp. Each lane counts the tiles of `chunk` sequences that follow
@@ -149,6 +157,7 @@ struct Runs8 {
   int chunk;
   __device__ long long start(int c) const { return base * c + min(c, rest); }
 };
+template <int D>
 __device__ __forceinline__ Runs8 runs8(const Serve8BitArgs& a, int unit, int grid, bool record) {
   Runs8 r;
   const int lane = threadIdx.x & 31;
@@ -163,7 +172,7 @@ __device__ __forceinline__ Runs8 runs8(const Serve8BitArgs& a, int unit, int gri
     for (int k = 0; k < 4; ++k) len[k] = a.lens[min(b + k, end - 1)];
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      if (b + k < end) r.mine += seq_work8(a, at[k], at[k + 1], len[k], unit, record).tiles;
+      if (b + k < end) r.mine += seq_work8<D>(a, at[k], at[k + 1], len[k], unit, record).tiles;
   }
   r.total = r.mine;
   for (int o = 16; o; o >>= 1) r.total += __shfl_xor_sync(0xffffffffu, r.total, o);
@@ -186,6 +195,7 @@ __device__ __forceinline__ int lane_with(long long mine, long long pos, long lon
   return k;
 }
 // The sequence that tile `pos` of all belongs to, and its first tile; by a whole warp. pos < total.
+template <int D>
 __device__ __forceinline__ int seek8(const Serve8BitArgs& a, int unit, const Runs8& runs, long long pos, long long* first) {
   *first = 0;
   const int k = lane_with(runs.mine, pos, first);
@@ -194,7 +204,7 @@ __device__ __forceinline__ int seek8(const Serve8BitArgs& a, int unit, const Run
   const int end = min(a.B, (k + 1) * runs.chunk);
   for (int b0 = k * runs.chunk; b0 < end; b0 += 32) {
     const int b = b0 + (threadIdx.x & 31);
-    const int x = lane_with(b < end ? seq_work8(a, b, unit, false).tiles : 0, pos, first);
+    const int x = lane_with(b < end ? seq_work8<D>(a, b, unit, false).tiles : 0, pos, first);
     if (x < 32) return b0 + x;
   }
   return a.B;
@@ -400,14 +410,19 @@ __global__ void __launch_bounds__(512, 1)
   };
   // K's (kv = 0) or V's copies of the item's tiles, the ring's entries from e on.
   auto load_tiles = [&](const Item8& it, int kv, int* e) {
-    int id = page_ids(it, 0), id_next = page_ids(it, 4);
-    for (int k = 0; k < it.cnt; ++k, ++*e) {
+    int id = page_ids(it, 0), id_next = page_ids(it, 4), s = *e % NT;
+    uint32_t phase = ((*e / NT) & 1) ^ 1;
+    auto next = [&] {
+      ++*e;
+      if (++s == NT) s = 0, phase ^= 1;
+    };
+    for (int k = 0; k < it.cnt; ++k, next()) {
       if (k && !(k & 3)) id = id_next, id_next = page_ids(it, k + 4);
-      const int j = it.j0 + k, s = *e % NT, rows = rows_here(it, j);
+      const int j = it.j0 + k, rows = rows_here(it, j);
       const bool cached = j < it.nc;
       const uint32_t bar = BAR(C::FULL + s), dst0 = sbase + s * C::ENTRY + kv * C::KV;
       const int box = cached ? prow : kNewBox8, boxes = (rows + box - 1) / box;
-      if (!wait_phase(BAR(C::EMPTY + s), ((*e / NT) & 1) ^ 1, st, SITE_T8_EMPTY)) return false;
+      if (!wait_phase(BAR(C::EMPTY + s), phase, st, SITE_T8_EMPTY)) return false;
       if (elect_one()) mbar_arrive_expect_tx(bar, (uint32_t)(boxes * box * (cached ? C::ROW : 2 * D)));
       __syncwarp();
       if (cached) {
@@ -455,25 +470,25 @@ __global__ void __launch_bounds__(512, 1)
     };
     Item8 it;
     const int unit = 2 * R;
-    const Runs8 runs = runs8(a, unit, gridDim.x, blockIdx.x == 0);
+    const Runs8 runs = runs8<D>(a, unit, gridDim.x, blockIdx.x == 0);
     int parts = 0;  // of the item that this CTA is the first to cut
     int4 cut = make_int4(0, 0, 0, 0);
     if ((int)blockIdx.x < runs.ctas && runs.total > 0) {
       long long pos = runs.start(blockIdx.x), first = 0;
       const long long end = runs.start(blockIdx.x + 1);
-      int b = seek8(a, unit, runs, pos, &first);
+      int b = seek8<D>(a, unit, runs, pos, &first);
       while (ok && pos < end) {
-        const SeqWork8 w = seq_work8(a, b, unit, false);
-        // the first item may be cut; from then on they start with their first tile
+        const SeqWork8 w = seq_work8<D>(a, b, unit, false);
+        const int span = w.nk + kItemTiles<D>;  // an item's share of the run: its costs, then its tiles
+        // the first item may be cut; from then on they are met from their start
         const long long at = pos - first;
-        const int q = at < (1LL << 31) ? (int)at / max(w.nk, 1) : (int)(at / w.nk);
-        int p = q / a.Hkv, kvh = q - p * a.Hkv, j0 = (int)(at - (long long)q * w.nk);
+        const int q = at < (1LL << 31) ? (int)at / span : (int)(at / span);
+        int p = q / a.Hkv, kvh = q - p * a.Hkv, x0 = (int)(at - (long long)q * span);
         while (ok && pos < end && pos - first < w.tiles) {
-          int j1 = (int)min((long long)w.nk, j0 + (end - pos));
-          const int taken = j1 - j0;
+          const int x1 = (int)min((long long)span, x0 + (end - pos));
           const int n0 = tiles_of_rows(a, w, p * unit, R), n1 = tiles_of_rows(a, w, p * unit + R, R), most = max(n0, n1);
           const bool dual = n1 == 0;
-          j1 = min(j1, most);
+          const int j0 = max(0, x0 - kItemTiles<D>), j1 = min(max(0, x1 - kItemTiles<D>), most);
           it.cnt = max(0, j1 - j0);
           it.flags = (dual ? ITEM8_DUAL : 0) | (j0 == 0 && j1 == most ? ITEM8_WHOLE : 0);
           it.c0 = dual ? (it.cnt + 1) >> 1 : max(0, min(j1, n0) - j0);
@@ -481,16 +496,17 @@ __global__ void __launch_bounds__(512, 1)
           it.j0 = j0, it.nc = w.nc, it.L = w.L, it.n = w.n, it.row0 = w.row0, it.r0 = p * unit, it.kvh = kvh;
           it.slot = 2 * blockIdx.x + (j0 == 0);
           it.b = b;
-          if (j0 > 0 && it.cnt > 0 && runs.start(blockIdx.x - 1) <= pos - j0) {
+          const long long tile0 = pos - x0 + kItemTiles<D>;  // the place of the item's first tile
+          if (j0 > 0 && it.cnt > 0 && runs.start(blockIdx.x - 1) <= tile0) {
             // (the first item only) how many CTAs, this one included, hold later parts of it
-            const long long end_of_item = pos + most - j0;
+            const long long end_of_item = tile0 + most;
             for (int k = blockIdx.x + lane; __any_sync(0xffffffffu, k < runs.ctas); k += 32)
               parts += __popc(__ballot_sync(0xffffffffu, k < runs.ctas && runs.start(k) < end_of_item));
             cut = make_int4(it.n * a.G, it.row0, it.r0, it.kvh);
           }
           if (it.cnt > 0) ok = publish(it) && load_tiles(it, 0, &e);
-          pos += taken;
-          j0 = 0;
+          pos += x1 - x0;
+          x0 = 0;
           if (++kvh == a.Hkv) kvh = 0, ++p;
         }
         first += w.tiles;
@@ -694,7 +710,7 @@ __global__ void __launch_bounds__(512, 1)
         if (!next_item(i, &it) || it.cnt < 0) break;
         const bool dual = it.flags & ITEM8_DUAL;
         const int tiles = t ? it.c1 : it.c0;
-        bool first = true;
+        bool first = true, first_new = true;
         for (int k = 0; ok && k < it.cnt; ++k, ++e) {
           const int s = e % NT;
           // waited for also where the other lane's: the arrival below must not count for an earlier use
@@ -727,7 +743,8 @@ __global__ void __launch_bounds__(512, 1)
             } else {
 #pragma unroll
               for (int x = 0; x < 4; ++x)
-                mma_ss(d, sdesc_join(va + x * (2048 >> 4), HI16), sdesc_join(pa + x * (16 * C::PX >> 4), HIP), I16, !first || x > 0);
+                mma_ss(tmem + C::tm_n(t), sdesc_join(va + x * (2048 >> 4), HI16), sdesc_join(pa + x * (16 * C::PX >> 4), HIP), I16,
+                       !first_new || x > 0);
             }
             mma_commit(BAR(C::O_DONE + 2 * t + (g & 1)));
             mma_commit(BAR(C::EMPTY + s));
@@ -735,6 +752,7 @@ __global__ void __launch_bounds__(512, 1)
           }
           __syncwarp();
           first = false;
+          if (!cached) first_new = false;
           ++g;
         }
         items += tiles > 0;
@@ -843,7 +861,7 @@ __global__ void __launch_bounds__(512, 1)
           float v = 0.f;
 #pragma unroll
           for (int x = 0; x < 4; ++x) v = fmaxf(v, red[x * (R + 4) + R]);
-          const float to = !cached ? 1.f : v > vref ? 2.f * v : vref, fv = s == 0 ? 1.f : vref / to;
+          const float to = cached && v > vref ? 2.f * v : vref, fv = vref / to;  // (cached tiles come first)
           vref = to;
           if (key < RV) {
             float m = -INFINITY, f = 1.f;
@@ -864,16 +882,17 @@ __global__ void __launch_bounds__(512, 1)
           if (s > 0) {
             if (!wait_pv(g - 1)) return false;
             tc_fence_after();
+            const int parts = cached_steps > 0 ? C::PPARTS : 0;  // of O that are there already; then that of new tokens
 #pragma unroll 1
-            for (int c = 0; c < RV; c += W) {
-#pragma unroll
-              for (int z = 0; z < C::PPARTS; ++z) {
-                const uint32_t at = tmem + tlane + C::tm_o(t) + z * R + c;
+            for (int z = 0; z < parts + (s > cached_steps); ++z) {
+#pragma unroll 1
+              for (int c = 0; c < RV; c += W) {
+                const uint32_t at = tmem + tlane + (z < parts ? C::tm_o(t) + z * R : C::tm_n(t)) + c;
                 uint32_t x[W];
                 tmem_ldn<W>(at, x);
                 tmem_wait_ld();
 #pragma unroll
-                for (int r = 0; r < W; ++r) x[r] = __float_as_uint(__uint_as_float(x[r]) * (facs[c + r] * fv));
+                for (int r = 0; r < W; ++r) x[r] = __float_as_uint(__uint_as_float(x[r]) * (facs[c + r] * (z < parts ? fv : 1.f)));
                 tmem_stn<W>(at, x);
               }
             }
@@ -883,7 +902,7 @@ __global__ void __launch_bounds__(512, 1)
           for (int r = 0; r < RV; ++r) l[r] *= facs[r];
           return true;
         };
-        bool moves = s == 0 || (!cached && vref != 1.f), vote = !moves;
+        bool moves = s == 0, vote = !moves;
         const uint32_t pbuf = sbase + C::OFF_P + (t * C::NP + (C::NP == 2 ? (g & 1) : 0)) * C::PBYTES;
         for (;;) {
           if (moves && !move()) return false;
@@ -1032,7 +1051,7 @@ __global__ void __launch_bounds__(512, 1)
         }
         // rows [ra, rb), four at a time: in a join each lane takes half of them
         const int half = (rows + 7) / 8 * 4, ra = join ? t * half : 0, rb = join && t == 0 ? half : rows;
-        const float v0 = vrefs[join ? 0 : t], v1 = join ? vrefs[1] : 0.f;
+        const float v0 = vrefs[0], v1 = vrefs[1];
         auto o_free = [&] {  // O is in registers: the issuers may write it again
           tc_fence_before();
           __syncwarp();
@@ -1055,7 +1074,7 @@ __global__ void __launch_bounds__(512, 1)
           }
           float f0 = ex2_approx(m0 - m), f1 = ex2_approx(m1 - m);
           const float sum = l0 * f0 + l1 * f1, inv = sum != 0.f ? 1.f / sum : 0.f;  // 0: no key; NaN stays NaN
-          f0 *= inv * v0, f1 *= inv * v1;
+          f0 *= inv, f1 *= inv;
           const int tok = qr[rr].tok;
           const long long token = qr[rr].to & 0xffffffffffll, head = qr[rr].to >> 40;
           if (wq == 0 && lane < 4 && rr < rb && tok >= 0) {
@@ -1070,22 +1089,23 @@ __global__ void __launch_bounds__(512, 1)
           if (key < D) {
 #pragma unroll 1
             for (int u = 0; u < 1 + join; ++u) {
-              uint32_t x[C::PPARTS][4];
-              const uint32_t at = tmem + tlane + C::tm_o(join ? u : t) + r0;
-              // (tiles of new tokens alone write the first part's columns only)
-              const bool parts = it.j0 + (dual ? (join ? u : t) : 0) < it.nc;
+              uint32_t x[C::PPARTS][4], y[4];
+              const int of = join ? u : t, first = it.j0 + (dual ? of : 0), last = dual ? it.j0 + it.cnt - 1 - ((it.cnt - 1 - of) & 1)
+                                                                                     : it.j0 + steps - 1;
+              const bool old = first < it.nc, fresh = last >= it.nc;  // that lane's tiles: cached ones, new ones
+              const float v = of ? v1 : v0;
 #pragma unroll
-              for (int z = 0; z < C::PPARTS; ++z) tmem_ldn<4>(at + z * R, x[z]);
+              for (int z = 0; z < C::PPARTS; ++z) tmem_ldn<4>(tmem + tlane + C::tm_o(of) + r0 + z * R, x[z]);
+              tmem_ldn<4>(tmem + tlane + C::tm_n(of) + r0, y);
               tmem_wait_ld();
 #pragma unroll
               for (int r = 0; r < 4; ++r) {
-                float v = __uint_as_float(x[0][r]);
-                if (parts) {
-                  float low = __uint_as_float(x[2][r]);
-                  if (F16) low += __uint_as_float(x[C::PPARTS - 1][r]);
-                  v = fmaf(low, 0.015625f, v + __uint_as_float(x[1][r]));
-                }
-                o[r] = fmaf(v, __shfl_sync(0xffffffffu, u ? f1 : f0, r), o[r]);
+                float low = __uint_as_float(x[2][r]);
+                if (F16) low += __uint_as_float(x[C::PPARTS - 1][r]);
+                low = fmaf(low, 0.015625f, __uint_as_float(x[0][r]) + __uint_as_float(x[1][r]));
+                // (what was never written is not looked at)
+                const float all = (old ? low * v : 0.f) + (fresh ? __uint_as_float(y[r]) : 0.f);
+                o[r] = fmaf(all, __shfl_sync(0xffffffffu, u ? f1 : f0, r), o[r]);
               }
             }
           }
