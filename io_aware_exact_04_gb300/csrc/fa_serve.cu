@@ -76,6 +76,9 @@ struct ServeCfg {
   static constexpr int NSUB = D / 64;
   static constexpr int SUB_BYTES = 128 * 128, Q_BYTES = NSUB * SUB_BYTES;
   static constexpr int TK = C8 ? 64 : 128, TK_LOG2 = C8 ? 6 : 7;  // keys of a tile
+  // what an item's start and end cost, in tiles, as the runs are balanced (an item's change of 15000 cycles stands beside
+  // 1200 to 1900 a tile with C8)
+  static constexpr int ITEM_TILES = C8 ? 10 : 0;
   static constexpr int KSUB_BYTES = TK * 128, TILE_BYTES = NSUB * KSUB_BYTES;
   static constexpr int NSLOT = C8 ? (D == 64 ? 10 : 6) : D == 64 ? 12 : 5;
   static constexpr int STAGE = TK * D, NS8 = C8 ? (D == 64 ? 12 : 6) : 0;  // pages of 8 bits
@@ -146,7 +149,7 @@ struct SeqWork {
   int row0, n, L, nc, nk, units;
   long long tiles;  // all heads and units, each counted with the nk tiles of the last one
 };
-template <bool PAGED, int TL>
+template <bool PAGED, int TL, int EX>
 __device__ __forceinline__ SeqWork seq_sizes(const ServeArgs& a, int lo, int hi, int len, int unit, bool record) {
   SeqWork w;
   w.row0 = min(max(lo, 0), a.T);
@@ -161,12 +164,12 @@ __device__ __forceinline__ SeqWork seq_sizes(const ServeArgs& a, int lo, int hi,
   w.nc = (w.L + (1 << TL) - 1) >> TL;
   w.nk = w.nc + ((w.n + (1 << TL) - 1) >> TL);
   w.units = (w.n + unit - 1) / unit;
-  w.tiles = (long long)w.units * a.Hkv * w.nk;
+  w.tiles = (long long)w.units * a.Hkv * (w.nk + EX);
   return w;
 }
-template <bool PAGED, int TL>
+template <bool PAGED, int TL, int EX>
 __device__ __forceinline__ SeqWork seq_work(const ServeArgs& a, int b, int unit, bool record) {
-  return seq_sizes<PAGED, TL>(a, a.cu[b], a.cu[b + 1], PAGED ? a.lens[b] : 0, unit, record);
+  return seq_sizes<PAGED, TL, EX>(a, a.cu[b], a.cu[b + 1], PAGED ? a.lens[b] : 0, unit, record);
 }
 
 __device__ __forceinline__ long long warp_sum(long long x) {
@@ -184,7 +187,7 @@ struct ServeRuns {
   int chunk;
   __device__ long long start(int c) const { return base * c + min(c, rest); }
 };
-template <int TL>
+template <int TL, int EX>
 __device__ __forceinline__ ServeRuns serve_runs(const ServeArgs& a, int unit, int grid, bool record) {
   ServeRuns r;
   const int lane = threadIdx.x & 31;
@@ -199,7 +202,7 @@ __device__ __forceinline__ ServeRuns serve_runs(const ServeArgs& a, int unit, in
     for (int k = 0; k < 4; ++k) len[k] = a.lens[min(b + k, end - 1)];
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      if (b + k < end) r.mine += seq_sizes<true, TL>(a, at[k], at[k + 1], len[k], unit, record).tiles;
+      if (b + k < end) r.mine += seq_sizes<true, TL, EX>(a, at[k], at[k + 1], len[k], unit, record).tiles;
   }
   r.total = warp_sum(r.mine);
   r.ctas = r.total < (long long)grid * kMinTiles ? max(1, ((int)r.total + kMinTiles - 1) / kMinTiles) : grid;
@@ -221,7 +224,7 @@ __device__ __forceinline__ int lane_of(long long mine, long long pos, long long*
   return k;
 }
 // The sequence that tile `pos` of all belongs to, and its first tile; by a whole warp. pos < total.
-template <int TL>
+template <int TL, int EX>
 __device__ __forceinline__ int serve_seek(const ServeArgs& a, int unit, const ServeRuns& runs, long long pos,
                                           long long* first) {
   *first = 0;
@@ -231,7 +234,7 @@ __device__ __forceinline__ int serve_seek(const ServeArgs& a, int unit, const Se
   const int end = min(a.B, (k + 1) * runs.chunk);
   for (int b0 = k * runs.chunk; b0 < end; b0 += 32) {
     const int b = b0 + (threadIdx.x & 31);
-    const int x = lane_of(b < end ? seq_work<true, TL>(a, b, unit, false).tiles : 0, pos, first);
+    const int x = lane_of(b < end ? seq_work<true, TL, EX>(a, b, unit, false).tiles : 0, pos, first);
     if (x < 32) return b0 + x;
   }
   return a.B;
@@ -262,7 +265,7 @@ __device__ __forceinline__ int prompt_unit(const ServeArgs& a, int npt, int grid
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       if (b0 + 32 * k >= a.B) break;
-      const SeqWork w = seq_sizes<false, 7>(a, lo[k], hi[k], 0, 2 * npt, record);
+      const SeqWork w = seq_sizes<false, 7, 0>(a, lo[k], hi[k], 0, 2 * npt, record);
       tiles += (w.tiles + (long long)w.units * a.Hkv) / 2;  // item p of a sequence has about (p + 1) nk / units
       longest = max(longest, w.nk);
     }
@@ -304,7 +307,7 @@ struct PromptItems {
   }
   __device__ int units(int from) const {
     const int b = from + (threadIdx.x & 31);
-    return b < a.B ? seq_work<false, 7>(a, b, unit, false).units : 0;
+    return b < a.B ? seq_work<false, 7, 0>(a, b, unit, false).units : 0;
   }
   __device__ int above(int l) const {  // items of that level and up
     int x = 0;
@@ -687,37 +690,40 @@ __global__ void __launch_bounds__(C8 ? 512 : 384, 1)
     ServeItem it;
     if (PAGED) {
       const int unit = 2 * npt;
-      const ServeRuns runs = serve_runs<C::TK_LOG2>(a, unit, gridDim.x, blockIdx.x == 0);
+      const ServeRuns runs = serve_runs<C::TK_LOG2, C::ITEM_TILES>(a, unit, gridDim.x, blockIdx.x == 0);
       int parts = 0;  // of the item that this CTA is the first to cut
       int4 cut = make_int4(0, 0, 0, 0);
       if ((int)blockIdx.x < runs.ctas && runs.total > 0) {
         long long pos = runs.start(blockIdx.x), first = 0;
         const long long end = runs.start(blockIdx.x + 1);
-        int b = serve_seek<C::TK_LOG2>(a, unit, runs, pos, &first);
+        int b = serve_seek<C::TK_LOG2, C::ITEM_TILES>(a, unit, runs, pos, &first);
         while (ok && pos < end) {
-          const SeqWork w = seq_work<PAGED, C::TK_LOG2>(a, b, unit, false);
-          // the first item may be cut; from then on they start with their first tile
+          const SeqWork w = seq_work<PAGED, C::TK_LOG2, C::ITEM_TILES>(a, b, unit, false);
+          // the first item may be cut; from then on they are met from their start
+          const int span = w.nk + C::ITEM_TILES;  // an item's share of the run: its costs, then its tiles
           const long long at = pos - first;
-          const int q = at < (1LL << 31) ? (int)at / max(w.nk, 1) : (int)(at / w.nk);
-          int p = q / a.Hkv, kvh = q - p * a.Hkv, j0 = (int)(at - (long long)q * w.nk);
+          const int q = at < (1LL << 31) ? (int)at / max(span, 1) : (int)(at / span);
+          int p = q / a.Hkv, kvh = q - p * a.Hkv, x0 = (int)(at - (long long)q * span);
           bool again = false;  // the last item was whole, and this one differs in its head only
           while (ok && pos < end && pos - first < w.tiles) {
-            const int j1 = (int)min((long long)w.nk, j0 + (end - pos));
+            const int x1 = (int)min((long long)span, x0 + (end - pos));
+            const int j0 = max(0, x0 - C::ITEM_TILES), j1 = max(0, x1 - C::ITEM_TILES);
             if (again && j1 == w.nk)
               it.kvh = kvh;
             else
               make_item(w, unit, kvh, p, j0, j1, &it);
-            if (j0 > 0 && it.cnt > 0 && runs.start(blockIdx.x - 1) <= pos - j0) {
+            const long long tile0 = pos - x0 + C::ITEM_TILES;  // the place of the item's first tile
+            if (j0 > 0 && it.cnt > 0 && runs.start(blockIdx.x - 1) <= tile0) {
               // (the first item only) how many CTAs, this one included, hold later parts of it
-              const long long end_of_item = pos + it.cnt_all - j0;
+              const long long end_of_item = tile0 + it.cnt_all;
               for (int k = blockIdx.x + lane; __any_sync(0xffffffffu, k < runs.ctas); k += 32)
                 parts += __popc(__ballot_sync(0xffffffffu, k < runs.ctas && runs.start(k) < end_of_item));
               cut = make_int4(it.n, it.row0, it.tok0, it.kvh);
             }
             if (it.cnt > 0) ok = run_item(it, b);
-            pos += j1 - j0;
+            pos += x1 - x0;
             again = j0 == 0 && j1 == w.nk;
-            j0 = 0;
+            x0 = 0;
             if (++kvh == a.Hkv) kvh = 0, ++p, again = false;
           }
           first += w.tiles;
@@ -737,7 +743,7 @@ __global__ void __launch_bounds__(C8 ? 512 : 384, 1)
         int b = 0, p = 0;
         if (i >= (long long)items_of.total * a.Hkv) break;  // later rounds lie past the end too
         items_of.find((int)(i / a.Hkv), &b, &p);
-        const SeqWork w = seq_work<PAGED, C::TK_LOG2>(a, b, unit, false);
+        const SeqWork w = seq_work<PAGED, C::TK_LOG2, C::ITEM_TILES>(a, b, unit, false);
         make_item(w, unit, (int)(i % a.Hkv), p, 0, w.nk, &it);
         ok = run_item(it, b);
       }
