@@ -38,18 +38,20 @@ struct RotaryArgs {
 };
 
 // ---------------------------------------------------------------------------------------------
-// A thread holds two chunks of 8 elements of a head row, chosen so that a rotation's pairs lie in one
-// thread: with halves, chunks p and p + dim / 16; behind the rotated part, neighbours.
+// A thread holds two chunks of 8 elements of a head row, chosen so that a rotation's pairs lie in one thread: with
+// halves, chunks p and p + dim / 16; behind the rotated part, the chunks of a row's two halves there. So the lanes of a
+// row load and store whole sectors.
 struct ChunkPair {
   int c0, c1;
   bool turned;
 };
+template <int LPR>  // lanes a row
 __device__ __forceinline__ ChunkPair chunk_pair(int p, int dim) {
   const int pairs = dim >> 4;
   ChunkPair c;
   c.turned = p < pairs;
-  c.c0 = c.turned ? p : 2 * p;
-  c.c1 = c.turned ? p + pairs : 2 * p + 1;
+  c.c0 = c.turned ? p : pairs + p;
+  c.c1 = c.turned ? p + pairs : LPR + p;
   return c;
 }
 
@@ -80,8 +82,7 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
 struct Turn {
   float c[8], s[8];
 };
-__device__ __forceinline__ void load_turn(const RotaryArgs& a, int position, const ChunkPair& cp, Turn* t) {
-  const float* row = a.angles + position * a.a_stride;
+__device__ __forceinline__ void load_turn(const RotaryArgs& a, const float* row, const ChunkPair& cp, Turn* t) {
   const int j0 = a.interleaved ? 4 * cp.c0 : 8 * cp.c0, j1 = a.interleaved ? 4 * cp.c1 : 8 * cp.c0 + 4;
   const float4 x0 = __ldg(reinterpret_cast<const float4*>(row + j0)), x1 = __ldg(reinterpret_cast<const float4*>(row + j1));
   row += a.dim >> 1;
@@ -133,9 +134,9 @@ __device__ __forceinline__ void rotate_rows(const RotaryArgs& a, int t, int spli
   const long long pos = (a.kc ? (long long)a.start[b] : 0) + i;
   const long long place = a.at ? a.at[t] : pos;
   if (place < 0 || place >= a.positions) return record_check(a.status, SITE_S_ANGLE);
-  const ChunkPair cp = chunk_pair(p, a.dim);
+  const ChunkPair cp = chunk_pair<LPR>(p, a.dim);
   Turn tn;
-  if (cp.turned) load_turn(a, (int)place, cp, &tn);
+  if (cp.turned) load_turn(a, a.angles + place * a.a_stride, cp, &tn);
   uint16_t *kc = nullptr, *vc = nullptr;
   if (KV && a.kc) {
     if (pos < 0 || pos >= (long long)a.table_width << a.page_shift) {
@@ -152,7 +153,7 @@ __device__ __forceinline__ void rotate_rows(const RotaryArgs& a, int t, int spli
     }
   }
   const int nq = a.q ? a.Hq : 0, keys = KV ? nq + a.Hkv : nq, all = KV && vc ? keys + a.Hkv : keys;
-  constexpr int U = 4;
+  constexpr int U = KV ? 4 : 2;
   for (int j0 = split * RPI; j0 < all; j0 += U * splits * RPI) {
     uint4 x[U], y[U];
 #pragma unroll
@@ -224,19 +225,42 @@ __device__ __forceinline__ int growth(float most, float scale) {
   split_float(scale, &s, &f);
   return e - f - 8 + (4 * m > 7 * s ? 1 : 8 * m <= 7 * s ? -1 : 0);
 }
+// The least k >= -118 with most <= 448 2^k, and 2^i for i in [-126, 127].
+__device__ __forceinline__ int growth_of_new(float most) {
+  const uint32_t u = __float_as_uint(most);
+  return max((int)(u >> 23) - 135 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0), -118);
+}
+__device__ __forceinline__ float pow2(int i) { return __uint_as_float((uint32_t)(i + 127) << 23); }
+// A block's scale, its reciprocal, and what multiplies the tokens that were there (1: they stay as they are).
+struct Rescale {
+  float now, inv, by;
+};
+// A kept scale that is no power of two: not this library's.
+__device__ __noinline__ Rescale rescale_any(float old, float most) {
+  const int k = most > 0.f ? max(growth(most, old), 0) : 0;
+  const float now = ldexpf(old, k);
+  return {now, 1.f / now, ldexpf(1.f, -k)};
+}
+// From the scale as it was (0, as any value that is no scale: none) and the largest magnitude of the new tokens.
+__device__ __forceinline__ Rescale rescale(float old, float most) {
+  const uint32_t u = __float_as_uint(old);
+  const int k = growth_of_new(most);
+  if (!(old >= FLT_MIN && old <= FLT_MAX)) return {pow2(k), pow2(-k), 1.f};
+  const int e = (int)(u >> 23) - 127;
+  if ((u & 0x7fffffu) || e < -118 || e > 120) return rescale_any(old, most);
+  const int now = max(e, k);
+  return {pow2(now), pow2(-now), pow2(max(e - now, -126))};  // (2^-126 already leaves nothing of an 8-bit value)
+}
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// Eight values times inv.
 __device__ __forceinline__ uint2 e4m3x8(const float (&x)[8], float inv) {
   uint32_t h[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    // an infinity would saturate: NaN, as the type has none
-    const float lo = fabsf(x[2 * i]) <= FLT_MAX ? x[2 * i] * inv : NAN, hi = fabsf(x[2 * i + 1]) <= FLT_MAX ? x[2 * i + 1] * inv : NAN;
-    h[i] = e4m3x2(lo, hi);
-  }
+  for (int i = 0; i < 4; ++i) h[i] = e4m3x2(x[2 * i] * inv, x[2 * i + 1] * inv);
   return make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
 }
 // Eight e4m3 values times a power of two, rounded again.
@@ -278,140 +302,215 @@ __device__ __forceinline__ int find_block(const RotaryArgs& a, long long u) {
   return (a.cu[lo] >> a.block_shift) + 2LL * lo <= u ? lo : -1;
 }
 
-// Into 8 bits. A team of block x D / 1024 warps takes one block of one head, of K or of V: a thread two
-// pairs of chunks, in registers from the load to the store, so that the block's largest magnitude is
-// known before anything is rounded and every row is read once. A CTA has as many teams as fit in eight
-// warps (one, where the block is larger), on heads that follow each other.
-template <int D, bool F16>
+// Into 8 bits: a block's share of the heads ("jobs"), of K or of V, by a team of warps each, one after the other. A thread
+// holds U pairs of chunks, in registers from the load to the store, so that the block's largest magnitude is known before
+// anything is rounded.
+//  - TEAM: block x D / (512 U) warps, all of the block at once: every row is read once. A CTA has as many teams as fit
+//    (one, where the block is large); the next job's rows are on their way while the last one's are rounded, and
+//    finding the sequence and the page, four loads in turn, is done once for all of them.
+//  - otherwise, where few tokens a sequence are appended: a warp, which goes over those parts of the block that
+//    have new tokens, twice where these are several (a CTA for each job, most of its threads idle: 64 sequences'
+//    next tokens took 11.7 us instead of 4.1).
+template <int D, bool F16, bool TEAM, int U>
 __device__ __forceinline__ void append_block(const RotaryArgs& a, long long unit) {
-  constexpr int LPR = D / 16, RPI = 32 / LPR;
-  __shared__ float warp_most[32];
+  constexpr int LPR = D / 16, RPI = 32 / LPR, TOKENS = U * RPI;  // lanes a row, rows at a time, tokens of a warp's part
+  __shared__ float warp_most[2][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int block = 1 << a.block_shift, wpt = block * D / 1024;
+  const int wpt = TEAM ? max(1, (D << a.block_shift) / (512 * U)) : 1, teams = (blockDim.x >> 5) / wpt;
   const int team = warp / wpt, w = warp - team * wpt;
   const long long slot = unit / a.head_groups;
-  const int job = (int)(unit - slot * a.head_groups) * max(1, 8 / wpt) + team;  // K of all heads, then V
-  const bool is_v = job >= a.Hkv;
-  const int h = is_v ? job - a.Hkv : job;
+  const int share = (int)(unit - slot * a.head_groups);
+  const bool is_v = share & 1;
   const int b = find_block(a, slot);
-  float f[2][2][8];
-  float most = 0.f;
-  bool fresh_token[2] = {false, false};
-  uint8_t* to = nullptr;
-  float* scale = nullptr;
-  int first = 0;  // the block's first new token
-  const ChunkPair cp = chunk_pair(lane % LPR, is_v ? 0 : a.dim);
-  const int place0 = w * 2 * RPI + lane / LPR;  // the thread's tokens in the block: this one and RPI behind it
-  if (b >= 0 && job < 2 * a.Hkv) {
-    const SeqRange r = seq_range(a.cu, b, a.T, a.status);
-    const long long start = a.start[b], end = start + (r.hi - r.lo);
-    const long long base = ((start >> a.block_shift) + (slot - ((a.cu[b] >> a.block_shift) + 2LL * b))) << a.block_shift;
-    if (r.hi > r.lo && base < end) {
-      int id = -1;
-      if (base < 0 || base >= (long long)a.table_width << a.page_shift) {
-        if (lane == 0) record_check(a.status, SITE_S_LENGTH);
-      } else {
-        id = a.table[b * a.table_stride + (base >> a.page_shift)];
-        if (id < 0 || id >= a.n_pages) {
-          if (lane == 0) record_check(a.status, SITE_S_PAGE);
-          id = -1;
-        }
-      }
-      const int in_page = (int)(base & ((1 << a.page_shift) - 1));
-      if (id >= 0) {
-        to = (is_v ? a.vc : a.kc) + id * a.c_sp + h * a.c_sh + in_page * a.c_st;
-        scale = (is_v ? a.vs : a.ks) + id * a.s_sp + h * a.s_sh + (in_page >> a.block_shift);
-      }
-      first = (int)max(0LL, start - base);
-      const int last = (int)min((long long)block, end - base);
-      uint4 x[2][2];
-      int place[2] = {0, 0};
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int i = place0 + u * RPI;
-        if (i < first || i >= last) continue;
-        const int t = (int)(r.lo + (base + i - start));
-        int row = t;
-        if (a.rows) {
-          row = a.rows[t];
-          if (row < 0 || row >= a.Tkv) {
-            record_check(a.status, SITE_S_ROW);
-            continue;
-          }
-        }
-        if (a.angles) {
-          const long long p = a.at ? a.at[t] : base + i;
-          if (p < 0 || p >= a.positions) {
-            record_check(a.status, SITE_S_ANGLE);
-            continue;
-          }
-          place[u] = (int)p;
-        }
-        fresh_token[u] = true;
-        const uint16_t* from = is_v ? a.v + row * a.v_st + h * a.v_sh : a.k + row * a.k_st + h * a.k_sh;
-        x[u][0] = *reinterpret_cast<const uint4*>(from + 8 * cp.c0);
-        x[u][1] = *reinterpret_cast<const uint4*>(from + 8 * cp.c1);
-      }
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        if (!fresh_token[u]) continue;
-        unpack8<F16>(x[u][0], f[u][0]);
-        unpack8<F16>(x[u][1], f[u][1]);
-        if (!is_v && a.angles && cp.turned) {
-          Turn tn;
-          load_turn(a, place[u], cp, &tn);
-          turn(f[u][0], f[u][1], tn, a.interleaved);
-        }
-        if (!is_v && a.ko) {
-          uint16_t* ko = a.ko + (r.lo + (base + place0 + u * RPI - start)) * a.ko_st + h * a.ko_sh;
-          *reinterpret_cast<uint4*>(ko + 8 * cp.c0) = pack8<F16>(f[u][0]);
-          *reinterpret_cast<uint4*>(ko + 8 * cp.c1) = pack8<F16>(f[u][1]);
-        }
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (const float m = fabsf(f[u][c][e]); m <= FLT_MAX) most = fmaxf(most, m);
-      }
+  if (b < 0) return;
+  const SeqRange r = seq_range(a.cu, b, a.T, a.status);
+  const long long start = a.start[b], end = start + (r.hi - r.lo);
+  const int block = 1 << a.block_shift;
+  const long long base = ((start >> a.block_shift) + (slot - ((a.cu[b] >> a.block_shift) + 2LL * b))) << a.block_shift;
+  if (r.hi <= r.lo || base >= end) return;
+  int id = -1;
+  if (base < 0 || base >= (long long)a.table_width << a.page_shift) {
+    if (lane == 0) record_check(a.status, SITE_S_LENGTH);
+  } else {
+    id = a.table[b * a.table_stride + (base >> a.page_shift)];
+    if (id < 0 || id >= a.n_pages) {
+      if (lane == 0) record_check(a.status, SITE_S_PAGE);
+      id = -1;
     }
   }
-  float old = 0.f;
-  if (scale && first > 0) old = *scale;
-  most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)));
-  if (lane == 0) warp_most[warp] = most;
-  __syncthreads();
-  if (!scale) return;
-  for (int k = 0; k < wpt; ++k) most = fmaxf(most, warp_most[team * wpt + k]);
-  const bool keeps = old >= FLT_MIN && old <= FLT_MAX;
-  int k = most > 0.f ? growth(most, keeps ? old : 1.f) : -118;
-  k = max(k, keeps ? 0 : -118);
-  const float now = ldexpf(keeps ? old : 1.f, k), inv = 1.f / now;
-  if (w == 0 && lane == 0) *scale = now;
+  const bool puts = !is_v && a.ko, turns = !is_v && a.angles;
+  if (id < 0 && !puts) return;
+  const int in_page = (int)(base & ((1 << a.page_shift) - 1));
+  const int first = (int)max(0LL, start - base), last = (int)min((long long)block, end - base);  // the block's new tokens
+  const ChunkPair cp = chunk_pair<LPR>(lane % LPR, is_v ? 0 : a.dim);
+  uint8_t* const pages = (is_v ? a.vc : a.kc) + id * a.c_sp + in_page * a.c_st;
+  float* const scales = (is_v ? a.vs : a.ks) + id * a.s_sp + (in_page >> a.block_shift);
+  const long long row_sh = is_v ? a.v_sh : a.k_sh;
+  // part `sub`: the thread's rows in head 0 (null: none), their angles, and where the rotated keys go
+  const uint16_t* from[U];
+  const float* angle[U];
+  uint16_t* ko[U];
+  auto find_rows = [&](int sub) {
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const int i = place0 + u * RPI;
-    uint8_t* row = to + i * a.c_st;
-    if (fresh_token[u]) {
-      *reinterpret_cast<uint2*>(row + 8 * cp.c0) = e4m3x8(f[u][0], inv);
-      *reinterpret_cast<uint2*>(row + 8 * cp.c1) = e4m3x8(f[u][1], inv);
-    } else if (i < first && keeps && k > 0) {
-      const float by = ldexpf(1.f, -k);
+    for (int u = 0; u < U; ++u) {
+      const int i = sub * TOKENS + u * RPI + lane / LPR;
+      from[u] = nullptr;
+      if (i < first || i >= last) continue;
+      const int t = (int)(r.lo + (base + i - start));
+      int row = t;
+      if (a.rows) {
+        row = a.rows[t];
+        if (row < 0 || row >= a.Tkv) {
+          record_check(a.status, SITE_S_ROW);
+          continue;
+        }
+      }
+      if (a.angles) {
+        const long long p = a.at ? a.at[t] : base + i;
+        if (p < 0 || p >= a.positions) {
+          record_check(a.status, SITE_S_ANGLE);
+          continue;
+        }
+        angle[u] = a.angles + p * a.a_stride;
+      }
+      from[u] = is_v ? a.v + row * a.v_st : a.k + row * a.k_st;
+      if (puts) ko[u] = a.ko + t * a.ko_st;
+    }
+  };
+  auto load = [&](int h, uint4 (&to)[U][2]) {
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint2* at = reinterpret_cast<uint2*>(row + 8 * (c ? cp.c1 : cp.c0));
-        *at = e4m3x8_scaled(*at, by);
+    for (int u = 0; u < U; ++u) {
+      if (!from[u]) continue;
+      const uint16_t* row = from[u] + h * row_sh;
+      to[u][0] = *reinterpret_cast<const uint4*>(row + 8 * cp.c0);
+      to[u][1] = *reinterpret_cast<const uint4*>(row + 8 * cp.c1);
+    }
+  };
+  // The values of loaded rows, and the largest finite magnitude of the warp's part; the rotated keys go out (put).
+  float f[U][2][8];
+  auto values = [&](int h, const uint4 (&x)[U][2], bool put) {
+    float most = 0.f;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (!from[u]) continue;
+      unpack8<F16>(x[u][0], f[u][0]);
+      unpack8<F16>(x[u][1], f[u][1]);
+      if (turns && cp.turned) {
+        Turn tn;
+        load_turn(a, angle[u], cp, &tn);
+        turn(f[u][0], f[u][1], tn, a.interleaved);
+      }
+      if (put && puts) {
+        uint16_t* row = ko[u] + h * a.ko_sh;
+        *reinterpret_cast<uint4*>(row + 8 * cp.c0) = pack8<F16>(f[u][0]);
+        *reinterpret_cast<uint4*>(row + 8 * cp.c1) = pack8<F16>(f[u][1]);
+      }
+#pragma unroll
+      for (int e = 0; e < 16; ++e) most = fmaxf(most, fabsf(f[u][e >> 3][e & 7]));  // (a NaN is never the larger one)
+    }
+    most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)));
+    if (most > FLT_MAX) {  // rare: infinities would saturate, and become NaN, as the type has none
+      most = 0.f;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (!from[u]) continue;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          float& x = f[u][e >> 3][e & 7];
+          if (fabsf(x) > FLT_MAX) x = NAN;
+          most = fmaxf(most, fabsf(x));
+        }
+      }
+      most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)));
+    }
+    return most;
+  };
+  auto scale_of = [&](int h) { return first > 0 && id >= 0 ? scales[h * a.s_sh] : 0.f; };
+  Rescale z;
+  auto store = [&](int h, int sub) {
+    uint8_t* to = pages + h * a.c_sh + (sub * TOKENS + lane / LPR) * a.c_st;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (!from[u]) continue;
+      uint8_t* at = to + u * RPI * a.c_st;
+      *reinterpret_cast<uint2*>(at + 8 * cp.c0) = e4m3x8(f[u][0], z.inv);
+      *reinterpret_cast<uint2*>(at + 8 * cp.c1) = e4m3x8(f[u][1], z.inv);
+    }
+  };
+  auto restate = [&](int h, int sub) {  // the tokens that were there, as their scale grows
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = sub * TOKENS + u * RPI + lane / LPR;
+      if (i >= first) continue;
+      uint4* at = reinterpret_cast<uint4*>(pages + h * a.c_sh + i * a.c_st) + lane % LPR;
+      const uint4 v = *at;
+      const uint2 lo = e4m3x8_scaled(make_uint2(v.x, v.y), z.by), hi = e4m3x8_scaled(make_uint2(v.z, v.w), z.by);
+      *at = make_uint4(lo.x, lo.y, hi.x, hi.y);
+    }
+  };
+  const int h0 = (share >> 1) * teams + team, step = (a.head_groups >> 1) * teams;
+  if (TEAM) {
+    find_rows(w);
+    uint4 next[U][2];
+    if (h0 < a.Hkv) load(h0, next);
+    // (the same number of rounds for all teams of the CTA: they meet)
+    for (int n = 0, h = h0; h - team < a.Hkv; ++n, h += step) {
+      const bool mine = h < a.Hkv;
+      float old = 0.f, most = 0.f;
+      if (mine) {
+        old = scale_of(h);
+        most = values(h, next, true);
+        if (h + step < a.Hkv) load(h + step, next);
+      }
+      if (lane == 0) warp_most[n & 1][warp] = most;
+      __syncthreads();
+      if (!mine || id < 0) continue;
+      most = warp_most[n & 1][team * wpt + min(lane, wpt - 1)];
+      z = rescale(old, __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most))));
+      if (w == 0 && lane == 0) scales[h * a.s_sh] = z.now;
+      store(h, w);
+      if (z.by < 1.f) restate(h, w);
+    }
+  } else {
+    const int sub0 = first / TOKENS, sub1 = (last - 1) / TOKENS;
+    const bool twice = sub0 != sub1;  // the rows are read again, so that the rotated keys, which may take their place, go out then
+    uint4 x[U][2];
+    for (int h = h0; h < a.Hkv; h += step) {
+      const float old = scale_of(h);
+      float most = 0.f;
+      for (int pass = 0; pass < 2; ++pass) {
+        for (int sub = sub0; sub <= sub1; ++sub) {
+          if (pass == 0 || twice) {
+            find_rows(sub);
+            load(h, x);
+            most = fmaxf(most, values(h, x, pass == (twice ? 1 : 0)));
+          }
+          if (pass == 1 && id >= 0) store(h, sub);
+        }
+        if (pass == 0) {
+          if (id < 0 && !twice) break;
+          z = rescale(old, most);
+          __syncwarp();  // (every lane has read the scale)
+          if (lane == 0 && id >= 0) scales[h * a.s_sh] = z.now;
+          for (int sub = 0; z.by < 1.f && sub * TOKENS < first; ++sub) restate(h, sub);
+        }
       }
     }
   }
 }
 
-template <int D, bool F16, int THREADS>
-__global__ void __launch_bounds__(THREADS) append_8bit_kernel(RotaryArgs a) {
+// U = 0: a warp a job. Two CTAs an SM where the registers allow it: what a round waits for (rows, the team's other warps)
+// needs warps, and its instructions, some 300 a warp, are next to the bytes what a long append is bound by. 8192 prompt
+// tokens of 8 heads (d = 128, blocks of 64): 29 us, of 14 for the bytes; with 32 query heads turned too 69 of 54
+// (5.4 TB/s). One CTA an SM: 96 with the queries; threads of two rows, fewer warps: 78. 64 sequences' next tokens:
+// 4.1 us in a graph (one CTA an SM 5.4, three with spilled registers 6.0).
+template <int D, bool F16, int U, int THREADS>
+__global__ void __launch_bounds__(THREADS, U <= 1 ? 2 : 1) append_8bit_kernel(RotaryArgs a) {
   griddep_wait();
   griddep_launch_dependents();
   if (blockIdx.x == 0) check_offsets(a.cu, a.B, a.T, a.status);
   if (blockIdx.x < a.blocks8) {
-    append_block<D, F16>(a, blockIdx.x);
+    append_block<D, F16, U != 0, U ? U : 2>(a, blockIdx.x);
   } else {
     const long long w = (blockIdx.x - a.blocks8) * (blockDim.x >> 5) + (threadIdx.x >> 5);
     const int t = (int)(w / a.splits), split = (int)(w - (long long)t * a.splits);
@@ -435,13 +534,20 @@ static int launch_rotary_d(RotaryArgs a, cudaStream_t stream) {
     if (grid > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
     return launch_pdl("rotary_rows_kernel", rotary_rows_kernel<D, F16>, dim3((unsigned)grid), dim3(128), 0, stream, a);
   }
-  const int wpt = (D << a.block_shift) / 1024, threads = 32 * std::max(8, wpt), teams = std::max(1, 8 / wpt);
-  a.head_groups = (2 * a.Hkv + teams - 1) / teams;
-  a.blocks8 = (((long long)a.T >> a.block_shift) + 2LL * a.B) * a.head_groups;
+  // a warp a job where few tokens a sequence come in, else teams, of which a CTA takes as many jobs in turn as make one
+  // wave of two CTAs an SM
+  const bool few = a.T <= 16LL * a.B;
+  const int pairs = (D << a.block_shift) / 512;  // warps of a team with U = 1
+  const int wpt = few ? 1 : pairs <= 16 ? pairs : pairs / 2, threads = 32 * std::max(few ? 8 : 16, wpt), teams = threads / 32 / wpt;
+  const long long slots = ((long long)a.T >> a.block_shift) + 2LL * a.B;
+  const int rounds = (a.Hkv + teams - 1) / teams;
+  a.head_groups = 2 * (few ? rounds : (int)std::min<long long>(rounds, std::max<long long>(1, (long long)sms / slots)));
+  a.blocks8 = slots * a.head_groups;
   const long long grid = a.blocks8 + (a.q ? (warps + threads / 32 - 1) / (threads / 32) : 0);
   if (grid > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
-  const auto kernel = threads <= 256 ? append_8bit_kernel<D, F16, 256>
-                                     : threads <= 512 ? append_8bit_kernel<D, F16, 512> : append_8bit_kernel<D, F16, 1024>;
+  const auto kernel = few ? append_8bit_kernel<D, F16, 0, 256>
+                          : pairs <= 16 ? append_8bit_kernel<D, F16, 1, 512>
+                          : wpt <= 16 ? append_8bit_kernel<D, F16, 2, 512> : append_8bit_kernel<D, F16, 2, 1024>;
   return launch_pdl("append_8bit_kernel", kernel, dim3((unsigned)grid), dim3(threads), 0, stream, a);
 }
 
