@@ -51,26 +51,26 @@ namespace fa {
 // first tile of an item, and where some score passes the reference by more than it may. A vote of the four
 // warps says so, taken while P is formed as if nothing moved (with four warps in step, latency bounds a
 // tile: a wait costs 100 to 200 cycles, also where its phase has completed). S has two buffers, so that the next one is
-// formed meanwhile, and so has P with lanes of 16 rows. Rows come in classes of 4, 8, 16 (or 16, 32): the
-// columns of others are never looked at, and what stands in them stays in them.
-template <int D, int R, bool F16>
+// formed meanwhile, and so has P. Rows come in classes of 4, 8 and 16: the columns of others are never looked at, and
+// what stands in them stays in them.
+template <int D, bool F16>
 struct Serve8Cfg {
+  static constexpr int R = 16;                       // rows of a lane
   static constexpr int ROW = D;                      // bytes of a cached row
   static constexpr int KV = 128 * ROW, ENTRY = 2 * KV;
   static constexpr int NEW = 64;                     // keys of a tile of new tokens
   static constexpr int NSUB = D / 64;                // 64-column halves of their rows
   static constexpr int QPARTS = F16 ? 3 : 2;
   static constexpr int Q16 = QPARTS * R * D, QSLOT = Q16 + R * D * 2;
-  static constexpr int NQ = R == 16 ? 4 : 3;
+  static constexpr int NQ = 4;                       // slots of Q
   static constexpr int PPARTS = F16 ? 4 : 3;
-  static constexpr int PX = 4 * R;                   // P: bytes of a key's row, [p1 | p2 | p3 | p4] of R bytes each
-  static constexpr int NP = R == 16 ? 2 : 1;         // buffers of P
+  static constexpr int PX = 4 * R;                   // P: bytes of a key's row, [p1 | p2 | p3 | p4] of R bytes each; two buffers a lane
   static constexpr int PBYTES = 128 * PX;
   static constexpr int QROW = 16;                    // of a row of Q: factor of its scores, token, place in O (8 bytes)
   static constexpr int MISC = 512 + 256 + 12 * 64 + NQ * R * QROW + 2 * (2 * R + R + R + 4 * R + 4 * (R + 4)) * 4 + 64;
-  static constexpr int FIXED = 2 * NP * PBYTES + NQ * QSLOT + MISC;
+  static constexpr int FIXED = 4 * PBYTES + NQ * QSLOT + MISC;
   static constexpr int NT = (232448 - FIXED) / ENTRY < 12 ? (232448 - FIXED) / ENTRY : 12;
-  static constexpr int OFF_P = NT * ENTRY, OFF_Q = OFF_P + 2 * NP * PBYTES, OFF_BAR = OFF_Q + NQ * QSLOT;
+  static constexpr int OFF_P = NT * ENTRY, OFF_Q = OFF_P + 4 * PBYTES, OFF_BAR = OFF_Q + NQ * QSLOT;
   static constexpr int OFF_DESC = OFF_BAR + 512, OFF_SC = OFF_DESC + 256, OFF_QROW = OFF_SC + 12 * 64;
   // of each lane: factor of each row's scores and 11 - its reference, factors of a move; of the item before: reference,
   // sums of each warp
@@ -81,7 +81,7 @@ struct Serve8Cfg {
   __device__ static constexpr uint32_t tm_o(int t) { return 8u * R + 4u * R * t; }
   __device__ static constexpr uint32_t tm_n(int t) { return 16u * R + R * t; }  // O of the new tokens
   static constexpr uint32_t TM_COLS = 512;
-  static_assert(18 * R <= 512, "tensor memory");
+  static_assert(18 * R <= TM_COLS, "tensor memory");
   static constexpr int THREADS = 512, PRODUCER = 8, S_BOTH = 9, PV0 = 10, PV1 = 11, SPLIT = 12, LOAD_V = 14, SCALES = 15;
   // barriers
   static constexpr int FULL = 0, EMPTY = NT, Q_FULL = 2 * NT, Q_EMPTY = Q_FULL + NQ, S_FULL = Q_EMPTY + NQ, S_FREE = S_FULL + 4,
@@ -280,10 +280,8 @@ __device__ __forceinline__ void halves(uint32_t w, float& lo, float& hi) {
 // N columns of the warp's 32 lanes.
 template <int N>
 __device__ __forceinline__ void tmem_ldn(uint32_t taddr, uint32_t (&r)[N]) {
-  static_assert(N == 2 || N == 4 || N == 8 || N == 16, "");
-  if constexpr (N == 2)
-    tmem_ld2(taddr, r);
-  else if constexpr (N == 4)
+  static_assert(N == 4 || N == 8 || N == 16, "");
+  if constexpr (N == 4)
     tmem_ld4(taddr, r);
   else if constexpr (N == 8)
     tmem_ld8(taddr, r);
@@ -309,11 +307,12 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
   return F16 ? pack_f16x2(lo, hi) : pack_bf16x2(lo, hi);
 }
 
-template <int D, int R, bool F16>
+template <int D, bool F16>
 __global__ void __launch_bounds__(512, 1)
     serve8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                   const __grid_constant__ CUtensorMap tm_kc, const __grid_constant__ CUtensorMap tm_vc, Serve8BitArgs a) {
-  using C = Serve8Cfg<D, R, F16>;
+  using C = Serve8Cfg<D, F16>;
+  constexpr int R = C::R;
   constexpr int NT = C::NT, NQ = C::NQ;
   // 1024-byte aligned, as the swizzled tiles have to be: there is no room to round the address up
   extern __shared__ __align__(1024) uint8_t sm[];
@@ -702,7 +701,7 @@ __global__ void __launch_bounds__(512, 1)
       constexpr uint32_t I8 = idesc_e4m3_f32(128, C::PPARTS * R, 1, 1) | 1u << 16;
       constexpr uint32_t I16 = F16 ? idesc_f16_f32(128, R, 1, 1) : idesc_bf16_f32(128, R, 1, 1);
       constexpr uint32_t HIV = desc_hi<C::ROW>(), HIP = desc_hi<C::PX>(), HI16 = sdesc_hi(1024);
-      const uint32_t d = tmem + C::tm_o(t), p_lo = sdesc_lo(sbase + C::OFF_P + t * C::NP * C::PBYTES, 8192);
+      const uint32_t d = tmem + C::tm_o(t), p_lo = sdesc_lo(sbase + C::OFF_P + t * 2 * C::PBYTES, 8192);
       const uint32_t v_lo = sdesc_lo(sbase + C::KV, 8192);
       int g = 0, items = 0;
       for (int i = 0; ok; ++i) {
@@ -734,7 +733,7 @@ __global__ void __launch_bounds__(512, 1)
           if (!(ok = wait_phase(BAR(C::P_READY + 2 * t + (g & 1)), (g >> 1) & 1, st, SITE_T8_P_READY))) break;
           if (first && items > 0 && !(ok = wait_phase(BAR(C::O_FREE + t), (items - 1) & 1, st, SITE_T8_O_FREE))) break;
           tc_fence_after();
-          const uint32_t va = v_lo + s * (C::ENTRY >> 4), pa = p_lo + (C::NP == 2 ? (g & 1) * (C::PBYTES >> 4) : 0);
+          const uint32_t va = v_lo + s * (C::ENTRY >> 4), pa = p_lo + (g & 1) * (C::PBYTES >> 4);
           if (elect_one()) {
             if (cached) {
 #pragma unroll
@@ -789,7 +788,7 @@ __global__ void __launch_bounds__(512, 1)
     };
     // One item, for lanes of which the first RV rows matter
     auto run_item = [&](const Item8& it, auto rv) {
-      constexpr int RV = decltype(rv)::value, W = RV < 16 ? RV : 16;  // rows, and rows at a time
+      constexpr int RV = decltype(rv)::value;
       const bool dual = it.flags & ITEM8_DUAL;
       const int slot = (uq + (dual ? 0 : t)) % NQ, steps = t ? it.c1 : it.c0;
       const QRow* qr = qrows + slot * R;
@@ -804,9 +803,9 @@ __global__ void __launch_bounds__(512, 1)
         constexpr bool cached = decltype(of_cache)::value;
         const int j = it.j0 + ahead + s * stride;
         // S is there, and P of the tile that had its buffer before has been read
-        const uint32_t s_bar = BAR(C::S_FULL + 2 * t + (g & 1)), p_bar = BAR(C::O_DONE + 2 * t + ((g - C::NP) & 1));
-        const uint32_t s_ph = (g >> 1) & 1, p_ph = ((g - C::NP) >> 1) & 1;
-        if (g < C::NP) {
+        const uint32_t s_bar = BAR(C::S_FULL + 2 * t + (g & 1)), p_bar = BAR(C::O_DONE + 2 * t + (g & 1));
+        const uint32_t s_ph = (g >> 1) & 1, p_ph = s_ph ^ 1;
+        if (g < 2) {
           if (!wait_phase(s_bar, s_ph, st, SITE_T8_S_FULL)) return false;
         } else if (!__all_sync(0xffffffffu, mbar_try_wait(s_bar, s_ph) && mbar_try_wait(p_bar, p_ph))) {
           if (!wait_slow(s_bar, s_ph, st, SITE_T8_S_FULL) || !wait_slow(p_bar, p_ph, st, SITE_T8_O_DONE)) return false;
@@ -830,31 +829,28 @@ __global__ void __launch_bounds__(512, 1)
             seen |= (uint32_t)sees << r;
           }
         }
-        // rows [c, c + W): scores to base 2 without their rows' factors
-        auto load_y = [&](int c, float (&y)[W]) {
-          uint32_t x0[W], x1[W];
-          tmem_ldn<W>(ts + c, x0);
-          if (cached) tmem_ldn<W>(ts + R + c, x1);
+        // scores to base 2 without their rows' factors
+        auto load_y = [&](float (&y)[RV]) {
+          uint32_t x0[RV], x1[RV];
+          tmem_ldn<RV>(ts, x0);
+          if (cached) tmem_ldn<RV>(ts + R, x1);
           tmem_wait_ld();
           const float k16 = kscale * 0.0625f;
 #pragma unroll
-          for (int r = 0; r < W; ++r)
+          for (int r = 0; r < RV; ++r)
             y[r] = cached ? fmaf(__uint_as_float(x1[r]), k16, __uint_as_float(x0[r]) * kscale) : __uint_as_float(x0[r]);
         };
         // References move: for the first tile, or where a score or a scale has passed its own.
         auto move = [&] {
-#pragma unroll 1
-          for (int c = 0; c < RV; c += W) {
-            float y[W], mine = 0.f;
-            load_y(c, y);
+          float y[RV], mine = 0.f;
+          load_y(y);
 #pragma unroll
-            for (int r = 0; r < W; ++r) {
-              const float f = cached ? qr[c + r].factor : a.scale_log2;
-              const float m = warp_max((seen >> (c + r) & 1) ? y[r] * f : -INFINITY);
-              if (lane == r) mine = m;
-            }
-            if (lane < W) red[wq * (R + 4) + c + lane] = mine;
+          for (int r = 0; r < RV; ++r) {
+            const float f = cached ? qr[r].factor : a.scale_log2;
+            const float m = warp_max((seen >> r & 1) ? y[r] * f : -INFINITY);
+            if (lane == r) mine = m;
           }
+          if (lane < RV) red[wq * (R + 4) + lane] = mine;
           const float vm = warp_max(there && cached ? vscale : 0.f);
           if (lane == 0) red[wq * (R + 4) + R] = vm;
           if (!meet()) return false;
@@ -885,16 +881,13 @@ __global__ void __launch_bounds__(512, 1)
             const int parts = cached_steps > 0 ? C::PPARTS : 0;  // of O that are there already; then that of new tokens
 #pragma unroll 1
             for (int z = 0; z < parts + (s > cached_steps); ++z) {
-#pragma unroll 1
-              for (int c = 0; c < RV; c += W) {
-                const uint32_t at = tmem + tlane + (z < parts ? C::tm_o(t) + z * R : C::tm_n(t)) + c;
-                uint32_t x[W];
-                tmem_ldn<W>(at, x);
-                tmem_wait_ld();
+              const uint32_t at = tmem + tlane + (z < parts ? C::tm_o(t) + z * R : C::tm_n(t));
+              uint32_t x[RV];
+              tmem_ldn<RV>(at, x);
+              tmem_wait_ld();
 #pragma unroll
-                for (int r = 0; r < W; ++r) x[r] = __float_as_uint(__uint_as_float(x[r]) * (facs[c + r] * (z < parts ? fv : 1.f)));
-                tmem_stn<W>(at, x);
-              }
+              for (int r = 0; r < RV; ++r) x[r] = __float_as_uint(__uint_as_float(x[r]) * (facs[r] * (z < parts ? fv : 1.f)));
+              tmem_stn<RV>(at, x);
             }
             tmem_wait_st();
           }
@@ -903,24 +896,20 @@ __global__ void __launch_bounds__(512, 1)
           return true;
         };
         bool moves = s == 0, vote = !moves;
-        const uint32_t pbuf = sbase + C::OFF_P + (t * C::NP + (C::NP == 2 ? (g & 1) : 0)) * C::PBYTES;
+        const uint32_t pbuf = sbase + C::OFF_P + (t * 2 + (g & 1)) * C::PBYTES;
         for (;;) {
           if (moves && !move()) return false;
           uint32_t x[RV / 2];
           float p[RV], top = -INFINITY;
           const float w = cached ? vscale / vref : 1.f;
+          load_y(p);
 #pragma unroll
-          for (int c = 0; c < RV; c += W) {
-            float y[W];
-            load_y(c, y);
-#pragma unroll
-            for (int r = 0; r < W; ++r) {
-              const float2 rc = rowc[c + r];
-              float tt = fmaf(y[r], cached ? rc.x : a.scale_log2, rc.y);
-              if (!(cached ? there : (seen >> (c + r) & 1))) tt = -INFINITY;
-              top = fmaxf(top, tt);
-              p[c + r] = tt;
-            }
+          for (int r = 0; r < RV; ++r) {
+            const float2 rc = rowc[r];
+            float tt = fmaf(p[r], cached ? rc.x : a.scale_log2, rc.y);
+            if (!(cached ? there : (seen >> r & 1))) tt = -INFINITY;
+            top = fmaxf(top, tt);
+            p[r] = tt;
           }
           if (vote) {
             const bool grows = __any_sync(0xffffffffu, top > kPLog2 + kLagLog2 || (there && cached && vscale > vref));
@@ -964,15 +953,12 @@ __global__ void __launch_bounds__(512, 1)
                 x[2 * r + 1] = h2_sub(x[2 * r + 1], hi);
                 if (z == 1) x[2 * r] = h2_mul64(x[2 * r]), x[2 * r + 1] = h2_mul64(x[2 * r + 1]);
               }
-              if constexpr (RV >= 16) {
-#pragma unroll
-                for (int c = 0; c < RV / 16; ++c)
-                  sts128(pbuf + swizzled<C::PX>(key, z * (R / 16) + c), part[4 * c], part[4 * c + 1], part[4 * c + 2], part[4 * c + 3]);
-              } else if constexpr (RV == 8) {
-                sts64(pbuf + swizzled<C::PX>(key, z * (R / 16)), part[0], part[1]);
-              } else {
-                sts32(pbuf + swizzled<C::PX>(key, z * (R / 16)), part[0]);
-              }
+              if constexpr (RV == 16)
+                sts128(pbuf + swizzled<C::PX>(key, z), part[0], part[1], part[2], part[3]);
+              else if constexpr (RV == 8)
+                sts64(pbuf + swizzled<C::PX>(key, z), part[0], part[1]);
+              else
+                sts32(pbuf + swizzled<C::PX>(key, z), part[0]);
             }
           } else if (key < C::NEW) {
             if constexpr (RV >= 8) {
@@ -1001,30 +987,24 @@ __global__ void __launch_bounds__(512, 1)
       if (steps > 0) {
         if (!wait_pv(g - 1)) return false;
         tc_fence_after();
-        // Sums over the warp's keys: of W rows at a time, groups of 32 / W lanes end with a row each. Where there are
-        // no steps nothing is written here: the other lane may still read what the item before left.
+        // Sums over the warp's keys: groups of 32 / RV lanes end with a row each. Where there are no steps nothing is
+        // written here: the other lane may still read what the item before left.
+        int row = 0;
 #pragma unroll
-        for (int c = 0; c < RV; c += W) {
-          float v[W];
-#pragma unroll
-          for (int r = 0; r < W; ++r) v[r] = l[c + r];
-          int row = 0;
-#pragma unroll
-          for (int o = 16, n = W / 2; o; o >>= 1, n >>= 1) {
-            if (n == 0) {
-              v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
-              continue;
-            }
-            const bool up = lane & o;
-            row += up ? n : 0;
-#pragma unroll
-            for (int r = 0; r < n; ++r) {
-              const float send = up ? v[r] : v[r + n], keep = up ? v[r + n] : v[r];
-              v[r] = keep + __shfl_xor_sync(0xffffffffu, send, o);
-            }
+        for (int o = 16, n = RV / 2; o; o >>= 1, n >>= 1) {
+          if (n == 0) {
+            l[0] += __shfl_xor_sync(0xffffffffu, l[0], o);
+            continue;
           }
-          if ((lane & (32 / W - 1)) == 0) sums[(t * 4 + wq) * R + c + row] = v[0];
+          const bool up = lane & o;
+          row += up ? n : 0;
+#pragma unroll
+          for (int r = 0; r < n; ++r) {
+            const float send = up ? l[r] : l[r + n], keep = up ? l[r + n] : l[r];
+            l[r] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+          }
         }
+        if ((lane & (32 / RV - 1)) == 0) sums[(t * 4 + wq) * R + row] = l[0];
         if (key < RV) refs[t * R + key] = kPLog2 - rowc[key].y;
         if (key == 0) vrefs[t] = vref;
       }
@@ -1146,11 +1126,7 @@ __global__ void __launch_bounds__(512, 1)
       for (int u = uq; ok && u < uq + (dual ? 1 : 2); ++u)
         ok = wait_phase(BAR(C::Q_FULL + u % NQ), (u / NQ) & 1, st, SITE_T8_Q_FULL);
       if (!ok) break;
-      if constexpr (R == 16) {
-        ok = rows <= 4 ? run_item(it, Rows8<4>()) : rows <= 8 ? run_item(it, Rows8<8>()) : run_item(it, Rows8<16>());
-      } else {
-        ok = rows <= 16 ? run_item(it, Rows8<16>()) : run_item(it, Rows8<32>());
-      }
+      ok = rows <= 4 ? run_item(it, Rows8<4>()) : rows <= 8 ? run_item(it, Rows8<8>()) : run_item(it, Rows8<16>());
       if (!ok || !finish(it)) break;
       uq += dual ? 1 : 2;
       e0 += it.cnt;
@@ -1169,7 +1145,7 @@ __global__ void __launch_bounds__(512, 1)
 // [16 y, 16 y + 16) of the item that boundary x + 1 is the first to cut, a group of D / 4 threads a row.
 // Latency bounds it: a long sequence has a part in many CTAs, so the group reads as many parts' LSEs at once as it
 // has threads, and eight parts' rows (one after the other, joining two contexts of 131072 tokens took 15 us).
-template <int D, int R, bool F16>
+template <int D, bool F16>
 __global__ void __launch_bounds__(4 * D) serve8_join_kernel(Serve8BitArgs a) {
   griddep_wait();
   griddep_launch_dependents();
@@ -1180,7 +1156,7 @@ __global__ void __launch_bounds__(4 * D) serve8_join_kernel(Serve8BitArgs a) {
   constexpr int LPR = D / 4;
   const int sub = threadIdx.x % LPR, row = blockIdx.y * 16 + threadIdx.x / LPR, rr = cut.z + row;
   const bool there = rr < cut.x;
-  auto at = [&](int k) { return (long long)(k == 0 ? 2 * (c - 1) + 1 : 2 * (c - 1 + k)) * (2 * R) + row; };
+  auto at = [&](int k) { return (long long)(k == 0 ? 2 * (c - 1) + 1 : 2 * (c - 1 + k)) * (2 * Serve8Cfg<D, F16>::R) + row; };
   float m = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int k0 = 0; k0 < parts; k0 += LPR) {
@@ -1219,9 +1195,9 @@ __global__ void __launch_bounds__(4 * D) serve8_join_kernel(Serve8BitArgs a) {
     a.lse[(long long)h * a.T + token] = (l != 0.f ? m + lg2_approx(l) : -INFINITY) * 0.6931471805599453f;
 }
 
-template <int D, int R, bool F16>
+template <int D, bool F16>
 static int launch_serve8_d(const fa_rows* k, const fa_rows* v, const fa_pages* c, Serve8BitArgs a, cudaStream_t stream) {
-  using C = Serve8Cfg<D, R, F16>;
+  using C = Serve8Cfg<D, F16>;
   const auto type = F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   CUtensorMap mk, mv, mkc, mvc;
   auto map3 = [&](CUtensorMap* m, const fa_rows* r) {
@@ -1239,24 +1215,24 @@ static int launch_serve8_d(const fa_rows* k, const fa_rows* v, const fa_pages* c
   };
   if (!map3(&mk, k) || !map3(&mv, v) || !map4(&mkc, c->k) || !map4(&mvc, c->v))
     return cuda_fail("cuTensorMapEncodeTiled", 0, "tensor map rejected");
-  const auto kernel = serve8_kernel<D, R, F16>;
+  const auto kernel = serve8_kernel<D, F16>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
   if (e != cudaSuccess) return cuda_fail("cudaFuncSetAttribute", (int)e, cudaGetErrorName(e));
   int sms = 0;
   if (!sm_count(&sms)) return FA_ERR_CUDA;
-  a.part_rows = 2LL * sms * 2 * R;
+  a.part_rows = 2LL * sms * 2 * C::R;
   a.part_lse = a.part_o + a.part_rows * D;
   a.cuts = reinterpret_cast<int4*>(a.part_lse + a.part_rows);
   const int rc = launch_pdl("serve8_kernel", kernel, dim3(sms), dim3(C::THREADS), C::SMEM_BYTES, stream, mk, mv, mkc, mvc, a);
   if (rc != FA_OK || sms < 2) return rc;
-  return launch_pdl("serve8_join_kernel", serve8_join_kernel<D, R, F16>, dim3(sms - 1, 2 * R / 16), dim3(4 * D), 0, stream, a);
+  return launch_pdl("serve8_join_kernel", serve8_join_kernel<D, F16>, dim3(sms - 1, 2), dim3(4 * D), 0, stream, a);
 }
 
 int launch_serve8(const fa_rows* k, const fa_rows* v, const fa_pages* cache, Serve8BitArgs a, int d, int dtype,
                   cudaStream_t stream) {
   const bool f16 = dtype == FA_FP16;
-  if (d == 64) return f16 ? launch_serve8_d<64, 16, true>(k, v, cache, a, stream) : launch_serve8_d<64, 16, false>(k, v, cache, a, stream);
-  return f16 ? launch_serve8_d<128, 16, true>(k, v, cache, a, stream) : launch_serve8_d<128, 16, false>(k, v, cache, a, stream);
+  if (d == 64) return f16 ? launch_serve8_d<64, true>(k, v, cache, a, stream) : launch_serve8_d<64, false>(k, v, cache, a, stream);
+  return f16 ? launch_serve8_d<128, true>(k, v, cache, a, stream) : launch_serve8_d<128, false>(k, v, cache, a, stream);
 }
 
 }  // namespace fa
