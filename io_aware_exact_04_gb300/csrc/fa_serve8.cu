@@ -343,11 +343,11 @@ __global__ void __launch_bounds__(512, 1)
   if (warp == C::PRODUCER && lane == 0) {
     for (int i = 0; i < NT; ++i) {
       mbar_init(BAR(C::FULL + i), 10);  // K's and V's copies, and each of 8 lanes' scales
-      mbar_init(BAR(C::EMPTY + i), 2);  // both lanes, or one twice
+      mbar_init(BAR(C::EMPTY + i), 2);  // both issuers of P V, also of a tile that only one of them takes: neither may fall a use behind
     }
     for (int i = 0; i < NQ; ++i) {
       mbar_init(BAR(C::Q_FULL + i), 2);
-      mbar_init(BAR(C::Q_EMPTY + i), 9);  // the issuer of S, and both lanes' warps, or one's twice
+      mbar_init(BAR(C::Q_EMPTY + i), 9);  // the issuer of S, and both lanes' warps, also those whose rows are in the other slot
     }
     for (int t = 0; t < 2; ++t) {
       for (int u = 0; u < 2; ++u) {
@@ -712,10 +712,11 @@ __global__ void __launch_bounds__(512, 1)
         bool first = true, first_new = true;
         for (int k = 0; ok && k < it.cnt; ++k, ++e) {
           const int s = e % NT;
-          // waited for also where the other lane's: the arrival below must not count for an earlier use
+          // waited for also where the other lane's, and let go by both: the arrival must not count for an earlier use, and
+          // a parity tells two uses of the slot apart, not three
           if (!(ok = wait_phase(BAR(C::FULL + s), (e / NT) & 1, st, SITE_T8_V_FULL))) break;
           if (dual ? (k & 1) != t : k >= tiles) {
-            if (!dual && elect_one()) mbar_arrive(BAR(C::EMPTY + s));
+            if (elect_one()) mbar_arrive(BAR(C::EMPTY + s));
             __syncwarp();
             continue;
           }
@@ -747,7 +748,6 @@ __global__ void __launch_bounds__(512, 1)
             }
             mma_commit(BAR(C::O_DONE + 2 * t + (g & 1)));
             mma_commit(BAR(C::EMPTY + s));
-            if (dual) mma_commit(BAR(C::EMPTY + s));
           }
           __syncwarp();
           first = false;
@@ -1113,7 +1113,7 @@ __global__ void __launch_bounds__(512, 1)
         a.part_lse[part0 + key] = -INFINITY;  // (a cut item only) none of this part's keys concerns these rows
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive_n(BAR(C::Q_EMPTY + slot), dual ? 1 : 2);
+      if (lane == 0) mbar_arrive(BAR(C::Q_EMPTY + slot));
       return true;
     };
     for (int i = 0;; ++i) {
@@ -1121,11 +1121,13 @@ __global__ void __launch_bounds__(512, 1)
       if (!next_item(i, &it) || it.cnt < 0) break;
       const bool dual = it.flags & ITEM8_DUAL;
       const int rows = it.n * a.G - it.r0 - (dual ? 0 : t * R);
-      // both slots of a pair: a barrier's parity tells two uses of a slot apart, not three, so none may be left out
+      // both slots of a pair, and the other lane's let go at once: a barrier's parity tells two uses of a slot apart, not
+      // three, so none may be left out, nor be two uses ahead of a wait for it
       bool ok = true;
       for (int u = uq; ok && u < uq + (dual ? 1 : 2); ++u)
         ok = wait_phase(BAR(C::Q_FULL + u % NQ), (u / NQ) & 1, st, SITE_T8_Q_FULL);
       if (!ok) break;
+      if (!dual && lane == 0) mbar_arrive(BAR(C::Q_EMPTY + (uq + (t ^ 1)) % NQ));
       ok = rows <= 4 ? run_item(it, Rows8<4>()) : rows <= 8 ? run_item(it, Rows8<8>()) : run_item(it, Rows8<16>());
       if (!ok || !finish(it)) break;
       uq += dual ? 1 : 2;
