@@ -450,7 +450,7 @@ __global__ void __launch_bounds__(C8 ? 512 : 384, 1)
     for (int t = 0; t < 2; ++t) {
       mbar_init(BAR(C::Q_FULL + t), TURN ? 4 : 1);
       if (C8) mbar_init(BAR(C::Q_RAW + t), 1);
-      mbar_init(BAR(C::Q_EMPTY + t), TURN ? 9 : 1);  // the issuer of S (and all softmax warps, or a lane's twice: its factors)
+      mbar_init(BAR(C::Q_EMPTY + t), TURN ? 9 : 1);  // the issuer of S (and all softmax warps)
       for (int h = 0; h < 2; ++h) {
         mbar_init(BAR(C::S_FULL + 2 * t + h), 1);
         mbar_init(BAR(C::P_READY + 2 * t + h), 4);
@@ -1061,13 +1061,15 @@ __global__ void __launch_bounds__(C8 ? 512 : 384, 1)
       const int qslot = (uq + (dual ? 0 : t)) & 1;
       auto q_read = [&] {
         __syncwarp();
-        if (lane == 0) mbar_arrive_n(BAR(C::Q_EMPTY + qslot), dual ? 1 : 2);
+        if (lane == 0) mbar_arrive(BAR(C::Q_EMPTY + qslot));
       };
-      // Every use of the slots is waited for, in order: the arrival that releases one may not count for the one before.
+      // Every use of both slots is waited for, in order, and the other lane's let go at once: the arrival may not count
+      // for the use before, nor may a slot be two uses ahead of a wait for it.
       if (TURN) {
         for (int y = uq; ok && y < uq + (dual ? 1 : 2); ++y)
           ok = wait_phase(BAR(C::Q_FULL + (y & 1)), (y >> 1) & 1, st, SITE_SW_Q_FULL);
         if (!ok) break;
+        if (!dual && lane == 0) mbar_arrive(BAR(C::Q_EMPTY + (qslot ^ 1)));
         if (steps == 0) q_read();
       }
       const int tok_first = __shfl_sync(0xffffffffu, tok, 0);  // the warp's tokens ascend with its rows
