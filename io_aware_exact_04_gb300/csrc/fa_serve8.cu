@@ -37,10 +37,12 @@ namespace fa {
 // The new tokens, in 16 bits, take the same way as tiles of 64 keys: kind::f16 products with Q and P in
 // 16 bits, into columns of O of their own (vref = 1 there).
 //
-// Rows: a row is (token, head of the group), numbered token * G + head; a lane (four warps) has R of
-// them. A work item is 2 R rows of a sequence and key/value head, R for each of two lanes, over the same
-// tiles of 128 keys; where there are R rows or fewer both lanes take them and alternate tiles ("dual"),
-// and join their results at the end. All tiles of all items form one sequence, of which every CTA
+// Rows: a row is (token, head of the group), numbered token * G + head; a lane (four warps) has up to RV of
+// them, 4, 8 or 16. A work item is 2 RV rows of a sequence and key/value head, RV for each of two lanes, over the same
+// tiles of 128 keys; where there are RV rows or fewer both lanes take them and alternate tiles ("dual"),
+// and join their results at the end. A kernel for each RV: one with all three has half as much code again, and what an
+// item's start and end run through once then no longer stays near the SM (12 heads of 64, 128 contexts of 4096: 211 us,
+// with rows in fours alone 171). All tiles of all items form one sequence, of which every CTA
 // takes an equal run; items cut between CTAs leave fp32 partial results for serve8_join_kernel.
 //
 // Roles, 512 threads: warps 0-3 and 4-7 the softmax of lanes 0 and 1, a thread a key, warp 8 the scheduler,
@@ -51,11 +53,11 @@ namespace fa {
 // first tile of an item, and where some score passes the reference by more than it may. A vote of the four
 // warps says so, taken while P is formed as if nothing moved (with four warps in step, latency bounds a
 // tile: a wait costs 100 to 200 cycles, also where its phase has completed). S has two buffers, so that the next one is
-// formed meanwhile, and so has P. Rows come in classes of 4, 8 and 16: the columns of others are never looked at, and
-// what stands in them stays in them.
+// formed meanwhile, and so has P. The layout has R = 16 rows a lane: the columns behind the
+// first RV are never looked at, and what stands in them stays in them.
 template <int D, bool F16>
 struct Serve8Cfg {
-  static constexpr int R = 16;                       // rows of a lane
+  static constexpr int R = 16;
   static constexpr int ROW = D;                      // bytes of a cached row
   static constexpr int KV = 128 * ROW, ENTRY = 2 * KV;
   static constexpr int NEW = 64;                     // keys of a tile of new tokens
@@ -298,16 +300,12 @@ __device__ __forceinline__ void tmem_stn(uint32_t taddr, const uint32_t (&r)[N])
   else
     tmem_st16(taddr, r);
 }
-template <int N>
-struct Rows8 {
-  static constexpr int value = N;
-};
 template <bool F16>
 __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
   return F16 ? pack_f16x2(lo, hi) : pack_bf16x2(lo, hi);
 }
 
-template <int D, bool F16>
+template <int D, bool F16, int RV>
 __global__ void __launch_bounds__(512, 1)
     serve8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                   const __grid_constant__ CUtensorMap tm_kc, const __grid_constant__ CUtensorMap tm_vc, Serve8BitArgs a) {
@@ -468,7 +466,7 @@ __global__ void __launch_bounds__(512, 1)
       return true;
     };
     Item8 it;
-    const int unit = 2 * R;
+    constexpr int unit = 2 * RV;
     const Runs8 runs = runs8<D>(a, unit, gridDim.x, blockIdx.x == 0);
     int parts = 0;  // of the item that this CTA is the first to cut
     int4 cut = make_int4(0, 0, 0, 0);
@@ -485,7 +483,7 @@ __global__ void __launch_bounds__(512, 1)
         int p = q / a.Hkv, kvh = q - p * a.Hkv, x0 = (int)(at - (long long)q * span);
         while (ok && pos < end && pos - first < w.tiles) {
           const int x1 = (int)min((long long)span, x0 + (end - pos));
-          const int n0 = tiles_of_rows(a, w, p * unit, R), n1 = tiles_of_rows(a, w, p * unit + R, R), most = max(n0, n1);
+          const int n0 = tiles_of_rows(a, w, p * unit, RV), n1 = tiles_of_rows(a, w, p * unit + RV, RV), most = max(n0, n1);
           const bool dual = n1 == 0;
           const int j0 = max(0, x0 - kItemTiles<D>), j1 = min(max(0, x1 - kItemTiles<D>), most);
           it.cnt = max(0, j1 - j0);
@@ -565,7 +563,7 @@ __global__ void __launch_bounds__(512, 1)
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp >= C::SPLIT) {
     // ------------------------------------------------------------ Q in parts
-    constexpr int LPR = D / 8, RPI = 32 / LPR, STEPS = R / 2 / RPI;  // lanes a row, rows and steps of a warp
+    constexpr int LPR = D / 8, RPI = 32 / LPR, MINE = RV / 2, STEPS = (MINE + RPI - 1) / RPI;  // lanes a row, rows and steps of a warp
     const int half = warp - C::SPLIT, sub = lane / LPR, c = lane % LPR;
     int uq = 0;
     for (int i = 0;; ++i) {
@@ -578,9 +576,9 @@ __global__ void __launch_bounds__(512, 1)
         uint4 x[STEPS];
 #pragma unroll
         for (int k = 0; k < STEPS; ++k) {
-          const int rr = it.r0 + t * R + half * (R / 2) + k * RPI + sub, tok = rr / a.G;
+          const int rr = it.r0 + t * RV + half * MINE + k * RPI + sub, tok = rr / a.G;
           x[k] = make_uint4(0, 0, 0, 0);
-          if (rr < rows)
+          if (k * RPI + sub < MINE && rr < rows)
             x[k] = *reinterpret_cast<const uint4*>(a.q + (long long)(it.row0 + tok) * a.q_st +
                                                    (long long)(it.kvh * a.G + rr - tok * a.G) * a.q_sh + 8 * c);
         }
@@ -588,8 +586,9 @@ __global__ void __launch_bounds__(512, 1)
         const uint32_t q8 = sbase + C::OFF_Q + s * C::QSLOT, q16 = q8 + C::Q16;
 #pragma unroll
         for (int k = 0; k < STEPS; ++k) {
-          const uint32_t r = half * (R / 2) + k * RPI + sub;
-          sts128(q16 + (c >> 3) * (R * 128) + swizzled<128>(r, c & 7), x[k].x, x[k].y, x[k].z, x[k].w);
+          const uint32_t r = half * MINE + k * RPI + sub;
+          const bool mine = k * RPI + sub < MINE;
+          if (mine) sts128(q16 + (c >> 3) * (R * 128) + swizzled<128>(r, c & 7), x[k].x, x[k].y, x[k].z, x[k].w);
           const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
           float f[8], most = 0.f;
 #pragma unroll
@@ -618,10 +617,10 @@ __global__ void __launch_bounds__(512, 1)
           }
 #pragma unroll
           for (int z = 0; z < C::QPARTS; ++z)
-            sts64(q8 + swizzled<C::ROW>(z * R + r, c >> 1) + (c & 1) * 8, part[z][0] | part[z][1] << 16,
+            if (mine) sts64(q8 + swizzled<C::ROW>(z * R + r, c >> 1) + (c & 1) * 8, part[z][0] | part[z][1] << 16,
                   part[z][2] | part[z][3] << 16);
-          if (c == 0) {
-            const int rr = it.r0 + t * R + r, tok = rr / a.G;
+          if (c == 0 && mine) {
+            const int rr = it.r0 + t * RV + r, tok = rr / a.G;
             QRow* to = qrows + s * R + r;
             to->factor = rr < rows ? up * a.scale_log2 : 0.f;
             to->tok = rr < rows ? tok : -1;
@@ -786,9 +785,7 @@ __global__ void __launch_bounds__(512, 1)
     auto wait_pv = [&](int x) {  // tile x of the lane is in O, its P is read
       return wait_phase(BAR(C::O_DONE + 2 * t + (x & 1)), (x >> 1) & 1, st, SITE_T8_O_DONE);
     };
-    // One item, for lanes of which the first RV rows matter
-    auto run_item = [&](const Item8& it, auto rv) {
-      constexpr int RV = decltype(rv)::value;
+    auto run_item = [&](const Item8& it) {
       const bool dual = it.flags & ITEM8_DUAL;
       const int slot = (uq + (dual ? 0 : t)) % NQ, steps = t ? it.c1 : it.c0;
       const QRow* qr = qrows + slot * R;
@@ -1010,13 +1007,13 @@ __global__ void __launch_bounds__(512, 1)
       }
       return true;
     };
-    // What becomes of an item's results, for all classes: code that runs once an item has to be fetched anew
+    // What becomes of an item's results
     auto finish = [&](const Item8& it) {
       const bool dual = it.flags & ITEM8_DUAL, join = dual && it.c1 > 0, whole = it.flags & ITEM8_WHOLE;
       const int slot = (uq + (dual ? 0 : t)) % NQ, steps = t ? it.c1 : it.c0;
       const QRow* qr = qrows + slot * R;
-      const long long part0 = (long long)it.slot * (2 * R) + (dual ? 0 : t * R);
-      const int rows = min(R, it.n * a.G - it.r0 - (dual ? 0 : t * R));  // 1 at least, where there are steps
+      const long long part0 = (long long)it.slot * (2 * R) + (dual ? 0 : t * RV);
+      const int rows = min(RV, it.n * a.G - it.r0 - (dual ? 0 : t * RV));  // 1 at least, where there are steps
       if (steps > 0) {
         // The other lane's results stay as they are until its next product into O, which waits for this lane's
         // arrival below.
@@ -1109,7 +1106,7 @@ __global__ void __launch_bounds__(512, 1)
                 a.part_o[(part0 + r0 + r) * D + key] = o[r];
           }
         }
-      } else if (!dual && key < R && qr[key].tok >= 0 && FA_CHECK(in_range(part0 + key, a.part_rows), st, DBG_GLOBAL_STORE)) {
+      } else if (!dual && key < RV && qr[key].tok >= 0 && FA_CHECK(in_range(part0 + key, a.part_rows), st, DBG_GLOBAL_STORE)) {
         a.part_lse[part0 + key] = -INFINITY;  // (a cut item only) none of this part's keys concerns these rows
       }
       __syncwarp();
@@ -1120,7 +1117,6 @@ __global__ void __launch_bounds__(512, 1)
       Item8 it;
       if (!next_item(i, &it) || it.cnt < 0) break;
       const bool dual = it.flags & ITEM8_DUAL;
-      const int rows = it.n * a.G - it.r0 - (dual ? 0 : t * R);
       // both slots of a pair, and the other lane's let go at once: a barrier's parity tells two uses of a slot apart, not
       // three, so none may be left out, nor be two uses ahead of a wait for it
       bool ok = true;
@@ -1128,8 +1124,7 @@ __global__ void __launch_bounds__(512, 1)
         ok = wait_phase(BAR(C::Q_FULL + u % NQ), (u / NQ) & 1, st, SITE_T8_Q_FULL);
       if (!ok) break;
       if (!dual && lane == 0) mbar_arrive(BAR(C::Q_EMPTY + (uq + (t ^ 1)) % NQ));
-      ok = rows <= 4 ? run_item(it, Rows8<4>()) : rows <= 8 ? run_item(it, Rows8<8>()) : run_item(it, Rows8<16>());
-      if (!ok || !finish(it)) break;
+      if (!run_item(it) || !finish(it)) break;
       uq += dual ? 1 : 2;
       e0 += it.cnt;
     }
@@ -1143,12 +1138,12 @@ __global__ void __launch_bounds__(512, 1)
   }
 }
 
-// Joins the partial results of the items that CTA boundaries cut: block (x, y) takes rows
+// Joins the partial results of the items, `unit` rows each, that CTA boundaries cut: block (x, y) takes rows
 // [16 y, 16 y + 16) of the item that boundary x + 1 is the first to cut, a group of D / 4 threads a row.
 // Latency bounds it: a long sequence has a part in many CTAs, so the group reads as many parts' LSEs at once as it
 // has threads, and eight parts' rows (one after the other, joining two contexts of 131072 tokens took 15 us).
 template <int D, bool F16>
-__global__ void __launch_bounds__(4 * D) serve8_join_kernel(Serve8BitArgs a) {
+__global__ void __launch_bounds__(4 * D) serve8_join_kernel(Serve8BitArgs a, int unit) {
   griddep_wait();
   griddep_launch_dependents();
   const int c = blockIdx.x + 1;
@@ -1157,7 +1152,7 @@ __global__ void __launch_bounds__(4 * D) serve8_join_kernel(Serve8BitArgs a) {
   const int4 cut = a.cuts[2 * c + 1];  // rows of the sequence, its first token, the item's first row, head
   constexpr int LPR = D / 4;
   const int sub = threadIdx.x % LPR, row = blockIdx.y * 16 + threadIdx.x / LPR, rr = cut.z + row;
-  const bool there = rr < cut.x;
+  const bool there = row < unit && rr < cut.x;
   auto at = [&](int k) { return (long long)(k == 0 ? 2 * (c - 1) + 1 : 2 * (c - 1 + k)) * (2 * Serve8Cfg<D, F16>::R) + row; };
   float m = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1197,7 +1192,7 @@ __global__ void __launch_bounds__(4 * D) serve8_join_kernel(Serve8BitArgs a) {
     a.lse[(long long)h * a.T + token] = (l != 0.f ? m + lg2_approx(l) : -INFINITY) * 0.6931471805599453f;
 }
 
-template <int D, bool F16>
+template <int D, bool F16, int RV>
 static int launch_serve8_d(const fa_rows* k, const fa_rows* v, const fa_pages* c, Serve8BitArgs a, cudaStream_t stream) {
   using C = Serve8Cfg<D, F16>;
   const auto type = F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
@@ -1217,7 +1212,7 @@ static int launch_serve8_d(const fa_rows* k, const fa_rows* v, const fa_pages* c
   };
   if (!map3(&mk, k) || !map3(&mv, v) || !map4(&mkc, c->k) || !map4(&mvc, c->v))
     return cuda_fail("cuTensorMapEncodeTiled", 0, "tensor map rejected");
-  const auto kernel = serve8_kernel<D, F16>;
+  const auto kernel = serve8_kernel<D, F16, RV>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
   if (e != cudaSuccess) return cuda_fail("cudaFuncSetAttribute", (int)e, cudaGetErrorName(e));
   int sms = 0;
@@ -1227,14 +1222,24 @@ static int launch_serve8_d(const fa_rows* k, const fa_rows* v, const fa_pages* c
   a.cuts = reinterpret_cast<int4*>(a.part_lse + a.part_rows);
   const int rc = launch_pdl("serve8_kernel", kernel, dim3(sms), dim3(C::THREADS), C::SMEM_BYTES, stream, mk, mv, mkc, mvc, a);
   if (rc != FA_OK || sms < 2) return rc;
-  return launch_pdl("serve8_join_kernel", serve8_join_kernel<D, F16>, dim3(sms - 1, 2), dim3(4 * D), 0, stream, a);
+  return launch_pdl("serve8_join_kernel", serve8_join_kernel<D, F16>, dim3(sms - 1, (2 * RV + 15) / 16), dim3(4 * D), 0, stream, a, 2 * RV);
+}
+
+template <int D, bool F16>
+static int launch_serve8_rows(const fa_rows* k, const fa_rows* v, const fa_pages* c, const Serve8BitArgs& a, cudaStream_t stream) {
+  // The rows of a sequence are on the device; their average decides: sequences with up to twice as many still have one
+  // item a head, others more.
+  const long long rows = (long long)a.T * a.G;
+  if (rows <= 4LL * a.B) return launch_serve8_d<D, F16, 4>(k, v, c, a, stream);
+  if (rows <= 8LL * a.B) return launch_serve8_d<D, F16, 8>(k, v, c, a, stream);
+  return launch_serve8_d<D, F16, 16>(k, v, c, a, stream);
 }
 
 int launch_serve8(const fa_rows* k, const fa_rows* v, const fa_pages* cache, Serve8BitArgs a, int d, int dtype,
                   cudaStream_t stream) {
   const bool f16 = dtype == FA_FP16;
-  if (d == 64) return f16 ? launch_serve8_d<64, true>(k, v, cache, a, stream) : launch_serve8_d<64, false>(k, v, cache, a, stream);
-  return f16 ? launch_serve8_d<128, true>(k, v, cache, a, stream) : launch_serve8_d<128, false>(k, v, cache, a, stream);
+  if (d == 64) return f16 ? launch_serve8_rows<64, true>(k, v, cache, a, stream) : launch_serve8_rows<64, false>(k, v, cache, a, stream);
+  return f16 ? launch_serve8_rows<128, true>(k, v, cache, a, stream) : launch_serve8_rows<128, false>(k, v, cache, a, stream);
 }
 
 }  // namespace fa

@@ -421,3 +421,13 @@ def test_a_serving_loop(gpu, dtype):
         table[b, -(-lens[b] // page):] = -1
     compare()
     extend([1, 2, 3])
+
+
+@TYPES
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("nodes,Hq,H", [([1] * 20 + [30, 0, 2], 1, 1), ([1, 1, 40] + [1] * 30, 4, 2), ([2] * 9 + [70], 6, 2)])
+def test_one_sequence_with_many_rows_among_few(gpu, dtype, nodes, Hq, H, tree):
+    """The average decides which kernel runs: a sequence with many more rows is several items."""
+    lens = [(137 * i) % 900 for i in range(len(nodes))]
+    for d in (64, 128):
+        Made(gpu, lens, nodes, Hq, H, d, 32, 16, dtype, seed=8, tree=tree).check()
