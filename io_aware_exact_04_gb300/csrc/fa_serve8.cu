@@ -407,14 +407,14 @@ __global__ void __launch_bounds__(512, 1)
   };
   // K's (kv = 0) or V's copies of the item's tiles, the ring's entries from e on.
   auto load_tiles = [&](const Item8& it, int kv, int* e) {
-    int id = page_ids(it, 0), id_next = page_ids(it, 4), s = *e % NT;
+    int id = 0, id_next = page_ids(it, 0), s = *e % NT;
     uint32_t phase = ((*e / NT) & 1) ^ 1;
     auto next = [&] {
       ++*e;
       if (++s == NT) s = 0, phase ^= 1;
     };
     for (int k = 0; k < it.cnt; ++k, next()) {
-      if (k && !(k & 3)) id = id_next, id_next = page_ids(it, k + 4);
+      if (!(k & 3)) id = id_next, id_next = page_ids(it, k + 4);
       const int j = it.j0 + k, rows = rows_here(it, j);
       const bool cached = j < it.nc;
       const uint32_t bar = BAR(C::FULL + s), dst0 = sbase + s * C::ENTRY + kv * C::KV;
@@ -534,9 +534,9 @@ __global__ void __launch_bounds__(512, 1)
     for (int i = 0; ok; ++i) {
       Item8 it;
       if (!next_item(i, &it) || it.cnt < 0) break;
-      int id = page_ids(it, 0), id_next = page_ids(it, 4);
+      int id = 0, id_next = page_ids(it, 0);
       for (int k = 0; k < it.cnt; ++k, ++e) {
-        if (k && !(k & 3)) id = id_next, id_next = page_ids(it, k + 4);
+        if (!(k & 3)) id = id_next, id_next = page_ids(it, k + 4);
         const int j = it.j0 + k, s = e % NT;
         const uint32_t bar = BAR(C::FULL + s);
         if (!(ok = wait_phase(BAR(C::EMPTY + s), ((e / NT) & 1) ^ 1, st, SITE_T8_EMPTY))) break;
@@ -642,12 +642,13 @@ __global__ void __launch_bounds__(512, 1)
     bool ok = true;
     int e = 0;
     if (warp == C::S_BOTH) {
-      // S^T = K Q^T of both lanes, tile after tile in the order of the ring
+      // S^T = K Q^T of both lanes, tile after tile in the order of the ring. One copy of the code for both lanes, and loops
+      // for the products of new tokens: less code to fetch anew at an item (decoding at d = 64 139 -> 133 us).
       constexpr uint32_t I8 = idesc_e4m3_f32(128, 2 * R, 0, 0), I8X = idesc_e4m3_f32(128, R, 0, 0);
       constexpr uint32_t I16 = F16 ? idesc_f16_f32(128, R, 0, 0) : idesc_bf16_f32(128, R, 0, 0);
       constexpr uint32_t HI = desc_hi<C::ROW>(), HI16 = sdesc_hi(1024);
       const uint32_t ring_lo = sdesc_lo(sbase, 16), q_lo = sdesc_lo(sbase + C::OFF_Q, 16);
-      int uq = 0, used[2] = {0, 0};
+      int uq = 0, used0 = 0, used1 = 0;
       for (int i = 0; ok; ++i) {
         Item8 it;
         if (!next_item(i, &it) || it.cnt < 0) break;
@@ -660,10 +661,9 @@ __global__ void __launch_bounds__(512, 1)
           const int j = it.j0 + k, s = e % NT;
           if (!(ok = wait_phase(BAR(C::FULL + s), (e / NT) & 1, st, SITE_T8_FULL))) break;
           const uint32_t ka = ring_lo + s * (C::ENTRY >> 4);
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            if (dual ? (k & 1) != t : k >= (t ? it.c1 : it.c0)) continue;
-            const int g = used[t]++, u = g & 1;
+#pragma unroll 1
+          for (int t = dual ? k & 1 : k >= it.c0; t < 2; t += dual ? 2 : 1) {
+            const int g = t ? used1++ : used0++, u = g & 1;
             // S of two tiles before is in registers
             if (g > 1 && !(ok = wait_phase(BAR(C::S_FREE + 2 * t + u), ((g >> 1) - 1) & 1, st, SITE_T8_S_FREE))) break;
             tc_fence_after();
@@ -678,7 +678,7 @@ __global__ void __launch_bounds__(512, 1)
                     mma8_ss(d + R, sdesc_join(ka + 2 * x, HI), sdesc_join(qb + (2 * R * D >> 4) + 2 * x, HI), I8X, 1);
                 }
               } else {
-#pragma unroll
+#pragma unroll 1
                 for (int x = 0; x < D / 16; ++x) {
                   const uint32_t ko = ((x >> 2) * (C::NEW * 128) + (x & 3) * 32) >> 4;
                   const uint32_t qo = (C::Q16 + (x >> 2) * (R * 128) + (x & 3) * 32) >> 4;
@@ -740,7 +740,7 @@ __global__ void __launch_bounds__(512, 1)
               for (int x = 0; x < 4; ++x)
                 mma8_ss(d, sdesc_join(va + x * (32 * C::ROW >> 4), HIV), sdesc_join(pa + x * (32 * C::PX >> 4), HIP), I8, !first || x > 0);
             } else {
-#pragma unroll
+#pragma unroll 1
               for (int x = 0; x < 4; ++x)
                 mma_ss(tmem + C::tm_n(t), sdesc_join(va + x * (2048 >> 4), HI16), sdesc_join(pa + x * (16 * C::PX >> 4), HIP), I16,
                        !first_new || x > 0);
