@@ -1026,8 +1026,9 @@ __global__ void __launch_bounds__(512, 1)
         } else if (!meet()) {
           return false;
         }
-        // rows [ra, rb), four at a time: in a join each lane takes half of them
-        const int half = (rows + 7) / 8 * 4, ra = join ? t * half : 0, rb = join && t == 0 ? half : rows;
+        // rows [ra, rb), RG at a time: in a join each lane takes half of them
+        constexpr int RG = RV == 16 ? 8 : 4;
+        const int half = (rows + 2 * RG - 1) / (2 * RG) * RG, ra = join ? t * half : 0, rb = join && t == 0 ? half : rows;
         const float v0 = vrefs[0], v1 = vrefs[1];
         auto o_free = [&] {  // O is in registers: the issuers may write it again
           tc_fence_before();
@@ -1039,9 +1040,9 @@ __global__ void __launch_bounds__(512, 1)
         };
         if (ra >= rb) o_free();
 #pragma unroll 1
-        for (int r0 = ra; r0 < rb; r0 += 4) {
-          // weights of both lanes' O for row r0 + lane % 4, and its LSE to base 2
-          const int rr = r0 + (lane & 3);
+        for (int r0 = ra; r0 < rb; r0 += RG) {
+          // weights of both lanes' O for row r0 + lane % RG, and its LSE to base 2
+          const int rr = r0 + (lane & (RG - 1));
           const float m0 = refs[(join ? 0 : t) * R + rr], m1 = join ? refs[R + rr] : kNoKey, m = fmaxf(m0, m1);
           float l0 = 0.f, l1 = 0.f;
 #pragma unroll
@@ -1054,7 +1055,7 @@ __global__ void __launch_bounds__(512, 1)
           f0 *= inv, f1 *= inv;
           const int tok = qr[rr].tok;
           const long long token = qr[rr].to & 0xffffffffffll, head = qr[rr].to >> 40;
-          if (wq == 0 && lane < 4 && rr < rb && tok >= 0) {
+          if (wq == 0 && lane < RG && rr < rb && tok >= 0) {
             const float lse2 = sum != 0.f ? m - kPLog2 + lg2_approx(sum) : -INFINITY;
             if (!whole) {
               if (FA_CHECK(in_range(part0 + rr, a.part_rows), st, DBG_GLOBAL_STORE)) a.part_lse[part0 + rr] = lse2;
@@ -1062,21 +1063,21 @@ __global__ void __launch_bounds__(512, 1)
               a.lse[head * a.T + token] = lse2 * 0.6931471805599453f;
             }
           }
-          float o[4] = {};
+          float o[RG] = {};
           if (key < D) {
 #pragma unroll 1
             for (int u = 0; u < 1 + join; ++u) {
-              uint32_t x[C::PPARTS][4], y[4];
+              uint32_t x[C::PPARTS][RG], y[RG];
               const int of = join ? u : t, first = it.j0 + (dual ? of : 0), last = dual ? it.j0 + it.cnt - 1 - ((it.cnt - 1 - of) & 1)
                                                                                      : it.j0 + steps - 1;
               const bool old = first < it.nc, fresh = last >= it.nc;  // that lane's tiles: cached ones, new ones
               const float v = of ? v1 : v0;
 #pragma unroll
-              for (int z = 0; z < C::PPARTS; ++z) tmem_ldn<4>(tmem + tlane + C::tm_o(of) + r0 + z * R, x[z]);
-              tmem_ldn<4>(tmem + tlane + C::tm_n(of) + r0, y);
+              for (int z = 0; z < C::PPARTS; ++z) tmem_ldn<RG>(tmem + tlane + C::tm_o(of) + r0 + z * R, x[z]);
+              tmem_ldn<RG>(tmem + tlane + C::tm_n(of) + r0, y);
               tmem_wait_ld();
 #pragma unroll
-              for (int r = 0; r < 4; ++r) {
+              for (int r = 0; r < RG; ++r) {
                 float low = __uint_as_float(x[2][r]);
                 if (F16) low += __uint_as_float(x[C::PPARTS - 1][r]);
                 low = fmaf(low, 0.015625f, __uint_as_float(x[0][r]) + __uint_as_float(x[1][r]));
@@ -1086,14 +1087,14 @@ __global__ void __launch_bounds__(512, 1)
               }
             }
           }
-          if (r0 + 4 >= rb) o_free();
+          if (r0 + RG >= rb) o_free();
           if (key >= D) continue;
           if (whole) {
             // even threads write the even rows of two columns each, odd threads the odd rows
             uint16_t* const row = a.o + token * a.o_st + head * a.o_sh;  // of this lane's rr
             const long long mine = tok >= 0 && FA_CHECK(in_range(token, a.T), st, DBG_GLOBAL_STORE) ? (long long)row : 0;
 #pragma unroll
-            for (int r = 0; r < 4; r += 2) {
+            for (int r = 0; r < RG; r += 2) {
               const float got = __shfl_xor_sync(0xffffffffu, (lane & 1) ? o[r] : o[r + 1], 1);
               const uint32_t y = (lane & 1) ? pack16<F16>(got, o[r + 1]) : pack16<F16>(o[r], got);
               const long long to = __shfl_sync(0xffffffffu, mine, r + (lane & 1));
@@ -1101,7 +1102,7 @@ __global__ void __launch_bounds__(512, 1)
             }
           } else {
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
+            for (int r = 0; r < RG; ++r)
               if (__shfl_sync(0xffffffffu, tok, r) >= 0 && FA_CHECK(in_range(part0 + r0 + r, a.part_rows), st, DBG_GLOBAL_STORE))
                 a.part_o[(part0 + r0 + r) * D + key] = o[r];
           }

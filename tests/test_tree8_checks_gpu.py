@@ -1,7 +1,7 @@
 """Attention over a cache in 8 bits: the library's test builds, invalid values on the device, what a NaN reaches,
 scales far apart, memory far away, other streams, graphs, and a serving loop of all the operators together.
 
-FEW has few rows a sequence (decoding, small drafts), MANY many: two kernels.
+FEW and SOME have few rows a sequence (decoding, small drafts), up to 8 and up to 32, MANY many: different kernels.
 """
 
 import math
@@ -16,8 +16,9 @@ from tests.test_tree8_gpu import BF16, E4M3, FP16, Made, ints
 
 pytestmark = pytest.mark.gpu
 FEW = dict(lens=[300, 0, 1000, 64], nodes=[2, 1, 1, 3], Hq=4, H=2)
+SOME = dict(lens=[300, 0, 1000, 64], nodes=[6, 5, 4, 7], Hq=8, H=2)
 MANY = dict(lens=[300, 0, 700, 64], nodes=[20, 9, 40, 33], Hq=8, H=2)
-BOTH = pytest.mark.parametrize("shape", [FEW, MANY], ids=["few", "many"])
+BOTH = pytest.mark.parametrize("shape", [FEW, SOME, MANY], ids=["few", "some", "many"])
 TYPES = pytest.mark.parametrize("dtype", [BF16, FP16])
 
 
@@ -48,7 +49,7 @@ def test_debug_build_is_silent_and_right(build, gpu, shape, d):
             made(gpu, shape, d=d, dtype=dtype, tree=tree).check()
 
 
-@pytest.mark.parametrize("nodes,Hq", [(1, 4), (40, 4)])
+@pytest.mark.parametrize("nodes,Hq", [(1, 4), (4, 4), (40, 4)])
 @pytest.mark.parametrize("d", [64, 128])
 def test_a_copy_that_never_arrives(build, gpu, d, nodes, Hq):
     """The wait for it runs out, the kernel says where and stops; the same call of the library's own build is right after."""
@@ -239,7 +240,7 @@ def test_pages_far_apart(gpu):
     H, page, d, far = 8, 64, 128, 70000
     pools = [torch.empty((far, H, page, d), dtype=torch.uint8, device=gpu) for _ in range(2)]
     scales = [torch.empty((far, H, 2), device=gpu) for _ in range(2)]
-    for shape in (FEW, MANY):
+    for shape in (FEW, SOME, MANY):
         m = Made(gpu, shape["lens"], shape["nodes"], 16, H, d, page, 32, BF16, tail=0)
         want = m.check()
         n = m.kc.shape[0]
