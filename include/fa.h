@@ -416,10 +416,15 @@ typedef struct {
 /* fa_forward_tree over a cache in 8 bits: the queries, the nodes' keys and values
  * and O are of the type `dtype`, the cached ones e4m3 with their blocks' scales.
  * As there otherwise, but for what is said here.
- *  - Rounding: e4m3 values, their products with q and all sums are exact or fp32; see
- *    there for the probabilities.
- *  - A page id outside the cache counts as a page of zeros.
- *  - An infinity or NaN in a query makes its row NaN.
+ *  - Rounding: scores and sums are fp32. An element of a query takes part with its bits
+ *    down to 2^-21 of its row's largest; in bf16 with many rows that of a query, or of a
+ *    node's key or value, with those down to 2^-38 of the largest of the rows it is taken
+ *    with (32 at most). A probability times the scale of its value's block is rounded
+ *    once, by half a step of the type at most, or by 2^-34 of the product of the row's
+ *    largest probability and the sequence's and head's largest such scale, whichever is
+ *    more. Which of the kernels runs follows from B, T, Hq / Hkv and d alone.
+ *  - A NaN in the cache, or a scale that is no positive number, reaches the rows that see
+ *    it. An infinity in a query counts as NaN: the row is NaN.
  * workspace: fa_forward_tree_8bit_workspace_size bytes, 256-byte aligned. */
 FA_API int fa_forward_tree_8bit(const fa_rows* q, const fa_rows* k, const fa_rows* v, const fa_rows* o, float* lse,
                                 const fa_pages* cache, const fa_scales* scales, const int32_t* lens,
