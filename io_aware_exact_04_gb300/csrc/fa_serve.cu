@@ -1669,7 +1669,7 @@ int forward(const fa_rows* q, const fa_rows* k, const fa_rows* v, const fa_rows*
   a.ks = scales->k, a.vs = scales->v, a.s_sp = scales->page_stride, a.s_sh = scales->head_stride;
   a.block_shift = log2_of(scales->block);
   // Few rows a sequence on the average (the lengths are on the device) have a kernel of their own. 32 sequences of 32 rows
-  // and 8 heads at d = 128: over 8192 tokens 125 us there and 168 here, over 1024 tokens 50 and 49; at d = 64, 12 heads, 20
+  // and 8 heads at d = 128: over 8192 tokens 122 us there and 168 here, over 1024 tokens 42 and 49; at d = 64, 12 heads, 20
   // rows and 4096 tokens 112 both.
   if ((long long)T * a.G <= (d == 64 ? 16LL : 32LL) * B) return fa::launch_serve8(k, v, cache, a, d, dtype, st);
   const bool f16 = dtype == FA_FP16;

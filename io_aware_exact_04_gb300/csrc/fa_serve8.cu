@@ -57,9 +57,9 @@ namespace fa {
 // first RV are never looked at, and what stands in them stays in them.
 //
 // Measured on one GB300: decoding 64 sequences over up to 8192 tokens, 32 heads over 8 of 128: 108 us, 86 % of the copy
-// rate (32 of the same length, 8192: 92 us, 86 %; 2048: 35 us, 57 %); 128 over up to 5000, 12 heads of 64: 132 us, 60 %;
+// rate (32 of the same length, 8192: 92 us, 86 %; 2048: 34 us, 59 %); 128 over up to 5000, 12 heads of 64: 132 us, 60 %;
 // two contexts of 131072, 32 heads over 4 of 128: 50 us, 66 %; drafts of up to 6 nodes over up to 8000, 40 heads over 8:
-// 92 us. Within an item memory bounds it. What is left are an item's start and end, where the code is fetched anew: the
+// 83 us. Within an item memory bounds it. What is left are an item's start and end, where the code is fetched anew: the
 // SM's instruction cache answers 91 % of the requests at d = 64, and the one behind it is busy 75 % of the time; and the
 // first and last 8 us of a call, a chain of loads, conversions and products that wait for each other.
 template <int D, bool F16>
@@ -107,10 +107,11 @@ enum { SITE_T8_EMPTY = 80, SITE_T8_FULL, SITE_T8_Q_FULL, SITE_T8_Q_EMPTY, SITE_T
 constexpr float kNoKey = -1e30f;     // reference maximum of a row that has met no key
 constexpr float kPLog2 = 11.f, kLagLog2 = 4.f;
 constexpr int kMinTiles8 = 2;        // tiles of a CTA where there are few
-// An item's start and end cost a CTA as much as some tiles do (2.2 us and 0.6 a tile at d = 128, 3.6 and 0.34 at d = 64): the
-// runs are balanced with that many more for each.
+// An item's start and end cost a CTA as much as some tiles do (some 2 us and 0.6 a tile at d = 128, 3.4 and 0.34 at
+// d = 64, partly beside the loads of the next one's): the runs are balanced with that many more for each. Drafts and
+// decoding at d = 64, 83 and 133 us, take 88 and 138 with 4 and 8, 88 and 134 with 2 and 4, 84 and 138 with 5 and 10.
 template <int D>
-constexpr int kItemTiles = D == 64 ? 8 : 4;
+constexpr int kItemTiles = D == 64 ? 5 : 3;
 constexpr int kNewBox8 = 16;         // rows of a TMA box of new tokens
 
 // A work item (or the part of it that this CTA computes), as the producer publishes it.
@@ -223,7 +224,8 @@ __device__ __forceinline__ int seek8(const Serve8BitArgs& a, int unit, const Run
 __device__ __forceinline__ int tiles_of_rows(const Serve8BitArgs& a, const SeqWork8& w, int r, int R) {
   const int rows = w.n * a.G;
   if (r >= rows) return 0;
-  return w.nc + (((a.mask ? w.n : min(w.n, (min(r + R, rows) - 1) / a.G + 1)) + 63) >> 6);
+  if (a.mask || w.n <= 64) return w.nk;
+  return w.nc + ((min(w.n, (min(r + R, rows) - 1) / a.G + 1) + 63) >> 6);
 }
 
 __device__ __forceinline__ float warp_max(float x) {
@@ -581,9 +583,11 @@ __global__ void __launch_bounds__(512, 1)
       for (int t = 0; ok && t < nq; ++t, ++uq) {
         const int s = uq % NQ;
         uint4 x[STEPS];
+        int toks[STEPS];
 #pragma unroll
         for (int k = 0; k < STEPS; ++k) {
           const int rr = it.r0 + t * RV + half * MINE + k * RPI + sub, tok = rr / a.G;
+          toks[k] = tok;
           x[k] = make_uint4(0, 0, 0, 0);
           if (k * RPI + sub < MINE && rr < rows)
             x[k] = *reinterpret_cast<const uint4*>(a.q + (long long)(it.row0 + tok) * a.q_st +
@@ -627,7 +631,7 @@ __global__ void __launch_bounds__(512, 1)
             if (mine) sts64(q8 + swizzled<C::ROW>(z * R + r, c >> 1) + (c & 1) * 8, part[z][0] | part[z][1] << 16,
                   part[z][2] | part[z][3] << 16);
           if (c == 0 && mine) {
-            const int rr = it.r0 + t * RV + r, tok = rr / a.G;
+            const int rr = it.r0 + t * RV + r, tok = toks[k];
             QRow* to = qrows + s * R + r;
             to->factor = rr < rows ? up * a.scale_log2 : 0.f;
             to->tok = rr < rows ? tok : -1;
@@ -731,9 +735,12 @@ __global__ void __launch_bounds__(512, 1)
           if (rows < (cached ? 128 : C::NEW)) {
             // rows past the sequence may hold anything; P is 0 there, but 0 x NaN is not
             uint8_t* v = sm + s * C::ENTRY + C::KV;
-            const int pitch = cached ? C::ROW : 128, chunks = ((cached ? 128 : C::NEW) - rows) * pitch / 16;
-            for (int z = lane; z < chunks * (cached ? 1 : C::NSUB); z += 32)
-              *reinterpret_cast<uint4*>(v + rows * pitch + z / chunks * (C::NEW * 128) + z % chunks * 16) = make_uint4(0, 0, 0, 0);
+            const int pitch = cached ? C::ROW : 128, end = (cached ? 128 : C::NEW) * pitch;
+#pragma unroll 1
+            for (int at = rows * pitch + lane * 16; at < end; at += 512) {
+              *reinterpret_cast<uint4*>(v + at) = make_uint4(0, 0, 0, 0);
+              if (D == 128 && !cached) *reinterpret_cast<uint4*>(v + C::NEW * 128 + at) = make_uint4(0, 0, 0, 0);
+            }
             fence_proxy_async_smem();
             __syncwarp();
           }
