@@ -1668,10 +1668,12 @@ int forward(const fa_rows* q, const fa_rows* k, const fa_rows* v, const fa_rows*
   if (!scales) return fa::launch_serve(a, d, dtype, st);
   a.ks = scales->k, a.vs = scales->v, a.s_sp = scales->page_stride, a.s_sh = scales->head_stride;
   a.block_shift = log2_of(scales->block);
-  // Few rows a sequence on the average (the lengths are on the device) have a kernel of their own. 32 sequences of 32 rows
-  // and 8 heads at d = 128: over 8192 tokens 122 us there and 168 here, over 1024 tokens 42 and 49; at d = 64, 12 heads, 20
-  // rows and 4096 tokens 112 both.
-  if ((long long)T * a.G <= (d == 64 ? 16LL : 32LL) * B) return fa::launch_serve8(k, v, cache, a, d, dtype, st);
+  // Few rows a sequence on the average (the lengths are on the device) have a kernel of their own; in fp16 more parts of P
+  // and Q cost it more. 32 sequences of some 30 rows, there and here: at d = 128, 8 heads, 122 and 168 us over 8192 tokens
+  // and 42 and 49 over 1024 (fp16 128 and 159, 46 and 44); at d = 64 in bf16 72 and 82 over 4096 (8 heads), 45 both over
+  // 700 (12 heads); in fp16, 12 heads, 106 and 112 over 4096, but 46 and 37 over 700.
+  const long long few = d == 64 && dtype == FA_FP16 ? 16 : 32;
+  if ((long long)T * a.G <= few * B) return fa::launch_serve8(k, v, cache, a, d, dtype, st);
   const bool f16 = dtype == FA_FP16;
   if (d == 64) return f16 ? fa::launch_serve_d<64, true, true, true>(a, st) : fa::launch_serve_d<64, false, true, true>(a, st);
   return f16 ? fa::launch_serve_d<128, true, true, true>(a, st) : fa::launch_serve_d<128, false, true, true>(a, st);
