@@ -423,8 +423,9 @@ typedef struct {
  *    once, by half a step of the type at most, or by 2^-34 of the product of the row's
  *    largest probability and the sequence's and head's largest such scale, whichever is
  *    more. Which of the kernels runs follows from B, T, Hq / Hkv and d alone.
- *  - A NaN in the cache, or a scale that is no positive number, reaches the rows that see
- *    it. An infinity in a query counts as NaN: the row is NaN.
+ *  - A NaN in the cache reaches the rows that see it. Scales have to be positive and
+ *    finite; others give undefined results, of their own sequence and head only. An
+ *    infinity in a query counts as NaN: the row is NaN.
  * workspace: fa_forward_tree_8bit_workspace_size bytes, 256-byte aligned. */
 FA_API int fa_forward_tree_8bit(const fa_rows* q, const fa_rows* k, const fa_rows* v, const fa_rows* o, float* lse,
                                 const fa_pages* cache, const fa_scales* scales, const int32_t* lens,
