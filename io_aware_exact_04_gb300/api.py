@@ -566,13 +566,15 @@ def cache_update(kv, table, lens, src, new_lens, workspace=None, scales=None) ->
     """Every slot s becomes the first min(new_lens[s], lens[src[s]]) tokens of slot src[s], with pages
     for new_lens[s] tokens (include/fa.h: fa_cache_update): forks, reorders, trims, frees and grows.
     kv [planes, n_pages, Hkv, page_size, d] holds K and V of every layer (float8_e4m3fn: with scales, float32
-    [planes, n_pages, Hkv, blocks]); table int32 [slots, width] and lens int32 [slots] are updated in place. Returns info, int32 [2]: the pages needed and the pages
-    free (where more are needed than free, nothing has changed; -1, -1: invalid tables)."""
+    [planes, n_pages, Hkv, blocks]); table int32 [slots, width] and lens int32 [slots] are updated in place.
+    Returns info, int32 [2]: the pages needed and the pages free (where more are needed than free, nothing has
+    changed; -1, -1: invalid tables)."""
     index, slots, pool, sizes = _pool(kv, table, lens, scales)
     workspace = _pool_workspace(workspace, sizes, index)
     info = torch.empty(2, dtype=_INT32, device=index)
-    _call("fa_cache_update" if len(pool) == 1 else "fa_cache_update_8bit", index, *pool, _ints("src", src, index, (slots,)), _ints("new_lens", new_lens, index, (slots,)),
-          info.data_ptr(), workspace.data_ptr(), workspace.numel())
+    _call("fa_cache_update" if len(pool) == 1 else "fa_cache_update_8bit", index, *pool,
+          _ints("src", src, index, (slots,)), _ints("new_lens", new_lens, index, (slots,)), info.data_ptr(),
+          workspace.data_ptr(), workspace.numel())
     return info
 
 
@@ -582,7 +584,8 @@ def cache_compact(kv, table, lens, workspace=None, scales=None) -> torch.Tensor:
     index, _, pool, sizes = _pool(kv, table, lens, scales)
     workspace = _pool_workspace(workspace, sizes, index)
     info = torch.empty(2, dtype=_INT32, device=index)
-    _call("fa_cache_compact" if len(pool) == 1 else "fa_cache_compact_8bit", index, *pool, info.data_ptr(), workspace.data_ptr(), workspace.numel())
+    _call("fa_cache_compact" if len(pool) == 1 else "fa_cache_compact_8bit", index, *pool, info.data_ptr(),
+          workspace.data_ptr(), workspace.numel())
     return info
 
 

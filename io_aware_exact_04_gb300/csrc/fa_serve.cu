@@ -1221,14 +1221,14 @@ __global__ void __launch_bounds__(C8 ? 512 : 384, 1)
           } else {
             float pm[4];
 #pragma unroll
-          for (int y = 0; y < 4; ++y) pm[y] = sv[y];
+            for (int y = 0; y < 4; ++y) pm[y] = sv[y];
 #pragma unroll
-          for (int x = 4; x < KT - 4; x += 8)
+            for (int x = 4; x < KT - 4; x += 8)
 #pragma unroll
-            for (int y = 0; y < 4; ++y) pm[y] = fmax3(pm[y], sv[x + 2 * y], sv[x + 2 * y + 1]);
-          const float mx = fmax3(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3]),
-                                 fmax3(sv[KT - 4], sv[KT - 3], fmaxf(sv[KT - 2], sv[KT - 1])));
-          m_tile = mx * sl2;
+              for (int y = 0; y < 4; ++y) pm[y] = fmax3(pm[y], sv[x + 2 * y], sv[x + 2 * y + 1]);
+            const float mx = fmax3(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3]),
+                                   fmax3(sv[KT - 4], sv[KT - 3], fmaxf(sv[KT - 2], sv[KT - 1])));
+            m_tile = mx * sl2;
           }
           // the reference maximum moves only when it grows by more than 2^LAG_LOG2; O and l share it
           if (s == 0) {
