@@ -422,7 +422,8 @@ typedef struct {
  *    with (32 at most). A probability times the scale of its value's block is rounded
  *    once, by half a step of the type at most, or by 2^-34 of the product of the row's
  *    largest probability and the sequence's and head's largest such scale, whichever is
- *    more. Which of the kernels runs follows from B, T, Hq / Hkv and d alone.
+ *    more. Which of the kernels runs follows from B, T, Hq / Hkv, d and dtype alone: a
+ *    batch that is mostly sequences without nodes is best given without those.
  *  - A NaN in the cache reaches the rows that see it. Scales have to be positive and
  *    finite; others give undefined results, of their own sequence and head only. An
  *    infinity in a query counts as NaN: the row is NaN.
