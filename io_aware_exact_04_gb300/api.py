@@ -313,16 +313,17 @@ def _cache(k_cache, v_cache, k_scale, v_scale, table, index: int, dtype, H: int,
     if k_scale is None or v_scale is None:
         raise ValueError("a cache in 8 bits needs k_scale and v_scale")
     pages = _pages(k_cache, v_cache, table, index, _E4M3, H, d, B, 16)
-    n, page = k_cache.shape[0], k_cache.shape[2]
+    n, _, page, _ = k_cache.shape
+    shape, strides = k_scale.shape, k_scale.stride()
     for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-        if t.dtype is not _FP32 or t.get_device() != index or t.dim() != 3 or t.shape[:2] != (n, H) or t.shape != k_scale.shape:
+        if t.dtype is not _FP32 or t.get_device() != index or t.shape != shape or len(shape) != 3 or shape[0] != n or shape[1] != H:
             raise ValueError(f"{name} must be a float32 tensor ({n}, {H}, blocks) on cuda:{index}, is {t.dtype} "
                              f"{tuple(t.shape)} on {t.device}")
-    blocks = k_scale.shape[2]
-    sp, sh, sb = k_scale.stride()
+    blocks = shape[2]
+    sp, sh, sb = strides
     if blocks < 1 or page % blocks or page // blocks not in (16, 32, 64, 128, 256):
         raise ValueError(f"{blocks} blocks of a page of {page} tokens: a block has 16, 32, 64, 128 or 256 of them")
-    if v_scale.stride() != k_scale.stride() or (sb != 1 and blocks > 1):
+    if v_scale.stride() != strides or (sb != 1 and blocks > 1):
         raise ValueError(f"k_scale and v_scale must have the same strides, the last 1: {k_scale.stride()}, {v_scale.stride()}")
     if n == 1:
         sp = 1
@@ -466,9 +467,11 @@ def _angles(angles: torch.Tensor, positions, interleaved: bool, index: int, T: i
 
 def _rotated(name: str, t, out, index: int, dtype, T: int, H: int, d: int):
     """fa_rows of a tensor to rotate and of its result (None: a new one)."""
+    rows = _rows(name, t, index, dtype, T, H, d)
     if out is None:
         out = torch.empty((T, H, d), dtype=dtype, device=index)
-    return _rows(name, t, index, dtype, T, H, d), _rows(name + "_out", out, index, dtype, T, H, d), out
+        return rows, _lib.Rows(out.data_ptr(), H * d, d), out
+    return rows, _rows(name + "_out", out, index, dtype, T, H, d), out
 
 
 def rotary(q, k, angles, positions, interleaved: bool = False, q_out=None, k_out=None):
