@@ -57,9 +57,9 @@ namespace fa {
 // first RV are never looked at, and what stands in them stays in them.
 //
 // Measured on one GB300: decoding 64 sequences over up to 8192 tokens, 32 heads over 8 of 128: 108 us, 86 % of the copy
-// rate (32 of the same length, 8192: 92 us, 86 %; 2048: 34 us, 59 %); 128 over up to 5000, 12 heads of 64: 132 us, 60 %;
+// rate (32 of the same length, 8192: 92 us, 86 %; 2048: 34 us, 59 %); 128 over up to 5000, 12 heads of 64: 125 us, 63 %;
 // two contexts of 131072, 32 heads over 4 of 128: 50 us, 66 %; drafts of up to 6 nodes over up to 8000, 40 heads over 8:
-// 83 us. Within an item memory bounds it. What is left are an item's start and end, where the code is fetched anew: the
+// 79 us. Within an item memory bounds it. What is left are an item's start and end, where the code is fetched anew: the
 // SM's instruction cache answers 91 % of the requests at d = 64, and the one behind it is busy 75 % of the time; and the
 // first and last 8 us of a call, a chain of loads, conversions and products that wait for each other.
 template <int D, bool F16>
@@ -456,8 +456,10 @@ __global__ void __launch_bounds__(512, 1)
     }
   };
 
-  if (warp == C::PRODUCER) {
-    // ------------------------------------------------------------ scheduler, and the loads of K
+  if (warp == C::PRODUCER || warp == C::LOAD_V) {
+    // ------------------------------------------------------------ scheduler and the loads of K; the loads of V
+    // (one copy of the loads' code for both: drafts 86 -> 79 us, decoding at d = 64 133 -> 125)
+    const int kv = warp == C::LOAD_V;
     int items = 0, e = 0;  // items published, ring entries used
     bool ok = true;
     auto publish = [&](const Item8& it) {
@@ -474,66 +476,85 @@ __global__ void __launch_bounds__(512, 1)
       ++items;
       return true;
     };
-    Item8 it;
     constexpr int unit = 2 * RV;
-    const Runs8 runs = runs8<D>(a, unit, gridDim.x, blockIdx.x == 0);
+    Runs8 runs = {};
     int parts = 0;  // of the item that this CTA is the first to cut
     int4 cut = make_int4(0, 0, 0, 0);
-    if ((int)blockIdx.x < runs.ctas && runs.total > 0) {
-      long long pos = runs.start(blockIdx.x), first = 0;
-      const long long end = runs.start(blockIdx.x + 1);
-      int b = seek8<D>(a, unit, runs, pos, &first);
-      while (ok && pos < end) {
-        const SeqWork8 w = seq_work8<D>(a, b, unit, false);
-        const int span = w.nk + kItemTiles<D>;  // an item's share of the run: its costs, then its tiles
-        // the first item may be cut; from then on they are met from their start
-        const long long at = pos - first;
-        const int q = at < (1LL << 31) ? (int)at / span : (int)(at / span);
-        int p = q / a.Hkv, kvh = q - p * a.Hkv, x0 = (int)(at - (long long)q * span);
-        while (ok && pos < end && pos - first < w.tiles) {
-          const int x1 = (int)min((long long)span, x0 + (end - pos));
-          const int n0 = tiles_of_rows(a, w, p * unit, RV), n1 = tiles_of_rows(a, w, p * unit + RV, RV), most = max(n0, n1);
-          const bool dual = n1 == 0;
-          const int j0 = max(0, x0 - kItemTiles<D>), j1 = min(max(0, x1 - kItemTiles<D>), most);
-          it.cnt = max(0, j1 - j0);
-          it.flags = (dual ? ITEM8_DUAL : 0) | (j0 == 0 && j1 == most ? ITEM8_WHOLE : 0);
-          it.c0 = dual ? (it.cnt + 1) >> 1 : max(0, min(j1, n0) - j0);
-          it.c1 = dual ? it.cnt >> 1 : it.cnt;
-          it.j0 = j0, it.nc = w.nc, it.L = w.L, it.n = w.n, it.row0 = w.row0, it.r0 = p * unit, it.kvh = kvh;
-          it.slot = 2 * blockIdx.x + (j0 == 0);
-          it.b = b;
-          const long long tile0 = pos - x0 + kItemTiles<D>;  // the place of the item's first tile
-          if (j0 > 0 && it.cnt > 0 && runs.start(blockIdx.x - 1) <= tile0) {
-            // (the first item only) how many CTAs, this one included, hold later parts of it
-            const long long end_of_item = tile0 + most;
-            for (int k = blockIdx.x + lane; __any_sync(0xffffffffu, k < runs.ctas); k += 32)
-              parts += __popc(__ballot_sync(0xffffffffu, k < runs.ctas && runs.start(k) < end_of_item));
-            cut = make_int4(it.n * a.G, it.row0, it.r0, it.kvh);
-          }
-          if (it.cnt > 0) ok = publish(it) && load_tiles(it, 0, &e);
-          pos += x1 - x0;
-          x0 = 0;
-          if (++kvh == a.Hkv) kvh = 0, ++p;
-        }
-        first += w.tiles;
-        ++b;
+    long long pos = 0, end = 0, first = 0;  // the run's rest; the first tile of sequence b
+    int b = 0, p = 0, kvh = 0, x0 = 0;      // the next item: its sequence, rows and head, and how much of it is others'
+    bool met = false;                       // sequence b's sizes are known
+    SeqWork8 w = {};
+    if (!kv) {
+      runs = runs8<D>(a, unit, gridDim.x, blockIdx.x == 0);
+      if ((int)blockIdx.x < runs.ctas && runs.total > 0) {
+        pos = runs.start(blockIdx.x), end = runs.start(blockIdx.x + 1);
+        b = seek8<D>(a, unit, runs, pos, &first);
       }
     }
-    if (lane == 0) {
-      a.cuts[2 * blockIdx.x] = make_int4(parts, 0, 0, 0);
-      a.cuts[2 * blockIdx.x + 1] = cut;
-    }
-    if (ok) {
-      it.cnt = -1;
-      ok = publish(it);
-    }
-    let_land(e);
-  } else if (warp == C::LOAD_V) {
-    // ------------------------------------------------------------ the loads of V
-    int e = 0;
-    for (int i = 0;; ++i) {
+    // The CTA's next item with tiles.
+    auto schedule = [&](Item8* it) {
+      while (pos < end) {
+        if (!met) w = seq_work8<D>(a, b, unit, false);
+        const int span = w.nk + kItemTiles<D>;  // an item's share of the run: its costs, then its tiles
+        if (!met) {
+          // the first item may be cut; from then on they are met from their start
+          const long long at = pos - first;
+          const int q = at < (1LL << 31) ? (int)at / span : (int)(at / span);
+          p = q / a.Hkv, kvh = q - p * a.Hkv, x0 = (int)(at - (long long)q * span);
+          met = true;
+        }
+        if (pos - first >= w.tiles) {
+          first += w.tiles;
+          ++b;
+          met = false;
+          continue;
+        }
+        const int x1 = (int)min((long long)span, x0 + (end - pos));
+        const int n0 = tiles_of_rows(a, w, p * unit, RV), n1 = tiles_of_rows(a, w, p * unit + RV, RV), most = max(n0, n1);
+        const bool dual = n1 == 0;
+        const int j0 = max(0, x0 - kItemTiles<D>), j1 = min(max(0, x1 - kItemTiles<D>), most);
+        it->cnt = max(0, j1 - j0);
+        it->flags = (dual ? ITEM8_DUAL : 0) | (j0 == 0 && j1 == most ? ITEM8_WHOLE : 0);
+        it->c0 = dual ? (it->cnt + 1) >> 1 : max(0, min(j1, n0) - j0);
+        it->c1 = dual ? it->cnt >> 1 : it->cnt;
+        it->j0 = j0, it->nc = w.nc, it->L = w.L, it->n = w.n, it->row0 = w.row0, it->r0 = p * unit, it->kvh = kvh;
+        it->slot = 2 * blockIdx.x + (j0 == 0);
+        it->b = b;
+        const long long tile0 = pos - x0 + kItemTiles<D>;  // the place of the item's first tile
+        if (j0 > 0 && it->cnt > 0 && runs.start(blockIdx.x - 1) <= tile0) {
+          // (the first item only) how many CTAs, this one included, hold later parts of it
+          const long long end_of_item = tile0 + most;
+          for (int k = blockIdx.x + lane; __any_sync(0xffffffffu, k < runs.ctas); k += 32)
+            parts += __popc(__ballot_sync(0xffffffffu, k < runs.ctas && runs.start(k) < end_of_item));
+          cut = make_int4(it->n * a.G, it->row0, it->r0, it->kvh);
+        }
+        pos += x1 - x0;
+        x0 = 0;
+        if (++kvh == a.Hkv) kvh = 0, ++p;
+        if (it->cnt > 0) return true;
+      }
+      return false;
+    };
+    for (int i = 0; ok; ++i) {
       Item8 it;
-      if (!next_item(i, &it) || it.cnt < 0 || !load_tiles(it, 1, &e)) break;
+      if (kv) {
+        if (!next_item(i, &it) || it.cnt < 0) break;
+      } else {
+        if (!schedule(&it)) break;
+        if (!(ok = publish(it))) break;
+      }
+      ok = load_tiles(it, kv, &e);
+    }
+    if (!kv) {
+      if (lane == 0) {
+        a.cuts[2 * blockIdx.x] = make_int4(parts, 0, 0, 0);
+        a.cuts[2 * blockIdx.x + 1] = cut;
+      }
+      if (ok) {
+        Item8 it = {};
+        it.cnt = -1;
+        publish(it);
+      }
     }
     let_land(e);
   } else if (warp == C::SCALES) {
