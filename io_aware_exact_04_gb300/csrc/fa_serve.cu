@@ -1177,7 +1177,9 @@ __global__ void __launch_bounds__(C8 ? 512 : 384, 1)
             }
 #pragma unroll
             for (int x = 0; x < GR; ++x) {
-              ks[x] = fmaxf(ks[x], 1.1754944e-38f) * (sl2 * qf);  // (not 0: -inf times it stays -inf)
+              // Not 0, as -inf times it has to stay -inf: of zeros, or where there are no rows, qf and a key's factor are
+              // 2^-114 each, and a block's scale 2^-118, so that their product is what has to be kept from 0.
+              ks[x] = fmaxf(ks[x] * (sl2 * qf), 1.1754944e-38f);
               // not below 2^-40: what is that small adds nothing to O, but to the sum
               w[x] = fmaxf(lg2_approx(vs[x]) - vref, -40.f);
             }
