@@ -426,7 +426,7 @@ typedef struct {
  *    batch that is mostly sequences without nodes is best given without those.
  *  - A NaN in the cache reaches the rows that see it. Scales have to be positive and
  *    finite; others give undefined results, of their own sequence and head only. An
- *    infinity in a query counts as NaN: the row is NaN.
+ *    infinity in a query makes the row NaN, as scores of -inf alone do.
  * workspace: fa_forward_tree_8bit_workspace_size bytes, 256-byte aligned. */
 FA_API int fa_forward_tree_8bit(const fa_rows* q, const fa_rows* k, const fa_rows* v, const fa_rows* o, float* lse,
                                 const fa_pages* cache, const fa_scales* scales, const int32_t* lens,

@@ -1432,6 +1432,12 @@ __global__ void __launch_bounds__(C8 ? 512 : 384, 1)
         tiles8 += here, news += it.cnt - here, uq += dual ? 1 : 2;
       }
       if (dual && t == 1 && !join) continue;  // lane 0 has all of them
+      if constexpr (C8) {  // scores of -inf alone, of an infinite query say: no maximum to take off, the row is NaN
+        if (l_run == 0.f && valid && steps > 0 &&
+            sees_a_key(a.mask, a.words, it.row0 + tok, tok, it.n, it.j0 < it.nc, max(0, it.j0 - it.nc) * C::TK,
+                       (it.j0 + it.cnt - it.nc) * C::TK))
+          l_run = NAN;
+      }
       // l = 0: no key; NaN stays NaN
       const float inv = l_run != 0.f ? 1.f / l_run : 0.f;
       const float lse2 = l_run != 0.f ? m_run - P_LOG2 + lg2_approx(l_run) : -INFINITY;

@@ -1086,9 +1086,15 @@ __global__ void __launch_bounds__(512, 1)
             if (join) l1 += sums[(4 + x) * R + rr];
           }
           float f0 = ex2_approx(m0 - m), f1 = ex2_approx(m1 - m);
-          const float sum = l0 * f0 + l1 * f1, inv = sum != 0.f ? 1.f / sum : 0.f;  // 0: no key; NaN stays NaN
-          f0 *= inv, f1 *= inv;
           const int tok = qr[rr].tok;
+          float sum = l0 * f0 + l1 * f1;
+          // scores of -inf alone, of an infinite query say: no maximum to take off, the row is NaN
+          if (sum == 0.f && tok >= 0 &&
+              sees_a_key(a.mask, a.words, it.row0 + tok, tok, it.n, it.j0 < it.nc, max(0, it.j0 - it.nc) * C::NEW,
+                         (it.j0 + it.cnt - it.nc) * C::NEW))
+            sum = NAN;
+          const float inv = sum != 0.f ? 1.f / sum : 0.f;  // 0: no key; NaN stays NaN
+          f0 *= inv, f1 *= inv;
           const long long token = qr[rr].to & 0xffffffffffll, head = qr[rr].to >> 40;
           if (wq == 0 && lane < RG && rr < rb && tok >= 0) {
             const float lse2 = sum != 0.f ? m - kPLog2 + lg2_approx(sum) : -INFINITY;

@@ -68,6 +68,20 @@ __device__ __forceinline__ int find_sequence(const int* cu, int B, int t) {
   return (lo < B && cu[lo] <= t) ? lo : -1;
 }
 
+// Whether node `tok` of a sequence of n sees a cached token or one of the nodes [k0, k1), k0 a multiple of 32, as
+// fa_forward_tree's mask (row `token` of it) or a chain has it. Asked only of rows without a finite score, so out of line.
+__device__ __noinline__ inline bool sees_a_key(const uint32_t* mask, int words, long long token, int tok, int n, bool cached,
+                                               int k0, int k1) {
+  if (cached) return true;
+  k1 = min(k1, n);
+  if (!mask) return k0 < k1 && k0 <= tok;
+  for (int k = k0; k < k1 && (k >> 5) < words; k += 32) {
+    const uint32_t here = k1 - k < 32 ? (1u << (k1 - k)) - 1 : 0xffffffffu;
+    if (mask[token * words + (k >> 5)] & here) return true;
+  }
+  return false;
+}
+
 // All offsets, by one block: kernels with a block or warp for each token never meet a sequence
 // that no token lies in.
 __device__ __forceinline__ void check_offsets(const int* cu, int B, int T, int* status) {
