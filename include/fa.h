@@ -420,9 +420,11 @@ typedef struct {
  *    down to 2^-21 of its row's largest; in bf16 with many rows that of a query, or of a
  *    node's key or value, with those down to 2^-38 of the largest of the rows it is taken
  *    with (32 at most). A probability times the scale of its value's block is rounded
- *    once, by half a step of the type at most, or by 2^-34 of the product of the row's
- *    largest probability and the sequence's and head's largest such scale, whichever is
- *    more. Which of the kernels runs follows from B, T, Hq / Hkv, d and dtype alone: a
+ *    once, by half a step of the type at most, or by 2^-32 (in bf16 with few rows 2^-30) of
+ *    the product of the row's largest probability and the sequence's and head's largest
+ *    such scale, whichever is more. With many rows that concerns nodes' values too: their
+ *    scale is 1, or in bf16 the power of two that brings the largest element of 32 rows
+ *    from [2^14, 2^15) to what it is. Which of the kernels runs follows from B, T, Hq / Hkv, d and dtype alone: a
  *    batch that is mostly sequences without nodes is best given without those.
  *  - A NaN in the cache reaches the rows that see it. Scales have to be positive and
  *    finite; others give undefined results, of their own sequence and head only. An

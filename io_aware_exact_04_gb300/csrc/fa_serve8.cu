@@ -25,10 +25,11 @@ namespace fa {
 //    (elements below 2^-10 of the row's largest keep bits down to 2^-21 of that one). q1 K and
 //    (q2 + q3) K have columns of their own, as the factor 16 must stay outside.
 //  - P, formed 2^11 times its value in fp16 (11 bits; below 2^-25 of the largest, steps of 2^-35 of it), is
-//    p1 + p2 + (p3 + p4) / 64, each the e5m2 nearest to what is left (bf16 does without p4). With the
-//    range of e5m2, 2^-16 to 2^15, three parts round a probability by half a step of 2^-8 of itself
-//    (2^-9), four by 2^-12, and either by no more than 2^-34 of the row's largest. (e4m3 would need as
-//    many parts and end at 2^-26.) Each has columns of O of its own: one product of N = 3 R or 4 R columns
+//    p1 + p2 + (p3 + p4) / 64, each the e5m2 nearest to what is left (bf16 does without p4). As what is left
+//    has a sign, three parts of three bits hold all 11, down to where e5m2, of 2^-16 to 2^15, ends: three parts are off
+//    by 2^-21 at most below 2^-10, four by 2^-23 below 2^-12. With fp16's own 2^-25, and as P has up to one bit less
+//    than 2^11 where vref is above the largest scale, that is 1.06 2^-31 and 1.25 2^-33 of the row's largest
+//    probability (times that scale). (e4m3 would need as many parts and end at 2^-26.) Each has columns of O of its own: one product of N = 3 R or 4 R columns
 //    takes 40 to 58 cycles, one of 16 takes 36. The reference maximum moves when it grows by 2^4, so
 //    that P stays within 2^15.
 //  - The scale of a key's block multiplies its scores, that of its values its probability, which is kept
