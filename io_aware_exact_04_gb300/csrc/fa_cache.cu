@@ -485,7 +485,7 @@ int check_pool(const fa_pool* p, const fa_pool_scales* scales, int elem, const i
     if ((reinterpret_cast<uintptr_t>(scales->data) & 3u) != 0) return FA_ERR_MISALIGNED;
     a->block_shift = 4;
     while ((p->page_size >> a->block_shift) > scales->blocks) ++a->block_shift;
-    if (scales->blocks << a->block_shift != p->page_size) return FA_ERR_UNSUPPORTED;
+    if ((long long)scales->blocks << a->block_shift != p->page_size) return FA_ERR_UNSUPPORTED;
     if (p->planes > 1 && scales->plane_stride < (long long)p->n_pages * p->Hkv * scales->blocks) return FA_ERR_INVALID_ARG;
     a->scales = scales->data, a->scale_plane = scales->plane_stride, a->blocks = scales->blocks;
   }
