@@ -29,9 +29,9 @@ namespace fa {
 //    has a sign, three parts of three bits hold all 11, down to where e5m2, of 2^-16 to 2^15, ends: three parts are off
 //    by 2^-21 at most below 2^-10, four by 2^-23 below 2^-12. With fp16's own 2^-25, and as P has up to one bit less
 //    than 2^11 where vref is above the largest scale, that is 1.06 2^-31 and 1.25 2^-33 of the row's largest
-//    probability (times that scale). (e4m3 would need as many parts and end at 2^-26.) Each has columns of O of its own: one product of N = 3 R or 4 R columns
-//    takes 40 to 58 cycles, one of 16 takes 36. The reference maximum moves when it grows by 2^4, so
-//    that P stays within 2^15.
+//    probability (times that scale). (e4m3 would need as many parts and end at 2^-26.) Each has columns of O of
+//    its own: one product of N = 3 R or 4 R columns takes 40 to 58 cycles, one of 16 takes 36. The reference
+//    maximum moves when it grows by 2^4, so that P stays within 2^15.
 //  - The scale of a key's block multiplies its scores, that of its values its probability, which is kept
 //    in range by a reference of its own (vref, at least each scale that was met).
 //
@@ -1260,6 +1260,8 @@ static int launch_serve8_d(const fa_rows* k, const fa_rows* v, const fa_pages* c
   if (e != cudaSuccess) return cuda_fail("cudaFuncSetAttribute", (int)e, cudaGetErrorName(e));
   int sms = 0;
   if (!sm_count(&sms)) return FA_ERR_CUDA;
+  // slots of its own in the workspace, which fa_forward_tree_workspace_size measures for slots of 256 rows
+  static_assert(2 * C::R <= 256, "the workspace");
   a.part_rows = 2LL * sms * 2 * C::R;
   a.part_lse = a.part_o + a.part_rows * D;
   a.cuts = reinterpret_cast<int4*>(a.part_lse + a.part_rows);
@@ -1270,11 +1272,12 @@ static int launch_serve8_d(const fa_rows* k, const fa_rows* v, const fa_pages* c
 
 template <int D, bool F16>
 static int launch_serve8_rows(const fa_rows* k, const fa_rows* v, const fa_pages* c, const Serve8BitArgs& a, cudaStream_t stream) {
-  // The rows of a sequence are on the device; their average decides: sequences with up to twice as many still have one
-  // item a head, others more. Whatever the distribution, that makes no more than 2 B items a head: a part of a prompt among
-  // decoding sequences, or a batch of mostly empty ones, costs at most what two decoding batches of B over its length do.
-  // 256 sequences over 4096 tokens, 32 heads over 8 of 128: 128 tokens of one and one of each other 414 us (the kernel for many
-  // rows 1055), 64 tokens of four and none of the others 167 (49).
+  // The rows of a sequence are on the device; their average decides. Up to an average of 16, sequences with up to twice as
+  // many still have one item a head; above it, where averages of up to 32 come here too, those with up to 32 rows. Others
+  // have more, and their context is read once for each. Whatever the distribution, that makes no more than 2 B items a
+  // head: a part of a prompt among decoding sequences, or a batch of mostly empty ones, costs at most what two decoding
+  // batches of B over its length do. 256 sequences over 4096 tokens, 32 heads over 8 of 128: 128 tokens of one and one of
+  // each other 414 us (the kernel for many rows 1055), 64 tokens of four and none of the others 167 (49).
   const long long rows = (long long)a.T * a.G;
   if (rows <= 4LL * a.B) return launch_serve8_d<D, F16, 4>(k, v, c, a, stream);
   if (rows <= 8LL * a.B) return launch_serve8_d<D, F16, 8>(k, v, c, a, stream);

@@ -27,11 +27,16 @@ struct ServeArgs {
   const int* cu;
   int B, T, Hq, Hkv, G;
   float scale_log2;
-  float* part_o;    // workspace: two slots of 256 rows for each CTA, O normalised by its own l
+  // Workspace, of fa_forward_tree_workspace_size bytes: two slots of rows for each CTA, then the cuts. A slot has 256
+  // rows, lane 1's from 128 on. The few-row kernel of fa_serve8.cu divides the same bytes into slots of 32, lane 1's
+  // rows following lane 0's.
+  float* part_o;    // O normalised by its own l
   float* part_lse;  // their LSEs, base 2 (-inf: no key, O not written)
   long long part_rows;
   int4* cuts;       // two for each CTA, of the item that it is the first to cut: {later parts (0: none), ..},
-                    // {tokens of the sequence, its first row, the item's first token, key/value head}
+                    // {tokens of the sequence, its first row, the item's first token, key/value head}, or of the
+                    // few-row kernel {rows of the sequence (tokens times heads of the group), its first token, the
+                    // item's first row, key/value head}
   int* status;
 };
 
