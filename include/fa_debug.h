@@ -2,8 +2,8 @@
  * Debug build of the attention library (libfa_debug.so): the C ABI of fa.h
  * unchanged, plus the one entry point below. It stands in for a memory checker.
  *
- * Built from the same sources with FA_DEBUG defined, every kernel checks the
- * following before use:
+ * Built from the same sources with FA_DEBUG defined, every kernel but those of
+ * the serving entry points checks the following before use:
  *  - the index of each direct global load and store;
  *  - the index of each metadata read (kv_len, cu_seqlens, partial slots);
  *  - the coordinates of each TMA or bulk copy: x inside the row on a 16-byte
@@ -11,6 +11,16 @@
  *    tensor's rows. A store or a reduce-add must also start at a row >= 0;
  *  - the shared-memory range of each copy and each MMA operand tile;
  *  - the TMEM lane quarter and columns of each warp's accumulators.
+ * The kernels of the serving entry points range-check what they take from device
+ * memory (offsets, lengths, positions, page ids, picked rows) in every build. In
+ * this one those of fa_forward_prompt, fa_forward_tree and fa_forward_tree_8bit
+ * also check the shared-memory destination of each key and value copy, and the
+ * row of each result and partial result; over a cache in 8 bits the tiles that
+ * are converted, the page table's index and the rows of queries read directly
+ * too. Those of fa_rotary_append and fa_cache_append_8bit check each token's row,
+ * and its place and head in an 8-bit cache. The operands and accumulators of
+ * serving MMAs, fa_cache_append, and the update and compaction of pools have no
+ * checks beyond those of every build.
  * A failed check does not fault. It records FA_ERR_DEVICE_CHECK in the status
  * word, with one of the sites below in detail[1] of
  * fa_get_last_device_status_detail(), and skips the access. The CTA then gives

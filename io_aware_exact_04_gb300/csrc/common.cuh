@@ -64,10 +64,10 @@ __device__ __forceinline__ void record_check(int* word, int site) {
 
 // ---------------------------------------------------------------------------------------------
 // Debug build (FA_DEBUG: libfa_debug.so, never the library's own build). Before use, the kernels
-// check the indices of their direct global loads and stores and of the metadata they read
-// (kv_len, cu_seqlens). They also check the coordinates and the shared-memory range of every TMA
-// or bulk copy, the shared-memory operands of their MMAs, and the TMEM lanes and columns of each
-// warp's accumulators. A failed check records FA_ERR_DEVICE_CHECK with its site (fa_debug.h) in
+// (those of the serving entry points a part of it, as fa_debug.h lists) check the indices of their
+// direct global loads and stores and of the metadata they read (kv_len, cu_seqlens). They also check
+// the coordinates and the shared-memory range of every TMA or bulk copy, the shared-memory operands
+// of their MMAs, and the TMEM lanes and columns of each warp's accumulators. A failed check records FA_ERR_DEVICE_CHECK with its site (fa_debug.h) in
 // the status word and raises the CTA's abort flag where the CTA has one, so that the CTA's
 // waits give up and it leaves through the same path as after a timeout. The access is skipped.
 // In every other build FA_CHECK is the literal `true` and its condition is not compiled.

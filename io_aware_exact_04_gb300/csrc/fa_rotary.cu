@@ -35,6 +35,10 @@ struct RotaryArgs {
   long long blocks8;          // blocks of the grid with work in 8 bits; those behind them rotate queries
   int head_groups;
   int* status;
+#ifdef FA_DEBUG
+  int dbg_B;           // batch count B, for the extents the debug build checks against
+  int dbg_slack;       // rows taken off those extents (fa_debug_set_check_slack)
+#endif
 };
 
 // ---------------------------------------------------------------------------------------------
@@ -130,7 +134,7 @@ __device__ __forceinline__ void rotate_rows(const RotaryArgs& a, int t, int spli
   const int lane = threadIdx.x & 31, sub = lane / LPR, p = lane % LPR;
   int i;
   const int b = token_of(a, t, &i);
-  if (b < 0) return;
+  if (b < 0 || !FA_CHECK(in_range(t, (long long)a.T - FA_SLACK(a)), a.status, DBG_GLOBAL_LOAD)) return;
   const long long pos = (a.kc ? (long long)a.start[b] : 0) + i;
   const long long place = a.at ? a.at[t] : pos;
   if (place < 0 || place >= a.positions) return record_check(a.status, SITE_S_ANGLE);
@@ -343,6 +347,10 @@ __device__ __forceinline__ void append_block(const RotaryArgs& a, long long unit
   const int in_page = (int)(base & ((1 << a.page_shift) - 1));
   const int first = (int)max(0LL, start - base), last = (int)min((long long)block, end - base);  // the block's new tokens
   const ChunkPair cp = chunk_pair<LPR>(lane % LPR, is_v ? 0 : a.dim);
+  // (debug build) row i of the block, of head h: inside the page, and the page inside the cache
+  [[maybe_unused]] auto in_cache = [&](int h, int i) {
+    return in_range(h, a.Hkv) && in_range(id, a.n_pages) && in_range(i, block) && in_range(in_page + i, 1LL << a.page_shift);
+  };
   uint8_t* const pages = (is_v ? a.vc : a.kc) + id * a.c_sp + in_page * a.c_st;
   float* const scales = (is_v ? a.vs : a.ks) + id * a.s_sp + (in_page >> a.block_shift);
   const long long row_sh = is_v ? a.v_sh : a.k_sh;
@@ -373,6 +381,7 @@ __device__ __forceinline__ void append_block(const RotaryArgs& a, long long unit
         }
         angle[u] = a.angles + p * a.a_stride;
       }
+      if (!FA_CHECK(in_range(row, (long long)a.Tkv - FA_SLACK(a)) && in_range(t, a.T), a.status, DBG_GLOBAL_LOAD)) continue;
       from[u] = is_v ? a.v + row * a.v_st : a.k + row * a.k_st;
       if (puts) ko[u] = a.ko + t * a.ko_st;
     }
@@ -380,7 +389,7 @@ __device__ __forceinline__ void append_block(const RotaryArgs& a, long long unit
   auto load = [&](int h, uint4 (&to)[U][2]) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (!from[u]) continue;
+      if (!from[u] || !FA_CHECK(in_range(h, a.Hkv), a.status, DBG_GLOBAL_LOAD)) continue;
       const uint16_t* row = from[u] + h * row_sh;
       to[u][0] = *reinterpret_cast<const uint4*>(row + 8 * cp.c0);
       to[u][1] = *reinterpret_cast<const uint4*>(row + 8 * cp.c1);
@@ -425,13 +434,13 @@ __device__ __forceinline__ void append_block(const RotaryArgs& a, long long unit
     }
     return most;
   };
-  auto scale_of = [&](int h) { return first > 0 && id >= 0 ? scales[h * a.s_sh] : 0.f; };
+  auto scale_of = [&](int h) { return first > 0 && id >= 0 && FA_CHECK(in_cache(h, 0), a.status, DBG_GLOBAL_LOAD) ? scales[h * a.s_sh] : 0.f; };
   Rescale z;
   auto store = [&](int h, int sub) {
     uint8_t* to = pages + h * a.c_sh + (sub * TOKENS + lane / LPR) * a.c_st;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (!from[u]) continue;
+      if (!from[u] || !FA_CHECK(in_cache(h, sub * TOKENS + u * RPI + lane / LPR), a.status, DBG_GLOBAL_STORE)) continue;
       uint8_t* at = to + u * RPI * a.c_st;
       *reinterpret_cast<uint2*>(at + 8 * cp.c0) = e4m3x8(f[u][0], z.inv);
       *reinterpret_cast<uint2*>(at + 8 * cp.c1) = e4m3x8(f[u][1], z.inv);
@@ -441,7 +450,7 @@ __device__ __forceinline__ void append_block(const RotaryArgs& a, long long unit
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int i = sub * TOKENS + u * RPI + lane / LPR;
-      if (i >= first) continue;
+      if (i >= first || !FA_CHECK(in_cache(h, i), a.status, DBG_GLOBAL_STORE)) continue;
       uint4* at = reinterpret_cast<uint4*>(pages + h * a.c_sh + i * a.c_st) + lane % LPR;
       const uint4 v = *at;
       const uint2 lo = e4m3x8_scaled(make_uint2(v.x, v.y), z.by), hi = e4m3x8_scaled(make_uint2(v.z, v.w), z.by);
@@ -467,7 +476,7 @@ __device__ __forceinline__ void append_block(const RotaryArgs& a, long long unit
       if (!mine || id < 0) continue;
       most = warp_most[n & 1][team * wpt + min(lane, wpt - 1)];
       z = rescale(old, __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most))));
-      if (w == 0 && lane == 0) scales[h * a.s_sh] = z.now;
+      if (w == 0 && lane == 0 && FA_CHECK(in_cache(h, 0), a.status, DBG_GLOBAL_STORE)) scales[h * a.s_sh] = z.now;
       store(h, w);
       if (z.by < 1.f) restate(h, w);
     }
@@ -491,7 +500,7 @@ __device__ __forceinline__ void append_block(const RotaryArgs& a, long long unit
           if (id < 0 && !twice) break;
           z = rescale(old, most);
           __syncwarp();  // (every lane has read the scale)
-          if (lane == 0 && id >= 0) scales[h * a.s_sh] = z.now;
+          if (lane == 0 && id >= 0 && FA_CHECK(in_cache(h, 0), a.status, DBG_GLOBAL_STORE)) scales[h * a.s_sh] = z.now;
           for (int sub = 0; z.by < 1.f && sub * TOKENS < first; ++sub) restate(h, sub);
         }
       }
@@ -606,6 +615,7 @@ int fa_cache_append_8bit(const fa_rows* k, const fa_rows* v, const fa_pages* cac
   take_cache(cache, scales, &a);
   a.start = start, a.cu = cu, a.rows = rows;
   a.B = B, a.T = T, a.Tkv = Tkv, a.Hkv = Hkv;
+  FA_DEBUG_ARGS(a, B);
   int err = FA_OK;
   a.status = fa::status_word(&err);
   if (!a.status) return err;
@@ -646,6 +656,7 @@ int fa_rotary_append(const fa_rows* q, const fa_rows* k, const fa_rows* v, const
   a.dim = rotary->dim, a.interleaved = rotary->interleaved, a.at = rotary->at;
   a.cu = cu;
   a.B = B, a.T = T, a.Tkv = T, a.Hq = Hq, a.Hkv = Hkv;
+  FA_DEBUG_ARGS(a, B);
   int err = FA_OK;
   a.status = fa::status_word(&err);
   if (!a.status) return err;

@@ -578,7 +578,7 @@ __global__ void __launch_bounds__(C8 ? 512 : 384, 1)
           }
           __syncwarp();
           float* to = scales + e % C::SCALES * 8 + lane;
-          if (mine && there) {
+          if (mine && there && FA_CHECK(in_range(it.kvh, a.Hkv), st, DBG_GLOBAL_LOAD)) {
             const float* from = (kv ? a.vs : a.ks) + id * a.s_sp + it.kvh * a.s_sh + (in_page >> a.block_shift);
             asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(to)), "l"(from) : "memory");
             asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(BAR(C::FULL8 + sk)) : "memory");
@@ -801,6 +801,12 @@ __global__ void __launch_bounds__(C8 ? 512 : 384, 1)
             const int s8 = (2 * x + kv) % NS8;
             if (!(ok = wait_phase(BAR(C::FULL8 + s8), ((2 * x + kv) / NS8) & 1, st, SITE_SW_FULL8))) break;
             if (!(ok = wait_phase(BAR(C::EMPTY + slot), phase, st, SITE_SW_EMPTY))) break;
+            if (!FA_CHECK(smem_in(smem_u32(to), C::TILE_BYTES, sbase + C::OFF_R, sbase + C::OFF_S8) &&
+                              smem_in(sbase + C::OFF_S8 + s8 * C::STAGE, C::STAGE, sbase + C::OFF_S8, sbase + C::OFF_BAR),
+                          st, DBG_SMEM)) {
+              ok = false;
+              break;
+            }
             const uint8_t* from = sm + C::OFF_S8 + s8 * C::STAGE;
             const int c0 = lane >> 3;
 #pragma unroll
@@ -1455,7 +1461,7 @@ __global__ void __launch_bounds__(C8 ? 512 : 384, 1)
         f0 *= exp2f(vref);
         if (join) f1 *= exp2f(vrefs[t ^ 1]);
       }
-      const bool write = valid && FA_CHECK(whole ? in_range(token, a.T) : in_range(part, a.part_rows), st, DBG_GLOBAL_STORE);
+      const bool write = valid && FA_CHECK(whole ? in_range(token, a.T - FA_SLACK(a)) : in_range(part, a.part_rows), st, DBG_GLOBAL_STORE);
       uint16_t* orow = a.o + token * a.o_st + head * a.o_sh;
       float* prow = a.part_o + part * D;
       // in a join each lane takes half of the columns
@@ -1549,6 +1555,9 @@ __global__ void __launch_bounds__(256) serve_join_kernel(ServeArgs a) {
     const int tok = cut.z + (row >> 7) * npt + rn;
     if (rn >= npt || tok >= cut.x) continue;
     auto at = [&](int k) { return (long long)(k == 0 ? 2 * (c - 1) + 1 : 2 * (c - 1 + k)) * 256 + row; };
+    if (!FA_CHECK(in_range(at(0), a.part_rows) && in_range(at(parts - 1), a.part_rows), a.status, DBG_GLOBAL_LOAD) ||
+        !FA_CHECK(in_range(cut.y + tok, a.T - FA_SLACK(a)) && in_range(cut.w, a.Hkv), a.status, DBG_GLOBAL_STORE))
+      continue;
     float m = -INFINITY;
     for (int k = 0; k < parts; ++k) m = fmaxf(m, a.part_lse[at(k)]);
     const float base = m == -INFINITY ? 0.f : m;
@@ -1666,6 +1675,7 @@ int forward(const fa_rows* q, const fa_rows* k, const fa_rows* v, const fa_rows*
   a.cu = cu;
   a.B = B, a.T = T, a.Hq = Hq, a.Hkv = Hkv, a.G = Hq / Hkv;
   a.scale_log2 = scale * 1.4426950408889634f;
+  FA_DEBUG_ARGS(a, B);
   int sms = 0;
   if (!fa::sm_count(&sms)) return FA_ERR_CUDA;
   a.part_rows = 2LL * sms * 256;

@@ -413,7 +413,8 @@ __global__ void __launch_bounds__(512, 1)
   const int page = 1 << a.page_shift, prow = min(page, 128), g8 = lane & 7, x8 = lane >> 3;
   auto page_ids = [&](const Item8& it, int k) {  // of the tiles k .. k + 3 of the item's part
     const int j = it.j0 + k + x8, t0 = j * 128 + g8 * 16;
-    return j < min(it.j0 + it.cnt, it.nc) && t0 < it.L ? a.table[it.b * a.table_stride + (t0 >> a.page_shift)] : 0;
+    return j < min(it.j0 + it.cnt, it.nc) && t0 < it.L &&
+                   FA_CHECK(in_range(it.b, a.B) && in_range(t0 >> a.page_shift, a.table_width), st, DBG_META) ? a.table[it.b * a.table_stride + (t0 >> a.page_shift)] : 0;
   };
   // K's (kv = 0) or V's copies of the item's tiles, the ring's entries from e on.
   auto load_tiles = [&](const Item8& it, int kv, int* e) {
@@ -578,7 +579,7 @@ __global__ void __launch_bounds__(512, 1)
           const bool mine = t0 < it.L, there = id >= 0 && id < a.n_pages;
           if (mine && !there) record_check(a.status, SITE_S_PAGE);
           float* to = scales + s * 16 + g8;
-          if (mine && there) {
+          if (mine && there && FA_CHECK(in_range(it.kvh, a.Hkv), st, DBG_GLOBAL_LOAD)) {
             const long long from = id * a.s_sp + it.kvh * a.s_sh + ((t0 & (page - 1)) >> a.block_shift);
             asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(to)), "l"(a.ks + from) : "memory");
             asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(to + 8)), "l"(a.vs + from) : "memory");
@@ -611,7 +612,7 @@ __global__ void __launch_bounds__(512, 1)
           const int rr = it.r0 + t * RV + half * MINE + k * RPI + sub, tok = rr / a.G;
           toks[k] = tok;
           x[k] = make_uint4(0, 0, 0, 0);
-          if (k * RPI + sub < MINE && rr < rows)
+          if (k * RPI + sub < MINE && rr < rows && FA_CHECK(in_range(it.row0 + tok, a.T - FA_SLACK(a)), st, DBG_GLOBAL_LOAD))
             x[k] = *reinterpret_cast<const uint4*>(a.q + (long long)(it.row0 + tok) * a.q_st +
                                                    (long long)(it.kvh * a.G + rr - tok * a.G) * a.q_sh + 8 * c);
         }
@@ -1101,7 +1102,7 @@ __global__ void __launch_bounds__(512, 1)
             const float lse2 = sum != 0.f ? m - kPLog2 + lg2_approx(sum) : -INFINITY;
             if (!whole) {
               if (FA_CHECK(in_range(part0 + rr, a.part_rows), st, DBG_GLOBAL_STORE)) a.part_lse[part0 + rr] = lse2;
-            } else if (a.lse && FA_CHECK(in_range(token, a.T), st, DBG_GLOBAL_STORE)) {
+            } else if (a.lse && FA_CHECK(in_range(token, a.T - FA_SLACK(a)), st, DBG_GLOBAL_STORE)) {
               a.lse[head * a.T + token] = lse2 * 0.6931471805599453f;
             }
           }
@@ -1134,7 +1135,7 @@ __global__ void __launch_bounds__(512, 1)
           if (whole) {
             // even threads write the even rows of two columns each, odd threads the odd rows
             uint16_t* const row = a.o + token * a.o_st + head * a.o_sh;  // of this lane's rr
-            const long long mine = tok >= 0 && FA_CHECK(in_range(token, a.T), st, DBG_GLOBAL_STORE) ? (long long)row : 0;
+            const long long mine = tok >= 0 && FA_CHECK(in_range(token, a.T - FA_SLACK(a)), st, DBG_GLOBAL_STORE) ? (long long)row : 0;
 #pragma unroll
             for (int r = 0; r < RG; r += 2) {
               const float got = __shfl_xor_sync(0xffffffffu, (lane & 1) ? o[r] : o[r + 1], 1);
@@ -1195,8 +1196,11 @@ __global__ void __launch_bounds__(4 * D) serve8_join_kernel(Serve8BitArgs a, int
   const int4 cut = a.cuts[2 * c + 1];  // rows of the sequence, its first token, the item's first row, head
   constexpr int LPR = D / 4;
   const int sub = threadIdx.x % LPR, row = blockIdx.y * 16 + threadIdx.x / LPR, rr = cut.z + row;
-  const bool there = row < unit && rr < cut.x;
+  const int tok = rr / a.G;
   auto at = [&](int k) { return (long long)(k == 0 ? 2 * (c - 1) + 1 : 2 * (c - 1 + k)) * (2 * Serve8Cfg<D, F16>::R) + row; };
+  const bool there = row < unit && rr < cut.x &&
+                     FA_CHECK(in_range(at(0), a.part_rows) && in_range(at(parts - 1), a.part_rows), a.status, DBG_GLOBAL_LOAD) &&
+                     FA_CHECK(in_range(cut.y + tok, a.T - FA_SLACK(a)) && in_range(cut.w, a.Hkv), a.status, DBG_GLOBAL_STORE);
   float m = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int k0 = 0; k0 < parts; k0 += LPR) {
@@ -1227,7 +1231,7 @@ __global__ void __launch_bounds__(4 * D) serve8_join_kernel(Serve8BitArgs a, int
   }
   if (!there) return;
   const float inv = l != 0.f ? 1.f / l : 0.f;
-  const int tok = rr / a.G, h = cut.w * a.G + rr - tok * a.G;
+  const int h = cut.w * a.G + rr - tok * a.G;
   const long long token = cut.y + tok;
   *reinterpret_cast<uint2*>(a.o + token * a.o_st + h * a.o_sh + 4 * sub) =
       make_uint2(pack16<F16>(o.x * inv, o.y * inv), pack16<F16>(o.z * inv, o.w * inv));

@@ -38,6 +38,10 @@ struct ServeArgs {
                     // few-row kernel {rows of the sequence (tokens times heads of the group), its first token, the
                     // item's first row, key/value head}
   int* status;
+#ifdef FA_DEBUG
+  int dbg_B;           // batch count B, for the extents the debug build checks against
+  int dbg_slack;       // rows taken off those extents (fa_debug_set_check_slack)
+#endif
 };
 
 // Over a cache in 8 bits: its scales. (Strides and tensor maps count its elements, bytes.)
