@@ -509,10 +509,13 @@ __device__ __forceinline__ void append_block(const RotaryArgs& a, long long unit
 }
 
 // U = 0: a warp a job. Two CTAs an SM where the registers allow it: what a round waits for (rows, the team's other warps)
-// needs warps, and its instructions, some 300 a warp, are next to the bytes what a long append is bound by. 8192 prompt
-// tokens of 8 heads (d = 128, blocks of 64): 29 us, of 14 for the bytes; with 32 query heads turned too 69 of 54
-// (5.4 TB/s). One CTA an SM: 96 with the queries; threads of two rows, fewer warps: 78. 64 sequences' next tokens:
-// 4.1 us in a graph (one CTA an SM 5.4, three with spilled registers 6.0).
+// needs warps, and its instructions, some 300 a warp, are next to the bytes what a long append is bound by, with the
+// barrier of all teams of a CTA in every round. 15019 prompt tokens of 8 heads (d = 128, blocks of 64): 28.5 us, of 13.6
+// for the bytes; with 32 query heads turned too 69 of 55 (5.4 TB/s). One CTA an SM: 96 with the queries; threads of two
+// rows, fewer warps: 78. 64 sequences' next tokens: 4.1 us in a graph (one CTA an SM 5.4, three 6.0).
+// Registers: with two CTAs an SM a thread has 64 and spills 64 to 68 bytes; teams of 32 warps with two rows a thread
+// (blocks of 256 at d = 128) spill 640 to 752. 8192 tokens of 8 heads take 15.5 us in blocks of 64, 16.9 of 128 and 25.7
+// of 256 (at d = 64 9.0, 9.4 and 8.9), of 7.4 (3.7) for the bytes.
 template <int D, bool F16, int U, int THREADS>
 __global__ void __launch_bounds__(THREADS, U <= 1 ? 2 : 1) append_8bit_kernel(RotaryArgs a) {
   griddep_wait();

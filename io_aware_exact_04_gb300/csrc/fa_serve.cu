@@ -71,8 +71,13 @@ constexpr int kNewBox = 16;
 // maximum; that of a value's adds its logarithm there, so that P is formed with it, and the sum l takes it out
 // again by blocks. A reference (vref, twice the largest so far) keeps P in range; O keeps up with it as it does
 // with the maximum. It takes one bit of P's range: what is below 2^-22 of the row's largest probability (times the
-// largest scale) is off by 2^-33 of it. 32 trees of up to 64 nodes over up to 16384 tokens, 32 heads over 8 of 128: 311 us, 730 TFLOP/s, the
-// tensor pipe busy 48 % of the cycles: a step of 64 keys takes both lanes' softmax some 1850, as in 16 bits.
+// largest scale) is off by 2^-33 of it.
+// 32 trees of up to 64 nodes over up to 16384 tokens, 32 heads over 8 of 128: 311 us, 730 TFLOP/s, the tensor pipe busy
+// 48 % of the cycles: a step of 64 keys takes both lanes' softmax some 1850. That is longer than in 16 bits, by the work
+// on the scales of each 16 keys, in 128 registers a thread: where rows are many, a cache of half the size is read more
+// slowly. The same calls over 8 bits and over 16, 32 heads over 8 of 128, bf16 (fp16): 32 trees of 32 to 64 nodes over
+// 2000 to 16384 tokens 322 and 249 us (298 and 256), 8 times 512 tokens over 8192 608 and 430 (497 and 432), 8 times
+// 2048 over 32768 8775 and 6994 (7541 and 7370).
 template <int D, bool C8 = false>
 struct ServeCfg {
   static constexpr int NSUB = D / 64;

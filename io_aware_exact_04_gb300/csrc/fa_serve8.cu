@@ -60,9 +60,11 @@ namespace fa {
 // Measured on one GB300: decoding 64 sequences over up to 8192 tokens, 32 heads over 8 of 128: 108 us, 86 % of the copy
 // rate (32 of the same length, 8192: 92 us, 86 %; 2048: 34 us, 59 %); 128 over up to 5000, 12 heads of 64: 125 us, 63 %;
 // two contexts of 131072, 32 heads over 4 of 128: 50 us, 66 %; drafts of up to 6 nodes over up to 8000, 40 heads over 8:
-// 79 us. Within an item memory bounds it. What is left are an item's start and end, where the code is fetched anew: the
-// SM's instruction cache answers 91 % of the requests at d = 64, and the one behind it is busy 75 % of the time; and the
-// first and last 8 us of a call, a chain of loads, conversions and products that wait for each other.
+// 82 us, 45 %. A tile takes 0.70 us at d = 128 with 4 rows a lane, which is memory's time, and 0.44 at d = 64 (memory
+// 0.37); with 30 rows, 15 in each lane, it takes 0.88: there the softmax bounds it. An item's start and end take 1.5 us at
+// d = 128, 1.9 to 3.4 at d = 64 (256 and 512 sequences) and 5.8 with 30 rows, partly because code is fetched anew: the
+// SM's instruction cache answers 94 % of the requests at d = 64, and the one behind it is busy 68 % of the time. The
+// first and last 8 us of a call are a chain of loads, conversions and products that wait for each other.
 template <int D, bool F16>
 struct Serve8Cfg {
   static constexpr int R = 16;
@@ -108,9 +110,10 @@ enum { SITE_T8_EMPTY = 80, SITE_T8_FULL, SITE_T8_Q_FULL, SITE_T8_Q_EMPTY, SITE_T
 constexpr float kNoKey = -1e30f;     // reference maximum of a row that has met no key
 constexpr float kPLog2 = 11.f, kLagLog2 = 4.f;
 constexpr int kMinTiles8 = 2;        // tiles of a CTA where there are few
-// An item's start and end cost a CTA as much as some tiles do (some 2 us and 0.6 a tile at d = 128, 3.4 and 0.34 at
-// d = 64, partly beside the loads of the next one's): the runs are balanced with that many more for each. Drafts and
-// decoding at d = 64, 83 and 133 us, take 88 and 138 with 4 and 8, 88 and 134 with 2 and 4, 84 and 138 with 5 and 10.
+// An item's start and end cost a CTA as much as some tiles do (1.5 us and 0.70 a tile at d = 128, up to 3.4 and 0.44 at
+// d = 64, partly beside the loads of the next one's): the runs are balanced with that many more for each. When drafts and
+// decoding at d = 64 took 83 and 133 us with these, they took 88 and 138 with 4 and 8, 88 and 134 with 2 and 4, 84 and 138
+// with 5 and 10.
 template <int D>
 constexpr int kItemTiles = D == 64 ? 5 : 3;
 constexpr int kNewBox8 = 16;         // rows of a TMA box of new tokens
