@@ -424,11 +424,13 @@ typedef struct {
  *    the product of the row's largest probability and the sequence's and head's largest
  *    such scale, whichever is more. With many rows that concerns nodes' values too: their
  *    scale is 1, or in bf16 the power of two that brings the largest element of 32 rows
- *    from [2^14, 2^15) to what it is. Which of the kernels runs follows from B, T, Hq / Hkv, d and dtype alone: a
- *    batch that is mostly sequences without nodes is best given without those.
- *  - A NaN in the cache reaches the rows that see it. Scales have to be positive and
- *    finite; others give undefined results, of their own sequence and head only. An
- *    infinity in a query makes the row NaN, as scores of -inf alone do.
+ *    from [2^14, 2^15) to what it is. Which of the kernels runs follows from B, T,
+ *    Hq / Hkv, d and dtype alone: a batch that is mostly sequences without nodes is best
+ *    given without those.
+ *  - A NaN in the cache reaches the rows that see it. Scales have to be positive, normal
+ *    and finite; others give undefined results, of their own sequence and head only. From
+ *    2^80 on (keys and values from 2^88 on) sums may pass fp32's range: the row is then
+ *    infinite or NaN. An infinity in a query makes the row NaN, as scores of -inf alone do.
  * workspace: fa_forward_tree_8bit_workspace_size bytes, 256-byte aligned. */
 FA_API int fa_forward_tree_8bit(const fa_rows* q, const fa_rows* k, const fa_rows* v, const fa_rows* o, float* lse,
                                 const fa_pages* cache, const fa_scales* scales, const int32_t* lens,
